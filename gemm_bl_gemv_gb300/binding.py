@@ -24,7 +24,7 @@ EXPORTS = [
     "bl_pack_i2s", "bl_pack_tq2_0", "bl_pack_w1", "bl_quantize_act_absmax_int8",
     "bl_gemv_i2s", "bl_gemv_i2s_residual", "bl_gemv_i2s_rmsnorm", "bl_gemv_i2s_gate_up", "bl_gemv_tq2_0", "bl_gemm_w1a8", "bl_gemm_w1a8_act", "bl_gemm_i2s_int8",
     "bl_gemm_tq2_0_int8", "bl_gemm_i2s_int8_act", "bl_gemm_i2s_int8_act_workspace",
-    "bl_gemm_i2s_int8_act_noalloc",
+    "bl_gemm_i2s_int8_act_noalloc", "bl_rmsnorm_quant_int8", "bl_lora_add", "bl_sample",
 ]
 
 
@@ -59,6 +59,9 @@ def _declare(L):
         "bl_gemm_i2s_int8_act": ([p, i32, p, i64, i64, i64, p, p, ctypes.c_size_t, i32, p], st),
         "bl_gemm_i2s_int8_act_workspace": ([i64, i64], ctypes.c_size_t),
         "bl_gemm_i2s_int8_act_noalloc": ([p, i32, p, i64, i64, i64, p, i32, p], st),
+        "bl_rmsnorm_quant_int8": ([p, p, i32, p, ctypes.c_float, i64, i64, p, p, p, p, p], st),
+        "bl_lora_add": ([p, i32, p, p, p, p, p, p, i32, i64, i64, i64, i64, i32, p], st),
+        "bl_sample": ([p, i32, p, p, p, p, p, i64, i64, p, p, p], st),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -344,3 +347,93 @@ def bl_gemm_tq2_0_int8(q, s, packed, N, y=None, stream=None):
         y = torch.empty((M, N), dtype=torch.float32, device=q.device)
     _check(_lib.bl_gemm_tq2_0_int8(_ptr(q), _ptr(s), _ptr(packed), M, N, K, _ptr(_cuda(y, "y")), _stream(stream)))
     return y
+
+
+# ---- around the products -----------------------------------------------------
+
+def _like(t, name, dtype, shape, device):
+    """An optional or given tensor must have exactly this dtype, shape and device."""
+    _cuda(t, name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    return t
+
+
+def bl_rmsnorm_quant_int8(x, rms_weight, eps=1e-5, residual=None, h=None, y=False, q=None, s=None, stream=None):
+    """(q, s, h, y): int8 codes and fp32 scales of RMSNorm(x + residual) * rms_weight, one launch.
+
+    h is the sum x + residual in x's dtype (None without a residual unless a
+    tensor is given), y the normed values in x's dtype (y=True or a tensor;
+    None otherwise)."""
+    _cuda(x, "x")
+    M, K = x.shape
+    xt, dev = _dtype_code(x), x.device
+    _like(rms_weight, "rms_weight", x.dtype, (K,), dev)
+    if residual is not None:
+        _like(residual, "residual", x.dtype, (M, K), dev)
+        if h is None:
+            h = torch.empty_like(x)
+    if h is not None:
+        _like(h, "h", x.dtype, (M, K), dev)
+    if y is True:
+        y = torch.empty_like(x)
+    elif y is False or y is None:
+        y = None
+    else:
+        _like(y, "y", x.dtype, (M, K), dev)
+    q = torch.empty((M, K), dtype=torch.int8, device=dev) if q is None else _like(q, "q", torch.int8, (M, K), dev)
+    s = torch.empty(M, dtype=torch.float32, device=dev) if s is None else _like(s, "s", torch.float32, (M,), dev)
+    _check(_lib.bl_rmsnorm_quant_int8(_ptr(x), _ptr(residual), xt, _ptr(rms_weight), float(eps), M, K, _ptr(h), _ptr(y),
+                                      _ptr(q), _ptr(s), _stream(stream)))
+    return q, s, h, y
+
+
+def bl_lora_add(x, adapter, a, b, scale, base, y=None, stream=None):
+    """y[m] = base[m] + scale[l] * b[l] (a[l] x[m]) with l = adapter[m] (negative: none).
+
+    x [M, K]; adapter int32 [M]; a bf16 [L, R, K]; b bf16 [L, N, R]; scale
+    fp32 [L]; base and y [M, N], y may be base."""
+    _cuda(x, "x")
+    M, K = x.shape
+    dev = x.device
+    _like(a, "a", torch.bfloat16, (a.shape[0], a.shape[1], K), dev)
+    L, R = a.shape[0], a.shape[1]
+    N = base.shape[1]
+    _like(b, "b", torch.bfloat16, (L, N, R), dev)
+    _like(scale, "scale", torch.float32, (L,), dev)
+    _like(adapter, "adapter", torch.int32, (M,), dev)
+    yt = _dtype_code(base)
+    _like(base, "base", base.dtype, (M, N), dev)
+    y = torch.empty_like(base) if y is None else _like(y, "y", base.dtype, (M, N), dev)
+    _check(_lib.bl_lora_add(_ptr(x), _dtype_code(x), _ptr(adapter), _ptr(a), _ptr(b), _ptr(scale), _ptr(base), _ptr(y), yt,
+                            M, N, K, L, R, _stream(stream)))
+    return y
+
+
+def bl_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, token=None, prob=False, stream=None):
+    """One int32 token per row of logits [M, V] from the uniform numbers u [M]; (token, prob) with prob=True or a tensor.
+
+    temperature, top_p, min_p (fp32 [M]) and top_k (int32 [M]) default to 1, 1, 0 and all tokens."""
+    _cuda(logits, "logits")
+    M, V = logits.shape
+    dev = logits.device
+    _like(u, "u", torch.float32, (M,), dev)
+    for t, n in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p")):
+        if t is not None:
+            _like(t, n, torch.float32, (M,), dev)
+    if top_k is not None:
+        _like(top_k, "top_k", torch.int32, (M,), dev)
+    token = torch.empty(M, dtype=torch.int32, device=dev) if token is None else _like(token, "token", torch.int32, (M,), dev)
+    if prob is True:
+        prob = torch.empty(M, dtype=torch.float32, device=dev)
+    elif prob is False or prob is None:
+        prob = None
+    else:
+        _like(prob, "prob", torch.float32, (M,), dev)
+    _check(_lib.bl_sample(_ptr(logits), _dtype_code(logits), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                          _ptr(u), M, V, _ptr(token), _ptr(prob), _stream(stream)))
+    return token if prob is None else (token, prob)

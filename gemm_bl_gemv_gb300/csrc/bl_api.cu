@@ -382,4 +382,57 @@ bl_status bl_gemm_i2s_int8_act(const void* x, bl_dtype xt, const uint8_t* packed
                        "bl_gemm_i2s_int8_act");
 }
 
+bl_status bl_rmsnorm_quant_int8(const void* x, const void* residual, bl_dtype xt, const void* rms_weight, float eps,
+                                int64_t M, int64_t K, void* h, void* y, int8_t* q, float* s, bl_stream_t stream) {
+  const char* fn = "bl_rmsnorm_quant_int8";
+  if (!x || !rms_weight || !q || !s) return fail(BL_ERR_NULL, "%s: NULL pointer", fn);
+  if (residual && !h) return fail(BL_ERR_NULL, "%s: h is required with a residual", fn);
+  if (xt != BL_F32 && xt != BL_BF16) return fail(BL_ERR_DTYPE, "%s: bad dtype %d", fn, int(xt));
+  if (M < 1 || K < 1 || M > 0x7fffffff || K > 0x7fffffff)
+    return fail(BL_ERR_SHAPE, "%s: need M, K >= 1 (M=%lld K=%lld)", fn, (long long)M, (long long)K);
+  if (!(eps >= 0.f)) return fail(BL_ERR_SHAPE, "%s: eps must be >= 0", fn);
+  if (y && y == h) return fail(BL_ERR_SHAPE, "%s: y and h must be different tensors", fn);
+  const size_t es = xt == BL_F32 ? 4 : 2;
+  if (!aligned(x, es) || !aligned(rms_weight, es) || (residual && !aligned(residual, es)) || (h && !aligned(h, es)) ||
+      (y && !aligned(y, es)) || !aligned(s, 4))
+    return fail(BL_ERR_ALIGN, "%s: tensors must be aligned to their element size", fn);
+  return launch_status(launch_rmsnorm_quant(x, residual, xt, rms_weight, eps, M, K, h, y, q, s, S(stream)), fn);
+}
+
+bl_status bl_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a_bf16,
+                      const uint16_t* b_bf16, const float* scale, const void* base, void* y, bl_dtype yt, int64_t M,
+                      int64_t N, int64_t K, int64_t adapters, int rank, bl_stream_t stream) {
+  const char* fn = "bl_lora_add";
+  if (!x || !adapter || !a_bf16 || !b_bf16 || !scale || !base || !y) return fail(BL_ERR_NULL, "%s: NULL pointer", fn);
+  if ((xt != BL_F32 && xt != BL_BF16) || (yt != BL_F32 && yt != BL_BF16))
+    return fail(BL_ERR_DTYPE, "%s: bad dtype (x %d, y %d)", fn, int(xt), int(yt));
+  if (M < 1 || N < 1 || K < 8 || K % 8 || adapters < 1 || M > 0x7fffffff || N > 0x7fffffff || adapters > 0x7fffffff)
+    return fail(BL_ERR_SHAPE, "%s: need M, N, adapters >= 1, K %% 8 == 0 (M=%lld N=%lld K=%lld adapters=%lld)", fn,
+                (long long)M, (long long)N, (long long)K, (long long)adapters);
+  if (rank < 8 || rank % 8) return fail(BL_ERR_SHAPE, "%s: need rank %% 8 == 0 (rank=%d)", fn, rank);
+  if (rank > 128 || K > 65536)
+    return fail(BL_ERR_UNSUPPORTED, "%s: rank <= 128 and K <= 65536 supported (rank=%d K=%lld)", fn, rank, (long long)K);
+  const size_t ys = yt == BL_F32 ? 4 : 2;
+  if (!aligned(x, 16) || !aligned(a_bf16, 16) || !aligned(b_bf16, 16) || !aligned(adapter, 4) || !aligned(scale, 4) ||
+      !aligned(base, ys) || !aligned(y, ys))
+    return fail(BL_ERR_ALIGN, "%s: x, a and b must be 16-byte aligned, the others to their element size", fn);
+  return launch_status(launch_lora_add(x, xt, adapter, a_bf16, b_bf16, scale, base, y, yt, M, N, K, adapters, rank,
+                                       S(stream)), fn);
+}
+
+bl_status bl_sample(const void* logits, bl_dtype lt, const float* temperature, const int32_t* top_k,
+                    const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V, int32_t* token,
+                    float* prob, bl_stream_t stream) {
+  const char* fn = "bl_sample";
+  if (!logits || !u || !token) return fail(BL_ERR_NULL, "%s: NULL pointer", fn);
+  if (lt != BL_F32 && lt != BL_BF16) return fail(BL_ERR_DTYPE, "%s: bad dtype %d", fn, int(lt));
+  if (M < 1 || V < 1 || M > 0x7fffffff)
+    return fail(BL_ERR_SHAPE, "%s: need M, V >= 1 (M=%lld V=%lld)", fn, (long long)M, (long long)V);
+  if (V > 524288) return fail(BL_ERR_UNSUPPORTED, "%s: V <= 524288 supported (V=%lld)", fn, (long long)V);
+  if (!aligned(logits, lt == BL_F32 ? 4 : 2) || !aligned(u, 4) || !aligned(token, 4) || !aligned(temperature, 4) ||
+      !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(prob, 4))
+    return fail(BL_ERR_ALIGN, "%s: pointers must be aligned to their element size", fn);
+  return launch_status(launch_sample(logits, lt, temperature, top_k, top_p, min_p, u, M, V, token, prob, S(stream)), fn);
+}
+
 }  // extern "C"

@@ -155,5 +155,15 @@ cudaError_t launch_gemm_i2s_int8_act(const void* x, bl_dtype xt, const uint8_t* 
 size_t gemm_i2s_int8_act_noalloc_limit();
 cudaError_t launch_gemm_i2s_int8_act_noalloc(const void* x, bl_dtype xt, const uint8_t* packed, int64_t M, int64_t N,
                                              int64_t K, float* y, int fuse, cudaStream_t s);
+// residual, h and y may be nullptr (h only without a residual)
+cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, bl_dtype xt, const void* rms_w, float eps,
+                                 int64_t M, int64_t K, void* h, void* y, int8_t* q, float* sc, cudaStream_t s);
+cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
+                            const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
+                            int64_t K, int64_t adapters, int rank, cudaStream_t s);
+// temperature, top_k, top_p, min_p and prob may be nullptr
+cudaError_t launch_sample(const void* logits, bl_dtype lt, const float* temperature, const int32_t* top_k,
+                          const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V,
+                          int32_t* token, float* prob, cudaStream_t s);
 
 }  // namespace bl

@@ -1,0 +1,157 @@
+// Residual addition, RMSNorm and absmax int8 quantization of a token, the
+// input side of the int8 products:
+//   h = rnd(x + residual);  r = fl(1 / sqrt(sum h^2 / K + eps));
+//   v = fl(fl(h r) w);  y = rnd(v);  q, s = absmax codes of v (act_quant.cuh).
+// The codes have to be the same for every launch shape, so the only quantity
+// that depends on an order of additions, the sum of squares, is carried as a
+// pair of floats (a two-sum per term: its error is below 2^-40 of the sum)
+// and r is rounded to binary32 once; everything after r is elementwise with
+// the _rn intrinsics, and a maximum.
+#include "act_quant.cuh"
+#include "bl_internal.h"
+
+namespace bl {
+namespace {
+
+// An unevaluated sum hi + lo.
+struct Pair {
+  float hi, lo;
+};
+
+// p + v, v added without rounding (two-sum); the rounding errors collect in lo.
+__device__ __forceinline__ void pair_add(Pair& p, float v) {
+  const float t = __fadd_rn(p.hi, v);
+  const float z = __fsub_rn(t, p.hi);
+  p.lo = __fadd_rn(p.lo, __fadd_rn(__fsub_rn(p.hi, __fsub_rn(t, z)), __fsub_rn(v, z)));
+  p.hi = t;
+}
+
+__device__ __forceinline__ void pair_add(Pair& p, const Pair& q) {
+  pair_add(p, q.hi);
+  p.lo = __fadd_rn(p.lo, q.lo);
+}
+
+// p + h^2; the square of a bf16 value is exact, that of a float is a pair.
+template <bool XB>
+__device__ __forceinline__ void pair_add_square(Pair& p, float h) {
+  const float sq = __fmul_rn(h, h);
+  if (!XB) p.lo = __fadd_rn(p.lo, __fmaf_rn(h, h, -sq));
+  pair_add(p, sq);
+}
+
+__device__ __forceinline__ Pair warp_pair_sum(Pair p) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Pair q;
+    q.hi = __shfl_xor_sync(0xffffffffu, p.hi, o);
+    q.lo = __shfl_xor_sync(0xffffffffu, p.lo, o);
+    // the two lanes add in the same order, so that every lane holds one result
+    if (threadIdx.x & o) {
+      pair_add(q, p);
+      p = q;
+    } else {
+      pair_add(p, q);
+    }
+  }
+  return p;
+}
+
+// fl(1 / sqrt(sum / K + eps)): the mean in pairs (1/K given as one), one
+// Newton step from the hardware's approximation whose residual is formed
+// exactly, one final rounding.  0 if the mean plus eps is 0.
+__device__ __forceinline__ float inv_rms(Pair sum, Pair inv_k, float eps) {
+  Pair m;
+  m.hi = __fmul_rn(sum.hi, inv_k.hi);
+  m.lo = __fmaf_rn(sum.hi, inv_k.hi, -m.hi) + __fmaf_rn(sum.hi, inv_k.lo, __fmul_rn(sum.lo, inv_k.hi));
+  pair_add(m, eps);
+  const float a = __fadd_rn(m.hi, m.lo);
+  const float b = __fsub_rn(m.lo, __fsub_rn(a, m.hi));
+  if (a == 0.f) return 0.f;
+  const float r = rsqrtf(a);
+  const float r2 = __fmul_rn(r, r);
+  const float r2l = __fmaf_rn(r, r, -r2);
+  const float d = __fsub_rn(__fsub_rn(__fmaf_rn(-a, r2, 1.f), __fmul_rn(a, r2l)), __fmul_rn(b, r2));  // 1 - (a+b) r^2
+  return __fmaf_rn(r, d * __fmaf_rn(0.375f, d, 0.5f), r);
+}
+
+struct Args {
+  const void *x, *res, *w;
+  void *h, *y;
+  int8_t* q;
+  float* s;
+  int64_t M, K;
+  Pair inv_k;
+  float eps;
+};
+
+template <bool XB>
+__device__ __forceinline__ float load(const void* x, int64_t i) {
+  if (XB) return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(x)[i]);
+  return reinterpret_cast<const float*>(x)[i];
+}
+template <bool XB>
+__device__ __forceinline__ void store(void* x, int64_t i, float v) {
+  if (XB)
+    reinterpret_cast<uint16_t*>(x)[i] = f32_to_bf16_bits_rn(v);
+  else
+    reinterpret_cast<float*>(x)[i] = v;
+}
+
+// One CTA per token, any K, any alignment; the row is read three times (its
+// second and third reads from L2).
+template <bool XB>
+__global__ void __launch_bounds__(512) rmsnorm_quant_any_kernel(const Args a) {
+  __shared__ Pair red[16];
+  __shared__ float redm[16];
+  const int64_t base = int64_t(blockIdx.x) * a.K;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  pdl_wait();
+  Pair p = {0.f, 0.f};
+  for (int64_t k = threadIdx.x; k < a.K; k += blockDim.x) {
+    float h = load<XB>(a.x, base + k);
+    if (a.res) {
+      h = __fadd_rn(h, load<XB>(a.res, base + k));
+      if (XB) h = bf16_bits_to_f32(f32_to_bf16_bits_rn(h));
+    }
+    if (a.h) store<XB>(a.h, base + k, h);
+    pair_add_square<XB>(p, h);
+  }
+  p = warp_pair_sum(p);
+  if (lane == 0) red[warp] = p;
+  __syncthreads();
+  p = Pair{0.f, 0.f};
+  for (int i = 0; i < nw; ++i) pair_add(p, red[i]);
+  const float r = inv_rms(p, a.inv_k, a.eps);
+  const void* hr = a.h ? a.h : a.x;  // this thread wrote the elements of h that it reads
+  float m = 0.f;
+  for (int64_t k = threadIdx.x; k < a.K; k += blockDim.x)
+    m = fmaxf(m, fabsf(__fmul_rn(__fmul_rn(load<XB>(hr, base + k), r), load<XB>(a.w, k))));
+  m = warp_max(m);
+  if (lane == 0) redm[warp] = m;
+  __syncthreads();
+  m = 0.f;
+  for (int i = 0; i < nw; ++i) m = fmaxf(m, redm[i]);
+  float sc, inv;
+  absmax_scales(m, sc, inv);
+  if (threadIdx.x == 0) a.s[blockIdx.x] = sc;
+  for (int64_t k = threadIdx.x; k < a.K; k += blockDim.x) {
+    const float v = __fmul_rn(__fmul_rn(load<XB>(hr, base + k), r), load<XB>(a.w, k));
+    if (a.y) store<XB>(a.y, base + k, v);
+    a.q[base + k] = int8_t(quant_code(v, inv));
+  }
+  pdl_launch_dependents();
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, bl_dtype xt, const void* rms_w, float eps,
+                                 int64_t M, int64_t K, void* h, void* y, int8_t* q, float* sc, cudaStream_t s) {
+  Args a{x, residual, rms_w, h, y, q, sc, M, K, {}, eps};
+  a.inv_k.hi = float(1.0 / double(K));
+  a.inv_k.lo = float(1.0 / double(K) - double(a.inv_k.hi));
+  const bool pdl = overlap_enabled();
+  if (xt == BL_BF16) return launch(rmsnorm_quant_any_kernel<true>, dim3(unsigned(M)), dim3(512), 0, s, pdl, a);
+  return launch(rmsnorm_quant_any_kernel<false>, dim3(unsigned(M)), dim3(512), 0, s, pdl, a);
+}
+
+}  // namespace bl

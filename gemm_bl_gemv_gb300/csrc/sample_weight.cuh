@@ -1,0 +1,121 @@
+// Order and weight of a logit, shared by the sampling kernels.
+//   key(l)    : unsigned, rising with l (NaN as -inf, -0 as 0).
+//   weight(l) : exp((l - max) / T) as an integer in units of 2^-44.
+#pragma once
+#include "bl_device.cuh"
+
+namespace bl {
+
+constexpr int kWeightBits = 44;  // the largest weight is 2^44, so 2^19 of them stay below 2^64
+constexpr float kGreedyBelow = 1e-5f;
+
+__device__ __forceinline__ uint32_t key_of_f32(float l) {
+  const uint32_t b = __float_as_uint(l != l ? -INFINITY : l + 0.f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float f32_of_key(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
+// log2(e) / T as a pair of floats; greedy: hi < 0.
+struct Slope {
+  float hi, lo;
+};
+__device__ __forceinline__ Slope slope_of(float t) {
+  if (!(t >= kGreedyBelow)) return Slope{-1.f, 0.f};
+  const float lh = 1.44269502162933349609375f;         // log2(e) to 24 bits
+  const float ll = 1.92596303313e-8f;                  // log2(e) - lh
+  const float q = __fdiv_rn(lh, t);
+  const float rest = __fadd_rn(__fmaf_rn(-q, t, lh), ll);  // lh - q t is exact
+  return Slope{q, q > 0.f ? __fdiv_rn(rest, t) : 0.f};
+}
+
+// 2^(j/32) in units of 2^-44, j = -16..16.
+struct Exp2Table {
+  unsigned long long v[33];
+};
+
+// The table by the whole CTA (fp64, one entry per thread); the caller synchronizes.
+__device__ __forceinline__ void fill_exp2_table(Exp2Table& t) {
+  for (int j = threadIdx.x; j < 33; j += blockDim.x)
+    t.v[j] = static_cast<unsigned long long>(rint(exp2(double(j - 16) / 32.0) * double(1ull << kWeightBits)));
+}
+
+// The weight of logit l: with -z = (l - max) log2(e) / T in pairs of floats,
+// 2^-z = 2^n 2^(j/32) 2^r, |r| <= 1/64: the power of two is a shift, 2^(j/32)
+// comes from the table, and 2^r - 1 <= 2^-6.5 is a polynomial in float, whose
+// 2^-24 relative error leaves about 2^-30 of the weight.
+// `shift` receives -n: the result is not shifted yet.
+__device__ __forceinline__ unsigned long long weight_mantissa(float l, float top, Slope c, const Exp2Table& t,
+                                                              int& shift) {
+  shift = 0;
+  if (l == top) return 1ull << kWeightBits;
+  if (c.hi < 0.f || !(l > -INFINITY) || top == INFINITY) return 0;
+  const float d = __fsub_rn(l, top);  // < 0; its rounding error is dl
+  const float z = __fsub_rn(d, l);
+  const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(d, z)), __fsub_rn(-top, z));
+  const float e = __fmul_rn(d, c.hi);
+  if (!(e > -63.f)) return 0;
+  const float el = __fmaf_rn(d, c.hi, -e) + __fmaf_rn(d, c.lo, __fmul_rn(dl, c.hi));
+  const float n = rintf(e);                 // -63..0
+  const float f = __fsub_rn(e, n);          // exact, |f| <= 1/2
+  const float j = rintf(f * 32.f);          // -16..16
+  const float r = __fmaf_rn(j, -0.03125f, f) + el;
+  // 2^r - 1 = a + a^2 / 2 + a^3 / 6 + a^4 / 24 with a = r ln 2
+  const float a = r * 0.693147180559945f;
+  const float p = a * __fmaf_rn(a, __fmaf_rn(a, __fmaf_rn(a, 0.041666667f, 0.16666667f), 0.5f), 1.f);
+  const unsigned long long base = t.v[int(j) + 16];
+  // base < 2^45, so |p base| < 2^39: in units of 2^8 it is a signed 32-bit integer
+  const long long more = static_cast<long long>(__float2int_rn(p * __ull2float_rn(base >> 8))) * 256;
+  shift = -int(n);                          // 0..63
+  return base + static_cast<unsigned long long>(more);
+}
+
+__device__ __forceinline__ unsigned long long weight_of(float l, float top, Slope c, const Exp2Table& t) {
+  int shift;
+  const unsigned long long w = weight_mantissa(l, top, c, t, shift);
+  return shift == 0 ? w : (w + (1ull << (shift - 1))) >> shift;
+}
+
+// The share of logit l's weight in `kept`; the weight keeps its full precision here.
+__device__ __forceinline__ float share_of(float l, float top, Slope c, const Exp2Table& t, unsigned long long kept) {
+  int shift;
+  const unsigned long long w = weight_mantissa(l, top, c, t, shift);
+  return float(double(w) * double(exp2i(-shift)) / double(kept));
+}
+
+// Row parameters after clamping.
+struct RowFilter {
+  Slope slope;
+  long long top_k;           // tokens that stay by count
+  float top_p, u;            // top_p = 2: no limit
+  unsigned long long min_w;  // smallest weight that stays (0: no limit)
+};
+
+__device__ __forceinline__ RowFilter row_filter(int64_t m, int64_t V, const float* temperature, const int32_t* top_k,
+                                                const float* top_p, const float* min_p, const float* u) {
+  RowFilter f;
+  f.slope = slope_of(temperature ? temperature[m] : 1.f);
+  const int k = top_k ? top_k[m] : 0;
+  f.top_k = (k <= 0 || k > V) ? V : k;
+  const float p = top_p ? top_p[m] : 1.f;
+  f.top_p = p < 1.f ? fmaxf(p, 0.f) : 2.f;
+  const float mp = min_p ? fminf(min_p[m], 1.f) : 0.f;
+  f.min_w = (min_p && min_p[m] > 0.f)
+                ? static_cast<unsigned long long>(ceil(double(mp) * double(1ull << kWeightBits)))
+                : 0ull;
+  const float v = u[m];
+  f.u = v > 0.f ? fminf(v, 0.99999994f) : 0.f;
+  return f;
+}
+
+// ceil(p * mass) for 0 <= p < 1 and floor(u * mass) for 0 <= u < 1.
+__device__ __forceinline__ unsigned long long mass_limit(float p, unsigned long long mass) {
+  return static_cast<unsigned long long>(ceil(double(p) * double(mass)));
+}
+__device__ __forceinline__ unsigned long long mass_target(float u, unsigned long long mass) {
+  const unsigned long long t = static_cast<unsigned long long>(double(u) * double(mass));
+  return t < mass ? t : mass - 1;
+}
+
+}  // namespace bl

@@ -392,6 +392,91 @@ bl_status bl_gemm_i2s_int8_act(const void* x, bl_dtype xt, const uint8_t* packed
 bl_status bl_gemm_i2s_int8_act_noalloc(const void* x, bl_dtype xt, const uint8_t* packed, int64_t M, int64_t N,
                                        int64_t K, float* y, int fuse, bl_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Around the products: a serving step's norm, adapters and sampling.         */
+/* (The pages stop at the product; these are the library's own additions.)    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Residual addition, RMSNorm and int8 quantization of M tokens, the input
+ * side of the int8 products, in one launch.  For every row, in binary32 with
+ * round-to-nearest-even:
+ *   h[k] = x[k] + residual[k], rounded to xt          (x[k] without a residual)
+ *   r    = 1 / sqrt(sum_k h[k]^2 / K + eps)           (see below)
+ *   v[k] = (h[k] * r) * rms_weight[k],   y[k] = v[k] rounded to xt
+ *   q, s = the absmax int8 codes and scale of v, by the steps of
+ *          bl_quantize_act_absmax_int8.
+ * The sum of squares is carried in pairs of floats and r is rounded to
+ * binary32 once, so q, s, h and y are the same for every launch shape and
+ * differ from the formula's only where r lies within about 2^-40 (relative)
+ * of a rounding border.  That holds while the squares neither overflow nor
+ * underflow binary32 against the sum (2^-50 < |h| < 2^60 does it); a row
+ * whose mean square plus eps is 0 gives y = 0, q = 0, s = 0.
+ *   x : [M, K] (xt);  residual : [M, K] (xt) or NULL;  rms_weight : [K] (xt).
+ *   h : [M, K] (xt) or NULL; required with a residual; may be x or residual.
+ *   y : [M, K] (xt) or NULL; may be x or residual, but not h.
+ *   q : int8 [M, K];  s : fp32 [M].
+ * Requires M, K >= 1, M < 2^31, eps >= 0; tensors aligned to their element
+ * size (16-byte aligned rows, K % 8 == 0 and K <= 32768 take the
+ * register-resident kernel, other shapes read the row three times).
+ * Non-finite inputs give unspecified outputs for their row.
+ */
+bl_status bl_rmsnorm_quant_int8(const void* x, const void* residual, bl_dtype xt, const void* rms_weight, float eps,
+                                int64_t M, int64_t K, void* h, void* y, int8_t* q, float* s, bl_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared product:
+ *   y[m,n] = base[m,n] + scale[a] * sum_r B[a,n,r] * (sum_k A[a,r,k] x[m,k]),
+ *   a = adapter[m];  a negative a means no adapter: y[m,:] = base[m,:].
+ *   x       : [M, K] fp32 or bf16 (xt).
+ *   adapter : int32 [M], in any order (tokens of one request next to each
+ *             other share the reads of its adapter).  A value >= adapters
+ *             sets BL_DEVERR_RANGE and is treated as no adapter.
+ *   a_bf16  : bf16 [adapters, rank, K];  b_bf16 : bf16 [adapters, N, rank].
+ *   scale   : fp32 [adapters] (alpha / rank).
+ *   base, y : [M, N] fp32 or bf16 (yt); y may be base.
+ * An adapter of a lower rank is padded with zero rows of A and zero columns
+ * of B.  Sums are fp32; y is rounded once.
+ * Requires M, N >= 1, adapters >= 1, rank a multiple of 8 in 8..128,
+ * K >= 8 with K % 8 == 0, K <= 65536; x, a, b 16-byte aligned, the other
+ * pointers aligned to their element size.
+ */
+bl_status bl_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a_bf16,
+                      const uint16_t* b_bf16, const float* scale, const void* base, void* y, bl_dtype yt, int64_t M,
+                      int64_t N, int64_t K, int64_t adapters, int rank, bl_stream_t stream);
+
+/*
+ * One token per row of logits, by temperature, top-k, top-p and min-p, from
+ * a given uniform number.  Per row, in this order:
+ *   order  : tokens by falling logit, ties by rising index; NaN counts as
+ *            -inf, and -0 equals 0.
+ *   weight : w[i] = exp((l[i] - max) / temperature), 1 for l[i] = max, 0 for
+ *            l[i] = -inf; a temperature below 1e-5 (or NaN) is greedy: only
+ *            the maxima have weight.
+ *   top_k  : the first top_k tokens stay (all if top_k <= 0).
+ *   top_p  : of these, a token stays while the weight before it is less than
+ *            top_p times the weight of the top_k tokens (all if top_p >= 1
+ *            or NaN).
+ *   min_p  : of these, tokens with w[i] >= min_p stay (all if min_p <= 0 or
+ *            NaN).  The first token always stays.
+ *   token  : the first token in the order whose cumulative weight exceeds
+ *            u times the weight that stayed; u is clamped to [0, 1) (NaN: 0).
+ *   prob   : w[token] / (weight that stayed).
+ * A row without a logit above -inf gives token -1 and prob 0.
+ * Weights are integers in units of 2^-44 of the largest, from an exp within
+ * about 2^-30 (relative), and their sums are exact, so the result does not
+ * depend on the order of the additions.
+ *   logits : [M, V] fp32 or bf16 (lt).   u : fp32 [M].
+ *   temperature, top_p, min_p : fp32 [M] or NULL (1, 1, 0);
+ *   top_k  : int32 [M] or NULL (all).
+ *   token  : int32 [M];  prob : fp32 [M] or NULL.
+ * Requires M >= 1, 1 <= V <= 524288 (BL_ERR_UNSUPPORTED above), M < 2^31;
+ * pointers aligned to their element size.
+ */
+bl_status bl_sample(const void* logits, bl_dtype lt, const float* temperature, const int32_t* top_k,
+                    const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V, int32_t* token,
+                    float* prob, bl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
