@@ -190,7 +190,12 @@ cudaError_t launch_sample(const void* logits, bl_dtype lt, const float* temperat
   const Args g{logits, temperature, top_p, min_p, u, top_k, M, V, token, prob};
   const bool pdl = overlap_enabled();
   const dim3 grid{unsigned(M)}, block{1024};
-  if (lt == BL_BF16) return launch(sample_any_kernel<true>, grid, block, 0, s, pdl, g);
+  if (lt == BL_BF16) {
+    const cudaError_t e = launch_sample_bf16(static_cast<const uint16_t*>(logits), temperature, top_k, top_p, min_p, u, M,
+                                             V, token, prob, s);
+    if (e != cudaErrorNotSupported) return e;
+    return launch(sample_any_kernel<true>, grid, block, 0, s, pdl, g);
+  }
   return launch(sample_any_kernel<false>, grid, block, 0, s, pdl, g);
 }
 

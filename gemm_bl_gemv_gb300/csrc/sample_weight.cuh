@@ -30,15 +30,25 @@ __device__ __forceinline__ Slope slope_of(float t) {
   return Slope{q, q > 0.f ? __fdiv_rn(rest, t) : 0.f};
 }
 
-// 2^(j/32) in units of 2^-44, j = -16..16.
+// 2^(j/32) in units of 2^-44, j = -16..16, rounded to nearest.
+constexpr int kExp2Entries = 33;
+__constant__ unsigned long long kExp2[kExp2Entries] = {
+    12439554047902ull, 12711944812080ull, 12990300157313ull, 13274750690919ull, 13565429880144ull,
+    13862474114787ull, 14166022771192ull, 14476218277651ull, 14793206181226ull, 15117135216047ull,
+    15448157373097ull, 15786427971528ull, 16132105731538ull, 16485352848846ull, 16846335070792ull,
+    17215221774115ull, 17592186044416ull, 17977404757381ull, 18371058661769ull, 18773332464219ull,
+    19184414915921ull, 19604498901178ull, 20033781527906ull, 20472464220127ull, 20920752812471ull,
+    21378857646762ull, 21846993670708ull, 22325380538761ull, 22814242715178ull, 23313809579344ull,
+    23824315533396ull, 24346000112214ull, 24879108095804ull};
+
+// The table in shared memory (lanes read different entries).
 struct Exp2Table {
-  unsigned long long v[33];
+  unsigned long long v[kExp2Entries];
 };
 
-// The table by the whole CTA (fp64, one entry per thread); the caller synchronizes.
+// By the whole CTA; the caller synchronizes.
 __device__ __forceinline__ void fill_exp2_table(Exp2Table& t) {
-  for (int j = threadIdx.x; j < 33; j += blockDim.x)
-    t.v[j] = static_cast<unsigned long long>(rint(exp2(double(j - 16) / 32.0) * double(1ull << kWeightBits)));
+  for (int j = threadIdx.x; j < kExp2Entries; j += blockDim.x) t.v[j] = kExp2[j];
 }
 
 // The weight of logit l: with -z = (l - max) log2(e) / T in pairs of floats,
@@ -84,6 +94,37 @@ __device__ __forceinline__ float share_of(float l, float top, Slope c, const Exp
   return float(double(w) * double(exp2i(-shift)) / double(kept));
 }
 
+// p * mass for 0 <= p < 1, rounded down (rest: whether a fraction was dropped),
+// in integers: exact, and no use of the slow fp64 pipe by a whole CTA.
+__device__ __forceinline__ unsigned long long scaled(float p, unsigned long long mass, bool& rest) {
+  const uint32_t b = __float_as_uint(p);
+  const uint32_t e = b >> 23;
+  const unsigned long long mant = (b & 0x7fffffu) | (e ? 0x800000u : 0u);  // p = mant 2^-sh, sh >= 24
+  const int sh = 150 - int(e ? e : 1u);
+  const unsigned long long lo = mass * mant, hi = __umul64hi(mass, mant);
+  if (sh < 64) {
+    rest = (lo << (64 - sh)) != 0;
+    return hi << (64 - sh) | lo >> sh;
+  }
+  if (sh < 128) {
+    rest = lo != 0 || (hi & ((1ull << (sh - 64)) - 1)) != 0;
+    return hi >> (sh - 64);
+  }
+  rest = (lo | hi) != 0;
+  return 0;
+}
+
+// ceil(p * mass) for 0 <= p < 1, and floor(u * mass) for 0 <= u < 1, mass > 0.
+__device__ __forceinline__ unsigned long long mass_limit(float p, unsigned long long mass) {
+  bool rest;
+  const unsigned long long q = scaled(p, mass, rest);
+  return q + rest;
+}
+__device__ __forceinline__ unsigned long long mass_target(float u, unsigned long long mass) {
+  bool rest;
+  return scaled(u, mass, rest);
+}
+
 // Row parameters after clamping.
 struct RowFilter {
   Slope slope;
@@ -100,22 +141,12 @@ __device__ __forceinline__ RowFilter row_filter(int64_t m, int64_t V, const floa
   f.top_k = (k <= 0 || k > V) ? V : k;
   const float p = top_p ? top_p[m] : 1.f;
   f.top_p = p < 1.f ? fmaxf(p, 0.f) : 2.f;
-  const float mp = min_p ? fminf(min_p[m], 1.f) : 0.f;
-  f.min_w = (min_p && min_p[m] > 0.f)
-                ? static_cast<unsigned long long>(ceil(double(mp) * double(1ull << kWeightBits)))
-                : 0ull;
+  const float mp = min_p ? min_p[m] : 0.f;
+  constexpr unsigned long long kOne = 1ull << kWeightBits;
+  f.min_w = mp > 0.f ? (mp < 1.f ? mass_limit(mp, kOne) : kOne) : 0ull;
   const float v = u[m];
   f.u = v > 0.f ? fminf(v, 0.99999994f) : 0.f;
   return f;
-}
-
-// ceil(p * mass) for 0 <= p < 1 and floor(u * mass) for 0 <= u < 1.
-__device__ __forceinline__ unsigned long long mass_limit(float p, unsigned long long mass) {
-  return static_cast<unsigned long long>(ceil(double(p) * double(mass)));
-}
-__device__ __forceinline__ unsigned long long mass_target(float u, unsigned long long mass) {
-  const unsigned long long t = static_cast<unsigned long long>(double(u) * double(mass));
-  return t < mass ? t : mass - 1;
 }
 
 }  // namespace bl
