@@ -6,11 +6,13 @@
 //
 // A cluster of C CTAs takes a row, each CTA a chunk of at most 65528 logits,
 // so that the 65536 counters fit in 16 bits each (128 KB): no counter can
-// overflow.  Then each CTA owns a slice of the bins (read from all C
-// histograms through distributed shared memory), every thread a few units of
-// 8 bins in falling order, and a place in the order is found by a scan over
-// the threads: the thread in whose bins a cumulative count or weight passes
-// the goal knows the place.
+// overflow.  The bins are cut into 1024 segments of 64; only the segments
+// that some CTA has hit (some tens, of a model's logits) are weighed, one
+// warp each, with the counts of all C histograms read through distributed
+// shared memory.  One warp of the first CTA then finds the places in the
+// order: first the segment in which a cumulative count or weight passes the
+// goal, then the bin.  The CTA whose chunk has the token looks up its index.
+// Clusters stay for several rows and clear only the segments that they hit.
 #include "bl_internal.h"
 #include "sample_weight.cuh"
 
@@ -22,6 +24,7 @@ using u64 = unsigned long long;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnits = 65536 / 8;            // units of 8 keys, 16 bytes of counters each
+constexpr int kSegments = 65536 / 64;        // segments of 64 keys, 32 words of counters
 constexpr int kMaxChunk = 65528;             // logits of a CTA: a counter stays below 2^16
 constexpr uint32_t kLowKey = 0x0080u;        // the lowest finite value; -inf and NaN lie below
 constexpr uint32_t kHighKey = 0xFF80u;       // +inf; NaN above
@@ -39,22 +42,33 @@ struct Args {
   int chunk;  // a multiple of 8
 };
 
+// A place in the order: the element of this key with `rank` others of the
+// same key before it; `before` is the weight of everything before that key.
 struct Place {
-  uint32_t key, pad;
+  uint32_t key;
   u64 rank, before, weight;
+};
+
+struct Segment {
+  u64 mass;
+  uint32_t count, index;
 };
 
 struct Shared {
   uint4 hist[kUnits];
-  Exp2Table exp2;
-  u64 warp_mass[kWarps];
-  uint32_t warp_count[kWarps];
-  uint32_t warp_max[kWarps];
   // read by the other CTAs of the cluster
-  uint32_t top, local[2];
-  u64 total_mass, total_count, min_mass;
-  Place place[3];
-  uint32_t pick[kWarps];
+  uint32_t bitmap[32];  // segments that this CTA has hit
+  uint32_t top;         // its largest key, 0 if it has no live logit
+  // written by the other CTAs (to rank 0's), in falling order
+  Segment seg[kSegments];
+  // written by rank 0
+  uint32_t pick_key, pick_rank, pick_owner;
+  u64 kept;
+  // local
+  u64 mass_before[kSegments];
+  uint32_t count_before[kSegments];
+  Exp2Table exp2;
+  uint32_t warp_max[kWarps], pick[kWarps];
 };
 
 template <class T>
@@ -99,6 +113,12 @@ __device__ __forceinline__ void load_keys(const uint16_t* row16, int off, int64_
   }
 }
 
+__device__ __forceinline__ u64 warp_sum_u64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 template <int C>
 __device__ __forceinline__ void sync_cluster() {
   if (C == 1)
@@ -107,148 +127,118 @@ __device__ __forceinline__ void sync_cluster() {
     cluster_sync();
 }
 
-template <int C>
-struct Sampler {
-  Shared& sh;
-  const uint32_t rank;
-  float top;
-  Slope slope;
-  int first_unit, units, per;  // falling units of the window; units of a thread
-  uint32_t count;              // of this thread's bins, of those before them
-  u64 mass, mass_before;
-  u64 count_before;
-
-  // Counters of a unit over the whole row.
-  __device__ __forceinline__ void unit_counts(int unit, uint32_t (&c)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = 0;
-#pragma unroll
-    for (int r = 0; r < C; ++r) {
-      const uint4 q = *(C == 1 ? &sh.hist[unit] : peer(&sh.hist[unit], r));
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[2 * j] += w[j] & 0xFFFFu;
-        c[2 * j + 1] += w[j] >> 16;
-      }
-    }
-  }
-  __device__ __forceinline__ u64 weight(uint32_t key) const { return weight_of(value_of(key), top, slope, sh.exp2); }
-
-  // Count and weight of this thread's bins, and of all before them.
-  __device__ __forceinline__ void scan() {
-    count = 0;
-    mass = 0;
-    const int d0 = (int(rank) * kThreads + int(threadIdx.x)) * per;
-    for (int i = 0; i < per && d0 + i < units; ++i) {
-      uint32_t c[8];
-      const int unit = first_unit - (d0 + i);
-      unit_counts(unit, c);
-#pragma unroll 1
-      for (int j = 7; j >= 0; --j) {
-        uint32_t n = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) n = e == j ? c[e] : n;
-        if (n) {
-          count += n;
-          mass += n * weight(unit * 8 + j);
-        }
-      }
-    }
-    uint32_t cs = count;
-    u64 ms = mass;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The live segments of a row in falling order, held by a warp: lane i has the
+// bits of word 31 - i, highest first.
+struct SegmentList {
+  uint32_t bits, upto;  // segments of this lane and the lanes before it
+  int n;
+  __device__ __forceinline__ SegmentList(uint32_t word, int lane) {
+    bits = word;
+    upto = __popc(word);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t c = __shfl_up_sync(0xffffffffu, cs, o);
-      const u64 m = __shfl_up_sync(0xffffffffu, ms, o);
-      if (lane >= o) cs += c, ms += m;
+      const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    if (lane == 31) sh.warp_count[warp] = cs, sh.warp_mass[warp] = ms;
-    __syncthreads();
-    u64 cb = 0, mb = 0, ct = 0, mt = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) cb = ct, mb = mt;
-      ct += sh.warp_count[w];
-      mt += sh.warp_mass[w];
-    }
-    if (threadIdx.x == 0) sh.total_count = ct, sh.total_mass = mt;
-    sync_cluster<C>();
-    if (C > 1)
-      for (uint32_t r = 0; r < rank; ++r) cb += *peer(&sh.total_count, r), mb += *peer(&sh.total_mass, r);
-    count_before = cb + cs - count;
-    mass_before = mb + ms - mass;
+    n = int(__shfl_sync(0xffffffffu, upto, 31));
   }
-
-  __device__ __forceinline__ u64 total_mass() const {
-    u64 t = 0;
-    for (uint32_t r = 0; r < C; ++r) t += C == 1 ? sh.total_mass : *peer(&sh.total_mass, r);
-    return t;
+  // The idx-th segment, idx < n (whole warp).
+  __device__ __forceinline__ uint32_t at(uint32_t idx, int lane) const {
+    const int src = __ffs(__ballot_sync(0xffffffffu, upto > idx)) - 1;
+    const uint32_t w = __shfl_sync(0xffffffffu, bits, src);
+    const uint32_t r = idx + __popc(w) - __shfl_sync(0xffffffffu, upto, src);
+    // lane b looks at bit 31 - b
+    const uint32_t above = lane == 0 ? 0u : w >> (32 - lane);
+    const bool here = ((w >> (31 - lane)) & 1u) && __popc(above) == int(r);
+    return 32u * (31 - src) + 31 - (__ffs(__ballot_sync(0xffffffffu, here)) - 1);
   }
+};
 
-  // The place where the cumulative count or weight first exceeds `goal`; the
-  // one thread that finds it tells all CTAs through slot `slot`.
-  __device__ __forceinline__ Place find(bool by_count, u64 goal, int slot) {
-    const u64 at = by_count ? count_before : mass_before;
-    const u64 mine = by_count ? count : mass;
-    if (at <= goal && goal - at < mine) {
-      u64 cb = count_before, mb = mass_before;
-      const int d0 = (int(rank) * kThreads + int(threadIdx.x)) * per;
-      bool done = false;
-      for (int i = 0; i < per && d0 + i < units && !done; ++i) {
-        uint32_t c[8];
-        const int unit = first_unit - (d0 + i);
-        unit_counts(unit, c);
-#pragma unroll 1
-        for (int j = 7; j >= 0 && !done; --j) {
-          uint32_t n = 0;
+template <int C>
+struct Row {
+  Shared& sh;
+  int lane;
+  float top;
+  Slope slope;
+  int n;  // live segments
+
+  __device__ __forceinline__ u64 weight(uint32_t key) const { return weight_of(value_of(key), top, slope, sh.exp2); }
+
+  // This lane's two bins of a segment, in falling order: keys k and k - 1.
+  struct Bins {
+    uint32_t key, c1, c0;
+    u64 w1, w0;
+  };
+  __device__ __forceinline__ Bins bins(uint32_t seg) const {
+    Bins b;
+    const uint32_t word = seg * 32 + 31 - lane;
+    b.key = 2 * word + 1;
+    b.c1 = b.c0 = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) n = e == j ? c[e] : n;
-          if (!n) continue;
-          const u64 w = weight(unit * 8 + j);
-          if (by_count ? goal - cb < n : goal - mb < n * w) {
-            const Place p{uint32_t(unit * 8 + j), 0u, by_count ? goal - cb : (goal - mb) / w, mb, w};
-            for (uint32_t r = 0; r < C; ++r) *(C == 1 ? &sh.place[slot] : peer(&sh.place[slot], r)) = p;
-            done = true;
-          }
-          cb += n;
-          mb += n * w;
-        }
+    for (int r = 0; r < C; ++r) {
+      const uint32_t* mine = reinterpret_cast<uint32_t*>(sh.hist) + word;
+      const uint32_t v = *(C == 1 ? mine : peer(mine, r));
+      b.c1 += v >> 16;
+      b.c0 += v & 0xFFFFu;
+    }
+    b.w1 = b.c1 ? weight(b.key) : 0;
+    b.w0 = b.c0 ? weight(b.key - 1) : 0;
+    return b;
+  }
+
+  // The place where the cumulative count or weight first exceeds `goal` (less
+  // than the whole); whole warp.
+  __device__ __forceinline__ Place find(bool by_count, u64 goal) const {
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      bool here = false;
+      if (i < n) {
+        const u64 at = by_count ? sh.count_before[i] : sh.mass_before[i];
+        here = at <= goal && goal - at < (by_count ? sh.seg[i].count : sh.seg[i].mass);
       }
+      const uint32_t hit = __ballot_sync(0xffffffffu, here);
+      if (!hit) continue;
+      const int s = i0 + __ffs(hit) - 1;
+      const Bins b = bins(sh.seg[s].index);
+      const u64 m1 = b.c1 * b.w1, m0 = b.c0 * b.w0;
+      u64 cm = m1 + m0;
+      uint32_t cc = b.c1 + b.c0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 m = __shfl_up_sync(0xffffffffu, cm, o);
+        const uint32_t c = __shfl_up_sync(0xffffffffu, cc, o);
+        if (lane >= o) cm += m, cc += c;
+      }
+      const u64 before = sh.mass_before[s] + cm - m1 - m0;
+      const u64 at = by_count ? u64(sh.count_before[s]) + cc - b.c1 - b.c0 : before;
+      const u64 n1 = by_count ? b.c1 : m1, n0 = by_count ? b.c0 : m0;
+      const bool in1 = at <= goal && goal - at < n1;
+      const bool in0 = at + n1 <= goal && goal - at - n1 < n0;
+      Place p{};
+      if (in1) p = Place{b.key, by_count ? goal - at : (goal - at) / b.w1, before, b.w1};
+      if (in0) p = Place{b.key - 1, by_count ? goal - at - n1 : (goal - at - n1) / b.w0, before + m1, b.w0};
+      const int src = __ffs(__ballot_sync(0xffffffffu, in1 || in0)) - 1;
+      p.key = __shfl_sync(0xffffffffu, p.key, src);
+      p.rank = __shfl_sync(0xffffffffu, p.rank, src);
+      p.before = __shfl_sync(0xffffffffu, p.before, src);
+      p.weight = __shfl_sync(0xffffffffu, p.weight, src);
+      return p;
     }
-    sync_cluster<C>();
-    return sh.place[slot];
+    return Place{};
   }
 
-  // Weight of the bins whose weight is at least `min_w`.
-  __device__ __forceinline__ u64 mass_from(u64 min_w) {
-    u64 m = 0;
-    const int d0 = (int(rank) * kThreads + int(threadIdx.x)) * per;
-    for (int i = 0; i < per && d0 + i < units && mass > 0; ++i) {
-      uint32_t c[8];
-      const int unit = first_unit - (d0 + i);
-      unit_counts(unit, c);
-#pragma unroll 1
-      for (int j = 7; j >= 0; --j) {
-        uint32_t n = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) n = e == j ? c[e] : n;
-        const u64 w = n ? weight(unit * 8 + j) : 0;
-        if (w >= min_w) m += n * w;
-      }
+  // Weight of the bins that weigh at least `min_w`: whole segments, and a part of one; whole warp.
+  __device__ __forceinline__ u64 mass_from(u64 min_w) const {
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const bool less = i < n && weight(max(sh.seg[i].index * 64, kLowKey)) < min_w;
+      const uint32_t hit = __ballot_sync(0xffffffffu, less);
+      if (!hit) continue;
+      const int s = i0 + __ffs(hit) - 1;
+      const Bins b = bins(sh.seg[s].index);
+      return sh.mass_before[s] + warp_sum_u64((b.w1 >= min_w ? b.c1 * b.w1 : 0) + (b.w0 >= min_w ? b.c0 * b.w0 : 0));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-    if ((threadIdx.x & 31) == 0) sh.warp_mass[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = 0;
-    for (int w = 0; w < kWarps; ++w) m += sh.warp_mass[w];
-    if (C == 1) return m;
-    if (threadIdx.x == 0) sh.min_mass = m;
-    cluster_sync();
-    m = 0;
-    for (uint32_t r = 0; r < C; ++r) m += *peer(&sh.min_mass, r);
-    return m;
+    return sh.mass_before[n - 1] + sh.seg[n - 1].mass;
   }
 };
 
@@ -257,156 +247,204 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
   extern __shared__ uint4 smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   const uint32_t rank = C == 1 ? 0 : cluster_ctarank();
-  const int64_t m = blockIdx.x / C;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t* words = reinterpret_cast<uint32_t*>(sh.hist);
   for (int i = threadIdx.x; i < kUnits; i += kThreads) sh.hist[i] = make_uint4(0, 0, 0, 0);
   fill_exp2_table(sh.exp2);
-  if (threadIdx.x < 2) sh.local[threadIdx.x] = 0;
   pdl_wait();
   __syncthreads();
 
-  // the chunk's histogram
-  const uint16_t* row = g.logits + m * g.V;
-  const int off = int((reinterpret_cast<uintptr_t>(row) >> 1) & 7);
-  const uint16_t* row16 = row - off;
-  const int64_t end = off + g.V;
-  const int64_t g0 = int64_t(rank) * (g.chunk / 8);
-  const int64_t g1 = min(g0 + g.chunk / 8, (end + 7) / 8);
-  uint32_t* words = reinterpret_cast<uint32_t*>(sh.hist);
-  uint32_t hi = 0;
-  for (int64_t i = g0 + threadIdx.x; i < g1; i += kThreads) {
-    uint32_t k[4];
-    load_keys(row16, off, end, i, k);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t key = (k[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-      if (key - kLowKey <= kHighKey - kLowKey) {
-        hi = max(hi, key);
-        atomicAdd(&words[key >> 1], 1u << (16 * (key & 1)));
-      }
-    }
-  }
-  hi = redux_max_u32(hi);
-  if (lane == 0) sh.warp_max[warp] = hi;
-  __syncthreads();
-  if (warp == 0) {
-    hi = redux_max_u32(sh.warp_max[lane]);
-    if (lane == 0) {
-      sh.top = hi == kZeroKey - 1 ? kZeroKey : hi;
-      // -0 counts as 0
-      const uint32_t n = words[(kZeroKey - 1) >> 1] >> 16;
-      words[(kZeroKey - 1) >> 1] &= 0xFFFFu;
-      words[kZeroKey >> 1] += n;
-    }
-  }
-  sync_cluster<C>();
-  hi = sh.top;
-  if (C > 1) {
-    hi = 0;
-    for (uint32_t r = 0; r < C; ++r) hi = max(hi, *peer(&sh.top, r));
-  }
-  if (hi == 0) {  // no live logit; the same in every CTA
-    if (rank == 0 && threadIdx.x == 0) {
-      g.token[m] = -1;
-      if (g.prob) g.prob[m] = 0.f;
-    }
-    if (C > 1) cluster_sync();
-    pdl_launch_dependents();
-    return;
-  }
+  for (int64_t m = blockIdx.x / C; m < g.M; m += gridDim.x / C) {
+    const RowFilter f = row_filter(m, g.V, g.temperature, g.top_k, g.top_p, g.min_p, g.u);
+    const float temp = g.temperature ? g.temperature[m] : 1.f;
 
-  const RowFilter f = row_filter(m, g.V, g.temperature, g.top_k, g.top_p, g.min_p, g.u);
-  const float top = value_of(hi);
-  uint32_t lo = hi;
-  if (f.slope.hi >= 0.f && hi < kHighKey) {
-    const float t = g.temperature ? g.temperature[m] : 1.f;
-    lo = max(kLowKey, key_of_f32(__fmaf_rn(-kWindow, t, top)) >> 16);
-  }
-  Sampler<C> s{sh, rank, top, f.slope};
-  s.first_unit = hi >> 3;
-  s.units = int(hi >> 3) - int(lo >> 3) + 1;
-  s.per = (s.units + C * kThreads - 1) / (C * kThreads);
-  s.scan();
-
-  Place endp{0, 0, 0, 0, 0};
-  u64 kept = s.total_mass();
-  bool whole = true;
-  if (f.top_k < g.V) {
-    u64 n = 0;
-    for (uint32_t r = 0; r < C; ++r) n += C == 1 ? sh.total_count : *peer(&sh.total_count, r);
-    if (u64(f.top_k) <= n) {  // otherwise the k-th token has no weight
-      endp = s.find(true, f.top_k - 1, 0);
-      kept = endp.before + (endp.rank + 1) * endp.weight;
-      whole = false;
-    }
-  }
-  if (f.top_p <= 1.f) {
-    const u64 limit = max(mass_limit(f.top_p, kept), u64(1));
-    endp = s.find(false, min(limit, kept) - 1, 1);
-    kept = endp.before + (endp.rank + 1) * endp.weight;
-    whole = false;
-  }
-  if (f.min_w > 0 && (whole || endp.weight < f.min_w)) kept = s.mass_from(f.min_w);
-  const Place at = s.find(false, mass_target(f.u, kept), 2);
-
-  // the element of that key with at.rank equal ones before it, in index order
-  auto local_count = [&](uint32_t r) {
-    const uint32_t w = *(C == 1 ? &words[at.key >> 1] : peer(&words[at.key >> 1], r));
-    return (w >> (16 * (at.key & 1))) & 0xFFFFu;
-  };
-  u64 want = at.rank;
-  uint32_t owner = 0;
-  if (C > 1)
-    for (; owner + 1 < C; ++owner) {
-      const uint32_t n = local_count(owner);
-      if (want < n) break;
-      want -= n;
-    }
-  if (C > 1) cluster_sync();  // the last read of another CTA's memory
-  if (rank == owner) {
-    // warps take contiguous ranges of groups; a warp counts, then the one that has the element walks
-    const int64_t n = g1 - g0, span = (n + kWarps - 1) / kWarps;
-    const int64_t w0 = g0 + warp * span, w1 = min(w0 + span, g1);
-    auto match = [&](int64_t i) {
-      uint32_t k[4], b = 0;
+    // the chunk's histogram
+    const uint16_t* row = g.logits + m * g.V;
+    const int off = int((reinterpret_cast<uintptr_t>(row) >> 1) & 7);
+    const uint16_t* row16 = row - off;
+    const int64_t end = off + g.V;
+    const int64_t g0 = int64_t(rank) * (g.chunk / 8);
+    const int64_t g1 = min(g0 + g.chunk / 8, (end + 7) / 8);
+    uint32_t hi = 0;
+    for (int64_t i = g0 + threadIdx.x; i < g1; i += kThreads) {
+      uint32_t k[4];
       load_keys(row16, off, end, i, k);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        uint32_t key = (k[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-        key += key == kZeroKey - 1;
-        b |= uint32_t(key == at.key) << j;
-      }
-      return b;
-    };
-    uint32_t mine = 0;
-    for (int64_t i = w0 + lane; i < w1; i += 32) mine += __popc(match(i));
-    mine = redux_add(int(mine));
-    if (lane == 0) sh.pick[warp] = mine;
-    __syncthreads();
-    uint32_t before = 0;
-    for (int w = 0; w < warp; ++w) before += sh.pick[w];
-    if (before <= want && want - before < mine) {
-      uint32_t left = uint32_t(want) - before;
-      for (int64_t i0 = w0; i0 < w1; i0 += 32) {
-        const uint32_t b = i0 + lane < w1 ? match(i0 + lane) : 0;
-        uint32_t incl = __popc(b);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
+        const uint32_t key = (k[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+        if (key - kLowKey <= kHighKey - kLowKey) {
+          hi = max(hi, key);
+          atomicAdd(&words[key >> 1], 1u << (16 * (key & 1)));
         }
-        const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
-        const uint32_t excl = incl - __popc(b);
-        if (left < all && left >= excl && left < incl) {
-          uint32_t bits = b;
-          for (uint32_t q = left - excl; q > 0; --q) bits &= bits - 1;
-          g.token[m] = int32_t((i0 + lane) * 8 + (__ffs(bits) - 1) - off);
-          if (g.prob) g.prob[m] = share_of(value_of(at.key), top, f.slope, sh.exp2, kept);
-        }
-        if (left < all) break;
-        left -= all;
       }
     }
+    hi = redux_max_u32(hi);
+    if (lane == 0) sh.warp_max[warp] = hi;
+    __syncthreads();
+    if (threadIdx.x == 0) {  // -0 counts as 0
+      const uint32_t neg = words[(kZeroKey - 1) >> 1] >> 16;
+      words[(kZeroKey - 1) >> 1] &= 0xFFFFu;
+      words[kZeroKey >> 1] += neg;
+    }
+    __syncthreads();
+    // which segments were hit: a warp reads four (512 bytes) at a time
+    for (int w = warp; w < 32; w += kWarps) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint4 v = sh.hist[(w * 8 + q) * 32 + lane];
+        const uint32_t b = __ballot_sync(0xffffffffu, (v.x | v.y | v.z | v.w) != 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bits |= uint32_t(((b >> (8 * e)) & 0xFFu) != 0) << (4 * q + e);
+      }
+      if (lane == 0) sh.bitmap[w] = bits;
+    }
+    if (warp == 0) {
+      hi = redux_max_u32(sh.warp_max[lane]);
+      if (lane == 0) sh.top = hi == kZeroKey - 1 ? kZeroKey : hi;
+    }
+    sync_cluster<C>();
+
+    uint32_t live = 0;  // lane i: word 31 - i of all CTAs' bitmaps
+    hi = 0;
+#pragma unroll
+    for (int r = 0; r < C; ++r) {
+      live |= *(C == 1 ? &sh.bitmap[31 - lane] : peer(&sh.bitmap[31 - lane], r));
+      hi = max(hi, *(C == 1 ? &sh.top : peer(&sh.top, r)));
+    }
+    Row<C> s{sh, lane, value_of(hi), f.slope, 0};
+    if (hi != 0) {
+      uint32_t lo = hi;
+      if (f.slope.hi >= 0.f && hi < kHighKey) lo = max(kLowKey, key_of_f32(__fmaf_rn(-kWindow, temp, s.top)) >> 16);
+      // segments from lo's on
+      const int from = int(lo >> 6) - 32 * (31 - lane);
+      live = from <= 0 ? live : (from < 32 ? live & (0xFFFFFFFFu << from) : 0u);
+      const SegmentList list(live, lane);
+      s.n = list.n;
+      for (int i = int(rank) * kWarps + warp; i < list.n; i += C * kWarps) {
+        const uint32_t seg = list.at(i, lane);
+        const typename Row<C>::Bins b = s.bins(seg);
+        const u64 mass = warp_sum_u64(b.c1 * b.w1 + b.c0 * b.w0);
+        const uint32_t count = uint32_t(redux_add(int(b.c1 + b.c0)));
+        if (lane == 0) *(C == 1 ? &sh.seg[i] : peer(&sh.seg[i], 0)) = Segment{mass, count, seg};
+      }
+    }
+    sync_cluster<C>();
+
+    if (rank == 0 && warp == 0 && hi != 0) {
+      u64 kept = 0;
+      uint32_t count = 0;
+      for (int i0 = 0; i0 < s.n; i0 += 32) {
+        const int i = i0 + lane;
+        const Segment e = i < s.n ? sh.seg[i] : Segment{0, 0, 0};
+        u64 cm = e.mass;
+        uint32_t cc = e.count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 v = __shfl_up_sync(0xffffffffu, cm, o);
+          const uint32_t c = __shfl_up_sync(0xffffffffu, cc, o);
+          if (lane >= o) cm += v, cc += c;
+        }
+        if (i < s.n) sh.mass_before[i] = kept + cm - e.mass, sh.count_before[i] = count + cc - e.count;
+        kept += __shfl_sync(0xffffffffu, cm, 31);
+        count += __shfl_sync(0xffffffffu, cc, 31);
+      }
+      __syncwarp();
+      Place last{};  // the last place that stays, unless all do
+      bool whole = true;
+      if (f.top_k < g.V && uint32_t(f.top_k) <= count) {  // beyond `count` tokens have no weight
+        last = s.find(true, f.top_k - 1);
+        kept = last.before + (last.rank + 1) * last.weight;
+        whole = false;
+      }
+      if (f.top_p <= 1.f) {
+        const u64 limit = max(mass_limit(f.top_p, kept), u64(1));
+        last = s.find(false, min(limit, kept) - 1);
+        kept = last.before + (last.rank + 1) * last.weight;
+        whole = false;
+      }
+      if (f.min_w > 0 && (whole || last.weight < f.min_w)) kept = s.mass_from(f.min_w);
+      const Place at = s.find(false, mass_target(f.u, kept));
+      // which CTA's chunk has it
+      uint32_t left = uint32_t(at.rank), owner = 0;
+#pragma unroll
+      for (int r = 0; r + 1 < C; ++r) {
+        const uint32_t v = *peer(&words[at.key >> 1], r);
+        const uint32_t c = (v >> (16 * (at.key & 1))) & 0xFFFFu;
+        if (owner == uint32_t(r) && left >= c) left -= c, ++owner;
+      }
+      if (lane < C) {
+        *(C == 1 ? &sh.pick_key : peer(&sh.pick_key, lane)) = at.key;
+        *(C == 1 ? &sh.pick_rank : peer(&sh.pick_rank, lane)) = left;
+        *(C == 1 ? &sh.pick_owner : peer(&sh.pick_owner, lane)) = owner;
+        *(C == 1 ? &sh.kept : peer(&sh.kept, lane)) = kept;
+      }
+    }
+    sync_cluster<C>();
+
+    // clear what was hit: warp w the segments of word w
+    for (int w = warp; w < 32; w += kWarps)
+      for (uint32_t bits = sh.bitmap[w]; bits; bits &= bits - 1) words[(w * 32 + __ffs(bits) - 1) * 32 + lane] = 0;
+
+    if (hi == 0) {
+      if (rank == 0 && threadIdx.x == 0) {
+        g.token[m] = -1;
+        if (g.prob) g.prob[m] = 0.f;
+      }
+    } else if (rank == sh.pick_owner) {
+      // the element of that key with `want` equal ones before it in the chunk: warps take contiguous
+      // ranges of groups and keep the matches of each, at most kMaxChunk / 8 / kWarps / 32 = 8 per lane
+      const uint32_t key_at = sh.pick_key, want = sh.pick_rank;
+      const int n = int(g1 - g0), span = (n + kWarps - 1) / kWarps;
+      const int64_t w0 = g0 + warp * span;
+      const int wn = max(0, min(span, n - warp * span));
+      u64 found = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (q * 32 + lane < wn) {
+          uint32_t k[4], b = 0;
+          load_keys(row16, off, end, w0 + q * 32 + lane, k);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t key = (k[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+            key += key == kZeroKey - 1;
+            b |= uint32_t(key == key_at) << j;
+          }
+          found |= u64(b) << (8 * q);
+        }
+      }
+      const uint32_t mine = uint32_t(redux_add(__popcll(found)));
+      if (lane == 0) sh.pick[warp] = mine;
+      __syncthreads();
+      const uint32_t before = uint32_t(redux_add(lane < warp ? int(sh.pick[lane]) : 0));
+      if (before <= want && want - before < mine) {
+        uint32_t left = want - before;
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t b = uint32_t(found >> (8 * q)) & 0xFFu;
+          const uint32_t all = uint32_t(redux_add(__popc(b)));
+          if (left >= all) {
+            left -= all;
+            continue;
+          }
+          uint32_t excl = __popc(b);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, excl, o);
+            if (lane >= o) excl += v;
+          }
+          excl -= __popc(b);
+          if (left >= excl && left - excl < uint32_t(__popc(b))) {
+            uint32_t bits = b;
+            for (uint32_t e = left - excl; e > 0; --e) bits &= bits - 1;
+            g.token[m] = int32_t((w0 + q * 32 + lane) * 8 + (__ffs(bits) - 1) - off);
+            if (g.prob) g.prob[m] = share_of(value_of(key_at), s.top, f.slope, sh.exp2, sh.kept);
+          }
+          break;
+        }
+      }
+    }
+    __syncthreads();  // the cleared histogram, before the next row's
   }
   pdl_launch_dependents();
 }
@@ -418,7 +456,7 @@ cudaError_t launch_rows(const Args& g, cudaStream_t s) {
   cudaError_t e = raise_smem_cap(sample_bf16_kernel<C>, dev, int(sizeof(Shared)));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(g.M * C));
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(g.M, std::max(1, sm_count() / C)) * C));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = s;
@@ -448,7 +486,7 @@ cudaError_t launch_sample_bf16(const uint16_t* logits, const float* temperature,
   auto chunk_of = [&](int c) { return ((V + 7 + c - 1) / c + 7) / 8 * 8; };
   int c = 1;
   while (c < 8 && (chunk_of(c) > kMaxChunk || (M * c * 2 <= sm_count() && chunk_of(c) > 8 * kThreads))) c *= 2;
-  if (chunk_of(c) > kMaxChunk || M * c > 0x7fffffff) return cudaErrorNotSupported;
+  if (chunk_of(c) > kMaxChunk) return cudaErrorNotSupported;
   const Args g{logits, temperature, top_p, min_p, u, top_k, M, V, token, prob, int(chunk_of(c))};
   switch (c) {
     case 1: return launch_rows<1>(g, s);
