@@ -165,8 +165,7 @@ cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, 
 cudaError_t launch_sample(const void* logits, bl_dtype lt, const float* temperature, const int32_t* top_k,
                           const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V,
                           int32_t* token, float* prob, cudaStream_t s);
-// bf16 logits (csrc/sample_bf16.cu); cudaErrorNotSupported, having launched
-// nothing, for rows longer than its eight chunks.
+// bf16 logits (csrc/sample_bf16.cu)
 cudaError_t launch_sample_bf16(const uint16_t* logits, const float* temperature, const int32_t* top_k,
                                const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V,
                                int32_t* token, float* prob, cudaStream_t s);

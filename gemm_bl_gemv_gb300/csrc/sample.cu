@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(1024) sample_any_kernel(const Args g) {
     pdl_launch_dependents();
     return;
   }
-  const RowFilter f = row_filter(m, g.V, g.temperature, g.top_k, g.top_p, g.min_p, g.u);
+  const RowFilter f = row_filter(RowValues(m, g.temperature, g.top_k, g.top_p, g.min_p, g.u), g.V);
   row.top = t + 0.f;
   row.slope = f.slope;
   Place end{0, 0, 0, 0};  // the last place that stays
@@ -190,12 +190,9 @@ cudaError_t launch_sample(const void* logits, bl_dtype lt, const float* temperat
   const Args g{logits, temperature, top_p, min_p, u, top_k, M, V, token, prob};
   const bool pdl = overlap_enabled();
   const dim3 grid{unsigned(M)}, block{1024};
-  if (lt == BL_BF16) {
-    const cudaError_t e = launch_sample_bf16(static_cast<const uint16_t*>(logits), temperature, top_k, top_p, min_p, u, M,
-                                             V, token, prob, s);
-    if (e != cudaErrorNotSupported) return e;
-    return launch(sample_any_kernel<true>, grid, block, 0, s, pdl, g);
-  }
+  if (lt == BL_BF16)
+    return launch_sample_bf16(static_cast<const uint16_t*>(logits), temperature, top_k, top_p, min_p, u, M, V, token,
+                              prob, s);
   return launch(sample_any_kernel<false>, grid, block, 0, s, pdl, g);
 }
 

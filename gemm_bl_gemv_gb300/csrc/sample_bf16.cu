@@ -4,15 +4,24 @@
 // tokens is the order of the bins.  No exp per logit, one shared-memory
 // atomic per logit.
 //
-// A cluster of C CTAs takes a row, each CTA a chunk of at most 65528 logits,
-// so that the 65536 counters fit in 16 bits each (128 KB): no counter can
-// overflow.  The bins are cut into 1024 segments of 64; only the segments
-// that some CTA has hit (some tens, of a model's logits) are weighed, one
-// warp each, with the counts of all C histograms read through distributed
-// shared memory.  One warp of the first CTA then finds the places in the
-// order: first the segment in which a cumulative count or weight passes the
-// goal, then the bin.  The CTA whose chunk has the token looks up its index.
-// Clusters stay for several rows and clear only the segments that they hit.
+// A cluster of C CTAs takes a row, each CTA a chunk of it.  Word i of a CTA's
+// histogram (128 KB) counts the positive logits of magnitude bits i in its
+// low half and the negative ones in its high half, so a logit finds its
+// counter without being turned into a key.  A counter holds 16 bits: before
+// one could overflow, a chunk of more than 65535 logits looks for the largest
+// counter and moves what is above half of the range to a short list.  The
+// bins are cut into 1024 segments of 64; only the segments that some CTA has
+// hit (some tens, of a model's logits) are weighed, one warp each, with the
+// counts of all C histograms read through distributed shared memory.  One
+// warp of the first CTA then finds the places in the order: first the segment
+// in which a cumulative count or weight passes the goal, then the bin.  The
+// CTA whose chunk has the token looks up its index while the next row's
+// places are found.  Clusters stay for several rows, clear only the segments
+// that they hit, and fetch the next row into L2 while they search.
+//
+// Bound: a random shared-memory atomic takes 3.5 clocks per warp (bank
+// conflicts, as a plain load's; measured), 23 us for 256 rows of 248320 logits
+// on 152 SMs, whose bytes take 18.7 us at the copy rate.
 #include "bl_internal.h"
 #include "sample_weight.cuh"
 
@@ -23,12 +32,13 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnits = 65536 / 8;            // units of 8 keys, 16 bytes of counters each
-constexpr int kSegments = 65536 / 64;        // segments of 64 keys, 32 words of counters
-constexpr int kMaxChunk = 65528;             // logits of a CTA: a counter stays below 2^16
-constexpr uint32_t kLowKey = 0x0080u;        // the lowest finite value; -inf and NaN lie below
-constexpr uint32_t kHighKey = 0xFF80u;       // +inf; NaN above
-constexpr uint32_t kZeroKey = 0x8000u;       // 0; 0x7fff is -0
+constexpr int kWords = 32768;                // counters of one magnitude: low half positive, high half negative
+constexpr int kSegments = 1024;              // 64 magnitudes of one sign each, in falling order
+constexpr int kBatch = 128;                  // groups of 8 logits that a warp looks through at a time
+constexpr int kMaxBatches = 524288 / 8 / kBatch + 1;
+constexpr int kSpills = 32;                  // at most 524288 / 32767 counters are moved
+constexpr uint32_t kMasked2 = 0xFF80FF80u;   // two logits of -inf
+constexpr uint32_t kInf = 0x7F80u;           // magnitude bits of an infinity; above: NaN
 // weights below 2^-45 of the largest are 0: no bin further than 46 octaves (31.9 T) matters
 constexpr float kWindow = 32.f;
 
@@ -42,33 +52,51 @@ struct Args {
   int chunk;  // a multiple of 8
 };
 
-// A place in the order: the element of this key with `rank` others of the
-// same key before it; `before` is the weight of everything before that key.
+// A place in the order: the logit of these bf16 bits with `rank` equal ones
+// before it; `before` is the weight of everything before those.
 struct Place {
-  uint32_t key;
+  uint32_t bits;
   u64 rank, before, weight;
 };
 
+// A segment with the sums over all CTAs.  index: its place among the 1024,
+// 0..511 positive (magnitudes falling), 512..1023 negative (rising).
 struct Segment {
   u64 mass;
   uint32_t count, index;
 };
 
+struct Spill {
+  uint32_t bits, count;
+};
+
+// What the lookup of a token's index needs, kept until the next row's search.
+struct Pick {
+  uint32_t bits, rank;
+  u64 kept;
+  float top;
+  Slope slope;
+};
+
 struct Shared {
-  uint4 hist[kUnits];
+  uint32_t hist[kWords];
   // read by the other CTAs of the cluster
-  uint32_t bitmap[32];  // segments that this CTA has hit
-  uint32_t top;         // its largest key, 0 if it has no live logit
+  uint16_t bitmap[64];  // segments that this CTA has hit: 16 positive per entry (rising), then 16 negative per entry
+  uint32_t top;         // its largest live logit's bits + 1, 0 if there is none
+  uint32_t spills;      // counters moved to the list
+  Spill spill[kSpills];
   // written by the other CTAs (to rank 0's), in falling order
   Segment seg[kSegments];
   // written by rank 0
-  uint32_t pick_key, pick_rank, pick_owner;
+  uint32_t pick_bits, pick_rank, pick_owner;
   u64 kept;
   // local
   u64 mass_before[kSegments];
   uint32_t count_before[kSegments];
   Exp2Table exp2;
-  uint32_t warp_max[kWarps], pick[kWarps];
+  Pick pick;
+  uint32_t warp_max[kWarps];
+  uint32_t matches[kMaxBatches + 31];  // by batch
 };
 
 template <class T>
@@ -78,40 +106,46 @@ __device__ __forceinline__ T* peer(T* p, uint32_t rank) {
   return reinterpret_cast<T*>(a);
 }
 
-// Keys of two packed bf16 values.
-__device__ __forceinline__ uint32_t keys2(uint32_t w) {
-  const uint32_t s = (w >> 15) & 0x00010001u;
-  return w ^ (((s << 15) - s) | 0x80008000u);
+__device__ __forceinline__ float value_of(uint32_t bits) { return __uint_as_float(bits << 16); }
+__device__ __forceinline__ uint32_t order_of(uint32_t bits) {  // rises with the value
+  return (bits & 0x8000u) ? 0xFFFFu - bits : bits | 0x8000u;
 }
-__device__ __forceinline__ float value_of(uint32_t key) { return f32_of_key(key << 16 | ((key & 0x8000u) ? 0u : 0xFFFFu)); }
 
-// The 8 logits of group `grp` (aligned in memory) as keys; those outside the
-// row are 0, a NaN's key.  `row16` is the 16-byte aligned start, `off` the
-// row's first element in it.
-__device__ __forceinline__ void load_keys(const uint16_t* row16, int off, int64_t end, int64_t grp, uint32_t (&k)[4]) {
-  const int64_t v = grp * 8;
-  if (v >= off && v + 8 <= end) {
-    const uint4 q = reinterpret_cast<const uint4*>(row16)[grp];
-    k[0] = keys2(q.x);
-    k[1] = keys2(q.y);
-    k[2] = keys2(q.z);
-    k[3] = keys2(q.w);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t w = 0;
-    const int64_t i = v + 2 * j;
-    if (i >= off && i < end) w = row16[i];
-    uint32_t key = keys2(w) & 0xFFFFu;
-    if (i < off || i >= end) key = 0;
-    w = 0;
-    if (i + 1 >= off && i + 1 < end) w = row16[i + 1];
-    uint32_t key1 = keys2(w) & 0xFFFFu;
-    if (i + 1 < off || i + 1 >= end) key1 = 0;
-    k[j] = key | key1 << 16;
-  }
+// Count two logits; -inf and negative NaN are left out (a mask would put them
+// all on one address), positive NaN are cleared later.
+__device__ __forceinline__ void count_pair(uint32_t* hist, uint32_t w) {
+  char* h = reinterpret_cast<char*>(hist);
+  if ((w << 16) < (0x8000u + kInf) << 16)
+    atomicAdd(reinterpret_cast<uint32_t*>(h + ((w << 2) & 0x1FFFCu)), (w & 0x8000u) ? 0x10000u : 1u);
+  if (w < (0x8000u + kInf) << 16)
+    atomicAdd(reinterpret_cast<uint32_t*>(h + ((w >> 14) & 0x1FFFCu)), (w & 0x80000000u) ? 0x10000u : 1u);
 }
+__device__ __forceinline__ void count_group(uint32_t* hist, uint4 q) {
+  count_pair(hist, q.x);
+  count_pair(hist, q.y);
+  count_pair(hist, q.z);
+  count_pair(hist, q.w);
+}
+
+// The logits of one value.
+struct Target {
+  uint32_t two, mask;  // in both halves; -0 equals 0
+  __device__ __forceinline__ explicit Target(uint32_t bits)
+      : two(bits | bits << 16), mask(bits == 0 ? 0x7FFF7FFFu : 0xFFFFFFFFu) {}
+  __device__ __forceinline__ uint32_t in(uint32_t w) const {
+    const uint32_t t = (w ^ two) & mask;
+    return uint32_t((t & 0xFFFFu) == 0) | uint32_t((t >> 16) == 0) << 1;
+  }
+  // bit j: logit j of the group has the value; most groups fail the quick test (a zero half of w ^ target)
+  __device__ __forceinline__ uint32_t in(const uint4& q) const {
+    auto zero = [&](uint32_t w) {
+      const uint32_t t = (w ^ two) & mask;
+      return (t - 0x00010001u) & ~t;
+    };
+    if (((zero(q.x) | zero(q.y) | zero(q.z) | zero(q.w)) & 0x80008000u) == 0) return 0;
+    return in(q.x) | in(q.y) << 2 | in(q.z) << 4 | in(q.w) << 6;
+  }
+};
 
 __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
 #pragma unroll
@@ -127,10 +161,10 @@ __device__ __forceinline__ void sync_cluster() {
     cluster_sync();
 }
 
-// The live segments of a row in falling order, held by a warp: lane i has the
-// bits of word 31 - i, highest first.
+// The live segments of a row in falling order, held by a warp: lane i has
+// segments 32 i .. 32 i + 31, from the highest bit down.
 struct SegmentList {
-  uint32_t bits, upto;  // segments of this lane and the lanes before it
+  uint32_t bits, upto;  // segments of this lane; of this lane and those before it
   int n;
   __device__ __forceinline__ SegmentList(uint32_t word, int lane) {
     bits = word;
@@ -150,9 +184,15 @@ struct SegmentList {
     // lane b looks at bit 31 - b
     const uint32_t above = lane == 0 ? 0u : w >> (32 - lane);
     const bool here = ((w >> (31 - lane)) & 1u) && __popc(above) == int(r);
-    return 32u * (31 - src) + 31 - (__ffs(__ballot_sync(0xffffffffu, here)) - 1);
+    return 32u * src + __ffs(__ballot_sync(0xffffffffu, here)) - 1;
   }
 };
+
+// Of a bitmap (Shared::bitmap), lane i's word of a SegmentList.
+__device__ __forceinline__ uint32_t list_word(const uint16_t* bitmap, int lane) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(bitmap);
+  return lane < 16 ? w[15 - lane] : __brev(w[lane]);
+}
 
 template <int C>
 struct Row {
@@ -160,29 +200,42 @@ struct Row {
   int lane;
   float top;
   Slope slope;
-  int n;  // live segments
+  int n;        // live segments
+  bool spills;  // some CTA has moved counters
 
-  __device__ __forceinline__ u64 weight(uint32_t key) const { return weight_of(value_of(key), top, slope, sh.exp2); }
+  __device__ __forceinline__ u64 weight(uint32_t bits) const { return weight_of(value_of(bits), top, slope, sh.exp2); }
 
-  // This lane's two bins of a segment, in falling order: keys k and k - 1.
+  // This lane's two bins of a segment, in falling order.
   struct Bins {
-    uint32_t key, c1, c0;
+    uint32_t bits1, bits0, c1, c0;
     u64 w1, w0;
   };
   __device__ __forceinline__ Bins bins(uint32_t seg) const {
     Bins b;
-    const uint32_t word = seg * 32 + 31 - lane;
-    b.key = 2 * word + 1;
+    const bool neg = seg >= 512;
+    const uint32_t word = neg ? (seg - 512) * 64 + 2 * lane : (511 - seg) * 64 + 62 - 2 * lane;  // of two
     b.c1 = b.c0 = 0;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
-      const uint32_t* mine = reinterpret_cast<uint32_t*>(sh.hist) + word;
-      const uint32_t v = *(C == 1 ? mine : peer(mine, r));
-      b.c1 += v >> 16;
-      b.c0 += v & 0xFFFFu;
+      const uint2* mine = reinterpret_cast<uint2*>(&sh.hist[word]);
+      const uint2 v = *(C == 1 ? mine : peer(mine, r));
+      b.c1 += neg ? v.x >> 16 : v.y & 0xFFFFu;
+      b.c0 += neg ? v.y >> 16 : v.x & 0xFFFFu;
     }
-    b.w1 = b.c1 ? weight(b.key) : 0;
-    b.w0 = b.c0 ? weight(b.key - 1) : 0;
+    b.bits1 = neg ? 0x8000u + word : word + 1;
+    b.bits0 = neg ? 0x8001u + word : word;
+    if (spills) {
+      for (int r = 0; r < C; ++r) {
+        const uint32_t moved = *(C == 1 ? &sh.spills : peer(&sh.spills, r));
+        for (uint32_t i = 0; i < moved; ++i) {
+          const Spill e = *(C == 1 ? &sh.spill[i] : peer(&sh.spill[i], r));
+          b.c1 += e.bits == b.bits1 ? e.count : 0;
+          b.c0 += e.bits == b.bits0 ? e.count : 0;
+        }
+      }
+    }
+    b.w1 = b.c1 ? weight(b.bits1) : 0;
+    b.w0 = b.c0 ? weight(b.bits0) : 0;
     return b;
   }
 
@@ -215,10 +268,10 @@ struct Row {
       const bool in1 = at <= goal && goal - at < n1;
       const bool in0 = at + n1 <= goal && goal - at - n1 < n0;
       Place p{};
-      if (in1) p = Place{b.key, by_count ? goal - at : (goal - at) / b.w1, before, b.w1};
-      if (in0) p = Place{b.key - 1, by_count ? goal - at - n1 : (goal - at - n1) / b.w0, before + m1, b.w0};
+      if (in1) p = Place{b.bits1, by_count ? goal - at : (goal - at) / b.w1, before, b.w1};
+      if (in0) p = Place{b.bits0, by_count ? goal - at - n1 : (goal - at - n1) / b.w0, before + m1, b.w0};
       const int src = __ffs(__ballot_sync(0xffffffffu, in1 || in0)) - 1;
-      p.key = __shfl_sync(0xffffffffu, p.key, src);
+      p.bits = __shfl_sync(0xffffffffu, p.bits, src);
       p.rank = __shfl_sync(0xffffffffu, p.rank, src);
       p.before = __shfl_sync(0xffffffffu, p.before, src);
       p.weight = __shfl_sync(0xffffffffu, p.weight, src);
@@ -231,7 +284,10 @@ struct Row {
   __device__ __forceinline__ u64 mass_from(u64 min_w) const {
     for (int i0 = 0; i0 < n; i0 += 32) {
       const int i = i0 + lane;
-      const bool less = i < n && weight(max(sh.seg[i].index * 64, kLowKey)) < min_w;
+      const uint32_t seg = i < n ? sh.seg[i].index : 0;
+      // its smallest value's bits (of finite ones)
+      const uint32_t last = seg < 512 ? (511 - seg) * 64 : 0x8000u + min((seg - 512) * 64 + 63, kInf - 1);
+      const bool less = i < n && weight(last) < min_w;
       const uint32_t hit = __ballot_sync(0xffffffffu, less);
       if (!hit) continue;
       const int s = i0 + __ffs(hit) - 1;
@@ -242,101 +298,274 @@ struct Row {
   }
 };
 
+// A CTA's part of a row: groups of 8 logits that are aligned in memory.  The
+// row starts at element `off` of group 0 and ends before element `end`; of the
+// chunk's groups [g0, g1), [ga, gb) are whole.
+struct Chunk {
+  const uint16_t* row16;
+  int off, end, g0, g1, ga, gb;
+  __device__ __forceinline__ Chunk(const uint16_t* row, int V, int rank, int groups) {
+    off = int((reinterpret_cast<uintptr_t>(row) >> 1) & 7);
+    row16 = row - off;
+    end = off + V;
+    g0 = rank * groups;
+    g1 = min(g0 + groups, (end + 7) / 8);
+    ga = max(g0, (off + 7) / 8);
+    gb = min(g1, end / 8);
+  }
+  __device__ __forceinline__ uint4 whole(int i) const { return reinterpret_cast<const uint4*>(row16)[i]; }
+  // Any group of the chunk: logits outside the row, and groups outside the chunk, are `other`.
+  __device__ __forceinline__ uint4 group(int i, uint32_t other) const {
+    if (i >= ga && i < gb) return whole(i);
+    uint32_t w[4] = {other, other, other, other};
+    if (i >= g0 && i < g1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = i * 8 + j;
+        if (e >= off && e < end) w[j >> 1] = __byte_perm(w[j >> 1], row16[e], (j & 1) ? 0x5410 : 0x3254);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// The index of the logit of row m of value `bits` with `rank` equal ones before
+// it in the chunk (Shared::pick), by warps 1.. of the CTA: matches are counted by batches of
+// groups, and one warp walks the batch that has it.
+__device__ __forceinline__ void look_up(const Args& g, Shared& sh, int64_t m, int rank) {
+  constexpr int kPickWarps = kWarps - 1;
+  const int lane = threadIdx.x & 31, warp = int(threadIdx.x >> 5) - 1;
+  const Chunk c(g.logits + m * g.V, int(g.V), rank, g.chunk / 8);
+  const Target target(sh.pick.bits);
+  const int batches = (c.g1 - c.g0 + kBatch - 1) / kBatch;
+  for (int b = warp; b < batches; b += 2 * kPickWarps) {
+    uint4 q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = c.g0 + (b + (j >> 2) * kPickWarps) * kBatch + (j & 3) * 32 + lane;
+      q[j] = i >= c.ga && i < c.gb ? c.whole(i) : make_uint4(~target.two, ~target.two, ~target.two, ~target.two);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = b + h * kPickWarps;
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) n += __popc(target.in(q[4 * h + j]));
+      // parts of groups: only the chunk's first and last group can be one
+      const int edge = lane == 0 && at == 0 ? c.g0 : lane == 1 && at == batches - 1 && c.g1 - 1 > c.g0 ? c.g1 - 1 : -1;
+      if (edge >= 0 && (edge < c.ga || edge >= c.gb)) n += __popc(target.in(c.group(edge, ~target.two)));
+      n = redux_add(n);
+      if (lane == 0 && at < batches) sh.matches[at] = n;
+    }
+  }
+  named_barrier_sync(1, 32 * kPickWarps);
+  if (warp != 0) return;
+  uint32_t left = sh.pick.rank;
+  for (int b0 = 0; b0 < batches; b0 += 32) {
+    const uint32_t n = b0 + lane < batches ? sh.matches[b0 + lane] : 0;
+    const uint32_t all = uint32_t(redux_add(int(n)));
+    if (left >= all) {
+      left -= all;
+      continue;
+    }
+    uint32_t upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, upto > left)) - 1;
+    left -= __shfl_sync(0xffffffffu, upto - n, src);
+    const int first = c.g0 + (b0 + src) * kBatch + lane;
+    uint32_t hits = 0;  // of this lane's four groups
+#pragma unroll
+    for (int j = 0; j < 4; ++j) hits |= target.in(c.group(first + 32 * j, ~target.two)) << (8 * j);
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      uint32_t bits = (hits >> (8 * j)) & 0xFFu;
+      uint32_t incl = __popc(bits);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t here = __shfl_sync(0xffffffffu, incl, 31), excl = incl - __popc(bits);
+      if (left >= excl && left < incl) {
+        for (uint32_t e = left - excl; e > 0; --e) bits &= bits - 1;
+        const Pick& p = sh.pick;
+        g.token[m] = (first + 32 * j) * 8 + (__ffs(bits) - 1) - c.off;
+        if (g.prob) g.prob[m] = share_of(value_of(p.bits), p.top, p.slope, sh.exp2, p.kept);
+      }
+      if (left < here) break;
+      left -= here;
+    }
+    break;
+  }
+}
+
+// The largest counter of the CTA's histogram, after moving what exceeds 1 of
+// every counter of at least 2^15 to the list, so that it stays below 2^15.
+// Whole CTA; ends with a barrier.
+__device__ __forceinline__ uint32_t largest_counter(Shared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t most = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int at = q * kThreads + int(threadIdx.x);
+    uint4& v = reinterpret_cast<uint4*>(sh.hist)[at];
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if ((w[0] | w[1] | w[2] | w[3]) & 0x80008000u) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t n = (w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+        if (n < 0x8000u) continue;
+        w[j >> 1] -= (n - 1) << (16 * (j & 1));
+        const uint32_t magnitude = at * 4 + (j >> 1);
+        if (magnitude > kInf) continue;  // NaN
+        const uint32_t i = atomicAdd(&sh.spills, 1u);  // at most 524288 / 32767 times
+        sh.spill[i] = Spill{magnitude == 0 ? 0u : magnitude | (j & 1) << 15, n - 1};
+      }
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) most = __vmaxu2(most, w[j]);
+  }
+  most = redux_max_u32(max(most & 0xFFFFu, most >> 16));
+  if (lane == 0) sh.warp_max[warp] = most;
+  __syncthreads();
+  most = redux_max_u32(sh.warp_max[lane]);
+  __syncthreads();
+  return most;
+}
+
 template <int C>
 __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
   extern __shared__ uint4 smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   const uint32_t rank = C == 1 ? 0 : cluster_ctarank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t* words = reinterpret_cast<uint32_t*>(sh.hist);
-  for (int i = threadIdx.x; i < kUnits; i += kThreads) sh.hist[i] = make_uint4(0, 0, 0, 0);
+  uint4* hist4 = reinterpret_cast<uint4*>(sh.hist);
+  for (int i = threadIdx.x; i < kWords / 4; i += kThreads) hist4[i] = make_uint4(0, 0, 0, 0);
   fill_exp2_table(sh.exp2);
+  if (threadIdx.x == 0) sh.spills = 0;
+  int64_t pick_row = -1;  // the row whose token is in this CTA's chunk and still to be looked up
   pdl_wait();
   __syncthreads();
 
   for (int64_t m = blockIdx.x / C; m < g.M; m += gridDim.x / C) {
-    const RowFilter f = row_filter(m, g.V, g.temperature, g.top_k, g.top_p, g.min_p, g.u);
-    const float temp = g.temperature ? g.temperature[m] : 1.f;
-
-    // the chunk's histogram
+    const RowValues values(m, g.temperature, g.top_k, g.top_p, g.min_p, g.u);
     const uint16_t* row = g.logits + m * g.V;
-    const int off = int((reinterpret_cast<uintptr_t>(row) >> 1) & 7);
-    const uint16_t* row16 = row - off;
-    const int64_t end = off + g.V;
-    const int64_t g0 = int64_t(rank) * (g.chunk / 8);
-    const int64_t g1 = min(g0 + g.chunk / 8, (end + 7) / 8);
-    uint32_t hi = 0;
-    for (int64_t i = g0 + threadIdx.x; i < g1; i += kThreads) {
-      uint32_t k[4];
-      load_keys(row16, off, end, i, k);
+    const Chunk c(row, int(g.V), int(rank), g.chunk / 8);
+
+    // histogram; the row's first and last part of a group by one thread each
+    if (threadIdx.x < 2) {
+      const int part = threadIdx.x == 0 ? 0 : c.end / 8;
+      if ((part < c.ga || part >= c.gb) && (threadIdx.x == 0 || part > 0))
+        count_group(sh.hist, c.group(part, kMasked2));
+    }
+    for (int from = c.ga, room = 65535 - 16; from < c.gb;) {
+      const int to = min(c.gb, from + room / 8);
+      for (int i = from + int(threadIdx.x); i < to; i += 4 * kThreads) {
+        uint4 q[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t key = (k[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-        if (key - kLowKey <= kHighKey - kLowKey) {
-          hi = max(hi, key);
-          atomicAdd(&words[key >> 1], 1u << (16 * (key & 1)));
-        }
+        for (int j = 0; j < 4; ++j)
+          q[j] = i + j * kThreads < to ? c.whole(i + j * kThreads) : make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) count_group(sh.hist, q[j]);
+      }
+      from = to;
+      if (from < c.gb) {
+        __syncthreads();
+        room = 65535 - int(largest_counter(sh));
       }
     }
-    hi = redux_max_u32(hi);
-    if (lane == 0) sh.warp_max[warp] = hi;
-    __syncthreads();
-    if (threadIdx.x == 0) {  // -0 counts as 0
-      const uint32_t neg = words[(kZeroKey - 1) >> 1] >> 16;
-      words[(kZeroKey - 1) >> 1] &= 0xFFFFu;
-      words[kZeroKey >> 1] += neg;
+    if (m + gridDim.x / C < g.M) {  // this chunk of the next row, into L2, a line per thread
+      const uint16_t* next = row + (gridDim.x / C) * g.V + int64_t(rank) * g.chunk;
+      const int n = min(int64_t(g.chunk), g.V - int64_t(rank) * g.chunk);
+      for (int at = int(threadIdx.x) * 64; at < n; at += 64 * kThreads)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(next + at));
     }
+    const RowFilter f = row_filter(values, g.V);
     __syncthreads();
-    // which segments were hit: a warp reads four (512 bytes) at a time
-    for (int w = warp; w < 32; w += kWarps) {
-      uint32_t bits = 0;
+    // -0 counts as 0; no NaN; which segments were hit: a lane looks through half of one (8 x 16
+    // bytes, from a start that keeps the lanes on different banks), a warp through 16 of both signs
+    {
+      uint32_t any = 0;
+      const int half = (warp * 16 + (lane & 15)) * 16 + (lane >> 4) * 8;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const uint4 v = sh.hist[(w * 8 + q) * 32 + lane];
-        const uint32_t b = __ballot_sync(0xffffffffu, (v.x | v.y | v.z | v.w) != 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bits |= uint32_t(((b >> (8 * e)) & 0xFFu) != 0) << (4 * q + e);
+        const int at = half + ((q + lane) & 7);
+        uint4 v = hist4[at];
+        if (at == 0) {
+          v.x = (v.x & 0xFFFFu) + (v.x >> 16);
+          if (v.x > 0xFFFFu) {
+            sh.spill[atomicAdd(&sh.spills, 1u)] = Spill{0u, v.x - 1};
+            v.x = 1;
+          }
+          sh.hist[0] = v.x;
+        }
+        if (at >= int(kInf) / 4) {
+          v.x = at == int(kInf) / 4 ? v.x & 0xFFFFu : 0u;
+          v.y = v.z = v.w = 0;
+          hist4[at] = v;
+        }
+        any |= v.x | v.y | v.z | v.w;
       }
-      if (lane == 0) sh.bitmap[w] = bits;
+      any |= __shfl_xor_sync(0xffffffffu, any, 16);
+      const uint32_t bl = __ballot_sync(0xffffffffu, (any & 0xFFFFu) != 0);
+      const uint32_t bh = __ballot_sync(0xffffffffu, (any >> 16) != 0);
+      if (lane == 0) sh.bitmap[warp] = uint16_t(bl), sh.bitmap[32 + warp] = uint16_t(bh);
     }
-    if (warp == 0) {
-      hi = redux_max_u32(sh.warp_max[lane]);
-      if (lane == 0) sh.top = hi == kZeroKey - 1 ? kZeroKey : hi;
+    __syncthreads();
+    if (warp == 0) {  // the largest logit: the first bin of the first segment
+      const SegmentList mine(list_word(sh.bitmap, lane), lane);
+      uint32_t top = 0;
+      if (mine.n > 0) {
+        const Row<1> one{sh, lane, INFINITY, f.slope, 0, false};  // weights are not used
+        const typename Row<1>::Bins b = one.bins(mine.at(0, lane));
+        const int src = __ffs(__ballot_sync(0xffffffffu, (b.c1 | b.c0) != 0)) - 1;
+        top = 1 + __shfl_sync(0xffffffffu, b.c1 ? b.bits1 : b.bits0, src);
+      }
+      if (lane == 0) sh.top = top;
     }
     sync_cluster<C>();
 
-    uint32_t live = 0;  // lane i: word 31 - i of all CTAs' bitmaps
-    hi = 0;
+    uint32_t live = 0, top = 0, moved = 0;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
-      live |= *(C == 1 ? &sh.bitmap[31 - lane] : peer(&sh.bitmap[31 - lane], r));
-      hi = max(hi, *(C == 1 ? &sh.top : peer(&sh.top, r)));
+      live |= list_word(C == 1 ? sh.bitmap : peer(sh.bitmap, r), lane);
+      const uint32_t t = *(C == 1 ? &sh.top : peer(&sh.top, r));
+      moved |= *(C == 1 ? &sh.spills : peer(&sh.spills, r));
+      if (t != 0 && (top == 0 || order_of(t - 1) > order_of(top - 1))) top = t;
     }
-    Row<C> s{sh, lane, value_of(hi), f.slope, 0};
-    if (hi != 0) {
-      uint32_t lo = hi;
-      if (f.slope.hi >= 0.f && hi < kHighKey) lo = max(kLowKey, key_of_f32(__fmaf_rn(-kWindow, temp, s.top)) >> 16);
-      // segments from lo's on
-      const int from = int(lo >> 6) - 32 * (31 - lane);
-      live = from <= 0 ? live : (from < 32 ? live & (0xFFFFFFFFu << from) : 0u);
+    const bool empty = top == 0;  // no logit above -inf
+    Row<C> s{sh, lane, value_of(top - 1), f.slope, 0, moved != 0};
+    if (!empty) {
+      float low = s.top;
+      if (f.slope.hi >= 0.f && top - 1 != kInf) low = __fmaf_rn(-kWindow, values.temperature, s.top);
+      const uint32_t lb = __float_as_uint(low) >> 16;  // towards 0: a negative one's own segment or one before
+      const int seg = (lb & 0x8000u) ? 512 + int(min((lb & 0x7FFFu) + 1, kInf) >> 6) : 511 - int(lb >> 6);
+      // segments up to that one
+      const int here = seg - 32 * lane;
+      live = here >= 31 ? live : (here < 0 ? 0u : live & ~(0x7FFFFFFFu >> here));
       const SegmentList list(live, lane);
       s.n = list.n;
-      for (int i = int(rank) * kWarps + warp; i < list.n; i += C * kWarps) {
-        const uint32_t seg = list.at(i, lane);
-        const typename Row<C>::Bins b = s.bins(seg);
+      for (int j = int(rank) * kWarps + warp; j < list.n; j += C * kWarps) {
+        const uint32_t index = list.at(j, lane);
+        const typename Row<C>::Bins b = s.bins(index);
         const u64 mass = warp_sum_u64(b.c1 * b.w1 + b.c0 * b.w0);
         const uint32_t count = uint32_t(redux_add(int(b.c1 + b.c0)));
-        if (lane == 0) *(C == 1 ? &sh.seg[i] : peer(&sh.seg[i], 0)) = Segment{mass, count, seg};
+        if (lane == 0) *(C == 1 ? &sh.seg[j] : peer(&sh.seg[j], 0)) = Segment{mass, count, index};
       }
     }
     sync_cluster<C>();
 
-    if (rank == 0 && warp == 0 && hi != 0) {
+    if (rank == 0 && warp == 0 && !empty) {
       u64 kept = 0;
       uint32_t count = 0;
       for (int i0 = 0; i0 < s.n; i0 += 32) {
-        const int i = i0 + lane;
-        const Segment e = i < s.n ? sh.seg[i] : Segment{0, 0, 0};
+        const int j = i0 + lane;
+        const Segment e = j < s.n ? sh.seg[j] : Segment{0, 0, 0};
         u64 cm = e.mass;
         uint32_t cc = e.count;
 #pragma unroll
@@ -345,7 +574,7 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
           const uint32_t c = __shfl_up_sync(0xffffffffu, cc, o);
           if (lane >= o) cm += v, cc += c;
         }
-        if (i < s.n) sh.mass_before[i] = kept + cm - e.mass, sh.count_before[i] = count + cc - e.count;
+        if (j < s.n) sh.mass_before[j] = kept + cm - e.mass, sh.count_before[j] = count + cc - e.count;
         kept += __shfl_sync(0xffffffffu, cm, 31);
         count += __shfl_sync(0xffffffffu, cc, 31);
       }
@@ -369,83 +598,40 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
       uint32_t left = uint32_t(at.rank), owner = 0;
 #pragma unroll
       for (int r = 0; r + 1 < C; ++r) {
-        const uint32_t v = *peer(&words[at.key >> 1], r);
-        const uint32_t c = (v >> (16 * (at.key & 1))) & 0xFFFFu;
-        if (owner == uint32_t(r) && left >= c) left -= c, ++owner;
+        const uint32_t v = *peer(&sh.hist[at.bits & 0x7FFFu], r);
+        uint32_t n = (at.bits & 0x8000u) ? v >> 16 : v & 0xFFFFu;
+        if (s.spills)
+          for (uint32_t i = 0; i < *peer(&sh.spills, r); ++i)
+            n += peer(&sh.spill[i], r)->bits == at.bits ? peer(&sh.spill[i], r)->count : 0;
+        if (owner == uint32_t(r) && left >= n) left -= n, ++owner;
       }
       if (lane < C) {
-        *(C == 1 ? &sh.pick_key : peer(&sh.pick_key, lane)) = at.key;
+        *(C == 1 ? &sh.pick_bits : peer(&sh.pick_bits, lane)) = at.bits;
         *(C == 1 ? &sh.pick_rank : peer(&sh.pick_rank, lane)) = left;
         *(C == 1 ? &sh.pick_owner : peer(&sh.pick_owner, lane)) = owner;
         *(C == 1 ? &sh.kept : peer(&sh.kept, lane)) = kept;
       }
     }
+    if (warp != 0 && pick_row >= 0) look_up(g, sh, pick_row, int(rank));  // of the row before this one
     sync_cluster<C>();
 
-    // clear what was hit: warp w the segments of word w
-    for (int w = warp; w < 32; w += kWarps)
-      for (uint32_t bits = sh.bitmap[w]; bits; bits &= bits - 1) words[(w * 32 + __ffs(bits) - 1) * 32 + lane] = 0;
-
-    if (hi == 0) {
+    pick_row = -1;
+    if (empty) {
       if (rank == 0 && threadIdx.x == 0) {
         g.token[m] = -1;
         if (g.prob) g.prob[m] = 0.f;
       }
     } else if (rank == sh.pick_owner) {
-      // the element of that key with `want` equal ones before it in the chunk: warps take contiguous
-      // ranges of groups and keep the matches of each, at most kMaxChunk / 8 / kWarps / 32 = 8 per lane
-      const uint32_t key_at = sh.pick_key, want = sh.pick_rank;
-      const int n = int(g1 - g0), span = (n + kWarps - 1) / kWarps;
-      const int64_t w0 = g0 + warp * span;
-      const int wn = max(0, min(span, n - warp * span));
-      u64 found = 0;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (q * 32 + lane < wn) {
-          uint32_t k[4], b = 0;
-          load_keys(row16, off, end, w0 + q * 32 + lane, k);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t key = (k[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
-            key += key == kZeroKey - 1;
-            b |= uint32_t(key == key_at) << j;
-          }
-          found |= u64(b) << (8 * q);
-        }
-      }
-      const uint32_t mine = uint32_t(redux_add(__popcll(found)));
-      if (lane == 0) sh.pick[warp] = mine;
-      __syncthreads();
-      const uint32_t before = uint32_t(redux_add(lane < warp ? int(sh.pick[lane]) : 0));
-      if (before <= want && want - before < mine) {
-        uint32_t left = want - before;
-#pragma unroll 1
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t b = uint32_t(found >> (8 * q)) & 0xFFu;
-          const uint32_t all = uint32_t(redux_add(__popc(b)));
-          if (left >= all) {
-            left -= all;
-            continue;
-          }
-          uint32_t excl = __popc(b);
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, excl, o);
-            if (lane >= o) excl += v;
-          }
-          excl -= __popc(b);
-          if (left >= excl && left - excl < uint32_t(__popc(b))) {
-            uint32_t bits = b;
-            for (uint32_t e = left - excl; e > 0; --e) bits &= bits - 1;
-            g.token[m] = int32_t((w0 + q * 32 + lane) * 8 + (__ffs(bits) - 1) - off);
-            if (g.prob) g.prob[m] = share_of(value_of(key_at), s.top, f.slope, sh.exp2, sh.kept);
-          }
-          break;
-        }
-      }
+      pick_row = m;
+      if (threadIdx.x == 0) sh.pick = Pick{sh.pick_bits, sh.pick_rank, sh.kept, s.top, f.slope};
     }
+    // clear what was hit (both signs share the words): warp w its 16 segments
+    for (uint32_t bits = sh.bitmap[warp] | sh.bitmap[32 + warp]; bits; bits &= bits - 1)
+      reinterpret_cast<uint2*>(sh.hist)[(warp * 16 + __ffs(bits) - 1) * 32 + lane] = make_uint2(0, 0);
+    if (threadIdx.x == 0) sh.spills = 0;
     __syncthreads();  // the cleared histogram, before the next row's
   }
+  if (warp != 0 && pick_row >= 0) look_up(g, sh, pick_row, int(rank));
   pdl_launch_dependents();
 }
 
@@ -479,16 +665,22 @@ cudaError_t launch_rows(const Args& g, cudaStream_t s) {
 
 }  // namespace
 
-// cudaErrorNotSupported, having launched nothing, for rows too long for eight chunks.
 cudaError_t launch_sample_bf16(const uint16_t* logits, const float* temperature, const int32_t* top_k,
                                const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V,
                                int32_t* token, float* prob, cudaStream_t s) {
   auto chunk_of = [&](int c) { return ((V + 7 + c - 1) / c + 7) / 8 * 8; };
-  int c = 1;
-  while (c < 8 && (chunk_of(c) > kMaxChunk || (M * c * 2 <= sm_count() && chunk_of(c) > 8 * kThreads))) c *= 2;
-  if (chunk_of(c) > kMaxChunk) return cudaErrorNotSupported;
-  const Args g{logits, temperature, top_p, min_p, u, top_k, M, V, token, prob, int(chunk_of(c))};
-  switch (c) {
+  // The number of CTAs of a row: a row costs each of them about 8 us beside its histogram, which takes
+  // 0.06 ns per logit of its chunk, and sm_count / c rows run at a time.  (One row of 248320: 8 CTAs
+  // KK us, 1 KK us; 256 rows: 1 CTA KK us, 4 KK us.)
+  int best = 1;
+  double least = 0;
+  for (int c = 1; c <= 8; c *= 2) {
+    const int64_t at_once = std::max(1, sm_count() / c);
+    const double t = double((M + at_once - 1) / at_once) * (8000.0 + 0.06 * double(chunk_of(c)));
+    if (c == 1 || t < 0.95 * least) best = c, least = t;
+  }
+  const Args g{logits, temperature, top_p, min_p, u, top_k, M, V, token, prob, int(chunk_of(best))};
+  switch (best) {
     case 1: return launch_rows<1>(g, s);
     case 2: return launch_rows<2>(g, s);
     case 4: return launch_rows<4>(g, s);

@@ -125,7 +125,16 @@ __device__ __forceinline__ unsigned long long mass_target(float u, unsigned long
   return scaled(u, mass, rest);
 }
 
-// Row parameters after clamping.
+// A row's parameters as given (loaded early, used late).
+struct RowValues {
+  float temperature, top_p, min_p, u;
+  int top_k;
+  __device__ __forceinline__ RowValues(int64_t m, const float* t, const int32_t* k, const float* p, const float* mp,
+                                       const float* uniform)
+      : temperature(t ? t[m] : 1.f), top_p(p ? p[m] : 1.f), min_p(mp ? mp[m] : 0.f), u(uniform[m]), top_k(k ? k[m] : 0) {}
+};
+
+// They after clamping.
 struct RowFilter {
   Slope slope;
   long long top_k;           // tokens that stay by count
@@ -133,19 +142,14 @@ struct RowFilter {
   unsigned long long min_w;  // smallest weight that stays (0: no limit)
 };
 
-__device__ __forceinline__ RowFilter row_filter(int64_t m, int64_t V, const float* temperature, const int32_t* top_k,
-                                                const float* top_p, const float* min_p, const float* u) {
-  RowFilter f;
-  f.slope = slope_of(temperature ? temperature[m] : 1.f);
-  const int k = top_k ? top_k[m] : 0;
-  f.top_k = (k <= 0 || k > V) ? V : k;
-  const float p = top_p ? top_p[m] : 1.f;
-  f.top_p = p < 1.f ? fmaxf(p, 0.f) : 2.f;
-  const float mp = min_p ? min_p[m] : 0.f;
+__device__ __forceinline__ RowFilter row_filter(const RowValues& r, int64_t V) {
   constexpr unsigned long long kOne = 1ull << kWeightBits;
-  f.min_w = mp > 0.f ? (mp < 1.f ? mass_limit(mp, kOne) : kOne) : 0ull;
-  const float v = u[m];
-  f.u = v > 0.f ? fminf(v, 0.99999994f) : 0.f;
+  RowFilter f;
+  f.slope = slope_of(r.temperature);
+  f.top_k = (r.top_k <= 0 || r.top_k > V) ? V : r.top_k;
+  f.top_p = r.top_p < 1.f ? fmaxf(r.top_p, 0.f) : 2.f;
+  f.min_w = r.min_p > 0.f ? (r.min_p < 1.f ? mass_limit(r.min_p, kOne) : kOne) : 0ull;
+  f.u = r.u > 0.f ? fminf(r.u, 0.99999994f) : 0.f;
   return f;
 }
 
