@@ -16,8 +16,8 @@
 // warp of the first CTA then finds the places in the order: first the segment
 // in which a cumulative count or weight passes the goal, then the bin.  The
 // CTA whose chunk has the token looks up its index while the next row's
-// places are found.  Clusters stay for several rows, clear only the segments
-// that they hit, and fetch the next row into L2 while they search.
+// places are found.  Clusters stay for several rows and clear only the segments
+// that they hit.
 //
 // Bound: a random shared-memory atomic takes 3.5 clocks per warp (bank
 // conflicts, as a plain load's; measured), 23 us for 256 rows of 248320 logits
@@ -35,7 +35,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kWords = 32768;                // counters of one magnitude: low half positive, high half negative
 constexpr int kSegments = 1024;              // 64 magnitudes of one sign each, in falling order
 constexpr int kBatch = 128;                  // groups of 8 logits that a warp looks through at a time
-constexpr int kMaxBatches = 524288 / 8 / kBatch + 1;
 constexpr int kSpills = 32;                  // at most 524288 / 32767 counters are moved
 constexpr uint32_t kMasked2 = 0xFF80FF80u;   // two logits of -inf
 constexpr uint32_t kInf = 0x7F80u;           // magnitude bits of an infinity; above: NaN
@@ -96,7 +95,7 @@ struct Shared {
   Exp2Table exp2;
   Pick pick;
   uint32_t warp_max[kWarps];
-  uint32_t matches[kMaxBatches + 31];  // by batch
+  uint32_t matches[2][2 * kWarps];  // by batch of a round
 };
 
 template <class T>
@@ -111,16 +110,25 @@ __device__ __forceinline__ uint32_t order_of(uint32_t bits) {  // rises with the
   return (bits & 0x8000u) ? 0xFFFFu - bits : bits | 0x8000u;
 }
 
-// Count two logits; -inf and negative NaN are left out (a mask would put them
-// all on one address), positive NaN are cleared later.
-__device__ __forceinline__ void count_pair(uint32_t* hist, uint32_t w) {
-  char* h = reinterpret_cast<char*>(hist);
-  if ((w << 16) < (0x8000u + kInf) << 16)
-    atomicAdd(reinterpret_cast<uint32_t*>(h + ((w << 2) & 0x1FFFCu)), (w & 0x8000u) ? 0x10000u : 1u);
-  if (w < (0x8000u + kInf) << 16)
-    atomicAdd(reinterpret_cast<uint32_t*>(h + ((w >> 14) & 0x1FFFCu)), (w & 0x80000000u) ? 0x10000u : 1u);
+// Count a logit whose bits are the upper half of `w`, at byte offset `at` of
+// the histogram; -inf and negative NaN are left out (a mask would put them all
+// on one address), positive NaN are cleared later.  A predicated instruction:
+// a branch around each atomic costs more than the atomic.
+__device__ __forceinline__ void count_logit(uint32_t hist, uint32_t w, uint32_t at) {
+  asm volatile(
+      "{\n\t.reg .pred live, neg;\n\t.reg .u32 one;\n\t"
+      "setp.lt.u32 live, %0, 0xFF800000;\n\t"
+      "setp.lt.s32 neg, %0, 0;\n\t"
+      "selp.u32 one, 0x10000, 1, neg;\n\t"
+      "@live red.shared.add.u32 [%1], one;\n\t}" ::"r"(w),
+      "r"(hist + at)
+      : "memory");
 }
-__device__ __forceinline__ void count_group(uint32_t* hist, uint4 q) {
+__device__ __forceinline__ void count_pair(uint32_t hist, uint32_t w) {
+  count_logit(hist, w << 16, (w << 2) & 0x1FFFCu);
+  count_logit(hist, w, (w >> 14) & 0x1FFFCu);
+}
+__device__ __forceinline__ void count_group(uint32_t hist, uint4 q) {
   count_pair(hist, q.x);
   count_pair(hist, q.y);
   count_pair(hist, q.z);
@@ -234,8 +242,8 @@ struct Row {
         }
       }
     }
-    b.w1 = b.c1 ? weight(b.bits1) : 0;
-    b.w0 = b.c0 ? weight(b.bits0) : 0;
+    b.w1 = weight(b.bits1);
+    b.w0 = weight(b.bits0);
     return b;
   }
 
@@ -330,53 +338,59 @@ struct Chunk {
 };
 
 // The index of the logit of row m of value `bits` with `rank` equal ones before
-// it in the chunk (Shared::pick), by warps 1.. of the CTA: matches are counted by batches of
-// groups, and one warp walks the batch that has it.
+// it in the chunk (Shared::pick), by warps 1.. of the CTA: matches are counted
+// by batches of groups, and one warp walks the batch that has it.
 __device__ __forceinline__ void look_up(const Args& g, Shared& sh, int64_t m, int rank) {
   constexpr int kPickWarps = kWarps - 1;
   const int lane = threadIdx.x & 31, warp = int(threadIdx.x >> 5) - 1;
   const Chunk c(g.logits + m * g.V, int(g.V), rank, g.chunk / 8);
   const Target target(sh.pick.bits);
-  const int batches = (c.g1 - c.g0 + kBatch - 1) / kBatch;
-  for (int b = warp; b < batches; b += 2 * kPickWarps) {
+  uint32_t left = sh.pick.rank;
+  // rounds of two batches per warp, in order, until the matches suffice
+  constexpr int kRound = 2 * kPickWarps;
+  for (int b0 = 0;; b0 += kRound) {
     uint4 q[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = c.g0 + (b + (j >> 2) * kPickWarps) * kBatch + (j & 3) * 32 + lane;
+      const int i = c.g0 + (b0 + warp + (j >> 2) * kPickWarps) * kBatch + (j & 3) * 32 + lane;
       q[j] = i >= c.ga && i < c.gb ? c.whole(i) : make_uint4(~target.two, ~target.two, ~target.two, ~target.two);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int at = b + h * kPickWarps;
+      const int first = c.g0 + (b0 + warp + h * kPickWarps) * kBatch;
       int n = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) n += __popc(target.in(q[4 * h + j]));
       // parts of groups: only the chunk's first and last group can be one
-      const int edge = lane == 0 && at == 0 ? c.g0 : lane == 1 && at == batches - 1 && c.g1 - 1 > c.g0 ? c.g1 - 1 : -1;
-      if (edge >= 0 && (edge < c.ga || edge >= c.gb)) n += __popc(target.in(c.group(edge, ~target.two)));
+      const int edge = lane == 0 ? c.g0 : c.g1 - 1;
+      if (lane < 2 && (lane == 0 || edge > c.g0) && edge >= first && edge < first + kBatch &&
+          (edge < c.ga || edge >= c.gb))
+        n += __popc(target.in(c.group(edge, ~target.two)));
       n = redux_add(n);
-      if (lane == 0 && at < batches) sh.matches[at] = n;
+      if (lane == 0) sh.matches[(b0 / kRound) & 1][warp + h * kPickWarps] = n;
     }
-  }
-  named_barrier_sync(1, 32 * kPickWarps);
-  if (warp != 0) return;
-  uint32_t left = sh.pick.rank;
-  for (int b0 = 0; b0 < batches; b0 += 32) {
-    const uint32_t n = b0 + lane < batches ? sh.matches[b0 + lane] : 0;
-    const uint32_t all = uint32_t(redux_add(int(n)));
-    if (left >= all) {
+    named_barrier_sync(1, 32 * kPickWarps);
+    const uint32_t* counts = sh.matches[(b0 / kRound) & 1];  // the other half is for the next round
+    const uint32_t n0 = counts[2 * lane < kRound ? 2 * lane : 0] * (2 * lane < kRound);
+    const uint32_t n1 = counts[2 * lane < kRound ? 2 * lane + 1 : 0] * (2 * lane < kRound);
+    const uint32_t all = uint32_t(redux_add(int(n0 + n1)));
+    if (left >= all && c.g0 + (b0 + kRound) * kBatch < c.g1) {
       left -= all;
       continue;
     }
-    uint32_t upto = n;
+    if (warp != 0) return;
+    uint32_t upto = n0 + n1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
     const int src = __ffs(__ballot_sync(0xffffffffu, upto > left)) - 1;
-    left -= __shfl_sync(0xffffffffu, upto - n, src);
-    const int first = c.g0 + (b0 + src) * kBatch + lane;
+    left -= __shfl_sync(0xffffffffu, upto - n0 - n1, src);
+    const uint32_t half = __shfl_sync(0xffffffffu, n0, src);
+    const int batch = b0 + 2 * src + (left >= half);
+    left -= left >= half ? half : 0;
+    const int first = c.g0 + batch * kBatch + lane;
     uint32_t hits = 0;  // of this lane's four groups
 #pragma unroll
     for (int j = 0; j < 4; ++j) hits |= target.in(c.group(first + 32 * j, ~target.two)) << (8 * j);
@@ -399,43 +413,44 @@ __device__ __forceinline__ void look_up(const Args& g, Shared& sh, int64_t m, in
       if (left < here) break;
       left -= here;
     }
-    break;
+    return;
   }
 }
 
-// The largest counter of the CTA's histogram, after moving what exceeds 1 of
-// every counter of at least 2^15 to the list, so that it stays below 2^15.
-// Whole CTA; ends with a barrier.
+// The largest counter of the CTA's histogram; counters of at least 2^15 are
+// moved to the list but for 1, so it stays below 2^15.  Whole CTA; ends with a
+// barrier.
 __device__ __forceinline__ uint32_t largest_counter(Shared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t most = 0;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int at = q * kThreads + int(threadIdx.x);
-    uint4& v = reinterpret_cast<uint4*>(sh.hist)[at];
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if ((w[0] | w[1] | w[2] | w[3]) & 0x80008000u) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t n = (w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+  for (int q = 0; q < kWords / 4 / kThreads; ++q) {
+    const uint4 v = reinterpret_cast<const uint4*>(sh.hist)[q * kThreads + threadIdx.x];
+    most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x, v.y), __vmaxu2(v.z, v.w)));
+  }
+  uint32_t mine = max(most & 0xFFFFu, most >> 16);
+  if (mine >= 0x8000u) {  // few threads, rarely
+    for (int q = 0; q < kWords / kThreads; ++q) {
+      const uint32_t magnitude = (q / 4 * kThreads + threadIdx.x) * 4 + q % 4;
+      uint32_t w = sh.hist[magnitude];
+      for (int sign = 0; sign < 2; ++sign) {
+        const uint32_t n = (w >> (16 * sign)) & 0xFFFFu;
         if (n < 0x8000u) continue;
-        w[j >> 1] -= (n - 1) << (16 * (j & 1));
-        const uint32_t magnitude = at * 4 + (j >> 1);
+        w -= (n - 1) << (16 * sign);
         if (magnitude > kInf) continue;  // NaN
         const uint32_t i = atomicAdd(&sh.spills, 1u);  // at most 524288 / 32767 times
-        sh.spill[i] = Spill{magnitude == 0 ? 0u : magnitude | (j & 1) << 15, n - 1};
+        sh.spill[i] = Spill{magnitude == 0 ? 0u : magnitude | sign << 15, n - 1};
       }
-      v = make_uint4(w[0], w[1], w[2], w[3]);
+      sh.hist[magnitude] = w;
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) most = __vmaxu2(most, w[j]);
+    mine = 0x7FFFu;
   }
-  most = redux_max_u32(max(most & 0xFFFFu, most >> 16));
-  if (lane == 0) sh.warp_max[warp] = most;
+  mine = redux_max_u32(mine);
+  if (lane == 0) sh.warp_max[warp] = mine;
   __syncthreads();
-  most = redux_max_u32(sh.warp_max[lane]);
+  mine = redux_max_u32(sh.warp_max[lane]);
   __syncthreads();
-  return most;
+  return mine;
 }
 
 template <int C>
@@ -445,6 +460,7 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
   const uint32_t rank = C == 1 ? 0 : cluster_ctarank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4* hist4 = reinterpret_cast<uint4*>(sh.hist);
+  const uint32_t hist = smem_addr(sh.hist);
   for (int i = threadIdx.x; i < kWords / 4; i += kThreads) hist4[i] = make_uint4(0, 0, 0, 0);
   fill_exp2_table(sh.exp2);
   if (threadIdx.x == 0) sh.spills = 0;
@@ -461,7 +477,7 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
     if (threadIdx.x < 2) {
       const int part = threadIdx.x == 0 ? 0 : c.end / 8;
       if ((part < c.ga || part >= c.gb) && (threadIdx.x == 0 || part > 0))
-        count_group(sh.hist, c.group(part, kMasked2));
+        count_group(hist, c.group(part, kMasked2));
     }
     for (int from = c.ga, room = 65535 - 16; from < c.gb;) {
       const int to = min(c.gb, from + room / 8);
@@ -471,19 +487,13 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
         for (int j = 0; j < 4; ++j)
           q[j] = i + j * kThreads < to ? c.whole(i + j * kThreads) : make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) count_group(sh.hist, q[j]);
+        for (int j = 0; j < 4; ++j) count_group(hist, q[j]);
       }
       from = to;
       if (from < c.gb) {
         __syncthreads();
         room = 65535 - int(largest_counter(sh));
       }
-    }
-    if (m + gridDim.x / C < g.M) {  // this chunk of the next row, into L2, a line per thread
-      const uint16_t* next = row + (gridDim.x / C) * g.V + int64_t(rank) * g.chunk;
-      const int n = min(int64_t(g.chunk), g.V - int64_t(rank) * g.chunk);
-      for (int at = int(threadIdx.x) * 64; at < n; at += 64 * kThreads)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(next + at));
     }
     const RowFilter f = row_filter(values, g.V);
     __syncthreads();

@@ -41,32 +41,34 @@ __constant__ unsigned long long kExp2[kExp2Entries] = {
     21378857646762ull, 21846993670708ull, 22325380538761ull, 22814242715178ull, 23313809579344ull,
     23824315533396ull, 24346000112214ull, 24879108095804ull};
 
-// The table in shared memory (lanes read different entries).
+// The table in shared memory (lanes read different entries), with each entry
+// in units of 2^8 as a float.
 struct Exp2Table {
-  unsigned long long v[kExp2Entries];
+  ulonglong2 v[kExp2Entries];
 };
 
 // By the whole CTA; the caller synchronizes.
 __device__ __forceinline__ void fill_exp2_table(Exp2Table& t) {
-  for (int j = threadIdx.x; j < kExp2Entries; j += blockDim.x) t.v[j] = kExp2[j];
+  for (int j = threadIdx.x; j < kExp2Entries; j += blockDim.x)
+    t.v[j] = make_ulonglong2(kExp2[j], __float_as_uint(__ull2float_rn(kExp2[j] >> 8)));
 }
 
 // The weight of logit l: with -z = (l - max) log2(e) / T in pairs of floats,
 // 2^-z = 2^n 2^(j/32) 2^r, |r| <= 1/64: the power of two is a shift, 2^(j/32)
 // comes from the table, and 2^r - 1 <= 2^-6.5 is a polynomial in float, whose
 // 2^-24 relative error leaves about 2^-30 of the weight.
-// `shift` receives -n: the result is not shifted yet.
+// `shift` receives -n: the result is not shifted yet.  No branches: callers
+// have several in flight.
 __device__ __forceinline__ unsigned long long weight_mantissa(float l, float top, Slope c, const Exp2Table& t,
                                                               int& shift) {
-  shift = 0;
-  if (l == top) return 1ull << kWeightBits;
-  if (c.hi < 0.f || !(l > -INFINITY) || top == INFINITY) return 0;
   const float d = __fsub_rn(l, top);  // < 0; its rounding error is dl
   const float z = __fsub_rn(d, l);
   const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(d, z)), __fsub_rn(-top, z));
-  const float e = __fmul_rn(d, c.hi);
-  if (!(e > -63.f)) return 0;
+  float e = __fmul_rn(d, c.hi);
   const float el = __fmaf_rn(d, c.hi, -e) + __fmaf_rn(d, c.lo, __fmul_rn(dl, c.hi));
+  // no weight: too small, greedy, -inf, NaN, beside +inf
+  const bool none = !(e > -63.f) || c.hi < 0.f;
+  e = none ? 0.f : e;
   const float n = rintf(e);                 // -63..0
   const float f = __fsub_rn(e, n);          // exact, |f| <= 1/2
   const float j = rintf(f * 32.f);          // -16..16
@@ -74,17 +76,17 @@ __device__ __forceinline__ unsigned long long weight_mantissa(float l, float top
   // 2^r - 1 = a + a^2 / 2 + a^3 / 6 + a^4 / 24 with a = r ln 2
   const float a = r * 0.693147180559945f;
   const float p = a * __fmaf_rn(a, __fmaf_rn(a, __fmaf_rn(a, 0.041666667f, 0.16666667f), 0.5f), 1.f);
-  const unsigned long long base = t.v[int(j) + 16];
+  const ulonglong2 base = t.v[int(j) + 16];
   // base < 2^45, so |p base| < 2^39: in units of 2^8 it is a signed 32-bit integer
-  const long long more = static_cast<long long>(__float2int_rn(p * __ull2float_rn(base >> 8))) * 256;
-  shift = -int(n);                          // 0..63
-  return base + static_cast<unsigned long long>(more);
+  const long long more = static_cast<long long>(__float2int_rn(p * __uint_as_float(uint32_t(base.y)))) * 256;
+  shift = l == top ? 0 : -int(n);           // 0..63
+  return l == top ? 1ull << kWeightBits : none ? 0ull : base.x + static_cast<unsigned long long>(more);
 }
 
 __device__ __forceinline__ unsigned long long weight_of(float l, float top, Slope c, const Exp2Table& t) {
   int shift;
   const unsigned long long w = weight_mantissa(l, top, c, t, shift);
-  return shift == 0 ? w : (w + (1ull << (shift - 1))) >> shift;
+  return (w + ((1ull << shift) >> 1)) >> shift;
 }
 
 // The share of logit l's weight in `kept`; the weight keeps its full precision here.
