@@ -9,6 +9,7 @@
 
 #include "bl.h"
 #include "bl_internal.h"
+#include "sample_common.cuh"
 
 namespace bl {
 
@@ -432,7 +433,8 @@ bl_status bl_sample(const void* logits, bl_dtype lt, const float* temperature, c
   if (!aligned(logits, lt == BL_F32 ? 4 : 2) || !aligned(u, 4) || !aligned(token, 4) || !aligned(temperature, 4) ||
       !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(prob, 4))
     return fail(BL_ERR_ALIGN, "%s: pointers must be aligned to their element size", fn);
-  return launch_status(launch_sample(logits, lt, temperature, top_k, top_p, min_p, u, M, V, token, prob, S(stream)), fn);
+  const bl::SampleArgs args{logits, temperature, top_p, min_p, u, top_k, M, V, token, prob, 0};
+  return launch_status(lt == BL_BF16 ? launch_sample_bf16(args, S(stream)) : launch_sample_f32(args, S(stream)), fn);
 }
 
 }  // extern "C"

@@ -161,13 +161,9 @@ cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, bl_dtype x
 cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
                             const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
                             int64_t K, int64_t adapters, int rank, cudaStream_t s);
-// temperature, top_k, top_p, min_p and prob may be nullptr
-cudaError_t launch_sample(const void* logits, bl_dtype lt, const float* temperature, const int32_t* top_k,
-                          const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V,
-                          int32_t* token, float* prob, cudaStream_t s);
-// bf16 logits (csrc/sample_bf16.cu)
-cudaError_t launch_sample_bf16(const uint16_t* logits, const float* temperature, const int32_t* top_k,
-                               const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V,
-                               int32_t* token, float* prob, cudaStream_t s);
+// Sampling (csrc/sample_bf16.cu, csrc/sample_f32.cu); the arguments are in sample_common.cuh.
+struct SampleArgs;
+cudaError_t launch_sample_bf16(const SampleArgs& args, cudaStream_t s);
+cudaError_t launch_sample_f32(const SampleArgs& args, cudaStream_t s);
 
 }  // namespace bl

@@ -22,18 +22,16 @@
 // Bound: a random shared-memory atomic takes 3.5 clocks per warp (bank
 // conflicts, as a plain load's; measured), 23 us for 256 rows of 248320 logits
 // on 152 SMs, whose bytes take 18.7 us at the copy rate.
-#include "bl_internal.h"
-#include "sample_weight.cuh"
+#include "sample_common.cuh"
 
 namespace bl {
 namespace {
-
-using u64 = unsigned long long;
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kWords = 32768;                // counters of one magnitude: low half positive, high half negative
 constexpr int kSegments = 1024;              // 64 magnitudes of one sign each, in falling order
+constexpr int kStep = 2000;                  // groups counted at a time, two per thread: four steps fit in 2^16 - 16 logits
 constexpr int kBatch = 128;                  // groups of 8 logits that a warp looks through at a time
 constexpr int kSpills = 32;                  // at most 524288 / 32767 counters are moved
 constexpr uint32_t kMasked2 = 0xFF80FF80u;   // two logits of -inf
@@ -41,15 +39,7 @@ constexpr uint32_t kInf = 0x7F80u;           // magnitude bits of an infinity; a
 // weights below 2^-45 of the largest are 0: no bin further than 46 octaves (31.9 T) matters
 constexpr float kWindow = 32.f;
 
-struct Args {
-  const uint16_t* logits;
-  const float *temperature, *top_p, *min_p, *u;
-  const int32_t* top_k;
-  int64_t M, V;
-  int32_t* token;
-  float* prob;
-  int chunk;  // a multiple of 8
-};
+using Args = SampleArgs;
 
 // A place in the order: the logit of these bf16 bits with `rank` equal ones
 // before it; `before` is the weight of everything before those.
@@ -97,13 +87,6 @@ struct Shared {
   uint32_t warp_max[kWarps];
   uint32_t matches[2][2 * kWarps];  // by batch of a round
 };
-
-template <class T>
-__device__ __forceinline__ T* peer(T* p, uint32_t rank) {
-  uint64_t a;
-  asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-  return reinterpret_cast<T*>(a);
-}
 
 __device__ __forceinline__ float value_of(uint32_t bits) { return __uint_as_float(bits << 16); }
 __device__ __forceinline__ uint32_t order_of(uint32_t bits) {  // rises with the value
@@ -155,20 +138,6 @@ struct Target {
   }
 };
 
-__device__ __forceinline__ u64 warp_sum_u64(u64 v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-template <int C>
-__device__ __forceinline__ void sync_cluster() {
-  if (C == 1)
-    __syncthreads();
-  else
-    cluster_sync();
-}
-
 // The live segments of a row in falling order, held by a warp: lane i has
 // segments 32 i .. 32 i + 31, from the highest bit down.
 struct SegmentList {
@@ -176,12 +145,7 @@ struct SegmentList {
   int n;
   __device__ __forceinline__ SegmentList(uint32_t word, int lane) {
     bits = word;
-    upto = __popc(word);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
+    upto = warp_scan(uint32_t(__popc(word)));
     n = int(__shfl_sync(0xffffffffu, upto, 31));
   }
   // The idx-th segment, idx < n (whole warp).
@@ -262,14 +226,8 @@ struct Row {
       const int s = i0 + __ffs(hit) - 1;
       const Bins b = bins(sh.seg[s].index);
       const u64 m1 = b.c1 * b.w1, m0 = b.c0 * b.w0;
-      u64 cm = m1 + m0;
-      uint32_t cc = b.c1 + b.c0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 m = __shfl_up_sync(0xffffffffu, cm, o);
-        const uint32_t c = __shfl_up_sync(0xffffffffu, cc, o);
-        if (lane >= o) cm += m, cc += c;
-      }
+      const u64 cm = warp_scan(m1 + m0);
+      const uint32_t cc = warp_scan(b.c1 + b.c0);
       const u64 before = sh.mass_before[s] + cm - m1 - m0;
       const u64 at = by_count ? u64(sh.count_before[s]) + cc - b.c1 - b.c0 : before;
       const u64 n1 = by_count ? b.c1 : m1, n0 = by_count ? b.c0 : m0;
@@ -343,7 +301,7 @@ struct Chunk {
 __device__ __forceinline__ void look_up(const Args& g, Shared& sh, int64_t m, int rank) {
   constexpr int kPickWarps = kWarps - 1;
   const int lane = threadIdx.x & 31, warp = int(threadIdx.x >> 5) - 1;
-  const Chunk c(g.logits + m * g.V, int(g.V), rank, g.chunk / 8);
+  const Chunk c(static_cast<const uint16_t*>(g.logits) + m * g.V, int(g.V), rank, g.chunk / 8);
   const Target target(sh.pick.bits);
   uint32_t left = sh.pick.rank;
   // rounds of two batches per warp, in order, until the matches suffice
@@ -379,12 +337,7 @@ __device__ __forceinline__ void look_up(const Args& g, Shared& sh, int64_t m, in
       continue;
     }
     if (warp != 0) return;
-    uint32_t upto = n0 + n1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
+    const uint32_t upto = warp_scan(n0 + n1);
     const int src = __ffs(__ballot_sync(0xffffffffu, upto > left)) - 1;
     left -= __shfl_sync(0xffffffffu, upto - n0 - n1, src);
     const uint32_t half = __shfl_sync(0xffffffffu, n0, src);
@@ -397,12 +350,7 @@ __device__ __forceinline__ void look_up(const Args& g, Shared& sh, int64_t m, in
 #pragma unroll 1
     for (int j = 0; j < 4; ++j) {
       uint32_t bits = (hits >> (8 * j)) & 0xFFu;
-      uint32_t incl = __popc(bits);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
+      const uint32_t incl = warp_scan(uint32_t(__popc(bits)));
       const uint32_t here = __shfl_sync(0xffffffffu, incl, 31), excl = incl - __popc(bits);
       if (left >= excl && left < incl) {
         for (uint32_t e = left - excl; e > 0; --e) bits &= bits - 1;
@@ -470,7 +418,7 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
 
   for (int64_t m = blockIdx.x / C; m < g.M; m += gridDim.x / C) {
     const RowValues values(m, g.temperature, g.top_k, g.top_p, g.min_p, g.u);
-    const uint16_t* row = g.logits + m * g.V;
+    const uint16_t* row = static_cast<const uint16_t*>(g.logits) + m * g.V;
     const Chunk c(row, int(g.V), int(rank), g.chunk / 8);
 
     // histogram; the row's first and last part of a group by one thread each
@@ -479,20 +427,27 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
       if ((part < c.ga || part >= c.gb) && (threadIdx.x == 0 || part > 0))
         count_group(hist, c.group(part, kMasked2));
     }
-    for (int from = c.ga, room = 65535 - 16; from < c.gb;) {
-      const int to = min(c.gb, from + room / 8);
-      for (int i = from + int(threadIdx.x); i < to; i += 4 * kThreads) {
-        uint4 q[4];
+    uint4 now[2], next[2];
+    auto fetch = [&](uint4 (&q)[2], int from) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          q[j] = i + j * kThreads < to ? c.whole(i + j * kThreads) : make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) count_group(hist, q[j]);
+      for (int j = 0; j < 2; ++j) {
+        const int i = from + j * kThreads + int(threadIdx.x);
+        q[j] = i < min(c.gb, from + kStep) ? c.whole(i) : make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
       }
-      from = to;
-      if (from < c.gb) {
+    };
+    fetch(now, c.ga);
+    int room = 65535 - 16;  // logits that cannot overflow a counter
+    for (int from = c.ga; from < c.gb; from += kStep) {
+      fetch(next, from + kStep);
+      if (room < 8 * kStep) {
         __syncthreads();
         room = 65535 - int(largest_counter(sh));
+      }
+      room -= 8 * kStep;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        count_group(hist, now[j]);
+        now[j] = next[j];
       }
     }
     const RowFilter f = row_filter(values, g.V);
@@ -576,14 +531,8 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
       for (int i0 = 0; i0 < s.n; i0 += 32) {
         const int j = i0 + lane;
         const Segment e = j < s.n ? sh.seg[j] : Segment{0, 0, 0};
-        u64 cm = e.mass;
-        uint32_t cc = e.count;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 v = __shfl_up_sync(0xffffffffu, cm, o);
-          const uint32_t c = __shfl_up_sync(0xffffffffu, cc, o);
-          if (lane >= o) cm += v, cc += c;
-        }
+        const u64 cm = warp_scan(e.mass);
+        const uint32_t cc = warp_scan(e.count);
         if (j < s.n) sh.mass_before[j] = kept + cm - e.mass, sh.count_before[j] = count + cc - e.count;
         kept += __shfl_sync(0xffffffffu, cm, 31);
         count += __shfl_sync(0xffffffffu, cc, 31);
@@ -647,50 +596,18 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
 
 template <int C>
 cudaError_t launch_rows(const Args& g, cudaStream_t s) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  cudaError_t e = raise_smem_cap(sample_bf16_kernel<C>, dev, int(sizeof(Shared)));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(std::min<int64_t>(g.M, std::max(1, sm_count() / C)) * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Shared);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (C > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim = {C, 1, 1};
-    ++n;
-  }
-  if (overlap_enabled()) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, sample_bf16_kernel<C>, g);
+  const int64_t clusters = std::min<int64_t>(g.M, std::max(1, sm_count() / C));
+  return launch_clusters<C>(sample_bf16_kernel<C>, clusters * C, kThreads, int(sizeof(Shared)), s, g);
 }
 
 }  // namespace
 
-cudaError_t launch_sample_bf16(const uint16_t* logits, const float* temperature, const int32_t* top_k,
-                               const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V,
-                               int32_t* token, float* prob, cudaStream_t s) {
-  auto chunk_of = [&](int c) { return ((V + 7 + c - 1) / c + 7) / 8 * 8; };
-  // The number of CTAs of a row: a row costs each of them about 8 us beside its histogram, which takes
-  // 0.06 ns per logit of its chunk, and sm_count / c rows run at a time.  (One row of 248320: 8 CTAs
-  // KK us, 1 KK us; 256 rows: 1 CTA KK us, 4 KK us.)
-  int best = 1;
-  double least = 0;
-  for (int c = 1; c <= 8; c *= 2) {
-    const int64_t at_once = std::max(1, sm_count() / c);
-    const double t = double((M + at_once - 1) / at_once) * (8000.0 + 0.06 * double(chunk_of(c)));
-    if (c == 1 || t < 0.95 * least) best = c, least = t;
-  }
-  const Args g{logits, temperature, top_p, min_p, u, top_k, M, V, token, prob, int(chunk_of(best))};
-  switch (best) {
+cudaError_t launch_sample_bf16(const SampleArgs& args, cudaStream_t s) {
+  // Measured per row and CTA: 8 us beside the histogram, 0.08 ns per logit.
+  const int c = ctas_per_row(args.M, args.V, 8000.0, 0.08);
+  SampleArgs g = args;
+  g.chunk = int(((g.V + 7 + c - 1) / c + 7) / 8 * 8);
+  switch (c) {
     case 1: return launch_rows<1>(g, s);
     case 2: return launch_rows<2>(g, s);
     case 4: return launch_rows<4>(g, s);
