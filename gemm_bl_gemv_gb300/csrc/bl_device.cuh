@@ -143,6 +143,14 @@ __device__ __forceinline__ float ld_peer_f32(const float* p, uint32_t rank) {
   return v;
 }
 
+// *p of cluster CTA `rank` (p: this CTA's copy), as a generic address.
+template <class T>
+__device__ __forceinline__ T* peer(T* p, uint32_t rank) {
+  uint64_t a;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+  return reinterpret_cast<T*>(a);
+}
+
 // ---- integer dot products -------------------------------------------------
 // sum over 4 bytes of (unsigned a_i) * (signed b_i) + c
 __device__ __forceinline__ int dp4a_us(uint32_t a, uint32_t b, int c) {

@@ -3,6 +3,7 @@
 // a = adapter[m], negative for none.
 #include "act_quant.cuh"
 #include "bl_internal.h"
+#include "lora.cuh"
 
 namespace bl {
 namespace {
@@ -17,6 +18,7 @@ struct Args {
   unsigned int* err;
   int64_t M, N, K, L;
   int R;
+  bool tiles;  // tiles of few runs are another kernel's
 };
 
 // One CTA per token: a warp forms each of the R inner products with A's rows,
@@ -27,6 +29,12 @@ __global__ void __launch_bounds__(256) lora_token_kernel(const Args g) {
   const int64_t m = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
+  if (g.tiles) {  // the tile's runs
+    const int64_t t = m / kTile * kTile + threadIdx.x;
+    const bool start = threadIdx.x < kTile && t < g.M &&
+                       (threadIdx.x == 0 || adapter_of(g.adapter, t, g.L) != adapter_of(g.adapter, t - 1, g.L));
+    if (__syncthreads_count(start) <= kTileRuns) return;
+  }
   int64_t l = g.adapter[m];
   if (l >= g.L) {
     if (threadIdx.x == 0 && g.err) atomicOr(g.err, BL_DEVERR_RANGE);
@@ -71,8 +79,13 @@ __global__ void __launch_bounds__(256) lora_token_kernel(const Args g) {
 cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
                             const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
                             int64_t K, int64_t adapters, int rank, cudaStream_t s) {
-  const Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank};
+  Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, false};
   const bool pdl = overlap_enabled();
+  if (xt == BL_BF16 && M > 32) {
+    const cudaError_t e = launch_lora_tile(x, adapter, a, b, scale, base, y, yt, M, N, K, adapters, rank, s);
+    if (e != cudaSuccess && e != cudaErrorNotSupported) return e;
+    g.tiles = e == cudaSuccess;
+  }
   const dim3 grid{unsigned(M)}, block{256};
   if (xt == BL_BF16 && yt == BL_BF16) return launch(lora_token_kernel<true, true>, grid, block, 0, s, pdl, g);
   if (xt == BL_BF16) return launch(lora_token_kernel<true, false>, grid, block, 0, s, pdl, g);

@@ -19,14 +19,6 @@ struct SampleArgs {
   int chunk;  // logits of a CTA
 };
 
-// *p of cluster CTA `rank` (p: this CTA's copy), as a generic address.
-template <class T>
-__device__ __forceinline__ T* peer(T* p, uint32_t rank) {
-  uint64_t a;
-  asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-  return reinterpret_cast<T*>(a);
-}
-
 __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
