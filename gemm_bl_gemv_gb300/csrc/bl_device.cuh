@@ -318,4 +318,14 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, 
       : "memory");
 }
 
+// ---- TMA tiled store, 2-D tensor map (bulk-group completion) ---------------
+// x * element size a multiple of 16 bytes, not negative; box elements outside
+// the tensor are not written.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(smem_addr(src))
+               : "memory");
+}
+
 }  // namespace bl

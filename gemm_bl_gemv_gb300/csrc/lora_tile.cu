@@ -14,10 +14,14 @@
 //   2. The sums, times the adapter's scale, become bf16 operands: two terms
 //      (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8, three
 //      (24 bits) for fp32 outputs.
-//   3. Up: each CTA takes tiles of 128 outputs.  B's rows come by TMA as they
-//      lie in memory, the product goes to one of two TMEM buffers, and eight
-//      warps turn it through shared memory so that base and y move in whole
-//      32-byte sectors, a row's 32 outputs per four lanes.
+//   3. Up: each CTA takes tiles of 256 bytes of outputs (128 bf16, 64 fp32).
+//      B's rows come by TMA as they lie in memory, and so does the tile of
+//      base, 128-byte swizzled, three tiles ahead.  Every run of the 128 tokens
+//      has its own product in one of two TMEM buffers; the thread of a row adds
+//      its run's to the base in place, and the tile goes out by TMA, rows
+//      without an adapter unchanged.  Rows of y that are not 16-byte aligned
+//      (N * element size not a multiple of 16) are read and written by the
+//      threads, a row's outputs by neighbouring lanes.
 //
 // Bound: HBM.  base and y are 4 of the 5 bytes that an output costs at K =
 // N / 2.7 and rank 64; the tensor work of 8192 x 2560 x 6912 at rank 64 (17
@@ -29,45 +33,48 @@
 namespace bl {
 namespace {
 
-constexpr int kWarps = 10, kThreads = 32 * kWarps;  // TMA, MMA, 8 epilogue warps
-constexpr int kEpilogue = 256;
+constexpr int kWarps = 11, kThreads = 32 * kWarps;  // loads, MMA, 8 epilogue warps, stores
+constexpr int kEpilogueWarps = 8;
 constexpr int kStages = 3;                 // K blocks of 64 in flight
-constexpr int kN = 128;                    // outputs of an up tile
-constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 64 bf16
-constexpr uint32_t kTmemCols = 256;        // two accumulators of 128 columns
-constexpr int kTurn = 36;                  // floats of a row of 32 outputs being turned: 16-byte aligned, few conflicts
+constexpr int kTiles = 3;                  // tiles of base in flight
+constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; half a tile of base
+constexpr uint32_t kTmemCols = 256;        // two accumulators of up to 128 columns
+constexpr int kTurn = 33;                  // floats of a row of 32 outputs being turned
 
 __host__ __device__ constexpr uint32_t idesc(int n) {  // bf16 x bf16 -> fp32, M = 128
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
 }
 
-// Shared memory: [ring | operand terms + turning buffers][partial sums | up ring]
+// Shared memory.  First [ring of x and A | partial sums]; then, over both,
+// [operand terms | ring of B | ring of base, or turning buffers].  The operand
+// lies within the ring, clear of the partial sums that it is made from.
 struct Plan {
   int rp, rk;             // rank rounded up to 16 (MMA N and K) and to 64 (operand sub-tiles)
   uint32_t a_bytes;       // of a ring stage's A block
   uint32_t stage;         // of a ring stage
   uint32_t term;          // of one operand term, [128][rk] in 64-column sub-tiles
-  uint32_t turn_at;       // byte offset of the turning buffers
-  uint32_t part_at;       // of the partial sums
+  uint32_t part_at;       // byte offset of the partial sums
   uint32_t part_row;      // floats of a row of them
-  uint32_t up_stage;      // of an up tile of B
+  uint32_t up_at, up_stage;  // ring of B tiles
+  uint32_t base_at;       // ring of base tiles
   uint32_t bar_at, total;
 };
-__host__ __device__ inline Plan make_plan(int rank, int terms) {
+__host__ __device__ inline Plan make_plan(int rank, int terms, int n_tile) {
   Plan p;
   p.rp = (rank + 15) / 16 * 16;
   p.rk = (rank + 63) / 64 * 64;
   p.a_bytes = uint32_t(p.rp) * 128;
   p.stage = kXBytes + (p.a_bytes + 1023) / 1024 * 1024;
   p.term = uint32_t(p.rk) / 64 * kTile * 128;
-  p.turn_at = p.term * terms;
-  const uint32_t first = p.turn_at + 8 * 32 * kTurn * 4, ring = kStages * p.stage;
-  p.part_at = ((first > ring ? first : ring) + 1023) / 1024 * 1024;
+  const uint32_t ring = kStages * p.stage, operand = p.term * terms;
+  p.part_at = ring > operand ? ring : operand;
   p.part_row = uint32_t(p.rp) + 4;
-  p.up_stage = uint32_t(p.rk) / 64 * kN * 128;
-  const uint32_t part = kTile * p.part_row * 4;
-  p.bar_at = p.part_at + (part > 2 * p.up_stage ? part : 2 * p.up_stage);
-  p.total = p.bar_at + 256;
+  p.up_at = operand;
+  p.up_stage = uint32_t(p.rk) / 64 * n_tile * 128;
+  p.base_at = p.up_at + 2 * p.up_stage;
+  const uint32_t one = p.part_at + kTile * p.part_row * 4, two = p.base_at + kTiles * 2 * kXBytes;
+  p.bar_at = (one > two ? one : two) / 1024 * 1024 + 1024;
+  p.total = p.bar_at + 1024;
   return p;
 }
 
@@ -79,38 +86,16 @@ struct Args {
   unsigned int* err;
   int64_t M, N, K, L;
   int rank;
-  bool vec;  // base and y rows are 16-byte aligned
 };
 
 struct Control {  // at Plan::bar_at
   uint64_t full[kStages], empty[kStages], sums[2], drained[2], up_full[2], up_empty[2], out_full[2], out_empty[2];
+  uint64_t base_full[kTiles], base_done[kTiles], base_empty[kTiles];
   uint32_t tmem, starts[4];
   int abort;
+  int adapter[kTile];  // of each token, -1: none
 };
-static_assert(sizeof(Control) <= 256, "");
-
-// base[m, n .. n+8) as fp32; outputs past N are 0.
-template <bool YB>
-__device__ __forceinline__ void load_base(const Args& g, int64_t m, int n, float (&v)[8]) {
-  const int64_t i = m * g.N + n;
-  if (g.vec && n + 8 <= g.N) {
-    load8<YB>(reinterpret_cast<const uint8_t*>(g.base) + i * (YB ? 2 : 4), 0, v);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = n + j < g.N ? load1<YB>(g.base, i + j) : 0.f;
-}
-template <bool YB>
-__device__ __forceinline__ void store_y(const Args& g, int64_t m, int n, const float (&v)[8]) {
-  const int64_t i = m * g.N + n;
-  if (g.vec && n + 8 <= g.N) {
-    store8<YB>(reinterpret_cast<uint8_t*>(g.y) + i * (YB ? 2 : 4), v);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (n + j < g.N) store1<YB>(g.y, i + j, v[j]);
-}
+static_assert(sizeof(Control) <= 1024, "");
 
 // The next run of the tile from token `t`: [t, end) and its adapter.
 struct Runs {
@@ -133,13 +118,17 @@ struct Runs {
   }
 };
 
-template <int CL, bool YB>
-__global__ void __launch_bounds__(kThreads) lora_tile_kernel(const __grid_constant__ CUtensorMap xmap,
+// YB: base and y are bf16.  TMA: they come and go by TMA.
+template <int CL, bool YB, bool TMA>
+__global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_constant__ CUtensorMap xmap,
                                                              const __grid_constant__ CUtensorMap amap,
-                                                             const __grid_constant__ CUtensorMap bmap, const Args g) {
+                                                             const __grid_constant__ CUtensorMap bmap,
+                                                             const __grid_constant__ CUtensorMap base_map,
+                                                             const __grid_constant__ CUtensorMap y_map, const Args g) {
   constexpr int kTerms = YB ? 2 : 3;
+  constexpr int kN = YB ? 128 : 64;  // outputs of an up tile
   extern __shared__ __align__(1024) uint8_t smem[];
-  const Plan p = make_plan(g.rank, kTerms);
+  const Plan p = make_plan(g.rank, kTerms, kN);
   Control& c = *reinterpret_cast<Control*>(smem + p.bar_at);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t me = CL == 1 ? 0 : cluster_ctarank();
@@ -156,11 +145,16 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const __grid_consta
     for (int i = 0; i < kStages; ++i) mbar_init(&c.full[i], 1), mbar_init(&c.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.sums[i], 1);
-      mbar_init(&c.drained[i], kEpilogue / 32);
+      mbar_init(&c.drained[i], kEpilogueWarps);
       mbar_init(&c.up_full[i], 1);
       mbar_init(&c.up_empty[i], 1);
       mbar_init(&c.out_full[i], 1);
-      mbar_init(&c.out_empty[i], kEpilogue / 32);
+      mbar_init(&c.out_empty[i], kEpilogueWarps);
+    }
+    for (int i = 0; i < kTiles; ++i) {
+      mbar_init(&c.base_full[i], 1);
+      mbar_init(&c.base_done[i], kEpilogueWarps);
+      mbar_init(&c.base_empty[i], 1);
     }
     fence_barrier_init();
   }
@@ -168,6 +162,7 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const __grid_consta
   if (threadIdx.x < kTile) {
     const int t = threadIdx.x;
     const int a = t < size ? adapter_of(g.adapter, m0 + t, g.L) : -1;
+    c.adapter[t] = a;
     const int before = t > 0 && t < size ? adapter_of(g.adapter, m0 + t - 1, g.L) : -2;
     const uint32_t b = __ballot_sync(0xffffffffu, t < size && a != before);
     if (lane == 0) c.starts[warp] = b;
@@ -186,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const __grid_consta
     if (warp == 0 && lane == 0) {
       int it = 0;
       for (Runs r(c.starts, size); r.next();) {
-        const int a = adapter_of(g.adapter, m0 + r.t, g.L);
+        const int a = c.adapter[r.t];
         if (a < 0) continue;
         for (int kb = k0; kb < k1; ++kb, ++it) {
           const int st = it % kStages;
@@ -206,8 +201,8 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const __grid_consta
       int it = 0, run = 0;
       const uint32_t sbase = smem_addr(smem);
       for (Runs r(c.starts, size); r.next();) {
-        if (adapter_of(g.adapter, m0 + r.t, g.L) < 0) continue;
-        const uint32_t acc = tmem + uint32_t(run & 1) * kN;
+        if (c.adapter[r.t] < 0) continue;
+        const uint32_t acc = tmem + uint32_t(run & 1) * 128;
         if (run >= 2 && !*abort && !mbar_wait_bounded(&c.drained[run & 1], uint32_t(run / 2 - 1) & 1u, g.err)) *abort = 1;
         tc_fence_after();
         for (int kb = k0; kb < k1; ++kb, ++it) {
@@ -224,17 +219,17 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const __grid_consta
         umma_commit(&c.sums[run & 1]);
         ++run;
       }
-    } else if (warp >= 2) {
+    } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
       float* part = reinterpret_cast<float*>(smem + p.part_at);
       const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane;
       int run = 0;
       for (Runs r(c.starts, size); r.next();) {
-        if (adapter_of(g.adapter, m0 + r.t, g.L) < 0) continue;
+        if (c.adapter[r.t] < 0) continue;
         if (!*abort && !mbar_wait_bounded(&c.sums[run & 1], uint32_t(run / 2) & 1u, g.err)) *abort = 1;
         tc_fence_after();
         for (int col = half * 16; col < p.rp; col += 32) {
           uint32_t v[16];
-          tmem_ld16(tmem + uint32_t(run & 1) * kN + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
+          tmem_ld16(tmem + uint32_t(run & 1) * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
           tmem_ld_wait();
           if (row >= r.t && row < r.end) {
 #pragma unroll
@@ -258,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const __grid_consta
     for (int i = threadIdx.x; i < kTile * (p.rp / 8); i += kThreads) {
       const int row = i / (p.rp / 8), chunk = i % (p.rp / 8);
       float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      const int a = row < size ? adapter_of(g.adapter, m0 + row, g.L) : -1;
+      const int a = c.adapter[row];
       if (a >= 0 && chunk * 8 < g.rank) {
         const float* src = reinterpret_cast<const float*>(smem + p.part_at) + row * p.part_row + chunk * 8;
 #pragma unroll
@@ -291,109 +286,168 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const __grid_consta
 
     // ---- 3. up ----
     const int tiles = int((g.N + kN - 1) / kN);
+    constexpr int kHalf = kN / 2;  // outputs of 128 bytes
     if (warp == 0 && lane == 0) {
-      int it = 0;
-      for (Runs r(c.starts, size); r.next();) {
-        const int a = adapter_of(g.adapter, m0 + r.t, g.L);
-        if (a < 0) continue;
-        for (int n = int(me); n < tiles && !*abort; n += CL, ++it) {
+      int it = 0, tl = 0;
+      for (int n = int(me); n < tiles && !*abort; n += CL, ++tl) {
+        if (TMA) {
+          const int bs = tl % kTiles;
+          if (tl >= kTiles && !mbar_wait_bounded(&c.base_empty[bs], uint32_t(tl / kTiles - 1) & 1u, g.err)) {
+            *abort = 1;
+            break;
+          }
+          const bool two = int64_t(n) * kN + kHalf < g.N;
+          uint8_t* dst = smem + p.base_at + bs * 2 * kXBytes;
+          mbar_arrive_expect_tx(&c.base_full[bs], two ? 2 * kXBytes : kXBytes);
+          tma_load_2d(dst, &base_map, n * 256, int(m0), &c.base_full[bs]);
+          if (two) tma_load_2d(dst + kXBytes, &base_map, n * 256 + 128, int(m0), &c.base_full[bs]);
+        }
+        for (Runs r(c.starts, size); r.next();) {
+          const int a = c.adapter[r.t];
+          if (a < 0) continue;
           const int st = it & 1;
           if (it >= 2 && !mbar_wait_bounded(&c.up_empty[st], uint32_t(it / 2 - 1) & 1u, g.err)) {
             *abort = 1;
             break;
           }
-          uint8_t* dst = smem + p.part_at + st * p.up_stage;
+          uint8_t* dst = smem + p.up_at + st * p.up_stage;
           mbar_arrive_expect_tx(&c.up_full[st], p.up_stage);
           for (int sub = 0; sub < p.rk / 64; ++sub)
             tma_load_2d(dst + sub * (kN * 128), &bmap, sub * 128, int(int64_t(a) * g.N + n * kN), &c.up_full[st]);
+          ++it;
         }
       }
       // the CTA must not finish while a load still writes its shared memory
       for (int i = max(0, it - 2); i < it; ++i) mbar_wait_bounded(&c.up_full[i & 1], uint32_t(i / 2) & 1u, nullptr);
+      if (TMA)
+        for (int i = max(0, tl - kTiles); i < tl; ++i)
+          mbar_wait_bounded(&c.base_full[i % kTiles], uint32_t(i / kTiles) & 1u, nullptr);
     } else if (warp == 1 && lane == 0) {
       int it = 0;
       const uint32_t sbase = smem_addr(smem);
-      for (Runs r(c.starts, size); r.next();) {
-        if (adapter_of(g.adapter, m0 + r.t, g.L) < 0) continue;
-        for (int n = int(me); n < tiles; n += CL, ++it) {
+      for (int n = int(me); n < tiles; n += CL)
+        for (Runs r(c.starts, size); r.next();) {
+          if (c.adapter[r.t] < 0) continue;
           const int st = it & 1;
           if (!*abort && !mbar_wait_bounded(&c.up_full[st], uint32_t(it / 2) & 1u, g.err)) *abort = 1;
           if (it >= 2 && !*abort && !mbar_wait_bounded(&c.out_empty[st], uint32_t(it / 2 - 1) & 1u, g.err)) *abort = 1;
           tc_fence_after();
-          const uint32_t ba = sbase + p.part_at + st * p.up_stage;
+          const uint32_t ba = sbase + p.up_at + st * p.up_stage;
           if (!*abort)
             for (int t = 0; t < kTerms; ++t)
-              for (int ks = 0; ks < p.rp / 16; ++ks) {
-                const uint32_t off = uint32_t(ks >> 2) * (kTile * 128) + (ks & 3) * 32;
-                umma_f16(tmem + st * kN, umma_desc_sw128(sbase + t * p.term + off), umma_desc_sw128(ba + off), idesc(kN),
-                         t > 0 || ks > 0);
-              }
+              for (int ks = 0; ks < p.rp / 16; ++ks)
+                umma_f16(tmem + st * 128,
+                         umma_desc_sw128(sbase + t * p.term + uint32_t(ks >> 2) * (kTile * 128) + (ks & 3) * 32),
+                         umma_desc_sw128(ba + uint32_t(ks >> 2) * (kN * 128) + (ks & 3) * 32), idesc(kN), t > 0 || ks > 0);
           umma_commit(&c.up_empty[st]);
           umma_commit(&c.out_full[st]);
+          ++it;
         }
-      }
-    } else if (warp >= 2) {
-      const int quarter = warp & 3, half = (warp - 2) >> 2;
-      float* turn = reinterpret_cast<float*>(smem + p.turn_at) + (warp - 2) * 32 * kTurn;
-      int it = 0;
-      for (Runs r(c.starts, size); r.next();) {
-        const bool has = adapter_of(g.adapter, m0 + r.t, g.L) >= 0;
-        // rows of this warp that are in the run
-        const int ra = max(r.t, quarter * 32), rb = min(r.end, quarter * 32 + 32);
-        if (!has) {
-          if (g.y != g.base)
-            for (int n = int(me) * kN + half * 64 + (lane & 7) * 8; n < int(g.N); n += CL * kN)
-              for (int row = ra + (lane >> 3); row < rb; row += 4) {
-                float v[8];
-                load_base<YB>(g, m0 + row, n, v);
-                store_y<YB>(g, m0 + row, n, v);
-              }
-          continue;
-        }
-        for (int n = int(me); n < tiles; n += CL, ++it) {
-          const int st = it & 1, n0 = n * kN + half * 64 + (lane & 3) * 8;
-          // base of the first 32 outputs, on its way while the product is formed
-          float v[4][8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = quarter * 32 + 8 * i + (lane >> 2);
-            if (row >= ra && row < rb && n0 < g.N) load_base<YB>(g, m0 + row, n0, v[i]);
+    } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
+      const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane;
+      float* turn = reinterpret_cast<float*>(smem + p.base_at) + (warp - 2) * 32 * kTurn;
+      int it = 0, tl = 0;
+      for (int n = int(me); n < tiles; n += CL, ++tl) {
+        const int bs = tl % kTiles, n0 = n * kN + half * kHalf;
+        // this thread's row of the tile of base: 16-byte unit u at u ^ (row % 8)
+        uint8_t* mine_row = smem + p.base_at + bs * 2 * kXBytes + half * kXBytes + row * 128;
+        if (TMA && !*abort && !mbar_wait_bounded(&c.base_full[bs], uint32_t(tl / kTiles) & 1u, g.err)) *abort = 1;
+        for (Runs r(c.starts, size); r.next();) {
+          const bool has = c.adapter[r.t] >= 0;
+          // rows of this warp that are in the run
+          const int ra = max(r.t, quarter * 32), rb = min(r.end, quarter * 32 + 32);
+          if (!has) {
+            if (!TMA && g.y != g.base)
+              for (int i = ra; i < rb; ++i)
+                for (int j = n0 + lane; j < min(n0 + kHalf, int(g.N)); j += 32)
+                  store1<YB>(g.y, (m0 + i) * g.N + j, load1<YB>(g.base, (m0 + i) * g.N + j));
+            continue;
           }
+          const int st = it & 1;
           if (!*abort && !mbar_wait_bounded(&c.out_full[st], uint32_t(it / 2) & 1u, g.err)) *abort = 1;
           tc_fence_after();
+          const uint32_t at = tmem + st * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(half * kHalf);
+          if (ra < rb && !*abort && n0 < g.N) {
+            if (TMA) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t d[32];
-            const uint32_t at = tmem + st * kN + (uint32_t(quarter * 32) << 16) + uint32_t(half * 64 + h * 32);
-            tmem_ld16(at, *reinterpret_cast<uint32_t(*)[16]>(d));
-            tmem_ld16(at + 16, *reinterpret_cast<uint32_t(*)[16]>(d + 16));
-            tmem_ld_wait();
-            if (h == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&c.out_empty[st]);
-            }
-            __syncwarp();
+              for (int h = 0; h < kHalf; h += 32) {
+                uint32_t d[32];
+                tmem_ld16(at + h, *reinterpret_cast<uint32_t(*)[16]>(d));
+                tmem_ld16(at + h + 16, *reinterpret_cast<uint32_t(*)[16]>(d + 16));
+                tmem_ld_wait();
+                if (row >= ra && row < rb) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(turn + lane * kTurn + 4 * j) =
-                  make_uint4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
-            __syncwarp();
-            const int nn = n0 + h * 32;
+                  for (int u = 0; u < (YB ? 4 : 8); ++u) {
+                    uint4* q = reinterpret_cast<uint4*>(mine_row + ((uint32_t(h * (YB ? 2 : 4) / 16 + u) ^ uint32_t(row & 7)) << 4));
+                    const uint4 v = *q;
+                    if (YB) {
+                      uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tr = 8 * i + (lane >> 2), row = quarter * 32 + tr;
-              if (row < ra || row >= rb || nn >= g.N || *abort) continue;
-              if (h == 1) load_base<YB>(g, m0 + row, nn, v[i]);
-              const float4 f0 = *reinterpret_cast<const float4*>(turn + tr * kTurn + (lane & 3) * 8);
-              const float4 f1 = *reinterpret_cast<const float4*>(turn + tr * kTurn + (lane & 3) * 8 + 4);
-              v[i][0] += f0.x, v[i][1] += f0.y, v[i][2] += f0.z, v[i][3] += f0.w;
-              v[i][4] += f1.x, v[i][5] += f1.y, v[i][6] += f1.z, v[i][7] += f1.w;
-              store_y<YB>(g, m0 + row, nn, v[i]);
+                      for (int j = 0; j < 4; ++j)
+                        w[j] = uint32_t(f32_to_bf16_bits_rn(__uint_as_float(w[j] << 16) + __uint_as_float(d[8 * u + 2 * j]))) |
+                               uint32_t(f32_to_bf16_bits_rn(__uint_as_float(w[j] & 0xffff0000u) +
+                                                            __uint_as_float(d[8 * u + 2 * j + 1]))) << 16;
+                      *q = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+                      const float4 f = *reinterpret_cast<const float4*>(&v);
+                      *reinterpret_cast<float4*>(q) =
+                          make_float4(f.x + __uint_as_float(d[4 * u]), f.y + __uint_as_float(d[4 * u + 1]),
+                                      f.z + __uint_as_float(d[4 * u + 2]), f.w + __uint_as_float(d[4 * u + 3]));
+                    }
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int h = 0; h < kHalf; h += 32) {
+                uint32_t d[32];
+                tmem_ld16(at + h, *reinterpret_cast<uint32_t(*)[16]>(d));
+                tmem_ld16(at + h + 16, *reinterpret_cast<uint32_t(*)[16]>(d + 16));
+                tmem_ld_wait();
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) turn[lane * kTurn + j] = __uint_as_float(d[j]);
+                __syncwarp();
+                const int nn = n0 + h + lane;
+                if (nn < g.N)
+                  for (int i = ra; i < rb; i += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                      if (i + j < rb) v[j] = load1<YB>(g.base, (m0 + i + j) * g.N + nn);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                      if (i + j < rb)
+                        store1<YB>(g.y, (m0 + i + j) * g.N + nn, v[j] + turn[(i + j - quarter * 32) * kTurn + lane]);
+                  }
+              }
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.out_empty[st]);
+          ++it;
+        }
+        if (TMA) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.base_done[bs]);
         }
       }
+    } else if (TMA && warp == 2 + kEpilogueWarps && lane == 0) {
+      int tl = 0;
+      for (int n = int(me); n < tiles; n += CL, ++tl) {
+        const int bs = tl % kTiles;
+        if (!*abort && !mbar_wait_bounded(&c.base_done[bs], uint32_t(tl / kTiles) & 1u, g.err)) *abort = 1;
+        if (*abort) break;
+        const uint8_t* src = smem + p.base_at + bs * 2 * kXBytes;
+        tma_store_2d(&y_map, n * 256, int(m0), src);
+        if (int64_t(n) * kN + kHalf < g.N) tma_store_2d(&y_map, n * 256 + 128, int(m0), src + kXBytes);
+        bulk_commit();
+        bulk_wait_read();
+        mbar_arrive(&c.base_empty[bs]);
+      }
+      bulk_wait();
     }
   }
   __syncwarp();
@@ -406,18 +460,21 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const __grid_consta
   }
 }
 
-template <int CL, bool YB>
-cudaError_t launch_tiles(const CUtensorMap& xmap, const CUtensorMap& amap, const CUtensorMap& bmap, const Args& g,
-                         cudaStream_t s) {
+struct Maps {
+  CUtensorMap x, a, b, base, y;
+};
+
+template <int CL, bool YB, bool TMA>
+cudaError_t launch_tiles(const Maps& maps, const Args& g, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
-  const uint32_t smem = make_plan(g.rank, YB ? 2 : 3).total;
-  const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB>, dev, int(make_plan(128, YB ? 2 : 3).total));
+  constexpr int kTerms = YB ? 2 : 3, kN = YB ? 128 : 64;
+  const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(make_plan(128, kTerms, kN).total));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((g.M + kTile - 1) / kTile * CL));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = make_plan(g.rank, kTerms, kN).total;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;
@@ -433,7 +490,17 @@ cudaError_t launch_tiles(const CUtensorMap& xmap, const CUtensorMap& amap, const
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, lora_tile_kernel<CL, YB>, xmap, amap, bmap, g);
+  return cudaLaunchKernelEx(&cfg, lora_tile_kernel<CL, YB, TMA>, maps.x, maps.a, maps.b, maps.base, maps.y, g);
+}
+
+template <bool YB, bool TMA>
+cudaError_t launch_tiles(int cl, const Maps& maps, const Args& g, cudaStream_t s) {
+  switch (cl) {
+    case 1: return launch_tiles<1, YB, TMA>(maps, g, s);
+    case 2: return launch_tiles<2, YB, TMA>(maps, g, s);
+    case 4: return launch_tiles<4, YB, TMA>(maps, g, s);
+    default: return launch_tiles<8, YB, TMA>(maps, g, s);
+  }
 }
 
 }  // namespace
@@ -441,27 +508,27 @@ cudaError_t launch_tiles(const CUtensorMap& xmap, const CUtensorMap& amap, const
 cudaError_t launch_lora_tile(const void* x, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
                              const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
                              int64_t K, int64_t adapters, int rank, cudaStream_t s) {
-  CUtensorMap xmap, amap, bmap;  // bytes; 128-byte wide boxes, swizzled
-  const Plan p = make_plan(rank, 2);
-  if (adapters * rank > 0x7fffffff || adapters * N > 0x7fffffff || K * 2 > 0x7fffffff ||
-      !encode_tmap_2d_u8(&xmap, x, uint64_t(K) * 2, uint64_t(M), uint64_t(K) * 2, 128, kTile, true) ||
-      !encode_tmap_2d_u8(&amap, a, uint64_t(K) * 2, uint64_t(adapters * rank), uint64_t(K) * 2, 128, uint32_t(p.rp), true) ||
-      !encode_tmap_2d_u8(&bmap, b, uint64_t(rank) * 2, uint64_t(adapters * N), uint64_t(rank) * 2, 128, kN, true))
+  const bool yb = yt == BL_BF16;
+  const uint64_t row = uint64_t(N) * (yb ? 2 : 4);
+  Maps maps;  // bytes; 128-byte wide boxes, swizzled
+  if (adapters * rank > 0x7fffffff || adapters * N > 0x7fffffff || row > 0x7fffffff ||
+      !encode_tmap_2d_u8(&maps.x, x, uint64_t(K) * 2, uint64_t(M), uint64_t(K) * 2, 128, kTile, true) ||
+      !encode_tmap_2d_u8(&maps.a, a, uint64_t(K) * 2, uint64_t(adapters * rank), uint64_t(K) * 2, 128,
+                         uint32_t(rank + 15) / 16 * 16, true) ||
+      !encode_tmap_2d_u8(&maps.b, b, uint64_t(rank) * 2, uint64_t(adapters * N), uint64_t(rank) * 2, 128, yb ? 128 : 64,
+                         true))
     return cudaErrorNotSupported;
-  const int es = yt == BL_BF16 ? 2 : 4;
-  const bool vec = N * es % 16 == 0 && ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(y)) & 15) == 0;
-  const Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, vec};
-  // CTAs of a tile: as many as keep two per SM busy
+  const bool tma = row % 16 == 0 && ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(y)) & 15) == 0 &&
+                   encode_tmap_2d_u8(&maps.base, base, row, uint64_t(M), row, 128, kTile, true) &&
+                   encode_tmap_2d_u8(&maps.y, y, row, uint64_t(M), row, 128, kTile, true);
+  if (!tma) maps.base = maps.y = maps.x;  // not used
+  const Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank};
+  // CTAs of a tile of tokens: as many as keep one per SM
   const int64_t tiles = (M + kTile - 1) / kTile;
   int cl = 1;
-  while (cl < 8 && tiles * cl * 2 <= 2 * sm_count()) cl *= 2;
-  const bool yb = yt == BL_BF16;
-  switch (cl) {
-    case 1: return yb ? launch_tiles<1, true>(xmap, amap, bmap, g, s) : launch_tiles<1, false>(xmap, amap, bmap, g, s);
-    case 2: return yb ? launch_tiles<2, true>(xmap, amap, bmap, g, s) : launch_tiles<2, false>(xmap, amap, bmap, g, s);
-    case 4: return yb ? launch_tiles<4, true>(xmap, amap, bmap, g, s) : launch_tiles<4, false>(xmap, amap, bmap, g, s);
-    default: return yb ? launch_tiles<8, true>(xmap, amap, bmap, g, s) : launch_tiles<8, false>(xmap, amap, bmap, g, s);
-  }
+  while (cl < 8 && tiles * cl * 2 <= sm_count()) cl *= 2;
+  if (yb) return tma ? launch_tiles<true, true>(cl, maps, g, s) : launch_tiles<true, false>(cl, maps, g, s);
+  return tma ? launch_tiles<false, true>(cl, maps, g, s) : launch_tiles<false, false>(cl, maps, g, s);
 }
 
 }  // namespace bl
