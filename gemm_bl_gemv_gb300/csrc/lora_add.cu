@@ -1,12 +1,27 @@
-// Low-rank adapters of many requests beside a shared product:
+// Low-rank adapters of many requests beside a shared product (bl_lora_add):
 //   y[m,n] = base[m,n] + scale[a] * sum_r B[a,n,r] (sum_k A[a,r,k] x[m,k]),
-// a = adapter[m], negative for none.
-#include "act_quant.cuh"
+// a = adapter[m], negative for none.  This file has the kernel for scattered
+// tokens (a decode step: every token has its own adapter); tiles of 128 tokens
+// with few runs of one adapter go to lora_tile.cu when x is bf16.
+//
+// A cluster of 8 CTAs takes up to four neighbouring tokens of one adapter.
+// Each CTA forms the inner products with an eighth of K, a warp a row of A at
+// a time; the eighths meet through distributed shared memory, added in rank
+// order; then each CTA forms an eighth of the outputs, a thread a row of B.
+// The CTA's part of B is fetched into L2 while A is being read, so that the
+// two matrices come from HBM in one stream.  All sums are fp32.
+//
+// Bound: HBM for many requests (A and B of every adapter once), latency for
+// one.
 #include "bl_internal.h"
 #include "lora.cuh"
 
 namespace bl {
 namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kParts = 8;      // CTAs of a cluster
+constexpr int kGroup = 4;      // tokens that share the reads of an adapter
 
 struct Args {
   const void* x;
@@ -18,60 +33,144 @@ struct Args {
   unsigned int* err;
   int64_t M, N, K, L;
   int R;
+  int per;     // tokens of a cluster
   bool tiles;  // tiles of few runs are another kernel's
 };
 
-// One CTA per token: a warp forms each of the R inner products with A's rows,
-// then a thread each output.
-template <bool XB, bool YB>
-__global__ void __launch_bounds__(256) lora_token_kernel(const Args g) {
-  __shared__ float low[128];
-  const int64_t m = blockIdx.x;
+struct Shared {
+  float part[2][kGroup][128];  // this CTA's share of the inner products; every second run uses the other half
+  float low[kGroup][128];
+};
+
+// This CTA's share of the inner products of `nt` tokens from m on with A[l].
+// A warp reads kRows rows of A at a time (kRows divides R).
+template <bool XB, int kRows>
+__device__ __forceinline__ void down(const Args& g, float (*part)[128], int64_t m, int nt, int64_t l, uint32_t me) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_wait();
+  const int chunks = int(g.K / 8), per = (chunks + kParts - 1) / kParts;
+  const int c0 = min(int(me) * per, chunks), c1 = min(c0 + per, chunks);
+  for (int r0 = warp * kRows; r0 < g.R; r0 += kWarps * kRows) {
+    float acc[kRows][kGroup] = {};
+    for (int c = c0 + lane; c < c1; c += 32) {
+      float av[kRows][8];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) load8<true>(g.a, (l * g.R + r0 + r) * chunks + c, av[r]);  // R % 8 == 0
+#pragma unroll
+      for (int t = 0; t < kGroup; ++t) {
+        if (t >= nt) break;
+        float xv[8];
+        load8<XB>(g.x, (m + t) * chunks + c, xv);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(av[r][j], xv[j], acc[r][t]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int t = 0; t < kGroup; ++t) {
+        if (t >= nt) break;
+        const float v = warp_sum(acc[r][t]);
+        if (lane == 0) part[t][r0 + r] = v;
+      }
+  }
+}
+
+template <bool XB, bool YB>
+__global__ void __launch_bounds__(kThreads) lora_token_kernel(const Args g) {
+  __shared__ Shared sh;
+  const uint32_t me = cluster_ctarank();
+  const int64_t first = int64_t(blockIdx.x / kParts) * g.per;
+  if (!g.tiles) pdl_wait();  // otherwise the tiles' kernel has waited, and runs beside this one
+  bool mine = true;
   if (g.tiles) {  // the tile's runs
-    const int64_t t = m / kTile * kTile + threadIdx.x;
+    const int64_t t = first / kTile * kTile + threadIdx.x;
     const bool start = threadIdx.x < kTile && t < g.M &&
                        (threadIdx.x == 0 || adapter_of(g.adapter, t, g.L) != adapter_of(g.adapter, t - 1, g.L));
-    if (__syncthreads_count(start) <= kTileRuns) return;
+    mine = __syncthreads_count(start) > kTileRuns;
   }
-  int64_t l = g.adapter[m];
-  if (l >= g.L) {
-    if (threadIdx.x == 0 && g.err) atomicOr(g.err, BL_DEVERR_RANGE);
-    l = -1;
-  }
-  if (l >= 0) {
-    for (int r = warp; r < g.R; r += blockDim.x / 32) {
-      float acc = 0.f;
-      for (int64_t i = lane; i < g.K / 8; i += 32) {
-        float xv[8], av[8];
-        load8<XB>(g.x, m * (g.K / 8) + i, xv);
-        load8<true>(g.a, (l * g.R + r) * (g.K / 8) + i, av);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc = fmaf(xv[j], av[j], acc);
-      }
-      acc = warp_sum(acc);
-      if (lane == 0) low[r] = acc * g.scale[l];
+  const int64_t n_part = (g.N + kParts - 1) / kParts, n0 = int64_t(me) * n_part, n1 = min(n0 + n_part, g.N);
+  int run = 0;
+  for (int64_t m = first; mine && m < min(first + g.per, g.M);) {
+    // the first of the tokens with this adapter among four aligned ones, and how many follow
+    const int l = adapter_of(g.adapter, m, g.L);
+    const int64_t end = min(g.M, (m / kGroup + 1) * kGroup);
+    if (m % kGroup != 0 && adapter_of(g.adapter, m - 1, g.L) == l) {
+      ++m;
+      continue;
     }
-  }
-  __syncthreads();
-  for (int64_t n = threadIdx.x; n < g.N; n += blockDim.x) {
-    const int64_t i = m * g.N + n;
-    float acc = 0.f;
-    if (l >= 0)
+    int nt = 1;
+    while (m + nt < end && adapter_of(g.adapter, m + nt, g.L) == l) ++nt;
+    if (me == 0 && threadIdx.x < nt && g.adapter[m + threadIdx.x] >= g.L && g.err) atomicOr(g.err, BL_DEVERR_RANGE);
+    if (l < 0) {
+      if (g.y != g.base)
+        for (int t = 0; t < nt; ++t)
+          for (int64_t n = n0 + threadIdx.x; n < n1; n += kThreads)
+            store1<YB>(g.y, (m + t) * g.N + n, load1<YB>(g.base, (m + t) * g.N + n));
+      m += nt;
+      continue;
+    }
+    const uint16_t* b = g.b + int64_t(l) * g.N * g.R;
+    for (int64_t i = n0 * g.R + int64_t(threadIdx.x) * 64; i < n1 * g.R; i += kThreads * 64)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(b + i));
+    float(*part)[128] = sh.part[run & 1];
+    if (g.R <= 16)
+      down<XB, 2>(g, part, m, nt, l, me);
+    else
+      down<XB, 4>(g, part, m, nt, l, me);
+    cluster_sync();
+    for (int i = threadIdx.x; i < nt * g.R; i += kThreads) {
+      const int t = i / g.R, r = i % g.R;
+      float v = 0.f;
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) v += *peer(&part[t][r], q);
+      sh.low[t][r] = v * g.scale[l];
+    }
+    __syncthreads();
+    for (int64_t n = n0 + threadIdx.x; n < n1; n += kThreads) {
+      float acc[kGroup] = {};
       for (int r = 0; r < g.R; r += 8) {
         float bv[8];
-        load8<true>(g.b, ((l * g.N + n) * g.R + r) / 8, bv);
+        load8<true>(b, (n * g.R + r) / 8, bv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc = fmaf(bv[j], low[r + j], acc);
+        for (int t = 0; t < kGroup; ++t) {
+          if (t >= nt) break;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[t] = fmaf(bv[j], sh.low[t][r + j], acc[t]);
+        }
       }
-    if (YB)
-      reinterpret_cast<uint16_t*>(g.y)[i] =
-          f32_to_bf16_bits_rn(bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(g.base)[i]) + acc);
-    else
-      reinterpret_cast<float*>(g.y)[i] = reinterpret_cast<const float*>(g.base)[i] + acc;
+#pragma unroll
+      for (int t = 0; t < kGroup; ++t) {
+        if (t >= nt) break;
+        const int64_t i = (m + t) * g.N + n;
+        store1<YB>(g.y, i, load1<YB>(g.base, i) + acc[t]);
+      }
+    }
+    __syncthreads();  // the last use of low
+    ++run;
+    m += nt;
   }
+  // another CTA may still read this one's share (after two runs the barrier between them has settled it)
+  if (run > 0) cluster_sync();
+  if (g.tiles && blockIdx.x == 0) pdl_wait();  // this kernel's end is the call's end
   pdl_launch_dependents();
+}
+
+template <bool XB, bool YB>
+cudaError_t launch_tokens(const Args& g, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((g.M + g.per - 1) / g.per * kParts));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {kParts, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap_enabled() || g.tiles ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, lora_token_kernel<XB, YB>, g);
 }
 
 }  // namespace
@@ -79,18 +178,18 @@ __global__ void __launch_bounds__(256) lora_token_kernel(const Args g) {
 cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
                             const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
                             int64_t K, int64_t adapters, int rank, cudaStream_t s) {
-  Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, false};
-  const bool pdl = overlap_enabled();
+  // A cluster per token while that is at most a few per SM; beyond, per four.
+  const int per = M <= 256 ? 1 : kGroup;
+  if ((M + per - 1) / per > 0x7fffffff / kParts) return cudaErrorInvalidConfiguration;
+  Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, per, false};
   if (xt == BL_BF16 && M > 32) {
     const cudaError_t e = launch_lora_tile(x, adapter, a, b, scale, base, y, yt, M, N, K, adapters, rank, s);
     if (e != cudaSuccess && e != cudaErrorNotSupported) return e;
     g.tiles = e == cudaSuccess;
   }
-  const dim3 grid{unsigned(M)}, block{256};
-  if (xt == BL_BF16 && yt == BL_BF16) return launch(lora_token_kernel<true, true>, grid, block, 0, s, pdl, g);
-  if (xt == BL_BF16) return launch(lora_token_kernel<true, false>, grid, block, 0, s, pdl, g);
-  if (yt == BL_BF16) return launch(lora_token_kernel<false, true>, grid, block, 0, s, pdl, g);
-  return launch(lora_token_kernel<false, false>, grid, block, 0, s, pdl, g);
+  const bool xb = xt == BL_BF16, yb = yt == BL_BF16;
+  if (xb) return yb ? launch_tokens<true, true>(g, s) : launch_tokens<true, false>(g, s);
+  return yb ? launch_tokens<false, true>(g, s) : launch_tokens<false, false>(g, s);
 }
 
 }  // namespace bl

@@ -5,8 +5,8 @@
 // A cluster of CL CTAs takes 128 tokens.  A run is a stretch of those tokens
 // with one adapter; a tile of more than kTileRuns runs is left to the kernel
 // for scattered tokens.
-//   1. Down: each CTA takes a part of K.  x (128 x 64 blocks) and the run's A
-//      (rank x 64) come by TMA through a ring; the tensor core forms the
+//   1. Down: each CTA takes a part of K.  x (128 x 64 blocks) and the runs' A
+//      (rank x 64, up to two runs at once) come by TMA through a ring; the tensor core forms the
 //      128 x rank product in TMEM, and the rows of the run go to shared
 //      memory as fp32.  The CTAs add their parts up in rank order through
 //      distributed shared memory, so the sum over K is never rounded below
@@ -17,7 +17,7 @@
 //   3. Up: each CTA takes tiles of 256 bytes of outputs (128 bf16, 64 fp32).
 //      B's rows come by TMA as they lie in memory, and so does the tile of
 //      base, 128-byte swizzled, three tiles ahead.  Every run of the 128 tokens
-//      has its own product in one of two TMEM buffers; the thread of a row adds
+//      has its own product in one of four TMEM buffers; the thread of a row adds
 //      its run's to the base in place, and the tile goes out by TMA, rows
 //      without an adapter unchanged.  Rows of y that are not 16-byte aligned
 //      (N * element size not a multiple of 16) are read and written by the
@@ -38,7 +38,8 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kStages = 3;                 // K blocks of 64 in flight
 constexpr int kTiles = 3;                  // tiles of base in flight
 constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; half a tile of base
-constexpr uint32_t kTmemCols = 256;        // two accumulators of up to 128 columns
+constexpr uint32_t kTmemCols = 512;        // four accumulators of up to 128 columns
+constexpr int kAcc = 4;
 constexpr int kTurn = 33;                  // floats of a row of 32 outputs being turned
 
 __host__ __device__ constexpr uint32_t idesc(int n) {  // bf16 x bf16 -> fp32, M = 128
@@ -46,36 +47,51 @@ __host__ __device__ constexpr uint32_t idesc(int n) {  // bf16 x bf16 -> fp32, M
 }
 
 // Shared memory.  First [ring of x and A | partial sums]; then, over both,
-// [operand terms | ring of B | ring of base, or turning buffers].  The operand
-// lies within the ring, clear of the partial sums that it is made from.
+// [operand terms | ring of B], and the ring of base or turning buffers.  The
+// operand lies within the ring, clear of the partial sums that it is made from.
 struct Plan {
   int rp, rk;             // rank rounded up to 16 (MMA N and K) and to 64 (operand sub-tiles)
-  uint32_t a_bytes;       // of a ring stage's A block
+  uint32_t a_bytes, a_at; // of a run's A block in a ring stage; from one to the next
+  int group;              // runs whose A goes through the ring together
   uint32_t stage;         // of a ring stage
   uint32_t term;          // of one operand term, [128][rk] in 64-column sub-tiles
   uint32_t part_at;       // byte offset of the partial sums
   uint32_t part_row;      // floats of a row of them
   uint32_t up_at, up_stage;  // ring of B tiles
+  int up_n;               // tiles of it
   uint32_t base_at;       // ring of base tiles
-  uint32_t bar_at, total;
+  bool early;             // they do not overlap the first part
+  uint32_t end;
 };
-__host__ __device__ inline Plan make_plan(int rank, int terms, int n_tile) {
+__host__ __device__ inline Plan make_plan(int rank, int terms, int n_tile, int runs) {
   Plan p;
   p.rp = (rank + 15) / 16 * 16;
   p.rk = (rank + 63) / 64 * 64;
   p.a_bytes = uint32_t(p.rp) * 128;
-  p.stage = kXBytes + (p.a_bytes + 1023) / 1024 * 1024;
+  p.a_at = (p.a_bytes + 1023) / 1024 * 1024;
+  p.group = p.rp <= 64 && runs > 1 ? 2 : 1;
+  p.stage = kXBytes + uint32_t(p.group) * p.a_at;
   p.term = uint32_t(p.rk) / 64 * kTile * 128;
   const uint32_t ring = kStages * p.stage, operand = p.term * terms;
-  p.part_at = ring > operand ? ring : operand;
-  p.part_row = uint32_t(p.rp) + 4;
   p.up_at = operand;
   p.up_stage = uint32_t(p.rk) / 64 * n_tile * 128;
-  p.base_at = p.up_at + 2 * p.up_stage;
-  const uint32_t one = p.part_at + kTile * p.part_row * 4, two = p.base_at + kTiles * 2 * kXBytes;
-  p.bar_at = (one > two ? one : two) / 1024 * 1024 + 1024;
-  p.total = p.bar_at + 1024;
+  p.up_n = p.rk == 64 ? 4 : 2;
+  const uint32_t up_end = p.up_at + p.up_n * p.up_stage;
+  p.part_at = ring > operand ? ring : operand;
+  p.part_row = uint32_t(p.rp) + 4;
+  // base tiles clear of everything else where that fits, so that they come early
+  const uint32_t one = p.part_at + kTile * p.part_row * 4, base = kTiles * 2 * kXBytes;
+  p.early = (one > up_end ? one : up_end) + base + 3072 <= 227 * 1024;  // and the control block
+  p.base_at = p.early ? ((one > up_end ? one : up_end) + 1023) / 1024 * 1024 : up_end;
+  const uint32_t two = p.base_at + base;
+  p.end = ((one > two ? one : two) + 1023) / 1024 * 1024;
   return p;
+}
+
+// The control block lies behind either layout.
+__host__ __device__ inline uint32_t control_at(int rank, int terms, int n_tile) {
+  const uint32_t one = make_plan(rank, terms, n_tile, 1).end, two = make_plan(rank, terms, n_tile, 2).end;
+  return one > two ? one : two;
 }
 
 struct Args {
@@ -88,10 +104,10 @@ struct Args {
   int rank;
 };
 
-struct Control {  // at Plan::bar_at
-  uint64_t full[kStages], empty[kStages], sums[2], drained[2], up_full[2], up_empty[2], out_full[2], out_empty[2];
+struct Control {  // at control_at()
+  uint64_t full[kStages], empty[kStages], sums, drained, up_full[kAcc], up_empty[kAcc], out_full[kAcc], out_empty[kAcc];
   uint64_t base_full[kTiles], base_done[kTiles], base_empty[kTiles];
-  uint32_t tmem, starts[4];
+  uint32_t tmem, starts[4], used[4];  // used: runs that have an adapter
   int abort;
   int adapter[kTile];  // of each token, -1: none
 };
@@ -102,19 +118,27 @@ struct Runs {
   const uint32_t* starts;
   int t, end, size;
   __device__ __forceinline__ Runs(const uint32_t* s, int n) : starts(s), t(0), end(0), size(n) {}
+  // The end of the run that starts at token s.
+  __device__ __forceinline__ int end_of(int s) const {
+    for (int w = (s + 1) / 32; w < 4; ++w) {
+      uint32_t b = starts[w];
+      if (w == (s + 1) / 32) b &= 0xFFFFFFFFu << ((s + 1) & 31);
+      if (b) return min(size, w * 32 + __ffs(b) - 1);
+    }
+    return size;
+  }
   __device__ __forceinline__ bool next() {
     t = end;
     if (t >= size) return false;
-    end = size;
-    for (int w = (t + 1) / 32; w < 4; ++w) {
-      uint32_t b = starts[w];
-      if (w == (t + 1) / 32) b &= 0xFFFFFFFFu << ((t + 1) & 31);
-      if (b) {
-        end = min(size, w * 32 + __ffs(b) - 1);
-        break;
-      }
-    }
+    end = end_of(t);
     return true;
+  }
+  // The starts of the next `most` runs with an adapter.
+  __device__ __forceinline__ int group(const int* adapter, int most, int* from) {
+    int n = 0;
+    while (n < most && next())
+      if (adapter[t] >= 0) from[n++] = t;
+    return n;
   }
 };
 
@@ -128,8 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   constexpr int kTerms = YB ? 2 : 3;
   constexpr int kN = YB ? 128 : 64;  // outputs of an up tile
   extern __shared__ __align__(1024) uint8_t smem[];
-  const Plan p = make_plan(g.rank, kTerms, kN);
-  Control& c = *reinterpret_cast<Control*>(smem + p.bar_at);
+  Control& c = *reinterpret_cast<Control*>(smem + control_at(g.rank, kTerms, kN));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t me = CL == 1 ? 0 : cluster_ctarank();
   const int64_t m0 = int64_t(blockIdx.x / CL) * kTile;
@@ -143,9 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   if (threadIdx.x == 0) {
     c.abort = 0;
     for (int i = 0; i < kStages; ++i) mbar_init(&c.full[i], 1), mbar_init(&c.empty[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&c.sums[i], 1);
-      mbar_init(&c.drained[i], kEpilogueWarps);
+    mbar_init(&c.sums, 1);
+    mbar_init(&c.drained, kEpilogueWarps);
+    for (int i = 0; i < kAcc; ++i) {
       mbar_init(&c.up_full[i], 1);
       mbar_init(&c.up_empty[i], 1);
       mbar_init(&c.out_full[i], 1);
@@ -159,13 +182,15 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     fence_barrier_init();
   }
   pdl_wait();
+  pdl_launch_dependents();  // the kernel for the other tiles, which ends after this one
   if (threadIdx.x < kTile) {
     const int t = threadIdx.x;
     const int a = t < size ? adapter_of(g.adapter, m0 + t, g.L) : -1;
     c.adapter[t] = a;
     const int before = t > 0 && t < size ? adapter_of(g.adapter, m0 + t - 1, g.L) : -2;
     const uint32_t b = __ballot_sync(0xffffffffu, t < size && a != before);
-    if (lane == 0) c.starts[warp] = b;
+    const uint32_t u = __ballot_sync(0xffffffffu, t < size && a != before && a >= 0);
+    if (lane == 0) c.starts[warp] = b, c.used[warp] = u;
     if (me == 0 && t < size && g.adapter[m0 + t] >= g.L && g.err) atomicOr(g.err, BL_DEVERR_RANGE);
   }
   tc_fence_before();
@@ -174,74 +199,92 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   const uint32_t tmem = c.tmem;
   const bool mine = __popc(c.starts[0]) + __popc(c.starts[1]) + __popc(c.starts[2]) + __popc(c.starts[3]) <= kTileRuns;
 
+  const Plan p = make_plan(g.rank, kTerms, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]));
+
   if (mine) {
     const int blocks = int((g.K + 63) / 64), per = (blocks + CL - 1) / CL;
     const int k0 = min(int(me) * per, blocks), k1 = min(k0 + per, blocks);
+    const int tiles = int((g.N + kN - 1) / kN);
+    constexpr int kHalf = kN / 2;  // outputs of 128 bytes
     // ---- 1. down ----
+    // Runs with an adapter, in groups whose A blocks go through the ring beside one block of x.
+    auto base_tile = [&](int n, int bs) {
+      const bool two = int64_t(n) * kN + kHalf < g.N;
+      uint8_t* dst = smem + p.base_at + bs * 2 * kXBytes;
+      mbar_arrive_expect_tx(&c.base_full[bs], two ? 2 * kXBytes : kXBytes);
+      tma_load_2d(dst, &base_map, n * 256, int(m0), &c.base_full[bs]);
+      if (two) tma_load_2d(dst + kXBytes, &base_map, n * 256 + 128, int(m0), &c.base_full[bs]);
+    };
+    int early = 0;  // base tiles requested before the up phase
     if (warp == 0 && lane == 0) {
       int it = 0;
-      for (Runs r(c.starts, size); r.next();) {
-        const int a = c.adapter[r.t];
-        if (a < 0) continue;
+      if (TMA && p.early)
+        for (int n = int(me); n < tiles && early < kTiles; n += CL, ++early) base_tile(n, early);
+      Runs r(c.starts, size);
+      for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0 && !*abort;) {
         for (int kb = k0; kb < k1; ++kb, ++it) {
           const int st = it % kStages;
           if (it >= kStages && !*abort && !mbar_wait_bounded(&c.empty[st], uint32_t(it / kStages - 1) & 1u, g.err))
             *abort = 1;
           if (*abort) break;
-          mbar_arrive_expect_tx(&c.full[st], kXBytes + p.a_bytes);
-          tma_load_2d(smem + st * p.stage, &xmap, kb * 128, int(m0), &c.full[st]);
-          tma_load_2d(smem + st * p.stage + kXBytes, &amap, kb * 128, a * g.rank, &c.full[st]);
+          uint8_t* dst = smem + st * p.stage;
+          mbar_arrive_expect_tx(&c.full[st], kXBytes + n * p.a_bytes);
+          tma_load_2d(dst, &xmap, kb * 128, int(m0), &c.full[st]);
+          for (int j = 0; j < n; ++j)
+            tma_load_2d(dst + kXBytes + j * p.a_at, &amap, kb * 128, c.adapter[group[j]] * g.rank, &c.full[st]);
         }
-        if (*abort) break;
       }
       // nothing may still be on its way into the ring when it is used for the operand
       for (int i = max(0, it - kStages); i < it; ++i)
         mbar_wait_bounded(&c.full[i % kStages], uint32_t(i / kStages) & 1u, nullptr);
     } else if (warp == 1 && lane == 0) {
-      int it = 0, run = 0;
+      int it = 0, turn = 0;
       const uint32_t sbase = smem_addr(smem);
-      for (Runs r(c.starts, size); r.next();) {
-        if (c.adapter[r.t] < 0) continue;
-        const uint32_t acc = tmem + uint32_t(run & 1) * 128;
-        if (run >= 2 && !*abort && !mbar_wait_bounded(&c.drained[run & 1], uint32_t(run / 2 - 1) & 1u, g.err)) *abort = 1;
+      Runs r(c.starts, size);
+      for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0; ++turn) {
+        if (turn > 0 && !*abort && !mbar_wait_bounded(&c.drained, uint32_t(turn - 1) & 1u, g.err)) *abort = 1;
         tc_fence_after();
         for (int kb = k0; kb < k1; ++kb, ++it) {
           const int st = it % kStages;
           if (!*abort && !mbar_wait_bounded(&c.full[st], uint32_t(it / kStages) & 1u, g.err)) *abort = 1;
           tc_fence_after();
-          const uint32_t xa = sbase + st * p.stage, aa = xa + kXBytes;
+          const uint32_t xa = sbase + st * p.stage;
           if (!*abort)
+            for (int j = 0; j < n; ++j)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_f16(acc, umma_desc_sw128(xa + ks * 32), umma_desc_sw128(aa + ks * 32), idesc(p.rp), kb > k0 || ks > 0);
+              for (int ks = 0; ks < 4; ++ks)
+                umma_f16(tmem + j * 128, umma_desc_sw128(xa + ks * 32),
+                         umma_desc_sw128(xa + kXBytes + j * p.a_at + ks * 32), idesc(p.rp), kb > k0 || ks > 0);
           umma_commit(&c.empty[st]);
         }
-        umma_commit(&c.sums[run & 1]);
-        ++run;
+        umma_commit(&c.sums);
       }
     } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
       float* part = reinterpret_cast<float*>(smem + p.part_at);
       const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane;
-      int run = 0;
-      for (Runs r(c.starts, size); r.next();) {
-        if (c.adapter[r.t] < 0) continue;
-        if (!*abort && !mbar_wait_bounded(&c.sums[run & 1], uint32_t(run / 2) & 1u, g.err)) *abort = 1;
+      int turn = 0;
+      Runs r(c.starts, size);
+      for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0; ++turn) {
+        if (!*abort && !mbar_wait_bounded(&c.sums, uint32_t(turn) & 1u, g.err)) *abort = 1;
         tc_fence_after();
-        for (int col = half * 16; col < p.rp; col += 32) {
-          uint32_t v[16];
-          tmem_ld16(tmem + uint32_t(run & 1) * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
-          tmem_ld_wait();
-          if (row >= r.t && row < r.end) {
+        for (int j = 0; j < n; ++j) {
+          const int from = group[j], to = Runs(c.starts, size).end_of(from);
+          if (max(from, quarter * 32) >= min(to, quarter * 32 + 32)) continue;
+          for (int col = half * 16; col < p.rp; col += 32) {
+            uint32_t v[16];
+            tmem_ld16(tmem + j * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
+            tmem_ld_wait();
+            if (row >= from && row < to) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(part + row * p.part_row + col + 4 * j) =
-                  k1 > k0 ? make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]) : make_uint4(0, 0, 0, 0);
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(part + row * p.part_row + col + 4 * q) =
+                    k1 > k0 ? make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_uint4(0, 0, 0, 0);
+            }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.drained[run & 1]);
-        ++run;
+        if (lane == 0) mbar_arrive(&c.drained);
       }
     }
     tc_fence_before();
@@ -285,28 +328,22 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     if (CL == 1) __syncthreads(); else cluster_sync();  // and nobody reads the partial sums any more
 
     // ---- 3. up ----
-    const int tiles = int((g.N + kN - 1) / kN);
-    constexpr int kHalf = kN / 2;  // outputs of 128 bytes
     if (warp == 0 && lane == 0) {
       int it = 0, tl = 0;
       for (int n = int(me); n < tiles && !*abort; n += CL, ++tl) {
-        if (TMA) {
+        if (TMA && tl >= early) {
           const int bs = tl % kTiles;
           if (tl >= kTiles && !mbar_wait_bounded(&c.base_empty[bs], uint32_t(tl / kTiles - 1) & 1u, g.err)) {
             *abort = 1;
             break;
           }
-          const bool two = int64_t(n) * kN + kHalf < g.N;
-          uint8_t* dst = smem + p.base_at + bs * 2 * kXBytes;
-          mbar_arrive_expect_tx(&c.base_full[bs], two ? 2 * kXBytes : kXBytes);
-          tma_load_2d(dst, &base_map, n * 256, int(m0), &c.base_full[bs]);
-          if (two) tma_load_2d(dst + kXBytes, &base_map, n * 256 + 128, int(m0), &c.base_full[bs]);
+          base_tile(n, bs);
         }
         for (Runs r(c.starts, size); r.next();) {
           const int a = c.adapter[r.t];
           if (a < 0) continue;
-          const int st = it & 1;
-          if (it >= 2 && !mbar_wait_bounded(&c.up_empty[st], uint32_t(it / 2 - 1) & 1u, g.err)) {
+          const int st = it % p.up_n;
+          if (it >= p.up_n && !mbar_wait_bounded(&c.up_empty[st], uint32_t(it / p.up_n - 1) & 1u, g.err)) {
             *abort = 1;
             break;
           }
@@ -318,9 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         }
       }
       // the CTA must not finish while a load still writes its shared memory
-      for (int i = max(0, it - 2); i < it; ++i) mbar_wait_bounded(&c.up_full[i & 1], uint32_t(i / 2) & 1u, nullptr);
+      for (int i = max(0, it - p.up_n); i < it; ++i)
+        mbar_wait_bounded(&c.up_full[i % p.up_n], uint32_t(i / p.up_n) & 1u, nullptr);
       if (TMA)
-        for (int i = max(0, tl - kTiles); i < tl; ++i)
+        for (int i = max(0, max(tl, early) - kTiles); i < max(tl, early); ++i)
           mbar_wait_bounded(&c.base_full[i % kTiles], uint32_t(i / kTiles) & 1u, nullptr);
     } else if (warp == 1 && lane == 0) {
       int it = 0;
@@ -328,19 +366,19 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       for (int n = int(me); n < tiles; n += CL)
         for (Runs r(c.starts, size); r.next();) {
           if (c.adapter[r.t] < 0) continue;
-          const int st = it & 1;
-          if (!*abort && !mbar_wait_bounded(&c.up_full[st], uint32_t(it / 2) & 1u, g.err)) *abort = 1;
-          if (it >= 2 && !*abort && !mbar_wait_bounded(&c.out_empty[st], uint32_t(it / 2 - 1) & 1u, g.err)) *abort = 1;
+          const int st = it % p.up_n, acc = it % kAcc;
+          if (!*abort && !mbar_wait_bounded(&c.up_full[st], uint32_t(it / p.up_n) & 1u, g.err)) *abort = 1;
+          if (it >= kAcc && !*abort && !mbar_wait_bounded(&c.out_empty[acc], uint32_t(it / kAcc - 1) & 1u, g.err)) *abort = 1;
           tc_fence_after();
           const uint32_t ba = sbase + p.up_at + st * p.up_stage;
           if (!*abort)
             for (int t = 0; t < kTerms; ++t)
               for (int ks = 0; ks < p.rp / 16; ++ks)
-                umma_f16(tmem + st * 128,
+                umma_f16(tmem + acc * 128,
                          umma_desc_sw128(sbase + t * p.term + uint32_t(ks >> 2) * (kTile * 128) + (ks & 3) * 32),
                          umma_desc_sw128(ba + uint32_t(ks >> 2) * (kN * 128) + (ks & 3) * 32), idesc(kN), t > 0 || ks > 0);
           umma_commit(&c.up_empty[st]);
-          umma_commit(&c.out_full[st]);
+          umma_commit(&c.out_full[acc]);
           ++it;
         }
     } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
@@ -363,10 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
                   store1<YB>(g.y, (m0 + i) * g.N + j, load1<YB>(g.base, (m0 + i) * g.N + j));
             continue;
           }
-          const int st = it & 1;
-          if (!*abort && !mbar_wait_bounded(&c.out_full[st], uint32_t(it / 2) & 1u, g.err)) *abort = 1;
+          const int acc = it % kAcc;
+          if (!*abort && !mbar_wait_bounded(&c.out_full[acc], uint32_t(it / kAcc) & 1u, g.err)) *abort = 1;
           tc_fence_after();
-          const uint32_t at = tmem + st * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(half * kHalf);
+          const uint32_t at = tmem + acc * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(half * kHalf);
           if (ra < rb && !*abort && n0 < g.N) {
             if (TMA) {
 #pragma unroll
@@ -425,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&c.out_empty[st]);
+          if (lane == 0) mbar_arrive(&c.out_empty[acc]);
           ++it;
         }
         if (TMA) {
@@ -451,7 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     }
   }
   __syncwarp();
-  pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -469,12 +506,12 @@ cudaError_t launch_tiles(const Maps& maps, const Args& g, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   constexpr int kTerms = YB ? 2 : 3, kN = YB ? 128 : 64;
-  const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(make_plan(128, kTerms, kN).total));
+  const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(control_at(128, kTerms, kN) + 1024));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((g.M + kTile - 1) / kTile * CL));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = make_plan(g.rank, kTerms, kN).total;
+  cfg.dynamicSmemBytes = control_at(g.rank, kTerms, kN) + 1024;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;
