@@ -184,6 +184,13 @@ __device__ __forceinline__ uint16_t f32_to_bf16_bits_rn(float f) {
   return r;
 }
 
+// Two floats as packed bf16, `lo` in the lower half.
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

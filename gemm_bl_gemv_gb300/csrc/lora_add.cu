@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads) lora_token_kernel(const Args g) {
       down<XB, 2>(g, part, m, nt, l, me);
     else
       down<XB, 4>(g, part, m, nt, l, me);
+    __syncwarp();  // the cluster barrier wants converged warps
     cluster_sync();
     for (int i = threadIdx.x; i < nt * g.R; i += kThreads) {
       const int t = i / g.R, r = i % g.R;
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(kThreads) lora_token_kernel(const Args g) {
     m += nt;
   }
   // another CTA may still read this one's share (after two runs the barrier between them has settled it)
+  __syncwarp();
   if (run > 0) cluster_sync();
   if (g.tiles && blockIdx.x == 0) pdl_wait();  // this kernel's end is the call's end
   pdl_launch_dependents();

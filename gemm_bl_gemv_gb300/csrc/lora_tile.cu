@@ -142,6 +142,12 @@ struct Runs {
   }
 };
 
+// Whether the condition holds in every lane.  Each lane polls a barrier by
+// itself, and tcgen05.ld is undefined unless the whole warp executes it
+// together: a warp-wide vote after the wait brings the lanes together again and
+// gives them one decision (the flag may be raised between two lanes' reads).
+__device__ __forceinline__ bool warp_agrees(bool c) { return __all_sync(0xffffffffu, c) != 0; }
+
 // YB: base and y are bf16.  TMA: they come and go by TMA.
 template <int CL, bool YB, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_constant__ CUtensorMap xmap,
@@ -160,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   volatile int* abort = &c.abort;
 
   if (warp == 1) {
+    __syncwarp();
     tmem_alloc(&c.tmem, kTmemCols);
     tmem_relinquish();
   }
@@ -200,6 +207,15 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   const bool mine = __popc(c.starts[0]) + __popc(c.starts[1]) + __popc(c.starts[2]) + __popc(c.starts[3]) <= kTileRuns;
 
   const Plan p = make_plan(g.rank, kTerms, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]));
+
+  // All threads of the cluster; the barrier wants converged warps.
+  auto sync_all = [] {
+    __syncwarp();
+    if (CL == 1)
+      __syncthreads();
+    else
+      cluster_sync();
+  };
 
   if (mine) {
     const int blocks = int((g.K + 63) / 64), per = (blocks + CL - 1) / CL;
@@ -267,11 +283,13 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0; ++turn) {
         if (!*abort && !mbar_wait_bounded(&c.sums, uint32_t(turn) & 1u, g.err)) *abort = 1;
         tc_fence_after();
+        const bool ok = warp_agrees(!*abort);  // and the warp is converged for tcgen05.ld
         for (int j = 0; j < n; ++j) {
           const int from = group[j], to = Runs(c.starts, size).end_of(from);
-          if (max(from, quarter * 32) >= min(to, quarter * 32 + 32)) continue;
+          if (!ok || max(from, quarter * 32) >= min(to, quarter * 32 + 32)) continue;
           for (int col = half * 16; col < p.rp; col += 32) {
             uint32_t v[16];
+            __syncwarp();
             tmem_ld16(tmem + j * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
             tmem_ld_wait();
             if (row >= from && row < to) {
@@ -288,8 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       }
     }
     tc_fence_before();
-    __syncwarp();
-    if (CL == 1) __syncthreads(); else cluster_sync();
+    sync_all();
     tc_fence_after();
 
     // ---- 2. the operand: eight columns of a row at a time ----
@@ -325,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       }
     }
     fence_async_smem();
-    if (CL == 1) __syncthreads(); else cluster_sync();  // and nobody reads the partial sums any more
+    sync_all();  // and nobody reads the partial sums any more
 
     // ---- 3. up ----
     if (warp == 0 && lane == 0) {
@@ -405,11 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           if (!*abort && !mbar_wait_bounded(&c.out_full[acc], uint32_t(it / kAcc) & 1u, g.err)) *abort = 1;
           tc_fence_after();
           const uint32_t at = tmem + acc * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(half * kHalf);
-          if (ra < rb && !*abort && n0 < g.N) {
+          const bool ok = warp_agrees(!*abort);  // and the warp is converged for tcgen05.ld
+          if (ra < rb && ok && n0 < g.N) {
             if (TMA) {
 #pragma unroll
               for (int h = 0; h < kHalf; h += 32) {
                 uint32_t d[32];
+                __syncwarp();
                 tmem_ld16(at + h, *reinterpret_cast<uint32_t(*)[16]>(d));
                 tmem_ld16(at + h + 16, *reinterpret_cast<uint32_t(*)[16]>(d + 16));
                 tmem_ld_wait();
@@ -439,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
 #pragma unroll
               for (int h = 0; h < kHalf; h += 32) {
                 uint32_t d[32];
+                __syncwarp();
                 tmem_ld16(at + h, *reinterpret_cast<uint32_t(*)[16]>(d));
                 tmem_ld16(at + h + 16, *reinterpret_cast<uint32_t(*)[16]>(d + 16));
                 tmem_ld_wait();
@@ -492,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

@@ -36,12 +36,15 @@ __device__ __forceinline__ T warp_scan(T v) {
   return v;
 }
 
+// All threads of the cluster; the cluster barrier wants converged warps.
 template <int C>
 __device__ __forceinline__ void sync_cluster() {
-  if (C == 1)
+  if (C == 1) {
     __syncthreads();
-  else
+  } else {
+    __syncwarp();
     cluster_sync();
+  }
 }
 
 // `grid` CTAs of `threads` in clusters of C.

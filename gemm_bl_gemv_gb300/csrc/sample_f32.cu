@@ -125,9 +125,9 @@ struct Row {
   __device__ __forceinline__ u64 cluster_total(u64 v) {
     v = cta_sum(v);
     if (C == 1) return v;
-    cluster_sync();  // earlier readers of sum
+    sync_cluster<C>();  // earlier readers of sum
     if (threadIdx.x == 0) sh.sum = v;
-    cluster_sync();
+    sync_cluster<C>();
     v = 0;
     for (uint32_t r = 0; r < C; ++r) v += *at(&sh.sum, r);
     return v;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) sample_f32_kernel(const Args g) {
   lo = -warp_max(-sh.redf[1][lane]);
   if (C > 1) {
     if (threadIdx.x == 0) sh.high = hi, sh.low = lo;
-    cluster_sync();
+    sync_cluster<C>();
 #pragma unroll
     for (uint32_t r = 0; r < C; ++r) hi = fmaxf(hi, *peer(&sh.high, r)), lo = fminf(lo, *peer(&sh.low, r));
   }
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) sample_f32_kernel(const Args g) {
       g.token[m] = -1;
       if (g.prob) g.prob[m] = 0.f;
     }
-    if (C > 1) cluster_sync();
+    if (C > 1) sync_cluster<C>();
     pdl_launch_dependents();
     return;
   }
@@ -364,9 +364,9 @@ __global__ void __launch_bounds__(kThreads) sample_f32_kernel(const Args g) {
   if constexpr (C > 1) {
     const uint32_t cta = uint32_t(redux_add(int(counts)));
     if (threadIdx.x == 0) sh.equal = cta;
-    cluster_sync();
+    sync_cluster<C>();
     for (uint32_t r = 0; r < rank; ++r) before += *peer(&sh.equal, r);
-    cluster_sync();  // the last read of another CTA's memory
+    sync_cluster<C>();  // the last read of another CTA's memory
   }
   if (before <= p.rank && p.rank - before < mine) {
     uint32_t left = p.rank - before;
