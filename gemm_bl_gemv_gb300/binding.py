@@ -93,12 +93,18 @@ def _check(status):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # ctypes takes the integer
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:  # the handle without a Stream object around it
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _dtype_code(t):
@@ -352,14 +358,17 @@ def bl_gemm_tq2_0_int8(q, s, packed, N, y=None, stream=None):
 # ---- around the products -----------------------------------------------------
 
 def _like(t, name, dtype, shape, device):
-    """An optional or given tensor must have exactly this dtype, shape and device."""
-    _cuda(t, name)
-    if t.dtype != dtype:
+    """A tensor given for an argument: exactly this dtype and shape, contiguous, on CUDA device `device`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s" % (name, dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s" % (name, tuple(shape)))
-    if t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.get_device() != device:
+        raise ValueError("%s must be on device %d" % (name, device))
     return t
 
 
@@ -371,7 +380,7 @@ def bl_rmsnorm_quant_int8(x, rms_weight, eps=1e-5, residual=None, h=None, y=Fals
     None otherwise)."""
     _cuda(x, "x")
     M, K = x.shape
-    xt, dev = _dtype_code(x), x.device
+    xt, dev = _dtype_code(x), x.get_device()
     _like(rms_weight, "rms_weight", x.dtype, (K,), dev)
     if residual is not None:
         _like(residual, "residual", x.dtype, (M, K), dev)
@@ -385,8 +394,8 @@ def bl_rmsnorm_quant_int8(x, rms_weight, eps=1e-5, residual=None, h=None, y=Fals
         y = None
     else:
         _like(y, "y", x.dtype, (M, K), dev)
-    q = torch.empty((M, K), dtype=torch.int8, device=dev) if q is None else _like(q, "q", torch.int8, (M, K), dev)
-    s = torch.empty(M, dtype=torch.float32, device=dev) if s is None else _like(s, "s", torch.float32, (M,), dev)
+    q = torch.empty((M, K), dtype=torch.int8, device=x.device) if q is None else _like(q, "q", torch.int8, (M, K), dev)
+    s = torch.empty(M, dtype=torch.float32, device=x.device) if s is None else _like(s, "s", torch.float32, (M,), dev)
     _check(_lib.bl_rmsnorm_quant_int8(_ptr(x), _ptr(residual), xt, _ptr(rms_weight), float(eps), M, K, _ptr(h), _ptr(y),
                                       _ptr(q), _ptr(s), _stream(stream)))
     return q, s, h, y
@@ -399,7 +408,7 @@ def bl_lora_add(x, adapter, a, b, scale, base, y=None, stream=None):
     fp32 [L]; base and y [M, N], y may be base."""
     _cuda(x, "x")
     M, K = x.shape
-    dev = x.device
+    dev = x.get_device()
     _like(a, "a", torch.bfloat16, (a.shape[0], a.shape[1], K), dev)
     L, R = a.shape[0], a.shape[1]
     N = base.shape[1]
@@ -420,16 +429,16 @@ def bl_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     temperature, top_p, min_p (fp32 [M]) and top_k (int32 [M]) default to 1, 1, 0 and all tokens."""
     _cuda(logits, "logits")
     M, V = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     _like(u, "u", torch.float32, (M,), dev)
     for t, n in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p")):
         if t is not None:
             _like(t, n, torch.float32, (M,), dev)
     if top_k is not None:
         _like(top_k, "top_k", torch.int32, (M,), dev)
-    token = torch.empty(M, dtype=torch.int32, device=dev) if token is None else _like(token, "token", torch.int32, (M,), dev)
+    token = torch.empty(M, dtype=torch.int32, device=logits.device) if token is None else _like(token, "token", torch.int32, (M,), dev)
     if prob is True:
-        prob = torch.empty(M, dtype=torch.float32, device=dev)
+        prob = torch.empty(M, dtype=torch.float32, device=logits.device)
     elif prob is False or prob is None:
         prob = None
     else:
