@@ -40,4 +40,15 @@ __device__ __forceinline__ void store8(void* at, const float (&v)[8]) {
   }
 }
 
+// acc + the product of eight bf16 with eight floats.
+__device__ __forceinline__ float dot8(uint4 q, const float (&v)[8], float acc) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    acc = fmaf(__uint_as_float(w[j] << 16), v[2 * j], acc);
+    acc = fmaf(__uint_as_float(w[j] & 0xffff0000u), v[2 * j + 1], acc);
+  }
+  return acc;
+}
+
 }  // namespace bl

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kParts = 8;      // CTAs of a cluster
+constexpr double kTileWork = 3e8;  // multiply-adds from which the tiles' kernel is launched as well
 constexpr int kGroup = 4;      // tokens that share the reads of an adapter
 
 struct Args {
@@ -37,48 +38,79 @@ struct Args {
   bool tiles;  // tiles of few runs are another kernel's
 };
 
-struct Shared {
+struct __align__(16) Shared {
   float part[2][kGroup][128];  // this CTA's share of the inner products; every second run uses the other half
   float low[kGroup][128];
 };
 
-// This CTA's share of the inner products of `nt` tokens from m on with A[l].
-// A warp reads kRows rows of A at a time (kRows divides R).
-template <bool XB, int kRows>
+// This CTA's share of the inner products of NT tokens from m on with A[l].  A
+// warp reads kRows rows of A at a time (kRows divides R).
+template <bool XB, int NT, int kRows>
 __device__ __forceinline__ void down(const Args& g, float (*part)[128], int64_t m, int nt, int64_t l, uint32_t me) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunks = int(g.K / 8), per = (chunks + kParts - 1) / kParts;
   const int c0 = min(int(me) * per, chunks), c1 = min(c0 + per, chunks);
   for (int r0 = warp * kRows; r0 < g.R; r0 += kWarps * kRows) {
-    float acc[kRows][kGroup] = {};
+    const uint4* rows = reinterpret_cast<const uint4*>(g.a) + (l * g.R + r0) * chunks;
+    float acc[kRows][NT] = {};
     for (int c = c0 + lane; c < c1; c += 32) {
-      float av[kRows][8];
+      uint4 q[kRows];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) load8<true>(g.a, (l * g.R + r0 + r) * chunks + c, av[r]);  // R % 8 == 0
+      for (int r = 0; r < kRows; ++r) q[r] = rows[int64_t(r) * chunks + c];
 #pragma unroll
-      for (int t = 0; t < kGroup; ++t) {
-        if (t >= nt) break;
+      for (int t = 0; t < NT; ++t) {
+        if (NT > 1 && t >= nt) break;
         float xv[8];
         load8<XB>(g.x, (m + t) * chunks + c, xv);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(av[r][j], xv[j], acc[r][t]);
+        for (int r = 0; r < kRows; ++r) acc[r][t] = dot8(q[r], xv, acc[r][t]);
       }
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
 #pragma unroll
-      for (int t = 0; t < kGroup; ++t) {
-        if (t >= nt) break;
+      for (int t = 0; t < NT; ++t) {
+        if (NT > 1 && t >= nt) break;
         const float v = warp_sum(acc[r][t]);
         if (lane == 0) part[t][r0 + r] = v;
       }
   }
 }
 
+// This CTA's outputs [n0, n1) of NT tokens: a thread a row of B, two rows at a time.
+template <bool YB, int NT>
+__device__ __forceinline__ void up(const Args& g, const float (*low)[128], int64_t m, int nt, const uint16_t* b,
+                                   int64_t n0, int64_t n1) {
+  const int r8 = g.R / 8;
+  for (int64_t n = n0 + threadIdx.x; n < n1; n += 2 * kThreads) {
+    const bool two = n + kThreads < n1;
+    const uint4* row0 = reinterpret_cast<const uint4*>(b + n * g.R);
+    const uint4* row1 = two ? row0 + int64_t(kThreads) * r8 : row0;
+    float acc0[NT] = {}, acc1[NT] = {};
+#pragma unroll 4
+    for (int r = 0; r < r8; ++r) {
+      const uint4 q0 = row0[r], q1 = row1[r];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float4 f0 = *reinterpret_cast<const float4*>(&low[t][8 * r]);
+        const float4 f1 = *reinterpret_cast<const float4*>(&low[t][8 * r + 4]);
+        const float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+        acc0[t] = dot8(q0, v, acc0[t]);
+        acc1[t] = dot8(q1, v, acc1[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (NT > 1 && t >= nt) break;
+      const int64_t i = (m + t) * g.N + n;
+      store1<YB>(g.y, i, load1<YB>(g.base, i) + acc0[t]);
+      if (two) store1<YB>(g.y, i + kThreads, load1<YB>(g.base, i + kThreads) + acc1[t]);
+    }
+  }
+}
+
 template <bool XB, bool YB>
-__global__ void __launch_bounds__(kThreads) lora_token_kernel(const Args g) {
+__global__ void __launch_bounds__(kThreads, 4) lora_token_kernel(const Args g) {
   __shared__ Shared sh;
   const uint32_t me = cluster_ctarank();
   const int64_t first = int64_t(blockIdx.x / kParts) * g.per;
@@ -115,10 +147,12 @@ __global__ void __launch_bounds__(kThreads) lora_token_kernel(const Args g) {
     for (int64_t i = n0 * g.R + int64_t(threadIdx.x) * 64; i < n1 * g.R; i += kThreads * 64)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(b + i));
     float(*part)[128] = sh.part[run & 1];
-    if (g.R <= 16)
-      down<XB, 2>(g, part, m, nt, l, me);
+    if (nt > 1)
+      down<XB, kGroup, 2>(g, part, m, nt, l, me);
+    else if (g.R <= 16)
+      down<XB, 1, 2>(g, part, m, nt, l, me);
     else
-      down<XB, 4>(g, part, m, nt, l, me);
+      down<XB, 1, 4>(g, part, m, nt, l, me);
     __syncwarp();  // the cluster barrier wants converged warps
     cluster_sync();
     for (int i = threadIdx.x; i < nt * g.R; i += kThreads) {
@@ -129,25 +163,10 @@ __global__ void __launch_bounds__(kThreads) lora_token_kernel(const Args g) {
       sh.low[t][r] = v * g.scale[l];
     }
     __syncthreads();
-    for (int64_t n = n0 + threadIdx.x; n < n1; n += kThreads) {
-      float acc[kGroup] = {};
-      for (int r = 0; r < g.R; r += 8) {
-        float bv[8];
-        load8<true>(b, (n * g.R + r) / 8, bv);
-#pragma unroll
-        for (int t = 0; t < kGroup; ++t) {
-          if (t >= nt) break;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[t] = fmaf(bv[j], sh.low[t][r + j], acc[t]);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < kGroup; ++t) {
-        if (t >= nt) break;
-        const int64_t i = (m + t) * g.N + n;
-        store1<YB>(g.y, i, load1<YB>(g.base, i) + acc[t]);
-      }
-    }
+    if (nt > 1)
+      up<YB, kGroup>(g, sh.low, m, nt, b, n0, n1);
+    else
+      up<YB, 1>(g, sh.low, m, nt, b, n0, n1);
     __syncthreads();  // the last use of low
     ++run;
     m += nt;
@@ -184,7 +203,10 @@ cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, 
   const int per = M <= 256 ? 1 : kGroup;
   if ((M + per - 1) / per > 0x7fffffff / kParts) return cudaErrorInvalidConfiguration;
   Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, per, false};
-  if (xt == BL_BF16 && M > 32) {
+  // The tiles' kernel takes some 25 us however few they are; this one reads an adapter again for every
+  // group of four tokens and does M rank (K + N) multiply-adds on the CUDA cores.  (517 tokens, rank 24, 2560
+  // -> 2560, 6e7 of them: KK us here, 42 us in tiles; 8192 tokens, rank 64, 2560 -> 6912, 5e9: 117 us in tiles.)
+  if (xt == BL_BF16 && M > 32 && double(M) * rank * double(K + N) > kTileWork) {
     const cudaError_t e = launch_lora_tile(x, adapter, a, b, scale, base, y, yt, M, N, K, adapters, rank, s);
     if (e != cudaSuccess && e != cudaErrorNotSupported) return e;
     g.tiles = e == cudaSuccess;
