@@ -84,22 +84,50 @@ struct Row {
     return C == 1 ? p : peer(p, r);
   }
 
+  // f(logit) for this thread's logits of the chunk, eight loads at a time (a loop of one load each waits
+  // for L2 every time: 16 us instead of KK for a chunk of 25001).
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    int i = threadIdx.x;
+    for (; i + 7 * kThreads < n; i += 8 * kThreads) {
+      float l[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) l[j] = x[i + j * kThreads];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f(l[j]);
+    }
+    float l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) l[j] = i + j * kThreads < n ? x[i + j * kThreads] : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j * kThreads < n) f(l[j]);
+  }
+
   // ---- a logit's digits ----
   __device__ __forceinline__ bool live(float l) const {
     return slope.hi < 0.f ? l == top : l > -INFINITY && __fmul_rn(__fsub_rn(top, l), slope.hi) < kOctaves;
   }
+  __device__ __forceinline__ float place_of(float l) const {  // rises as l falls; its whole part is the first digit
+    return slope.hi < 0.f ? 0.f : fminf(__fmul_rn(__fsub_rn(top, l), scale), float(kBins) - 0.0625f);
+  }
   __device__ __forceinline__ uint32_t digit_of(float l, int depth) const {
     if (depth < 2) {
-      const float y = slope.hi < 0.f ? 0.f : fminf(__fmul_rn(__fsub_rn(top, l), scale), float(kBins) - 0.0625f);  // rises as l falls
+      const float y = place_of(l);
       const uint32_t b = uint32_t(y);
       return depth == 0 ? b : uint32_t((y - float(b)) * float(kBins));
     }
     const uint32_t k = ~key_of_f32(l);
     return depth == 2 ? k >> 21 : depth == 3 ? (k >> 10) & 2047u : k & 1023u;
   }
-  __device__ __forceinline__ bool matches(float l, const Path& p) const {
+  // Whether a logit is on the path; most fail the first comparison.  `from` is the path's first digit.
+  __device__ __forceinline__ bool matches(float l, const Path& p, float from) const {
+    if (p.depth > 0) {
+      const float y = place_of(l);
+      if (!(y >= from && y < from + 1.f)) return false;
+    }
     if (!live(l)) return false;
-    for (int d = 0; d < p.depth; ++d)
+    for (int d = 1; d < p.depth; ++d)
       if (digit_of(l, d) != p.bin[d]) return false;
     return true;
   }
@@ -137,15 +165,15 @@ struct Row {
   __device__ void cut(const Path& p, Sums& sums) {
     for (int i = threadIdx.x; i < kBins; i += kThreads) sh.digit.count[i] = sh.digit.hi[i] = sh.digit.lo[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const float l = x[i];
-      if (!matches(l, p)) continue;
+    const float from = p.depth > 0 ? float(p.bin[0]) : 0.f;
+    each([&](float l) {
+      if (!matches(l, p, from)) return;
       const uint32_t b = digit_of(l, p.depth);
       const uint32_t w = relative(l, octave_of(p.depth == 0 ? b : p.bin[0]));
       atomicAdd(&sh.digit.count[b], 1u);
       atomicAdd(&sh.digit.hi[b], w >> 16);
       atomicAdd(&sh.digit.lo[b], w & 0xFFFFu);
-    }
+    });
     sync_cluster<C>();
     // each CTA adds up a slice of the bins
     constexpr int kSlice = kBins / C;
@@ -224,10 +252,10 @@ struct Row {
       // its logits' keys, falling, one per thread of rank 0
       if (threadIdx.x == 0) sh.listed = 0;
       sync_cluster<C>();
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const float l = x[i];
-        if (matches(l, p)) at(&sh.list[0], 0)[atomicAdd(at(&sh.listed, 0), 1u)] = key_of_f32(l);
-      }
+      const float from = float(p.bin[0]);
+      each([&](float l) {
+        if (matches(l, p, from)) at(&sh.list[0], 0)[atomicAdd(at(&sh.listed, 0), 1u)] = key_of_f32(l);
+      });
       sync_cluster<C>();
       if (rank == 0) {
         const uint32_t i = threadIdx.x;
@@ -289,11 +317,10 @@ __global__ void __launch_bounds__(kThreads) sample_f32_kernel(const Args g) {
 
   // the largest and the smallest live logit
   float hi = -INFINITY, lo = INFINITY;
-  for (int i = threadIdx.x; i < row.n; i += kThreads) {
-    const float l = row.x[i];
+  row.each([&](float l) {
     hi = fmaxf(hi, l);
     if (l > -INFINITY) lo = fminf(lo, l);
-  }
+  });
   hi = warp_max(hi);
   lo = -warp_max(-lo);
   if (lane == 0) sh.redf[0][warp] = hi, sh.redf[1][warp] = lo;
@@ -341,11 +368,10 @@ __global__ void __launch_bounds__(kThreads) sample_f32_kernel(const Args g) {
   }
   if (f.min_w > 0 && (whole || last.weight < f.min_w)) {
     kept = 0;
-    for (int i = threadIdx.x; i < row.n; i += kThreads) {
-      const float l = row.x[i];
+    row.each([&](float l) {
       const u64 w = row.live(l) ? weight_of(l, row.top, row.slope, sh.exp2) : 0;
       kept += w >= f.min_w ? w : 0;
-    }
+    });
     kept = row.cluster_total(kept);
   }
   const Place p = row.find(false, mass_target(f.u, kept));
