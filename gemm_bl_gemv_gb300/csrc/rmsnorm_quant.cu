@@ -154,15 +154,39 @@ __device__ __forceinline__ void store8(void* row, int i, const float (&v)[8]) {
   }
 }
 
+// v rounded to bf16 and widened again, two at a time.
+__device__ __forceinline__ void round8(float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint32_t w = bf16x2_rn(v[j], v[j + 1]);
+    v[j] = __uint_as_float(w << 16);
+    v[j + 1] = __uint_as_float(w & 0xffff0000u);
+  }
+}
+
+// quant8's codes without its slow conversions: adding 1.5 * 2^23 rounds a
+// value of |v inv| < 2^22 to the nearest integer, ties to even, and leaves it
+// in the low bits.  |v inv| <= 127 (1 + 2^-22) here, so no clamp is needed.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+  uint32_t b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.f));
+  return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
+
 // The row stays in registers: thread t of a token's threads has chunks t, t +
 // threads, ... of 8 elements, at most CH of them; everything is read and
 // written once.  WARP: a warp per token, eight tokens per CTA (no barriers);
 // otherwise a CTA per token, whose sums and maxima meet in shared memory.
 // 16-byte aligned rows, K % 8 == 0.
 //
-// Bound: HBM.  (8192 x 5120 bf16 with a residual: KK us, KK GB/s.)  The pair
-// sums are 7 float operations per element beside about 12 for the rest, of
-// the 23 that the SMs issue per element in the time its bytes take.
+// The thread's sum starts from its largest square m0, which is taken off
+// again: then no term exceeds the sum so far, and the rounding error of an
+// addition is (v - (t - hi)), four operations instead of seven.
+//
+// Bound: HBM, with the arithmetic close behind: about 20 operations per
+// element of the 23 that the SMs issue in the time its 7 bytes take.
 template <bool XB, int CH, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_quant_rows_kernel(const Args a) {
   __shared__ Pair red[WARP ? 1 : 32];
@@ -193,23 +217,36 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_quant_rows_kernel(c
         float r[8];
         load8<XB>(res, i, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[c][j] = __fadd_rn(v[c][j], r[j]);
-          if (XB) v[c][j] = bf16_bits_to_f32(f32_to_bf16_bits_rn(v[c][j]));
-        }
+        for (int j = 0; j < 8; ++j) v[c][j] = __fadd_rn(v[c][j], r[j]);
+        if (XB) round8(v[c]);
       }
     }
   }
-  Pair p = {0.f, 0.f};
+  float m0 = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = t + c * threads;
     if (i < n8) {
       if (h) store8<XB>(h, i, v[c]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) pair_add_square<XB>(p, v[c][j]);
+      for (int j = 0; j < 8; ++j) m0 = fmaxf(m0, fabsf(v[c][j]));
     }
   }
+  m0 = __fmul_rn(m0, m0);
+  Pair p = {m0, 0.f};
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+    if (t + c * threads < n8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float sq = __fmul_rn(v[c][j], v[c][j]);
+        if (!XB) p.lo = __fadd_rn(p.lo, __fmaf_rn(v[c][j], v[c][j], -sq));
+        const float sum = __fadd_rn(p.hi, sq);
+        p.lo = __fadd_rn(p.lo, __fsub_rn(sq, __fsub_rn(sum, p.hi)));
+        p.hi = sum;
+      }
+    }
+  pair_add(p, -m0);
   p = warp_pair_sum(p);
   if (!WARP) {
     if (lane == 0) red[warp] = p;
@@ -245,7 +282,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_quant_rows_kernel(c
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = t + c * threads;
-    if (i < n8) q[i] = quant8(v[c], inv);
+    if (i < n8) q[i] = codes8(v[c], inv);
   }
   pdl_launch_dependents();
 }
