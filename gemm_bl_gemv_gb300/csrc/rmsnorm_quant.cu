@@ -39,21 +39,19 @@ __device__ __forceinline__ void pair_add_square(Pair& p, float h) {
   pair_add(p, sq);
 }
 
-__device__ __forceinline__ Pair warp_pair_sum(Pair p) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Pair q;
-    q.hi = __shfl_xor_sync(0xffffffffu, p.hi, o);
-    q.lo = __shfl_xor_sync(0xffffffffu, p.lo, o);
-    // the two lanes add in the same order, so that every lane holds one result
-    if (threadIdx.x & o) {
-      pair_add(q, p);
-      p = q;
-    } else {
-      pair_add(p, q);
-    }
+// Sum over groups of `lanes` lanes (a power of two).  A two-sum's error term
+// is exact, so the lanes of a pair compute the same result in either order.
+__device__ __forceinline__ Pair warp_pair_sum(Pair p, int lanes = 32) {
+  for (int o = lanes / 2; o > 0; o >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, p.hi, o), lo = __shfl_xor_sync(0xffffffffu, p.lo, o);
+    p.lo = __fadd_rn(p.lo, lo);
+    pair_add(p, hi);
   }
   return p;
+}
+__device__ __forceinline__ float warp_max_of(float v, int lanes) {
+  for (int o = lanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
 // fl(1 / sqrt(sum / K + eps)): the mean in pairs (1/K given as one), one
@@ -248,10 +246,13 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_quant_rows_kernel(c
     }
   pair_add(p, -m0);
   p = warp_pair_sum(p);
+  int lanes = 1;  // that hold the warps' sums, several times over
   if (!WARP) {
+    while (lanes < nw) lanes *= 2;
     if (lane == 0) red[warp] = p;
     __syncthreads();
-    p = warp_pair_sum(lane < nw ? red[lane] : Pair{0.f, 0.f});
+    const int w = lane & (lanes - 1);
+    p = warp_pair_sum(w < nw ? red[w] : Pair{0.f, 0.f}, lanes);
   }
   const float r = inv_rms(p, a.inv_k, a.eps);
   float most = 0.f;
@@ -273,11 +274,15 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_quant_rows_kernel(c
   if (!WARP) {
     if (lane == 0) redm[warp] = most;
     __syncthreads();
-    most = warp_max(lane < nw ? redm[lane] : 0.f);
+    const int w = lane & (lanes - 1);
+    most = warp_max_of(w < nw ? redm[w] : 0.f, lanes);
   }
-  float sc, inv;
-  absmax_scales(most, sc, inv);
-  if (t == 0) a.s[m] = sc;
+  const float inv = most == 0.f ? 0.f : __fdiv_rn(127.f, most);  // absmax_scales, its scale by one thread
+  if (t == 0) {
+    float sc, unused;
+    absmax_scales(most, sc, unused);
+    a.s[m] = sc;
+  }
   uint2* q = reinterpret_cast<uint2*>(a.q + m * a.K);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -308,13 +313,13 @@ cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, bl_dtype x
   const uintptr_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) |
                         reinterpret_cast<uintptr_t>(rms_w) | reinterpret_cast<uintptr_t>(h) | reinterpret_cast<uintptr_t>(y);
   if (K % 8 == 0 && (all & 15) == 0 && (reinterpret_cast<uintptr_t>(q) & 7) == 0 && K <= 32768) {
-    // Chunks per thread: one while a row then has at most 512 threads (the shortest chain of loads and
-    // barriers: one token), two to four beyond, so that several rows share an SM.
+    // Chunks per thread: for few tokens one while a row then has at most 512 threads (the shortest chain),
+    // for many four: a warp's share of the two reductions costs as much as 8 elements per lane (8192 x 5120
+    // bf16: 320 threads with two chunks 67 us, 160 with four 62 us).
     const int64_t n8 = K / 8;
-    if (n8 <= 128 && n8 > 32 && M > sm_count())  // a warp per token
-      return xb ? launch_rows<true, 4>(a, s, pdl) : launch_rows<false, 4>(a, s, pdl);
-    if (n8 <= 512) return xb ? launch_rows<true, 1>(a, s, pdl) : launch_rows<false, 1>(a, s, pdl);
-    if (n8 <= 1024) return xb ? launch_rows<true, 2>(a, s, pdl) : launch_rows<false, 2>(a, s, pdl);
+    const bool many = M > 2 * sm_count();
+    if (n8 <= 512 && !many) return xb ? launch_rows<true, 1>(a, s, pdl) : launch_rows<false, 1>(a, s, pdl);
+    if (n8 <= 1024 && !many) return xb ? launch_rows<true, 2>(a, s, pdl) : launch_rows<false, 2>(a, s, pdl);
     return xb ? launch_rows<true, 4>(a, s, pdl) : launch_rows<false, 4>(a, s, pdl);
   }
   if (xb) return launch(rmsnorm_quant_any_kernel<true>, dim3(unsigned(M)), dim3(512), 0, s, pdl, a);
