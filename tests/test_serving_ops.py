@@ -520,3 +520,33 @@ def test_streams_overlap_and_graphs(B, M):
             assert same(got)
     finally:
         B.set_overlap(False)
+
+
+# ---------------------------------------------------------------------------
+# the operators together, as the example runs them
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("requests", [1, 7, 40])
+def test_example_serving_step(B, requests):
+    """The step's tokens are those of its logits, and an adapter changes the logits of its own requests only."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serving_step.py")
+    spec = importlib.util.spec_from_file_location("serving_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    model = example.Model(256, 512, 4000, adapters=4, rank=16)
+    v = list(example.inputs(requests, 256, 4))
+    token, prob, logits = example.step(model, *v)
+    rows = host(logits)
+    args = [t.cpu().numpy() for t in v[3:]]
+    for m in range(requests):
+        u, t, k, p, mp = (a[m] for a in args)
+        want, pr, margin, near = R.sample_row(rows[m], u, t, int(k), p, mp)
+        assert token[m].item() == want or (margin < 2.0 ** -28 and near[token[m].item()] < 2.0 ** -28)
+    none = v[2] < 0
+    v[2] = torch.full_like(v[2], -1)
+    plain = example.step(model, *v)[2]
+    assert torch.equal(plain[none], logits[none])
+    assert bool((plain != logits).any(1)[~none].all())
