@@ -14,9 +14,9 @@
 //   2. The sums, times the adapter's scale, become bf16 operands: two terms
 //      (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8, three
 //      (24 bits) for fp32 outputs.
-//   3. Up: each CTA takes tiles of 256 bytes of outputs (128 bf16, 64 fp32).
+//   3. Up: each CTA takes tiles of 128 bytes of outputs (64 bf16, 32 fp32).
 //      B's rows come by TMA as they lie in memory, and so does the tile of
-//      base, 128-byte swizzled, three tiles ahead.  Every run of the 128 tokens
+//      base, 128-byte swizzled, two tiles ahead.  Every run of the 128 tokens
 //      has its own product in one of four TMEM buffers; the thread of a row adds
 //      its run's to the base in place, and the tile goes out by TMA, rows
 //      without an adapter unchanged.  Rows of y that are not 16-byte aligned
@@ -33,13 +33,13 @@
 namespace bl {
 namespace {
 
-constexpr int kWarps = 11, kThreads = 32 * kWarps;  // loads, MMA, 8 epilogue warps, stores
+constexpr int kWarps = 11, kThreads = 32 * kWarps;  // x, A and B; MMA; 8 epilogue warps; base and y
 constexpr int kEpilogueWarps = 8;
-constexpr int kStages = 3;                 // K blocks of 64 in flight
+constexpr int kStages = 3;                 // most K blocks of 64 in flight
 constexpr int kTiles = 3;                  // tiles of base in flight
-constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; half a tile of base
-constexpr uint32_t kTmemCols = 512;        // four accumulators of up to 128 columns
-constexpr int kAcc = 4;
+constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; a tile of base
+constexpr int kAcc = 4, kAccCols = 64;     // accumulators of up to 64 columns (one of the down phase: 128)
+constexpr uint32_t kTmemCols = kAcc * kAccCols;
 constexpr int kTurn = 33;                  // floats of a row of 32 outputs being turned
 
 __host__ __device__ constexpr uint32_t idesc(int n) {  // bf16 x bf16 -> fp32, M = 128
@@ -47,20 +47,21 @@ __host__ __device__ constexpr uint32_t idesc(int n) {  // bf16 x bf16 -> fp32, M
 }
 
 // Shared memory.  First [ring of x and A | partial sums]; then, over both,
-// [operand terms | ring of B], and the ring of base or turning buffers.  The
-// operand lies within the ring, clear of the partial sums that it is made from.
+// [operand terms | ring of B | ring of base, or turning buffers].  The operand
+// lies within the ring, clear of the partial sums that it is made from.  At
+// ranks up to 64 two CTAs fit on an SM: one moves x while the other moves y.
 struct Plan {
   int rp, rk;             // rank rounded up to 16 (MMA N and K) and to 64 (operand sub-tiles)
   uint32_t a_bytes, a_at; // of a run's A block in a ring stage; from one to the next
   int group;              // runs whose A goes through the ring together
   uint32_t stage;         // of a ring stage
+  int stages;             // of the ring: two where two runs' A blocks would keep a second CTA off the SM
   uint32_t term;          // of one operand term, [128][rk] in 64-column sub-tiles
   uint32_t part_at;       // byte offset of the partial sums
   uint32_t part_row;      // floats of a row of them
   uint32_t up_at, up_stage;  // ring of B tiles
   int up_n;               // tiles of it
   uint32_t base_at;       // ring of base tiles
-  bool early;             // they do not overlap the first part
   uint32_t end;
 };
 __host__ __device__ inline Plan make_plan(int rank, int terms, int n_tile, int runs) {
@@ -72,18 +73,16 @@ __host__ __device__ inline Plan make_plan(int rank, int terms, int n_tile, int r
   p.group = p.rp <= 64 && runs > 1 ? 2 : 1;
   p.stage = kXBytes + uint32_t(p.group) * p.a_at;
   p.term = uint32_t(p.rk) / 64 * kTile * 128;
-  const uint32_t ring = kStages * p.stage, operand = p.term * terms;
+  p.stages = p.group == 2 && p.rp > 32 ? 2 : kStages;
+  const uint32_t ring = p.stages * p.stage, operand = p.term * terms;
   p.up_at = operand;
   p.up_stage = uint32_t(p.rk) / 64 * n_tile * 128;
-  p.up_n = p.rk == 64 ? 4 : 2;
+  p.up_n = p.rk == 64 ? 3 : 2;
   const uint32_t up_end = p.up_at + p.up_n * p.up_stage;
   p.part_at = ring > operand ? ring : operand;
   p.part_row = uint32_t(p.rp) + 4;
-  // base tiles clear of everything else where that fits, so that they come early
-  const uint32_t one = p.part_at + kTile * p.part_row * 4, base = kTiles * 2 * kXBytes;
-  p.early = (one > up_end ? one : up_end) + base + 3072 <= 227 * 1024;  // and the control block
-  p.base_at = p.early ? ((one > up_end ? one : up_end) + 1023) / 1024 * 1024 : up_end;
-  const uint32_t two = p.base_at + base;
+  p.base_at = up_end;
+  const uint32_t one = p.part_at + kTile * p.part_row * 4, two = p.base_at + kTiles * kXBytes;
   p.end = ((one > two ? one : two) + 1023) / 1024 * 1024;
   return p;
 }
@@ -106,7 +105,7 @@ struct Args {
 
 struct Control {  // at control_at()
   uint64_t full[kStages], empty[kStages], sums, drained, up_full[kAcc], up_empty[kAcc], out_full[kAcc], out_empty[kAcc];
-  uint64_t base_full[kTiles], base_done[kTiles], base_empty[kTiles];
+  uint64_t base_full[kTiles], base_done[kTiles];
   uint32_t tmem, starts[4], used[4];  // used: runs that have an adapter
   int abort;
   int adapter[kTile];  // of each token, -1: none
@@ -117,7 +116,9 @@ static_assert(sizeof(Control) <= 1024, "");
 struct Runs {
   const uint32_t* starts;
   int t, end, size;
-  __device__ __forceinline__ Runs(const uint32_t* s, int n) : starts(s), t(0), end(0), size(n) {}
+  bool one;  // the tile is one run
+  __device__ __forceinline__ Runs(const uint32_t* s, int n, bool single)
+      : starts(s), t(0), end(0), size(n), one(single) {}
   // The end of the run that starts at token s.
   __device__ __forceinline__ int end_of(int s) const {
     for (int w = (s + 1) / 32; w < 4; ++w) {
@@ -130,7 +131,7 @@ struct Runs {
   __device__ __forceinline__ bool next() {
     t = end;
     if (t >= size) return false;
-    end = end_of(t);
+    end = one ? size : end_of(t);
     return true;
   }
   // The starts of the next `most` runs with an adapter.
@@ -150,13 +151,13 @@ __device__ __forceinline__ bool warp_agrees(bool c) { return __all_sync(0xffffff
 
 // YB: base and y are bf16.  TMA: they come and go by TMA.
 template <int CL, bool YB, bool TMA>
-__global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_constant__ CUtensorMap xmap,
+__global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_constant__ CUtensorMap xmap,
                                                              const __grid_constant__ CUtensorMap amap,
                                                              const __grid_constant__ CUtensorMap bmap,
                                                              const __grid_constant__ CUtensorMap base_map,
                                                              const __grid_constant__ CUtensorMap y_map, const Args g) {
   constexpr int kTerms = YB ? 2 : 3;
-  constexpr int kN = YB ? 128 : 64;  // outputs of an up tile
+  constexpr int kN = YB ? 64 : 32;  // outputs of an up tile
   extern __shared__ __align__(1024) uint8_t smem[];
   Control& c = *reinterpret_cast<Control*>(smem + control_at(g.rank, kTerms, kN));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -184,7 +185,6 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(&c.base_full[i], 1);
       mbar_init(&c.base_done[i], kEpilogueWarps);
-      mbar_init(&c.base_empty[i], 1);
     }
     fence_barrier_init();
   }
@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
-  const bool mine = __popc(c.starts[0]) + __popc(c.starts[1]) + __popc(c.starts[2]) + __popc(c.starts[3]) <= kTileRuns;
+  const int starts = __popc(c.starts[0]) + __popc(c.starts[1]) + __popc(c.starts[2]) + __popc(c.starts[3]);
+  const bool mine = starts <= kTileRuns, one = starts == 1;
 
   const Plan p = make_plan(g.rank, kTerms, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]));
 
@@ -221,26 +222,15 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     const int blocks = int((g.K + 63) / 64), per = (blocks + CL - 1) / CL;
     const int k0 = min(int(me) * per, blocks), k1 = min(k0 + per, blocks);
     const int tiles = int((g.N + kN - 1) / kN);
-    constexpr int kHalf = kN / 2;  // outputs of 128 bytes
     // ---- 1. down ----
     // Runs with an adapter, in groups whose A blocks go through the ring beside one block of x.
-    auto base_tile = [&](int n, int bs) {
-      const bool two = int64_t(n) * kN + kHalf < g.N;
-      uint8_t* dst = smem + p.base_at + bs * 2 * kXBytes;
-      mbar_arrive_expect_tx(&c.base_full[bs], two ? 2 * kXBytes : kXBytes);
-      tma_load_2d(dst, &base_map, n * 256, int(m0), &c.base_full[bs]);
-      if (two) tma_load_2d(dst + kXBytes, &base_map, n * 256 + 128, int(m0), &c.base_full[bs]);
-    };
-    int early = 0;  // base tiles requested before the up phase
     if (warp == 0 && lane == 0) {
       int it = 0;
-      if (TMA && p.early)
-        for (int n = int(me); n < tiles && early < kTiles; n += CL, ++early) base_tile(n, early);
-      Runs r(c.starts, size);
+      Runs r(c.starts, size, one);
       for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0 && !*abort;) {
         for (int kb = k0; kb < k1; ++kb, ++it) {
-          const int st = it % kStages;
-          if (it >= kStages && !*abort && !mbar_wait_bounded(&c.empty[st], uint32_t(it / kStages - 1) & 1u, g.err))
+          const int st = it % p.stages;
+          if (it >= p.stages && !*abort && !mbar_wait_bounded(&c.empty[st], uint32_t(it / p.stages - 1) & 1u, g.err))
             *abort = 1;
           if (*abort) break;
           uint8_t* dst = smem + st * p.stage;
@@ -251,25 +241,25 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         }
       }
       // nothing may still be on its way into the ring when it is used for the operand
-      for (int i = max(0, it - kStages); i < it; ++i)
-        mbar_wait_bounded(&c.full[i % kStages], uint32_t(i / kStages) & 1u, nullptr);
+      for (int i = max(0, it - p.stages); i < it; ++i)
+        mbar_wait_bounded(&c.full[i % p.stages], uint32_t(i / p.stages) & 1u, nullptr);
     } else if (warp == 1 && lane == 0) {
       int it = 0, turn = 0;
       const uint32_t sbase = smem_addr(smem);
-      Runs r(c.starts, size);
+      Runs r(c.starts, size, one);
       for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0; ++turn) {
         if (turn > 0 && !*abort && !mbar_wait_bounded(&c.drained, uint32_t(turn - 1) & 1u, g.err)) *abort = 1;
         tc_fence_after();
         for (int kb = k0; kb < k1; ++kb, ++it) {
-          const int st = it % kStages;
-          if (!*abort && !mbar_wait_bounded(&c.full[st], uint32_t(it / kStages) & 1u, g.err)) *abort = 1;
+          const int st = it % p.stages;
+          if (!*abort && !mbar_wait_bounded(&c.full[st], uint32_t(it / p.stages) & 1u, g.err)) *abort = 1;
           tc_fence_after();
           const uint32_t xa = sbase + st * p.stage;
           if (!*abort)
             for (int j = 0; j < n; ++j)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                umma_f16(tmem + j * 128, umma_desc_sw128(xa + ks * 32),
+                umma_f16(tmem + j * kAccCols, umma_desc_sw128(xa + ks * 32),
                          umma_desc_sw128(xa + kXBytes + j * p.a_at + ks * 32), idesc(p.rp), kb > k0 || ks > 0);
           umma_commit(&c.empty[st]);
         }
@@ -279,18 +269,18 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       float* part = reinterpret_cast<float*>(smem + p.part_at);
       const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane;
       int turn = 0;
-      Runs r(c.starts, size);
+      Runs r(c.starts, size, one);
       for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0; ++turn) {
         if (!*abort && !mbar_wait_bounded(&c.sums, uint32_t(turn) & 1u, g.err)) *abort = 1;
         tc_fence_after();
         const bool ok = warp_agrees(!*abort);  // and the warp is converged for tcgen05.ld
         for (int j = 0; j < n; ++j) {
-          const int from = group[j], to = Runs(c.starts, size).end_of(from);
+          const int from = group[j], to = r.end_of(from);
           if (!ok || max(from, quarter * 32) >= min(to, quarter * 32 + 32)) continue;
           for (int col = half * 16; col < p.rp; col += 32) {
             uint32_t v[16];
             __syncwarp();
-            tmem_ld16(tmem + j * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
+            tmem_ld16(tmem + j * kAccCols + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
             tmem_ld_wait();
             if (row >= from && row < to) {
 #pragma unroll
@@ -346,17 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
 
     // ---- 3. up ----
     if (warp == 0 && lane == 0) {
-      int it = 0, tl = 0;
-      for (int n = int(me); n < tiles && !*abort; n += CL, ++tl) {
-        if (TMA && tl >= early) {
-          const int bs = tl % kTiles;
-          if (tl >= kTiles && !mbar_wait_bounded(&c.base_empty[bs], uint32_t(tl / kTiles - 1) & 1u, g.err)) {
-            *abort = 1;
-            break;
-          }
-          base_tile(n, bs);
-        }
-        for (Runs r(c.starts, size); r.next();) {
+      int it = 0;
+      for (int n = int(me); n < tiles && !*abort; n += CL) {
+        for (Runs r(c.starts, size, one); r.next();) {
           const int a = c.adapter[r.t];
           if (a < 0) continue;
           const int st = it % p.up_n;
@@ -374,111 +356,100 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       // the CTA must not finish while a load still writes its shared memory
       for (int i = max(0, it - p.up_n); i < it; ++i)
         mbar_wait_bounded(&c.up_full[i % p.up_n], uint32_t(i / p.up_n) & 1u, nullptr);
-      if (TMA)
-        for (int i = max(0, max(tl, early) - kTiles); i < max(tl, early); ++i)
-          mbar_wait_bounded(&c.base_full[i % kTiles], uint32_t(i / kTiles) & 1u, nullptr);
     } else if (warp == 1 && lane == 0) {
       int it = 0;
       const uint32_t sbase = smem_addr(smem);
       for (int n = int(me); n < tiles; n += CL)
-        for (Runs r(c.starts, size); r.next();) {
+        for (Runs r(c.starts, size, one); r.next();) {
           if (c.adapter[r.t] < 0) continue;
           const int st = it % p.up_n, acc = it % kAcc;
           if (!*abort && !mbar_wait_bounded(&c.up_full[st], uint32_t(it / p.up_n) & 1u, g.err)) *abort = 1;
           if (it >= kAcc && !*abort && !mbar_wait_bounded(&c.out_empty[acc], uint32_t(it / kAcc - 1) & 1u, g.err)) *abort = 1;
           tc_fence_after();
-          const uint32_t ba = sbase + p.up_at + st * p.up_stage;
+          // 64 columns at a time; a step of 16 columns is 32 bytes, 2 in a descriptor's address field
           if (!*abort)
             for (int t = 0; t < kTerms; ++t)
-              for (int ks = 0; ks < p.rp / 16; ++ks)
-                umma_f16(tmem + acc * 128,
-                         umma_desc_sw128(sbase + t * p.term + uint32_t(ks >> 2) * (kTile * 128) + (ks & 3) * 32),
-                         umma_desc_sw128(ba + uint32_t(ks >> 2) * (kN * 128) + (ks & 3) * 32), idesc(kN), t > 0 || ks > 0);
+              for (int sub = 0; sub < p.rk / 64; ++sub) {
+                uint64_t ad = umma_desc_sw128(sbase + t * p.term + sub * (kTile * 128));
+                uint64_t bd = umma_desc_sw128(sbase + p.up_at + st * p.up_stage + sub * (kN * 128));
+                const int steps = min(4, p.rp / 16 - 4 * sub);
+                for (int ks = 0; ks < steps; ++ks, ad += 2, bd += 2)
+                  umma_f16(tmem + acc * kAccCols, ad, bd, idesc(kN), t > 0 || sub > 0 || ks > 0);
+              }
           umma_commit(&c.up_empty[st]);
           umma_commit(&c.out_full[acc]);
           ++it;
         }
     } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
+      constexpr int kCols = kN / 2;  // outputs of a warp: 64 bytes of a row
       const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane;
       float* turn = reinterpret_cast<float*>(smem + p.base_at) + (warp - 2) * 32 * kTurn;
       int it = 0, tl = 0;
       for (int n = int(me); n < tiles; n += CL, ++tl) {
-        const int bs = tl % kTiles, n0 = n * kN + half * kHalf;
-        // this thread's row of the tile of base: 16-byte unit u at u ^ (row % 8)
-        uint8_t* mine_row = smem + p.base_at + bs * 2 * kXBytes + half * kXBytes + row * 128;
+        const int bs = tl % kTiles, n0 = n * kN + half * kCols;
+        // this thread's 64 bytes of base: 16-byte unit u of a 128-byte row at u ^ (row % 8)
+        uint8_t* mine_row = smem + p.base_at + bs * kXBytes + row * 128;
+        auto unit = [&](int u) { return reinterpret_cast<uint4*>(mine_row + ((half * 4 + u) ^ (row & 7)) * 16); };
         if (TMA && !*abort && !mbar_wait_bounded(&c.base_full[bs], uint32_t(tl / kTiles) & 1u, g.err)) *abort = 1;
-        for (Runs r(c.starts, size); r.next();) {
+        for (Runs r(c.starts, size, one); r.next();) {
           const bool has = c.adapter[r.t] >= 0;
           // rows of this warp that are in the run
           const int ra = max(r.t, quarter * 32), rb = min(r.end, quarter * 32 + 32);
           if (!has) {
             if (!TMA && g.y != g.base)
-              for (int i = ra; i < rb; ++i)
-                for (int j = n0 + lane; j < min(n0 + kHalf, int(g.N)); j += 32)
-                  store1<YB>(g.y, (m0 + i) * g.N + j, load1<YB>(g.base, (m0 + i) * g.N + j));
+              for (int i = ra + lane / kCols; i < rb; i += 32 / kCols) {
+                const int j = n0 + lane % kCols;
+                if (j < g.N) store1<YB>(g.y, (m0 + i) * g.N + j, load1<YB>(g.base, (m0 + i) * g.N + j));
+              }
             continue;
           }
           const int acc = it % kAcc;
           if (!*abort && !mbar_wait_bounded(&c.out_full[acc], uint32_t(it / kAcc) & 1u, g.err)) *abort = 1;
           tc_fence_after();
-          const uint32_t at = tmem + acc * 128 + (uint32_t(quarter * 32) << 16) + uint32_t(half * kHalf);
           const bool ok = warp_agrees(!*abort);  // and the warp is converged for tcgen05.ld
           if (ra < rb && ok && n0 < g.N) {
+            const uint32_t at = tmem + acc * kAccCols + (uint32_t(quarter * 32) << 16) + uint32_t(half * kCols);
+            uint32_t d[kCols];
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < kCols; h += 16) tmem_ld16(at + h, *reinterpret_cast<uint32_t(*)[16]>(d + h));
             if (TMA) {
+              uint4 v[4];
 #pragma unroll
-              for (int h = 0; h < kHalf; h += 32) {
-                uint32_t d[32];
-                __syncwarp();
-                tmem_ld16(at + h, *reinterpret_cast<uint32_t(*)[16]>(d));
-                tmem_ld16(at + h + 16, *reinterpret_cast<uint32_t(*)[16]>(d + 16));
-                tmem_ld_wait();
-                if (row >= ra && row < rb) {
+              for (int u = 0; u < 4; ++u) v[u] = *unit(u);
+              tmem_ld_wait();
+              if (row >= ra && row < rb) {
 #pragma unroll
-                  for (int u = 0; u < (YB ? 4 : 8); ++u) {
-                    uint4* q = reinterpret_cast<uint4*>(mine_row + ((uint32_t(h * (YB ? 2 : 4) / 16 + u) ^ uint32_t(row & 7)) << 4));
-                    const uint4 v = *q;
-                    if (YB) {
-                      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int u = 0; u < 4; ++u) {
+                  uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-                      for (int j = 0; j < 4; ++j)
-                        w[j] = uint32_t(f32_to_bf16_bits_rn(__uint_as_float(w[j] << 16) + __uint_as_float(d[8 * u + 2 * j]))) |
-                               uint32_t(f32_to_bf16_bits_rn(__uint_as_float(w[j] & 0xffff0000u) +
-                                                            __uint_as_float(d[8 * u + 2 * j + 1]))) << 16;
-                      *q = make_uint4(w[0], w[1], w[2], w[3]);
-                    } else {
-                      const float4 f = *reinterpret_cast<const float4*>(&v);
-                      *reinterpret_cast<float4*>(q) =
-                          make_float4(f.x + __uint_as_float(d[4 * u]), f.y + __uint_as_float(d[4 * u + 1]),
-                                      f.z + __uint_as_float(d[4 * u + 2]), f.w + __uint_as_float(d[4 * u + 3]));
-                    }
-                  }
+                  for (int j = 0; j < 4; ++j)
+                    w[j] = YB ? bf16x2_rn(__uint_as_float(w[j] << 16) + __uint_as_float(d[(8 * u + 2 * j) % kCols]),
+                                          __uint_as_float(w[j] & 0xffff0000u) + __uint_as_float(d[(8 * u + 2 * j + 1) % kCols]))
+                              : __float_as_uint(__uint_as_float(w[j]) + __uint_as_float(d[(4 * u + j) % kCols]));
+                  *unit(u) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
               }
             } else {
+              tmem_ld_wait();
+              __syncwarp();
 #pragma unroll
-              for (int h = 0; h < kHalf; h += 32) {
-                uint32_t d[32];
-                __syncwarp();
-                tmem_ld16(at + h, *reinterpret_cast<uint32_t(*)[16]>(d));
-                tmem_ld16(at + h + 16, *reinterpret_cast<uint32_t(*)[16]>(d + 16));
-                tmem_ld_wait();
-                __syncwarp();
+              for (int j = 0; j < kCols; ++j) turn[lane * kTurn + j] = __uint_as_float(d[j]);
+              __syncwarp();
+              const int nn = n0 + lane % kCols;
+              constexpr int kStep = 32 / kCols;  // rows at a time
+              if (nn < g.N)
+                for (int i = ra + lane / kCols; i < rb; i += 8 * kStep) {
+                  float v[8];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) turn[lane * kTurn + j] = __uint_as_float(d[j]);
-                __syncwarp();
-                const int nn = n0 + h + lane;
-                if (nn < g.N)
-                  for (int i = ra; i < rb; i += 8) {
-                    float v[8];
+                  for (int j = 0; j < 8; ++j)
+                    if (i + j * kStep < rb) v[j] = load1<YB>(g.base, (m0 + i + j * kStep) * g.N + nn);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                      if (i + j < rb) v[j] = load1<YB>(g.base, (m0 + i + j) * g.N + nn);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                      if (i + j < rb)
-                        store1<YB>(g.y, (m0 + i + j) * g.N + nn, v[j] + turn[(i + j - quarter * 32) * kTurn + lane]);
-                  }
-              }
+                  for (int j = 0; j < 8; ++j)
+                    if (i + j * kStep < rb)
+                      store1<YB>(g.y, (m0 + i + j * kStep) * g.N + nn,
+                                 v[j] + turn[(i + j * kStep - quarter * 32) * kTurn + lane % kCols]);
+                }
             }
           }
           tc_fence_before();
@@ -493,18 +464,24 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         }
       }
     } else if (TMA && warp == 2 + kEpilogueWarps && lane == 0) {
-      int tl = 0;
+      auto fetch = [&](int n, int bs) {
+        mbar_arrive_expect_tx(&c.base_full[bs], kXBytes);
+        tma_load_2d(smem + p.base_at + bs * kXBytes, &base_map, n * 128, int(m0), &c.base_full[bs]);
+      };
+      int tl = 0, asked = 0;  // tiles stored, tiles asked for
+      for (; asked < kTiles && int(me) + asked * CL < tiles; ++asked) fetch(int(me) + asked * CL, asked);
       for (int n = int(me); n < tiles; n += CL, ++tl) {
         const int bs = tl % kTiles;
         if (!*abort && !mbar_wait_bounded(&c.base_done[bs], uint32_t(tl / kTiles) & 1u, g.err)) *abort = 1;
         if (*abort) break;
-        const uint8_t* src = smem + p.base_at + bs * 2 * kXBytes;
-        tma_store_2d(&y_map, n * 256, int(m0), src);
-        if (int64_t(n) * kN + kHalf < g.N) tma_store_2d(&y_map, n * 256 + 128, int(m0), src + kXBytes);
+        tma_store_2d(&y_map, n * 128, int(m0), smem + p.base_at + bs * kXBytes);
         bulk_commit();
         bulk_wait_read();
-        mbar_arrive(&c.base_empty[bs]);
+        if (n + kTiles * CL < tiles) fetch(n + kTiles * CL, bs), ++asked;
       }
+      // the CTA must not finish while a load still writes its shared memory
+      for (int i = max(0, asked - kTiles); i < asked; ++i)
+        mbar_wait_bounded(&c.base_full[i % kTiles], uint32_t(i / kTiles) & 1u, nullptr);
       bulk_wait();
     }
   }
@@ -526,7 +503,7 @@ template <int CL, bool YB, bool TMA>
 cudaError_t launch_tiles(const Maps& maps, const Args& g, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
-  constexpr int kTerms = YB ? 2 : 3, kN = YB ? 128 : 64;
+  constexpr int kTerms = YB ? 2 : 3, kN = YB ? 64 : 32;
   const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(control_at(128, kTerms, kN) + 1024));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -573,7 +550,7 @@ cudaError_t launch_lora_tile(const void* x, const int32_t* adapter, const uint16
       !encode_tmap_2d_u8(&maps.x, x, uint64_t(K) * 2, uint64_t(M), uint64_t(K) * 2, 128, kTile, true) ||
       !encode_tmap_2d_u8(&maps.a, a, uint64_t(K) * 2, uint64_t(adapters * rank), uint64_t(K) * 2, 128,
                          uint32_t(rank + 15) / 16 * 16, true) ||
-      !encode_tmap_2d_u8(&maps.b, b, uint64_t(rank) * 2, uint64_t(adapters * N), uint64_t(rank) * 2, 128, yb ? 128 : 64,
+      !encode_tmap_2d_u8(&maps.b, b, uint64_t(rank) * 2, uint64_t(adapters * N), uint64_t(rank) * 2, 128, yb ? 64 : 32,
                          true))
     return cudaErrorNotSupported;
   const bool tma = row % 16 == 0 && ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(y)) & 15) == 0 &&
@@ -581,10 +558,10 @@ cudaError_t launch_lora_tile(const void* x, const int32_t* adapter, const uint16
                    encode_tmap_2d_u8(&maps.y, y, row, uint64_t(M), row, 128, kTile, true);
   if (!tma) maps.base = maps.y = maps.x;  // not used
   const Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank};
-  // CTAs of a tile of tokens: as many as keep one per SM
-  const int64_t tiles = (M + kTile - 1) / kTile;
+  // CTAs of a tile of tokens: as many as are resident at once
+  const int64_t tiles = (M + kTile - 1) / kTile, resident = int64_t(rank <= 64 ? 2 : 1) * sm_count();
   int cl = 1;
-  while (cl < 8 && tiles * cl * 2 <= sm_count()) cl *= 2;
+  while (cl < 8 && tiles * cl * 2 <= resident) cl *= 2;
   if (yb) return tma ? launch_tiles<true, true>(cl, maps, g, s) : launch_tiles<true, false>(cl, maps, g, s);
   return tma ? launch_tiles<false, true>(cl, maps, g, s) : launch_tiles<false, false>(cl, maps, g, s);
 }

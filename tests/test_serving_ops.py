@@ -340,6 +340,64 @@ def test_lora_a_bad_row_stays_in_its_row(B):
     assert torch.equal(got[rest], want[rest]) and bool(torch.isnan(got[3]).all())
 
 
+def tile_case(lengths, N, K, rank, yb, seed):
+    """Enough work for the tensor-core kernel (3e8 multiply-adds): runs of one adapter, some of none."""
+    index = np.repeat([[0, 2, -1, 1, 0, 3, -1][i % 7] for i in range(len(lengths))], lengths)
+    assert len(index) * rank * (N + K) > 3e8
+    return lora_inputs(len(index), N, K, rank, 4, True, yb, seed, index)
+
+
+def check_lora_rows(y, v, yb, rows):
+    x, index, a, b, scale, base = v
+    check_lora(y[torch.from_numpy(rows).cuda()], (x[rows], index[rows], a, b, scale, base[rows]), yb)
+
+
+@gpu
+@pytest.mark.parametrize("yb", [True, False])
+@pytest.mark.parametrize("N,K,rank,lengths", [
+    (1537, 4096, 64, [1, 127, 128, 129, 5, 250, 384]), (2048, 4096, 64, [1, 127, 128, 129, 5, 250, 260]),
+    (3000, 2056, 128, [64, 17, 200, 16, 15, 1, 190]), (2051, 4096, 24, [511, 1, 1, 1, 2, 30, 1600]),
+    (2600, 5000, 8, [1000, 24, 4000]), (9000, 264, 96, [260, 140]), (2049, 2048, 72, [300, 300, 500]),
+    (2560, 4096, 32, [200] + [1] * 140 + [300, 800]), (5000, 1000, 40, [8] * 160), (4104, 2048, 16, [3200])])
+def test_lora_tiles(B, N, K, rank, lengths, yb):
+    """Tiles of one run, of several, of none, and tiles of many runs (the other kernel's) in one call."""
+    v = tile_case(lengths, N, K, rank, yb, 7)
+    M = len(v[1])
+    edges = np.cumsum([0] + lengths)
+    rows = np.unique(np.clip(np.concatenate([edges[:30], edges[:30] - 1, [0, 127, 128, 255, 256, M - 1],
+                                             rng(M).integers(0, M, 20)]), 0, M - 1))
+    y = run_lora(B, v, True, yb)
+    check_lora_rows(y, v, yb, rows)
+    # every row, against the library's kernel for scattered tokens (one token a call cannot reach the tiles)
+    bf = torch.bfloat16
+    x, index, a, b, scale, base = [dev(t, d) for t, d in zip(v, (bf, None, bf, bf, None, bf if yb else None))]
+    part = torch.cat([B.bl_lora_add(x[i:i + 32], index[i:i + 32], a, b, scale, base[i:i + 32]) for i in range(0, M, 32)])
+    far = (y.float() - part.float()).abs()
+    step = 2.0 ** -8 if yb else 2.0 ** -16  # one rounding of the output each; fp32: sums in another order
+    assert bool((far <= 2 * step * part.float().abs() + 2.0 ** -12).all())
+    same = run_lora(B, v, True, yb)
+    assert torch.equal(y, same)
+
+
+@gpu
+def test_lora_tiles_in_place_out_of_range_and_bad_rows(B):
+    v = tile_case([300, 200, 400, 300], 2048, 3000, 64, True, 8)
+    x, index, a, b, scale, base = v
+    bf = torch.bfloat16
+    want = run_lora(B, v, True, True)
+    y = dev(base, bf)
+    assert torch.equal(B.bl_lora_add(dev(x, bf), dev(index), dev(a, bf), dev(b, bf), dev(scale), y, y=y), want)
+    x[5, 3], x[450, 7], x[1100, 9] = np.nan, np.inf, -np.inf  # 300..499 have adapter 2, 500..899 none
+    x[600, 0] = np.nan
+    index[1150] = 4
+    got = run_lora(B, v, True, True)
+    torch.cuda.synchronize()
+    assert B.device_error(clear=True) == B.BL_DEVERR_RANGE
+    rest = [m for m in range(1200) if m not in (5, 450, 1100, 1150)]
+    assert torch.equal(got[rest], want[rest]) and np.array_equal(host(got)[1150], base[1150])
+    assert bool(torch.isnan(got[5]).all())
+
+
 # ---------------------------------------------------------------------------
 # sampling: tokens exactly, unless a decision lies within 2^-28 of going the
 # other way (weights are within 2^-30): then the token's interval has to reach
