@@ -11,13 +11,14 @@
 //      memory as fp32.  The CTAs add their parts up in rank order through
 //      distributed shared memory, so the sum over K is never rounded below
 //      fp32.
-//   2. The sums, times the adapter's scale, become bf16 operands: two terms
-//      (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8, three
-//      (24 bits) for fp32 outputs.
-//   3. Up: each CTA takes tiles of 128 bytes of outputs (64 bf16, 32 fp32).
+//   2. The sums, times the adapter's scale, become bf16 operands in TMEM: two
+//      terms (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8,
+//      three (24 bits) for fp32 outputs.  (From shared memory the operand would
+//      be read again by every MMA: 143 clocks per 128 x 64 x 16 instead of KK.)
+//   3. Up: each CTA takes tiles of 256 bytes of outputs (128 bf16, 64 fp32).
 //      B's rows come by TMA as they lie in memory, and so does the tile of
-//      base, 128-byte swizzled, two tiles ahead.  Every run of the 128 tokens
-//      has its own product in one of four TMEM buffers; the thread of a row adds
+//      base, 128-byte swizzled, three tiles ahead.  Every run of the 128 tokens
+//      has its own product in one of two TMEM buffers; the thread of a row adds
 //      its run's to the base in place, and the tile goes out by TMA, rows
 //      without an adapter unchanged.  Rows of y that are not 16-byte aligned
 //      (N * element size not a multiple of 16) are read and written by the
@@ -33,13 +34,15 @@
 namespace bl {
 namespace {
 
-constexpr int kWarps = 11, kThreads = 32 * kWarps;  // x, A and B; MMA; 8 epilogue warps; base and y
-constexpr int kEpilogueWarps = 8;
-constexpr int kStages = 3;                 // most K blocks of 64 in flight
-constexpr int kTiles = 3;                  // tiles of base in flight
-constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; a tile of base
-constexpr int kAcc = 4, kAccCols = 64;     // accumulators of up to 64 columns (one of the down phase: 128)
-constexpr uint32_t kTmemCols = kAcc * kAccCols;
+constexpr int kEpilogueWarps = 16;         // four per quarter of the TMEM lanes
+constexpr int kWarps = 3 + kEpilogueWarps, kThreads = 32 * kWarps;  // x, A and B; MMA; epilogue; base and y
+constexpr int kStages = 3;                 // K blocks of 64 in flight
+constexpr int kUp = 3;                     // tiles of B in flight
+constexpr int kTiles = 4;                  // tiles of base in flight
+constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; half a tile of base
+constexpr int kAcc = 2, kAccCols = 128;    // accumulators
+constexpr uint32_t kOperand = 256;         // TMEM column of the operand's first term, three of 64 at most
+constexpr uint32_t kTmemCols = 512;
 constexpr int kTurn = 33;                  // floats of a row of 32 outputs being turned
 
 __host__ __device__ constexpr uint32_t idesc(int n) {  // bf16 x bf16 -> fp32, M = 128
@@ -47,24 +50,20 @@ __host__ __device__ constexpr uint32_t idesc(int n) {  // bf16 x bf16 -> fp32, M
 }
 
 // Shared memory.  First [ring of x and A | partial sums]; then, over both,
-// [operand terms | ring of B | ring of base, or turning buffers].  The operand
-// lies within the ring, clear of the partial sums that it is made from.  At
-// ranks up to 64 two CTAs fit on an SM: one moves x while the other moves y.
+// [ring of B | ring of base, or turning buffers].
 struct Plan {
   int rp, rk;             // rank rounded up to 16 (MMA N and K) and to 64 (operand sub-tiles)
   uint32_t a_bytes, a_at; // of a run's A block in a ring stage; from one to the next
   int group;              // runs whose A goes through the ring together
   uint32_t stage;         // of a ring stage
-  int stages;             // of the ring: two where two runs' A blocks would keep a second CTA off the SM
-  uint32_t term;          // of one operand term, [128][rk] in 64-column sub-tiles
+  int term;               // TMEM columns of one operand term
   uint32_t part_at;       // byte offset of the partial sums
   uint32_t part_row;      // floats of a row of them
   uint32_t up_at, up_stage;  // ring of B tiles
-  int up_n;               // tiles of it
   uint32_t base_at;       // ring of base tiles
   uint32_t end;
 };
-__host__ __device__ inline Plan make_plan(int rank, int terms, int n_tile, int runs) {
+__host__ __device__ inline Plan make_plan(int rank, int n_tile, int runs) {
   Plan p;
   p.rp = (rank + 15) / 16 * 16;
   p.rk = (rank + 63) / 64 * 64;
@@ -72,26 +71,35 @@ __host__ __device__ inline Plan make_plan(int rank, int terms, int n_tile, int r
   p.a_at = (p.a_bytes + 1023) / 1024 * 1024;
   p.group = p.rp <= 64 && runs > 1 ? 2 : 1;
   p.stage = kXBytes + uint32_t(p.group) * p.a_at;
-  p.term = uint32_t(p.rk) / 64 * kTile * 128;
-  p.stages = p.group == 2 && p.rp > 32 ? 2 : kStages;
-  const uint32_t ring = p.stages * p.stage, operand = p.term * terms;
-  p.up_at = operand;
+  p.term = p.rk / 2;
+  p.up_at = 0;
   p.up_stage = uint32_t(p.rk) / 64 * n_tile * 128;
-  p.up_n = p.rk == 64 ? 3 : 2;
-  const uint32_t up_end = p.up_at + p.up_n * p.up_stage;
-  p.part_at = ring > operand ? ring : operand;
+  const uint32_t up_end = p.up_at + kUp * p.up_stage;
+  p.part_at = kStages * p.stage;
   p.part_row = uint32_t(p.rp) + 4;
   p.base_at = up_end;
-  const uint32_t one = p.part_at + kTile * p.part_row * 4, two = p.base_at + kTiles * kXBytes;
+  const uint32_t one = p.part_at + kTile * p.part_row * 4, two = p.base_at + kTiles * 2 * kXBytes;
   p.end = ((one > two ? one : two) + 1023) / 1024 * 1024;
   return p;
 }
 
 // The control block lies behind either layout.
-__host__ __device__ inline uint32_t control_at(int rank, int terms, int n_tile) {
-  const uint32_t one = make_plan(rank, terms, n_tile, 1).end, two = make_plan(rank, terms, n_tile, 2).end;
+__host__ __device__ inline uint32_t control_at(int rank, int n_tile) {
+  const uint32_t one = make_plan(rank, n_tile, 1).end, two = make_plan(rank, n_tile, 2).end;
   return one > two ? one : two;
 }
+
+// A place in a ring of `n`, and how often it has gone round (a division by a
+// number known at run time costs a few hundred clocks in a one-lane loop).
+struct Ring {
+  int n, at, round;
+  __device__ __forceinline__ explicit Ring(int size) : n(size), at(0), round(0) {}
+  __device__ __forceinline__ void next() {
+    if (++at == n) at = 0, ++round;
+  }
+  __device__ __forceinline__ uint32_t parity() const { return uint32_t(round) & 1u; }           // of a wait for data
+  __device__ __forceinline__ uint32_t free_parity() const { return uint32_t(round - 1) & 1u; }  // of a wait for room
+};
 
 struct Args {
   const int32_t* adapter;
@@ -104,7 +112,7 @@ struct Args {
 };
 
 struct Control {  // at control_at()
-  uint64_t full[kStages], empty[kStages], sums, drained, up_full[kAcc], up_empty[kAcc], out_full[kAcc], out_empty[kAcc];
+  uint64_t full[kStages], empty[kStages], sums, drained, up_full[kUp], up_empty[kUp], out_full[kAcc], out_empty[kAcc];
   uint64_t base_full[kTiles], base_done[kTiles];
   uint32_t tmem, starts[4], used[4];  // used: runs that have an adapter
   int abort;
@@ -151,15 +159,16 @@ __device__ __forceinline__ bool warp_agrees(bool c) { return __all_sync(0xffffff
 
 // YB: base and y are bf16.  TMA: they come and go by TMA.
 template <int CL, bool YB, bool TMA>
-__global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_constant__ CUtensorMap xmap,
+__global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_constant__ CUtensorMap xmap,
                                                              const __grid_constant__ CUtensorMap amap,
                                                              const __grid_constant__ CUtensorMap bmap,
                                                              const __grid_constant__ CUtensorMap base_map,
                                                              const __grid_constant__ CUtensorMap y_map, const Args g) {
   constexpr int kTerms = YB ? 2 : 3;
-  constexpr int kN = YB ? 64 : 32;  // outputs of an up tile
+  constexpr int kN = YB ? 128 : 64;  // outputs of an up tile
+  constexpr int kHalf = kN / 2;      // 128 bytes of them
   extern __shared__ __align__(1024) uint8_t smem[];
-  Control& c = *reinterpret_cast<Control*>(smem + control_at(g.rank, kTerms, kN));
+  Control& c = *reinterpret_cast<Control*>(smem + control_at(g.rank, kN));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t me = CL == 1 ? 0 : cluster_ctarank();
   const int64_t m0 = int64_t(blockIdx.x / CL) * kTile;
@@ -176,9 +185,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
     for (int i = 0; i < kStages; ++i) mbar_init(&c.full[i], 1), mbar_init(&c.empty[i], 1);
     mbar_init(&c.sums, 1);
     mbar_init(&c.drained, kEpilogueWarps);
+    for (int i = 0; i < kUp; ++i) mbar_init(&c.up_full[i], 1), mbar_init(&c.up_empty[i], 1);
     for (int i = 0; i < kAcc; ++i) {
-      mbar_init(&c.up_full[i], 1);
-      mbar_init(&c.up_empty[i], 1);
       mbar_init(&c.out_full[i], 1);
       mbar_init(&c.out_empty[i], kEpilogueWarps);
     }
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
   const int starts = __popc(c.starts[0]) + __popc(c.starts[1]) + __popc(c.starts[2]) + __popc(c.starts[3]);
   const bool mine = starts <= kTileRuns, one = starts == 1;
 
-  const Plan p = make_plan(g.rank, kTerms, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]));
+  const Plan p = make_plan(g.rank, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]));
 
   // All threads of the cluster; the barrier wants converged warps.
   auto sync_all = [] {
@@ -225,13 +233,12 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
     // ---- 1. down ----
     // Runs with an adapter, in groups whose A blocks go through the ring beside one block of x.
     if (warp == 0 && lane == 0) {
-      int it = 0;
+      Ring at(kStages);
       Runs r(c.starts, size, one);
       for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0 && !*abort;) {
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const int st = it % p.stages;
-          if (it >= p.stages && !*abort && !mbar_wait_bounded(&c.empty[st], uint32_t(it / p.stages - 1) & 1u, g.err))
-            *abort = 1;
+        for (int kb = k0; kb < k1; ++kb, at.next()) {
+          const int st = at.at;
+          if (at.round > 0 && !*abort && !mbar_wait_bounded(&c.empty[st], at.free_parity(), g.err)) *abort = 1;
           if (*abort) break;
           uint8_t* dst = smem + st * p.stage;
           mbar_arrive_expect_tx(&c.full[st], kXBytes + n * p.a_bytes);
@@ -241,18 +248,20 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
         }
       }
       // nothing may still be on its way into the ring when it is used for the operand
-      for (int i = max(0, it - p.stages); i < it; ++i)
-        mbar_wait_bounded(&c.full[i % p.stages], uint32_t(i / p.stages) & 1u, nullptr);
+      for (int st = 0; st < kStages; ++st)  // the last use of each place
+        if (at.round > 0 || st < at.at)
+          mbar_wait_bounded(&c.full[st], uint32_t(st < at.at ? at.round : at.round - 1) & 1u, nullptr);
     } else if (warp == 1 && lane == 0) {
-      int it = 0, turn = 0;
+      Ring at(kStages);
+      int turn = 0;
       const uint32_t sbase = smem_addr(smem);
       Runs r(c.starts, size, one);
       for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0; ++turn) {
         if (turn > 0 && !*abort && !mbar_wait_bounded(&c.drained, uint32_t(turn - 1) & 1u, g.err)) *abort = 1;
         tc_fence_after();
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const int st = it % p.stages;
-          if (!*abort && !mbar_wait_bounded(&c.full[st], uint32_t(it / p.stages) & 1u, g.err)) *abort = 1;
+        for (int kb = k0; kb < k1; ++kb, at.next()) {
+          const int st = at.at;
+          if (!*abort && !mbar_wait_bounded(&c.full[st], at.parity(), g.err)) *abort = 1;
           tc_fence_after();
           const uint32_t xa = sbase + st * p.stage;
           if (!*abort)
@@ -267,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
       }
     } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
       float* part = reinterpret_cast<float*>(smem + p.part_at);
-      const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane;
+      const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
       int turn = 0;
       Runs r(c.starts, size, one);
       for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0; ++turn) {
@@ -277,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
         for (int j = 0; j < n; ++j) {
           const int from = group[j], to = r.end_of(from);
           if (!ok || max(from, quarter * 32) >= min(to, quarter * 32 + 32)) continue;
-          for (int col = half * 16; col < p.rp; col += 32) {
+          for (int col = part4 * 16; col < p.rp; col += 64) {
             uint32_t v[16];
             __syncwarp();
             tmem_ld16(tmem + j * kAccCols + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
@@ -299,50 +308,59 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
     sync_all();
     tc_fence_after();
 
-    // ---- 2. the operand: eight columns of a row at a time ----
-    for (int i = threadIdx.x; i < kTile * (p.rp / 8); i += kThreads) {
-      const int row = i / (p.rp / 8), chunk = i % (p.rp / 8);
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    // ---- 2. the operand: a thread 32 columns of a row at a time ----
+    if (warp >= 2 && warp < 2 + kEpilogueWarps) {
+      const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
       const int a = c.adapter[row];
-      if (a >= 0 && chunk * 8 < g.rank) {
-        const float* src = reinterpret_cast<const float*>(smem + p.part_at) + row * p.part_row + chunk * 8;
+      const float scale = a >= 0 ? g.scale[a] : 0.f;
+      for (int k = part4 * 32; k < p.rk; k += 128) {
+        float v[32];
 #pragma unroll
-        for (int q = 0; q < CL; ++q) {
-          const float4* f = reinterpret_cast<const float4*>(CL == 1 ? src : peer(src, q));
-          const float4 f0 = f[0], f1 = f[1];
-          v[0] += f0.x, v[1] += f0.y, v[2] += f0.z, v[3] += f0.w;
-          v[4] += f1.x, v[5] += f1.y, v[6] += f1.z, v[7] += f1.w;
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        if (a >= 0) {
+          const float* src = reinterpret_cast<const float*>(smem + p.part_at) + row * p.part_row + k;
+#pragma unroll
+          for (int q = 0; q < CL; ++q) {
+            const float4* f = reinterpret_cast<const float4*>(CL == 1 ? src : peer(src, q));
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (k + 4 * j < g.rank) {
+                const float4 f4 = f[j];
+                v[4 * j] += f4.x, v[4 * j + 1] += f4.y, v[4 * j + 2] += f4.z, v[4 * j + 3] += f4.w;
+              }
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= scale;
         }
-        const float s = g.scale[a];
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= s;
-      }
-      uint8_t* dst = smem + (chunk / 8) * (kTile * 128) + row * 128 + ((uint32_t(chunk & 7) ^ uint32_t(row & 7)) << 4);
+        for (int t = 0; t < kTerms; ++t) {  // the nearest bf16, and the same of what it leaves
+          uint32_t w[16];
 #pragma unroll
-      for (int t = 0; t < kTerms; ++t) {  // the nearest bf16, and the same of what it leaves
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = f32_to_bf16_bits_rn(v[2 * j]), hi = f32_to_bf16_bits_rn(v[2 * j + 1]);
-          v[2 * j] -= bf16_bits_to_f32(uint16_t(lo));
-          v[2 * j + 1] -= bf16_bits_to_f32(uint16_t(hi));
-          w[j] = lo | hi << 16;
+          for (int j = 0; j < 16; ++j) {
+            w[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
+            v[2 * j] -= __uint_as_float(w[j] << 16);
+            v[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
+          }
+          tmem_st16(tmem + kOperand + uint32_t(t * p.term + k / 2) + (uint32_t(quarter * 32) << 16), w);
         }
-        *reinterpret_cast<uint4*>(dst + t * p.term) = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      tmem_st_wait();
     }
-    fence_async_smem();
+    tc_fence_before();
+    fence_async_smem();  // the rings come over the partial sums
     sync_all();  // and nobody reads the partial sums any more
+    tc_fence_after();
 
     // ---- 3. up ----
     if (warp == 0 && lane == 0) {
-      int it = 0;
+      Ring at(kUp);
       for (int n = int(me); n < tiles && !*abort; n += CL) {
         for (Runs r(c.starts, size, one); r.next();) {
           const int a = c.adapter[r.t];
           if (a < 0) continue;
-          const int st = it % p.up_n;
-          if (it >= p.up_n && !mbar_wait_bounded(&c.up_empty[st], uint32_t(it / p.up_n - 1) & 1u, g.err)) {
+          const int st = at.at;
+          if (at.round > 0 && !mbar_wait_bounded(&c.up_empty[st], at.free_parity(), g.err)) {
             *abort = 1;
             break;
           }
@@ -350,46 +368,46 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
           mbar_arrive_expect_tx(&c.up_full[st], p.up_stage);
           for (int sub = 0; sub < p.rk / 64; ++sub)
             tma_load_2d(dst + sub * (kN * 128), &bmap, sub * 128, int(int64_t(a) * g.N + n * kN), &c.up_full[st]);
-          ++it;
+          at.next();
         }
       }
       // the CTA must not finish while a load still writes its shared memory
-      for (int i = max(0, it - p.up_n); i < it; ++i)
-        mbar_wait_bounded(&c.up_full[i % p.up_n], uint32_t(i / p.up_n) & 1u, nullptr);
+      for (int st = 0; st < kUp; ++st)
+        if (at.round > 0 || st < at.at)
+          mbar_wait_bounded(&c.up_full[st], uint32_t(st < at.at ? at.round : at.round - 1) & 1u, nullptr);
     } else if (warp == 1 && lane == 0) {
       int it = 0;
+      Ring at(kUp);
       const uint32_t sbase = smem_addr(smem);
       for (int n = int(me); n < tiles; n += CL)
         for (Runs r(c.starts, size, one); r.next();) {
           if (c.adapter[r.t] < 0) continue;
-          const int st = it % p.up_n, acc = it % kAcc;
-          if (!*abort && !mbar_wait_bounded(&c.up_full[st], uint32_t(it / p.up_n) & 1u, g.err)) *abort = 1;
+          const int st = at.at, acc = it % kAcc;
+          if (!*abort && !mbar_wait_bounded(&c.up_full[st], at.parity(), g.err)) *abort = 1;
           if (it >= kAcc && !*abort && !mbar_wait_bounded(&c.out_empty[acc], uint32_t(it / kAcc - 1) & 1u, g.err)) *abort = 1;
           tc_fence_after();
-          // 64 columns at a time; a step of 16 columns is 32 bytes, 2 in a descriptor's address field
+          // 16 columns of the operand and of B's rows at a time (8 TMEM columns, 32 bytes)
+          const uint32_t ba = sbase + p.up_at + st * p.up_stage;
           if (!*abort)
             for (int t = 0; t < kTerms; ++t)
-              for (int sub = 0; sub < p.rk / 64; ++sub) {
-                uint64_t ad = umma_desc_sw128(sbase + t * p.term + sub * (kTile * 128));
-                uint64_t bd = umma_desc_sw128(sbase + p.up_at + st * p.up_stage + sub * (kN * 128));
-                const int steps = min(4, p.rp / 16 - 4 * sub);
-                for (int ks = 0; ks < steps; ++ks, ad += 2, bd += 2)
-                  umma_f16(tmem + acc * kAccCols, ad, bd, idesc(kN), t > 0 || sub > 0 || ks > 0);
-              }
+              for (int ks = 0; ks < p.rp / 16; ++ks)
+                umma_f16_ta(tmem + acc * kAccCols, tmem + kOperand + uint32_t(t * p.term + 8 * ks),
+                            umma_desc_sw128(ba + uint32_t(ks >> 2) * (kN * 128) + (ks & 3) * 32), idesc(kN), t > 0 || ks > 0);
           umma_commit(&c.up_empty[st]);
           umma_commit(&c.out_full[acc]);
           ++it;
+          at.next();
         }
     } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
-      constexpr int kCols = kN / 2;  // outputs of a warp: 64 bytes of a row
-      const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane;
+      constexpr int kCols = kN / 4;  // outputs of a warp: 64 bytes of a row
+      const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
       float* turn = reinterpret_cast<float*>(smem + p.base_at) + (warp - 2) * 32 * kTurn;
       int it = 0, tl = 0;
       for (int n = int(me); n < tiles; n += CL, ++tl) {
-        const int bs = tl % kTiles, n0 = n * kN + half * kCols;
+        const int bs = tl % kTiles, n0 = n * kN + part4 * kCols;
         // this thread's 64 bytes of base: 16-byte unit u of a 128-byte row at u ^ (row % 8)
-        uint8_t* mine_row = smem + p.base_at + bs * kXBytes + row * 128;
-        auto unit = [&](int u) { return reinterpret_cast<uint4*>(mine_row + ((half * 4 + u) ^ (row & 7)) * 16); };
+        uint8_t* mine_row = smem + p.base_at + (bs * 2 + (part4 >> 1)) * kXBytes + row * 128;
+        auto unit = [&](int u) { return reinterpret_cast<uint4*>(mine_row + (((part4 & 1) * 4 + u) ^ (row & 7)) * 16); };
         if (TMA && !*abort && !mbar_wait_bounded(&c.base_full[bs], uint32_t(tl / kTiles) & 1u, g.err)) *abort = 1;
         for (Runs r(c.starts, size, one); r.next();) {
           const bool has = c.adapter[r.t] >= 0;
@@ -408,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
           tc_fence_after();
           const bool ok = warp_agrees(!*abort);  // and the warp is converged for tcgen05.ld
           if (ra < rb && ok && n0 < g.N) {
-            const uint32_t at = tmem + acc * kAccCols + (uint32_t(quarter * 32) << 16) + uint32_t(half * kCols);
+            const uint32_t at = tmem + acc * kAccCols + (uint32_t(quarter * 32) << 16) + uint32_t(part4 * kCols);
             uint32_t d[kCols];
             __syncwarp();
 #pragma unroll
@@ -465,8 +483,11 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
       }
     } else if (TMA && warp == 2 + kEpilogueWarps && lane == 0) {
       auto fetch = [&](int n, int bs) {
-        mbar_arrive_expect_tx(&c.base_full[bs], kXBytes);
-        tma_load_2d(smem + p.base_at + bs * kXBytes, &base_map, n * 128, int(m0), &c.base_full[bs]);
+        const bool two = int64_t(n) * kN + kHalf < g.N;
+        uint8_t* dst = smem + p.base_at + bs * 2 * kXBytes;
+        mbar_arrive_expect_tx(&c.base_full[bs], two ? 2 * kXBytes : kXBytes);
+        tma_load_2d(dst, &base_map, n * 256, int(m0), &c.base_full[bs]);
+        if (two) tma_load_2d(dst + kXBytes, &base_map, n * 256 + 128, int(m0), &c.base_full[bs]);
       };
       int tl = 0, asked = 0;  // tiles stored, tiles asked for
       for (; asked < kTiles && int(me) + asked * CL < tiles; ++asked) fetch(int(me) + asked * CL, asked);
@@ -474,7 +495,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_tile_kernel(const __grid_con
         const int bs = tl % kTiles;
         if (!*abort && !mbar_wait_bounded(&c.base_done[bs], uint32_t(tl / kTiles) & 1u, g.err)) *abort = 1;
         if (*abort) break;
-        tma_store_2d(&y_map, n * 128, int(m0), smem + p.base_at + bs * kXBytes);
+        const uint8_t* src = smem + p.base_at + bs * 2 * kXBytes;
+        tma_store_2d(&y_map, n * 256, int(m0), src);
+        if (int64_t(n) * kN + kHalf < g.N) tma_store_2d(&y_map, n * 256 + 128, int(m0), src + kXBytes);
         bulk_commit();
         bulk_wait_read();
         if (n + kTiles * CL < tiles) fetch(n + kTiles * CL, bs), ++asked;
@@ -503,13 +526,13 @@ template <int CL, bool YB, bool TMA>
 cudaError_t launch_tiles(const Maps& maps, const Args& g, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
-  constexpr int kTerms = YB ? 2 : 3, kN = YB ? 64 : 32;
-  const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(control_at(128, kTerms, kN) + 1024));
+  constexpr int kN = YB ? 128 : 64;
+  const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(control_at(128, kN) + 1024));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((g.M + kTile - 1) / kTile * CL));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = control_at(g.rank, kTerms, kN) + 1024;
+  cfg.dynamicSmemBytes = control_at(g.rank, kN) + 1024;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;
@@ -550,7 +573,7 @@ cudaError_t launch_lora_tile(const void* x, const int32_t* adapter, const uint16
       !encode_tmap_2d_u8(&maps.x, x, uint64_t(K) * 2, uint64_t(M), uint64_t(K) * 2, 128, kTile, true) ||
       !encode_tmap_2d_u8(&maps.a, a, uint64_t(K) * 2, uint64_t(adapters * rank), uint64_t(K) * 2, 128,
                          uint32_t(rank + 15) / 16 * 16, true) ||
-      !encode_tmap_2d_u8(&maps.b, b, uint64_t(rank) * 2, uint64_t(adapters * N), uint64_t(rank) * 2, 128, yb ? 64 : 32,
+      !encode_tmap_2d_u8(&maps.b, b, uint64_t(rank) * 2, uint64_t(adapters * N), uint64_t(rank) * 2, 128, yb ? 128 : 64,
                          true))
     return cudaErrorNotSupported;
   const bool tma = row % 16 == 0 && ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(y)) & 15) == 0 &&
@@ -558,10 +581,10 @@ cudaError_t launch_lora_tile(const void* x, const int32_t* adapter, const uint16
                    encode_tmap_2d_u8(&maps.y, y, row, uint64_t(M), row, 128, kTile, true);
   if (!tma) maps.base = maps.y = maps.x;  // not used
   const Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank};
-  // CTAs of a tile of tokens: as many as are resident at once
-  const int64_t tiles = (M + kTile - 1) / kTile, resident = int64_t(rank <= 64 ? 2 : 1) * sm_count();
+  // CTAs of a tile of tokens: as many as keep one per SM
+  const int64_t tiles = (M + kTile - 1) / kTile;
   int cl = 1;
-  while (cl < 8 && tiles * cl * 2 <= resident) cl *= 2;
+  while (cl < 8 && tiles * cl * 2 <= sm_count()) cl *= 2;
   if (yb) return tma ? launch_tiles<true, true>(cl, maps, g, s) : launch_tiles<true, false>(cl, maps, g, s);
   return tma ? launch_tiles<false, true>(cl, maps, g, s) : launch_tiles<false, false>(cl, maps, g, s);
 }
