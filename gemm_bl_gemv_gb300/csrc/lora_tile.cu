@@ -120,33 +120,48 @@ struct Control {  // at control_at()
 };
 static_assert(sizeof(Control) <= 1024, "");
 
-// The next run of the tile from token `t`: [t, end) and its adapter.
-struct Runs {
-  const uint32_t* starts;
-  int t, end, size;
-  bool one;  // the tile is one run
-  __device__ __forceinline__ Runs(const uint32_t* s, int n, bool single)
-      : starts(s), t(0), end(0), size(n), one(single) {}
-  // The end of the run that starts at token s.
-  __device__ __forceinline__ int end_of(int s) const {
-    for (int w = (s + 1) / 32; w < 4; ++w) {
-      uint32_t b = starts[w];
-      if (w == (s + 1) / 32) b &= 0xFFFFFFFFu << ((s + 1) & 31);
-      if (b) return min(size, w * 32 + __ffs(b) - 1);
-    }
-    return size;
+// The runs of a tile, at most kTileRuns, in registers: eight bits for each
+// end, a bit for each that has an adapter.
+struct RunTable {
+  uint64_t ends;
+  uint32_t has;
+  int n;
+  __device__ __forceinline__ RunTable(const uint32_t* starts, const int* adapter, int size) : ends(0), has(0), n(0) {
+    for (int w = 0; w < kTile / 32; ++w)
+      for (uint32_t bits = starts[w]; bits && n < kTileRuns; bits &= bits - 1) {
+        const int t = w * 32 + __ffs(bits) - 1;
+        if (n > 0) ends |= uint64_t(t) << (8 * (n - 1));
+        has |= uint32_t(adapter[t] >= 0) << n;
+        ++n;
+      }
+    ends |= uint64_t(size) << (8 * (n - 1));
   }
+};
+
+// A walk over them: tokens [t, end).
+struct Runs {
+  const RunTable& table;
+  int i, t, end;
+  __device__ __forceinline__ explicit Runs(const RunTable& r) : table(r), i(0), t(0), end(0) {}
   __device__ __forceinline__ bool next() {
+    if (i == table.n) return false;
     t = end;
-    if (t >= size) return false;
-    end = one ? size : end_of(t);
+    end = int(table.ends >> (8 * i)) & 255;
+    ++i;
     return true;
   }
-  // The starts of the next `most` runs with an adapter.
-  __device__ __forceinline__ int group(const int* adapter, int most, int* from) {
+  __device__ __forceinline__ bool has() const { return (table.has >> (i - 1)) & 1u; }
+  // The next `most` (one or two) runs with an adapter: their tokens [t[j], end[j]).
+  __device__ __forceinline__ int group(int most, int (&from)[2], int (&to)[2]) {
     int n = 0;
     while (n < most && next())
-      if (adapter[t] >= 0) from[n++] = t;
+      if (has()) {
+        if (n == 0)
+          from[0] = t, to[0] = end;
+        else
+          from[1] = t, to[1] = end;
+        ++n;
+      }
     return n;
   }
 };
@@ -213,7 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = c.tmem;
   const int starts = __popc(c.starts[0]) + __popc(c.starts[1]) + __popc(c.starts[2]) + __popc(c.starts[3]);
-  const bool mine = starts <= kTileRuns, one = starts == 1;
+  const bool mine = starts <= kTileRuns;
+  const RunTable table(c.starts, c.adapter, size);
 
   const Plan p = make_plan(g.rank, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]));
 
@@ -234,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     // Runs with an adapter, in groups whose A blocks go through the ring beside one block of x.
     if (warp == 0 && lane == 0) {
       Ring at(kStages);
-      Runs r(c.starts, size, one);
-      for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0 && !*abort;) {
+      Runs r(table);
+      for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0 && !*abort;) {
         for (int kb = k0; kb < k1; ++kb, at.next()) {
           const int st = at.at;
           if (at.round > 0 && !*abort && !mbar_wait_bounded(&c.empty[st], at.free_parity(), g.err)) *abort = 1;
@@ -243,8 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           uint8_t* dst = smem + st * p.stage;
           mbar_arrive_expect_tx(&c.full[st], kXBytes + n * p.a_bytes);
           tma_load_2d(dst, &xmap, kb * 128, int(m0), &c.full[st]);
-          for (int j = 0; j < n; ++j)
-            tma_load_2d(dst + kXBytes + j * p.a_at, &amap, kb * 128, c.adapter[group[j]] * g.rank, &c.full[st]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (j < n) tma_load_2d(dst + kXBytes + j * p.a_at, &amap, kb * 128, c.adapter[from[j]] * g.rank, &c.full[st]);
         }
       }
       // nothing may still be on its way into the ring when it is used for the operand
@@ -255,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       Ring at(kStages);
       int turn = 0;
       const uint32_t sbase = smem_addr(smem);
-      Runs r(c.starts, size, one);
-      for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0; ++turn) {
+      Runs r(table);
+      for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0; ++turn) {
         if (turn > 0 && !*abort && !mbar_wait_bounded(&c.drained, uint32_t(turn - 1) & 1u, g.err)) *abort = 1;
         tc_fence_after();
         for (int kb = k0; kb < k1; ++kb, at.next()) {
@@ -278,20 +295,21 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       float* part = reinterpret_cast<float*>(smem + p.part_at);
       const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
       int turn = 0;
-      Runs r(c.starts, size, one);
-      for (int group[2], n; (n = r.group(c.adapter, p.group, group)) > 0; ++turn) {
+      Runs r(table);
+      for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0; ++turn) {
         if (!*abort && !mbar_wait_bounded(&c.sums, uint32_t(turn) & 1u, g.err)) *abort = 1;
         tc_fence_after();
         const bool ok = warp_agrees(!*abort);  // and the warp is converged for tcgen05.ld
-        for (int j = 0; j < n; ++j) {
-          const int from = group[j], to = r.end_of(from);
-          if (!ok || max(from, quarter * 32) >= min(to, quarter * 32 + 32)) continue;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (j >= n) break;
+          if (!ok || max(from[j], quarter * 32) >= min(to[j], quarter * 32 + 32)) continue;
           for (int col = part4 * 16; col < p.rp; col += 64) {
             uint32_t v[16];
             __syncwarp();
             tmem_ld16(tmem + j * kAccCols + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
             tmem_ld_wait();
-            if (row >= from && row < to) {
+            if (row >= from[j] && row < to[j]) {
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 *reinterpret_cast<uint4*>(part + row * p.part_row + col + 4 * q) =
@@ -356,9 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     if (warp == 0 && lane == 0) {
       Ring at(kUp);
       for (int n = int(me); n < tiles && !*abort; n += CL) {
-        for (Runs r(c.starts, size, one); r.next();) {
+        for (Runs r(table); r.next();) {
+          if (!r.has()) continue;
           const int a = c.adapter[r.t];
-          if (a < 0) continue;
           const int st = at.at;
           if (at.round > 0 && !mbar_wait_bounded(&c.up_empty[st], at.free_parity(), g.err)) {
             *abort = 1;
@@ -380,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       Ring at(kUp);
       const uint32_t sbase = smem_addr(smem);
       for (int n = int(me); n < tiles; n += CL)
-        for (Runs r(c.starts, size, one); r.next();) {
-          if (c.adapter[r.t] < 0) continue;
+        for (Runs r(table); r.next();) {
+          if (!r.has()) continue;
           const int st = at.at, acc = it % kAcc;
           if (!*abort && !mbar_wait_bounded(&c.up_full[st], at.parity(), g.err)) *abort = 1;
           if (it >= kAcc && !*abort && !mbar_wait_bounded(&c.out_empty[acc], uint32_t(it / kAcc - 1) & 1u, g.err)) *abort = 1;
@@ -409,11 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         uint8_t* mine_row = smem + p.base_at + (bs * 2 + (part4 >> 1)) * kXBytes + row * 128;
         auto unit = [&](int u) { return reinterpret_cast<uint4*>(mine_row + (((part4 & 1) * 4 + u) ^ (row & 7)) * 16); };
         if (TMA && !*abort && !mbar_wait_bounded(&c.base_full[bs], uint32_t(tl / kTiles) & 1u, g.err)) *abort = 1;
-        for (Runs r(c.starts, size, one); r.next();) {
-          const bool has = c.adapter[r.t] >= 0;
+        for (Runs r(table); r.next();) {
           // rows of this warp that are in the run
           const int ra = max(r.t, quarter * 32), rb = min(r.end, quarter * 32 + 32);
-          if (!has) {
+          if (!r.has()) {
             if (!TMA && g.y != g.base)
               for (int i = ra + lane / kCols; i < rb; i += 32 / kCols) {
                 const int j = n0 + lane % kCols;
