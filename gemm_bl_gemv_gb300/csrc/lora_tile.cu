@@ -404,13 +404,23 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           if (!*abort && !mbar_wait_bounded(&c.up_full[st], at.parity(), g.err)) *abort = 1;
           if (it >= kAcc && !*abort && !mbar_wait_bounded(&c.out_empty[acc], uint32_t(it / kAcc - 1) & 1u, g.err)) *abort = 1;
           tc_fence_after();
-          // 16 columns of the operand and of B's rows at a time (8 TMEM columns, 32 bytes)
-          const uint32_t ba = sbase + p.up_at + st * p.up_stage;
+          // 16 columns of the operand and of B's rows at a time (8 TMEM columns, 32 bytes), 64 where there
+          // are so many: one descriptor after the other is made while the tensor core works
+          const uint32_t ba = sbase + p.up_at + st * p.up_stage, da = tmem + acc * kAccCols;
           if (!*abort)
             for (int t = 0; t < kTerms; ++t)
-              for (int ks = 0; ks < p.rp / 16; ++ks)
-                umma_f16_ta(tmem + acc * kAccCols, tmem + kOperand + uint32_t(t * p.term + 8 * ks),
-                            umma_desc_sw128(ba + uint32_t(ks >> 2) * (kN * 128) + (ks & 3) * 32), idesc(kN), t > 0 || ks > 0);
+              for (int sub = 0; sub < p.rk / 64; ++sub) {
+                const uint32_t oa = tmem + kOperand + uint32_t(t * p.term + 32 * sub), bs = ba + sub * (kN * 128);
+                const uint32_t more = t > 0 || sub > 0;
+                if (p.rp - 64 * sub >= 64) {
+#pragma unroll
+                  for (int ks = 0; ks < 4; ++ks)
+                    umma_f16_ta(da, oa + 8 * ks, umma_desc_sw128(bs + ks * 32), idesc(kN), ks > 0 ? 1u : more);
+                } else {
+                  for (int ks = 0; ks < p.rp / 16 - 4 * sub; ++ks)
+                    umma_f16_ta(da, oa + 8 * ks, umma_desc_sw128(bs + ks * 32), idesc(kN), ks > 0 ? 1u : more);
+                }
+              }
           umma_commit(&c.up_empty[st]);
           umma_commit(&c.out_full[acc]);
           ++it;
