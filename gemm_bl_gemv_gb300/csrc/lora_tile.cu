@@ -36,8 +36,8 @@ namespace {
 
 constexpr int kEpilogueWarps = 16;         // four per quarter of the TMEM lanes
 constexpr int kWarps = 3 + kEpilogueWarps, kThreads = 32 * kWarps;  // x, A and B; MMA; epilogue; base and y
-constexpr int kStages = 3;                 // K blocks of 64 in flight
-constexpr int kUp = 3;                     // tiles of B in flight
+constexpr int kStages = 5;                 // K blocks of 64 in flight at most
+constexpr int kUp = 6;                     // tiles of B in flight at most
 constexpr int kTiles = 4;                  // tiles of base in flight
 constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; half a tile of base
 constexpr int kAcc = 2, kAccCols = 128;    // accumulators
@@ -55,6 +55,7 @@ struct Plan {
   int rp, rk;             // rank rounded up to 16 (MMA N and K) and to 64 (operand sub-tiles)
   uint32_t a_bytes, a_at; // of a run's A block in a ring stage; from one to the next
   int group;              // runs whose A goes through the ring together
+  int stages, up;         // places of the ring of x and A, and of the ring of B
   uint32_t stage;         // of a ring stage
   int term;               // TMEM columns of one operand term
   uint32_t part_at;       // byte offset of the partial sums
@@ -71,11 +72,13 @@ __host__ __device__ inline Plan make_plan(int rank, int n_tile, int runs) {
   p.a_at = (p.a_bytes + 1023) / 1024 * 1024;
   p.group = p.rp <= 64 && runs > 1 ? 2 : 1;
   p.stage = kXBytes + uint32_t(p.group) * p.a_at;
+  p.stages = p.rp <= 64 ? kStages : kStages - 1;
   p.term = p.rk / 2;
   p.up_at = 0;
   p.up_stage = uint32_t(p.rk) / 64 * n_tile * 128;
-  const uint32_t up_end = p.up_at + kUp * p.up_stage;
-  p.part_at = kStages * p.stage;
+  p.up = p.rk == 64 ? kUp : kUp / 2;
+  const uint32_t up_end = p.up_at + p.up * p.up_stage;
+  p.part_at = p.stages * p.stage;
   p.part_row = uint32_t(p.rp) + 4;
   p.base_at = up_end;
   const uint32_t one = p.part_at + kTile * p.part_row * 4, two = p.base_at + kTiles * 2 * kXBytes;
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     // ---- 1. down ----
     // Runs with an adapter, in groups whose A blocks go through the ring beside one block of x.
     if (warp == 0 && lane == 0) {
-      Ring at(kStages);
+      Ring at(p.stages);
       Runs r(table);
       for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0 && !*abort;) {
         for (int kb = k0; kb < k1; ++kb, at.next()) {
@@ -265,11 +268,11 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         }
       }
       // nothing may still be on its way into the ring when it is used for the operand
-      for (int st = 0; st < kStages; ++st)  // the last use of each place
+      for (int st = 0; st < p.stages; ++st)  // the last use of each place
         if (at.round > 0 || st < at.at)
           mbar_wait_bounded(&c.full[st], uint32_t(st < at.at ? at.round : at.round - 1) & 1u, nullptr);
     } else if (warp == 1 && lane == 0) {
-      Ring at(kStages);
+      Ring at(p.stages);
       int turn = 0;
       const uint32_t sbase = smem_addr(smem);
       Runs r(table);
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
 
     // ---- 3. up ----
     if (warp == 0 && lane == 0) {
-      Ring at(kUp);
+      Ring at(p.up);
       for (int n = int(me); n < tiles && !*abort; n += CL) {
         for (Runs r(table); r.next();) {
           if (!r.has()) continue;
@@ -390,12 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         }
       }
       // the CTA must not finish while a load still writes its shared memory
-      for (int st = 0; st < kUp; ++st)
+      for (int st = 0; st < p.up; ++st)
         if (at.round > 0 || st < at.at)
           mbar_wait_bounded(&c.up_full[st], uint32_t(st < at.at ? at.round : at.round - 1) & 1u, nullptr);
     } else if (warp == 1 && lane == 0) {
       int it = 0;
-      Ring at(kUp);
+      Ring at(p.up);
       const uint32_t sbase = smem_addr(smem);
       for (int n = int(me); n < tiles; n += CL)
         for (Runs r(table); r.next();) {
