@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   constexpr int kHalf = kN / 2;      // 128 bytes of them
   extern __shared__ __align__(1024) uint8_t smem[];
   Control& c = *reinterpret_cast<Control*>(smem + control_at(g.rank, kN));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t me = CL == 1 ? 0 : cluster_ctarank();
   const int64_t m0 = int64_t(blockIdx.x / CL) * kTile;
   const int size = int(min(int64_t(kTile), g.M - m0));
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     const int tiles = int((g.N + kN - 1) / kN);
     // ---- 1. down ----
     // Runs with an adapter, in groups whose A blocks go through the ring beside one block of x.
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
       Ring at(p.stages);
       Runs r(table);
       for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0 && !*abort;) {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       for (int st = 0; st < p.stages; ++st)  // the last use of each place
         if (at.round > 0 || st < at.at)
           mbar_wait_bounded(&c.full[st], uint32_t(st < at.at ? at.round : at.round - 1) & 1u, nullptr);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
       Ring at(p.stages);
       int turn = 0;
       const uint32_t sbase = smem_addr(smem);
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     tc_fence_after();
 
     // ---- 3. up ----
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
       Ring at(p.up);
       for (int n = int(me); n < tiles && !*abort; n += CL) {
         for (Runs r(table); r.next();) {
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       for (int st = 0; st < p.up; ++st)
         if (at.round > 0 || st < at.at)
           mbar_wait_bounded(&c.up_full[st], uint32_t(st < at.at ? at.round : at.round - 1) & 1u, nullptr);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
       int it = 0;
       Ring at(p.up);
       const uint32_t sbase = smem_addr(smem);
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           if (lane == 0) mbar_arrive(&c.base_done[bs]);
         }
       }
-    } else if (TMA && warp == 2 + kEpilogueWarps && lane == 0) {
+    } else if (TMA && warp == 2 + kEpilogueWarps && elect_one()) {
       auto fetch = [&](int n, int bs) {
         const bool two = int64_t(n) * kN + kHalf < g.N;
         uint8_t* dst = smem + p.base_at + bs * 2 * kXBytes;
