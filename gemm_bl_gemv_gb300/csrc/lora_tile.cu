@@ -53,7 +53,7 @@ __host__ __device__ constexpr uint32_t idesc(int n) {  // bf16 x bf16 -> fp32, M
 // [ring of B | ring of base, or turning buffers].
 struct Plan {
   int rp, rk;             // rank rounded up to 16 (MMA N and K) and to 64 (operand sub-tiles)
-  uint32_t a_bytes, a_at; // of a run's A block in a ring stage; from one to the next
+  uint32_t a_bytes;       // of a run's A block in a ring stage
   int group;              // runs whose A goes through the ring together
   int stages, up;         // places of the ring of x and A, and of the ring of B
   uint32_t stage;         // of a ring stage
@@ -69,9 +69,8 @@ __host__ __device__ inline Plan make_plan(int rank, int n_tile, int runs) {
   p.rp = (rank + 15) / 16 * 16;
   p.rk = (rank + 63) / 64 * 64;
   p.a_bytes = uint32_t(p.rp) * 128;
-  p.a_at = (p.a_bytes + 1023) / 1024 * 1024;
   p.group = p.rp <= 64 && runs > 1 ? 2 : 1;
-  p.stage = kXBytes + uint32_t(p.group) * p.a_at;
+  p.stage = kXBytes + uint32_t(p.group) * p.a_bytes;
   p.stages = p.rp <= 64 ? kStages : kStages - 1;
   p.term = p.rk / 2;
   p.up_at = 0;
@@ -264,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           tma_load_2d(dst, &xmap, kb * 128, int(m0), &c.full[st]);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            if (j < n) tma_load_2d(dst + kXBytes + j * p.a_at, &amap, kb * 128, c.adapter[from[j]] * g.rank, &c.full[st]);
+            if (j < n) tma_load_2d(dst + kXBytes + j * p.a_bytes, &amap, kb * 128, c.adapter[from[j]] * g.rank, &c.full[st]);
         }
       }
       // nothing may still be on its way into the ring when it is used for the operand
@@ -284,12 +283,11 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           if (!*abort && !mbar_wait_bounded(&c.full[st], at.parity(), g.err)) *abort = 1;
           tc_fence_after();
           const uint32_t xa = sbase + st * p.stage;
-          if (!*abort)
-            for (int j = 0; j < n; ++j)
+          if (!*abort)  // the runs' A blocks lie one behind the other: one product for all
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                umma_f16(tmem + j * kAccCols, umma_desc_sw128(xa + ks * 32),
-                         umma_desc_sw128(xa + kXBytes + j * p.a_at + ks * 32), idesc(p.rp), kb > k0 || ks > 0);
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16(tmem, umma_desc_sw128(xa + ks * 32), umma_desc_sw128(xa + kXBytes + ks * 32), idesc(n * p.rp),
+                       kb > k0 || ks > 0);
           umma_commit(&c.empty[st]);
         }
         umma_commit(&c.sums);
@@ -310,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           for (int col = part4 * 16; col < p.rp; col += 64) {
             uint32_t v[16];
             __syncwarp();
-            tmem_ld16(tmem + j * kAccCols + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
+            tmem_ld16(tmem + uint32_t(j * p.rp) + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
             tmem_ld_wait();
             if (row >= from[j] && row < to[j]) {
 #pragma unroll
@@ -397,38 +395,39 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         if (at.round > 0 || st < at.at)
           mbar_wait_bounded(&c.up_full[st], uint32_t(st < at.at ? at.round : at.round - 1) & 1u, nullptr);
     } else if (warp == 1 && elect_one()) {
-      int it = 0;
-      Ring at(p.up);
+      // a product for every tile and run with an adapter, in the order in which B comes
+      const int products = (tiles - int(me) + CL - 1) / CL * __popc(table.has);
       const uint32_t sbase = smem_addr(smem);
-      for (int n = int(me); n < tiles; n += CL)
-        for (Runs r(table); r.next();) {
-          if (!r.has()) continue;
-          const int st = at.at, acc = it % kAcc;
-          if (!*abort && !mbar_wait_bounded(&c.up_full[st], at.parity(), g.err)) *abort = 1;
-          if (it >= kAcc && !*abort && !mbar_wait_bounded(&c.out_empty[acc], uint32_t(it / kAcc - 1) & 1u, g.err)) *abort = 1;
-          tc_fence_after();
-          // 16 columns of the operand and of B's rows at a time (8 TMEM columns, 32 bytes), 64 where there
-          // are so many: one descriptor after the other is made while the tensor core works
-          const uint32_t ba = sbase + p.up_at + st * p.up_stage, da = tmem + acc * kAccCols;
-          if (!*abort)
-            for (int t = 0; t < kTerms; ++t)
-              for (int sub = 0; sub < p.rk / 64; ++sub) {
-                const uint32_t oa = tmem + kOperand + uint32_t(t * p.term + 32 * sub), bs = ba + sub * (kN * 128);
-                const uint32_t more = t > 0 || sub > 0;
-                if (p.rp - 64 * sub >= 64) {
+      bool dead = *abort;
+      Ring at(p.up);
+      for (int it = 0; it < products; ++it, at.next()) {
+        const int st = at.at, acc = it % kAcc;
+        dead = dead || !mbar_wait_bounded(&c.up_full[st], at.parity(), g.err);
+        dead = dead || (it >= kAcc && !mbar_wait_bounded(&c.out_empty[acc], uint32_t(it / kAcc - 1) & 1u, g.err));
+        if (dead) *abort = 1;
+        tc_fence_after();
+        // 16 columns of the operand and of B's rows at a time (8 TMEM columns, 32 bytes), 64 where there
+        // are so many: one descriptor after the other is made while the tensor core works
+        const uint32_t ba = sbase + p.up_at + st * p.up_stage, da = tmem + acc * kAccCols;
+        if (!dead)
+          for (int t = 0; t < kTerms; ++t)
+            for (int sub = 0; sub < p.rk / 64; ++sub) {
+              const uint32_t oa = tmem + kOperand + uint32_t(t * p.term + 32 * sub), bs = ba + sub * (kN * 128);
+              const uint32_t more = t > 0 || sub > 0;
+              if (p.rp - 64 * sub >= 64) {
 #pragma unroll
-                  for (int ks = 0; ks < 4; ++ks)
-                    umma_f16_ta(da, oa + 8 * ks, umma_desc_sw128(bs + ks * 32), idesc(kN), ks > 0 ? 1u : more);
-                } else {
-                  for (int ks = 0; ks < p.rp / 16 - 4 * sub; ++ks)
-                    umma_f16_ta(da, oa + 8 * ks, umma_desc_sw128(bs + ks * 32), idesc(kN), ks > 0 ? 1u : more);
-                }
+                for (int ks = 0; ks < 4; ++ks)
+                  umma_f16_ta(da, oa + 8 * ks, umma_desc_sw128(bs + ks * 32), idesc(kN), ks > 0 ? 1u : more);
+              } else {
+                for (int ks = 0; ks < p.rp / 16 - 4 * sub; ++ks)
+                  umma_f16_ta(da, oa + 8 * ks, umma_desc_sw128(bs + ks * 32), idesc(kN), ks > 0 ? 1u : more);
               }
-          umma_commit(&c.up_empty[st]);
-          umma_commit(&c.out_full[acc]);
-          ++it;
-          at.next();
-        }
+            }
+        umma_commit(&c.up_empty[st]);
+        umma_commit(&c.out_full[acc]);
+      }
+      if (dead && products > 0)  // none may still run when the CTA ends
+        mbar_wait_bounded(&c.out_full[(products - 1) % kAcc], uint32_t((products - 1) / kAcc) & 1u, nullptr);
     } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
       constexpr int kCols = kN / 4;  // outputs of a warp: 64 bytes of a row
       const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
