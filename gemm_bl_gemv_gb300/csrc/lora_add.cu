@@ -8,11 +8,13 @@
 // Each CTA forms the inner products with an eighth of K, a warp a row of A at
 // a time; the eighths meet through distributed shared memory, added in rank
 // order; then each CTA forms an eighth of the outputs, a thread a row of B.
-// The CTA's part of B is fetched into L2 while A is being read, so that the
-// two matrices come from HBM in one stream.  All sums are fp32.
+// The CTA's part of B and of base is fetched into L2 while A is being read, so
+// that they come from HBM in one stream.  All sums are fp32.
 //
-// Bound: HBM for many requests (A and B of every adapter once), latency for
-// one.
+// Bound: latency: launch, adapter -> A, the cluster's exchange, B, each a
+// dependent step of one to three us (one token, 2560 -> 6912, rank 16: 5.1 us;
+// 64 tokens over 40 adapters, 5120 -> 13824, rank 32: 20.6 us, a third of HBM's
+// rate for the 47 MB that they need).
 #include "bl_internal.h"
 #include "lora.cuh"
 
@@ -21,7 +23,8 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kParts = 8;      // CTAs of a cluster
-constexpr double kTileWork = 3e8;  // multiply-adds from which the tiles' kernel is launched as well
+constexpr int64_t kTileTokens = 384;  // tokens and multiply-adds from which the tiles' kernel is launched as well
+constexpr double kTileWork = 1e8;
 constexpr int kGroup = 4;      // tokens that share the reads of an adapter
 
 struct Args {
@@ -86,7 +89,14 @@ __device__ __forceinline__ void up(const Args& g, const float (*low)[128], int64
     const bool two = n + kThreads < n1;
     const uint4* row0 = reinterpret_cast<const uint4*>(b + n * g.R);
     const uint4* row1 = two ? row0 + int64_t(kThreads) * r8 : row0;
-    float acc0[NT] = {}, acc1[NT] = {};
+    float acc0[NT] = {}, acc1[NT] = {}, add0[NT], add1[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (NT == 1 || t < nt) {
+        const int64_t i = (m + t) * g.N + n;
+        add0[t] = load1<YB>(g.base, i);
+        add1[t] = two ? load1<YB>(g.base, i + kThreads) : 0.f;
+      }
 #pragma unroll 4
     for (int r = 0; r < r8; ++r) {
       const uint4 q0 = row0[r], q1 = row1[r];
@@ -103,8 +113,8 @@ __device__ __forceinline__ void up(const Args& g, const float (*low)[128], int64
     for (int t = 0; t < NT; ++t) {
       if (NT > 1 && t >= nt) break;
       const int64_t i = (m + t) * g.N + n;
-      store1<YB>(g.y, i, load1<YB>(g.base, i) + acc0[t]);
-      if (two) store1<YB>(g.y, i + kThreads, load1<YB>(g.base, i + kThreads) + acc1[t]);
+      store1<YB>(g.y, i, add0[t] + acc0[t]);
+      if (two) store1<YB>(g.y, i + kThreads, add1[t] + acc1[t]);
     }
   }
 }
@@ -146,6 +156,12 @@ __global__ void __launch_bounds__(kThreads, 4) lora_token_kernel(const Args g) {
     const uint16_t* b = g.b + int64_t(l) * g.N * g.R;
     for (int64_t i = n0 * g.R + int64_t(threadIdx.x) * 64; i < n1 * g.R; i += kThreads * 64)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(b + i));
+    for (int t = 0; t < nt; ++t) {
+      constexpr int kSize = YB ? 2 : 4;
+      const char* at = static_cast<const char*>(g.base) + (m + t) * g.N * kSize;
+      for (int64_t i = n0 * kSize + int64_t(threadIdx.x) * 128; i < n1 * kSize; i += kThreads * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
+    }
     float(*part)[128] = sh.part[run & 1];
     if (nt > 1)
       down<XB, kGroup, 2>(g, part, m, nt, l, me);
@@ -203,10 +219,12 @@ cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, 
   const int per = M <= 256 ? 1 : kGroup;
   if ((M + per - 1) / per > 0x7fffffff / kParts) return cudaErrorInvalidConfiguration;
   Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, per, false};
-  // The tiles' kernel takes some 25 us however few they are; this one reads an adapter again for every
-  // group of four tokens and does M rank (K + N) multiply-adds on the CUDA cores.  (517 tokens, rank 24, 2560
-  // -> 2560, 6e7 of them: KK us here, 42 us in tiles; 8192 tokens, rank 64, 2560 -> 6912, 5e9: 117 us in tiles.)
-  if (xt == BL_BF16 && M > 32 && double(M) * rank * double(K + N) > kTileWork) {
+  // The tiles' kernel takes much the same time up to 1024 tokens, for a cluster has the fewer CTAs the more
+  // tiles there are; this one reads an adapter again for every group of four tokens and does M rank (K + N)
+  // multiply-adds on the CUDA cores.  Three adapters, scattered / tiles, us: 2560 -> 2560, rank 24: 512 tokens
+  // 25 / 27, 1024 (1.3e8) 44 / 27; 2560 -> 6912, rank 64: 256 tokens (1.6e8) 46 / 55, 512 74 / 54;
+  // 5120 -> 13824, rank 16: 256 tokens (8e7) 24 / 32, 512 (1.6e8) 35 / 32, 1024 65 / 33.
+  if (xt == BL_BF16 && M >= kTileTokens && double(M) * rank * double(K + N) > kTileWork) {
     const cudaError_t e = launch_lora_tile(x, adapter, a, b, scale, base, y, yt, M, N, K, adapters, rank, s);
     if (e != cudaSuccess && e != cudaErrorNotSupported) return e;
     g.tiles = e == cudaSuccess;

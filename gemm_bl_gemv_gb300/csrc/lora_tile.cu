@@ -6,27 +6,31 @@
 // with one adapter; a tile of more than kTileRuns runs is left to the kernel
 // for scattered tokens.
 //   1. Down: each CTA takes a part of K.  x (128 x 64 blocks) and the runs' A
-//      (rank x 64, up to two runs at once) come by TMA through a ring; the tensor core forms the
-//      128 x rank product in TMEM, and the rows of the run go to shared
-//      memory as fp32.  The CTAs add their parts up in rank order through
-//      distributed shared memory, so the sum over K is never rounded below
-//      fp32.
+//      (rank x 64, up to two runs at once) come by TMA through a ring; the
+//      tensor core forms the 128 x rank product in TMEM, and the rows of the
+//      run go to shared memory as fp32.  The CTAs add their parts up in rank
+//      order through distributed shared memory, so the sum over K is never
+//      rounded below fp32.
 //   2. The sums, times the adapter's scale, become bf16 operands in TMEM: two
 //      terms (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8,
-//      three (24 bits) for fp32 outputs.  (From shared memory the operand would
-//      be read again by every MMA: 143 clocks per 128 x 64 x 16 instead of KK.)
+//      three (24 bits) for fp32 outputs.  (In shared memory it would take up to
+//      96 KB of what the rings have.)
 //   3. Up: each CTA takes tiles of 256 bytes of outputs (128 bf16, 64 fp32).
 //      B's rows come by TMA as they lie in memory, and so does the tile of
-//      base, 128-byte swizzled, three tiles ahead.  Every run of the 128 tokens
+//      base, 128-byte swizzled, four in flight.  Every run of the 128 tokens
 //      has its own product in one of two TMEM buffers; the thread of a row adds
 //      its run's to the base in place, and the tile goes out by TMA, rows
 //      without an adapter unchanged.  Rows of y that are not 16-byte aligned
 //      (N * element size not a multiple of 16) are read and written by the
 //      threads, a row's outputs by neighbouring lanes.
 //
-// Bound: HBM.  base and y are 4 of the 5 bytes that an output costs at K =
-// N / 2.7 and rank 64; the tensor work of 8192 x 2560 x 6912 at rank 64 (17
-// GFLOP with two terms) is 9 us of the 41 us that its bytes take.
+// Bound: HBM; base and y are 4 of the 5 bytes that an output costs at K = N / 2.7
+// and rank 64.  8192 tokens of 12 prompts, 2560 -> 6912, rank 64: 74.5 us, 41 us of
+// them HBM's for 276 MB, 9 us the tensor core's (17 GFLOP with two terms).  The
+// CTAs of tiles with one run end after 45 us; the rest is the 12 tiles in which
+// one prompt ends and the next begins, with two products for every output tile.
+// One run's rows are not masked out of the other's product (one sum for both):
+// an infinite weight of one request's adapter must not reach another's outputs.
 #include "bl_device.cuh"
 #include "bl_internal.h"
 #include "lora.cuh"

@@ -341,7 +341,7 @@ def test_lora_a_bad_row_stays_in_its_row(B):
 
 
 def tile_case(lengths, N, K, rank, yb, seed):
-    """Enough work for the tensor-core kernel (3e8 multiply-adds): runs of one adapter, some of none."""
+    """Enough work and tokens for the tensor-core kernel: runs of one adapter, some of none."""
     index = np.repeat([[0, 2, -1, 1, 0, 3, -1][i % 7] for i in range(len(lengths))], lengths)
     assert len(index) * rank * (N + K) > 3e8
     return lora_inputs(len(index), N, K, rank, 4, True, yb, seed, index)
