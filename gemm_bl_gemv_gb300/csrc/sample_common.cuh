@@ -17,6 +17,7 @@ struct SampleArgs {
   int32_t* token;
   float* prob;
   int chunk;  // logits of a CTA
+  bool copy;  // fp32: a chunk is kept in shared memory
 };
 
 __device__ __forceinline__ u64 warp_sum_u64(u64 v) {

@@ -9,6 +9,9 @@
 // within its bin by sorting the bin's logits; a bin with more than 1024 of
 // them is cut again, by the rest of z and then by the bits of the value.
 //
+// The first pass, for the largest logit, leaves the chunk in shared memory where
+// it fits there (37000 logits), and the later passes read it from there.
+//
 // Bound: three shared-memory atomics and one weight (about 30 instructions)
 // per logit in the first pass; the later passes touch few logits.
 #include "sample_common.cuh"
@@ -22,6 +25,7 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxChunk = 65536;  // logits of a CTA: 16-bit halves of weights add up in 32 bits
+constexpr size_t kMaxShared = 227 * 1024;
 constexpr float kOctaves = 46.f;  // weights below 2^-45 of the largest are 0
 
 // A digit of the descent: counts and weights of 2048 bins.
@@ -51,7 +55,7 @@ struct Place {
   u64 weight, through;
 };
 
-struct Shared {
+struct __align__(16) Shared {
   Digit digit;
   Sums first, later;  // rank 0's: the first digit's, a later one's
   uint32_t list[kThreads];
@@ -84,24 +88,27 @@ struct Row {
     return C == 1 ? p : peer(p, r);
   }
 
-  // f(logit) for this thread's logits of the chunk, eight loads at a time (a loop of one load each waits
-  // for L2 every time: 16 us instead of KK for a chunk of 25001).
+  // f(index, logit) for this thread's logits of the chunk, eight loads at a time (a load waits for L2).
   template <class F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each_at(F f) const {
     int i = threadIdx.x;
     for (; i + 7 * kThreads < n; i += 8 * kThreads) {
       float l[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) l[j] = x[i + j * kThreads];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f(l[j]);
+      for (int j = 0; j < 8; ++j) f(i + j * kThreads, l[j]);
     }
     float l[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) l[j] = i + j * kThreads < n ? x[i + j * kThreads] : -INFINITY;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (i + j * kThreads < n) f(l[j]);
+      if (i + j * kThreads < n) f(i + j * kThreads, l[j]);
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    each_at([&](int, float l) { f(l); });
   }
 
   // ---- a logit's digits ----
@@ -260,7 +267,7 @@ struct Row {
       if (rank == 0) {
         const uint32_t i = threadIdx.x;
         uint32_t key = i < p.n ? sh.list[i] : 0u;  // 0: below every logit's
-        for (uint32_t k = 2; k <= kThreads; k <<= 1)
+        for (uint32_t k = 2; k < 2 * p.n; k <<= 1)
           for (uint32_t j = k >> 1; j > 0; j >>= 1) {
             uint32_t other;
             if (j >= 32) {
@@ -317,7 +324,9 @@ __global__ void __launch_bounds__(kThreads) sample_f32_kernel(const Args g) {
 
   // the largest and the smallest live logit
   float hi = -INFINITY, lo = INFINITY;
-  row.each([&](float l) {
+  float* copy = reinterpret_cast<float*>(smem + sizeof(Shared) / sizeof(uint4));
+  row.each_at([&](int i, float l) {
+    if (g.copy) copy[i] = l;
     hi = fmaxf(hi, l);
     if (l > -INFINITY) lo = fminf(lo, l);
   });
@@ -325,6 +334,7 @@ __global__ void __launch_bounds__(kThreads) sample_f32_kernel(const Args g) {
   lo = -warp_max(-lo);
   if (lane == 0) sh.redf[0][warp] = hi, sh.redf[1][warp] = lo;
   __syncthreads();
+  if (g.copy) row.x = copy;
   hi = warp_max(sh.redf[0][lane]);
   lo = -warp_max(-sh.redf[1][lane]);
   if (C > 1) {
@@ -414,7 +424,12 @@ __global__ void __launch_bounds__(kThreads) sample_f32_kernel(const Args g) {
 
 template <int C>
 cudaError_t launch_rows(const Args& g, cudaStream_t s) {
-  return launch_clusters<C>(sample_f32_kernel<C>, g.M * C, kThreads, int(sizeof(Shared)), s, g);
+  const int smem = int(sizeof(Shared)) + (g.copy ? g.chunk * 4 : 0);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const cudaError_t e = raise_smem_cap(sample_f32_kernel<C>, dev, int(kMaxShared));  // one limit for every chunk
+  if (e != cudaSuccess) return e;
+  return launch_clusters<C>(sample_f32_kernel<C>, g.M * C, kThreads, smem, s, g);
 }
 
 }  // namespace
@@ -425,6 +440,7 @@ cudaError_t launch_sample_f32(const SampleArgs& args, cudaStream_t s) {
   while ((args.V + c - 1) / c > kMaxChunk) c *= 2;
   SampleArgs g = args;
   g.chunk = int((g.V + c - 1) / c);
+  g.copy = sizeof(Shared) + size_t(g.chunk) * 4 <= kMaxShared;
   if (g.M * c > 0x7fffffff) return cudaErrorInvalidConfiguration;
   switch (c) {
     case 1: return launch_rows<1>(g, s);
