@@ -1,6 +1,7 @@
 // C ABI of libbl: argument checks (before any launch), status codes, the
 // device error word and the overlap switch.  Every product and conversion is
 // done by the kernels in the other translation units.
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -107,6 +108,35 @@ cudaError_t raise_smem_cap_impl(const void* kernel, int dev, int bytes) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && n < 256) entries[n++] = Entry{kernel, dev, bytes};
   return e;
+}
+
+__global__ void one_per_sm_kernel() {}
+
+int clusters_at_once(int c) {
+  constexpr int kMost = 8, kBytes = 200 * 1024;  // of shared memory, so that an SM has one CTA
+  static int cache[64][kMost + 1] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (c <= 1 || c > kMost) return std::max(1, sm_count() / std::max(c, 1));
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev][c] == 0) {
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(c));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = kBytes;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {unsigned(c), 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const bool ok = raise_smem_cap(one_per_sm_kernel, dev, kBytes) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, one_per_sm_kernel, &cfg) == cudaSuccess;
+    cache[dev][c] = ok && n > 0 ? n : std::max(1, sm_count() / c);
+  }
+  return cache[dev][c];
 }
 
 int sm_count() {

@@ -20,6 +20,9 @@ unsigned long long wait_limit_ns();
 
 // Number of SMs of the current device (cached per device).
 int sm_count();
+// Clusters of c CTAs (up to 8) that run at once when every CTA has an SM to itself: fewer than sm_count() / c, for a
+// cluster lies within a group of SMs (152 SMs: 36 clusters of 4).
+int clusters_at_once(int c);
 
 // Device address of the library's error word on the current device (the
 // BL_DEVERR_* bits read by bl_device_error()); kernels receive it as an

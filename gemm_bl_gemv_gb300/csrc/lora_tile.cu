@@ -614,10 +614,10 @@ cudaError_t launch_lora_tile(const void* x, const int32_t* adapter, const uint16
                    encode_tmap_2d_u8(&maps.y, y, row, uint64_t(M), row, 128, kTile, true);
   if (!tma) maps.base = maps.y = maps.x;  // not used
   const Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank};
-  // CTAs of a tile of tokens: as many as keep one per SM
+  // CTAs of a tile of tokens: as many as run at once
   const int64_t tiles = (M + kTile - 1) / kTile;
   int cl = 1;
-  while (cl < 8 && tiles * cl * 2 <= sm_count()) cl *= 2;
+  while (cl < 8 && tiles <= clusters_at_once(2 * cl)) cl *= 2;
   if (yb) return tma ? launch_tiles<true, true>(cl, maps, g, s) : launch_tiles<true, false>(cl, maps, g, s);
   return tma ? launch_tiles<false, true>(cl, maps, g, s) : launch_tiles<false, false>(cl, maps, g, s);
 }

@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreads) sample_bf16_kernel(const Args g) {
 
 template <int C>
 cudaError_t launch_rows(const Args& g, cudaStream_t s) {
-  const int64_t clusters = std::min<int64_t>(g.M, std::max(1, sm_count() / C));
+  const int64_t clusters = std::min<int64_t>(g.M, clusters_at_once(C));
   return launch_clusters<C>(sample_bf16_kernel<C>, clusters * C, kThreads, int(sizeof(Shared)), s, g);
 }
 
@@ -604,7 +604,7 @@ cudaError_t launch_rows(const Args& g, cudaStream_t s) {
 
 cudaError_t launch_sample_bf16(const SampleArgs& args, cudaStream_t s) {
   // Measured per row and CTA: 8 us beside the histogram, 0.08 ns per logit.
-  const int c = ctas_per_row(args.M, args.V, 8000.0, 0.08);
+  const int c = ctas_per_row(args.M, [&](int c) { return 8000.0 + 0.08 * double(args.V) / c; });
   SampleArgs g = args;
   g.chunk = int(((g.V + 7 + c - 1) / c + 7) / 8 * 8);
   switch (c) {

@@ -78,14 +78,14 @@ cudaError_t launch_clusters(void (*kernel)(const SampleArgs), int64_t grid, int 
   return cudaLaunchKernelEx(&cfg, kernel, g);
 }
 
-// The number of CTAs of a row: it costs each of them `fixed` ns beside
-// `per_logit` ns for each logit of its chunk, and sm_count / c rows run at a time.
-inline int ctas_per_row(int64_t M, int64_t V, double fixed, double per_logit) {
+// The number of CTAs of a row: cost(c) is the time of a row in c CTAs.
+template <class F>
+int ctas_per_row(int64_t M, F cost) {
   int best = 1;
   double least = 0;
   for (int c = 1; c <= 8; c *= 2) {
-    const int64_t at_once = std::max(1, sm_count() / c);
-    const double t = double((M + at_once - 1) / at_once) * (fixed + per_logit * double(V) / c);
+    const int64_t at_once = clusters_at_once(c);
+    const double t = double((M + at_once - 1) / at_once) * cost(c);
     if (c == 1 || t < 0.95 * least) best = c, least = t;
   }
   return best;

@@ -12,8 +12,11 @@
 // The first pass, for the largest logit, leaves the chunk in shared memory where
 // it fits there (37000 logits), and the later passes read it from there.
 //
-// Bound: three shared-memory atomics and one weight (about 30 instructions)
-// per logit in the first pass; the later passes touch few logits.
+// Bound: instruction issue in the pass that counts and weighs (some 70
+// instructions per logit, 40 of them the weight: 11 us for 25001 logits a CTA;
+// one atomic less, additions in place of the conversions, and a table without
+// bank conflicts each changed nothing), and 7 us of exchanges in the cluster
+// for every place that is looked for.  32 rows of 100003, mixed filters: 46 us.
 #include "sample_common.cuh"
 
 namespace bl {
@@ -435,12 +438,16 @@ cudaError_t launch_rows(const Args& g, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_sample_f32(const SampleArgs& args, cudaStream_t s) {
-  // Measured per row and CTA: 20 us beside the passes, 0.5 ns per logit.
-  int c = ctas_per_row(args.M, args.V, 20000.0, 0.5);
+  auto fits = [&](int c) { return sizeof(Shared) + size_t((args.V + c - 1) / c) * 4 <= kMaxShared; };
+  // Measured with top-k and top-p: 20 us beside the passes in one CTA, 26 in a cluster; 0.65 ns per logit of a
+  // chunk in shared memory, 1 ns from L2.
+  int c = ctas_per_row(args.M, [&](int c) {
+    return (c == 1 ? 20000.0 : 26000.0) + (fits(c) ? 0.65 : 1.0) * double(args.V) / c;
+  });
   while ((args.V + c - 1) / c > kMaxChunk) c *= 2;
   SampleArgs g = args;
   g.chunk = int((g.V + c - 1) / c);
-  g.copy = sizeof(Shared) + size_t(g.chunk) * 4 <= kMaxShared;
+  g.copy = fits(c);
   if (g.M * c > 0x7fffffff) return cudaErrorInvalidConfiguration;
   switch (c) {
     case 1: return launch_rows<1>(g, s);
