@@ -7,6 +7,11 @@
 // pair of floats (a two-sum per term: its error is below 2^-40 of the sum)
 // and r is rounded to binary32 once; everything after r is elementwise with
 // the _rn intrinsics, and a maximum.
+//
+// Bound: HBM for many tokens (8192 x 5120 bf16 with a residual: 62 us, 69 % of
+// the copy rate; the row's two reductions stand between its loads and its
+// stores, and 55 registers a thread leave half of the warps), latency for few:
+// one token of 2560 2.9 us, of which the launch is most.
 #include "act_quant.cuh"
 #include "bl_internal.h"
 
