@@ -466,6 +466,20 @@ def test_sample_ties_and_equal_rows(B, V, bf16):
 
 @gpu
 @pytest.mark.parametrize("bf16", [True, False])
+def test_sample_is_the_same_for_every_number_of_rows(B, bf16):
+    """The number of rows chooses the CTAs of a row; the row's token and probability do not depend on it."""
+    g, n, V = rng(41), 200, 40001
+    l = dev((3 * g.standard_normal((n, V))).astype(np.float32), torch.bfloat16 if bf16 else None)
+    u, t = dev(g.random(n).astype(np.float32)), dev(g.uniform(0.5, 1.5, n).astype(np.float32))
+    k, p = dev(np.where(g.random(n) < 0.5, 40, 0).astype(np.int32)), dev(g.uniform(0.8, 1.1, n).astype(np.float32))
+    token, prob = B.bl_sample(l, u, t, k, p, prob=True)
+    for m in (1, 16, 19, 36, 38, 74, 76, 77, 152, 153):
+        a, b = B.bl_sample(l[:m], u[:m], t[:m], k[:m], p[:m], prob=True)
+        assert torch.equal(a, token[:m]) and torch.equal(b, prob[:m]), m
+
+
+@gpu
+@pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("V", [5, 1025, 40000])
 def test_sample_masks_infinities_and_odd_parameters(B, V, bf16):
     g = rng(V, 6)
