@@ -164,10 +164,10 @@ cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, bl_dtype x
 cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
                             const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
                             int64_t K, int64_t adapters, int rank, cudaStream_t s);
-// The tiles of 128 tokens with few runs of one adapter (csrc/lora_tile.cu, bf16
-// x); cudaErrorNotSupported, having launched nothing, when no tensor map
+// The tiles of 128 tokens with few runs of one adapter (csrc/lora_tile.cu);
+// cudaErrorNotSupported, having launched nothing, when no tensor map
 // describes the operands.
-cudaError_t launch_lora_tile(const void* x, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
+cudaError_t launch_lora_tile(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
                              const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
                              int64_t K, int64_t adapters, int rank, cudaStream_t s);
 // Sampling (csrc/sample_bf16.cu, csrc/sample_f32.cu); the arguments are in sample_common.cuh.

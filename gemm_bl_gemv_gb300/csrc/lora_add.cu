@@ -2,7 +2,7 @@
 //   y[m,n] = base[m,n] + scale[a] * sum_r B[a,n,r] (sum_k A[a,r,k] x[m,k]),
 // a = adapter[m], negative for none.  This file has the kernel for scattered
 // tokens (a decode step: every token has its own adapter); tiles of 128 tokens
-// with few runs of one adapter go to lora_tile.cu when x is bf16.
+// with few runs of one adapter go to lora_tile.cu when there are many.
 //
 // A cluster of 8 CTAs takes up to four neighbouring tokens of one adapter.
 // Each CTA forms the inner products with an eighth of K, a warp a row of A at
@@ -224,8 +224,8 @@ cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, 
   // multiply-adds on the CUDA cores.  Three adapters, scattered / tiles, us: 2560 -> 2560, rank 24: 512 tokens
   // 25 / 27, 1024 (1.3e8) 44 / 27; 2560 -> 6912, rank 64: 256 tokens (1.6e8) 46 / 55, 512 74 / 54;
   // 5120 -> 13824, rank 16: 256 tokens (8e7) 24 / 32, 512 (1.6e8) 35 / 32, 1024 65 / 33.
-  if (xt == BL_BF16 && M >= kTileTokens && double(M) * rank * double(K + N) > kTileWork) {
-    const cudaError_t e = launch_lora_tile(x, adapter, a, b, scale, base, y, yt, M, N, K, adapters, rank, s);
+  if (M >= kTileTokens && double(M) * rank * double(K + N) > kTileWork) {
+    const cudaError_t e = launch_lora_tile(x, xt, adapter, a, b, scale, base, y, yt, M, N, K, adapters, rank, s);
     if (e != cudaSuccess && e != cudaErrorNotSupported) return e;
     g.tiles = e == cudaSuccess;
   }

@@ -1,5 +1,5 @@
 // Low-rank adapters of long runs of tokens (bl_lora_add), on the 5th-generation
-// tensor cores (tcgen05), bf16 activations:
+// tensor cores (tcgen05):
 //   y[m,n] = base[m,n] + scale[a] * sum_r B[a,n,r] (sum_k A[a,r,k] x[m,k]).
 //
 // A cluster of CL CTAs takes 128 tokens.  A run is a stretch of those tokens
@@ -10,7 +10,9 @@
 //      tensor core forms the 128 x rank product in TMEM, and the rows of the
 //      run go to shared memory as fp32.  The CTAs add their parts up in rank
 //      order through distributed shared memory, so the sum over K is never
-//      rounded below fp32.
+//      rounded below fp32.  fp32 x (two boxes of 32 columns) is turned by the
+//      epilogue warps, idle here, into three bf16 terms in TMEM, 24 bits
+//      (8192 tokens, 5120 -> 5120, rank 128: 114 us; 1894 on the CUDA cores).
 //   2. The sums, times the adapter's scale, become bf16 operands in TMEM: two
 //      terms (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8,
 //      three (24 bits) for fp32 outputs.  (In shared memory it would take up to
@@ -31,6 +33,8 @@
 // one prompt ends and the next begins, with two products for every output tile.
 // One run's rows are not masked out of the other's product (one sum for both):
 // an infinite weight of one request's adapter must not reach another's outputs.
+#include <algorithm>
+
 #include "bl_device.cuh"
 #include "bl_internal.h"
 #include "lora.cuh"
@@ -41,12 +45,15 @@ namespace {
 constexpr int kEpilogueWarps = 16;         // four per quarter of the TMEM lanes
 constexpr int kWarps = 3 + kEpilogueWarps, kThreads = 32 * kWarps;  // x, A and B; MMA; epilogue; base and y
 constexpr int kStages = 5;                 // K blocks of 64 in flight at most
+constexpr int kFloatStages = 3;            // of fp32 x, whose terms take 96 TMEM columns each
 constexpr int kUp = 6;                     // tiles of B in flight at most
 constexpr int kTiles = 4;                  // tiles of base in flight
 constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; half a tile of base
 constexpr int kAcc = 2, kAccCols = 128;    // accumulators
 constexpr uint32_t kOperand = 256;         // TMEM column of the operand's first term, three of 64 at most
+constexpr uint32_t kTermsOfX = 128;        // TMEM column of the terms of fp32 x, three of 32 per stage
 constexpr uint32_t kTmemCols = 512;
+static_assert(kTermsOfX + kFloatStages * 96 <= kTmemCols, "");
 constexpr int kTurn = 33;                  // floats of a row of 32 outputs being turned
 
 __host__ __device__ constexpr uint32_t idesc(int n) {  // bf16 x bf16 -> fp32, M = 128
@@ -60,6 +67,7 @@ struct Plan {
   uint32_t a_bytes;       // of a run's A block in a ring stage
   int group;              // runs whose A goes through the ring together
   int stages, up;         // places of the ring of x and A, and of the ring of B
+  uint32_t x_bytes;       // of a block of x: 64 bf16, or two halves of 32 floats, of 128 rows
   uint32_t stage;         // of a ring stage
   int term;               // TMEM columns of one operand term
   uint32_t part_at;       // byte offset of the partial sums
@@ -68,14 +76,15 @@ struct Plan {
   uint32_t base_at;       // ring of base tiles
   uint32_t end;
 };
-__host__ __device__ inline Plan make_plan(int rank, int n_tile, int runs) {
+__host__ __device__ inline Plan make_plan(int rank, int n_tile, int runs, bool xf) {
   Plan p;
   p.rp = (rank + 15) / 16 * 16;
   p.rk = (rank + 63) / 64 * 64;
   p.a_bytes = uint32_t(p.rp) * 128;
   p.group = p.rp <= 64 && runs > 1 ? 2 : 1;
-  p.stage = kXBytes + uint32_t(p.group) * p.a_bytes;
-  p.stages = p.rp <= 64 ? kStages : kStages - 1;
+  p.x_bytes = xf ? 2 * kXBytes : kXBytes;
+  p.stage = p.x_bytes + uint32_t(p.group) * p.a_bytes;
+  p.stages = xf ? kFloatStages : p.rp <= 64 ? kStages : kStages - 1;
   p.term = p.rk / 2;
   p.up_at = 0;
   p.up_stage = uint32_t(p.rk) / 64 * n_tile * 128;
@@ -90,8 +99,8 @@ __host__ __device__ inline Plan make_plan(int rank, int n_tile, int runs) {
 }
 
 // The control block lies behind either layout.
-__host__ __device__ inline uint32_t control_at(int rank, int n_tile) {
-  const uint32_t one = make_plan(rank, n_tile, 1).end, two = make_plan(rank, n_tile, 2).end;
+__host__ __device__ inline uint32_t control_at(int rank, int n_tile, bool xf) {
+  const uint32_t one = make_plan(rank, n_tile, 1, xf).end, two = make_plan(rank, n_tile, 2, xf).end;
   return one > two ? one : two;
 }
 
@@ -115,10 +124,11 @@ struct Args {
   unsigned int* err;
   int64_t M, N, K, L;
   int rank;
+  bool xf;  // x is fp32
 };
 
 struct Control {  // at control_at()
-  uint64_t full[kStages], empty[kStages], sums, drained, up_full[kUp], up_empty[kUp], out_full[kAcc], out_empty[kAcc];
+  uint64_t full[kStages], empty[kStages], terms[kFloatStages], sums, drained, up_full[kUp], up_empty[kUp], out_full[kAcc], out_empty[kAcc];
   uint64_t base_full[kTiles], base_done[kTiles];
   uint32_t tmem, starts[4], used[4];  // used: runs that have an adapter
   int abort;
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   constexpr int kN = YB ? 128 : 64;  // outputs of an up tile
   constexpr int kHalf = kN / 2;      // 128 bytes of them
   extern __shared__ __align__(1024) uint8_t smem[];
-  Control& c = *reinterpret_cast<Control*>(smem + control_at(g.rank, kN));
+  Control& c = *reinterpret_cast<Control*>(smem + control_at(g.rank, kN, g.xf));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t me = CL == 1 ? 0 : cluster_ctarank();
   const int64_t m0 = int64_t(blockIdx.x / CL) * kTile;
@@ -204,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   if (threadIdx.x == 0) {
     c.abort = 0;
     for (int i = 0; i < kStages; ++i) mbar_init(&c.full[i], 1), mbar_init(&c.empty[i], 1);
+    for (int i = 0; i < kFloatStages; ++i) mbar_init(&c.terms[i], kEpilogueWarps);
     mbar_init(&c.sums, 1);
     mbar_init(&c.drained, kEpilogueWarps);
     for (int i = 0; i < kUp; ++i) mbar_init(&c.up_full[i], 1), mbar_init(&c.up_empty[i], 1);
@@ -237,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   const bool mine = starts <= kTileRuns;
   const RunTable table(c.starts, c.adapter, size);
 
-  const Plan p = make_plan(g.rank, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]));
+  const Plan p = make_plan(g.rank, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]), g.xf);
 
   // All threads of the cluster; the barrier wants converged warps.
   auto sync_all = [] {
@@ -263,11 +274,12 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           if (at.round > 0 && !*abort && !mbar_wait_bounded(&c.empty[st], at.free_parity(), g.err)) *abort = 1;
           if (*abort) break;
           uint8_t* dst = smem + st * p.stage;
-          mbar_arrive_expect_tx(&c.full[st], kXBytes + n * p.a_bytes);
-          tma_load_2d(dst, &xmap, kb * 128, int(m0), &c.full[st]);
+          mbar_arrive_expect_tx(&c.full[st], p.x_bytes + n * p.a_bytes);
+          tma_load_2d(dst, &xmap, kb * int(p.x_bytes / kTile), int(m0), &c.full[st]);
+          if (g.xf) tma_load_2d(dst + kXBytes, &xmap, kb * 256 + 128, int(m0), &c.full[st]);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            if (j < n) tma_load_2d(dst + kXBytes + j * p.a_bytes, &amap, kb * 128, c.adapter[from[j]] * g.rank, &c.full[st]);
+            if (j < n) tma_load_2d(dst + p.x_bytes + j * p.a_bytes, &amap, kb * 128, c.adapter[from[j]] * g.rank, &c.full[st]);
         }
       }
       // nothing may still be on its way into the ring when it is used for the operand
@@ -287,11 +299,22 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           if (!*abort && !mbar_wait_bounded(&c.full[st], at.parity(), g.err)) *abort = 1;
           tc_fence_after();
           const uint32_t xa = sbase + st * p.stage;
-          if (!*abort)  // the runs' A blocks lie one behind the other: one product for all
+          // the runs' A blocks lie one behind the other: one product for all
+          if (g.xf) {
+            if (!*abort && !mbar_wait_bounded(&c.terms[st], at.parity(), g.err)) *abort = 1;
+            tc_fence_after();
+            if (!*abort)
+              for (int t = 0; t < 3; ++t)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  umma_f16_ta(tmem, tmem + kTermsOfX + uint32_t(st * 96 + t * 32 + ks * 8),
+                              umma_desc_sw128(xa + p.x_bytes + ks * 32), idesc(n * p.rp), kb > k0 || t > 0 || ks > 0);
+          } else if (!*abort) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               umma_f16(tmem, umma_desc_sw128(xa + ks * 32), umma_desc_sw128(xa + kXBytes + ks * 32), idesc(n * p.rp),
                        kb > k0 || ks > 0);
+          }
           umma_commit(&c.empty[st]);
         }
         umma_commit(&c.sums);
@@ -300,8 +323,38 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       float* part = reinterpret_cast<float*>(smem + p.part_at);
       const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
       int turn = 0;
+      Ring at(p.stages);
       Runs r(table);
       for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0; ++turn) {
+        if (g.xf)  // the terms of x, 16 columns of a row in a thread: unit u of a 128-byte row is at u ^ (row % 8)
+          for (int kb = k0; kb < k1; ++kb, at.next()) {
+            const int st = at.at;
+            if (!*abort && !mbar_wait_bounded(&c.full[st], at.parity(), g.err)) *abort = 1;
+            tc_fence_after();
+            float v[16];
+            const uint8_t* mine_row = smem + st * p.stage + (part4 >> 1) * kXBytes + row * 128;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float4 f = *reinterpret_cast<const float4*>(mine_row + (((part4 & 1) * 4 + u) ^ (row & 7)) * 16);
+              v[4 * u] = f.x, v[4 * u + 1] = f.y, v[4 * u + 2] = f.z, v[4 * u + 3] = f.w;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+              uint32_t w[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                w[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
+                v[2 * j] -= __uint_as_float(w[j] << 16);
+                v[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
+              }
+              tmem_st8(tmem + kTermsOfX + uint32_t(st * 96 + t * 32 + part4 * 8) + (uint32_t(quarter * 32) << 16), w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.terms[st]);
+          }
         if (!*abort && !mbar_wait_bounded(&c.sums, uint32_t(turn) & 1u, g.err)) *abort = 1;
         tc_fence_after();
         const bool ok = warp_agrees(!*abort);  // and the warp is converged for tcgen05.ld
@@ -560,12 +613,12 @@ cudaError_t launch_tiles(const Maps& maps, const Args& g, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   constexpr int kN = YB ? 128 : 64;
-  const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(control_at(128, kN) + 1024));
+  const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(std::max(control_at(128, kN, false), control_at(128, kN, true)) + 1024));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((g.M + kTile - 1) / kTile * CL));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = control_at(g.rank, kN) + 1024;
+  cfg.dynamicSmemBytes = control_at(g.rank, kN, g.xf) + 1024;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;
@@ -596,14 +649,15 @@ cudaError_t launch_tiles(int cl, const Maps& maps, const Args& g, cudaStream_t s
 
 }  // namespace
 
-cudaError_t launch_lora_tile(const void* x, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
+cudaError_t launch_lora_tile(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
                              const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
                              int64_t K, int64_t adapters, int rank, cudaStream_t s) {
   const bool yb = yt == BL_BF16;
-  const uint64_t row = uint64_t(N) * (yb ? 2 : 4);
+  const bool xf = xt == BL_F32;
+  const uint64_t row = uint64_t(N) * (yb ? 2 : 4), x_row = uint64_t(K) * (xf ? 4 : 2);
   Maps maps;  // bytes; 128-byte wide boxes, swizzled
   if (adapters * rank > 0x7fffffff || adapters * N > 0x7fffffff || row > 0x7fffffff ||
-      !encode_tmap_2d_u8(&maps.x, x, uint64_t(K) * 2, uint64_t(M), uint64_t(K) * 2, 128, kTile, true) ||
+      !encode_tmap_2d_u8(&maps.x, x, x_row, uint64_t(M), x_row, 128, kTile, true) ||
       !encode_tmap_2d_u8(&maps.a, a, uint64_t(K) * 2, uint64_t(adapters * rank), uint64_t(K) * 2, 128,
                          uint32_t(rank + 15) / 16 * 16, true) ||
       !encode_tmap_2d_u8(&maps.b, b, uint64_t(rank) * 2, uint64_t(adapters * N), uint64_t(rank) * 2, 128, yb ? 128 : 64,
@@ -613,7 +667,7 @@ cudaError_t launch_lora_tile(const void* x, const int32_t* adapter, const uint16
                    encode_tmap_2d_u8(&maps.base, base, row, uint64_t(M), row, 128, kTile, true) &&
                    encode_tmap_2d_u8(&maps.y, y, row, uint64_t(M), row, 128, kTile, true);
   if (!tma) maps.base = maps.y = maps.x;  // not used
-  const Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank};
+  const Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, xf};
   // CTAs of a tile of tokens: as many as run at once
   const int64_t tiles = (M + kTile - 1) / kTile;
   int cl = 1;

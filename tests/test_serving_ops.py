@@ -380,6 +380,36 @@ def test_lora_tiles(B, N, K, rank, lengths, yb):
 
 
 @gpu
+@pytest.mark.parametrize("yb", [True, False])
+@pytest.mark.parametrize("N,K,rank,lengths", [
+    (1537, 4096, 64, [1, 127, 128, 129, 5, 250, 384]), (3000, 2056, 128, [64, 17, 200, 16, 15, 1, 190]),
+    (2051, 4096, 24, [511, 1, 1, 1, 2, 30, 1600]), (2600, 5000, 8, [1000, 24, 4000]), (9000, 264, 96, [260, 140]),
+    (2560, 4096, 32, [200] + [1] * 140 + [300, 800]), (5000, 1000, 40, [8] * 160), (4104, 2048, 16, [3200])])
+def test_lora_tiles_fp32_activations(B, N, K, rank, lengths, yb):
+    """fp32 x enters the tensor cores as three bf16 terms (24 bits): the same bounds as everywhere."""
+    x, index, a, b, scale, base = tile_case(lengths, N, K, rank, yb, 9)
+    x = rng(len(index), K, 10).standard_normal(x.shape).astype(np.float32)
+    x[::7] *= np.float32(2.0 ** 40)  # rows of other magnitudes
+    x[3::7] *= np.float32(2.0 ** -40)
+    v = (x, index, a, b, scale, base)
+    M = len(index)
+    edges = np.cumsum([0] + lengths)
+    rows = np.unique(np.clip(np.concatenate([edges[:30], edges[:30] - 1, [0, 127, 128, 255, 256, M - 1],
+                                             rng(M).integers(0, M, 20)]), 0, M - 1))
+    y = run_lora(B, v, False, yb)
+    for size in (0, 3, 1):  # each magnitude by itself, for the 2-norm
+        some = rows[rows % 7 == size]
+        if len(some):
+            check_lora_rows(y, v, yb, some)
+    check_lora_rows(y, v, yb, rows)
+    assert torch.equal(run_lora(B, v, False, yb), y)
+    x[5, 3], x[M - 2, 7] = np.nan, np.inf
+    got = run_lora(B, v, False, yb)
+    rest = np.array([m for m in range(M) if m not in (5, M - 2)])
+    assert torch.equal(got[rest], y[rest])
+
+
+@gpu
 def test_lora_tiles_in_place_out_of_range_and_bad_rows(B):
     v = tile_case([300, 200, 400, 300], 2048, 3000, 64, True, 8)
     x, index, a, b, scale, base = v
