@@ -23,8 +23,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kParts = 8;      // CTAs of a cluster
-constexpr int64_t kTileTokens = 384;  // tokens and multiply-adds from which the tiles' kernel is launched as well
-constexpr double kTileWork = 1e8;
+constexpr int64_t kTileTokens = 257;  // tokens from which the tiles' kernel is launched as well
 constexpr int kGroup = 4;      // tokens that share the reads of an adapter
 
 struct Args {
@@ -219,12 +218,11 @@ cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, 
   const int per = M <= 256 ? 1 : kGroup;
   if ((M + per - 1) / per > 0x7fffffff / kParts) return cudaErrorInvalidConfiguration;
   Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, per, false};
-  // The tiles' kernel takes much the same time up to 1024 tokens, for a cluster has the fewer CTAs the more
-  // tiles there are; this one reads an adapter again for every group of four tokens and does M rank (K + N)
-  // multiply-adds on the CUDA cores.  Three adapters, scattered / tiles, us: 2560 -> 2560, rank 24: 512 tokens
-  // 25 / 27, 1024 (1.3e8) 44 / 27; 2560 -> 6912, rank 64: 256 tokens (1.6e8) 46 / 55, 512 74 / 54;
-  // 5120 -> 13824, rank 16: 256 tokens (8e7) 24 / 32, 512 (1.6e8) 35 / 32, 1024 65 / 33.
-  if (M >= kTileTokens && double(M) * rank * double(K + N) > kTileWork) {
+  // Up to 256 tokens may be as many requests, whose tiles would be left to this kernel after a launch of the
+  // other for nothing (64 tokens over 40 adapters, 5120 -> 13824, rank 32: 21 us without, 29 with it).  Beyond,
+  // three adapters, scattered / tiles, us: 257 tokens, 264 -> 264, rank 8 9 / 11; 2560 -> 2560, rank 24 15 / 13;
+  // 2560 -> 6912, rank 64 43 / 15; 1024 tokens 25 / 11, 44 / 15, 132 / 20.
+  if (M >= kTileTokens) {
     const cudaError_t e = launch_lora_tile(x, xt, adapter, a, b, scale, base, y, yt, M, N, K, adapters, rank, s);
     if (e != cudaSuccess && e != cudaErrorNotSupported) return e;
     g.tiles = e == cudaSuccess;

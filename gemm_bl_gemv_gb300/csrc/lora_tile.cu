@@ -2,7 +2,9 @@
 // tensor cores (tcgen05):
 //   y[m,n] = base[m,n] + scale[a] * sum_r B[a,n,r] (sum_k A[a,r,k] x[m,k]).
 //
-// A cluster of CL CTAs takes 128 tokens.  A run is a stretch of those tokens
+// A cluster of CL CTAs takes 128 tokens; while there are few, several clusters
+// do, each with the first product and a share of the outputs (512 tokens, 2560
+// -> 6912, rank 64: 16 us).  A run is a stretch of those tokens
 // with one adapter; a tile of more than kTileRuns runs is left to the kernel
 // for scattered tokens.
 //   1. Down: each CTA takes a part of K.  x (128 x 64 blocks) and the runs' A
@@ -12,7 +14,7 @@
 //      order through distributed shared memory, so the sum over K is never
 //      rounded below fp32.  fp32 x (two boxes of 32 columns) is turned by the
 //      epilogue warps, idle here, into three bf16 terms in TMEM, 24 bits
-//      (8192 tokens, 5120 -> 5120, rank 128: 114 us; 1894 on the CUDA cores).
+//      (8192 tokens, 5120 -> 5120, rank 128: 111 us; 1894 on the CUDA cores).
 //   2. The sums, times the adapter's scale, become bf16 operands in TMEM: two
 //      terms (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8,
 //      three (24 bits) for fp32 outputs.  (In shared memory it would take up to
@@ -27,7 +29,7 @@
 //      threads, a row's outputs by neighbouring lanes.
 //
 // Bound: HBM; base and y are 4 of the 5 bytes that an output costs at K = N / 2.7
-// and rank 64.  8192 tokens of 12 prompts, 2560 -> 6912, rank 64: 74.5 us, 41 us of
+// and rank 64.  8192 tokens of 12 prompts, 2560 -> 6912, rank 64: 73.3 us, 41 us of
 // them HBM's for 276 MB, 9 us the tensor core's (17 GFLOP with two terms).  The
 // CTAs of tiles with one run end after 45 us; the rest is the 12 tiles in which
 // one prompt ends and the next begins, with two products for every output tile.
@@ -124,7 +126,8 @@ struct Args {
   unsigned int* err;
   int64_t M, N, K, L;
   int rank;
-  bool xf;  // x is fp32
+  bool xf;     // x is fp32
+  int shares;  // clusters of 128 tokens: each forms the inner products, and a share of the outputs
 };
 
 struct Control {  // at control_at()
@@ -202,7 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   Control& c = *reinterpret_cast<Control*>(smem + control_at(g.rank, kN, g.xf));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t me = CL == 1 ? 0 : cluster_ctarank();
-  const int64_t m0 = int64_t(blockIdx.x / CL) * kTile;
+  const int cluster = int(blockIdx.x / CL), share = cluster % g.shares;
+  const int64_t m0 = int64_t(cluster / g.shares) * kTile;
+  const int first = share * CL + int(me), step = g.shares * CL;  // of this CTA's tiles of outputs
   const int size = int(min(int64_t(kTile), g.M - m0));
   volatile int* abort = &c.abort;
 
@@ -384,7 +389,25 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     sync_all();
     tc_fence_after();
 
-    // ---- 2. the operand: a thread 32 columns of a row at a time ----
+    // ---- 2. the operand ----
+    // A CTA adds up its rows of all parts, in rank order, and gives the sums to all (each reading all parts
+    // itself, a row in a thread, took 35 us in clusters of 8 at rank 64).
+    if (CL > 1) {
+      constexpr int kRows = kTile / CL;
+      const int quads = p.rp / 4;
+      for (int i = threadIdx.x; i < kRows * quads; i += kThreads) {
+        float* at = reinterpret_cast<float*>(smem + p.part_at) + (int(me) * kRows + i / quads) * p.part_row + i % quads * 4;
+        float4 f[CL];
+#pragma unroll
+        for (int q = 0; q < CL; ++q) f[q] = *reinterpret_cast<const float4*>(peer(at, q));
+#pragma unroll
+        for (int q = 1; q < CL; ++q) f[0].x += f[q].x, f[0].y += f[q].y, f[0].z += f[q].z, f[0].w += f[q].w;
+#pragma unroll
+        for (int q = 0; q < CL; ++q) *reinterpret_cast<float4*>(peer(at, q)) = f[0];
+      }
+      sync_all();
+    }
+    // then a thread 32 columns of a row at a time
     if (warp >= 2 && warp < 2 + kEpilogueWarps) {
       const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
       const int a = c.adapter[row];
@@ -394,19 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
         if (a >= 0) {
-          const float* src = reinterpret_cast<const float*>(smem + p.part_at) + row * p.part_row + k;
+          const float4* f = reinterpret_cast<const float4*>(smem + p.part_at) + (row * p.part_row + k) / 4;
 #pragma unroll
-          for (int q = 0; q < CL; ++q) {
-            const float4* f = reinterpret_cast<const float4*>(CL == 1 ? src : peer(src, q));
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (k + 4 * j < g.rank) {
-                const float4 f4 = f[j];
-                v[4 * j] += f4.x, v[4 * j + 1] += f4.y, v[4 * j + 2] += f4.z, v[4 * j + 3] += f4.w;
-              }
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= scale;
+          for (int j = 0; j < 8; ++j)
+            if (k + 4 * j < g.rank) {
+              const float4 f4 = f[j];
+              v[4 * j] = f4.x * scale, v[4 * j + 1] = f4.y * scale, v[4 * j + 2] = f4.z * scale, v[4 * j + 3] = f4.w * scale;
+            }
         }
         __syncwarp();
 #pragma unroll
@@ -425,13 +442,13 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     }
     tc_fence_before();
     fence_async_smem();  // the rings come over the partial sums
-    sync_all();  // and nobody reads the partial sums any more
+    __syncthreads();  // and nobody reads the partial sums any more
     tc_fence_after();
 
     // ---- 3. up ----
     if (warp == 0 && elect_one()) {
       Ring at(p.up);
-      for (int n = int(me); n < tiles && !*abort; n += CL) {
+      for (int n = first; n < tiles && !*abort; n += step) {
         for (Runs r(table); r.next();) {
           if (!r.has()) continue;
           const int a = c.adapter[r.t];
@@ -453,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           mbar_wait_bounded(&c.up_full[st], uint32_t(st < at.at ? at.round : at.round - 1) & 1u, nullptr);
     } else if (warp == 1 && elect_one()) {
       // a product for every tile and run with an adapter, in the order in which B comes
-      const int products = (tiles - int(me) + CL - 1) / CL * __popc(table.has);
+      const int products = (tiles - first + step - 1) / step * __popc(table.has);
       const uint32_t sbase = smem_addr(smem);
       bool dead = *abort;
       Ring at(p.up);
@@ -490,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
       const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
       float* turn = reinterpret_cast<float*>(smem + p.base_at) + (warp - 2) * 32 * kTurn;
       int it = 0, tl = 0;
-      for (int n = int(me); n < tiles; n += CL, ++tl) {
+      for (int n = first; n < tiles; n += step, ++tl) {
         const int bs = tl % kTiles, n0 = n * kN + part4 * kCols;
         // this thread's 64 bytes of base: 16-byte unit u of a 128-byte row at u ^ (row % 8)
         uint8_t* mine_row = smem + p.base_at + (bs * 2 + (part4 >> 1)) * kXBytes + row * 128;
@@ -576,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         if (two) tma_load_2d(dst + kXBytes, &base_map, n * 256 + 128, int(m0), &c.base_full[bs]);
       };
       int tl = 0, asked = 0;  // tiles stored, tiles asked for
-      for (; asked < kTiles && int(me) + asked * CL < tiles; ++asked) fetch(int(me) + asked * CL, asked);
-      for (int n = int(me); n < tiles; n += CL, ++tl) {
+      for (; asked < kTiles && first + asked * step < tiles; ++asked) fetch(first + asked * step, asked);
+      for (int n = first; n < tiles; n += step, ++tl) {
         const int bs = tl % kTiles;
         if (!*abort && !mbar_wait_bounded(&c.base_done[bs], uint32_t(tl / kTiles) & 1u, g.err)) *abort = 1;
         if (*abort) break;
@@ -586,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         if (int64_t(n) * kN + kHalf < g.N) tma_store_2d(&y_map, n * 256 + 128, int(m0), src + kXBytes);
         bulk_commit();
         bulk_wait_read();
-        if (n + kTiles * CL < tiles) fetch(n + kTiles * CL, bs), ++asked;
+        if (n + kTiles * step < tiles) fetch(n + kTiles * step, bs), ++asked;
       }
       // the CTA must not finish while a load still writes its shared memory
       for (int i = max(0, asked - kTiles); i < asked; ++i)
@@ -616,7 +633,7 @@ cudaError_t launch_tiles(const Maps& maps, const Args& g, cudaStream_t s) {
   const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(std::max(control_at(128, kN, false), control_at(128, kN, true)) + 1024));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((g.M + kTile - 1) / kTile * CL));
+  cfg.gridDim = dim3(unsigned((g.M + kTile - 1) / kTile * CL * g.shares));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = control_at(g.rank, kN, g.xf) + 1024;
   cfg.stream = s;
@@ -667,11 +684,14 @@ cudaError_t launch_lora_tile(const void* x, bl_dtype xt, const int32_t* adapter,
                    encode_tmap_2d_u8(&maps.base, base, row, uint64_t(M), row, 128, kTile, true) &&
                    encode_tmap_2d_u8(&maps.y, y, row, uint64_t(M), row, 128, kTile, true);
   if (!tma) maps.base = maps.y = maps.x;  // not used
-  const Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, xf};
+  Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, xf, 1};
   // CTAs of a tile of tokens: as many as run at once
   const int64_t tiles = (M + kTile - 1) / kTile;
   int cl = 1;
   while (cl < 8 && tiles <= clusters_at_once(2 * cl)) cl *= 2;
+  // and clusters of them, while each CTA has a tile of outputs
+  const int64_t out_tiles = (N + (yb ? 127 : 63)) / (yb ? 128 : 64);
+  g.shares = int(std::max<int64_t>(1, std::min(clusters_at_once(cl) / tiles, out_tiles / cl)));
   if (yb) return tma ? launch_tiles<true, true>(cl, maps, g, s) : launch_tiles<true, false>(cl, maps, g, s);
   return tma ? launch_tiles<false, true>(cl, maps, g, s) : launch_tiles<false, false>(cl, maps, g, s);
 }

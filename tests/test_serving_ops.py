@@ -410,6 +410,20 @@ def test_lora_tiles_fp32_activations(B, N, K, rank, lengths, yb):
 
 
 @gpu
+@pytest.mark.parametrize("xb,yb", [(True, True), (True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("N,K,rank,lengths", [
+    (8, 8, 8, [100, 1, 300]), (1, 8, 8, [257]), (33, 72, 16, [5, 400, 2]), (129, 264, 128, [256, 1, 1, 200]),
+    (64, 520, 40, [300]), (1000, 136, 56, [1] * 9 + [300]), (6912, 64, 64, [128] * 5)])
+def test_lora_tiles_of_small_shapes(B, N, K, rank, lengths, xb, yb):
+    """Parts of K without a block, clusters without a tile of outputs, boxes wider than the tensors."""
+    index = np.repeat([[0, 2, -1, 1, 0, 3, -1][i % 7] for i in range(len(lengths))], lengths)
+    v = lora_inputs(len(index), N, K, rank, 4, xb, yb, 12, index)
+    y = run_lora(B, v, xb, yb)
+    check_lora(y, v, yb)
+    assert torch.equal(run_lora(B, v, xb, yb), y)
+
+
+@gpu
 def test_lora_tiles_in_place_out_of_range_and_bad_rows(B):
     v = tile_case([300, 200, 400, 300], 2048, 3000, 64, True, 8)
     x, index, a, b, scale, base = v
