@@ -15,6 +15,8 @@
 // dependent step of one to three us (one token, 2560 -> 6912, rank 16: 5.1 us;
 // 64 tokens over 40 adapters, 5120 -> 13824, rank 32: 20.6 us, a third of HBM's
 // rate for the 47 MB that they need).
+#include <algorithm>
+
 #include "bl_internal.h"
 #include "lora.cuh"
 
@@ -24,6 +26,8 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kParts = 8;      // CTAs of a cluster
 constexpr int64_t kTileTokens = 257;  // tokens from which the tiles' kernel is launched as well
+constexpr int kPerSm = 4;      // CTAs of an SM
+constexpr int kBatch = 256;    // tiles looked at together
 constexpr int kGroup = 4;      // tokens that share the reads of an adapter
 
 struct Args {
@@ -43,6 +47,60 @@ struct Args {
 struct __align__(16) Shared {
   float part[2][kGroup][128];  // this CTA's share of the inner products; every second run uses the other half
   float low[kGroup][128];
+  uint32_t scattered[kBatch / 32];  // bit i: tile batch + i is this kernel's
+};
+
+// The groups of tokens in tiles of many runs, of which this cluster takes every `clusters`-th: the other kernel has
+// the rest, and a cluster for each of them, with nothing to do, would take longer than looking (8192 tokens: 10 us).
+struct Scattered {
+  const Args& g;
+  Shared& sh;
+  int clusters, group, word;
+  uint32_t bits;
+  int64_t batch, tile;
+  __device__ __forceinline__ Scattered(const Args& args, Shared& shared, int cluster, int n)
+      : g(args), sh(shared), clusters(n), group(cluster - n), word(kBatch / 32), bits(0), batch(-kBatch), tile(-1) {}
+  __device__ void look() {  // a warp a tile
+    const int lane = threadIdx.x & 31;
+    __syncthreads();
+    if (threadIdx.x < kBatch / 32) sh.scattered[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < kBatch && (batch + i) * kTile < g.M; i += kWarps) {
+      int starts = 0;
+#pragma unroll
+      for (int j = 0; j < kTile / 32; ++j) {
+        const int64_t t = (batch + i) * kTile + 32 * j + lane;
+        const bool start = t < g.M && ((j == 0 && lane == 0) || adapter_of(g.adapter, t, g.L) != adapter_of(g.adapter, t - 1, g.L));
+        starts += __popc(__ballot_sync(0xffffffffu, start));
+      }
+      if (lane == 0 && starts > kTileRuns) atomicOr(&sh.scattered[i >> 5], 1u << (i & 31));
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ bool next_tile() {
+    while (bits == 0) {
+      if (++word < kBatch / 32) {
+        bits = sh.scattered[word];
+        continue;
+      }
+      batch += kBatch;
+      if (batch * kTile >= g.M) return false;
+      look();
+      word = -1;
+    }
+    tile = batch + word * 32 + __ffs(bits) - 1;
+    bits &= bits - 1;
+    return true;
+  }
+  // The first token of the next group, -1 behind the last.
+  __device__ __forceinline__ int64_t next() {
+    constexpr int kGroups = kTile / kGroup;
+    group += clusters;
+    if (tile < 0 && !next_tile()) return -1;
+    for (; group >= kGroups; group -= kGroups)
+      if (!next_tile()) return -1;
+    return tile * kTile + group * kGroup;
+  }
 };
 
 // This CTA's share of the inner products of NT tokens from m on with A[l].  A
@@ -119,21 +177,21 @@ __device__ __forceinline__ void up(const Args& g, const float (*low)[128], int64
 }
 
 template <bool XB, bool YB>
-__global__ void __launch_bounds__(kThreads, 4) lora_token_kernel(const Args g) {
+__global__ void __launch_bounds__(kThreads, kPerSm) lora_token_kernel(const Args g) {
   __shared__ Shared sh;
   const uint32_t me = cluster_ctarank();
-  const int64_t first = int64_t(blockIdx.x / kParts) * g.per;
+  const int cluster = int(blockIdx.x / kParts);
   if (!g.tiles) pdl_wait();  // otherwise the tiles' kernel has waited, and runs beside this one
-  bool mine = true;
-  if (g.tiles) {  // the tile's runs
-    const int64_t t = first / kTile * kTile + threadIdx.x;
-    const bool start = threadIdx.x < kTile && t < g.M &&
-                       (threadIdx.x == 0 || adapter_of(g.adapter, t, g.L) != adapter_of(g.adapter, t - 1, g.L));
-    mine = __syncthreads_count(start) > kTileRuns;
-  }
+  Scattered units(g, sh, cluster, int(gridDim.x / kParts));
   const int64_t n_part = (g.N + kParts - 1) / kParts, n0 = int64_t(me) * n_part, n1 = min(n0 + n_part, g.N);
   int run = 0;
-  for (int64_t m = first; mine && m < min(first + g.per, g.M);) {
+  int64_t m = g.tiles ? units.next() : int64_t(cluster) * g.per, last = min(m + g.per, g.M);
+  while (m >= 0) {
+    if (m >= last) {
+      m = g.tiles ? units.next() : -1;
+      last = min(m + g.per, g.M);
+      continue;
+    }
     // the first of the tokens with this adapter among four aligned ones, and how many follow
     const int l = adapter_of(g.adapter, m, g.L);
     const int64_t end = min(g.M, (m / kGroup + 1) * kGroup);
@@ -196,7 +254,9 @@ __global__ void __launch_bounds__(kThreads, 4) lora_token_kernel(const Args g) {
 template <bool XB, bool YB>
 cudaError_t launch_tokens(const Args& g, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((g.M + g.per - 1) / g.per * kParts));
+  int64_t clusters = (g.M + g.per - 1) / g.per;
+  if (g.tiles) clusters = std::min<int64_t>(clusters, kPerSm * clusters_at_once(kParts));  // they look for their tokens
+  cfg.gridDim = dim3(unsigned(clusters * kParts));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

@@ -49,6 +49,7 @@ constexpr int kWarps = 3 + kEpilogueWarps, kThreads = 32 * kWarps;  // x, A and 
 constexpr int kStages = 5;                 // K blocks of 64 in flight at most
 constexpr int kFloatStages = 3;            // of fp32 x, whose terms take 96 TMEM columns each
 constexpr int kUp = 6;                     // tiles of B in flight at most
+constexpr int kMostHelped = 256;           // tiles of tokens among which helpers look for theirs
 constexpr int kTiles = 4;                  // tiles of base in flight
 constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; half a tile of base
 constexpr int kAcc = 2, kAccCols = 128;    // accumulators
@@ -128,12 +129,15 @@ struct Args {
   int rank;
   bool xf;     // x is fp32
   int shares;  // clusters of 128 tokens: each forms the inner products, and a share of the outputs
+  int tiles;   // of 128 tokens
+  int helpers; // clusters beyond tiles * shares: each takes half of the outputs of a tile with several runs
 };
 
 struct Control {  // at control_at()
   uint64_t full[kStages], empty[kStages], terms[kFloatStages], sums, drained, up_full[kUp], up_empty[kUp], out_full[kAcc], out_empty[kAcc];
   uint64_t base_full[kTiles], base_done[kTiles];
   uint32_t tmem, starts[4], used[4];  // used: runs that have an adapter
+  uint32_t several[kMostHelped / 32]; // bit t: tile t has several runs, and is this kernel's
   int abort;
   int adapter[kTile];  // of each token, -1: none
 };
@@ -191,6 +195,28 @@ struct Runs {
 // gives them one decision (the flag may be raised between two lanes' reads).
 __device__ __forceinline__ bool warp_agrees(bool c) { return __all_sync(0xffffffffu, c) != 0; }
 
+// The tiles of tokens with several runs, at most kTileRuns (a warp a tile at a time), by the whole CTA.
+__device__ __forceinline__ void find_several(const Args& g, uint32_t (&several)[kMostHelped / 32]) {
+  const int lane = threadIdx.x & 31;
+  __syncthreads();
+  if (threadIdx.x < kMostHelped / 32) several[threadIdx.x] = 0;
+  __syncthreads();
+  for (int tile = threadIdx.x >> 5; tile < g.tiles; tile += kWarps) {
+    int starts = 0, used = 0;
+#pragma unroll
+    for (int j = 0; j < kTile / 32; ++j) {
+      const int64_t t = int64_t(tile) * kTile + 32 * j + lane;
+      const int a = t < g.M ? adapter_of(g.adapter, t, g.L) : -1;
+      const int before = t < g.M && (j > 0 || lane > 0) ? adapter_of(g.adapter, t - 1, g.L) : -2;
+      const uint32_t start = __ballot_sync(0xffffffffu, t < g.M && a != before);
+      starts += __popc(start);
+      used += __popc(start & __ballot_sync(0xffffffffu, a >= 0));
+    }
+    if (lane == 0 && used > 1 && starts <= kTileRuns) atomicOr(&several[tile >> 5], 1u << (tile & 31));
+  }
+  __syncthreads();
+}
+
 // YB: base and y are bf16.  TMA: they come and go by TMA.
 template <int CL, bool YB, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_constant__ CUtensorMap xmap,
@@ -205,10 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   Control& c = *reinterpret_cast<Control*>(smem + control_at(g.rank, kN, g.xf));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t me = CL == 1 ? 0 : cluster_ctarank();
-  const int cluster = int(blockIdx.x / CL), share = cluster % g.shares;
-  const int64_t m0 = int64_t(cluster / g.shares) * kTile;
-  const int first = share * CL + int(me), step = g.shares * CL;  // of this CTA's tiles of outputs
-  const int size = int(min(int64_t(kTile), g.M - m0));
+  const int cluster = int(blockIdx.x / CL), helper = cluster - g.tiles * g.shares;  // helper >= 0: one of them
   volatile int* abort = &c.abort;
 
   if (warp == 1) {
@@ -235,6 +258,28 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
   }
   pdl_wait();
   pdl_launch_dependents();  // the kernel for the other tiles, which ends after this one
+  int tile = cluster / g.shares;
+  int first = cluster % g.shares * CL + int(me), step = g.shares * CL;  // of this CTA's tiles of outputs
+  bool idle = false;
+  if (helper >= 0) {  // the helper-th tile of several runs
+    find_several(g, c.several);
+    int left = helper;
+    tile = -1;
+    for (int w = 0; w < kMostHelped / 32 && tile < 0; ++w) {
+      uint32_t bits = c.several[w];
+      if (left >= __popc(bits)) {
+        left -= __popc(bits);
+        continue;
+      }
+      for (; left > 0; --left) bits &= bits - 1;
+      tile = w * 32 + __ffs(bits) - 1;
+    }
+    idle = tile < 0;
+    tile = max(tile, 0);
+    first = CL + int(me), step = 2 * CL;
+  }
+  const int64_t m0 = int64_t(tile) * kTile;
+  const int size = int(min(int64_t(kTile), g.M - m0));
   if (threadIdx.x < kTile) {
     const int t = threadIdx.x;
     const int a = t < size ? adapter_of(g.adapter, m0 + t, g.L) : -1;
@@ -243,15 +288,22 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     const uint32_t b = __ballot_sync(0xffffffffu, t < size && a != before);
     const uint32_t u = __ballot_sync(0xffffffffu, t < size && a != before && a >= 0);
     if (lane == 0) c.starts[warp] = b, c.used[warp] = u;
-    if (me == 0 && t < size && g.adapter[m0 + t] >= g.L && g.err) atomicOr(g.err, BL_DEVERR_RANGE);
+    if (me == 0 && first < CL && t < size && g.adapter[m0 + t] >= g.L && g.err) atomicOr(g.err, BL_DEVERR_RANGE);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
   const int starts = __popc(c.starts[0]) + __popc(c.starts[1]) + __popc(c.starts[2]) + __popc(c.starts[3]);
-  const bool mine = starts <= kTileRuns;
+  const bool mine = starts <= kTileRuns && !idle;
   const RunTable table(c.starts, c.adapter, size);
+  if (g.helpers > 0 && helper < 0 && mine && __popc(table.has) > 1) {  // does it have a helper?
+    find_several(g, c.several);
+    int before = 0;
+    for (int w = 0; w < tile / 32; ++w) before += __popc(c.several[w]);
+    before += __popc(c.several[tile / 32] & ((1u << (tile & 31)) - 1));
+    if (before < g.helpers) step = 2 * CL;
+  }
 
   const Plan p = make_plan(g.rank, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]), g.xf);
 
@@ -633,7 +685,7 @@ cudaError_t launch_tiles(const Maps& maps, const Args& g, cudaStream_t s) {
   const cudaError_t e = raise_smem_cap(lora_tile_kernel<CL, YB, TMA>, dev, int(std::max(control_at(128, kN, false), control_at(128, kN, true)) + 1024));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((g.M + kTile - 1) / kTile * CL * g.shares));
+  cfg.gridDim = dim3(unsigned((int64_t(g.tiles) * g.shares + g.helpers) * CL));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = control_at(g.rank, kN, g.xf) + 1024;
   cfg.stream = s;
@@ -684,7 +736,7 @@ cudaError_t launch_lora_tile(const void* x, bl_dtype xt, const int32_t* adapter,
                    encode_tmap_2d_u8(&maps.base, base, row, uint64_t(M), row, 128, kTile, true) &&
                    encode_tmap_2d_u8(&maps.y, y, row, uint64_t(M), row, 128, kTile, true);
   if (!tma) maps.base = maps.y = maps.x;  // not used
-  Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, xf, 1};
+  Args g{adapter, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, xf, 1, 0, 0};
   // CTAs of a tile of tokens: as many as run at once
   const int64_t tiles = (M + kTile - 1) / kTile;
   int cl = 1;
@@ -692,6 +744,10 @@ cudaError_t launch_lora_tile(const void* x, bl_dtype xt, const int32_t* adapter,
   // and clusters of them, while each CTA has a tile of outputs
   const int64_t out_tiles = (N + (yb ? 127 : 63)) / (yb ? 128 : 64);
   g.shares = int(std::max<int64_t>(1, std::min(clusters_at_once(cl) / tiles, out_tiles / cl)));
+  // A tile with several runs takes a product of each for every output tile: idle SMs help with such tiles.
+  g.tiles = int(tiles);
+  if (g.shares == 1 && tiles <= kMostHelped && out_tiles >= 2 * cl)
+    g.helpers = int(std::min<int64_t>(std::max<int64_t>(clusters_at_once(cl) - tiles, 0), tiles));
   if (yb) return tma ? launch_tiles<true, true>(cl, maps, g, s) : launch_tiles<true, false>(cl, maps, g, s);
   return tma ? launch_tiles<false, true>(cl, maps, g, s) : launch_tiles<false, false>(cl, maps, g, s);
 }

@@ -424,6 +424,33 @@ def test_lora_tiles_of_small_shapes(B, N, K, rank, lengths, xb, yb):
 
 
 @gpu
+@pytest.mark.parametrize("yb", [True, False])
+@pytest.mark.parametrize("M,longest", [(3000, 200), (4500, 400), (6000, 90), (9600, 300), (10000, 2000), (13000, 60),
+                                       (25000, 500)])
+def test_lora_tiles_with_helpers(B, M, longest, yb):
+    """Idle SMs take half of the outputs of tiles with several runs: fewer and more of them than helpers."""
+    lengths = rng(M, longest).integers(1, longest + 1, M // 4 + 1)
+    index = np.repeat([[0, 2, -1, 1, 0, 3, -1][i % 7] for i in range(len(lengths))], lengths)[:M]
+    v = lora_inputs(M, 1032, 136, 16, 4, True, yb, 13, index)
+    y = run_lora(B, v, True, yb)
+    check_lora(y, v, yb)
+    x, index, a, b, scale, base = v
+    bf = torch.bfloat16
+    at = dev(base, bf if yb else None)
+    assert torch.equal(B.bl_lora_add(dev(x, bf), dev(index), dev(a, bf), dev(b, bf), dev(scale), at, y=at), y)
+
+
+@gpu
+@pytest.mark.parametrize("xb", [True, False])
+def test_lora_scattered_tiles_far_behind_long_runs(B, xb):
+    """Tiles of many runs among more than 256 tiles, the first, some in the middle and the last ones."""
+    lengths = [1] * 200 + [20000] + [3] * 100 + [12500] + [2] * 301
+    index = np.repeat([[0, 2, -1, 1, 0, 3, -1][i % 7] for i in range(len(lengths))], lengths)
+    v = lora_inputs(len(index), 72, 64, 16, 4, xb, True, 14, index)
+    check_lora(run_lora(B, v, xb, True), v, True)
+
+
+@gpu
 def test_lora_tiles_in_place_out_of_range_and_bad_rows(B):
     v = tile_case([300, 200, 400, 300], 2048, 3000, 64, True, 8)
     x, index, a, b, scale, base = v
