@@ -41,7 +41,6 @@ struct Args {
   int64_t M, N, K, L;
   int R;
   int per;     // tokens of a cluster
-  bool tiles;  // tiles of few runs are another kernel's
 };
 
 struct __align__(16) Shared {
@@ -176,19 +175,20 @@ __device__ __forceinline__ void up(const Args& g, const float (*low)[128], int64
   }
 }
 
-template <bool XB, bool YB>
+// TILES: tiles of few runs are another kernel's.
+template <bool XB, bool YB, bool TILES>
 __global__ void __launch_bounds__(kThreads, kPerSm) lora_token_kernel(const Args g) {
   __shared__ Shared sh;
   const uint32_t me = cluster_ctarank();
   const int cluster = int(blockIdx.x / kParts);
-  if (!g.tiles) pdl_wait();  // otherwise the tiles' kernel has waited, and runs beside this one
+  if (!TILES) pdl_wait();  // otherwise the tiles' kernel has waited, and runs beside this one
   Scattered units(g, sh, cluster, int(gridDim.x / kParts));
   const int64_t n_part = (g.N + kParts - 1) / kParts, n0 = int64_t(me) * n_part, n1 = min(n0 + n_part, g.N);
   int run = 0;
-  int64_t m = g.tiles ? units.next() : int64_t(cluster) * g.per, last = min(m + g.per, g.M);
+  int64_t m = TILES ? units.next() : int64_t(cluster) * g.per, last = min(m + g.per, g.M);
   while (m >= 0) {
     if (m >= last) {
-      m = g.tiles ? units.next() : -1;
+      m = TILES ? units.next() : -1;
       last = min(m + g.per, g.M);
       continue;
     }
@@ -247,15 +247,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) lora_token_kernel(const Args
   // another CTA may still read this one's share (after two runs the barrier between them has settled it)
   __syncwarp();
   if (run > 0) cluster_sync();
-  if (g.tiles && blockIdx.x == 0) pdl_wait();  // this kernel's end is the call's end
+  if (TILES && blockIdx.x == 0) pdl_wait();  // this kernel's end is the call's end
   pdl_launch_dependents();
 }
 
-template <bool XB, bool YB>
+template <bool XB, bool YB, bool TILES>
 cudaError_t launch_tokens(const Args& g, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   int64_t clusters = (g.M + g.per - 1) / g.per;
-  if (g.tiles) clusters = std::min<int64_t>(clusters, kPerSm * clusters_at_once(kParts));  // they look for their tokens
+  if (TILES) clusters = std::min<int64_t>(clusters, kPerSm * clusters_at_once(kParts));  // they look for their tokens
   cfg.gridDim = dim3(unsigned(clusters * kParts));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
@@ -265,8 +265,12 @@ cudaError_t launch_tokens(const Args& g, cudaStream_t s) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = overlap_enabled() || g.tiles ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, lora_token_kernel<XB, YB>, g);
+  cfg.numAttrs = overlap_enabled() || TILES ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, lora_token_kernel<XB, YB, TILES>, g);
+}
+template <bool XB, bool YB>
+cudaError_t launch_tokens(bool tiles, const Args& g, cudaStream_t s) {
+  return tiles ? launch_tokens<XB, YB, true>(g, s) : launch_tokens<XB, YB, false>(g, s);
 }
 
 }  // namespace
@@ -277,7 +281,8 @@ cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, 
   // A cluster per token while that is at most a few per SM; beyond, per four.
   const int per = M <= 256 ? 1 : kGroup;
   if ((M + per - 1) / per > 0x7fffffff / kParts) return cudaErrorInvalidConfiguration;
-  Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, per, false};
+  Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, per};
+  bool tiles = false;
   // Up to 256 tokens may be as many requests, whose tiles would be left to this kernel after a launch of the
   // other for nothing (64 tokens over 40 adapters, 5120 -> 13824, rank 32: 21 us without, 29 with it).  Beyond,
   // three adapters, scattered / tiles, us: 257 tokens, 264 -> 264, rank 8 9 / 11; 2560 -> 2560, rank 24 15 / 13;
@@ -285,11 +290,11 @@ cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, 
   if (M >= kTileTokens) {
     const cudaError_t e = launch_lora_tile(x, xt, adapter, a, b, scale, base, y, yt, M, N, K, adapters, rank, s);
     if (e != cudaSuccess && e != cudaErrorNotSupported) return e;
-    g.tiles = e == cudaSuccess;
+    tiles = e == cudaSuccess;
   }
   const bool xb = xt == BL_BF16, yb = yt == BL_BF16;
-  if (xb) return yb ? launch_tokens<true, true>(g, s) : launch_tokens<true, false>(g, s);
-  return yb ? launch_tokens<false, true>(g, s) : launch_tokens<false, false>(g, s);
+  if (xb) return yb ? launch_tokens<true, true>(tiles, g, s) : launch_tokens<true, false>(tiles, g, s);
+  return yb ? launch_tokens<false, true>(tiles, g, s) : launch_tokens<false, false>(tiles, g, s);
 }
 
 }  // namespace bl

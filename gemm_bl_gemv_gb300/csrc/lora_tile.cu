@@ -14,7 +14,7 @@
 //      order through distributed shared memory, so the sum over K is never
 //      rounded below fp32.  fp32 x (two boxes of 32 columns) is turned by the
 //      epilogue warps, idle here, into three bf16 terms in TMEM, 24 bits
-//      (8192 tokens, 5120 -> 5120, rank 128: 111 us; 1894 on the CUDA cores).
+//      (8192 tokens, 5120 -> 5120, rank 128: 100 us; 1894 on the CUDA cores).
 //   2. The sums, times the adapter's scale, become bf16 operands in TMEM: two
 //      terms (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8,
 //      three (24 bits) for fp32 outputs.  (In shared memory it would take up to
@@ -28,11 +28,13 @@
 //      (N * element size not a multiple of 16) are read and written by the
 //      threads, a row's outputs by neighbouring lanes.
 //
+// A tile with several runs takes a product of each for every output tile, and
+// so nearly twice as long; where SMs are left, a second cluster takes half of
+// its outputs (65.5 -> 57.7 us in the case below).
+//
 // Bound: HBM; base and y are 4 of the 5 bytes that an output costs at K = N / 2.7
-// and rank 64.  8192 tokens of 12 prompts, 2560 -> 6912, rank 64: 73.3 us, 41 us of
-// them HBM's for 276 MB, 9 us the tensor core's (17 GFLOP with two terms).  The
-// CTAs of tiles with one run end after 45 us; the rest is the 12 tiles in which
-// one prompt ends and the next begins, with two products for every output tile.
+// and rank 64.  8192 tokens of 12 prompts, 2560 -> 6912, rank 64: 57.7 us, 70 % of
+// the copy rate for 276 MB, 9 us the tensor core's (17 GFLOP with two terms).
 // One run's rows are not masked out of the other's product (one sum for both):
 // an infinite weight of one request's adapter must not reach another's outputs.
 #include <algorithm>
