@@ -9,12 +9,16 @@
 // for scattered tokens.
 //   1. Down: each CTA takes a part of K.  x (128 x 64 blocks) and the runs' A
 //      (rank x 64, up to two runs at once) come by TMA through a ring; the
-//      tensor core forms the 128 x rank product in TMEM, and the rows of the
-//      run go to shared memory as fp32.  The CTAs add their parts up in rank
-//      order through distributed shared memory, so the sum over K is never
-//      rounded below fp32.  fp32 x (two boxes of 32 columns) is turned by the
-//      epilogue warps, idle here, into three bf16 terms in TMEM, 24 bits
-//      (8192 tokens, 5120 -> 5120, rank 128: 100 us; 1894 on the CUDA cores).
+//      tensor core forms the 128 x rank product in TMEM.  It cuts its sums off
+//      instead of rounding them, always towards zero: a bias of 1.8e-8 of the sum
+//      for every 16 products of K, 1.6e-5 at K = 13824.  So the epilogue warps take
+//      the sums over a few blocks (kChunk, kFloatChunk) and add them up in
+//      registers, in fp32 to nearest, while the next ones are formed in a second
+//      accumulator: 4e-7 at any K.  The rows of the run go to shared memory, and
+//      the CTAs add their parts up in rank order through distributed shared memory.
+//      fp32 x (two boxes of 32 columns) is turned by the epilogue warps into three
+//      bf16 terms in TMEM, 24 bits (8192 tokens, 5120 -> 5120, rank 128: 107 us, 99
+//      in one sum; 1894 on the CUDA cores).
 //   2. The sums, times the adapter's scale, become bf16 operands in TMEM: two
 //      terms (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8,
 //      three (24 bits) for fp32 outputs.  (In shared memory it would take up to
@@ -55,6 +59,7 @@ constexpr int kMostHelped = 256;           // tiles of tokens among which helper
 constexpr int kTiles = 4;                  // tiles of base in flight
 constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; half a tile of base
 constexpr int kAcc = 2, kAccCols = 128;    // accumulators
+constexpr int kChunk = 4, kFloatChunk = 2; // blocks of K, of bf16 and fp32 x, whose sums the tensor core forms: 16 and 24 additions
 constexpr uint32_t kOperand = 256;         // TMEM column of the operand's first term, three of 64 at most
 constexpr uint32_t kTermsOfX = 128;        // TMEM column of the terms of fp32 x, three of 32 per stage
 constexpr uint32_t kTmemCols = 512;
@@ -136,7 +141,7 @@ struct Args {
 };
 
 struct Control {  // at control_at()
-  uint64_t full[kStages], empty[kStages], terms[kFloatStages], sums, drained, up_full[kUp], up_empty[kUp], out_full[kAcc], out_empty[kAcc];
+  uint64_t full[kStages], empty[kStages], terms[kFloatStages], sums[kAcc], drained[kAcc], up_full[kUp], up_empty[kUp], out_full[kAcc], out_empty[kAcc];
   uint64_t base_full[kTiles], base_done[kTiles];
   uint32_t tmem, starts[4], used[4];  // used: runs that have an adapter
   uint32_t several[kMostHelped / 32]; // bit t: tile t has several runs, and is this kernel's
@@ -227,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
                                                              const __grid_constant__ CUtensorMap base_map,
                                                              const __grid_constant__ CUtensorMap y_map, const Args g) {
   constexpr int kTerms = YB ? 2 : 3;
+  const int chunk = g.xf ? kFloatChunk : kChunk;
   constexpr int kN = YB ? 128 : 64;  // outputs of an up tile
   constexpr int kHalf = kN / 2;      // 128 bytes of them
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -245,10 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     c.abort = 0;
     for (int i = 0; i < kStages; ++i) mbar_init(&c.full[i], 1), mbar_init(&c.empty[i], 1);
     for (int i = 0; i < kFloatStages; ++i) mbar_init(&c.terms[i], kEpilogueWarps);
-    mbar_init(&c.sums, 1);
-    mbar_init(&c.drained, kEpilogueWarps);
     for (int i = 0; i < kUp; ++i) mbar_init(&c.up_full[i], 1), mbar_init(&c.up_empty[i], 1);
     for (int i = 0; i < kAcc; ++i) {
+      mbar_init(&c.sums[i], 1);
+      mbar_init(&c.drained[i], kEpilogueWarps);
       mbar_init(&c.out_full[i], 1);
       mbar_init(&c.out_empty[i], kEpilogueWarps);
     }
@@ -322,6 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     const int blocks = int((g.K + 63) / 64), per = (blocks + CL - 1) / CL;
     const int k0 = min(int(me) * per, blocks), k1 = min(k0 + per, blocks);
     const int tiles = int((g.N + kN - 1) / kN);
+    // TMEM beside the first accumulator: the terms of fp32 x, of three blocks or two, and the second accumulator
+    const int term_sets = p.group * p.rp <= int(kTmemCols - kTermsOfX - kFloatStages * 96) ? kFloatStages : kFloatStages - 1;
+    const uint32_t second = g.xf ? kTermsOfX + uint32_t(term_sets) * 96 : kAccCols;
     // ---- 1. down ----
     // Runs with an adapter, in groups whose A blocks go through the ring beside one block of x.
     if (warp == 0 && elect_one()) {
@@ -346,97 +355,120 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         if (at.round > 0 || st < at.at)
           mbar_wait_bounded(&c.full[st], uint32_t(st < at.at ? at.round : at.round - 1) & 1u, nullptr);
     } else if (warp == 1 && elect_one()) {
-      Ring at(p.stages);
-      int turn = 0;
+      Ring at(p.stages), terms(term_sets), sum(kAcc);
       const uint32_t sbase = smem_addr(smem);
       Runs r(table);
-      for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0; ++turn) {
-        if (turn > 0 && !*abort && !mbar_wait_bounded(&c.drained, uint32_t(turn - 1) & 1u, g.err)) *abort = 1;
-        tc_fence_after();
-        for (int kb = k0; kb < k1; ++kb, at.next()) {
-          const int st = at.at;
-          if (!*abort && !mbar_wait_bounded(&c.full[st], at.parity(), g.err)) *abort = 1;
+      for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0;)
+        for (int kb = k0; kb < k1; sum.next()) {
+          if (sum.round > 0 && !*abort && !mbar_wait_bounded(&c.drained[sum.at], sum.free_parity(), g.err)) *abort = 1;
           tc_fence_after();
-          const uint32_t xa = sbase + st * p.stage;
-          // the runs' A blocks lie one behind the other: one product for all
-          if (g.xf) {
-            if (!*abort && !mbar_wait_bounded(&c.terms[st], at.parity(), g.err)) *abort = 1;
-            tc_fence_after();
-            if (!*abort)
-              for (int t = 0; t < 3; ++t)
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  umma_f16_ta(tmem, tmem + kTermsOfX + uint32_t(st * 96 + t * 32 + ks * 8),
-                              umma_desc_sw128(xa + p.x_bytes + ks * 32), idesc(n * p.rp), kb > k0 || t > 0 || ks > 0);
-          } else if (!*abort) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_f16(tmem, umma_desc_sw128(xa + ks * 32), umma_desc_sw128(xa + kXBytes + ks * 32), idesc(n * p.rp),
-                       kb > k0 || ks > 0);
-          }
-          umma_commit(&c.empty[st]);
-        }
-        umma_commit(&c.sums);
-      }
-    } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
-      float* part = reinterpret_cast<float*>(smem + p.part_at);
-      const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
-      int turn = 0;
-      Ring at(p.stages);
-      Runs r(table);
-      for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0; ++turn) {
-        if (g.xf)  // the terms of x, 16 columns of a row in a thread: unit u of a 128-byte row is at u ^ (row % 8)
-          for (int kb = k0; kb < k1; ++kb, at.next()) {
+          const uint32_t da = tmem + uint32_t(sum.at) * second;
+          for (const int first_kb = kb, end = min(kb + chunk, k1); kb < end; ++kb, at.next(), terms.next()) {
             const int st = at.at;
             if (!*abort && !mbar_wait_bounded(&c.full[st], at.parity(), g.err)) *abort = 1;
             tc_fence_after();
-            float v[16];
-            const uint8_t* mine_row = smem + st * p.stage + (part4 >> 1) * kXBytes + row * 128;
+            const uint32_t xa = sbase + st * p.stage;
+            // the runs' A blocks lie one behind the other: one product for all
+            if (g.xf) {
+              if (!*abort && !mbar_wait_bounded(&c.terms[terms.at], terms.parity(), g.err)) *abort = 1;
+              tc_fence_after();
+              if (!*abort)
+                for (int t = 2; t >= 0; --t)  // the smallest first, as in the second product
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float4 f = *reinterpret_cast<const float4*>(mine_row + (((part4 & 1) * 4 + u) ^ (row & 7)) * 16);
-              v[4 * u] = f.x, v[4 * u + 1] = f.y, v[4 * u + 2] = f.z, v[4 * u + 3] = f.w;
+                  for (int ks = 0; ks < 4; ++ks)
+                    umma_f16_ta(da, tmem + kTermsOfX + uint32_t(terms.at * 96 + t * 32 + ks * 8),
+                                umma_desc_sw128(xa + p.x_bytes + ks * 32), idesc(n * p.rp), kb > first_kb || t < 2 || ks > 0);
+            } else if (!*abort) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                umma_f16(da, umma_desc_sw128(xa + ks * 32), umma_desc_sw128(xa + kXBytes + ks * 32), idesc(n * p.rp),
+                         kb > first_kb || ks > 0);
             }
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < 3; ++t) {
-              uint32_t w[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                w[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
-                v[2 * j] -= __uint_as_float(w[j] << 16);
-                v[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
-              }
-              tmem_st8(tmem + kTermsOfX + uint32_t(st * 96 + t * 32 + part4 * 8) + (uint32_t(quarter * 32) << 16), w);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c.terms[st]);
+            umma_commit(&c.empty[st]);
           }
-        if (!*abort && !mbar_wait_bounded(&c.sums, uint32_t(turn) & 1u, g.err)) *abort = 1;
-        tc_fence_after();
-        const bool ok = warp_agrees(!*abort);  // and the warp is converged for tcgen05.ld
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (j >= n) break;
-          if (!ok || max(from[j], quarter * 32) >= min(to[j], quarter * 32 + 32)) continue;
-          for (int col = part4 * 16; col < p.rp; col += 64) {
-            uint32_t v[16];
-            __syncwarp();
-            tmem_ld16(tmem + uint32_t(j * p.rp) + (uint32_t(quarter * 32) << 16) + uint32_t(col), v);
-            tmem_ld_wait();
-            if (row >= from[j] && row < to[j]) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<uint4*>(part + row * p.part_row + col + 4 * q) =
-                    k1 > k0 ? make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_uint4(0, 0, 0, 0);
-            }
-          }
+          umma_commit(&c.sums[sum.at]);
         }
+    } else if (warp >= 2 && warp < 2 + kEpilogueWarps) {
+      float* part = reinterpret_cast<float*>(smem + p.part_at);
+      const int quarter = warp & 3, part4 = (warp - 2) >> 2, row = quarter * 32 + lane;
+      Ring at(p.stages), terms(term_sets), used(p.stages), sum(kAcc);
+      // the terms of x, 16 columns of a row in a thread: unit u of a 128-byte row is at u ^ (row % 8)
+      auto make_terms = [&] {
+        const int st = at.at;
+        if (!*abort && !mbar_wait_bounded(&c.full[st], at.parity(), g.err)) *abort = 1;
+        if (terms.round > 0) {  // the products with the terms that were there
+          if (!*abort && !mbar_wait_bounded(&c.empty[used.at], used.parity(), g.err)) *abort = 1;
+          used.next();
+        }
+        tc_fence_after();
+        float v[16];
+        const uint8_t* mine_row = smem + st * p.stage + (part4 >> 1) * kXBytes + row * 128;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 f = *reinterpret_cast<const float4*>(mine_row + (((part4 & 1) * 4 + u) ^ (row & 7)) * 16);
+          v[4 * u] = f.x, v[4 * u + 1] = f.y, v[4 * u + 2] = f.z, v[4 * u + 3] = f.w;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            w[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
+            v[2 * j] -= __uint_as_float(w[j] << 16);
+            v[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
+          }
+          tmem_st8(tmem + kTermsOfX + uint32_t(terms.at * 96 + t * 32 + part4 * 8) + (uint32_t(quarter * 32) << 16), w);
+        }
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.drained);
+        if (lane == 0) mbar_arrive(&c.terms[terms.at]);
+        at.next(), terms.next();
+      };
+      Runs r(table);
+      for (int from[2], to[2], n; (n = r.group(p.group, from, to)) > 0;) {
+        // two pieces of 16 columns: of each run's, or of the one's
+        float total[2][16] = {};
+        int col[2], begin[2], end[2];
+        bool here[2];  // the warp has rows of the run
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool other = i > 0 && p.rp <= 64;
+          col[i] = part4 * 16 + (i > 0 && !other ? 64 : 0);
+          begin[i] = other ? from[1] : from[0], end[i] = other ? to[1] : to[0];
+          here[i] = (!other || n > 1) && col[i] < p.rp && max(begin[i], quarter * 32) < min(end[i], quarter * 32 + 32);
+        }
+        int ready = k0;  // blocks whose terms are made
+        for (int kb = k0; kb < k1; kb += chunk, sum.next()) {
+          if (g.xf)  // those of the next sums before these are waited for
+            for (; ready < min(kb + 2 * chunk, k1); ++ready) make_terms();
+          if (!*abort && !mbar_wait_bounded(&c.sums[sum.at], sum.parity(), g.err)) *abort = 1;
+          tc_fence_after();
+          if (warp_agrees(!*abort)) {  // and the warp is converged for tcgen05.ld
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!here[i]) continue;
+              uint32_t v[16];
+              __syncwarp();
+              tmem_ld16(tmem + uint32_t(sum.at) * second + uint32_t((i > 0 && p.rp <= 64 ? p.rp : 0) + col[i]) + (uint32_t(quarter * 32) << 16), v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 16; ++q) total[i][q] += __uint_as_float(v[q]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.drained[sum.at]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (here[i] && row >= begin[i] && row < end[i]) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<float4*>(part + row * p.part_row + col[i] + 4 * q) =
+                  make_float4(total[i][4 * q], total[i][4 * q + 1], total[i][4 * q + 2], total[i][4 * q + 3]);
+          }
       }
     }
     tc_fence_before();
@@ -538,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
         // are so many: one descriptor after the other is made while the tensor core works
         const uint32_t ba = sbase + p.up_at + st * p.up_stage, da = tmem + acc * kAccCols;
         if (!dead)
-          for (int t = 0; t < kTerms; ++t)
+          for (int t = kTerms - 1; t >= 0; --t)  // the smallest first: an addition drops bits below the sum's own
             for (int sub = 0; sub < p.rk / 64; ++sub) {
               const uint32_t oa = tmem + kOperand + uint32_t(t * p.term + 32 * sub), bs = ba + sub * (kN * 128);
-              const uint32_t more = t > 0 || sub > 0;
+              const uint32_t more = t < kTerms - 1 || sub > 0;
               if (p.rp - 64 * sub >= 64) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)

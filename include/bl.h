@@ -436,11 +436,13 @@ bl_status bl_rmsnorm_quant_int8(const void* x, const void* residual, bl_dtype xt
  *   scale   : fp32 [adapters] (alpha / rank).
  *   base, y : [M, N] fp32 or bf16 (yt); y may be base.
  * An adapter of a lower rank is padded with zero rows of A and zero columns
- * of B.  Sums are fp32; y is rounded once.  Beyond 256 tokens, tiles
- * of 128 tokens that hold at most 8 runs of one adapter go to the tensor cores, where fp32 x enters as a sum of three
- * bf16 numbers (2^-24 of it), and scale times the inner product as two (bf16
- * y, 2^-16) or three (fp32 y).  An infinity or NaN of one token or
- * adapter reaches no other token.
+ * of B.  Sums are fp32; y is rounded once.  Beyond 256 tokens, tiles of 128
+ * tokens that hold at most 8 runs of one adapter go to the tensor cores, which
+ * cut off the sums of up to 256 products before they are added up in fp32
+ * (4e-7 of the result in the 2-norm; plain fp32 sums have 2e-7).  There fp32 x
+ * enters as a sum of three bf16 numbers (2^-24 of it), and scale times the
+ * inner product as two (bf16 y, 2^-16) or three (fp32 y).  An infinity or NaN
+ * of one token or adapter reaches no other token.
  * Requires M, N >= 1, adapters >= 1, rank a multiple of 8 in 8..128,
  * K >= 8 with K % 8 == 0, K <= 65536; x, a, b 16-byte aligned, the other
  * pointers aligned to their element size.
