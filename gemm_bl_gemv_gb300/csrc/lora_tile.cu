@@ -17,12 +17,12 @@
 //      accumulator: 4e-7 at any K.  The rows of the run go to shared memory, and
 //      the CTAs add their parts up in rank order through distributed shared memory.
 //      fp32 x (two boxes of 32 columns) is turned by the epilogue warps into three
-//      bf16 terms in TMEM, 24 bits (8192 tokens, 5120 -> 5120, rank 128: 107 us, 99
-//      in one sum; 1894 on the CUDA cores).
-//   2. The sums, times the adapter's scale, become bf16 operands in TMEM: two
-//      terms (hi + lo, 16 bits) for bf16 outputs, whose own rounding is 2^-8,
-//      three (24 bits) for fp32 outputs.  (In shared memory it would take up to
-//      96 KB of what the rings have.)
+//      bf16 terms in TMEM, 24 bits (8192 tokens, 5120 -> 5120, rank 128: 112 us;
+//      1894 on the CUDA cores).
+//   2. The sums, times the adapter's scale, become bf16 operands in TMEM, three
+//      terms: 24 bits, as many as they have.  (With two, 16 bits, 0.2 % of the bf16
+//      outputs were a step off; 8192 tokens, rank 64: 1 % less time, rank 128: 5 %.
+//      In shared memory they would take up to 96 KB of what the rings have.)
 //   3. Up: each CTA takes tiles of 256 bytes of outputs (128 bf16, 64 fp32).
 //      B's rows come by TMA as they lie in memory, and so does the tile of
 //      base, 128-byte swizzled, four in flight.  Every run of the 128 tokens
@@ -38,7 +38,7 @@
 //
 // Bound: HBM; base and y are 4 of the 5 bytes that an output costs at K = N / 2.7
 // and rank 64.  8192 tokens of 12 prompts, 2560 -> 6912, rank 64: 57.7 us, 70 % of
-// the copy rate for 276 MB, 9 us the tensor core's (17 GFLOP with two terms).
+// the copy rate for 276 MB, 13 us the tensor core's (24 GFLOP with three terms).
 // One run's rows are not masked out of the other's product (one sum for both):
 // an infinite weight of one request's adapter must not reach another's outputs.
 #include <algorithm>
@@ -60,7 +60,8 @@ constexpr int kTiles = 4;                  // tiles of base in flight
 constexpr uint32_t kXBytes = kTile * 128;  // 128 rows of 128 bytes: 64 bf16 of x; half a tile of base
 constexpr int kAcc = 2, kAccCols = 128;    // accumulators
 constexpr int kChunk = 4, kFloatChunk = 2; // blocks of K, of bf16 and fp32 x, whose sums the tensor core forms: 16 and 24 additions
-constexpr uint32_t kOperand = 256;         // TMEM column of the operand's first term, three of 64 at most
+constexpr int kTerms = 3;                  // of the operand
+constexpr uint32_t kOperand = 256;         // TMEM column of its first term; a term takes 64 at most
 constexpr uint32_t kTermsOfX = 128;        // TMEM column of the terms of fp32 x, three of 32 per stage
 constexpr uint32_t kTmemCols = 512;
 static_assert(kTermsOfX + kFloatStages * 96 <= kTmemCols, "");
@@ -231,7 +232,6 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
                                                              const __grid_constant__ CUtensorMap bmap,
                                                              const __grid_constant__ CUtensorMap base_map,
                                                              const __grid_constant__ CUtensorMap y_map, const Args g) {
-  constexpr int kTerms = YB ? 2 : 3;
   const int chunk = g.xf ? kFloatChunk : kChunk;
   constexpr int kN = YB ? 128 : 64;  // outputs of an up tile
   constexpr int kHalf = kN / 2;      // 128 bytes of them

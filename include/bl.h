@@ -440,9 +440,9 @@ bl_status bl_rmsnorm_quant_int8(const void* x, const void* residual, bl_dtype xt
  * tokens that hold at most 8 runs of one adapter go to the tensor cores, which
  * cut off the sums of up to 256 products before they are added up in fp32
  * (4e-7 of the result in the 2-norm; plain fp32 sums have 2e-7).  There fp32 x
- * enters as a sum of three bf16 numbers (2^-24 of it), and scale times the
- * inner product as two (bf16 y, 2^-16) or three (fp32 y).  An infinity or NaN
- * of one token or adapter reaches no other token.
+ * enters as a sum of three bf16 numbers (2^-24 of it), and so does scale times
+ * the inner product.  An infinity or NaN of one token or adapter reaches no
+ * other token.
  * Requires M, N >= 1, adapters >= 1, rank a multiple of 8 in 8..128,
  * K >= 8 with K % 8 == 0, K <= 65536; x, a, b 16-byte aligned, the other
  * pointers aligned to their element size.

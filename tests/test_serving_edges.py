@@ -39,3 +39,55 @@ def test_lora_fp32_outputs_of_long_sums(B, M, N, K, rank, xb):
     ref = R.lora_add(x[rows], index[rows], a, b, scale, np.zeros((len(rows), N), np.float32))[0]
     off = np.linalg.norm(y[rows] - ref) / np.linalg.norm(ref)
     assert off <= (11 + np.sqrt(K / 128) / 2 + rank / 16 + 2) * 2.0 ** -23, off * 2 ** 23
+
+
+@gpu
+@pytest.mark.parametrize("xb", [True, False])
+@pytest.mark.parametrize("M,N,K,rank", [(9, 1000, 512, 16), (300, 1000, 512, 64), (700, 1537, 1000, 128), (2500, 520, 2560, 16),
+                                        (4225, 648, 384, 128)])
+def test_lora_bf16_outputs_are_the_rounded_sums(B, M, N, K, rank, xb):
+    """A bf16 output is another than its exact value's rounding only where a border lies within the error of the fp32
+    sums, at most 2^-20 of a value of the usual size: for 2 2^-20 / 2^-8 = 2^-11 of such values, and, as the smaller ones
+    have finer steps, for no more than 2^-10 of all."""
+    g = rng(M, N, K, rank, 26)
+    index = np.repeat([0, 1, 2, 1], [M // 4] * 3 + [M - M // 4 * 3]).astype(np.int32)
+    x = g.standard_normal((M, K)).astype(np.float32)
+    a, b = R.bf16_round(g.standard_normal((3, rank, K)) / np.sqrt(K)), R.bf16_round(g.standard_normal((3, N, rank)) * 0.1)
+    base = R.bf16_round(g.standard_normal((M, N)))
+    v = (R.bf16_round(x) if xb else x, index, a, b, g.uniform(0.25, 4, 3).astype(np.float32), base)
+    y = run_edge(B, *v, xb, True)
+    rows = np.arange(0, M, max(1, M // 300))
+    ref = R.lora_add(v[0][rows], index[rows], a, b, v[4], base[rows])[0]
+    assert (y[rows] != R.bf16_round(ref)).mean() <= 2.0 ** -10
+
+
+def one_hot(M, N, K, rank, adapters, xb, seed):
+    """One product per inner product and per output: no sums, so a term that is lost shows in full."""
+    g = rng(M, N, K, rank, seed)
+    x = g.standard_normal((M, K)).astype(np.float32)
+    x[np.abs(x) < 0.01] = 1.2345678
+    if xb:
+        x = R.bf16_round(x)
+    a, b = np.zeros((adapters, rank, K), np.float32), np.zeros((adapters, N, rank), np.float32)
+    for l in range(adapters):
+        a[l, np.arange(rank), g.integers(0, K, rank)] = R.bf16_round(g.uniform(0.5, 2, rank))
+        b[l, np.arange(N), g.integers(0, rank, N)] = R.bf16_round(g.uniform(0.5, 2, N))
+    return x, a, b, g.uniform(0.25, 4, adapters).astype(np.float32)
+
+
+@gpu
+@pytest.mark.parametrize("xb", [True, False])
+@pytest.mark.parametrize("M,N,K,rank", [(9, 300, 520, 16), (300, 136, 264, 8), (700, 1537, 1000, 64), (1300, 260, 2056, 128),
+                                        (11000, 72, 520, 24), (6000, 1032, 264, 72)])
+def test_lora_fp32_outputs_keep_24_bits(B, M, N, K, rank, xb):
+    """x, the inner product and its product with the scale are rounded to binary32 at most, the last two and the
+    output by up to a step each where the tensor core truncates, and the terms that they are split into are added up
+    with as many: 2^-21 in all."""
+    x, a, b, scale = one_hot(M, N, K, rank, 3, xb, 24)
+    index = np.repeat([0, 1, -1, 2], [M // 4] * 3 + [M - M // 4 * 3]).astype(np.int32)
+    y = run_edge(B, x, index, a, b, scale, np.zeros((M, N), np.float32), xb, False)
+    rows = np.unique(np.concatenate([np.arange(0, M, max(1, M // 300)), [M - 1]]))
+    for m in rows:
+        l = index[m]
+        ref = np.zeros(N) if l < 0 else np.float64(scale[l]) * (b[l].astype(np.float64) @ (a[l].astype(np.float64) @ x[m]))
+        assert np.all(np.abs(y[m] - ref) <= 2.0 ** -21 * np.abs(ref)), (m, np.abs(y[m] / ref - 1).max() * 2 ** 21)
