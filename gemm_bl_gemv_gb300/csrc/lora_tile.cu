@@ -42,6 +42,7 @@
 // One run's rows are not masked out of the other's product (one sum for both):
 // an infinite weight of one request's adapter must not reach another's outputs.
 #include <algorithm>
+#include <cfloat>
 
 #include "bl_device.cuh"
 #include "bl_internal.h"
@@ -202,6 +203,35 @@ struct Runs {
 // together: a warp-wide vote after the wait brings the lanes together again and
 // gives them one decision (the flag may be raised between two lanes' reads).
 __device__ __forceinline__ bool warp_agrees(bool c) { return __all_sync(0xffffffffu, c) != 0; }
+
+// The bf16 nearest to each of v, two at a time; v keeps what they leave.  first: v may hold anything.  An infinity or
+// NaN then leaves nothing (inf - inf would be a NaN), and a value that rounds to an infinity takes the largest bf16.
+template <int N>
+__device__ __forceinline__ void take_term(float (&v)[N], uint32_t (&w)[N / 2], bool first) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) {
+    w[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
+    if (first) most = __vmaxu2(most, w[j] & 0x7fff7fffu);
+  }
+  const bool odd = first && __vmaxu2(most, 0x7f7f7f7fu) != 0x7f7f7f7fu;
+  if (odd) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      if ((w[j] & 0x7fffu) == 0x7f80u && fabsf(v[2 * j]) <= FLT_MAX) --w[j];
+      if ((w[j] >> 16 & 0x7fffu) == 0x7f80u && fabsf(v[2 * j + 1]) <= FLT_MAX) w[j] -= 0x10000u;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) {
+    v[2 * j] -= __uint_as_float(w[j] << 16);
+    v[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
+  }
+  if (odd) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = fabsf(v[j]) <= FLT_MAX ? v[j] : 0.f;
+  }
+}
 
 // The tiles of tokens with several runs, at most kTileRuns (a warp a tile at a time), by the whole CTA.
 __device__ __forceinline__ void find_several(const Args& g, uint32_t (&several)[kMostHelped / 32]) {
@@ -408,16 +438,11 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           const float4 f = *reinterpret_cast<const float4*>(mine_row + (((part4 & 1) * 4 + u) ^ (row & 7)) * 16);
           v[4 * u] = f.x, v[4 * u + 1] = f.y, v[4 * u + 2] = f.z, v[4 * u + 3] = f.w;
         }
-        __syncwarp();
 #pragma unroll
         for (int t = 0; t < 3; ++t) {
           uint32_t w[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            w[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
-            v[2 * j] -= __uint_as_float(w[j] << 16);
-            v[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
-          }
+          take_term(v, w, t == 0);
+          __syncwarp();
           tmem_st8(tmem + kTermsOfX + uint32_t(terms.at * 96 + t * 32 + part4 * 8) + (uint32_t(quarter * 32) << 16), w);
         }
         tmem_st_wait();
@@ -511,16 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
               v[4 * j] = f4.x * scale, v[4 * j + 1] = f4.y * scale, v[4 * j + 2] = f4.z * scale, v[4 * j + 3] = f4.w * scale;
             }
         }
-        __syncwarp();
 #pragma unroll
         for (int t = 0; t < kTerms; ++t) {  // the nearest bf16, and the same of what it leaves
           uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            w[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
-            v[2 * j] -= __uint_as_float(w[j] << 16);
-            v[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
-          }
+          take_term(v, w, t == 0);
+          __syncwarp();
           tmem_st16(tmem + kOperand + uint32_t(t * p.term + k / 2) + (uint32_t(quarter * 32) << 16), w);
         }
       }

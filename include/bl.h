@@ -442,7 +442,8 @@ bl_status bl_rmsnorm_quant_int8(const void* x, const void* residual, bl_dtype xt
  * (4e-7 of the result in the 2-norm; plain fp32 sums have 2e-7).  There fp32 x
  * enters as a sum of three bf16 numbers (2^-24 of it), and so does scale times
  * the inner product.  An infinity or NaN of one token or adapter reaches no
- * other token.
+ * other token.  An infinite x or inner product gives what the formula gives; a
+ * weight of A or B that is not finite may give a NaN in place of an infinity.
  * Requires M, N >= 1, adapters >= 1, rank a multiple of 8 in 8..128,
  * K >= 8 with K % 8 == 0, K <= 65536; x, a, b 16-byte aligned, the other
  * pointers aligned to their element size.

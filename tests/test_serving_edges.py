@@ -91,3 +91,43 @@ def test_lora_fp32_outputs_keep_24_bits(B, M, N, K, rank, xb):
         l = index[m]
         ref = np.zeros(N) if l < 0 else np.float64(scale[l]) * (b[l].astype(np.float64) @ (a[l].astype(np.float64) @ x[m]))
         assert np.all(np.abs(y[m] - ref) <= 2.0 ** -21 * np.abs(ref)), (m, np.abs(y[m] / ref - 1).max() * 2 ** 21)
+
+
+@gpu
+@pytest.mark.parametrize("yb", [True, False])
+@pytest.mark.parametrize("xb", [True, False])
+@pytest.mark.parametrize("M,N,rank", [(10, 200, 16), (300, 200, 16), (300, 203, 72), (1500, 1032, 64)])
+def test_lora_infinities_and_values_near_the_largest(B, M, N, rank, xb, yb):
+    """Infinite inner products stay infinite, and finite ones beyond the largest bf16 stay finite, by both kernels."""
+    K, big = 256, np.float32(3.4e38)  # above the largest bf16, 3.3895e38
+    g = rng(M, N, 23)
+    x = np.zeros((M, K), np.float32)
+    x[:, 0] = 1
+    a = np.zeros((4, rank, K), np.float32)
+    a[:, :, 0] = 1
+    a[1, 0, 0], a[1, 1:, 0] = 2.0 ** -80, 0  # a finite inner product of a huge x
+    a[2, 1:, 0] = 0
+    b = R.bf16_round(g.uniform(0.5, 2, (4, N, rank)))
+    b[1] *= np.float32(2.0 ** -20)
+    b[2] *= np.float32(2.0 ** -100)
+    index = np.repeat([0, 1, 2, 3, -1], [M // 5] * 4 + [M - M // 5 * 4]).astype(np.int32)
+    at = [np.nonzero(index == i)[0] for i in range(4)]
+    x[at[0][0], 0] = np.inf
+    x[at[3][0], 0] = -np.inf
+    x[at[1], 0] = R.bf16_round(np.float32(3.3e38)) if xb else big
+    x[at[2], 0] = 2.0 ** 126
+    a[2, 0, 0] = R.bf16_round(np.float32(3.99))
+    base = R.bf16_round(g.standard_normal((M, N)))
+    scale = np.float32([1, 1, 1.003, 1])  # the third inner product passes the largest bf16 by its scale
+    y = run_edge(B, x, index, a, b, scale, base, xb, yb)
+    assert np.all(y[at[0][0]] == np.inf) and np.all(y[at[3][0]] == -np.inf)
+    rows = np.setdiff1d(np.arange(M), [at[0][0], at[3][0]])
+    ref, cond = R.lora_add(x[rows], index[rows], a, b, scale, base[rows])
+    assert np.all(np.isfinite(ref)) and ref.max() < 1e38
+    # a single product of K; rank + 8 additions; bf16 outputs: half a step, and 16 bits of the inner product
+    bound = (rank + 8) * 2.0 ** -23 * cond + (2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * cond if yb else 0)
+    assert np.all(np.abs(y[rows] - ref) <= bound)
+    x[at[0][0], 0], x[at[3][0], 0] = 1, 1
+    x[at[0][1], 0] = np.uint32(0x7F800001).view(np.float32)  # a NaN that a truncation would make an infinity
+    y = run_edge(B, x, index, a, b, scale, base, xb, yb)
+    assert np.all(np.isnan(y[at[0][1]])) and np.all(np.isfinite(np.delete(y, at[0][1], 0)))
