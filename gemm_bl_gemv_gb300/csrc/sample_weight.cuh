@@ -149,6 +149,7 @@ __device__ __forceinline__ RowFilter row_filter(const RowValues& r, int64_t V) {
   RowFilter f;
   f.slope = slope_of(r.temperature);
   f.top_k = (r.top_k <= 0 || r.top_k > V) ? V : r.top_k;
+  if (r.min_p > 1.f) f.top_k = 1;  // no weight reaches it, so the first token alone stays, whatever ties with it
   f.top_p = r.top_p < 1.f ? fmaxf(r.top_p, 0.f) : 2.f;
   f.min_w = r.min_p > 0.f ? (r.min_p < 1.f ? mass_limit(r.min_p, kOne) : kOne) : 0ull;
   f.u = r.u > 0.f ? fminf(r.u, 0.99999994f) : 0.f;

@@ -465,7 +465,7 @@ bl_status bl_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, const 
  *            top_p times the weight of the top_k tokens (all if top_p >= 1
  *            or NaN).
  *   min_p  : of these, tokens with w[i] >= min_p stay (all if min_p <= 0 or
- *            NaN).  The first token always stays.
+ *            NaN).  The first token always stays (it alone if min_p > 1).
  *   token  : the first token in the order whose cumulative weight exceeds
  *            u times the weight that stayed; u is clamped to [0, 1) (NaN: 0).
  *   prob   : w[token] / (weight that stayed).

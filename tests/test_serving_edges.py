@@ -11,6 +11,37 @@ gpu = pytest.mark.gpu
 
 
 # ---------------------------------------------------------------------------
+# sampling
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("V", [2, 5, 3000, 70000, 248320])
+def test_sample_min_p_above_one_keeps_the_first_token_alone(B, V, bf16):
+    """No weight reaches a min_p above 1, so only the first token stays, whatever ties with it; at 1 all maxima stay."""
+    g = rng(V, 21)
+    l = g.choice(np.float32([2, 2, 1, 0.5, -3]), (10, V))
+    l[:, [0, V - 1]] = 2
+    l[9] = [-np.inf] * (V - 1) + [-7]
+    above = np.nextafter(np.float32(1), np.float32(2))
+    mp = np.float32([above, 1.5, 2, 1e30, np.inf, 1, 1, np.inf, 1.5, 3])
+    k = np.int32([0, 0, V, 1, 0, 0, 2, 7, 0, 0])
+    p = np.float32([1, 1, 0.9, 1, 1, 1, 1, 0.5, 0.99, 1])
+    t = np.float32([1, 0.7, 1, 1, 2, 1, 1, 0, 1, 1])
+    u = np.float32([0.9, 0.5, 0.999, 0.99999994, 0.75, 0.9, 0.75, 0.9, 0.9, 0.9])
+    token, prob = B.bl_sample(dev(l, torch.bfloat16 if bf16 else None), dev(u), dev(t), dev(k), dev(p), dev(mp), prob=True)
+    token, prob = token.cpu().numpy(), prob.cpu().numpy()
+    for m in range(10):
+        ties = np.nonzero(l[m] == l[m].max())[0]
+        if mp[m] > 1:
+            ties = ties[:1]
+        if k[m] > 0:
+            ties = ties[:k[m]]
+        assert token[m] == ties[int(np.float64(u[m]) * len(ties))], (m, token[m])
+        assert prob[m] == np.float32(1 / len(ties)), (m, prob[m])
+
+
+# ---------------------------------------------------------------------------
 # adapters
 # ---------------------------------------------------------------------------
 
