@@ -12,6 +12,8 @@
 // the copy rate; the row's two reductions stand between its loads and its
 // stores, and 55 registers a thread leave half of the warps), latency for few:
 // one token of 2560 2.9 us, of which the launch is most.
+#include <cfloat>
+
 #include "act_quant.cuh"
 #include "bl_internal.h"
 
@@ -169,7 +171,8 @@ __device__ __forceinline__ void round8(float (&v)[8]) {
 
 // quant8's codes without its slow conversions: adding 1.5 * 2^23 rounds a
 // value of |v inv| < 2^22 to the nearest integer, ties to even, and leaves it
-// in the low bits.  |v inv| <= 127 (1 + 2^-22) here, so no clamp is needed.
+// in the low bits.  |v inv| <= 127 (1 + 2^-22) for a finite inv, so no clamp is
+// needed; 127 / max|v| overflows below 3.7e-37.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
   uint32_t b[8];
 #pragma unroll
@@ -282,7 +285,14 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_quant_rows_kernel(c
     const int w = lane & (lanes - 1);
     most = warp_max_of(w < nw ? redm[w] : 0.f, lanes);
   }
-  const float inv = most == 0.f ? 0.f : __fdiv_rn(127.f, most);  // absmax_scales, its scale by one thread
+  float inv = most == 0.f ? 0.f : __fdiv_rn(127.f, most);  // absmax_scales, its scale by one thread
+  if (inv > FLT_MAX) {  // codes8 has no clamp
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[c][j] = float(quant_code(v[c][j], inv));
+    inv = 1.f;
+  }
   if (t == 0) {
     float sc, unused;
     absmax_scales(most, sc, unused);

@@ -42,6 +42,32 @@ def test_sample_min_p_above_one_keeps_the_first_token_alone(B, V, bf16):
 
 
 # ---------------------------------------------------------------------------
+# norm with codes
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("M,K", [(3, 256), (2, 2560), (2, 2561), (400, 5120), (3, 6912), (2, 13824), (2, 32776)])
+def test_norm_codes_where_the_inverse_scale_overflows(B, M, K, bf16):
+    """127 / max|v| beyond binary32: the steps of the quantization give +-127 for what is not 0, for every shape."""
+    g = rng(M, K, 22)
+    x = (np.sign(g.standard_normal((M, K))) * g.uniform(0.5, 2, (M, K))).astype(np.float32)
+    w = np.full(K, 2.0 ** -125, np.float32) * g.choice(np.float32([1, 0.5, 0.75]), K)
+    if bf16:
+        x, w = R.bf16_round(x), R.bf16_round(w)
+    x[0] *= np.float32(2.0 ** 10)  # the factor of a row undoes it
+    t = torch.bfloat16 if bf16 else torch.float32
+    with np.errstate(over="ignore"):
+        rq, rs, _, ry, clear = R.rmsnorm_quant(x, None, w, 1e-5, bf16)
+    assert clear.all() and np.all(np.abs(rq) == 127) and np.all(rs > 0)
+    q, s, _, y = B.bl_rmsnorm_quant_int8(dev(x, t), dev(w, t), 1e-5, y=True)
+    assert np.array_equal(s.cpu().numpy(), rs) and np.array_equal(host(y), ry)
+    assert np.array_equal(q.cpu().numpy(), rq)
+    if not bf16:
+        assert torch.equal(B.bl_quantize_act_absmax_int8(y)[0], q)
+
+
+# ---------------------------------------------------------------------------
 # adapters
 # ---------------------------------------------------------------------------
 
