@@ -181,7 +181,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) lora_token_kernel(const Args
   __shared__ Shared sh;
   const uint32_t me = cluster_ctarank();
   const int cluster = int(blockIdx.x / kParts);
-  if (!TILES) pdl_wait();  // otherwise the tiles' kernel has waited, and runs beside this one
+  if (TILES)
+    __threadfence();  // the tiles' kernel has waited, fenced and started this one, which runs beside it
+  else
+    pdl_wait();
   Scattered units(g, sh, cluster, int(gridDim.x / kParts));
   const int64_t n_part = (g.N + kParts - 1) / kParts, n0 = int64_t(me) * n_part, n1 = min(n0 + n_part, g.N);
   int run = 0;

@@ -295,7 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     fence_barrier_init();
   }
   pdl_wait();
-  pdl_launch_dependents();  // the kernel for the other tiles, which ends after this one
   int tile = cluster / g.shares;
   int first = cluster % g.shares * CL + int(me), step = g.shares * CL;  // of this CTA's tiles of outputs
   bool idle = false;
@@ -343,6 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
     if (before < g.helpers) step = 2 * CL;
   }
 
+  if (warp == 2 + kEpilogueWarps && lane == 0) {  // it has nothing else to do yet
+    // The kernel for the other tiles starts here and ends after this one.  It does not wait for the grids before, whose
+    // results this grid's wait has made visible to this grid's threads: the fence passes them on.
+    __threadfence();
+    pdl_launch_dependents();
+  }
   const Plan p = make_plan(g.rank, kN, __popc(c.used[0]) + __popc(c.used[1]) + __popc(c.used[2]) + __popc(c.used[3]), g.xf);
 
   // All threads of the cluster; the barrier wants converged warps.

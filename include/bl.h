@@ -103,6 +103,9 @@ bl_status bl_set_wait_limit(uint64_t ns);
  * kernel writes the weight buffers right before a product that reads them
  * (weights written by bl_pack_* must be followed by a stream-ordered event
  * or any other kernel first).  Default: disabled.  Process-wide setting.
+ * The two kernels of one bl_lora_add of more than 256 tokens overlap each
+ * other in either setting; with what comes before and after that call they
+ * overlap as the setting says.
  */
 void bl_set_overlap(int enable);
 int bl_get_overlap(void);
