@@ -42,7 +42,6 @@
 // One run's rows are not masked out of the other's product (one sum for both):
 // an infinite weight of one request's adapter must not reach another's outputs.
 #include <algorithm>
-#include <cfloat>
 
 #include "bl_device.cuh"
 #include "bl_internal.h"
@@ -204,32 +203,27 @@ struct Runs {
 // gives them one decision (the flag may be raised between two lanes' reads).
 __device__ __forceinline__ bool warp_agrees(bool c) { return __all_sync(0xffffffffu, c) != 0; }
 
-// The bf16 nearest to each of v, two at a time; v keeps what they leave.  first: v may hold anything.  An infinity or
-// NaN then leaves nothing (inf - inf would be a NaN), and a value that rounds to an infinity takes the largest bf16.
+// Two bf16, infinities turned into the largest finite ones.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\tmin.bf16x2 t, %1, %2;\n\tmax.bf16x2 %0, t, %3;\n\t}"
+      : "=r"(r)
+      : "r"(w), "r"(0x7f7f7f7fu), "r"(0xff7fff7fu));
+  return r;
+}
+
+// The bf16 nearest to each of v, two at a time, as term t; v keeps what they leave.  What rounds to an infinity takes
+// the largest bf16 as its first term, so that a finite value stays finite; an infinity is left over as itself, and is
+// every later term (never inf - inf).
 template <int N>
-__device__ __forceinline__ void take_term(float (&v)[N], uint32_t (&w)[N / 2], bool first) {
-  uint32_t most = 0;
+__device__ __forceinline__ void take_term(float (&v)[N], uint32_t (&w)[N / 2], int t) {
 #pragma unroll
   for (int j = 0; j < N / 2; ++j) {
     w[j] = bf16x2_rn(v[2 * j], v[2 * j + 1]);
-    if (first) most = __vmaxu2(most, w[j] & 0x7fff7fffu);
-  }
-  const bool odd = first && __vmaxu2(most, 0x7f7f7f7fu) != 0x7f7f7f7fu;
-  if (odd) {
-#pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-      if ((w[j] & 0x7fffu) == 0x7f80u && fabsf(v[2 * j]) <= FLT_MAX) --w[j];
-      if ((w[j] >> 16 & 0x7fffu) == 0x7f80u && fabsf(v[2 * j + 1]) <= FLT_MAX) w[j] -= 0x10000u;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < N / 2; ++j) {
-    v[2 * j] -= __uint_as_float(w[j] << 16);
-    v[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
-  }
-  if (odd) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = fabsf(v[j]) <= FLT_MAX ? v[j] : 0.f;
+    const uint32_t f = finite_bf16x2(w[j]);
+    if (t == 0) w[j] = f;
+    v[2 * j] -= __uint_as_float(f << 16);
+    v[2 * j + 1] -= __uint_as_float(f & 0xffff0000u);
   }
 }
 
@@ -446,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
 #pragma unroll
         for (int t = 0; t < 3; ++t) {
           uint32_t w[8];
-          take_term(v, w, t == 0);
+          take_term(v, w, t);
           __syncwarp();
           tmem_st8(tmem + kTermsOfX + uint32_t(terms.at * 96 + t * 32 + part4 * 8) + (uint32_t(quarter * 32) << 16), w);
         }
@@ -544,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
 #pragma unroll
         for (int t = 0; t < kTerms; ++t) {  // the nearest bf16, and the same of what it leaves
           uint32_t w[16];
-          take_term(v, w, t == 0);
+          take_term(v, w, t);
           __syncwarp();
           tmem_st16(tmem + kOperand + uint32_t(t * p.term + k / 2) + (uint32_t(quarter * 32) << 16), w);
         }
