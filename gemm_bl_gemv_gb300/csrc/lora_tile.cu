@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_tile_kernel(const __grid_con
           tmem_st16(tmem + kOperand + uint32_t(t * p.term + k / 2) + (uint32_t(quarter * 32) << 16), w);
         }
       }
+      __syncwarp();
       tmem_st_wait();
     }
     tc_fence_before();
