@@ -409,9 +409,9 @@ def bl_lora_add(x, adapter, a, b, scale, base, y=None, stream=None):
     _cuda(x, "x")
     M, K = x.shape
     dev = x.get_device()
-    _like(a, "a", torch.bfloat16, (a.shape[0], a.shape[1], K), dev)
-    L, R = a.shape[0], a.shape[1]
-    N = base.shape[1]
+    L, R, _ = _cuda(a, "a").shape
+    _, N = _cuda(base, "base").shape
+    _like(a, "a", torch.bfloat16, (L, R, K), dev)
     _like(b, "b", torch.bfloat16, (L, N, R), dev)
     _like(scale, "scale", torch.float32, (L,), dev)
     _like(adapter, "adapter", torch.int32, (M,), dev)

@@ -188,3 +188,20 @@ def test_lora_infinities_and_values_near_the_largest(B, M, N, rank, xb, yb):
     x[at[0][1], 0] = np.uint32(0x7F800001).view(np.float32)  # a NaN that a truncation would make an infinity
     y = run_edge(B, x, index, a, b, scale, base, xb, yb)
     assert np.all(np.isnan(y[at[0][1]])) and np.all(np.isfinite(np.delete(y, at[0][1], 0)))
+
+
+@gpu
+def test_binding_names_the_tensor_that_does_not_fit(B):
+    bf = torch.bfloat16
+    x, index = torch.zeros(3, 16, device="cuda", dtype=bf), torch.zeros(3, dtype=torch.int32, device="cuda")
+    a, b = torch.zeros(2, 8, 16, device="cuda", dtype=bf), torch.zeros(2, 5, 8, device="cuda", dtype=bf)
+    scale, base = torch.ones(2, device="cuda"), torch.zeros(3, 5, device="cuda")
+    B.bl_lora_add(x, index, a, b, scale, base)
+    for bad in ((x, index, a[0], b, scale, base), (x, index, a, b, scale, base[0]), (x, index, a, b[0], scale, base),
+                (x, index, a[:, :, :8].contiguous(), b, scale, base), (x, index, a, b, scale, base[:2])):
+        with pytest.raises(ValueError):
+            B.bl_lora_add(*bad)
+    for bad in ((x, index, None, b, scale, base), (x, index, a, b, scale, None), (x, index, a, b, scale, base.cpu()),
+                (x, index, a.float(), b, scale, base), (x, index.long(), a, b, scale, base)):
+        with pytest.raises(TypeError):
+            B.bl_lora_add(*bad)
