@@ -410,11 +410,12 @@ bl_status bl_gemm_i2s_int8_act_noalloc(const void* x, bl_dtype xt, const uint8_t
  *   q, s = the absmax int8 codes and scale of v, by the steps of
  *          bl_quantize_act_absmax_int8.
  * The sum of squares is carried in pairs of floats and r is rounded to
- * binary32 once, so q, s, h and y are the same for every launch shape and
- * differ from the formula's only where r lies within about 2^-40 (relative)
- * of a rounding border.  That holds while the squares neither overflow nor
- * underflow binary32 against the sum (2^-50 < |h| < 2^60 does it); a row
- * whose mean square plus eps is 0 gives y = 0, q = 0, s = 0.
+ * binary32 once, so q, s, h and y are the formula's, and the same for every
+ * launch shape, unless r lies within about 2^-40 (relative) of a rounding
+ * border.  That holds while the squares neither underflow against the sum
+ * (2^-50 < |h| or h = 0 does it) nor come near binary32's largest (|h| < 2^50
+ * does it up to K = 2^27); a row whose mean square plus eps is 0 gives y = 0,
+ * q = 0, s = 0.
  *   x : [M, K] (xt);  residual : [M, K] (xt) or NULL;  rms_weight : [K] (xt).
  *   h : [M, K] (xt) or NULL; required with a residual; may be x or residual.
  *   y : [M, K] (xt) or NULL; may be x or residual, but not h.
@@ -447,9 +448,9 @@ bl_status bl_rmsnorm_quant_int8(const void* x, const void* residual, bl_dtype xt
  * the inner product.  An infinity or NaN of one token or adapter reaches no
  * other token.  An infinite x or inner product gives what the formula gives; a
  * weight of A or B that is not finite may give a NaN in place of an infinity.
- * Requires M, N >= 1, adapters >= 1, rank a multiple of 8 in 8..128,
- * K >= 8 with K % 8 == 0, K <= 65536; x, a, b 16-byte aligned, the other
- * pointers aligned to their element size.
+ * Requires M, N >= 1, M < 2^30 - 3 (BL_ERR_UNSUPPORTED above), adapters >= 1,
+ * rank a multiple of 8 in 8..128, K >= 8 with K % 8 == 0, K <= 65536; x, a, b
+ * 16-byte aligned, the other pointers aligned to their element size.
  */
 bl_status bl_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a_bf16,
                       const uint16_t* b_bf16, const float* scale, const void* base, void* y, bl_dtype yt, int64_t M,

@@ -67,6 +67,27 @@ def test_norm_codes_where_the_inverse_scale_overflows(B, M, K, bf16):
         assert torch.equal(B.bl_quantize_act_absmax_int8(y)[0], q)
 
 
+@gpu
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("K", [256, 2560, 2561, 32768])
+def test_norm_codes_at_the_ends_of_their_range(B, K, bf16):
+    """Rows from just above 2^-50 to just below 2^50, with zeros among them: codes bit for bit."""
+    g, M = rng(K, 27), 48
+    x = (np.sign(g.standard_normal((M, K))) * g.uniform(1.1, 1.9, (M, K))).astype(np.float32)
+    x *= np.float32(2.0) ** np.where(np.arange(M) % 2, np.linspace(-50, -1, M), np.linspace(49, 1, M)).round().astype(np.float32)[:, None]
+    x[:, :: 5] = 0
+    w = (1 + 0.3 * g.standard_normal(K)).astype(np.float32)
+    if bf16:
+        x, w = R.bf16_round(x), R.bf16_round(w)
+    t = torch.bfloat16 if bf16 else torch.float32
+    for eps in (0.0, 1e-5):
+        rq, rs, _, ry, clear = R.rmsnorm_quant(x, None, w, eps, bf16)
+        q, s, _, y = B.bl_rmsnorm_quant_int8(dev(x, t), dev(w, t), eps, y=True)
+        assert clear.sum() > M - 4
+        assert np.array_equal(s.cpu().numpy()[clear], rs[clear]) and np.array_equal(host(y)[clear], ry[clear])
+        assert np.array_equal(q.cpu().numpy()[clear], rq[clear])
+
+
 # ---------------------------------------------------------------------------
 # adapters
 # ---------------------------------------------------------------------------
@@ -188,6 +209,16 @@ def test_lora_infinities_and_values_near_the_largest(B, M, N, rank, xb, yb):
     x[at[0][1], 0] = np.uint32(0x7F800001).view(np.float32)  # a NaN that a truncation would make an infinity
     y = run_edge(B, x, index, a, b, scale, base, xb, yb)
     assert np.all(np.isnan(y[at[0][1]])) and np.all(np.isfinite(np.delete(y, at[0][1], 0)))
+
+
+def test_lora_refuses_more_tokens_than_a_grid_has_clusters(B):
+    """The header's limit on M is refused before any CUDA call; so are counts and sizes beyond 32 bits."""
+    import ctypes
+    P, f = ctypes.c_void_p, B.lib().bl_lora_add
+    a = P(1 << 14)
+    for M, N, L, want in ((2 ** 30 - 3, 4, 1, B.BL_ERR_UNSUPPORTED), (2 ** 31 - 1, 4, 1, B.BL_ERR_UNSUPPORTED),
+                          (2 ** 31, 4, 1, B.BL_ERR_SHAPE), (1, 2 ** 31, 1, B.BL_ERR_SHAPE), (1, 4, 2 ** 31, B.BL_ERR_SHAPE)):
+        assert f(a, B.BL_BF16, a, a, a, a, a, a, B.BL_F32, M, N, 8, L, 8, None) == want, (M, N, L)
 
 
 @gpu
