@@ -25,7 +25,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kParts = 8;      // CTAs of a cluster
+constexpr int64_t kOnePerCluster = 256;  // tokens up to which each has a cluster
 constexpr int64_t kTileTokens = 257;  // tokens from which the tiles' kernel is launched as well
+static_assert(kTileTokens > kOnePerCluster, "beside the tiles a cluster takes a group of tokens");
 constexpr int kPerSm = 4;      // CTAs of an SM
 constexpr int kBatch = 256;    // tiles looked at together
 constexpr int kGroup = 4;      // tokens that share the reads of an adapter
@@ -282,14 +284,16 @@ cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, 
                             const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
                             int64_t K, int64_t adapters, int rank, cudaStream_t s) {
   // A cluster per token while that is at most a few per SM; beyond, per four.
-  const int per = M <= 256 ? 1 : kGroup;
+  const int per = M <= kOnePerCluster ? 1 : kGroup;
   if ((M + per - 1) / per > 0x7fffffff / kParts) return cudaErrorInvalidConfiguration;
   Args g{x, adapter, a, b, scale, base, y, dev_error_ptr(), M, N, K, adapters, rank, per};
   bool tiles = false;
   // Up to 256 tokens may be as many requests, whose tiles would be left to this kernel after a launch of the
-  // other for nothing (64 tokens over 40 adapters, 5120 -> 13824, rank 32: 21 us without, 29 with it).  Beyond,
-  // three adapters, scattered / tiles, us: 257 tokens, 264 -> 264, rank 8 9 / 11; 2560 -> 2560, rank 24 15 / 13;
-  // 2560 -> 6912, rank 64 43 / 15; 1024 tokens 25 / 11, 44 / 15, 132 / 20.
+  // other for nothing; which it is stands in device memory.  2560 -> 6912, scattered alone / with the tiles, us, rank
+  // 16, 64, 128: 64 tokens of 40 runs 8 / 19, 32 / 51, 57 / 87; 256 tokens of 256 runs 25 / 43, 98 / 137, 190 / 249.
+  // The price is paid by few runs in few tokens: 64 tokens of one run 11 / 11, 36 / 13, 66 / 16; 256 tokens of three
+  // 17 / 13, 44 / 15, 76 / 20.  Beyond, three runs: 257 tokens, 264 -> 264, rank 8 9 / 11; 2560 -> 2560, rank 24
+  // 15 / 13; 1024 tokens 25 / 11, 44 / 15.
   if (M >= kTileTokens) {
     const cudaError_t e = launch_lora_tile(x, xt, adapter, a, b, scale, base, y, yt, M, N, K, adapters, rank, s);
     if (e != cudaSuccess && e != cudaErrorNotSupported) return e;
