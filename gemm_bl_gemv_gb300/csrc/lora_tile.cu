@@ -4,7 +4,7 @@
 //
 // A cluster of CL CTAs takes 128 tokens; while there are few, several clusters
 // do, each with the first product and a share of the outputs (512 tokens, 2560
-// -> 6912, rank 64: 16 us).  A run is a stretch of those tokens
+// -> 6912, rank 64: 17 us).  A run is a stretch of those tokens
 // with one adapter; a tile of more than kTileRuns runs is left to the kernel
 // for scattered tokens.
 //   1. Down: each CTA takes a part of K.  x (128 x 64 blocks) and the runs' A
@@ -17,8 +17,8 @@
 //      accumulator: 4e-7 at any K.  The rows of the run go to shared memory, and
 //      the CTAs add their parts up in rank order through distributed shared memory.
 //      fp32 x (two boxes of 32 columns) is turned by the epilogue warps into three
-//      bf16 terms in TMEM, 24 bits (8192 tokens, 5120 -> 5120, rank 128: 112 us;
-//      1894 on the CUDA cores).
+//      bf16 terms in TMEM, 24 bits (8192 tokens, 5120 -> 5120, rank 128: 116 us;
+//      1894 on the CUDA cores; 112 if infinities were not looked for).
 //   2. The sums, times the adapter's scale, become bf16 operands in TMEM, three
 //      terms: 24 bits, as many as they have.  (With two, 16 bits, 0.2 % of the bf16
 //      outputs were a step off; 8192 tokens, rank 64: 1 % less time, rank 128: 5 %.
@@ -34,10 +34,10 @@
 //
 // A tile with several runs takes a product of each for every output tile, and
 // so nearly twice as long; where SMs are left, a second cluster takes half of
-// its outputs (65.5 -> 57.7 us in the case below).
+// its outputs (12 % in the case below).
 //
 // Bound: HBM; base and y are 4 of the 5 bytes that an output costs at K = N / 2.7
-// and rank 64.  8192 tokens of 12 prompts, 2560 -> 6912, rank 64: 57.7 us, 70 % of
+// and rank 64.  8192 tokens of 12 prompts, 2560 -> 6912, rank 64: 58.7 us, 69 % of
 // the copy rate for 276 MB, 13 us the tensor core's (24 GFLOP with three terms).
 // One run's rows are not masked out of the other's product (one sum for both):
 // an infinite weight of one request's adapter must not reach another's outputs.
