@@ -25,6 +25,7 @@ EXPORTS = [
     "bl_gemv_i2s", "bl_gemv_i2s_residual", "bl_gemv_i2s_rmsnorm", "bl_gemv_i2s_gate_up", "bl_gemv_tq2_0", "bl_gemm_w1a8", "bl_gemm_w1a8_act", "bl_gemm_i2s_int8",
     "bl_gemm_tq2_0_int8", "bl_gemm_i2s_int8_act", "bl_gemm_i2s_int8_act_workspace",
     "bl_gemm_i2s_int8_act_noalloc", "bl_rmsnorm_quant_int8", "bl_lora_add", "bl_sample",
+    "bl_page_map", "bl_rope_append", "bl_attn_paged", "bl_attn_paged_workspace", "bl_verify", "bl_verify_workspace",
 ]
 
 
@@ -62,6 +63,13 @@ def _declare(L):
         "bl_rmsnorm_quant_int8": ([p, p, i32, p, ctypes.c_float, i64, i64, p, p, p, p, p], st),
         "bl_lora_add": ([p, i32, p, p, p, p, p, p, i32, i64, i64, i64, i64, i32, p], st),
         "bl_sample": ([p, i32, p, p, p, p, p, i64, i64, p, p, p], st),
+        "bl_page_map": ([p, p, p, p, p, p, i64, i64, i64, i32, i64, p, p, p, p, p, p, p], st),
+        "bl_rope_append": ([p, i32, p, p, p, p, i64, i32, i32, i32, i32, i64, p, p, p, i64, i32, p], st),
+        "bl_attn_paged_workspace": ([i64, i32, i32, i32], ctypes.c_size_t),
+        "bl_attn_paged": ([p, p, p, p, p, p, ctypes.c_float, i64, i64, i64, i64, i32, i32, i32, i64, i32, i64, p, i32, p,
+                           ctypes.c_size_t, p], st),
+        "bl_verify_workspace": ([i64], ctypes.c_size_t),
+        "bl_verify": ([p, p, i32, p, p, p, p, p, i64, i64, i64, p, p, p, ctypes.c_size_t, p], st),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -446,3 +454,147 @@ def bl_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     _check(_lib.bl_sample(_ptr(logits), _dtype_code(logits), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
                           _ptr(u), M, V, _ptr(token), _ptr(prob), _stream(stream)))
     return token if prob is None else (token, prob)
+
+
+# ---- a decode step over a paged key-value cache --------------------------------
+
+def _here(t, name, dims):
+    """A contiguous CUDA tensor of so many dimensions on the current device; its device's number."""
+    if _cuda(t, name).dim() != dims:
+        raise ValueError("%s must have %d dimensions" % (name, dims))
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError("%s must be on the current device" % name)
+    return dev
+
+
+def _out(t, name, dtype, shape, dev):
+    """The tensor given for an output, or a new one."""
+    return torch.empty(shape, dtype=dtype, device="cuda:%d" % dev) if t is None else _like(t, name, dtype, shape, dev)
+
+
+def bl_page_map(length, count, table, owned, free, free_count, page, tokens, start=None, position=None, slot=None,
+                length_out=None, owned_out=None, free_left=None, stream=None):
+    """(start, position, slot, length_out, owned_out, free_left) of a step: pages from the stack `free` into the block
+    tables (in place), positions and cache slots of the new tokens (`tokens` rows; -1 behind the last request's).
+
+    length, count, owned int32 [R]; table int32 [R, W]; free int32 [pages], free_count int32 [1].  A negative count ends a
+    request.  length_out, owned_out and free_left may be length, owned and free_count."""
+    dev = _here(table, "table", 2)
+    R, W = table.shape
+    i32 = torch.int32
+    _like(table, "table", i32, (R, W), dev)
+    for t, n in ((length, "length"), (count, "count"), (owned, "owned")):
+        _like(t, n, i32, (R,), dev)
+    _here(free, "free", 1)
+    _like(free, "free", i32, free.shape, dev)
+    _like(free_count, "free_count", i32, (1,), dev)
+    M = int(tokens)
+    start, position, slot = (_out(t, n, i32, shape, dev) for t, n, shape in (
+        (start, "start", (R + 1,)), (position, "position", (M,)), (slot, "slot", (M,))))
+    length_out, owned_out, free_left = (_out(t, n, i32, shape, dev) for t, n, shape in (
+        (length_out, "length_out", (R,)), (owned_out, "owned_out", (R,)), (free_left, "free_left", (1,))))
+    _check(_lib.bl_page_map(_ptr(length), _ptr(count), _ptr(table), _ptr(owned), _ptr(free), _ptr(free_count), R, W,
+                            free.numel(), int(page), M, _ptr(start), _ptr(position), _ptr(slot), _ptr(length_out),
+                            _ptr(owned_out), _ptr(free_left), _stream(stream)))
+    return start, position, slot, length_out, owned_out, free_left
+
+
+def _caches(k_cache, v_cache):
+    """(device, pages, key-value heads, page size, head size) of a pair of caches."""
+    dev = _here(k_cache, "k_cache", 4)
+    _like(k_cache, "k_cache", torch.bfloat16, k_cache.shape, dev)
+    _like(v_cache, "v_cache", torch.bfloat16, k_cache.shape, dev)
+    return (dev, *k_cache.shape)
+
+
+def bl_rope_append(qkv, cos, sin, position, slot, k_cache, v_cache, heads, q=None, stream=None):
+    """q (bf16 [M, heads, D]) of the rows qkv [M, (heads + 2 Hk) D], turned by cos and sin (fp32 [positions, rotary / 2]) at
+    position (int32 [M]); k, turned too, and v go to the caches (bf16 [pages, Hk, page, D]) at slot (int32 [M])."""
+    dev, pages, Hk, page, D = _caches(k_cache, v_cache)
+    H = int(heads)
+    _here(qkv, "qkv", 2)
+    M = qkv.shape[0]
+    xt = _dtype_code(qkv)
+    _like(qkv, "qkv", qkv.dtype, (M, (H + 2 * Hk) * D), dev)
+    _here(cos, "cos", 2)
+    positions, half = cos.shape
+    _like(cos, "cos", torch.float32, (positions, half), dev)
+    _like(sin, "sin", torch.float32, (positions, half), dev)
+    _like(position, "position", torch.int32, (M,), dev)
+    _like(slot, "slot", torch.int32, (M,), dev)
+    q = _out(q, "q", torch.bfloat16, (M, H, D), dev)
+    _check(_lib.bl_rope_append(_ptr(qkv), xt, _ptr(cos), _ptr(sin), _ptr(position), _ptr(slot), M, H, Hk, D, 2 * half,
+                               positions, _ptr(q), _ptr(k_cache), _ptr(v_cache), pages, page, _stream(stream)))
+    return q
+
+
+def attn_paged_workspace(M, heads, kv_heads, D, device="cuda"):
+    """A workspace for bl_attn_paged (uint8, 256-byte aligned by the allocator)."""
+    n = int(_lib.bl_attn_paged_workspace(int(M), int(heads), int(kv_heads), int(D)))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def bl_attn_paged(q, k_cache, v_cache, table, length, start, scale, window=0, sinks=0, out=None, out_dtype=None,
+                  workspace=None, stream=None):
+    """softmax(scale q k^T) v of the new tokens q (bf16 [M, H, D]) of R requests over their cached ones, causal.
+
+    table int32 [R, W]; length int32 [R] with the new tokens; start int32 [R + 1], the requests' rows.  window > 0: a token
+    sees the last `window` ones and the first `sinks`.  out bf16 (default) or fp32."""
+    dev, pages, Hk, page, D = _caches(k_cache, v_cache)
+    _here(q, "q", 3)
+    M, H, _ = q.shape
+    _like(q, "q", torch.bfloat16, (M, H, D), dev)
+    _here(table, "table", 2)
+    R, W = table.shape
+    _like(table, "table", torch.int32, (R, W), dev)
+    _like(length, "length", torch.int32, (R,), dev)
+    _like(start, "start", torch.int32, (R + 1,), dev)
+    out = _out(out, "out", out_dtype or (torch.bfloat16 if out is None else out.dtype), (M, H, D), dev)
+    ot = _dtype_code(out)
+    if workspace is None:
+        workspace = attn_paged_workspace(M, H, Hk, D, q.device)
+    else:
+        _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _check(_lib.bl_attn_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(length), _ptr(start), float(scale),
+                              int(window), int(sinks), M, R, H, Hk, D, pages, page, W, _ptr(out), ot, _ptr(workspace),
+                              workspace.numel(), _stream(stream)))
+    return out
+
+
+def verify_workspace(M, device="cuda"):
+    """A workspace for bl_verify (uint8, 256-byte aligned by the allocator)."""
+    return torch.empty(int(_lib.bl_verify_workspace(int(M))), dtype=torch.uint8, device=device)
+
+
+def bl_verify(logits, token, start, u, u_sample, draft_logits=None, temperature=None, accepted=None, next_token=None,
+              workspace=None, stream=None):
+    """(accepted, next_token), int32 [R]: how many of each request's drafted tokens hold against logits [M, V], and the
+    token that follows them.
+
+    token int32 [M]: the requests' rows (start int32 [R + 1]), each its last known token and the drafted ones; row i of
+    logits judges token i + 1.  draft_logits [M, V] (None: the drafts are certain); temperature fp32 [R] (None: 1); u fp32
+    [M], u_sample fp32 [R]."""
+    dev = _here(logits, "logits", 2)
+    M, V = logits.shape
+    lt = _dtype_code(logits)
+    _here(start, "start", 1)
+    R = start.shape[0] - 1
+    _like(start, "start", torch.int32, (R + 1,), dev)
+    _like(token, "token", torch.int32, (M,), dev)
+    _like(u, "u", torch.float32, (M,), dev)
+    _like(u_sample, "u_sample", torch.float32, (max(R, 0),), dev)
+    if draft_logits is not None:
+        _like(draft_logits, "draft_logits", logits.dtype, (M, V), dev)
+    if temperature is not None:
+        _like(temperature, "temperature", torch.float32, (R,), dev)
+    accepted = _out(accepted, "accepted", torch.int32, (max(R, 0),), dev)
+    next_token = _out(next_token, "next_token", torch.int32, (max(R, 0),), dev)
+    if workspace is None:
+        workspace = verify_workspace(M, logits.device)
+    else:
+        _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _check(_lib.bl_verify(_ptr(logits), _ptr(draft_logits), lt, _ptr(token), _ptr(start), _ptr(temperature), _ptr(u),
+                          _ptr(u_sample), M, R, V, _ptr(accepted), _ptr(next_token), _ptr(workspace), workspace.numel(),
+                          _stream(stream)))
+    return accepted, next_token

@@ -467,4 +467,104 @@ bl_status bl_sample(const void* logits, bl_dtype lt, const float* temperature, c
   return launch_status(lt == BL_BF16 ? launch_sample_bf16(args, S(stream)) : launch_sample_f32(args, S(stream)), fn);
 }
 
+bl_status bl_page_map(const int32_t* length, const int32_t* count, int32_t* table, const int32_t* owned,
+                      int32_t* free_pages, const int32_t* free_count, int64_t R, int64_t W, int64_t pages, int page,
+                      int64_t M, int32_t* start, int32_t* position, int32_t* slot, int32_t* length_out, int32_t* owned_out,
+                      int32_t* free_left, bl_stream_t stream) {
+  const char* fn = "bl_page_map";
+  const void* all[] = {length, count, table, owned, free_pages, free_count, start, position, slot, length_out, owned_out,
+                       free_left};
+  for (const void* p : all)
+    if (!p) return fail(BL_ERR_NULL, "%s: NULL pointer", fn);
+  if (R < 1 || W < 1 || pages < 1 || page < 1 || M < 1 || R > 0x7fffffff || W > 0x7fffffff || M > 0x7fffffff)
+    return fail(BL_ERR_SHAPE, "%s: need R, W, pages, page, M >= 1 (R=%lld W=%lld pages=%lld page=%d M=%lld)", fn,
+                (long long)R, (long long)W, (long long)pages, page, (long long)M);
+  if (pages > 0x7fffffff / page)
+    return fail(BL_ERR_UNSUPPORTED, "%s: pages * page < 2^31 supported (pages=%lld page=%d)", fn, (long long)pages, page);
+  for (const void* p : all)
+    if (!aligned(p, 4)) return fail(BL_ERR_ALIGN, "%s: pointers must be 4-byte aligned", fn);
+  return launch_status(launch_page_map(length, count, table, owned, free_pages, free_count, R, W, pages, page, M, start,
+                                       position, slot, length_out, owned_out, free_left, S(stream)), fn);
+}
+
+bl_status bl_rope_append(const void* qkv, bl_dtype xt, const float* cos, const float* sin, const int32_t* position,
+                         const int32_t* slot, int64_t M, int H, int Hk, int D, int rotary, int64_t positions,
+                         uint16_t* q_bf16, uint16_t* k_cache, uint16_t* v_cache, int64_t pages, int page,
+                         bl_stream_t stream) {
+  const char* fn = "bl_rope_append";
+  if (!qkv || !cos || !sin || !position || !slot || !q_bf16 || !k_cache || !v_cache)
+    return fail(BL_ERR_NULL, "%s: NULL pointer", fn);
+  if (xt != BL_F32 && xt != BL_BF16) return fail(BL_ERR_DTYPE, "%s: bad dtype %d", fn, int(xt));
+  if (M < 1 || H < 1 || Hk < 1 || D < 8 || D % 8 || rotary < 2 || rotary % 2 || rotary > D || positions < 1 || pages < 1 ||
+      page < 1 || M > 0x7fffffff || positions > 0x7fffffff)
+    return fail(BL_ERR_SHAPE,
+                "%s: need M, H, Hk, positions, pages, page >= 1, D %% 8 == 0, rotary even in 2..D (M=%lld H=%d Hk=%d D=%d "
+                "rotary=%d positions=%lld pages=%lld page=%d)",
+                fn, (long long)M, H, Hk, D, rotary, (long long)positions, (long long)pages, page);
+  if (pages > 0x7fffffff / page || H > 65536 || Hk > 65536 || D > 1024)
+    return fail(BL_ERR_UNSUPPORTED, "%s: pages * page < 2^31, H, Hk <= 65536 and D <= 1024 supported", fn);
+  if (!aligned(qkv, 16) || !aligned(q_bf16, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(cos, 4) ||
+      !aligned(sin, 4) || !aligned(position, 4) || !aligned(slot, 4))
+    return fail(BL_ERR_ALIGN, "%s: qkv, q and the caches must be 16-byte aligned, the others to their element size", fn);
+  return launch_status(launch_rope_append(qkv, xt, cos, sin, position, slot, M, H, Hk, D, rotary, positions, q_bf16, k_cache,
+                                          v_cache, pages, page, S(stream)), fn);
+}
+
+size_t bl_attn_paged_workspace(int64_t M, int H, int Hk, int D) {
+  if (M < 1 || H < 1 || Hk < 1 || H % Hk || D < 8 || D > 256 || D % 8) return 0;
+  return bl::attn_paged_workspace(M, H, Hk, D);
+}
+
+bl_status bl_attn_paged(const uint16_t* q_bf16, const uint16_t* k_cache, const uint16_t* v_cache, const int32_t* table,
+                        const int32_t* length, const int32_t* start, float scale, int64_t window, int64_t sinks, int64_t M,
+                        int64_t R, int H, int Hk, int D, int64_t pages, int page, int64_t W, void* out, bl_dtype ot,
+                        void* workspace, size_t workspace_bytes, bl_stream_t stream) {
+  const char* fn = "bl_attn_paged";
+  if (!q_bf16 || !k_cache || !v_cache || !table || !length || !start || !out || !workspace)
+    return fail(BL_ERR_NULL, "%s: NULL pointer", fn);
+  if (ot != BL_F32 && ot != BL_BF16) return fail(BL_ERR_DTYPE, "%s: bad dtype %d", fn, int(ot));
+  if (M < 1 || R < 1 || H < 1 || Hk < 1 || H % Hk || D < 8 || D % 8 || pages < 1 || page < 1 || W < 1 || M > 0x7fffffff ||
+      R > 0x7fffffff || W > 0x7fffffff || window < 0 || sinks < 0)
+    return fail(BL_ERR_SHAPE,
+                "%s: need M, R, pages, page, W >= 1, H %% Hk == 0, D %% 8 == 0, window, sinks >= 0 (M=%lld R=%lld H=%d Hk=%d "
+                "D=%d pages=%lld page=%d W=%lld window=%lld sinks=%lld)",
+                fn, (long long)M, (long long)R, H, Hk, D, (long long)pages, page, (long long)W, (long long)window,
+                (long long)sinks);
+  if (D > 256 || pages > 0x7fffffff / page || H > 65536)
+    return fail(BL_ERR_UNSUPPORTED, "%s: D <= 256, H <= 65536 and pages * page < 2^31 supported", fn);
+  if (workspace_bytes < bl::attn_paged_workspace(M, H, Hk, D))
+    return fail(BL_ERR_SHAPE, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes,
+                bl::attn_paged_workspace(M, H, Hk, D));
+  if (!aligned(q_bf16, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 256) || !aligned(table, 4) || !aligned(length, 4) || !aligned(start, 4))
+    return fail(BL_ERR_ALIGN, "%s: workspace 256-byte, q, caches and out 16-byte, the others 4-byte aligned", fn);
+  return launch_status(launch_attn_paged(q_bf16, k_cache, v_cache, table, length, start, scale, window, sinks, M, R, H, Hk,
+                                         D, pages, page, W, out, ot, static_cast<uint8_t*>(workspace), S(stream)), fn);
+}
+
+size_t bl_verify_workspace(int64_t M) { return M < 1 ? 0 : bl::verify_workspace(M); }
+
+bl_status bl_verify(const void* logits, const void* draft_logits, bl_dtype lt, const int32_t* token, const int32_t* start,
+                    const float* temperature, const float* u, const float* u_sample, int64_t M, int64_t R, int64_t V,
+                    int32_t* accepted, int32_t* next_token, void* workspace, size_t workspace_bytes, bl_stream_t stream) {
+  const char* fn = "bl_verify";
+  if (!logits || !token || !start || !u || !u_sample || !accepted || !next_token || !workspace)
+    return fail(BL_ERR_NULL, "%s: NULL pointer", fn);
+  if (lt != BL_F32 && lt != BL_BF16) return fail(BL_ERR_DTYPE, "%s: bad dtype %d", fn, int(lt));
+  if (M < 1 || R < 1 || V < 1 || M > 0x7fffffff || R > 0x7fffffff)
+    return fail(BL_ERR_SHAPE, "%s: need M, R, V >= 1 (M=%lld R=%lld V=%lld)", fn, (long long)M, (long long)R, (long long)V);
+  if (V > 524288 || M >= (1 << 26) || R >= (1 << 26))
+    return fail(BL_ERR_UNSUPPORTED, "%s: V <= 524288, M and R < 2^26 supported (M=%lld R=%lld V=%lld)", fn, (long long)M,
+                (long long)R, (long long)V);
+  if (workspace_bytes < bl::verify_workspace(M))
+    return fail(BL_ERR_SHAPE, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes, bl::verify_workspace(M));
+  const size_t es = lt == BL_F32 ? 4 : 2;
+  if (!aligned(logits, es) || !aligned(draft_logits, es) || !aligned(token, 4) || !aligned(start, 4) ||
+      !aligned(temperature, 4) || !aligned(u, 4) || !aligned(u_sample, 4) || !aligned(accepted, 4) ||
+      !aligned(next_token, 4) || !aligned(workspace, 256))
+    return fail(BL_ERR_ALIGN, "%s: workspace 256-byte aligned, the other pointers to their element size", fn);
+  return launch_status(launch_verify(logits, draft_logits, lt, token, start, temperature, u, u_sample, M, R, V, accepted,
+                                     next_token, workspace, S(stream)), fn);
+}
+
 }  // extern "C"

@@ -170,6 +170,24 @@ cudaError_t launch_lora_add(const void* x, bl_dtype xt, const int32_t* adapter, 
 cudaError_t launch_lora_tile(const void* x, bl_dtype xt, const int32_t* adapter, const uint16_t* a, const uint16_t* b,
                              const float* scale, const void* base, void* y, bl_dtype yt, int64_t M, int64_t N,
                              int64_t K, int64_t adapters, int rank, cudaStream_t s);
+// The paged key-value cache and what works on it (csrc/page_map.cu, rope_append.cu, attn_paged.cu, verify.cu).
+cudaError_t launch_page_map(const int32_t* length, const int32_t* count, int32_t* table, const int32_t* owned,
+                            int32_t* free_pages, const int32_t* free_count, int64_t R, int64_t W, int64_t pages, int page,
+                            int64_t M, int32_t* start, int32_t* position, int32_t* slot, int32_t* length_out,
+                            int32_t* owned_out, int32_t* free_left, cudaStream_t s);
+cudaError_t launch_rope_append(const void* qkv, bl_dtype xt, const float* cos, const float* sin, const int32_t* position,
+                               const int32_t* slot, int64_t M, int H, int Hk, int D, int rotary, int64_t positions,
+                               uint16_t* q, uint16_t* k_cache, uint16_t* v_cache, int64_t pages, int page, cudaStream_t s);
+size_t attn_paged_workspace(int64_t M, int H, int Hk, int D);
+cudaError_t launch_attn_paged(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache, const int32_t* table,
+                              const int32_t* length, const int32_t* start, float scale, int64_t window, int64_t sinks,
+                              int64_t M, int64_t R, int H, int Hk, int D, int64_t pages, int page, int64_t W, void* out,
+                              bl_dtype ot, uint8_t* ws, cudaStream_t s);
+// draft_logits and temperature may be nullptr
+size_t verify_workspace(int64_t M);
+cudaError_t launch_verify(const void* logits, const void* draft_logits, bl_dtype lt, const int32_t* token,
+                          const int32_t* start, const float* temperature, const float* u, const float* u_sample, int64_t M,
+                          int64_t R, int64_t V, int32_t* accepted, int32_t* next, void* ws, cudaStream_t s);
 // Sampling (csrc/sample_bf16.cu, csrc/sample_f32.cu); the arguments are in sample_common.cuh.
 struct SampleArgs;
 cudaError_t launch_sample_bf16(const SampleArgs& args, cudaStream_t s);

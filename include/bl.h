@@ -488,6 +488,156 @@ bl_status bl_sample(const void* logits, bl_dtype lt, const float* temperature, c
                     const float* top_p, const float* min_p, const float* u, int64_t M, int64_t V, int32_t* token,
                     float* prob, bl_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* A decode step over a paged key-value cache.                                */
+/* (The library's own additions as well.)                                     */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A request's tokens lie in pages of `page` tokens; table[r][i] (int32 [R, W])
+ * is the page of its tokens i * page .. (i + 1) * page - 1.  The caches are
+ * bf16 [pages, Hk, page, D]; slot = page number * page + offset names a token's
+ * place in them.  The new tokens of all requests of a step are rows 0 .. M - 1
+ * of its tensors, request r's from start[r] to start[r + 1] (int32 [R + 1]);
+ * rows behind the last request's (a batch padded to a captured size) are left
+ * alone.
+ *
+ * Block tables, positions and slots of a step's new tokens, with the pages
+ * that they need from a stack of free ones, in the order of the requests:
+ *   ask[r]   = max(0, ceil((length[r] + count[r]) / page) - owned[r])
+ *   the k-th page asked for is free_pages[free_count - 1 - k]; it becomes the
+ *   next entry of its request's row of the table.
+ *   start    = the sums of count before each request (and of all at the end)
+ *   for token i of request r:  position[i] = length[r] + i - start[r],
+ *   slot[i] = table[r][position / page] * page + position % page;
+ *   both are -1 for rows behind the last request's.
+ *   length_out = length + count; owned_out = owned + pages received;
+ *   free_left = pages left on the stack.
+ * A negative count ends a request: it has no new tokens, its owned pages go
+ * back on top of the stack (after all requests have taken theirs; in the order
+ * of the requests and of their tables), length_out and owned_out become 0.
+ * A request may own more pages than its length needs (drafts that were
+ * refused); they are used first.
+ * Without a page (the stack is empty, or W entries do not hold the request)
+ * a token has slot -1 and its entry, if any, becomes -1; that sets
+ * BL_DEVERR_RANGE, and so do a negative length, an owned or free_count outside
+ * [0, W] or [0, pages] (both are brought into the range), more than M new
+ * tokens (those behind M are left out), pages returned beyond `pages` (left
+ * out), and a table entry >= pages that a new token lies in.
+ *   length, count, owned : int32 [R];  table : int32 [R, W], updated in place;
+ *   free_pages : int32 [pages], updated in place where requests end;
+ *   free_count : int32 [1];  start : int32 [R + 1];  position, slot : int32
+ *   [M];  length_out, owned_out : int32 [R], may be length and owned;
+ *   free_left : int32 [1], may be free_count.  No other two may overlap.
+ * Requires R, W, pages, page, M >= 1, pages * page < 2^31 (BL_ERR_UNSUPPORTED
+ * above); pointers 4-byte aligned.
+ */
+bl_status bl_page_map(const int32_t* length, const int32_t* count, int32_t* table, const int32_t* owned,
+                      int32_t* free_pages, const int32_t* free_count, int64_t R, int64_t W, int64_t pages, int page,
+                      int64_t M, int32_t* start, int32_t* position, int32_t* slot, int32_t* length_out, int32_t* owned_out,
+                      int32_t* free_left, bl_stream_t stream);
+
+/*
+ * Rotary positions of q and k, and the cache's new rows, in one launch.  A row
+ * of qkv holds a token's H heads of q, then Hk of k, then Hk of v, each of D
+ * values.  For the q and k heads, i < rotary / 2, p = position[token]:
+ *   y[i]              = x[i] cos[p][i] - x[i + rotary / 2] sin[p][i]
+ *   y[i + rotary / 2] = x[i + rotary / 2] cos[p][i] + x[i] sin[p][i]
+ * and y[i] = x[i] from rotary on; in fp32, rounded to bf16 once.  q goes to
+ * q_bf16, k and v (rounded to bf16) to the caches at slot[token].
+ *   qkv : [M, (H + 2 Hk) D] fp32 or bf16 (xt).  cos, sin : fp32 [positions,
+ *   rotary / 2].  position, slot : int32 [M].  q_bf16 : bf16 [M, H, D].
+ *   k_cache, v_cache : bf16 [pages, Hk, page, D].
+ * A negative position marks a row without a token: nothing of it is written.
+ * A negative slot stores nothing in the caches (q is written).  A position
+ * >= positions (nothing is written) and a slot >= pages * page (nothing is
+ * stored) set BL_DEVERR_RANGE.  Of two tokens with one slot either may be the
+ * one that stays, value by value.
+ * Requires M, H, Hk, positions, pages, page >= 1, D % 8 == 0, 8 <= D <= 1024,
+ * rotary even, 2 <= rotary <= D, pages * page < 2^31; qkv, q and the caches
+ * 16-byte aligned, the others 4-byte aligned.  rotary % 16 == 0 and 16-byte
+ * aligned cos and sin take vector loads.
+ */
+bl_status bl_rope_append(const void* qkv, bl_dtype xt, const float* cos, const float* sin, const int32_t* position,
+                         const int32_t* slot, int64_t M, int H, int Hk, int D, int rotary, int64_t positions,
+                         uint16_t* q_bf16, uint16_t* k_cache, uint16_t* v_cache, int64_t pages, int page,
+                         bl_stream_t stream);
+
+/*
+ * Attention of the new tokens of R requests over their cached ones.  length[r]
+ * counts the request's tokens in the cache, the new ones (rows start[r] ..
+ * start[r + 1] - 1) among them, as its last; the t-th new token is at p =
+ * length[r] - n + t.  For each of its heads h, with key-value head h / (H / Hk):
+ *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale q . k_j - max),
+ * over the tokens j <= p that it sees: all of them if window = 0, otherwise
+ * those with j > p - window or j < sinks.
+ * A token on a page outside [0, pages), or behind the table's W pages, is left
+ * out and sets BL_DEVERR_RANGE (as do a negative length and a start outside
+ * 0 .. M or falling).  A row that sees no token, or whose scores are all -inf,
+ * gives 0.  Infinities and NaN in tokens that a row does not see, in the rest
+ * of a page and in other rows do not reach it.
+ * Any number of new tokens is computed, but the kernel is made for few
+ * (a decode step, drafts): every 16 or 32 rows (new tokens times H / Hk) read
+ * the request's cache again.
+ *   q_bf16 : bf16 [M, H, D].  k_cache, v_cache : bf16 [pages, Hk, page, D].
+ *   table : int32 [R, W].  length : int32 [R].  start : int32 [R + 1].
+ *   out : [M, H, D] fp32 or bf16 (ot).
+ *   workspace : at least bl_attn_paged_workspace(M, H, Hk, D) bytes, 256-byte
+ *   aligned; its contents do not matter and nothing is kept in it between
+ *   calls.  Calls that share one must not overlap on the GPU.
+ * Products are bf16 with fp32 sums; weights enter the second product in 16
+ * bits for bf16 results and 24 for fp32 ones, and the running maximum, sum and
+ * weighted sum are fp32.  Which warp takes which tokens depends on the lengths
+ * and the device's number of SMs, so sums are the same from call to call but
+ * not between batches.
+ * Requires M, R, pages, page, W >= 1, H % Hk == 0, H <= 65536, D % 8 == 0,
+ * 8 <= D <= 256, window, sinks >= 0, pages * page < 2^31; q, caches and out
+ * 16-byte aligned, the others 4-byte aligned.
+ */
+size_t bl_attn_paged_workspace(int64_t M, int H, int Hk, int D);
+bl_status bl_attn_paged(const uint16_t* q_bf16, const uint16_t* k_cache, const uint16_t* v_cache, const int32_t* table,
+                        const int32_t* length, const int32_t* start, float scale, int64_t window, int64_t sinks, int64_t M,
+                        int64_t R, int H, int Hk, int D, int64_t pages, int page, int64_t W, void* out, bl_dtype ot,
+                        void* workspace, size_t workspace_bytes, bl_stream_t stream);
+
+/*
+ * Verification of drafted tokens, from given uniform numbers.  Request r has
+ * rows start[r] .. start[r + 1] - 1: its last known token and behind it the
+ * drafted ones (token).  Row i of logits is the model's answer to token[i], so
+ * it judges the draft x = token[i + 1] of the same request.  With p and q the
+ * softmax of row i of logits and of draft_logits, both divided by the
+ * request's temperature:
+ *   the draft is accepted if u[i] q(x) < p(x); the first that is not ends it.
+ *   accepted[r]   = drafts accepted.
+ *   next_token[r] = one token more, from max(p - q, 0) of the row where a
+ *                   draft was refused, from p of the last row otherwise: the
+ *                   first token, in the vocabulary's order, at which the sum
+ *                   of these exceeds u_sample[r] times their total.
+ * Without draft_logits the drafts are taken as certain: q is 1 at x.  Where
+ * nothing is left of max(p - q, 0), p is taken.  Weights are as in bl_sample:
+ * NaN counts as -inf, a temperature below 1e-5 (or NaN) leaves the maxima;
+ * the uniform numbers are clamped to [0, 1), NaN to 0.  Filters are set by -inf in the
+ * logits.  A row without a logit above -inf refuses its draft, and its token
+ * is -1, as is that of a request without rows (accepted 0).  A draft outside
+ * [0, V) is refused and sets BL_DEVERR_RANGE, as does a start outside 0 .. M
+ * or falling.
+ * The test of acceptance is made in fp32 (2^-20 of p and q); the sums that the
+ * token is found by are sums of integers, with weights within 2^-21 of their
+ * value, those above 2^-8 of the largest within 2^-30.
+ *   logits, draft_logits : [M, V] fp32 or bf16 (lt); draft_logits may be NULL
+ *   (its last row of a request is not read).  token : int32 [M].  temperature :
+ *   fp32 [R] or NULL (1).  u : fp32 [M].  u_sample : fp32 [R].
+ *   accepted, next_token : int32 [R].
+ *   workspace : at least bl_verify_workspace(M) bytes, 256-byte aligned; its
+ *   contents do not matter.  Calls that share one must not overlap on the GPU.
+ * Requires M, R >= 1, 1 <= V <= 524288, M and R < 2^26 (BL_ERR_UNSUPPORTED
+ * above); pointers aligned to their element size.
+ */
+size_t bl_verify_workspace(int64_t M);
+bl_status bl_verify(const void* logits, const void* draft_logits, bl_dtype lt, const int32_t* token, const int32_t* start,
+                    const float* temperature, const float* u, const float* u_sample, int64_t M, int64_t R, int64_t V,
+                    int32_t* accepted, int32_t* next_token, void* workspace, size_t workspace_bytes, bl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
