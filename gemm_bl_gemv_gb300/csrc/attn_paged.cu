@@ -10,8 +10,9 @@
 // it fetches its tiles by asynchronous copies into its own ring of shared memory,
 // several tiles ahead and across units, and keeps the running maximum, sum and
 // weighted sum of a unit's rows in registers.  A unit inside one warp's stretch is
-// written out at once; of a unit cut by stretches each warp leaves its part in the
-// workspace, and a second kernel joins the parts.
+// written out at once.  The parts of a unit that is cut by stretches are joined by
+// the CTA, where the warps' rings have room for them by then, and those of a unit
+// that is cut between CTAs by a second kernel, from the workspace.
 //
 // The products run on mma.sync m16n8k16 (bf16, fp32 sums): up to 16 rows of queries
 // against the tile.  They are bound by the cache's bytes: at the measured copy rate an
@@ -20,6 +21,8 @@
 // The tensor core cuts its sums off instead of rounding them, so a tile's weighted
 // sum starts from zero and is added to the running one in fp32.  The weights go in
 // as two bf16 terms (16 bits) for bf16 results, three (24 bits) for fp32 ones.
+#include <cmath>
+
 #include "bl_device.cuh"
 #include "bl_internal.h"
 #include "paged.cuh"
@@ -28,16 +31,36 @@ namespace bl {
 namespace {
 
 constexpr int kMostCtas = 160;  // of the first kernel, for the size of the workspace
-constexpr int kMostWarps = 8;   // of a CTA
+constexpr int kMostWarps = 12;  // of a CTA
 
-// What a warp leaves of the unit that goes on in the next warp's stretch.
+// Rows of a unit: n from row0 on, of a request's new tokens from `token` on and a key-value head.
+struct Unit {
+  int token, head, row0, n;
+};
+// Division of 0 <= n < 2^31 by a number known at launch.
+struct Divisor {
+  uint32_t mul, shift, d;
+  void set(uint32_t by) {  // mul = ceil(2^(31 + shift) / by), 2^(shift - 1) < by <= 2^shift
+    d = by;
+    for (shift = 0; (uint64_t(1) << shift) < by;) ++shift;
+    mul = uint32_t(((uint64_t(1) << (31 + shift)) + by - 1) / by);
+  }
+  __device__ __forceinline__ int quotient(int n) const { return int(__umulhi(2 * uint32_t(n), mul) >> shift); }
+};
+// What a CTA leaves of the unit that goes on in the next CTA's stretch.
 struct __align__(16) Header {
+  Unit unit;
   int present;
-  int token;    // first new token of the request
-  int head;     // key-value head
-  int row0, n;  // the unit's rows: n from row0 on
-  int follow;   // warps after this one that have a part
+  int follow;  // CTAs after this one that have a part
   int pad[2];
+};
+// A warp's part of a unit that is cut by stretches.
+struct Part {
+  bool present, ends;  // ends: the unit's last tile is in it
+  Unit unit;
+  int64_t last;        // the unit's last tile
+  const float2* stat;  // by row: maximum and sum
+  const float* acc;    // [row][D] weighted sums
 };
 
 struct Args {
@@ -45,12 +68,16 @@ struct Args {
   const int32_t *table, *length, *start;
   void* out;
   Header* header;
-  float2* stat;  // (max, sum) of each row of each part
+  float2* stat;  // (max, sum) of each row of each part: two parts of every CTA, then one of every warp
   float* acc;    // weighted sums
   int64_t M, R, pages, W;
   int H, Hk, G, D, page, rows;  // rows: kept of a part
   int64_t window, sinks;
-  float scale;  // times log2(e)
+  float scale;    // |scale| log2(e), of the queries times `sign`
+  uint32_t sign;  // xor on a pair of queries
+  bool zero;      // a scale of 0: so are the queries
+  Divisor by_page, by_group;
+  bool tiled;  // a tile lies within a page
   unsigned int* err;
 };
 
@@ -59,8 +86,8 @@ struct Shape {
   static constexpr int DP = DP_, MT = MT_;
   static constexpr int ROWS = 16 * MT;
   static constexpr int TT = DP == 64 ? 32 : 16;        // tokens of a tile
-  static constexpr int WARPS = DP == 256 ? 4 : 8;
-  static constexpr int STAGES = 3;
+  static constexpr int WARPS = DP == 256 ? 4 : MT == 1 ? 12 : 8;
+  static constexpr int STAGES = WARPS == 12 ? 2 : 3;
   static constexpr int CHUNKS = DP / 8;                // 16-byte chunks of a row
   static constexpr int TILE = TT * DP * 2;             // bytes of a tile of k
   static constexpr int SMEM = WARPS * STAGES * 2 * TILE;
@@ -88,6 +115,12 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same from zero.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // 16 bytes to shared memory, or zeros.
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
@@ -126,6 +159,77 @@ __device__ __forceinline__ Request request_of(const Args& a, int64_t r) {
   return q;
 }
 
+// Where a row of a unit lies in q and out.
+__device__ __forceinline__ int64_t row_at(const Args& a, const Unit& u, int row) {
+  const int t = a.by_group.quotient(u.row0 + row), h = u.row0 + row - t * a.G;
+  return ((int64_t(u.token) + t) * a.H + u.head * a.G + h) * a.D;
+}
+
+// Joins a row's parts by a warp: stat(p) and acc(p) of parts 0..n-1; out(l, top, o) gets the result, lane by lane four
+// columns from 4 lane + 128 i on.
+template <class Stat, class Acc, class Out>
+__device__ __forceinline__ void join_row(const Args& a, int n, Stat stat, Acc acc, Out out) {
+  const int lane = threadIdx.x & 31;
+  float2 s = lane < n ? stat(lane) : make_float2(-INFINITY, 0.f);
+  float top = s.x;
+  for (int p = lane + 32; p < n; p += 32) top = fmaxf(top, stat(p).x);
+  top = warp_max(top);
+  const float base = top == -INFINITY ? 0.f : top;
+  float l = 0.f;
+  float4 o[2] = {};
+  for (int p0 = 0; p0 < n; p0 += 32) {
+    float f = 0.f;
+    if (p0 + lane < n) {
+      if (p0 > 0) s = stat(p0 + lane);
+      f = exp2_fast((s.x - base) * a.scale);
+      l = __fmaf_rn(f, s.y, l);
+    }
+    const int m = min(32, n - p0);
+#pragma unroll 1
+    for (int p = 0; p < m; p += 8) {  // eight loads at a time
+      float4 y[8][2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          y[j][i] = p + j < m && lane + 32 * i < a.D / 4 ? reinterpret_cast<const float4*>(acc(p0 + p + j))[lane + 32 * i]
+                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float fp = __shfl_sync(0xffffffffu, f, (p + j) & 31);
+        if (p + j < m) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            o[i].x = __fmaf_rn(fp, y[j][i].x, o[i].x);
+            o[i].y = __fmaf_rn(fp, y[j][i].y, o[i].y);
+            o[i].z = __fmaf_rn(fp, y[j][i].z, o[i].z);
+            o[i].w = __fmaf_rn(fp, y[j][i].w, o[i].w);
+          }
+        }
+      }
+    }
+  }
+  l = warp_sum(l);
+  out(l, top, o);
+}
+
+// The row's result, of a joined row.
+template <bool F32>
+__device__ __forceinline__ void store_row(const Args& a, int64_t to, float l, float top, const float4 (&o)[2]) {
+  const int lane = threadIdx.x & 31;
+  const float inv = top == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 32 * i < a.D / 4) {
+      const int64_t d = to + (lane + 32 * i) * 4;
+      if (F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + d) = make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + d) =
+            make_uint2(bf16x2_rn(o[i].x * inv, o[i].y * inv), bf16x2_rn(o[i].z * inv, o[i].w * inv));
+    }
+}
+
 // A place in the sequence of all tiles.
 template <class S>
 struct Place {
@@ -154,10 +258,13 @@ template <class S, bool F32>
 __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args a) {
   constexpr int TT = S::TT, NT = TT / 8, KS = S::DP / 16, MT = S::MT, TERMS = F32 ? 3 : 2;
   constexpr int kThreads = S::WARPS * 32;
+  constexpr uint32_t kAll = TT == 32 ? 0xffffffffu : (1u << TT) - 1;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int64_t before[kThreads + 1];
   __shared__ int64_t warp_total[S::WARPS];
   __shared__ uint32_t real[S::WARPS][S::STAGES];  // tokens of a stage that are there
+  // of every warp: its part of a unit begun before its stretch, and of one that goes on behind it
+  __shared__ Part parts[S::WARPS][2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
   pdl_wait();
@@ -186,13 +293,14 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
     __syncthreads();
   }
   const int64_t all = before[kThreads];
-  const int64_t warps = int64_t(gridDim.x) * S::WARPS;
-  const int64_t quota = max(int64_t(1), (all + warps - 1) / warps);
-  // neighbouring stretches lie on different SMs, so that few tiles spread over all of them
-  const int64_t me = int64_t(warp) * gridDim.x + blockIdx.x;
-  const int64_t t0 = me * quota;
-  const int count = int(max(int64_t(0), min(quota, all - t0)));
-  Header header = {};
+  // equal stretches for the CTAs, and for the warps of a CTA
+  const int64_t quota = max(int64_t(1), (all + gridDim.x - 1) / gridDim.x);
+  const int64_t end = min(all, (blockIdx.x + 1) * quota);
+  const int64_t each = (quota + S::WARPS - 1) / S::WARPS;
+  const int64_t t0 = blockIdx.x * quota + warp * each;
+  const int count = int(max(int64_t(0), min(each, end - t0)));
+  if (lane < 2) parts[warp][lane].present = false;
+  __syncwarp();
 
   if (count > 0) {
     // the first tile
@@ -218,47 +326,71 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
     }
     uint8_t* mine = ring + warp * (S::STAGES * 2 * S::TILE);
 
-    // The row of the cache (page * page size + offset) of this lane's token of a tile, -1: none.
-    auto row_of = [&](const Place<S>& p) {
+    // The page of this lane's token of a tile, -1: none.
+    auto page_of = [&](const Place<S>& p) {
       const int j = p.token() + lane;
       if (lane >= TT || j >= p.q.length || (a.window > 0 && j < p.q.low && j >= a.sinks)) return -1;
-      const int entry = a.table[p.r * a.W + j / a.page];
+      const int entry = a.table[p.r * a.W + a.by_page.quotient(j)];
       if (entry < 0 || entry >= a.pages) {
         bad = true;
         return -1;
       }
       return entry;
     };
-    // Starts the copies of a tile; `entry`: this lane's token's page.
+    // Starts the copies of a tile.  Lane l copies chunk l % CHUNKS of every kRows-th row, from row l / CHUNKS on.
+    constexpr int kRows = 32 / S::CHUNKS;
+    const int chunk = lane % S::CHUNKS, sub = lane / S::CHUNKS;
+    const bool inside = chunk * 8 < a.D;
+    const uint32_t lane_to = sub * (S::DP * 2) + ((chunk ^ sub) * 16);  // of row i + sub: xor of the row's low bits
     auto fetch = [&](const Place<S>& p, int entry, int stage) {
-      const int j = p.token() + lane;
       const unsigned there = __ballot_sync(0xffffffffu, entry >= 0);
       if (lane == 0) real[warp][stage] = there;
-      const int64_t base = entry < 0 ? 0 : ((int64_t(entry) * a.Hk + p.head()) * a.page + j % a.page) * a.D;
-      const uint32_t k = smem_addr(mine + stage * 2 * S::TILE), v = k + S::TILE;
-      constexpr int kRows = 32 / S::CHUNKS;  // rows that the warp copies at a time
-      const int chunk = lane % S::CHUNKS, sub = lane / S::CHUNKS;
+      const int j0 = p.token();
+      const uint32_t k = smem_addr(mine + stage * 2 * S::TILE) + lane_to;
+      if (a.tiled) {
+        const int one = __shfl_sync(0xffffffffu, entry, __ffs(there) - 1);
+        const int64_t at = ((int64_t(max(one, 0)) * a.Hk + p.head()) * a.page + j0 - a.by_page.quotient(j0) * a.page + sub) * a.D + (inside ? chunk * 8 : 0);
+        const uint16_t *kf = a.k + at, *vf = a.v + at;
+        if (there == kAll) {
 #pragma unroll
-      for (int i = 0; i < TT; i += kRows) {
-        const int row = i + sub;
-        const int64_t from = __shfl_sync(0xffffffffu, base, row) + chunk * 8;
-        const bool ok = (there >> row & 1) && chunk * 8 < a.D;
-        const uint32_t to = row * (S::DP * 2) + ((chunk ^ (row & 7)) * 16);
-        copy16(k + to, a.k + (ok ? from : 0), ok);
-        copy16(v + to, a.v + (ok ? from : 0), ok);
+          for (int i = 0; i < TT; i += kRows) {
+            const uint32_t to = (k ^ ((i & 7) * 16)) + i * (S::DP * 2);
+            copy16(to, kf + uint32_t(i * a.D), inside);
+            copy16(to + S::TILE, vf + uint32_t(i * a.D), inside);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < TT; i += kRows) {
+            const uint32_t to = (k ^ ((i & 7) * 16)) + i * (S::DP * 2);
+            const bool ok = (there >> (i + sub) & 1) && inside;
+            copy16(to, kf + (ok ? uint32_t(i * a.D) : 0), ok);
+            copy16(to + S::TILE, vf + (ok ? uint32_t(i * a.D) : 0), ok);
+          }
+        }
+      } else {
+        const int j = j0 + lane;
+        const int64_t base = entry < 0 ? 0 : ((int64_t(entry) * a.Hk + p.head()) * a.page + j - a.by_page.quotient(j) * a.page) * a.D;
+#pragma unroll
+        for (int i = 0; i < TT; i += kRows) {
+          const int64_t from = __shfl_sync(0xffffffffu, base, i + sub) + chunk * 8;
+          const bool ok = (there >> (i + sub) & 1) && inside;
+          const uint32_t to = (k ^ ((i & 7) * 16)) + i * (S::DP * 2);
+          copy16(to, a.k + (ok ? from : 0), ok);
+          copy16(to + S::TILE, a.v + (ok ? from : 0), ok);
+        }
       }
     };
 
     Place<S> ahead = at;
     int fetched = 0;
-    int entry = row_of(ahead);
+    int entry = page_of(ahead);
     auto fetch_next = [&]() {
       if (fetched < count) {
         fetch(ahead, entry, fetched % S::STAGES);
         ++fetched;
         if (fetched < count) {
           ahead.next(a);
-          entry = row_of(ahead);
+          entry = page_of(ahead);
         }
       }
       copies_commit();
@@ -286,16 +418,15 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const int row = mt * 16 + g + s * 8;
-            const int t = (row0 + row) / a.G, h = (row0 + row) % a.G;
-            const uint16_t* q = a.q + ((int64_t(at.q.first) + t) * a.H + head * a.G + h) * a.D;
-            mine_at[mt][s] = at.q.length - at.q.n + t;
+            const uint16_t* q = a.q + row_at(a, {at.q.first, head, row0, nrows}, row);
+            mine_at[mt][s] = at.q.length - at.q.n + a.by_group.quotient(row0 + row);
             top[mt][s] = -INFINITY;
             sum[mt][s] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
               const int d = ks * 16 + c2;
-              qf[mt][ks][s] = row < nrows && d < a.D ? *reinterpret_cast<const uint32_t*>(q + d) : 0;
-              qf[mt][ks][s + 2] = row < nrows && d + 8 < a.D ? *reinterpret_cast<const uint32_t*>(q + d + 8) : 0;
+              qf[mt][ks][s] = row < nrows && d < a.D && !a.zero ? *reinterpret_cast<const uint32_t*>(q + d) ^ a.sign : 0;
+              qf[mt][ks][s + 2] = row < nrows && d + 8 < a.D && !a.zero ? *reinterpret_cast<const uint32_t*>(q + d + 8) ^ a.sign : 0;
             }
           }
 #pragma unroll
@@ -314,12 +445,6 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
       // scores
       float z[MT][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[mt][nt][e] = 0.f;
-#pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int p = 0; p < NT / 2; ++p) {
@@ -328,28 +453,32 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
           ldmatrix4(b, k + row * (S::DP * 2) + ((chunk ^ (row & 7)) * 16));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            mma(z[mt][2 * p], qf[mt][ks], b[0], b[1]);
-            mma(z[mt][2 * p + 1], qf[mt][ks], b[2], b[3]);
+            if (ks == 0) {
+              mma_first(z[mt][2 * p], qf[mt][ks], b[0], b[1]);
+              mma_first(z[mt][2 * p + 1], qf[mt][ks], b[2], b[3]);
+            } else {
+              mma(z[mt][2 * p], qf[mt][ks], b[0], b[1]);
+              mma(z[mt][2 * p + 1], qf[mt][ks], b[2], b[3]);
+            }
           }
         }
       // Every row sees the whole tile, unless it reaches past the first new token, lies at the window's edge or has
       // tokens that are not there.
       const uint32_t there = real[warp][stage];
-      constexpr uint32_t kAll = TT == 32 ? 0xffffffffu : (1u << TT) - 1;
       const bool whole = there == kAll && j0 + TT - 1 <= at.q.length - at.q.n &&
                          (a.window <= 0 || j0 + TT <= a.sinks || j0 > int64_t(at.q.length) - 1 - a.window);
       auto sees = [&](int at_row, int j) {
         return (there >> (j - j0) & 1) && j <= at_row && (a.window <= 0 || j > at_row - a.window || j < a.sinks);
       };
+      if (!whole) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            z[mt][nt][e] *= a.scale;
-            if (!whole && !sees(mine_at[mt][e / 2], j0 + nt * 8 + c2 + (e & 1))) z[mt][nt][e] = -INFINITY;
-          }
+            for (int e = 0; e < 4; ++e)
+              if (!sees(mine_at[mt][e / 2], j0 + nt * 8 + c2 + (e & 1))) z[mt][nt][e] = -INFINITY;
+      }
       // weights
       float keep[MT][2];  // what the sums so far are multiplied by
 #pragma unroll
@@ -362,14 +491,15 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
           const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: all weights are 0
-          keep[mt][s] = exp2_fast(top[mt][s] - base);
+          const float shift = base * a.scale;
+          keep[mt][s] = exp2_fast((top[mt][s] - base) * a.scale);
           top[mt][s] = m;
           float add = 0.f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 2 * s; e < 2 * s + 2; ++e) {
-              z[mt][nt][e] = exp2_fast(z[mt][nt][e] - base);
+              z[mt][nt][e] = exp2_fast(__fmaf_rn(z[mt][nt][e], a.scale, -shift));
               add += z[mt][nt][e];
             }
           sum[mt][s] = __fmaf_rn(sum[mt][s], keep[mt][s], add);
@@ -416,13 +546,18 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            float o0[4] = {0.f, 0.f, 0.f, 0.f}, o1[4] = {0.f, 0.f, 0.f, 0.f};
+            float o0[4], o1[4];
 #pragma unroll
             for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
               for (int p = 0; p < TT / 16; ++p) {
-                mma(o0, w[mt][p][t], b[p][0], b[p][1]);
-                mma(o1, w[mt][p][t], b[p][2], b[p][3]);
+                if (t == TERMS - 1 && p == 0) {
+                  mma_first(o0, w[mt][p][t], b[p][0], b[p][1]);
+                  mma_first(o1, w[mt][p][t], b[p][2], b[p][3]);
+                } else {
+                  mma(o0, w[mt][p][t], b[p][0], b[p][1]);
+                  mma(o1, w[mt][p][t], b[p][2], b[p][3]);
+                }
               }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -473,7 +608,15 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
       const bool ends = at.tile + 1 == at.q.tiles;
       if (ends || i + 1 == count) {
         const bool out = begun && ends;
-        const int64_t part = 2 * me + (begun ? 1 : 0);
+        // the ring is free at the stretch's end; a part that ends before it waits in the workspace
+        const bool final = i + 1 == count;
+        if (final) {
+          copies_wait<0>();
+          __syncwarp();
+        }
+        const int64_t slot = 2 * int64_t(gridDim.x) + blockIdx.x * S::WARPS + warp;
+        float2* stat = final ? reinterpret_cast<float2*>(mine) : a.stat + slot * a.rows;
+        float* sums = final ? reinterpret_cast<float*>(mine + S::ROWS * sizeof(float2)) : a.acc + slot * a.rows * a.D;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -484,8 +627,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
             const int row = mt * 16 + g + s * 8;
             if (row >= nrows) continue;
             if (out) {
-              const int t = (row0 + row) / a.G, h = (row0 + row) % a.G;
-              const int64_t to = ((int64_t(at.q.first) + t) * a.H + head * a.G + h) * a.D;
+              const int64_t to = row_at(a, {at.q.first, head, row0, nrows}, row);
               const float inv = top[mt][s] == -INFINITY && l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
               for (int n = 0; n < 2 * KS; ++n)
@@ -497,87 +639,80 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
                     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to + n * 8 + c2) = bf16x2_rn(x, y);
                 }
             } else {
-              if (lane % 4 == 0) a.stat[part * a.rows + row] = make_float2(top[mt][s], l);
-              float* to = a.acc + (part * a.rows + row) * a.D;
+              if (lane % 4 == 0) stat[row] = make_float2(top[mt][s], l);
+              float* to = sums + row * a.D;
 #pragma unroll
               for (int n = 0; n < 2 * KS; ++n)
                 if (n * 8 < a.D)
                   *reinterpret_cast<float2*>(to + n * 8 + c2) = make_float2(acc[mt][n][2 * s], acc[mt][n][2 * s + 1]);
             }
           }
-        if (begun && !ends) {
-          const int64_t last = t0 + i + (at.q.tiles - 1 - at.tile);  // the unit's last tile
-          header = {1, at.q.first, head, row0, nrows, int(last / quota - me), {0, 0}};
-        }
+        if (!out && lane == 0)
+          parts[warp][begun] = {true, ends, {at.q.first, head, row0, nrows}, t0 + i + (at.q.tiles - 1 - at.tile), stat, sums};
         fresh = true;
       }
       if (i + 1 < count) at.next(a);
     }
-    copies_wait<0>();
   }
-  if (lane == 0) a.header[me] = header;
-  if (__syncthreads_or(bad) && tid == 0) atomicOr(a.err, BL_DEVERR_RANGE);
+  // The units that are cut: each begins with a part that goes on (or, the first, with what an earlier CTA began) and
+  // runs through the next warps' parts.  A warp joins every eighth row of all of them.
+  const bool any_bad = __syncthreads_or(bad);
+  if (any_bad && tid == 0) atomicOr(a.err, BL_DEVERR_RANGE);
+  if (tid == 0) {
+    Header header = {};
+    for (int w = 0; w < S::WARPS; ++w)
+      if (parts[w][1].present && parts[w][1].last >= end) {
+        header.unit = parts[w][1].unit;
+        header.present = 1;
+        header.follow = int(parts[w][1].last / quota - blockIdx.x);
+      }
+    a.header[blockIdx.x] = header;
+  }
+  int task = warp;
+  for (int w0 = -1; w0 < S::WARPS; ++w0) {
+    // w0 = -1: the unit that was begun before this CTA
+    const Part& first = w0 < 0 ? parts[0][0] : parts[w0][1];
+    if (!first.present) continue;
+    int n = 1;
+    if (!first.ends)
+      for (int w = max(w0, 0) + 1; w < S::WARPS && parts[w][0].present; ++w) {
+        ++n;
+        if (parts[w][0].ends) break;
+      }
+    const int from = max(w0, 0);
+    auto part = [&](int p) -> const Part& { return p == 0 ? first : parts[from + p][0]; };
+    for (; task < first.unit.n; task += S::WARPS) {
+      const int row = task;
+      join_row(a, n, [&](int p) { return part(p).stat[row]; }, [&](int p) { return part(p).acc + row * a.D; },
+               [&](float l, float top, const float4(&o)[2]) {
+                 if (w0 >= 0 && first.last < end) {
+                   store_row<F32>(a, row_at(a, first.unit, row), l, top, o);
+                 } else {
+                   const int64_t to = (2 * int64_t(blockIdx.x) + (w0 >= 0)) * a.rows + row;
+                   if (lane == 0) a.stat[to] = make_float2(top, l);
+#pragma unroll
+                   for (int i = 0; i < 2; ++i)
+                     if (lane + 32 * i < a.D / 4) reinterpret_cast<float4*>(a.acc + to * a.D)[lane + 32 * i] = o[i];
+                 }
+               });
+    }
+    task -= first.unit.n;
+  }
   pdl_launch_dependents();
 }
 
-// Joins the parts of the units that were cut: a CTA looks at the headers of 8 warps, a warp takes rows.
+// Joins the parts of the units that are cut between CTAs: a CTA looks at one header, a warp takes rows.
 template <bool F32>
-__global__ void __launch_bounds__(128) attn_join_kernel(const Args a, int64_t warps) {
-  const int lane = threadIdx.x & 31;
-  const int first_row = blockIdx.y * 4 + (threadIdx.x >> 5), step = gridDim.y * 4;
+__global__ void __launch_bounds__(128) attn_join_kernel(const Args a) {
   pdl_wait();
-  for (int64_t w = int64_t(blockIdx.x) * 8; w < min(warps, int64_t(blockIdx.x) * 8 + 8); ++w) {
-    const Header hd = a.header[w];
-    if (!hd.present) continue;
-    const int parts = 1 + hd.follow;
-    // part p: what the first warp left of a unit that begins in it, then what the next ones have of a unit begun before
-    auto part = [&](int p) { return p == 0 ? 2 * w + 1 : 2 * (w + p); };
-    for (int row = first_row; row < hd.n; row += step) {
-      float top = -INFINITY;
-      for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.stat[part(p) * a.rows + row].x);
-      top = warp_max(top);
-      const float base = top == -INFINITY ? 0.f : top;
-      float l = 0.f;
-      float4 o[2] = {};
-      for (int p0 = 0; p0 < parts; p0 += 32) {
-        float f = 0.f;
-        if (p0 + lane < parts) {
-          const float2 s = a.stat[part(p0 + lane) * a.rows + row];
-          f = exp2_fast(s.x - base);
-          l = __fmaf_rn(f, s.y, l);
-        }
-        const int n = min(32, parts - p0);
-#pragma unroll 4
-        for (int p = 0; p < n; ++p) {
-          const float fp = __shfl_sync(0xffffffffu, f, p);
-          const float4* x = reinterpret_cast<const float4*>(a.acc + (part(p0 + p) * a.rows + row) * a.D);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (lane + 32 * i < a.D / 4) {
-              const float4 y = x[lane + 32 * i];
-              o[i].x = __fmaf_rn(fp, y.x, o[i].x);
-              o[i].y = __fmaf_rn(fp, y.y, o[i].y);
-              o[i].z = __fmaf_rn(fp, y.z, o[i].z);
-              o[i].w = __fmaf_rn(fp, y.w, o[i].w);
-            }
-        }
-      }
-      l = warp_sum(l);
-      const float inv = top == -INFINITY && l == 0.f ? 0.f : 1.f / l;
-      const int t = (hd.row0 + row) / a.G, h = (hd.row0 + row) % a.G;
-      const int64_t to = ((int64_t(hd.token) + t) * a.H + hd.head * a.G + h) * a.D;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (lane + 32 * i < a.D / 4) {
-          const int64_t d = to + (lane + 32 * i) * 4;
-          if (F32)
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + d) =
-                make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
-          else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + d) =
-                make_uint2(bf16x2_rn(o[i].x * inv, o[i].y * inv), bf16x2_rn(o[i].z * inv, o[i].w * inv));
-        }
-    }
+  const Header hd = a.header[blockIdx.x];
+  if (hd.present) {
+    // part p: what the first CTA left of a unit that begins in it, then what the next ones have of a unit begun before
+    auto part = [&](int p) { return 2 * int64_t(blockIdx.x + p) + (p == 0); };
+    for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < hd.unit.n; row += gridDim.y * 4)
+      join_row(a, 1 + hd.follow, [&](int p) { return a.stat[part(p) * a.rows + row]; },
+               [&](int p) { return a.acc + (part(p) * a.rows + row) * a.D; },
+               [&](float l, float top, const float4(&o)[2]) { store_row<F32>(a, row_at(a, hd.unit, row), l, top, o); });
   }
   pdl_launch_dependents();
 }
@@ -590,17 +725,18 @@ int part_rows(int64_t M, int H, int Hk, int D) {
 }
 
 template <class S, bool F32>
-cudaError_t launch_as(const Args& a, cudaStream_t s) {
+cudaError_t launch_as(const Args& given, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t e = raise_smem_cap(attn_paged_kernel<S, F32>, dev, S::SMEM);
   if (e != cudaSuccess) return e;
   const int grid = std::min(sm_count(), kMostCtas);
+  Args a = given;
+  a.tiled = a.page % S::TT == 0;
   e = launch(attn_paged_kernel<S, F32>, dim3(grid), dim3(S::WARPS * 32), S::SMEM, s, overlap_enabled(), a);
   if (e != cudaSuccess) return e;
-  const int64_t warps = int64_t(grid) * S::WARPS;
   // The join waits for the whole first kernel, so the two may overlap in either setting.
-  return launch(attn_join_kernel<F32>, dim3(unsigned((warps + 7) / 8), S::ROWS / 4), dim3(128), 0, s, true, a, warps);
+  return launch(attn_join_kernel<F32>, dim3(grid, S::ROWS / 4), dim3(128), 0, s, true, a);
 }
 
 template <bool F32>
@@ -614,9 +750,11 @@ cudaError_t launch_for(const Args& a, cudaStream_t s) {
 
 }  // namespace
 
+constexpr size_t kMostParts = size_t(kMostCtas) * (2 + kMostWarps);
+
 size_t attn_paged_workspace(int64_t M, int H, int Hk, int D) {
-  const size_t warps = size_t(kMostCtas) * kMostWarps, rows = part_rows(M, H, Hk, D);
-  return align256(warps * sizeof(Header)) + align256(2 * warps * rows * sizeof(float2)) + 2 * warps * rows * D * sizeof(float);
+  const size_t rows = part_rows(M, H, Hk, D);
+  return align256(kMostCtas * sizeof(Header)) + align256(kMostParts * rows * sizeof(float2)) + kMostParts * rows * D * sizeof(float);
 }
 
 cudaError_t launch_attn_paged(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache, const int32_t* table,
@@ -628,12 +766,18 @@ cudaError_t launch_attn_paged(const uint16_t* q, const uint16_t* k_cache, const 
   if (!a.err) return cudaErrorUnknown;
   a.M = M, a.R = R, a.pages = pages, a.W = W;
   a.H = H, a.Hk = Hk, a.G = H / Hk, a.D = D, a.page = page, a.rows = part_rows(M, H, Hk, D);
-  a.window = window, a.sinks = sinks, a.scale = scale * 1.4426950408889634f;
-  const size_t warps = size_t(kMostCtas) * kMostWarps;
+  a.window = window, a.sinks = sinks;
+  // The kernel works with a positive factor, whose largest score is the largest sum: the sign goes to the queries, and
+  // with a scale of 0 all of them (times any key) are 0.
+  a.scale = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;
+  a.sign = scale < 0.f ? 0x80008000u : 0u;
+  a.zero = scale == 0.f;
+  a.by_page.set(uint32_t(page));
+  a.by_group.set(uint32_t(a.G));
   a.header = reinterpret_cast<Header*>(ws);
-  ws += align256(warps * sizeof(Header));
+  ws += align256(kMostCtas * sizeof(Header));
   a.stat = reinterpret_cast<float2*>(ws);
-  ws += align256(2 * warps * a.rows * sizeof(float2));
+  ws += align256(kMostParts * a.rows * sizeof(float2));
   a.acc = reinterpret_cast<float*>(ws);
   return ot == BL_F32 ? launch_for<true>(a, s) : launch_for<false>(a, s);
 }

@@ -530,8 +530,8 @@ bl_status bl_attn_paged(const uint16_t* q_bf16, const uint16_t* k_cache, const u
                 "D=%d pages=%lld page=%d W=%lld window=%lld sinks=%lld)",
                 fn, (long long)M, (long long)R, H, Hk, D, (long long)pages, page, (long long)W, (long long)window,
                 (long long)sinks);
-  if (D > 256 || pages > 0x7fffffff / page || H > 65536)
-    return fail(BL_ERR_UNSUPPORTED, "%s: D <= 256, H <= 65536 and pages * page < 2^31 supported", fn);
+  if (D > 256 || pages > 0x7fffffff / page || M > 0x7fffffff / H)
+    return fail(BL_ERR_UNSUPPORTED, "%s: D <= 256, M * H < 2^31 and pages * page < 2^31 supported", fn);
   if (workspace_bytes < bl::attn_paged_workspace(M, H, Hk, D))
     return fail(BL_ERR_SHAPE, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes,
                 bl::attn_paged_workspace(M, H, Hk, D));

@@ -4,9 +4,6 @@
 // for coordinates i and i + rotary / 2, in fp32 and rounded to bf16 once; q goes to
 // q, k and v to row `slot` of the paged cache.
 //
-// An item is VEC pairs of a head, or VEC coordinates that are only copied; a CTA
-// takes the items of a few tokens.
-//
 // Bound: HBM for prompts, launch and two dependent reads (position, angle) for few tokens.
 #include "bl_device.cuh"
 #include "bl_internal.h"
@@ -22,27 +19,31 @@ struct Args {
   const int32_t *position, *slot;
   uint16_t *q, *k, *v;
   int64_t M, positions, slots;
-  int H, Hk, D, half, page, tokens;  // tokens: per CTA
+  int H, Hk, D, half, page;
   unsigned int* err;
 };
 
+// VEC values as they lie in memory.
 template <bool XB, int VEC>
-__device__ __forceinline__ void load(const void* x, int64_t i, float (&v)[VEC]) {
-  if (VEC == 1) {
-    v[0] = XB ? bf16_bits_to_f32(static_cast<const uint16_t*>(x)[i]) : static_cast<const float*>(x)[i];
-  } else if (XB) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+  static constexpr int W = VEC == 1 ? 1 : VEC * (XB ? 2 : 4) / 4;
+  uint32_t u[W];
+  __device__ __forceinline__ void load(const void* x, int64_t i) {
+    if (VEC == 1) {
+      u[0] = XB ? uint32_t(static_cast<const uint16_t*>(x)[i]) << 16 : static_cast<const uint32_t*>(x)[i];
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + i * (XB ? 2 : 4));
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float(j & 1 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
-  } else {
-#pragma unroll
-    for (int j = 0; j < VEC / 4; ++j) {
-      const float4 f = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i)[j];
-      v[4 * j] = f.x, v[4 * j + 1] = f.y, v[4 * j + 2] = f.z, v[4 * j + 3] = f.w;
+      for (int j = 0; j < W / 4; ++j) {
+        const uint4 v = p[j];
+        u[4 * j] = v.x, u[4 * j + 1] = v.y, u[4 * j + 2] = v.z, u[4 * j + 3] = v.w;
+      }
     }
   }
-}
+  __device__ __forceinline__ float get(int j) const {
+    return __uint_as_float(VEC == 1 || !XB ? u[j] : j & 1 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+  }
+};
 
 template <int VEC>
 __device__ __forceinline__ void store(uint16_t* y, int64_t i, const float (&v)[VEC]) {
@@ -56,67 +57,109 @@ __device__ __forceinline__ void store(uint16_t* y, int64_t i, const float (&v)[V
   }
 }
 
+// A token's threads: blockDim.x; thread t turns chunk t % pairs of every few heads, so it reads its angles once.  The
+// first loads of a row go out before its position and slot are there.
 template <bool XB, int VEC>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a) {
-  const int pairs = a.half / VEC, rest = (a.D - 2 * a.half) / VEC;  // items of a turned head
-  const int turned = (a.H + a.Hk) * (pairs + rest), copied = a.Hk * (a.D / VEC);
-  const int items = turned + copied, heads = a.H + 2 * a.Hk;
-  const int64_t first = int64_t(blockIdx.x) * a.tokens;
-  const int mine = int(min(int64_t(a.tokens), a.M - first));
+  constexpr int kTurn = XB ? 4 : 2, kCopy = 2;  // loads in flight
+  const int64_t m = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int t = threadIdx.x, threads = blockDim.x;
+  const int pairs = a.half / VEC, heads = a.H + 2 * a.Hk, turned = a.H + a.Hk;
+  const int groups = max(1, threads / pairs);              // heads that are turned at a time
+  const int group = pairs < threads ? t / pairs : 0;
+  const int rest = (a.D - 2 * a.half) / VEC, all = a.D / VEC;
+  const int first = turned * rest, items = first + a.Hk * all;  // what is only copied: the turned heads' rest, then v
+  const int64_t from = m * heads * a.D;
   bool bad = false;
   pdl_wait();
-  for (int at = threadIdx.x; at < mine * items; at += kThreads) {
-    const int64_t m = first + at / items;
-    const int item = at % items;
+  if (m < a.M) {
     const int position = a.position[m], slot = a.slot[m];
-    if (position < 0) continue;  // no token
-    if (position >= a.positions || slot >= a.slots) bad = true;
-    if (position >= a.positions) continue;
-    int head, i;  // head of the row, coordinate in it
-    bool pair = false;
-    if (item < turned) {
-      const int j = item % (pairs + rest);
-      head = item / (pairs + rest);
-      pair = j < pairs;
-      i = pair ? j * VEC : 2 * a.half + (j - pairs) * VEC;
-    } else {
-      head = a.H + a.Hk + (item - turned) / (a.D / VEC);
-      i = (item - turned) % (a.D / VEC) * VEC;
-    }
-    uint16_t* to = nullptr;
-    if (head < a.H) {
-      to = a.q + (m * a.H + head) * a.D;
-    } else if (slot >= 0 && slot < a.slots) {
-      const int h = head - a.H < a.Hk ? head - a.H : head - a.H - a.Hk;
-      to = (head - a.H < a.Hk ? a.k : a.v) + ((int64_t(slot / a.page) * a.Hk + h) * a.page + slot % a.page) * a.D;
-    }
-    if (!to) continue;
-    const int64_t from = (m * heads + head) * a.D + i;
-    float v[VEC];
-    load<XB, VEC>(a.x, from, v);
-    if (pair) {
-      float w[VEC], c[VEC], s[VEC];
-      load<XB, VEC>(a.x, from + a.half, w);
-      load<false, VEC>(a.cos, int64_t(position) * a.half + i, c);
-      load<false, VEC>(a.sin, int64_t(position) * a.half + i, s);
+    Raw<XB, VEC> v[kTurn], w[kTurn], c[kCopy];
+    auto load_pairs = [&](int h0, int chunk) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float t = __fmaf_rn(v[j], c[j], -__fmul_rn(w[j], s[j]));
-        w[j] = __fmaf_rn(w[j], c[j], __fmul_rn(v[j], s[j]));
-        v[j] = t;
+      for (int k = 0; k < kTurn; ++k)
+        if (h0 + k * groups < turned && group < groups) {
+          const int64_t i = from + int64_t(h0 + k * groups) * a.D + chunk * VEC;
+          v[k].load(a.x, i);
+          w[k].load(a.x, i + a.half);
+        }
+    };
+    auto item = [&](int at, int& head, int& i) {
+      head = at < first ? at / rest : turned + (at - first) / all;
+      i = at < first ? 2 * a.half + at % rest * VEC : (at - first) % all * VEC;
+    };
+    auto load_items = [&](int at0) {
+#pragma unroll
+      for (int k = 0; k < kCopy; ++k)
+        if (at0 + k * threads < items) {
+          int head, i;
+          item(at0 + k * threads, head, i);
+          c[k].load(a.x, from + int64_t(head) * a.D + i);
+        }
+    };
+    const int chunk0 = t % min(pairs, threads);
+    load_pairs(group, chunk0);
+    load_items(t);
+    const bool stored = slot >= 0 && slot < a.slots;
+    bad = position >= a.positions || (position >= 0 && slot >= a.slots);
+    if (position >= 0 && position < a.positions) {
+      const int64_t row = stored ? (int64_t(slot / a.page) * a.Hk * a.page + slot % a.page) * a.D : 0;
+      const int64_t head_rows = int64_t(a.page) * a.D;
+      // where a head's result goes; nullptr: nowhere
+      auto place = [&](int head) -> uint16_t* {
+        if (head < a.H) return a.q + (m * a.H + head) * a.D;
+        if (!stored) return nullptr;
+        return head < turned ? a.k + row + (head - a.H) * head_rows : a.v + row + (head - turned) * head_rows;
+      };
+      for (int chunk = chunk0; chunk < pairs && group < groups; chunk += threads) {  // one chunk, unless a head has more than the threads
+        Raw<false, VEC> cs, sn;
+        cs.load(a.cos, int64_t(position) * a.half + chunk * VEC);
+        sn.load(a.sin, int64_t(position) * a.half + chunk * VEC);
+        for (int h0 = group; h0 < turned; h0 += kTurn * groups) {
+          if (h0 != group || chunk != chunk0) load_pairs(h0, chunk);
+#pragma unroll
+          for (int k = 0; k < kTurn; ++k) {
+            const int head = h0 + k * groups;
+            uint16_t* to = head < turned ? place(head) : nullptr;
+            if (!to) continue;
+            float x[VEC], y[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+              const float p = v[k].get(j), q = w[k].get(j), co = cs.get(j), si = sn.get(j);
+              x[j] = __fmaf_rn(p, co, -__fmul_rn(q, si));
+              y[j] = __fmaf_rn(q, co, __fmul_rn(p, si));
+            }
+            store<VEC>(to, chunk * VEC, x);
+            store<VEC>(to, chunk * VEC + a.half, y);
+          }
+        }
       }
-      store<VEC>(to, i + a.half, w);
+      for (int at0 = t; at0 < items; at0 += kCopy * threads) {
+        if (at0 != t) load_items(at0);
+#pragma unroll
+        for (int k = 0; k < kCopy; ++k)
+          if (at0 + k * threads < items) {
+            int head, i;
+            item(at0 + k * threads, head, i);
+            uint16_t* to = place(head);
+            if (!to) continue;
+            float x[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) x[j] = c[k].get(j);
+            store<VEC>(to, i, x);
+          }
+      }
     }
-    store<VEC>(to, i, v);
   }
-  if (bad) atomicOr(a.err, BL_DEVERR_RANGE);
+  if (bad && t == 0) atomicOr(a.err, BL_DEVERR_RANGE);
   pdl_launch_dependents();
 }
 
 template <bool XB, int VEC>
 cudaError_t launch_as(const Args& a, cudaStream_t s) {
-  const int64_t grid = (a.M + a.tokens - 1) / a.tokens;
-  return launch(rope_append_kernel<XB, VEC>, dim3(unsigned(grid)), dim3(kThreads), 0, s, overlap_enabled(), a);
+  // few tokens: as many threads as a CTA has for each
+  const unsigned per = a.M > 4 * sm_count() ? 64 : kThreads, tokens = kThreads / per;
+  return launch(rope_append_kernel<XB, VEC>, dim3(unsigned((a.M + tokens - 1) / tokens)), dim3(per, tokens), 0, s, overlap_enabled(), a);
 }
 
 }  // namespace
@@ -126,8 +169,7 @@ cudaError_t launch_rope_append(const void* qkv, bl_dtype xt, const float* cos, c
                                uint16_t* q, uint16_t* k_cache, uint16_t* v_cache, int64_t pages, int page, cudaStream_t s) {
   unsigned int* err = dev_error_ptr();
   if (!err) return cudaErrorUnknown;
-  Args a{qkv, cos, sin, position, slot, q, k_cache, v_cache, M, positions, pages * page, H, Hk, D, rotary / 2, page, 1, err};
-  a.tokens = M > 8 * sm_count() ? 4 : 1;
+  const Args a{qkv, cos, sin, position, slot, q, k_cache, v_cache, M, positions, pages * page, H, Hk, D, rotary / 2, page, err};
   const bool wide = a.half % 8 == 0 && ((reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) & 15) == 0;
   if (xt == BL_BF16) return wide ? launch_as<true, 8>(a, s) : launch_as<true, 1>(a, s);
   return wide ? launch_as<false, 8>(a, s) : launch_as<false, 1>(a, s);

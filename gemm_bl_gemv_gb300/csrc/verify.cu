@@ -8,8 +8,12 @@
 // comparisons of two numbers, fp32 will do.  The second kernel takes a cluster per
 // request: it joins the stretches, finds the row where the request stops, and draws
 // from that row.  There the sums' borders between neighbouring tokens count, so the
-// weights are integers (sample_weight.cuh) and their sums exact; for max(p - q, 0)
-// both are brought to units of 2^-60 by an integer reciprocal of their mass.
+// weights are integers in units of 2^-44 and their sums exact; for max(p - q, 0) both
+// are brought to units of 2^-60 by an integer reciprocal of their mass.  A token's own
+// weight need not be better than its stretch of the sum is wide: those below 2^-8 of the
+// largest come from the hardware's exp2 (2^-22, without a bias between them and the
+// others: their exponent is formed from an exact offset), in 10 instructions; the few
+// others from sample_weight.cuh (2^-30), in 40.
 //
 // Bound: HBM and exponentials in the first kernel, instruction issue in the second.
 #include <cfloat>
@@ -24,7 +28,6 @@ namespace {
 
 constexpr int kMassThreads = 256;
 constexpr int kMostStretches = 16;
-constexpr int kC = 8;  // CTAs of a request
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 
 struct Args {
@@ -47,6 +50,53 @@ __device__ __forceinline__ float exp2_fast(float x) {
 template <bool XB>
 __device__ __forceinline__ float logit(const void* x, int64_t i) {
   return XB ? bf16_bits_to_f32(static_cast<const uint16_t*>(x)[i]) : static_cast<const float*>(x)[i];
+}
+
+// f(v, i) for elements [from, to) of MATS rows at x[m] + base, shared by n threads (this is the t-th): v[m] holds the
+// elements i, i + 1, ... of row m, as many as 16 bytes have, or one at the ends.  The rows' addresses are equal modulo 16
+// (`wide`), or every element comes by itself.  Several loads are in flight.
+template <bool XB, int MATS, class F>
+__device__ __forceinline__ void each(const void* const (&x)[2], bool wide, int64_t base, int from, int to, int t, int n, F f) {
+  constexpr int E = XB ? 8 : 4, kAtOnce = MATS == 1 ? 4 : 2;
+  const int off = int((reinterpret_cast<uintptr_t>(x[0]) / (XB ? 2 : 4) + uint64_t(base) + uint64_t(from)) % E);
+  const int body = wide ? min(to, from + (E - off) % E) : to;  // of [from, to): from here on 16-byte words
+  const int words = (to - body) / E, tail = body + words * E;
+  for (int i = t; i < body - from + to - tail; i += n) {
+    const int at = i < body - from ? from + i : tail + i - (body - from);
+    float v[MATS][1];
+#pragma unroll
+    for (int m = 0; m < MATS; ++m) v[m][0] = logit<XB>(x[m], base + at);
+    f(v, at);
+  }
+  for (int w0 = t; w0 < words; w0 += kAtOnce * n) {
+    uint4 raw[kAtOnce][MATS];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+        if (w0 + j * n < words)
+          raw[j][m] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x[m]) + (base + body + int64_t(w0 + j * n) * E) * (XB ? 2 : 4));
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if (w0 + j * n < words) {
+        float v[MATS][E];
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          const uint32_t u[4] = {raw[j][m].x, raw[j][m].y, raw[j][m].z, raw[j][m].w};
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[m][e] = __uint_as_float(!XB ? u[e % 4] : e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+        }
+        f(v, body + (w0 + j * n) * E);
+      }
+  }
+}
+template <int N>
+struct Count {
+  static constexpr int n = N;
+};
+template <int MATS, int N>
+__device__ __forceinline__ Count<N> count_of(const float (&)[MATS][N]) {
+  return {};
 }
 
 // log2(e) / temperature; negative: greedy, only the maxima have weight.
@@ -85,9 +135,22 @@ __global__ void __launch_bounds__(kMassThreads) verify_mass_kernel(const Args a)
   if (found >= 0) {
     const float rate = rate_of(a.temperature, found);
     const void* x = mat ? a.drafts : a.logits;
-    const int64_t base = row * a.V, from = a.V * stretch / a.stretches, to = a.V * (stretch + 1) / a.stretches;
+    const int from = int(a.V * stretch / a.stretches), to = int(a.V * (stretch + 1) / a.stretches);
     float2 s = {-FLT_MAX, 0.f};
-    for (int64_t i = from + threadIdx.x; i < to; i += kMassThreads) s = join(s, {logit<XB>(x, base + i), 1.f}, rate);
+    each<XB, 1>({x, x}, true, row * a.V, from, to, threadIdx.x, kMassThreads, [&](auto& v, int) {
+      constexpr int N = decltype(count_of(v))::n;
+      float top = s.x;
+#pragma unroll
+      for (int e = 0; e < N; ++e) top = fmaxf(top, v[0][e]);
+      if (top > s.x) s = make_float2(top, s.y * weight(s.x, top, rate));
+      if (rate < 0.f || top == INFINITY) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s.y += float(v[0][e] == top);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s.y += exp2_fast(fmaxf((v[0][e] - top) * rate, -200.f));  // NaN: 0
+      }
+    });
     for (int o = 16; o > 0; o >>= 1)
       s = join(s, {__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)}, rate);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
@@ -110,6 +173,36 @@ struct Reciprocal {
     shift = 22 - s;
   }
   __device__ __forceinline__ u64 share(u64 w) const { return __umul64hi(w << 19, r) >> shift; }
+};
+
+// Weights of a row's logits beside its largest, in units of 2^-44: light ones, below 2^-8 of the largest, by the
+// hardware's exp2.
+struct Weights {
+  float top;
+  Slope slope;
+  float k, rest;  // top log2(e) / T - 40 = k + rest
+  bool none, few;  // no logit above -inf; greedy or an infinity, where only the largest have weight
+
+  __device__ __forceinline__ void set(float largest, Slope s) {
+    top = largest;
+    slope = s;
+    none = top == -INFINITY;
+    few = s.hi < 0.f || top == INFINITY;
+    const float p = __fmul_rn(top, s.hi);
+    k = __fsub_rn(p, 40.f);
+    // what the two roundings left, and the slope's lower part
+    const float z = __fsub_rn(k, p);
+    rest = __fsub_rn(p, __fsub_rn(k, z)) - __fadd_rn(40.f, z);
+    rest += __fmaf_rn(top, s.hi, -p) + __fmul_rn(top, s.lo);
+  }
+  // log2 of the weight in units of 2^-40; not below 32 (or NaN) where the weight is not light
+  __device__ __forceinline__ float light(float l) const {
+    l = fmaxf(l, -FLT_MAX);  // NaN and -inf
+    return __fmaf_rn(l, slope.hi, -k) + __fmaf_rn(l, slope.lo, -rest);
+  }
+  __device__ __forceinline__ u64 full(float l, const Exp2Table& t) const {
+    return none ? 0ull : few ? u64(l == top) << kWeightBits : weight_of(l, top, slope, t);
+  }
 };
 
 // What a CTA shows the others of its cluster.
@@ -138,11 +231,12 @@ __device__ __forceinline__ u64 cta_sum(u64 v, u64* warps) {
   return s;
 }
 
-template <bool XB>
+template <bool XB, int kC>  // kC: CTAs of a request
 __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
   __shared__ Shared sh;
   const int64_t r = blockIdx.x / kC;
-  const uint32_t rank = cluster_ctarank();
+  const int rank = kC == 1 ? 0 : int(cluster_ctarank());
+  auto of = [&](auto* p, int c) { return kC == 1 ? p : peer(p, c); };  // p in CTA c's shared memory
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   fill_exp2_table(sh.exp2);
   pdl_wait();
@@ -179,65 +273,145 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
     if (!(double(u > 0.f ? fminf(u, 0.99999994f) : 0.f) * qx < px)) atomicMin(&sh.shown.stop, j);
   }
   sync_cluster<kC>();
-  const Shown* first = peer(&sh.shown, 0);  // one CTA decides for all
+  const Shown* first = of(&sh.shown, 0);  // one CTA decides for all
   const int n = first->n, stop = first->stop;
   const bool refused = stop < n - 1;
   const int64_t row = int64_t(first->first) + stop, base = row * a.V;
   const int from = int(a.V * rank / kC), to = int(a.V * (rank + 1) / kC);
-  // this warp's part of the CTA's
-  const int wfrom = from + int(int64_t(to - from) * warp / kWarps), wto = from + int(int64_t(to - from) * (warp + 1) / kWarps);
+  // where warp w's part of [f, e) begins
+  auto part = [](int f, int e, int w) { return f + int(int64_t(e - f) * w / kWarps); };
   const bool both = refused && a.drafts;
   const Slope slope = slope_of(t);
 
   if (n > 0) {
+    const void* const x[2] = {a.logits, both ? a.drafts : a.logits};
+    const bool wide = ((reinterpret_cast<uintptr_t>(x[0]) ^ reinterpret_cast<uintptr_t>(x[1])) & 15) == 0;
+    const void* const xd[2] = {x[1], x[1]};
     float top[2] = {-INFINITY, -INFINITY};
     for (int m = 0; m < 2; ++m) {
       if (m == 1 && !both) break;
-      const void* x = m ? a.drafts : a.logits;
-      float v = -INFINITY;
-      for (int i = from + tid; i < to; i += kThreads) v = fmaxf(v, logit<XB>(x, base + i));
-      v = warp_max(v);
+      float most = -INFINITY;
+      each<XB, 1>(m ? xd : x, true, base, from, to, tid, kThreads, [&](auto& v, int) {
+#pragma unroll
+        for (int e = 0; e < decltype(count_of(v))::n; ++e) most = fmaxf(most, v[0][e]);
+      });
+      most = warp_max(most);
       __syncthreads();
-      if (lane == 0) sh.redf[warp] = v;
+      if (lane == 0) sh.redf[warp] = most;
       __syncthreads();
-      for (int w = 0; w < kWarps; ++w) v = fmaxf(v, sh.redf[w]);
-      if (tid == 0) sh.shown.top[m] = v;
+      for (int w = 0; w < kWarps; ++w) most = fmaxf(most, sh.redf[w]);
+      if (tid == 0) sh.shown.top[m] = most;
     }
     sync_cluster<kC>();
-    for (int m = 0; m < 2; ++m)
+    Weights w[2];
+    for (int m = 0; m < 2; ++m) {
       if (m == 0 || both)
-        for (uint32_t c = 0; c < kC; ++c) top[m] = fmaxf(top[m], *peer(&sh.shown.top[m], c));
-    auto weight_at = [&](int m, int i) {
-      return top[m] == -INFINITY ? 0ull : weight_of(logit<XB>(m ? a.drafts : a.logits, base + i), top[m], slope, sh.exp2);
+        for (int c = 0; c < kC; ++c) top[m] = fmaxf(top[m], *of(&sh.shown.top[m], c));
+      w[m].set(top[m], slope);
+    }
+    // The sum of the weights of 16 bytes of logits.
+    auto weigh = [&](const Weights& w, const auto& l) {
+      constexpr int N = sizeof(l) / sizeof(float);
+      float y[N], most = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        y[e] = w.light(l[e]);
+        most = y[e] < 32.f ? most : 64.f;
+      }
+      u64 s = 0;
+      if (w.few || w.none) {
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) n += l[e] == w.top;
+        return w.none ? 0 : u64(n) << kWeightBits;
+      }
+      if (most < 32.f) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s += __float2uint_rn(exp2_fast(y[e]));
+        return s << 4;
+      }
+#pragma unroll 1
+      for (int e = 0; e < N; ++e) {
+        float le = l[0], ye = y[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) le = e == i ? l[i] : le, ye = e == i ? y[i] : ye;
+        s += ye < 32.f ? u64(__float2uint_rn(exp2_fast(ye))) << 4 : w.full(le, sh.exp2);
+      }
+      return s;
     };
     u64 mass[2] = {0, 0};
     if (both) {
       for (int m = 0; m < 2; ++m) {
         u64 s = 0;
-        for (int i = from + tid; i < to; i += kThreads) s += weight_at(m, i);
+        each<XB, 1>(m ? xd : x, true, base, from, to, tid, kThreads, [&](auto& v, int) { s += weigh(w[m], v[0]); });
         s = cta_sum(s, sh.warps);
         if (tid == 0) sh.shown.mass[m] = s;
       }
       sync_cluster<kC>();
       for (int m = 0; m < 2; ++m)
-        for (uint32_t c = 0; c < kC; ++c) mass[m] += *peer(&sh.shown.mass[m], c);
+        for (int c = 0; c < kC; ++c) mass[m] += *of(&sh.shown.mass[m], c);
+      if (tid < 2) sh.share[tid].set(mass[tid]);
+      __syncthreads();
     }
-    if (tid < 2) sh.share[tid].set(mass[tid]);
-    __syncthreads();
-    const int x = refused ? a.token[row + 1] : -1;
-    const Reciprocal rp = sh.share[0], rq = sh.share[1];
-    // attempt 0: what p has over q; 1: p, where nothing is left
-    auto rest_at = [&](int attempt, int i) {
-      const u64 w = weight_at(0, i);
-      if (attempt == 1 || !refused) return w;
-      if (!both) return i == x ? 0ull : w;
-      const u64 p = rp.share(w), q = rq.share(weight_at(1, i));
-      return p > q ? p - q : 0ull;
+    const int drafted = refused ? a.token[row + 1] : -1;
+    // light weights of p and q in units of 2^-40 of the masses
+    constexpr float kOne = float(1ull << kWeightBits);
+    const float fp = mass[0] ? kOne / float(mass[0]) : 0.f, fq = mass[1] ? kOne / float(mass[1]) : 0.f;
+    // One token's share of what is drawn from: attempt 0: what p has over q; 1: p, where nothing is left.
+    auto rest_at = [&](int attempt, float lp, float lq, int i) {
+      const float yp = w[0].light(lp);
+      const bool light = yp < 32.f && !w[0].few && !w[0].none;
+      if (attempt == 1 || !both) {
+        if (attempt == 0 && i == drafted) return u64(0);
+        return light ? u64(__float2uint_rn(exp2_fast(yp))) << 4 : w[0].full(lp, sh.exp2);
+      }
+      const float yq = w[1].light(lq);
+      const bool light_q = yq < 32.f && !w[1].few && !w[1].none;
+      if (light && light_q) return u64(__float2uint_rn(__fmaf_rn(exp2_fast(yp), fp, -__fmul_rn(exp2_fast(yq), fq)))) << 20;
+      const u64 p = sh.share[0].share(light ? u64(__float2uint_rn(exp2_fast(yp))) << 4 : w[0].full(lp, sh.exp2));
+      const u64 q = sh.share[1].share(light_q ? u64(__float2uint_rn(exp2_fast(yq))) << 4 : w[1].full(lq, sh.exp2));
+      return p > q ? p - q : u64(0);
+    };
+    const u64 few_only = both ? sh.share[0].share(1ull << kWeightBits) : 0, few_q = both ? sh.share[1].share(1ull << kWeightBits) : 0;
+    const u64 few_both = few_only > few_q ? few_only - few_q : 0;
+    // The sum of those of [f, e), by a warp.
+    auto sum_of = [&](int attempt, int f, int e) {
+      u64 s = 0;
+      if (attempt == 1 || !both) {
+        each<XB, 1>(x, true, base, f, e, lane, 32, [&](auto& v, int i) {
+          constexpr int N = decltype(count_of(v))::n;
+          if (attempt == 0 && drafted >= i && drafted < i + N) {
+#pragma unroll 1
+            for (int j = 0; j < N; ++j) s += rest_at(0, logit<XB>(x[0], base + i + j), 0.f, i + j);
+          } else {
+            s += weigh(w[0], v[0]);
+          }
+        });
+      } else {
+        each<XB, 2>(x, wide, base, f, e, lane, 32, [&](auto& v, int i) {
+          constexpr int N = decltype(count_of(v))::n;
+          float yp[N], yq[N], most = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            yp[j] = w[0].light(v[0][j]);
+            yq[j] = w[1].light(v[1][j]);
+            most = yp[j] < 32.f && yq[j] < 32.f ? most : 64.f;
+          }
+          if (most < 32.f && !w[0].few && !w[0].none && !w[1].few && !w[1].none) {
+            u64 t = 0;
+#pragma unroll
+            for (int j = 0; j < N; ++j) t += __float2uint_rn(__fmaf_rn(exp2_fast(yp[j]), fp, -__fmul_rn(exp2_fast(yq[j]), fq)));
+            s += t << 20;
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < N; ++j) s += rest_at(0, logit<XB>(x[0], base + i + j), logit<XB>(x[1], base + i + j), i + j);
+          }
+        });
+      }
+      return warp_sum_u64(s);
     };
     for (int attempt = 0; attempt < 2; ++attempt) {
-      u64 s = 0;
-      for (int i = wfrom + lane; i < wto; i += 32) s += rest_at(attempt, i);
-      s = warp_sum_u64(s);
+      const u64 s = sum_of(attempt, part(from, to, warp), part(from, to, warp + 1));
       __syncthreads();
       if (lane == 0) sh.warps[warp] = s;
       __syncthreads();
@@ -248,8 +422,8 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
       }
       sync_cluster<kC>();
       u64 all = 0, before = 0, mine = 0;
-      for (uint32_t c = 0; c < kC; ++c) {
-        const u64 v = *peer(&sh.shown.rest[attempt], c);
+      for (int c = 0; c < kC; ++c) {
+        const u64 v = *of(&sh.shown.rest[attempt], c);
         if (c < rank) before += v;
         if (c == rank) mine = v;
         all += v;
@@ -263,12 +437,22 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
       const u64 target = mass_target(us > 0.f ? fminf(us, 0.99999994f) : 0.f, all);
       if (before <= target && target < before + mine) {  // in this CTA's part
         u64 at = before;
-        int w = 0;
-        while (at + sh.warps[w] <= target) at += sh.warps[w++];
-        const int f = from + int(int64_t(to - from) * w / kWarps), e = from + int(int64_t(to - from) * (w + 1) / kWarps);
-        __syncthreads();  // sh.warps has been read
+        int f = from, e = to;
+        while (true) {  // the warp's part that has it, cut again while it is long
+          int in = 0;
+          while (at + sh.warps[in] <= target) at += sh.warps[in++];
+          const int nf = part(f, e, in), ne = part(f, e, in + 1);
+          f = nf;
+          e = ne;
+          __syncthreads();  // sh.warps has been read
+          if (e - f <= 2 * kThreads) break;
+          const u64 t = sum_of(attempt, part(f, e, warp), part(f, e, warp + 1));
+          if (lane == 0) sh.warps[warp] = t;
+          __syncthreads();
+        }
         for (int i0 = f; i0 < e; i0 += kThreads) {
-          const u64 v = i0 + tid < e ? rest_at(attempt, i0 + tid) : 0ull;
+          const int64_t i = base + i0 + tid;
+          const u64 v = i0 + tid < e ? rest_at(attempt, logit<XB>(x[0], i), logit<XB>(x[1], i), i0 + tid) : 0ull;
           const u64 through = warp_scan(v);
           if (lane == 31) sh.warps[warp] = through;
           __syncthreads();
@@ -293,6 +477,12 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
   pdl_launch_dependents();
 }
 
+// It waits for the whole first kernel, so the two may overlap in either setting.
+template <bool XB, int C>
+cudaError_t launch_draw(const Args& a, cudaStream_t s) {
+  return launch_cluster(verify_draw_kernel<XB, C>, C, dim3(unsigned(a.R * C)), dim3(kThreads), 0, s, true, a);
+}
+
 }  // namespace
 
 size_t verify_workspace(int64_t M) { return size_t(M) * 2 * kMostStretches * sizeof(float2); }
@@ -306,13 +496,15 @@ cudaError_t launch_verify(const void* logits, const void* draft_logits, bl_dtype
   const int mats = draft_logits ? 2 : 1;
   a.stretches = int(std::max<int64_t>(1, std::min<int64_t>({kMostStretches, 8 * sm_count() / (M * mats), V / 4096})));
   const bool pdl = overlap_enabled();
+  const bool xb = lt == BL_BF16;
   const dim3 grid(unsigned(M * mats * a.stretches));
-  const cudaError_t e = lt == BL_BF16 ? launch(verify_mass_kernel<true>, grid, dim3(kMassThreads), 0, s, pdl, a)
-                                      : launch(verify_mass_kernel<false>, grid, dim3(kMassThreads), 0, s, pdl, a);
+  const cudaError_t e = xb ? launch(verify_mass_kernel<true>, grid, dim3(kMassThreads), 0, s, pdl, a)
+                           : launch(verify_mass_kernel<false>, grid, dim3(kMassThreads), 0, s, pdl, a);
   if (e != cudaSuccess) return e;
-  // The second kernel waits for the whole first one, so the two may overlap in either setting.
-  return lt == BL_BF16 ? launch_cluster(verify_draw_kernel<true>, kC, dim3(unsigned(R * kC)), dim3(kThreads), 0, s, true, a)
-                       : launch_cluster(verify_draw_kernel<false>, kC, dim3(unsigned(R * kC)), dim3(kThreads), 0, s, true, a);
+  // a row in c CTAs: some passes over its share, and the exchanges
+  const int c = ctas_per_row(R, [&](int c) { return 6.0 + 4.0 * (c > 1) + double(V) / c * 1e-4; });
+  if (xb) return c == 1 ? launch_draw<true, 1>(a, s) : c == 2 ? launch_draw<true, 2>(a, s) : c == 4 ? launch_draw<true, 4>(a, s) : launch_draw<true, 8>(a, s);
+  return c == 1 ? launch_draw<false, 1>(a, s) : c == 2 ? launch_draw<false, 2>(a, s) : c == 4 ? launch_draw<false, 4>(a, s) : launch_draw<false, 8>(a, s);
 }
 
 }  // namespace bl

@@ -590,7 +590,7 @@ bl_status bl_rope_append(const void* qkv, bl_dtype xt, const float* cos, const f
  * weighted sum are fp32.  Which warp takes which tokens depends on the lengths
  * and the device's number of SMs, so sums are the same from call to call but
  * not between batches.
- * Requires M, R, pages, page, W >= 1, H % Hk == 0, H <= 65536, D % 8 == 0,
+ * Requires M, R, pages, page, W >= 1, H % Hk == 0, M * H < 2^31, D % 8 == 0,
  * 8 <= D <= 256, window, sinks >= 0, pages * page < 2^31; q, caches and out
  * 16-byte aligned, the others 4-byte aligned.
  */
