@@ -53,21 +53,14 @@ __device__ __forceinline__ void fill_exp2_table(Exp2Table& t) {
     t.v[j] = make_ulonglong2(kExp2[j], __float_as_uint(__ull2float_rn(kExp2[j] >> 8)));
 }
 
-// The weight of logit l: with -z = (l - max) log2(e) / T in pairs of floats,
-// 2^-z = 2^n 2^(j/32) 2^r, |r| <= 1/64: the power of two is a shift, 2^(j/32)
-// comes from the table, and 2^r - 1 <= 2^-6.5 is a polynomial in float, whose
-// 2^-24 relative error leaves about 2^-30 of the weight.
+// 2^(e + el) in units of 2^-44, e <= 0 and |el| small, e and el a pair: 2^n 2^(j/32)
+// 2^r, |r| <= 1/64: the power of two is a shift, 2^(j/32) comes from the table, and
+// 2^r - 1 <= 2^-6.5 is a polynomial in float, whose 2^-24 relative error leaves about
+// 2^-30 of the weight.  0 for e <= -63, NaN, or where `none` is given.
 // `shift` receives -n: the result is not shifted yet.  No branches: callers
 // have several in flight.
-__device__ __forceinline__ unsigned long long weight_mantissa(float l, float top, Slope c, const Exp2Table& t,
-                                                              int& shift) {
-  const float d = __fsub_rn(l, top);  // < 0; its rounding error is dl
-  const float z = __fsub_rn(d, l);
-  const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(d, z)), __fsub_rn(-top, z));
-  float e = __fmul_rn(d, c.hi);
-  const float el = __fmaf_rn(d, c.hi, -e) + __fmaf_rn(d, c.lo, __fmul_rn(dl, c.hi));
-  // no weight: too small, greedy, -inf, NaN, beside +inf
-  const bool none = !(e > -63.f) || c.hi < 0.f;
+__device__ __forceinline__ unsigned long long exp2_mantissa(float e, float el, bool none, const Exp2Table& t, int& shift) {
+  none |= !(e > -63.f);
   e = none ? 0.f : e;
   const float n = rintf(e);                 // -63..0
   const float f = __fsub_rn(e, n);          // exact, |f| <= 1/2
@@ -79,8 +72,22 @@ __device__ __forceinline__ unsigned long long weight_mantissa(float l, float top
   const ulonglong2 base = t.v[int(j) + 16];
   // base < 2^45, so |p base| < 2^39: in units of 2^8 it is a signed 32-bit integer
   const long long more = static_cast<long long>(__float2int_rn(p * __uint_as_float(uint32_t(base.y)))) * 256;
-  shift = l == top ? 0 : -int(n);           // 0..63
-  return l == top ? 1ull << kWeightBits : none ? 0ull : base.x + static_cast<unsigned long long>(more);
+  shift = -int(n);                          // 0..63
+  return none ? 0ull : base.x + static_cast<unsigned long long>(more);
+}
+
+// The weight of logit l: -z = (l - max) log2(e) / T in pairs of floats.
+__device__ __forceinline__ unsigned long long weight_mantissa(float l, float top, Slope c, const Exp2Table& t,
+                                                              int& shift) {
+  const float d = __fsub_rn(l, top);  // < 0; its rounding error is dl
+  const float z = __fsub_rn(d, l);
+  const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(d, z)), __fsub_rn(-top, z));
+  const float e = __fmul_rn(d, c.hi);
+  const float el = __fmaf_rn(d, c.hi, -e) + __fmaf_rn(d, c.lo, __fmul_rn(dl, c.hi));
+  // no weight: too small, greedy, -inf, NaN, beside +inf
+  const unsigned long long w = exp2_mantissa(e, el, c.hi < 0.f, t, shift);
+  shift = l == top ? 0 : shift;
+  return l == top ? 1ull << kWeightBits : w;
 }
 
 __device__ __forceinline__ unsigned long long weight_of(float l, float top, Slope c, const Exp2Table& t) {

@@ -28,7 +28,8 @@ namespace {
 
 constexpr int kMassThreads = 256;
 constexpr int kMostStretches = 16;
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;  // a lane per warp in the sums over warps
+constexpr int kListed = 32;
 
 struct Args {
   const void *logits, *drafts;
@@ -37,7 +38,7 @@ struct Args {
   int64_t M, R, V;
   int32_t *accepted, *next;
   float2* part;  // [row][target, draft][stretch]: maximum, mass
-  int stretches;
+  int stretches, stretch;  // of a row, and their length
   unsigned int* err;
 };
 
@@ -52,51 +53,105 @@ __device__ __forceinline__ float logit(const void* x, int64_t i) {
   return XB ? bf16_bits_to_f32(static_cast<const uint16_t*>(x)[i]) : static_cast<const float*>(x)[i];
 }
 
-// f(v, i) for elements [from, to) of MATS rows at x[m] + base, shared by n threads (this is the t-th): v[m] holds the
-// elements i, i + 1, ... of row m, as many as 16 bytes have, or one at the ends.  The rows' addresses are equal modulo 16
-// (`wide`), or every element comes by itself.  Several loads are in flight.
-template <bool XB, int MATS, class F>
-__device__ __forceinline__ void each(const void* const (&x)[2], bool wide, int64_t base, int from, int to, int t, int n, F f) {
-  constexpr int E = XB ? 8 : 4, kAtOnce = MATS == 1 ? 4 : 2;
-  const int off = int((reinterpret_cast<uintptr_t>(x[0]) / (XB ? 2 : 4) + uint64_t(base) + uint64_t(from)) % E);
+// Pairs of floats for the packed fp32 instructions.
+using f2 = u64;
+__device__ __forceinline__ f2 pack2(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 exp2_of(f2 v) {
+  float x, y;
+  unpack2(v, x, y);
+  return pack2(exp2_fast(x), exp2_fast(y));
+}
+
+// 16 bytes of logits.
+template <bool XB>
+struct Word {
+  static constexpr int E = XB ? 8 : 4;
+  uint32_t u[4];
+  __device__ __forceinline__ void load(const void* x, int64_t i) {
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + i * (XB ? 2 : 4));
+    u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+  }
+  __device__ __forceinline__ float at(int e) const {
+    return __uint_as_float(!XB ? u[e % 4] : e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+  }
+  __device__ __forceinline__ f2 pair(int k) const { return pack2(at(2 * k), at(2 * k + 1)); }
+  // e known at run time only
+  __device__ __forceinline__ float pick(int e) const {
+    float v = at(0);
+#pragma unroll
+    for (int j = 1; j < E; ++j) v = e == j ? at(j) : v;
+    return v;
+  }
+  // The largest; NaN if there is one.
+  __device__ __forceinline__ float most() const {
+    float r;
+    if (XB) {
+      uint32_t a, b, c;
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(u[0]), "r"(u[1]));
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(u[2]), "r"(u[3]));
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(c << 16)), "f"(__uint_as_float(c & 0xffff0000u)));
+    } else {
+      float a, b;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(at(0)), "f"(at(1)));
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(at(2)), "f"(at(3)));
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    }
+    return r;
+  }
+};
+
+// The elements [from, to) of MATS rows at x[m] + base, shared by n threads (this is the t-th): words(w, i) gets 16 bytes
+// of each row, of its elements i, i + 1, ..., and one(i) the elements at the ends.  The rows' addresses are equal modulo 16
+// (`wide`), or every element comes by itself.  The next words are loaded before the present ones are worked on.
+template <bool XB, int MATS, int kAtOnce, class One, class Words>
+__device__ __forceinline__ void each(const void* x0, const void* x1, bool wide, int64_t base, int from, int to, int t, int n, One one, Words f) {
+  constexpr int E = Word<XB>::E;
+  const int off = int((reinterpret_cast<uintptr_t>(x0) / (XB ? 2 : 4) + uint64_t(base) + uint64_t(from)) % E);
   const int body = wide ? min(to, from + (E - off) % E) : to;  // of [from, to): from here on 16-byte words
   const int words = (to - body) / E, tail = body + words * E;
-  for (int i = t; i < body - from + to - tail; i += n) {
-    const int at = i < body - from ? from + i : tail + i - (body - from);
-    float v[MATS][1];
-#pragma unroll
-    for (int m = 0; m < MATS; ++m) v[m][0] = logit<XB>(x[m], base + at);
-    f(v, at);
-  }
-  for (int w0 = t; w0 < words; w0 += kAtOnce * n) {
-    uint4 raw[kAtOnce][MATS];
-#pragma unroll
-    for (int j = 0; j < kAtOnce; ++j)
-#pragma unroll
-      for (int m = 0; m < MATS; ++m)
-        if (w0 + j * n < words)
-          raw[j][m] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x[m]) + (base + body + int64_t(w0 + j * n) * E) * (XB ? 2 : 4));
+  for (int i = t; i < body - from + to - tail; i += n) one(i < body - from ? from + i : tail + i - (body - from));
+  Word<XB> next[kAtOnce][MATS];
+  auto load = [&](int w0) {
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j)
       if (w0 + j * n < words) {
-        float v[MATS][E];
-#pragma unroll
-        for (int m = 0; m < MATS; ++m) {
-          const uint32_t u[4] = {raw[j][m].x, raw[j][m].y, raw[j][m].z, raw[j][m].w};
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[m][e] = __uint_as_float(!XB ? u[e % 4] : e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
-        }
-        f(v, body + (w0 + j * n) * E);
+        next[j][0].load(x0, base + body + int64_t(w0 + j * n) * E);
+        if (MATS == 2) next[j][MATS - 1].load(x1, base + body + int64_t(w0 + j * n) * E);
       }
+  };
+  load(t);
+  for (int w0 = t; w0 < words; w0 += kAtOnce * n) {
+    Word<XB> now[kAtOnce][MATS];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) now[j][m] = next[j][m];
+    load(w0 + kAtOnce * n);
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if (w0 + j * n < words) f(now[j], body + (w0 + j * n) * E);
   }
-}
-template <int N>
-struct Count {
-  static constexpr int n = N;
-};
-template <int MATS, int N>
-__device__ __forceinline__ Count<N> count_of(const float (&)[MATS][N]) {
-  return {};
 }
 
 // log2(e) / temperature; negative: greedy, only the maxima have weight.
@@ -120,115 +175,165 @@ template <bool XB>
 __global__ void __launch_bounds__(kMassThreads) verify_mass_kernel(const Args a) {
   __shared__ int64_t found;
   __shared__ float2 red[kMassThreads / 32];
-  const int mats = a.drafts ? 2 : 1;
-  const int64_t row = blockIdx.x / (a.stretches * mats);
-  const int mat = int(blockIdx.x / a.stretches % mats), stretch = int(blockIdx.x % a.stretches);
+  const int64_t row = blockIdx.x;
+  const int mat = int(blockIdx.z), stretch = int(blockIdx.y);
   if (threadIdx.x == 0) found = -1;
   __syncthreads();
   pdl_wait();
-  // the request that has this row and a draft behind it
+  // the request that has this row; a row of the draft's logits has to have a draft behind it
   for (int64_t r = threadIdx.x; r < a.R; r += kMassThreads) {
     const Rows q = rows_of(a.start, r, a.M);
-    if (row >= q.first && row + 1 < int64_t(q.first) + q.n) found = r;
+    if (row >= q.first && row + mat < int64_t(q.first) + q.n) found = r;
   }
   __syncthreads();
   if (found >= 0) {
     const float rate = rate_of(a.temperature, found);
+    const bool few = rate < 0.f;
     const void* x = mat ? a.drafts : a.logits;
-    const int from = int(a.V * stretch / a.stretches), to = int(a.V * (stretch + 1) / a.stretches);
-    float2 s = {-FLT_MAX, 0.f};
-    each<XB, 1>({x, x}, true, row * a.V, from, to, threadIdx.x, kMassThreads, [&](auto& v, int) {
-      constexpr int N = decltype(count_of(v))::n;
-      float top = s.x;
+    const int from = stretch * a.stretch, to = min(int(a.V), from + a.stretch);
+    // The sum is in units of 2^E, E a whole number, so that l rate - E is rounded once; -inf: only the largest have
+    // weight (greedy, or exponents beyond fp32, where the next smaller number has none).
+    float top = -INFINITY, E = -INFINITY, sum = 0.f;
+    auto raise = [&](float l) {  // to a larger maximum
+      top = l;
+      const float next = few || !(fabsf(l * rate) <= FLT_MAX) ? -INFINITY : ceilf(l * rate);
+      sum *= next > -INFINITY ? exp2_fast(E - next) : 0.f;
+      E = next;
+    };
+    auto add = [&](float l) {  // NaN: nothing
+      if (l > top) raise(l);
+      if (!(l > -INFINITY)) return;
+      sum += E > -INFINITY ? exp2_fast(__fmaf_rn(l, rate, -E)) : float(l == top);
+    };
+    const f2 rate2 = pack2(rate, rate);
+    each<XB, 1, 4>(x, x, true, row * a.V, from, to, threadIdx.x, kMassThreads, [&](int i) { add(logit<XB>(x, row * a.V + i)); },
+                   [&](const Word<XB>(&w)[1], int) {
+                     const float most = w[0].most();
+                     if (most > top) raise(most);
+                     if (most == -INFINITY) return;
+                     if (most == most && !(E > -INFINITY)) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) top = fmaxf(top, v[0][e]);
-      if (top > s.x) s = make_float2(top, s.y * weight(s.x, top, rate));
-      if (rate < 0.f || top == INFINITY) {
+                       for (int e = 0; e < Word<XB>::E; ++e) sum += float(w[0].at(e) == top);
+                     } else if (most == most && E > -INFINITY && rate > 0.f) {
+                       const f2 e2 = pack2(-E, -E);
+                       f2 t = exp2_of(fma2(w[0].pair(0), rate2, e2));
 #pragma unroll
-        for (int e = 0; e < N; ++e) s.y += float(v[0][e] == top);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) s.y += exp2_fast(fmaxf((v[0][e] - top) * rate, -200.f));  // NaN: 0
-      }
-    });
-    for (int o = 16; o > 0; o >>= 1)
-      s = join(s, {__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)}, rate);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+                       for (int k = 1; k < Word<XB>::E / 2; ++k) t = add2(t, exp2_of(fma2(w[0].pair(k), rate2, e2)));
+                       float t0, t1;
+                       unpack2(t, t0, t1);
+                       sum += t0 + t1;
+                     } else {
+#pragma unroll 1
+                       for (int e = 0; e < Word<XB>::E; ++e) add(w[0].pick(e));
+                     }
+                   });
+    // to the warp's and the CTA's largest: the sums are beside their maximum from here on, as elsewhere
+    if (E > -INFINITY) sum *= exp2_fast(-__fmaf_rn(top, rate, -E));
+    float most = warp_max(top);
+    sum = warp_sum(sum * weight(top, most, rate));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(most, sum);
     __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kMassThreads / 32; ++w) s = join(s, red[w], rate);
-      a.part[(row * 2 + mat) * a.stretches + stretch] = s;
+    if (threadIdx.x < kMassThreads / 32) {
+      constexpr unsigned kLanes = (1u << kMassThreads / 32) - 1;
+      const float2 s = red[threadIdx.x];
+      most = s.x;
+#pragma unroll
+      for (int o = kMassThreads / 64; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kLanes, most, o));
+      sum = s.y * weight(s.x, most, rate);
+#pragma unroll
+      for (int o = kMassThreads / 64; o > 0; o >>= 1) sum += __shfl_xor_sync(kLanes, sum, o);
+      if (threadIdx.x == 0) a.part[(row * 2 + mat) * a.stretches + stretch] = make_float2(most, sum);
     }
   }
   pdl_launch_dependents();
 }
 
-// A mass in [2^44, 2^63] (0: none) as a 64-bit reciprocal: share(w) = w / mass in units of 2^-60.
+// A mass in [2^43, 2^63] (0: none) as a 64-bit reciprocal: share(w) = w / mass in units of 2^-60, to 2^-61 of it.
 struct Reciprocal {
-  u64 r;
+  u64 r;  // 2^127 / (mass << s)
   int shift;
   __device__ __forceinline__ void set(u64 mass) {
-    const int s = mass ? __clzll(mass) : 0;  // 0..19
-    r = mass ? u64((((unsigned __int128)1 << 127) - 1) / (mass << s)) : 0;
+    const int s = mass ? __clzll(mass) : 0;  // 0..20
+    const u64 n = mass << s;
     shift = 22 - s;
+    r = 0;
+    if (n == 1ull << 63) {
+      r = ~0ull;
+    } else if (mass) {
+      u64 x = __float2ull_rz(__fdiv_rd(1.7014117e38f, __ull2float_ru(n)));  // a little below 2^127 / n, 23 bits
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // x += x (2^127 - n x) / 2^127: 46 bits, then all; the remainder is positive
+        const u64 e = (1ull << 63) - __umul64hi(n, x) - 1;
+        x += __umul64hi(x, e) * 2;
+      }
+      r = x;
+    }
   }
   __device__ __forceinline__ u64 share(u64 w) const { return __umul64hi(w << 19, r) >> shift; }
 };
 
-// Weights of a row's logits beside its largest, in units of 2^-44: light ones, below 2^-8 of the largest, by the
-// hardware's exp2.
+// Weights of a row's logits, 2^(l log2(e) / T - E) in units of 2^-44, where E is a whole number so near to the largest
+// logit's exponent that its weight is in (2^43, 2^44].  log2(e) / T = hi + lo with lo > 0 (-inf has weight 0 then).
 struct Weights {
+  float hi, lo, E;
   float top;
-  Slope slope;
-  float k, rest;  // top log2(e) / T - 40 = k + rest
-  bool none, few;  // no logit above -inf; greedy or an infinity, where only the largest have weight
+  bool none, few;  // no logit above -inf; only the largest have weight: greedy, an infinity, or exponents beyond fp32
+  float offset;    // 40 - E
 
-  __device__ __forceinline__ void set(float largest, Slope s) {
-    top = largest;
-    slope = s;
-    none = top == -INFINITY;
-    few = s.hi < 0.f || top == INFINITY;
-    const float p = __fmul_rn(top, s.hi);
-    k = __fsub_rn(p, 40.f);
-    // what the two roundings left, and the slope's lower part
-    const float z = __fsub_rn(k, p);
-    rest = __fsub_rn(p, __fsub_rn(k, z)) - __fadd_rn(40.f, z);
-    rest += __fmaf_rn(top, s.hi, -p) + __fmul_rn(top, s.lo);
+  __device__ __forceinline__ void set(float2 stat, float temperature) {
+    top = stat.x;
+    none = !(stat.y > 0.f);
+    const float lh = 1.44269502162933349609375f, ll = 1.92596303313e-8f;  // log2(e) = lh + ll
+    hi = __fdiv_rd(lh, temperature);
+    lo = fmaxf(__fdiv_rn(__fadd_rn(__fmaf_rn(-hi, temperature, lh), ll), temperature), FLT_MIN);  // lh - hi T is exact
+    const float p = __fmul_rn(top, hi);
+    E = ceilf(p);
+    few = !(temperature >= kGreedyBelow) || !(fabsf(p) <= FLT_MAX);
+    offset = !few && !none && fabsf(E) < 4194304.f ? 40.f - E : NAN;  // every weight by full()
   }
-  // log2 of the weight in units of 2^-40; not below 32 (or NaN) where the weight is not light
-  __device__ __forceinline__ float light(float l) const {
-    l = fmaxf(l, -FLT_MAX);  // NaN and -inf
-    return __fmaf_rn(l, slope.hi, -k) + __fmaf_rn(l, slope.lo, -rest);
-  }
+  // log2 of the weight in units of 2^-40, where it is below 32 (NaN where only the largest have weight)
+  __device__ __forceinline__ float light(float l) const { return __fmaf_rn(l, lo, __fmaf_rn(l, hi, offset)); }
   __device__ __forceinline__ u64 full(float l, const Exp2Table& t) const {
-    return none ? 0ull : few ? u64(l == top) << kWeightBits : weight_of(l, top, slope, t);
+    const float p = __fmul_rn(l, hi);
+    const float e = __fsub_rn(p, E), z = __fsub_rn(e, p);
+    const float el = __fadd_rn(__fsub_rn(p, __fsub_rn(e, z)), __fsub_rn(-E, z)) + __fmaf_rn(l, lo, __fmaf_rn(l, hi, -p));
+    int shift;
+    const u64 w = exp2_mantissa(e, el, none || few, t, shift);
+    return few && !none ? u64(l == top) << kWeightBits : (w + ((1ull << shift) >> 1)) >> shift;
   }
 };
 
 // What a CTA shows the others of its cluster.
 struct Shown {
   int first, n, stop;  // rank 0's: the request's rows, the draft that is refused (or how many there are)
-  float top[2];
+  float2 stat[2];      // rank 0's: maximum and mass (fp32) of the row in the target's and the draft's logits
   u64 mass[2], rest[2];
 };
 
 struct __align__(16) Shared {
   Exp2Table exp2;
   Shown shown;
+  Weights w[2];
   Reciprocal share[2];
-  u64 warps[kWarps];
-  float redf[kWarps];
+  float scale[2];  // light weights in units of 2^-40 of the mass
+  u64 warps[kWarps], masses[2][kWarps];
+  int listed[kWarps];          // tokens of a warp's part whose weights are not light, and where they are
+  int list[kWarps][kListed];
+  float value[kWarps][kListed][2];  // of p's and q's logits
 };
 
-// Sum over the CTA's threads, in all of them.
-__device__ __forceinline__ u64 cta_sum(u64 v, u64* warps) {
-  v = warp_sum_u64(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 s = 0;
-  for (int w = 0; w < kWarps; ++w) s += warps[w];
-  return s;
+// The weight of a logit of the target's row (m = 0) or the draft's.
+__device__ __noinline__ u64 weight_in(const Shared& sh, int m, float l) {
+  const float y = sh.w[m].light(l);
+  return y < 32.f ? __float2ull_rn(16.f * exp2_fast(y)) : sh.w[m].full(l, sh.exp2);
+}
+// What p has over q, in units of 2^-60 of their masses.
+__device__ __noinline__ u64 excess(const Shared& sh, float lp, float lq) {
+  const float yp = sh.w[0].light(lp), yq = sh.w[1].light(lq);
+  if (yp < 32.f && yq < 32.f)
+    return __float2ull_rn(1048576.f * fmaxf(__fmaf_rn(exp2_fast(yp), sh.scale[0], -__fmul_rn(exp2_fast(yq), sh.scale[1])), 0.f));
+  const u64 p = sh.share[0].share(weight_in(sh, 0, lp)), q = sh.share[1].share(weight_in(sh, 1, lq));
+  return p > q ? p - q : 0;
 }
 
 template <bool XB, int kC>  // kC: CTAs of a request
@@ -245,32 +350,41 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
   const Rows rows = rows_of(a.start, r, a.M);
   const int drafts = max(rows.n - 1, 0);
   bool bad = rows.bad;
+  if (tid < kWarps) sh.listed[tid] = 0;
   if (tid == 0) sh.shown.first = rows.first, sh.shown.n = rows.n, sh.shown.stop = drafts;
   __syncthreads();
 
-  // the first draft that is refused
-  auto mass_of = [&](int64_t row, int mat) {
-    const float2* p = a.part + (row * 2 + mat) * a.stretches;
-    float2 s = p[0];
-    for (int i = 1; i < a.stretches; ++i) s = join(s, p[i], rate);
+  // Maximum and mass of a row, lanes 0..15 the target's and the others the draft's: a lane per stretch.
+  auto mass_of = [&](int64_t row, bool drafts) {
+    const int i = lane % kMostStretches;
+    float2 s = {-INFINITY, 0.f};
+    if (i < a.stretches && (lane < kMostStretches || drafts)) s = a.part[(row * 2 + lane / kMostStretches) * a.stretches + i];
+#pragma unroll
+    for (int o = kMostStretches / 2; o > 0; o >>= 1)
+      s = join(s, {__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)}, rate);
     return s;
   };
-  for (int j = tid; rank == 0 && j < drafts; j += kThreads) {
+  // the first draft that is refused: a warp per draft
+  for (int j = warp; rank == 0 && j < drafts; j += kWarps) {
     const int64_t row = int64_t(rows.first) + j;
     const int x = a.token[row + 1];
-    double px = 0, qx = 1;
+    const float u = a.u[row];
+    const bool mine = lane < kMostStretches || a.drafts;
+    const float2 s = mass_of(row, a.drafts != nullptr);
+    float share = lane < kMostStretches ? 0.f : 1.f;
     if (x < 0 || x >= a.V) {
       bad = true;
-    } else {
-      const float2 p = mass_of(row, 0);
-      if (p.y > 0.f) px = double(weight(logit<XB>(a.logits, row * a.V + x), p.x, rate)) / double(p.y);
-      if (a.drafts) {
-        const float2 q = mass_of(row, 1);
-        qx = q.y > 0.f ? double(weight(logit<XB>(a.drafts, row * a.V + x), q.x, rate)) / double(q.y) : 0.0;
-      }
+    } else if (mine) {
+      const float l = logit<XB>(lane < kMostStretches ? a.logits : a.drafts, row * a.V + x);
+      share = s.y > 0.f ? __fdiv_rn(weight(l, s.x, rate), s.y) : 0.f;
     }
-    const float u = a.u[row];
-    if (!(double(u > 0.f ? fminf(u, 0.99999994f) : 0.f) * qx < px)) atomicMin(&sh.shown.stop, j);
+    const float qx = __shfl_sync(0xffffffffu, share, kMostStretches);
+    if (lane == 0 && !(__fmul_rn(u > 0.f ? fminf(u, 0.99999994f) : 0.f, qx) < share)) atomicMin(&sh.shown.stop, j);
+  }
+  __syncthreads();
+  if (rank == 0 && warp == 0 && rows.n > 0) {
+    const float2 s = mass_of(int64_t(rows.first) + sh.shown.stop, a.drafts && sh.shown.stop < drafts);
+    if (lane % kMostStretches == 0) sh.shown.stat[lane / kMostStretches] = s;
   }
   sync_cluster<kC>();
   const Shown* first = of(&sh.shown, 0);  // one CTA decides for all
@@ -281,153 +395,175 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
   // where warp w's part of [f, e) begins
   auto part = [](int f, int e, int w) { return f + int(int64_t(e - f) * w / kWarps); };
   const bool both = refused && a.drafts;
-  const Slope slope = slope_of(t);
 
   if (n > 0) {
     const void* const x[2] = {a.logits, both ? a.drafts : a.logits};
     const bool wide = ((reinterpret_cast<uintptr_t>(x[0]) ^ reinterpret_cast<uintptr_t>(x[1])) & 15) == 0;
-    const void* const xd[2] = {x[1], x[1]};
-    float top[2] = {-INFINITY, -INFINITY};
-    for (int m = 0; m < 2; ++m) {
-      if (m == 1 && !both) break;
-      float most = -INFINITY;
-      each<XB, 1>(m ? xd : x, true, base, from, to, tid, kThreads, [&](auto& v, int) {
-#pragma unroll
-        for (int e = 0; e < decltype(count_of(v))::n; ++e) most = fmaxf(most, v[0][e]);
-      });
-      most = warp_max(most);
-      __syncthreads();
-      if (lane == 0) sh.redf[warp] = most;
-      __syncthreads();
-      for (int w = 0; w < kWarps; ++w) most = fmaxf(most, sh.redf[w]);
-      if (tid == 0) sh.shown.top[m] = most;
-    }
-    sync_cluster<kC>();
-    Weights w[2];
-    for (int m = 0; m < 2; ++m) {
-      if (m == 0 || both)
-        for (int c = 0; c < kC; ++c) top[m] = fmaxf(top[m], *of(&sh.shown.top[m], c));
-      w[m].set(top[m], slope);
-    }
-    // The sum of the weights of 16 bytes of logits.
-    auto weigh = [&](const Weights& w, const auto& l) {
-      constexpr int N = sizeof(l) / sizeof(float);
-      float y[N], most = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        y[e] = w.light(l[e]);
-        most = y[e] < 32.f ? most : 64.f;
-      }
-      u64 s = 0;
-      if (w.few || w.none) {
-        int n = 0;
-#pragma unroll
-        for (int e = 0; e < N; ++e) n += l[e] == w.top;
-        return w.none ? 0 : u64(n) << kWeightBits;
-      }
-      if (most < 32.f) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) s += __float2uint_rn(exp2_fast(y[e]));
-        return s << 4;
-      }
-#pragma unroll 1
-      for (int e = 0; e < N; ++e) {
-        float le = l[0], ye = y[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) le = e == i ? l[i] : le, ye = e == i ? y[i] : ye;
-        s += ye < 32.f ? u64(__float2uint_rn(exp2_fast(ye))) << 4 : w.full(le, sh.exp2);
-      }
-      return s;
+    if (tid < 2) sh.w[tid].set(first->stat[tid], t);
+    __syncthreads();
+    const int drafted = refused ? a.token[row + 1] : -1;
+    // Logits whose weight is not light are few and spread; one by one they would stop their warps.  They are listed, and
+    // weighed after the pass, a lane each (at once where the list is full).
+    auto list = [&](int i, float lp, float lq) {
+      const int k = atomicAdd(&sh.listed[warp], 1);
+      if (k < kListed) sh.list[warp][k] = i, sh.value[warp][k][0] = lp, sh.value[warp][k][1] = lq;
+      return k < kListed;
     };
+    // f(i, lp, lq) for what this warp has listed.
+    auto each_listed = [&](auto f) {
+      __syncwarp();
+      const int n = min(sh.listed[warp], kListed);
+      for (int k = lane; k < n; k += 32) f(sh.list[warp][k], sh.value[warp][k][0], sh.value[warp][k][1]);
+      __syncwarp();
+      if (lane == 0) sh.listed[warp] = 0;
+      __syncwarp();
+    };
+    auto at = [&](int m, int i) { return logit<XB>(x[m], base + i); };
+    // The weights of logits from i on: light ones to `sum` (fp32: a lane has few of them), in units of 2^-40, others to
+    // the list or `more`.
+    auto weigh_one = [&](int m, int i, u64& more) { more += weight_in(sh, m, at(m, i)); };
+    auto weigh = [&](int m, const Word<XB>& l, int i, float& sum, u64& more) {
+      constexpr int N = Word<XB>::E;
+      const Weights& w = sh.w[m];
+      if (w.light(l.most()) < 32.f) {
+        const f2 hi = pack2(w.hi, w.hi), lo = pack2(w.lo, w.lo), offset = pack2(w.offset, w.offset);
+        f2 t = 0;
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) t = add2(t, exp2_of(fma2(l.pair(k), lo, fma2(l.pair(k), hi, offset))));
+        float t0, t1;
+        unpack2(t, t0, t1);
+        sum += t0 + t1;
+      } else if (!w.none && !(w.few && l.most() < w.top)) {
+        unsigned heavy = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float y = w.light(l.at(e));
+          if (y < 32.f)
+            sum += exp2_fast(y);
+          else
+            heavy |= unsigned(l.at(e) > -INFINITY && !(w.few && l.at(e) < w.top)) << e;  // -inf and NaN have no weight
+        }
+        for (; heavy; heavy &= heavy - 1) {
+          const int e = __ffs(heavy) - 1;
+          const float le = l.pick(e);
+          if (!list(i + e, le, le)) more += weight_in(sh, m, le);
+        }
+      }
+    };
+    const int wfrom = part(from, to, warp), wto = part(from, to, warp + 1);
     u64 mass[2] = {0, 0};
     if (both) {
+      float sum[2] = {0.f, 0.f};
+      // (q's entries in the list: negative)
+      each<XB, 2, 1>(x[0], x[1], wide, base, wfrom, wto, lane, 32,
+                     [&](int i) {
+                       weigh_one(0, i, mass[0]);
+                       weigh_one(1, i, mass[1]);
+                     },
+                     [&](const Word<XB>(&v)[2], int i) {
+                       weigh(0, v[0], i, sum[0], mass[0]);
+                       weigh(1, v[1], -1 - i - (Word<XB>::E - 1), sum[1], mass[1]);
+                     });
+      each_listed([&](int i, float l, float) {
+        const u64 w = weight_in(sh, i < 0, l);
+        mass[0] += i < 0 ? 0 : w;
+        mass[1] += i < 0 ? w : 0;
+      });
       for (int m = 0; m < 2; ++m) {
-        u64 s = 0;
-        each<XB, 1>(m ? xd : x, true, base, from, to, tid, kThreads, [&](auto& v, int) { s += weigh(w[m], v[0]); });
-        s = cta_sum(s, sh.warps);
-        if (tid == 0) sh.shown.mass[m] = s;
+        mass[m] = warp_sum_u64(mass[m] + __float2ull_rn(16.f * sum[m]));
+        if (lane == 0) sh.masses[m][warp] = mass[m];
+      }
+      __syncthreads();
+      if (warp < 2) {
+        const u64 s = warp_sum_u64(sh.masses[warp][lane]);
+        if (lane == 0) sh.shown.mass[warp] = s;
       }
       sync_cluster<kC>();
-      for (int m = 0; m < 2; ++m)
-        for (int c = 0; c < kC; ++c) mass[m] += *of(&sh.shown.mass[m], c);
-      if (tid < 2) sh.share[tid].set(mass[tid]);
+      if (tid < 2) {
+        u64 s = 0;
+        for (int c = 0; c < kC; ++c) s += *of(&sh.shown.mass[tid], c);
+        sh.share[tid].set(s);
+        sh.scale[tid] = s ? float(1ull << kWeightBits) / float(s) : 0.f;
+      }
       __syncthreads();
     }
-    const int drafted = refused ? a.token[row + 1] : -1;
-    // light weights of p and q in units of 2^-40 of the masses
-    constexpr float kOne = float(1ull << kWeightBits);
-    const float fp = mass[0] ? kOne / float(mass[0]) : 0.f, fq = mass[1] ? kOne / float(mass[1]) : 0.f;
-    // One token's share of what is drawn from: attempt 0: what p has over q; 1: p, where nothing is left.
-    auto rest_at = [&](int attempt, float lp, float lq, int i) {
-      const float yp = w[0].light(lp);
-      const bool light = yp < 32.f && !w[0].few && !w[0].none;
-      if (attempt == 1 || !both) {
-        if (attempt == 0 && i == drafted) return u64(0);
-        return light ? u64(__float2uint_rn(exp2_fast(yp))) << 4 : w[0].full(lp, sh.exp2);
-      }
-      const float yq = w[1].light(lq);
-      const bool light_q = yq < 32.f && !w[1].few && !w[1].none;
-      if (light && light_q) return u64(__float2uint_rn(__fmaf_rn(exp2_fast(yp), fp, -__fmul_rn(exp2_fast(yq), fq)))) << 20;
-      const u64 p = sh.share[0].share(light ? u64(__float2uint_rn(exp2_fast(yp))) << 4 : w[0].full(lp, sh.exp2));
-      const u64 q = sh.share[1].share(light_q ? u64(__float2uint_rn(exp2_fast(yq))) << 4 : w[1].full(lq, sh.exp2));
-      return p > q ? p - q : u64(0);
+    // One token's share of what is drawn from: attempt 0: what p has over q, in units of 2^-60 of the mass, or p without
+    // the draft; 1: p, where nothing is left.
+    auto rest_at = [&](int attempt, int i, float lp, float lq) {
+      if (attempt == 0 && both) return excess(sh, lp, lq);
+      return attempt == 0 && i == drafted ? u64(0) : weight_in(sh, 0, lp);
     };
-    const u64 few_only = both ? sh.share[0].share(1ull << kWeightBits) : 0, few_q = both ? sh.share[1].share(1ull << kWeightBits) : 0;
-    const u64 few_both = few_only > few_q ? few_only - few_q : 0;
     // The sum of those of [f, e), by a warp.
     auto sum_of = [&](int attempt, int f, int e) {
-      u64 s = 0;
-      if (attempt == 1 || !both) {
-        each<XB, 1>(x, true, base, f, e, lane, 32, [&](auto& v, int i) {
-          constexpr int N = decltype(count_of(v))::n;
-          if (attempt == 0 && drafted >= i && drafted < i + N) {
+      u64 more = 0;
+      float sum = 0.f;
+      const bool p_only = attempt == 1 || !both;
+      if (p_only) {
+        each<XB, 1, 2>(x[0], x[0], true, base, f, e, lane, 32, [&](int i) { more += rest_at(attempt, i, at(0, i), 0.f); },
+                       [&](const Word<XB>(&v)[1], int i) {
+                         if (attempt == 0 && drafted >= i && drafted < i + Word<XB>::E) {
 #pragma unroll 1
-            for (int j = 0; j < N; ++j) s += rest_at(0, logit<XB>(x[0], base + i + j), 0.f, i + j);
-          } else {
-            s += weigh(w[0], v[0]);
-          }
-        });
+                           for (int j = 0; j < Word<XB>::E; ++j) more += rest_at(0, i + j, v[0].pick(j), 0.f);
+                         } else {
+                           weigh(0, v[0], i, sum, more);
+                         }
+                       });
       } else {
-        each<XB, 2>(x, wide, base, f, e, lane, 32, [&](auto& v, int i) {
-          constexpr int N = decltype(count_of(v))::n;
-          float yp[N], yq[N], most = -INFINITY;
+        const Weights &wp = sh.w[0], &wq = sh.w[1];
+        each<XB, 2, 1>(x[0], x[1], wide, base, f, e, lane, 32, [&](int i) { more += excess(sh, at(0, i), at(1, i)); },
+                       [&](const Word<XB>(&v)[2], int i) {
+                         constexpr int N = Word<XB>::E;
+                         if (wp.light(v[0].most()) < 32.f && wq.light(v[1].most()) < 32.f) {
+                           const f2 hp = pack2(wp.hi, wp.hi), lp = pack2(wp.lo, wp.lo), op = pack2(wp.offset, wp.offset);
+                           const f2 hq = pack2(wq.hi, wq.hi), lq = pack2(wq.lo, wq.lo), oq = pack2(wq.offset, wq.offset);
+                           const f2 sp = pack2(sh.scale[0], sh.scale[0]), sq = pack2(-sh.scale[1], -sh.scale[1]);
+                           f2 t = 0;
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            yp[j] = w[0].light(v[0][j]);
-            yq[j] = w[1].light(v[1][j]);
-            most = yp[j] < 32.f && yq[j] < 32.f ? most : 64.f;
-          }
-          if (most < 32.f && !w[0].few && !w[0].none && !w[1].few && !w[1].none) {
-            u64 t = 0;
+                           for (int k = 0; k < N / 2; ++k) {
+                             const f2 ep = exp2_of(fma2(v[0].pair(k), lp, fma2(v[0].pair(k), hp, op)));
+                             const f2 eq = exp2_of(fma2(v[1].pair(k), lq, fma2(v[1].pair(k), hq, oq)));
+                             float d0, d1;
+                             unpack2(fma2(ep, sp, mul2(eq, sq)), d0, d1);
+                             t = add2(t, pack2(fmaxf(d0, 0.f), fmaxf(d1, 0.f)));
+                           }
+                           float t0, t1;
+                           unpack2(t, t0, t1);
+                           sum += t0 + t1;
+                         } else if (!wp.none && !(wp.few && v[0].most() < wp.top)) {
+                           unsigned heavy = 0;
 #pragma unroll
-            for (int j = 0; j < N; ++j) t += __float2uint_rn(__fmaf_rn(exp2_fast(yp[j]), fp, -__fmul_rn(exp2_fast(yq[j]), fq)));
-            s += t << 20;
-          } else {
-#pragma unroll 1
-            for (int j = 0; j < N; ++j) s += rest_at(0, logit<XB>(x[0], base + i + j), logit<XB>(x[1], base + i + j), i + j);
-          }
-        });
+                           for (int j = 0; j < N; ++j) {
+                             const float l0 = v[0].at(j), yp = wp.light(l0), yq = wq.light(v[1].at(j));
+                             if (yp < 32.f && yq < 32.f)
+                               sum += fmaxf(__fmaf_rn(exp2_fast(yp), sh.scale[0], -__fmul_rn(exp2_fast(yq), sh.scale[1])), 0.f);
+                             else
+                               heavy |= unsigned(l0 > -INFINITY && !(wp.few && l0 < wp.top)) << j;  // p has none otherwise
+                           }
+                           for (; heavy; heavy &= heavy - 1) {
+                             const int j = __ffs(heavy) - 1;
+                             const float l0 = v[0].pick(j), l1 = v[1].pick(j);
+                             if (!list(i + j, l0, l1)) more += excess(sh, l0, l1);
+                           }
+                         }
+                       });
       }
-      return warp_sum_u64(s);
+      each_listed([&](int i, float lp, float lq) { more += rest_at(attempt, i, lp, lq); });
+      return warp_sum_u64(more + __float2ull_rn((p_only ? 16.f : 1048576.f) * sum));
     };
     for (int attempt = 0; attempt < 2; ++attempt) {
-      const u64 s = sum_of(attempt, part(from, to, warp), part(from, to, warp + 1));
+      const u64 s = sum_of(attempt, wfrom, wto);
       __syncthreads();
       if (lane == 0) sh.warps[warp] = s;
       __syncthreads();
-      if (tid == 0) {
-        u64 all = 0;
-        for (int w = 0; w < kWarps; ++w) all += sh.warps[w];
-        sh.shown.rest[attempt] = all;
+      if (warp == 0) {
+        const u64 all = warp_sum_u64(sh.warps[lane]);
+        if (lane == 0) sh.shown.rest[attempt] = all;
       }
       sync_cluster<kC>();
-      u64 all = 0, before = 0, mine = 0;
-      for (int c = 0; c < kC; ++c) {
-        const u64 v = *of(&sh.shown.rest[attempt], c);
-        if (c < rank) before += v;
-        if (c == rank) mine = v;
-        all += v;
-      }
+      const u64 theirs = lane < kC ? *of(&sh.shown.rest[attempt], lane) : 0;
+      const u64 up_to = warp_scan(theirs);
+      const u64 all = __shfl_sync(0xffffffffu, up_to, 31), through_mine = __shfl_sync(0xffffffffu, up_to, rank);
+      const u64 before = through_mine - __shfl_sync(0xffffffffu, theirs, rank);
       if (all == 0) {
         if (attempt == 0 && refused) continue;
         if (rank == 0 && tid == 0) a.next[r] = -1;
@@ -435,12 +571,14 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
       }
       const float us = a.u_sample[r];
       const u64 target = mass_target(us > 0.f ? fminf(us, 0.99999994f) : 0.f, all);
-      if (before <= target && target < before + mine) {  // in this CTA's part
-        u64 at = before;
+      if (before <= target && target < through_mine) {  // in this CTA's part
+        u64 through_parts = before;
         int f = from, e = to;
         while (true) {  // the warp's part that has it, cut again while it is long
-          int in = 0;
-          while (at + sh.warps[in] <= target) at += sh.warps[in++];
+          const u64 v = sh.warps[lane], through = warp_scan(v);
+          const unsigned live = __ballot_sync(0xffffffffu, v != 0), past = __ballot_sync(0xffffffffu, through_parts + through > target);
+          const int in = past ? __ffs(past) - 1 : 31 - __clz(live);  // the last that has any, where the sums end early
+          through_parts += __shfl_sync(0xffffffffu, through - v, in);
           const int nf = part(f, e, in), ne = part(f, e, in + 1);
           f = nf;
           e = ne;
@@ -450,20 +588,34 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
           if (lane == 0) sh.warps[warp] = t;
           __syncthreads();
         }
+        // The part's sum was formed in another order than the tokens' own shares are: where these end before the
+        // target, the last token that has one is taken, and the likeliest where the shares are below their unit.
+        u64 best = 0;  // (whether it has a share, how likely) over the token
         for (int i0 = f; i0 < e; i0 += kThreads) {
-          const int64_t i = base + i0 + tid;
-          const u64 v = i0 + tid < e ? rest_at(attempt, logit<XB>(x[0], i), logit<XB>(x[1], i), i0 + tid) : 0ull;
+          const int i = i0 + tid;
+          const float l = i < e ? at(0, i) : -INFINITY;
+          const u64 v = i < e ? rest_at(attempt, i, l, at(1, i)) : 0ull;
           const u64 through = warp_scan(v);
           if (lane == 31) sh.warps[warp] = through;
           __syncthreads();
-          u64 b = at;
-          for (int k = 0; k < kWarps; ++k) {
-            if (k < warp) b += sh.warps[k];
-            at += sh.warps[k];
-          }
-          b += through - v;
-          if (b <= target && target < b + v) a.next[r] = i0 + tid;
+          const u64 w = sh.warps[lane], through_w = warp_scan(w);
+          const u64 b = through_parts + __shfl_sync(0xffffffffu, through_w - w, warp) + through - v;
+          through_parts += __shfl_sync(0xffffffffu, through_w, 31);
+          if (v > 0 && b <= target)
+            best = max(best, 1ull << 63 | u64(i));
+          else if (l > -INFINITY)
+            best = max(best, u64(key_of_f32(l) >> 1) << 32 | u64(i));
           __syncthreads();
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        if (lane == 0) sh.warps[warp] = best;
+        __syncthreads();
+        if (warp == 0) {
+          best = sh.warps[lane];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+          if (lane == 0) a.next[r] = int(best & 0xffffffffu);
         }
       }
       break;
@@ -492,17 +644,20 @@ cudaError_t launch_verify(const void* logits, const void* draft_logits, bl_dtype
                           int64_t R, int64_t V, int32_t* accepted, int32_t* next, void* ws, cudaStream_t s) {
   unsigned int* err = dev_error_ptr();
   if (!err) return cudaErrorUnknown;
-  Args a{logits, draft_logits, token, start, temperature, u, u_sample, M, R, V, accepted, next, static_cast<float2*>(ws), 1, err};
+  Args a{logits, draft_logits, token, start, temperature, u, u_sample, M, R, V, accepted, next, static_cast<float2*>(ws), 1, 0, err};
   const int mats = draft_logits ? 2 : 1;
-  a.stretches = int(std::max<int64_t>(1, std::min<int64_t>({kMostStretches, 8 * sm_count() / (M * mats), V / 4096})));
+  // Long stretches: a CTA's own 1.5 us are little then; short ones fill the GPU when there are few rows.
+  const int64_t wanted = std::max<int64_t>({V / 32768, 4 * sm_count() / (M * mats), 1});
+  a.stretch = int((V + wanted - 1) / std::min<int64_t>(wanted, kMostStretches) + 4095) / 4096 * 4096;
+  a.stretches = int((V + a.stretch - 1) / a.stretch);
   const bool pdl = overlap_enabled();
   const bool xb = lt == BL_BF16;
-  const dim3 grid(unsigned(M * mats * a.stretches));
+  const dim3 grid(unsigned(M), unsigned(a.stretches), unsigned(mats));
   const cudaError_t e = xb ? launch(verify_mass_kernel<true>, grid, dim3(kMassThreads), 0, s, pdl, a)
                            : launch(verify_mass_kernel<false>, grid, dim3(kMassThreads), 0, s, pdl, a);
   if (e != cudaSuccess) return e;
   // a row in c CTAs: some passes over its share, and the exchanges
-  const int c = ctas_per_row(R, [&](int c) { return 6.0 + 4.0 * (c > 1) + double(V) / c * 1e-4; });
+  const int c = ctas_per_row(R, [&](int c) { return 8.0 + 1.5 * (c > 1) + double(V) / c * 1e-4; });
   if (xb) return c == 1 ? launch_draw<true, 1>(a, s) : c == 2 ? launch_draw<true, 2>(a, s) : c == 4 ? launch_draw<true, 4>(a, s) : launch_draw<true, 8>(a, s);
   return c == 1 ? launch_draw<false, 1>(a, s) : c == 2 ? launch_draw<false, 2>(a, s) : c == 4 ? launch_draw<false, 4>(a, s) : launch_draw<false, 8>(a, s);
 }
