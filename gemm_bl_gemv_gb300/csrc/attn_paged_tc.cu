@@ -1,0 +1,628 @@
+// Attention of new tokens over a paged key-value cache (bl_attn_paged) on the 5th-generation tensor cores, for requests
+// whose new tokens make many rows of a key-value head (drafts), D <= 128.
+//
+// Units, tiles and stretches are those of the other kernel (attn_paged.cu), with tiles of 128 tokens, and the CTA as the
+// one worker of a stretch.  A unit has up to NR rows, and the products stand on their sides, so that the few rows are the
+// short dimension:
+//   S^T [128 tokens x NR]  = K [tokens x D] Q^T,           a tile of k as it lies in the cache, K-major
+//   O^T [D x TERMS NR]     = V^T [D x tokens] P^T,         a tile of v as it lies in the cache, M-major
+// A thread then has a token's scores of half of the rows, or a coordinate's sums of all: nothing is exchanged between
+// threads in a tile, unless a row's maximum rises by more than 2^8: weights are beside a maximum that may be that much
+// out of date.  The weights' bf16 terms (two, 16 bits, for bf16 results, three, 24 bits, for fp32 ones) are TERMS rows of
+// P each, so one pass over v does for all.  The tensor core cuts its sums off instead of rounding them; a tile's sums
+// start from zero and are added to the running ones in registers, in fp32.
+//
+// Warps: 0-7 weights; 8-11 sums; 12-13 copies (16 bytes at a time, from pages of any size, zeros where no row sees a
+// token); 14 products; 15 looks ahead: the pages of the next tiles' tokens.  k and v of a tile share a ring of five
+// half tiles.
+#include "attn_paged.cuh"
+
+namespace bl {
+namespace {
+
+using namespace attn;
+
+template <int NR_>
+struct TcShape {
+  static constexpr int ROWS = NR_, TT = 128;
+};
+
+constexpr int kThreads = 16 * 32;
+constexpr int kCopy = 2;                      // warps that copy
+constexpr int kSlots = 5, kHalf = 128 * 256;  // bytes of 128 rows of k or v
+constexpr int kBack = 4, kInfo = 8;           // tiles whose lists of odd values, whose descriptions are kept
+constexpr int kWeigh = 256;                   // threads of the weights
+constexpr float kSlack = 8.f;                 // log2 of what a weight may be above 1
+
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool a_m_major) {  // bf16 x bf16 -> fp32, M = 128
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_m_major) << 15) | (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+// M-major operand in the 128-byte swizzle: 64 values of M in 128 bytes, 8 rows of K in 1024; the next 64 of M lie
+// `m_bytes` on.
+__device__ __forceinline__ uint64_t tc_desc_m_major(uint32_t saddr, uint32_t m_bytes) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | uint64_t(m_bytes >> 4) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+
+// A tile, for the warps that weigh it and add it up.
+struct Tile {
+  int j0, length, n;      // its first token; the request's tokens, and new ones
+  Unit unit;
+  int fresh, begun, ends; // the first tile of a unit or of the stretch; the unit's first is in the stretch; its last
+  int left;               // tiles of the unit after this one
+  int request, whole;     // every row sees all of its tokens, if they are there
+  uint32_t real[4];       // tokens that are there
+};
+
+// A token of a tile whose value has infinities or NaN and that some rows do not see.
+struct Odd {
+  int token;              // of the tile
+  uint32_t seen;          // by row: who sees it
+};
+
+template <int NR>
+struct __align__(16) Tables {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t s_full[2], s_empty[2], o_full[2], o_empty[2], p_full, p_empty, voted[2], info[kBack], last;
+  uint64_t found[kBack], taken[kBack];  // the rows of a tile
+  uint32_t tmem;
+  Tile tile[kInfo];
+  int64_t row[kBack][128];       // where a token's row of k and v lies, -1: nowhere
+  float4 shift[NR / 4];          // maximum times scale
+  float top[NR];                 // the maximum that weights are beside
+  float part[4][NR];             // largest scores of the warps' tokens
+  int vote[kBack];               // whether a score of the tile is far above it
+  float4 keep[kBack][NR / 4];    // what the sums before the tile are multiplied by
+  float sum[kBack][4][NR], final_top[kBack][NR];  // of a unit that ends (here) with the tile
+  int odd_count[kBack];
+  Odd odd[kBack][128];
+  int64_t before[kThreads + 1];
+  int64_t warp_total[kThreads / 32];
+};
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+}
+// Folds v[0..15] over the 32 lanes: lane l gets op over all lanes of v[l % 16].
+template <class Op>
+__device__ __forceinline__ float fold(float (&v)[16], int lane, Op op) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = op(v[k], __shfl_xor_sync(0xffffffffu, v[k], 16));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < o; ++k) {
+      const bool up = lane & o;
+      const float mine = up ? v[k + o] : v[k], other = up ? v[k] : v[k + o];
+      v[k] = op(mine, __shfl_xor_sync(0xffffffffu, other, o));
+    }
+  return v[0];
+}
+
+__device__ __forceinline__ bool odd_value(uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; }
+
+// The rest of a wait that did not end at once, out of line: the roles' loops have to share the instruction cache.
+// Returns whether this or an earlier wait gave up.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, bool dead, unsigned int* err) {
+  if (!dead) dead = !mbar_wait_bounded(bar, parity, err);
+  return __any_sync(0xffffffffu, dead);
+}
+
+template <class S>
+__device__ __noinline__ Place<S> first_tile(const Args& a, const int64_t* before, int64_t share, int64_t t0) {
+  Place<S> at;
+  at.find(a, before, kThreads, share, t0);
+  return at;
+}
+
+template <int NR, bool F32>
+__global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a) {
+  using S = TcShape<NR>;
+  constexpr int TERMS = F32 ? 3 : 2, PN = TERMS * NR;
+  constexpr int kQBytes = NR * 256, kCols = 2 * NR + 2 * PN <= 128 ? 128 : 256;
+  extern __shared__ uint8_t raw[];
+  __shared__ Tables<NR> c;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* queries = ring + kSlots * kHalf;     // three units' q: [2][NR][64]
+  uint8_t* weights = queries + 3 * kQBytes;     // [2][PN][64 tokens]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool bad = false, dead = false;
+  // A wait that gave up is not repeated: the rest of the work then goes on on whatever is there.
+  auto wait = [&](uint64_t* bar, int parity) {
+    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, uint32_t(parity & 1)))) dead = wait_on(bar, parity & 1, dead, a.err);
+  };
+
+  if (warp == 14) {
+    tmem_alloc(&c.tmem, kCols);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&c.full[i], 32 * kCopy + kCopy);
+      mbar_init(&c.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.s_empty[i], 8);
+      mbar_init(&c.o_full[i], 1);
+      mbar_init(&c.o_empty[i], 4);
+      mbar_init(&c.voted[i], 8);
+    }
+    for (int i = 0; i < kBack; ++i) {
+      mbar_init(&c.info[i], 8);
+      mbar_init(&c.found[i], 1);
+      mbar_init(&c.taken[i], kCopy);
+      c.vote[i] = 0;
+      c.odd_count[i] = 0;
+    }
+    mbar_init(&c.p_full, 8);
+    mbar_init(&c.p_empty, 1);
+    mbar_init(&c.last, 1);
+    fence_barrier_init();
+  }
+  pdl_wait();
+
+  // tiles before every share of the requests
+  const int64_t share = (a.R + kThreads - 1) / kThreads;
+  {
+    int64_t mine = 0;
+    for (int64_t r = tid * share; r < min(a.R, (tid + 1) * share); ++r) {
+      const Request q = request_of<S>(a, r);
+      mine += int64_t(a.Hk) * q.blocks * q.tiles;
+      bad |= q.bad;
+    }
+    int64_t through = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t w = __shfl_up_sync(0xffffffffu, through, o);
+      if (lane >= o) through += w;
+    }
+    if (lane == 31) c.warp_total[warp] = through;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int64_t sum = 0;
+    for (int i = 0; i < warp; ++i) sum += c.warp_total[i];
+    c.before[tid + 1] = sum + through;
+    if (tid == 0) c.before[0] = 0;
+    __syncthreads();
+  }
+  const uint32_t tmem = c.tmem;
+  const int64_t all = c.before[kThreads];
+  const int64_t quota = max(int64_t(1), (all + gridDim.x - 1) / gridDim.x);
+  const int64_t t0 = blockIdx.x * quota;
+  const int count = int(max(int64_t(0), min(quota, all - t0)));
+
+  if (count > 0 && warp == 15) {
+    // ---- ahead: a lane has four tokens of a tile ----
+    Place<S> at = first_tile<S>(a, c.before, share, t0);
+    // Whether a row sees token `k` of a tile, and its page as the table has it (not looked at before it is needed).
+    auto seen = [&](const Place<S>& pl, int k) {
+      const int j = pl.token() + k;
+      return j < pl.q.length && !(a.window > 0 && j < pl.q.low && j >= a.sinks);
+    };
+    auto page_of = [&](const Place<S>& pl, int k) { return seen(pl, k) ? a.table[pl.r * a.W + a.by_page.quotient(pl.token() + k)] : -1; };
+    int entry[4], then_entry[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) entry[h] = page_of(at, h * 32 + lane);
+    Place<S> then = at;  // the tile after this one, whose pages are looked up meanwhile
+    bool fresh = true, begun = false;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const int buf = i % kBack;
+      if (i + 1 < count) {
+        then.next(a);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) then_entry[h] = page_of(then, h * 32 + lane);
+      }
+      if (i >= kBack) wait(&c.taken[buf], i / kBack - 1);
+      const int head = at.head(), row0 = at.row0(), j0 = at.token();
+      Tile& info = c.tile[i % kInfo];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int k = h * 32 + lane, j = j0 + k;
+        if (entry[h] < 0 || entry[h] >= a.pages) {
+          bad |= seen(at, k);
+          entry[h] = -1;
+        }
+        const unsigned there = __ballot_sync(0xffffffffu, entry[h] >= 0);
+        if (lane == 0) info.real[h] = there;
+        c.row[buf][k] = entry[h] < 0 ? -1 : ((int64_t(entry[h]) * a.Hk + head) * a.page + j - a.by_page.quotient(j) * a.page) * a.D;
+      }
+      if (fresh) begun = at.tile == 0;
+      if (lane == 0) {
+        info.j0 = j0;
+        info.length = at.q.length;
+        info.n = at.q.n;
+        info.unit = {at.q.first, head, row0, int(min(int64_t(at.q.n) * a.G - row0, int64_t(NR)))};
+        info.fresh = fresh;
+        info.begun = begun;
+        info.ends = at.tile + 1 == at.q.tiles;
+        info.left = at.q.tiles - 1 - at.tile;
+        info.request = int(at.r);
+        info.whole = j0 + 127 <= at.q.length - at.q.n &&
+                     (a.window <= 0 || j0 + 128 <= a.sinks || j0 > int64_t(at.q.length) - 1 - a.window);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.found[buf]);
+      fresh = at.tile + 1 == at.q.tiles;
+      at = then;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) entry[h] = then_entry[h];
+    }
+  } else if (count > 0 && (warp == 12 || warp == 13)) {
+    // ---- copies: a warp copies the rows of 64 tokens, two at a time ----
+    const int w = warp - 12;
+    const int chunk = lane % 16, sub = lane / 16;
+    const bool inside = chunk * 8 < a.D;
+    const uint32_t lane_to = smem_addr(ring) + (chunk / 8) * (kHalf / 2) + (w * 64 + sub) * 128 + (((chunk % 8) ^ sub) * 16);  // row 0 or 1
+    int unit = -1;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const int buf = i % kBack;
+      wait(&c.found[buf], i / kBack);
+      const Tile& now = c.tile[i % kInfo];
+      const bool fresh = now.fresh;
+      unit += fresh;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int seq = 2 * i + half, slot = seq % kSlots;
+        if (seq >= kSlots) wait(&c.empty[slot], seq / kSlots - 1);
+        if (half == 0 && fresh) {  // the unit's queries; the buffer's last reader was three units ago
+          const Unit u = now.unit;
+#pragma unroll 1
+          for (int k = w * 32 + lane; k < NR * 16; k += 32 * kCopy) {
+            const int row = k / 16, ch = k % 16;
+            const bool real = row < u.n && ch * 8 < a.D && !a.zero;
+            copy16(smem_addr(queries) + (unit % 3) * kQBytes + (ch / 8) * (kQBytes / 2) + row * 128 + ((ch % 8) ^ (row & 7)) * 16,
+                   a.q + (real ? row_at(a, u, row) + ch * 8 : 0), real);
+          }
+        }
+        const uint16_t* from = (half ? a.v : a.k) + (inside ? chunk * 8 : 0);
+        const uint32_t to = lane_to + slot * kHalf;
+        const int64_t* rows = c.row[buf] + w * 64 + sub;
+#pragma unroll 1
+        for (int g = 0; g < 32; g += 8) {
+          int64_t row[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) row[k] = rows[2 * (g + k)];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            copy16((to ^ ((2 * k & 6) * 16)) + 2 * (g + k) * 128, from + max(row[k], int64_t(0)), inside && row[k] >= 0);
+        }
+        // arrives when this thread's copies so far are done; the first lane's arrival is for the tile's description
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&c.full[slot])) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.full[slot]);
+      }
+      if (lane == 0) mbar_arrive(&c.taken[buf]);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (count > 0 && warp == 14) {
+    // ---- products: the next tile's scores are formed while this one's are weighed ----
+    const uint64_t k_at = umma_desc_sw128(smem_addr(ring)), q_at = umma_desc_sw128(smem_addr(queries));
+    const uint64_t v_at = tc_desc_m_major(smem_addr(ring), kHalf / 2), p_at = umma_desc_sw128(smem_addr(weights));
+    int units = -1;
+#pragma unroll 1
+    for (int i = 0; i <= count; ++i) {
+      if (i < count) {  // S(i)
+        const int slot = 2 * i % kSlots;
+        wait(&c.full[slot], 2 * i / kSlots);
+        if (i >= 2) wait(&c.s_empty[i & 1], i / 2 - 1);
+        tc_fence_after();
+        units += c.tile[i % kInfo].fresh;
+        if (elect_one()) {
+          fence_async_smem();  // the copies were made by the generic proxy
+          const uint64_t k = k_at + slot * (kHalf >> 4), q = q_at + (units % 3) * (kQBytes >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_f16(tmem + (i & 1) * NR, k + (ks / 4) * (kHalf >> 5) + (ks % 4) * 2, q + (ks / 4) * (kQBytes >> 5) + (ks % 4) * 2, tc_idesc(NR, false), ks > 0);
+          umma_commit(&c.s_full[i & 1]);
+          umma_commit(&c.empty[slot]);
+        }
+        __syncwarp();
+      }
+      if (i > 0) {  // O(i - 1)
+        const int j = i - 1, slot = (2 * j + 1) % kSlots;
+        wait(&c.full[slot], (2 * j + 1) / kSlots);
+        if (j >= 2) wait(&c.o_empty[j & 1], j / 2 - 1);
+        wait(&c.p_full, j);
+        tc_fence_after();
+        if (elect_one()) {
+          fence_async_smem();
+          const uint64_t v = v_at + slot * (kHalf >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_f16(tmem + 2 * NR + (j & 1) * PN, v + ks * (16 * 128 >> 4), p_at + (ks / 4) * (PN * 128 >> 4) + (ks % 4) * 2, tc_idesc(PN, true), ks > 0);
+          umma_commit(&c.o_full[j & 1]);
+          umma_commit(&c.p_empty);
+          umma_commit(&c.empty[slot]);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) umma_commit(&c.last);
+    __syncwarp();
+  } else if (count > 0 && warp >= 8) {
+    // ---- sums: thread t has coordinate t ----
+    const int t = tid - 256;
+    const uint32_t lanes = uint32_t(warp % 4 * 32) << 16;
+    float acc[NR];
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const int buf = i % kBack;
+      const Tile& was = c.tile[i % kInfo];
+      wait(&c.info[buf], i / kBack);
+      wait(&c.o_full[i & 1], i / 2);
+      __syncwarp();
+      tc_fence_after();
+      if (was.fresh) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) acc[r] = 0.f;
+      }
+#pragma unroll
+      for (int h = 0; h < NR; h += 16) {
+        uint32_t u[TERMS][16];
+        float o[16];
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) tmem_ld16(tmem + lanes + 2 * NR + (i & 1) * PN + k * NR + h, u[k]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          o[r] = __uint_as_float(u[TERMS - 1][r]);
+#pragma unroll
+          for (int k = TERMS - 2; k >= 0; --k) o[r] += __uint_as_float(u[k][r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const float4 keep = c.keep[buf][(h + r) / 4];
+          acc[h + r] = __fmaf_rn(acc[h + r], keep.x, o[r]);
+          acc[h + r + 1] = __fmaf_rn(acc[h + r + 1], keep.y, o[r + 1]);
+          acc[h + r + 2] = __fmaf_rn(acc[h + r + 2], keep.z, o[r + 2]);
+          acc[h + r + 3] = __fmaf_rn(acc[h + r + 3], keep.w, o[r + 3]);
+        }
+      }
+      tc_fence_before();
+      const int odd = c.odd_count[buf];
+#pragma unroll 1
+      for (int k = 0; k < odd; ++k) {
+        const Odd x = c.odd[buf][k];
+        const int j = was.j0 + x.token;
+        const int64_t entry = a.table[was.request * a.W + a.by_page.quotient(j)];
+        const float v = t < a.D ? bf16_bits_to_f32(a.v[((entry * a.Hk + was.unit.head) * a.page + j - a.by_page.quotient(j) * a.page) * a.D + t]) : 0.f;
+        if (!(fabsf(v) < INFINITY)) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (x.seen >> r & 1) acc[r] += v;  // times a weight above 0
+        }
+      }
+      if (was.ends || i + 1 == count) {
+        // To the workspace: as a part, or for the rolled loop below, which reads this thread's own sums back.
+        const bool out = was.begun && was.ends;
+        const int64_t part = out ? 2 * int64_t(gridDim.x) + blockIdx.x : 2 * int64_t(blockIdx.x) + was.begun;
+        float* sums = a.acc + part * a.rows * a.D + t;
+        if (t < a.D) {
+#pragma unroll
+          for (int row = 0; row < NR; ++row)
+            if (row < was.unit.n) sums[row * a.D] = acc[row];
+        }
+#pragma unroll 1
+        for (int row = 0; row < was.unit.n; ++row) {
+          const float l = (c.sum[buf][0][row] + c.sum[buf][1][row]) + (c.sum[buf][2][row] + c.sum[buf][3][row]);
+          const float top = c.final_top[buf][row];
+          if (!out) {
+            if (t == 0) a.stat[part * a.rows + row] = make_float2(top, l);
+          } else if (t < a.D) {
+            const float v = top == -INFINITY && l == 0.f ? 0.f : sums[row * a.D] * (1.f / l);
+            const int64_t to = row_at(a, was.unit, row) + t;
+            if (F32)
+              static_cast<float*>(a.out)[to] = v;
+            else
+              static_cast<uint16_t*>(a.out)[to] = f32_to_bf16_bits_rn(v);
+          }
+        }
+        if (t == 0 && i + 1 == count) {
+          Header header = {};
+          if (was.begun && !was.ends) header = Header{was.unit, 1, int((t0 + i + was.left) / quota - blockIdx.x), {0, 0}};
+          a.header[blockIdx.x] = header;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.o_empty[i & 1]);  // of the tile's tables too
+    }
+  } else if (count > 0) {
+    // ---- weights: thread t % 128 has a token of a tile, and 16 of the rows ----
+    static_assert(NR == 32, "16 rows to a thread");
+    constexpr int HR = 16;
+    const int t = tid % 128, first_row = tid / 128 * HR;
+    const uint32_t lanes = uint32_t(warp % 4 * 32) << 16;
+    const uint32_t flip = a.sign & 0x80000000u;
+    // where this lane stores weights: of tokens t & ~1 and t | 1, of the rows 4, 5, 6, 7 beyond every eight for odd lanes
+    const uint32_t p_to = smem_addr(weights) + first_row * 128 + (t / 64) * (PN * 128) + (t % 8 & 6) * 2;
+    const uint32_t p_chunk = t % 64 / 8;
+    const bool up = lane & 1;
+    float sum[HR];
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const int buf = i % kBack;
+      wait(&c.s_full[i & 1], i / 2);
+      __syncwarp();
+      tc_fence_after();
+      uint32_t zu[HR];
+      tmem_ld16(tmem + lanes + (i & 1) * NR + first_row, zu);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.s_empty[i & 1]);
+      const Tile& now = c.tile[i % kInfo];
+      const int j = now.j0 + t, nrows = now.unit.n;
+      const bool fresh = now.fresh;
+      float z[HR];
+#pragma unroll
+      for (int r = 0; r < HR; ++r) z[r] = __uint_as_float(zu[r] ^ flip);
+      const unsigned there = now.real[warp % 4];
+      const bool whole = now.whole && (now.real[0] & now.real[1] & now.real[2] & now.real[3]) == 0xffffffffu;
+      auto sees = [&](int row) {
+        const int mine = now.length - now.n + a.by_group.quotient(now.unit.row0 + row);
+        return (there >> lane & 1) && row < nrows && j <= mine && (a.window <= 0 || j > mine - a.window || j < a.sinks);
+      };
+      bool partly = false;
+      if (__builtin_expect(!whole, 0)) {
+        uint32_t mine = 0;
+#pragma unroll 1
+        for (int r = 0; r < HR; ++r) mine |= unsigned(sees(first_row + r)) << r;
+#pragma unroll
+        for (int r = 0; r < HR; ++r) z[r] = mine >> r & 1 ? z[r] : -INFINITY;
+        if (there >> lane & 1)
+#pragma unroll 1
+          for (int row = 0; row < nrows; ++row) partly |= !sees(row);
+      }
+      // Weights beside the maximum as it was; a unit's first tile has none yet.
+      float p[HR];
+      auto weigh = [&]() {
+#pragma unroll
+        for (int r = 0; r < HR; r += 4) {
+          const float4 shift = c.shift[(first_row + r) / 4];
+          p[r] = __fmaf_rn(z[r], a.scale, -shift.x);
+          p[r + 1] = __fmaf_rn(z[r + 1], a.scale, -shift.y);
+          p[r + 2] = __fmaf_rn(z[r + 2], a.scale, -shift.z);
+          p[r + 3] = __fmaf_rn(z[r + 3], a.scale, -shift.w);
+        }
+        float most = p[0];
+#pragma unroll
+        for (int r = 1; r < HR; ++r) most = fmaxf(most, p[r]);
+#pragma unroll
+        for (int r = 0; r < HR; ++r) p[r] = exp2_fast(p[r]);
+        return most;
+      };
+      const bool far = fresh || weigh() > kSlack;
+      if (__any_sync(0xffffffffu, far) && lane == 0) c.vote[buf] = 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.voted[i & 1]);
+      wait(&c.voted[i & 1], i / 2);
+      const bool rises = c.vote[buf] != 0;
+      if (__builtin_expect(rises, 0)) {
+        float v[HR];
+#pragma unroll
+        for (int r = 0; r < HR; ++r) v[r] = z[r];
+        const float most = fold(v, lane, [](float x, float y) { return fmaxf(x, y); });
+        if (lane < HR) c.part[warp % 4][first_row + lane] = most;
+        named_barrier_sync(2, kWeigh);
+        if (tid < NR) {
+          const float old = fresh ? -INFINITY : c.top[tid];
+          const float top = fmaxf(fmaxf(fmaxf(c.part[0][tid], c.part[1][tid]), fmaxf(c.part[2][tid], c.part[3][tid])), old);
+          const float base = top == -INFINITY ? 0.f : top;  // nothing seen yet: all weights are 0
+          c.top[tid] = top;
+          reinterpret_cast<float*>(c.shift)[tid] = base * a.scale;
+          reinterpret_cast<float*>(c.keep[buf])[tid] = exp2_fast((old - base) * a.scale);
+        }
+        named_barrier_sync(2, kWeigh);
+        weigh();
+#pragma unroll
+        for (int r = 0; r < HR; ++r) sum[r] = fresh ? p[r] : __fmaf_rn(sum[r], reinterpret_cast<const float*>(c.keep[buf])[first_row + r], p[r]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < HR; ++r) sum[r] += p[r];
+      }
+      if (!rises && tid < NR) reinterpret_cast<float*>(c.keep[buf])[tid] = 1.f;
+      if (tid == 0) c.vote[(i + 2) % kBack] = 0;
+      if (i > 0) wait(&c.p_empty, i - 1);
+      __syncwarp();
+      if (tid == 0) c.odd_count[(i + 1) % kBack] = 0;
+      // Two lanes exchange rows, so that each stores a pair of tokens; rows r and r + 4 lie in different banks.
+#pragma unroll
+      for (int k = 0; k < HR / 2; ++k) {
+        const int r = k / 4 * 8 + k % 4;
+        const float other = __shfl_xor_sync(0xffffffffu, up ? p[r] : p[r + 4], 1);
+        float lo = up ? other : p[r], hi = up ? p[r + 4] : other;
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term) {
+          const int row = term * NR + r;
+          const uint32_t u = bf16x2_rn(lo, hi);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_to + (up ? (row + 4) * 128 + ((p_chunk ^ ((r + 4) & 7)) * 16) : row * 128 + ((p_chunk ^ (r & 7)) * 16))),
+                       "r"(u)
+                       : "memory");
+          lo -= __uint_as_float(u << 16);
+          hi -= __uint_as_float(u & 0xffff0000u);
+        }
+      }
+      // A value that some rows do not see must not reach them, and 0 times an infinity or NaN would: such values are taken
+      // out of the tile, and added to the sums of the rows that see them.
+      if (__builtin_expect(__any_sync(0xffffffffu, partly), 0)) {
+        const int seq = 2 * i + 1, slot = seq % kSlots;
+        wait(&c.full[slot], seq / kSlots);
+        __syncwarp();
+        if (partly && first_row == 0) {  // the other half of the rows leaves it to this thread
+          bool odd = false;
+#pragma unroll 1
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t v = smem_addr(ring) + slot * kHalf + (k / 8) * (kHalf / 2) + t * 128 + (k % 8) * 16;
+            uint32_t u[4];
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(v) : "memory");
+            if (odd_value(u[0]) || odd_value(u[1]) || odd_value(u[2]) || odd_value(u[3])) {
+              odd = true;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((u[e] & 0x7f80u) == 0x7f80u) u[e] &= 0xffff0000u;
+                if ((u[e] & 0x7f800000u) == 0x7f800000u) u[e] &= 0x0000ffffu;
+              }
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(v), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+            }
+          }
+          if (odd) {
+            uint32_t seen = 0;
+#pragma unroll 1
+            for (int row = 0; row < nrows; ++row) seen |= unsigned(sees(row)) << row;
+            c.odd[buf][atomicAdd(&c.odd_count[buf], 1)] = Odd{t, seen};
+          }
+        }
+      }
+      if (__builtin_expect(now.ends || i + 1 == count, 0)) {
+        float v[HR];
+#pragma unroll
+        for (int r = 0; r < HR; ++r) v[r] = sum[r];
+        const float total = fold(v, lane, [](float x, float y) { return x + y; });
+        if (lane < HR) {
+          c.sum[buf][warp % 4][first_row + lane] = total;
+          if (warp % 4 == 0) c.final_top[buf][first_row + lane] = c.top[first_row + lane];
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&c.p_full);
+        mbar_arrive(&c.info[buf]);
+      }
+    }
+  } else if (count == 0 && tid == 0) {
+    a.header[blockIdx.x] = Header{};
+  }
+  if (count > 0 && warp == 14) mbar_wait_bounded(&c.last, 0, a.err);  // no product is in flight
+  __syncwarp();
+  if (__syncthreads_or(bad) && tid == 0) atomicOr(a.err, BL_DEVERR_RANGE);
+  if (warp == 14) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+  pdl_launch_dependents();
+}
+
+template <int NR, bool F32>
+cudaError_t launch_as(const Args& a, int grid, cudaStream_t s) {
+  constexpr int kBytes = 1024 + kSlots * kHalf + 3 * NR * 256 + (F32 ? 3 : 2) * NR * 256;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const cudaError_t e = raise_smem_cap(attn_paged_tc_kernel<NR, F32>, dev, kBytes);
+  if (e != cudaSuccess) return e;
+  return launch(attn_paged_tc_kernel<NR, F32>, dim3(grid), dim3(kThreads), kBytes, s, overlap_enabled(), a);
+}
+
+}  // namespace
+
+namespace attn {
+
+cudaError_t launch_tc(const Args& a, int grid, bool f32, cudaStream_t s) {
+  return f32 ? launch_as<32, true>(a, grid, s) : launch_as<32, false>(a, grid, s);
+}
+
+}  // namespace attn
+}  // namespace bl

@@ -461,7 +461,8 @@ def test_attn_one_token(B, lengths, H, Hk, D, page, f32):
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("lengths,counts,H,Hk,D,page", [
     ([40, 100, 17], [5, 2, 1], 10, 2, 128, 16), ([5, 9, 200], [5, 8, 3], 8, 8, 64, 16), ([70, 16, 30], [9, 16, 0], 6, 3, 128, 7), ([300], [33], 4, 1, 128, 16),
-    ([130, 60], [4, 7], 16, 1, 256, 32), ([64, 40], [40, 40], 5, 1, 80, 16), ([20, 8, 100, 1], [0, 8, 0, 1], 4, 2, 64, 16)])
+    ([130, 60], [4, 7], 16, 1, 256, 32), ([64, 40], [40, 40], 5, 1, 80, 16), ([20, 8, 100, 1], [0, 8, 0, 1], 4, 2, 64, 16),
+    ([500, 3, 130, 128, 129], [5, 3, 8, 4, 1], 10, 2, 128, 16), ([1000, 127], [8, 7], 8, 1, 128, 64), ([260, 255, 40], [5, 6, 5], 8, 2, 72, 16), ([90, 4, 385], [17, 4, 9], 3, 1, 128, 1)])
 def test_attn_drafts(B, lengths, counts, H, Hk, D, page, f32):
     """Several new tokens, each of which sees those before it; requests without any; rows behind the last request."""
     check_attn(B, Cache(lengths, Hk, D, page, 2), counts, H, f32, padding=3)
@@ -469,7 +470,8 @@ def test_attn_drafts(B, lengths, counts, H, Hk, D, page, f32):
 
 @gpu
 @pytest.mark.parametrize("window,sinks", [(1, 0), (16, 0), (16, 4), (100, 1), (5, 64), (33, 17), (1000, 4), (40, 1000), (1, 1)])
-@pytest.mark.parametrize("lengths,counts,H,Hk,D", [([300, 17, 64, 1], [1, 1, 1, 1], 10, 2, 128), ([260, 40, 90], [5, 3, 8], 4, 2, 64), ([150, 33], [4, 2], 6, 2, 256)])
+@pytest.mark.parametrize("lengths,counts,H,Hk,D", [([300, 17, 64, 1], [1, 1, 1, 1], 10, 2, 128), ([260, 40, 90], [5, 3, 8], 4, 2, 64), ([150, 33], [4, 2], 6, 2, 256),
+                                                   ([700, 140, 9], [5, 8, 9], 8, 1, 128), ([400, 130], [7, 6], 8, 2, 64)])
 def test_attn_window(B, lengths, counts, H, Hk, D, window, sinks):
     check_attn(B, Cache(lengths, Hk, D, 16, 3), counts, H, True, window=window, sinks=sinks)
 
@@ -481,6 +483,8 @@ def test_attn_many_requests_and_long_ones(B, f32):
     lengths = [int(n) for n in g.integers(1, 60, 300)]
     check_attn(B, Cache(lengths, 1, 64, 16, 4), [1] * 300, 2, f32)
     check_attn(B, Cache([6000, 3, 2500], 1, 128, 16, 5), [1, 1, 2], 2, f32)
+    check_attn(B, Cache([6000, 5, 2500], 1, 128, 16, 5), [3, 5, 6], 5, f32)
+    check_attn(B, Cache([max(n, 4) for n in lengths], 1, 64, 16, 4), [4] * 300, 5, f32)
 
 
 @gpu
