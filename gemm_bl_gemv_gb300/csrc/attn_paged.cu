@@ -559,8 +559,8 @@ cudaError_t launch_for(const Args& a, cudaStream_t s) {
   if (two && a.D <= 128) {
     const int grid = std::min(sm_count(), kMostCtas);
     const cudaError_t e = launch_tc(a, grid, F32, s);
-    if (e != cudaSuccess) return e;
-    return launch(attn_join_kernel<F32>, dim3(grid, 8), dim3(128), 0, s, true, a);
+    if (e == cudaSuccess) return launch(attn_join_kernel<F32>, dim3(grid, 8), dim3(128), 0, s, true, a);
+    if (e != cudaErrorNotSupported) return e;
   }
   if (a.D <= 64) return launch_as<Shape<64, 1>, F32>(a, s);
   if (a.D <= 128) return launch_as<Shape<128, 1>, F32>(a, s);

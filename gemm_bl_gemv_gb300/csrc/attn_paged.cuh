@@ -196,7 +196,8 @@ struct Place {
   }
 };
 
-// The kernel on the tensor cores of attn_paged_tc.cu: D <= 128, 32 rows to a unit.
+// The kernel of attn_paged_tc.cu: D <= 128, 32 rows to a unit; cudaErrorNotSupported, having launched nothing, for pages
+// that it has no boxes for.
 cudaError_t launch_tc(const Args& a, int grid, bool f32, cudaStream_t s);
 
 }  // namespace attn

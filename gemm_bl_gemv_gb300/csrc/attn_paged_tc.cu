@@ -12,9 +12,9 @@
 // P each, so one pass over v does for all.  The tensor core cuts its sums off instead of rounding them; a tile's sums
 // start from zero and are added to the running ones in registers, in fp32.
 //
-// Warps: 0-7 weights; 8-11 sums; 12-13 copies (16 bytes at a time, from pages of any size, zeros where no row sees a
-// token); 14 products; 15 looks ahead: the pages of the next tiles' tokens.  k and v of a tile share a ring of five
-// half tiles.
+// Warps: 0-7 weights; 8-11 sums; 12 and 13 start the copies of k and v (TMA boxes of a page's rows, zeros for a page that
+// is not there); 14 products; 15 looks ahead: the pages of the next tiles' tokens.  k and v of a tile share a ring of
+// five half tiles.  A page is 128 tokens or more in steps of 128, or 8, 16, 32 or 64; the other kernel takes others.
 #include "attn_paged.cuh"
 
 namespace bl {
@@ -28,7 +28,6 @@ struct TcShape {
 };
 
 constexpr int kThreads = 16 * 32;
-constexpr int kCopy = 2;                      // warps that copy
 constexpr int kSlots = 5, kHalf = 128 * 256;  // bytes of 128 rows of k or v
 constexpr int kBack = 4, kInfo = 8;           // tiles whose lists of odd values, whose descriptions are kept
 constexpr int kWeigh = 256;                   // threads of the weights
@@ -63,10 +62,12 @@ template <int NR>
 struct __align__(16) Tables {
   uint64_t full[kSlots], empty[kSlots];
   uint64_t s_full[2], s_empty[2], o_full[2], o_empty[2], p_full, p_empty, voted[2], info[kBack], last;
-  uint64_t found[kBack], taken[kBack];  // the rows of a tile
+  uint64_t found[kBack], taken[kBack];  // the pages of a tile
+  uint64_t q_full[3];
   uint32_t tmem;
   Tile tile[kInfo];
-  int64_t row[kBack][128];       // where a token's row of k and v lies, -1: nowhere
+  int block[kBack][16];          // the blocks of rows of a tile's pages in the caches
+  int row[kBack];                // the first row in them
   float4 shift[NR / 4];          // maximum times scale
   float top[NR];                 // the maximum that weights are beside
   float part[4][NR];             // largest scores of the warps' tokens
@@ -115,7 +116,8 @@ __device__ __noinline__ Place<S> first_tile(const Args& a, const int64_t* before
 }
 
 template <int NR, bool F32>
-__global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a, const __grid_constant__ CUtensorMap k_map,
+                                                                   const __grid_constant__ CUtensorMap v_map) {
   using S = TcShape<NR>;
   constexpr int TERMS = F32 ? 3 : 2, PN = TERMS * NR;
   constexpr int kQBytes = NR * 256, kCols = 2 * NR + 2 * PN <= 128 ? 128 : 256;
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
   }
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&c.full[i], 32 * kCopy + kCopy);
+      mbar_init(&c.full[i], 1);
       mbar_init(&c.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -150,10 +152,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
     for (int i = 0; i < kBack; ++i) {
       mbar_init(&c.info[i], 8);
       mbar_init(&c.found[i], 1);
-      mbar_init(&c.taken[i], kCopy);
+      mbar_init(&c.taken[i], 2);
       c.vote[i] = 0;
       c.odd_count[i] = 0;
     }
+    for (int i = 0; i < 3; ++i) mbar_init(&c.q_full[i], 32);
     mbar_init(&c.p_full, 8);
     mbar_init(&c.p_empty, 1);
     mbar_init(&c.last, 1);
@@ -195,12 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
   if (count > 0 && warp == 15) {
     // ---- ahead: a lane has four tokens of a tile ----
     Place<S> at = first_tile<S>(a, c.before, share, t0);
-    // Whether a row sees token `k` of a tile, and its page as the table has it (not looked at before it is needed).
-    auto seen = [&](const Place<S>& pl, int k) {
+    // The page of token `k` of a tile as the table has it (not looked at before it is needed).
+    auto page_of = [&](const Place<S>& pl, int k) {
       const int j = pl.token() + k;
-      return j < pl.q.length && !(a.window > 0 && j < pl.q.low && j >= a.sinks);
+      return j < pl.q.length ? a.table[pl.r * a.W + a.by_page.quotient(j)] : -1;
     };
-    auto page_of = [&](const Place<S>& pl, int k) { return seen(pl, k) ? a.table[pl.r * a.W + a.by_page.quotient(pl.token() + k)] : -1; };
+    const int box_log = 31 - __clz(min(a.page, 128));
     int entry[4], then_entry[4];
 #pragma unroll
     for (int h = 0; h < 4; ++h) entry[h] = page_of(at, h * 32 + lane);
@@ -220,13 +223,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const int k = h * 32 + lane, j = j0 + k;
+        const bool seen = j < at.q.length && !(a.window > 0 && j < at.q.low && j >= a.sinks);  // by a row
         if (entry[h] < 0 || entry[h] >= a.pages) {
-          bad |= seen(at, k);
+          bad |= seen;
           entry[h] = -1;
         }
-        const unsigned there = __ballot_sync(0xffffffffu, entry[h] >= 0);
+        const unsigned there = __ballot_sync(0xffffffffu, seen && entry[h] >= 0);
         if (lane == 0) info.real[h] = there;
-        c.row[buf][k] = entry[h] < 0 ? -1 : ((int64_t(entry[h]) * a.Hk + head) * a.page + j - a.by_page.quotient(j) * a.page) * a.D;
+        // of the page's first token in the tile: the block, one behind the last where there is none
+        const int off = j - a.by_page.quotient(j) * a.page;
+        if (k == 0) c.row[buf] = off;
+        if (k == 0 || off == 0) c.block[buf][k >> box_log] = entry[h] < 0 ? int(a.pages) * a.Hk : entry[h] * a.Hk + head;
       }
       if (fresh) begun = at.tile == 0;
       if (lane == 0) {
@@ -250,50 +257,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       for (int h = 0; h < 4; ++h) entry[h] = then_entry[h];
     }
   } else if (count > 0 && (warp == 12 || warp == 13)) {
-    // ---- copies: a warp copies the rows of 64 tokens, two at a time ----
-    const int w = warp - 12;
-    const int chunk = lane % 16, sub = lane / 16;
-    const bool inside = chunk * 8 < a.D;
-    const uint32_t lane_to = smem_addr(ring) + (chunk / 8) * (kHalf / 2) + (w * 64 + sub) * 128 + (((chunk % 8) ^ sub) * 16);  // row 0 or 1
+    // ---- copies of k (and the queries) or v ----
+    const int half = warp - 12;
+    const int rows = min(a.page, 128), boxes = 128 / rows;
+    const CUtensorMap* map = half ? &v_map : &k_map;
     int unit = -1;
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
-      const int buf = i % kBack;
+      const int buf = i % kBack, seq = 2 * i + half, slot = seq % kSlots;
       wait(&c.found[buf], i / kBack);
       const Tile& now = c.tile[i % kInfo];
-      const bool fresh = now.fresh;
-      unit += fresh;
+      if (seq >= kSlots) wait(&c.empty[slot], seq / kSlots - 1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&c.full[slot], kHalf);
+      __syncwarp();
+      // a lane per box of 64 columns of a page's rows
+      for (int x = lane; x < 2 * boxes; x += 32)
+        tma_load_3d(smem_addr(ring) + slot * kHalf + (x & 1) * (kHalf / 2) + (x >> 1) * rows * 128, map, (x & 1) * 64, c.row[buf], c.block[buf][x >> 1],
+                    &c.full[slot]);
+      if (half == 0 && now.fresh) {  // the unit's queries; the buffer's last reader was three units ago
+        ++unit;
+        const Unit u = now.unit;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int seq = 2 * i + half, slot = seq % kSlots;
-        if (seq >= kSlots) wait(&c.empty[slot], seq / kSlots - 1);
-        if (half == 0 && fresh) {  // the unit's queries; the buffer's last reader was three units ago
-          const Unit u = now.unit;
-#pragma unroll 1
-          for (int k = w * 32 + lane; k < NR * 16; k += 32 * kCopy) {
-            const int row = k / 16, ch = k % 16;
-            const bool real = row < u.n && ch * 8 < a.D && !a.zero;
-            copy16(smem_addr(queries) + (unit % 3) * kQBytes + (ch / 8) * (kQBytes / 2) + row * 128 + ((ch % 8) ^ (row & 7)) * 16,
-                   a.q + (real ? row_at(a, u, row) + ch * 8 : 0), real);
-          }
+        for (int k = lane; k < NR * 16; k += 32) {
+          const int row = k / 16, ch = k % 16;
+          const bool real = row < u.n && ch * 8 < a.D && !a.zero;
+          copy16(smem_addr(queries) + (unit % 3) * kQBytes + (ch / 8) * (kQBytes / 2) + row * 128 + ((ch % 8) ^ (row & 7)) * 16,
+                 a.q + (real ? row_at(a, u, row) + ch * 8 : 0), real);
         }
-        const uint16_t* from = (half ? a.v : a.k) + (inside ? chunk * 8 : 0);
-        const uint32_t to = lane_to + slot * kHalf;
-        const int64_t* rows = c.row[buf] + w * 64 + sub;
-#pragma unroll 1
-        for (int g = 0; g < 32; g += 8) {
-          int64_t row[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) row[k] = rows[2 * (g + k)];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            copy16((to ^ ((2 * k & 6) * 16)) + 2 * (g + k) * 128, from + max(row[k], int64_t(0)), inside && row[k] >= 0);
-        }
-        // arrives when this thread's copies so far are done; the first lane's arrival is for the tile's description
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&c.full[slot])) : "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.full[slot]);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&c.q_full[unit % 3])) : "memory");
       }
+      __syncwarp();
       if (lane == 0) mbar_arrive(&c.taken[buf]);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -309,9 +303,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
         wait(&c.full[slot], 2 * i / kSlots);
         if (i >= 2) wait(&c.s_empty[i & 1], i / 2 - 1);
         tc_fence_after();
-        units += c.tile[i % kInfo].fresh;
+        if (c.tile[i % kInfo].fresh) {
+          ++units;
+          wait(&c.q_full[units % 3], units / 3);
+          fence_async_smem();  // the queries were copied by the generic proxy
+          __syncwarp();
+        }
         if (elect_one()) {
-          fence_async_smem();  // the copies were made by the generic proxy
           const uint64_t k = k_at + slot * (kHalf >> 4), q = q_at + (units % 3) * (kQBytes >> 4);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
@@ -328,7 +326,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
         wait(&c.p_full, j);
         tc_fence_after();
         if (elect_one()) {
-          fence_async_smem();
           const uint64_t v = v_at + slot * (kHalf >> 4);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
@@ -461,21 +458,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       for (int r = 0; r < HR; ++r) z[r] = __uint_as_float(zu[r] ^ flip);
       const unsigned there = now.real[warp % 4];
       const bool whole = now.whole && (now.real[0] & now.real[1] & now.real[2] & now.real[3]) == 0xffffffffu;
-      auto sees = [&](int row) {
-        const int mine = now.length - now.n + a.by_group.quotient(now.unit.row0 + row);
-        return (there >> lane & 1) && row < nrows && j <= mine && (a.window <= 0 || j > mine - a.window || j < a.sinks);
-      };
-      bool partly = false;
-      if (__builtin_expect(!whole, 0)) {
-        uint32_t mine = 0;
-#pragma unroll 1
-        for (int r = 0; r < HR; ++r) mine |= unsigned(sees(first_row + r)) << r;
+      // Which rows see the token: those from its own new token on, up to the one whose window it has left.
+      const uint32_t rows_mask = nrows >= 32 ? 0xffffffffu : (1u << nrows) - 1;
+      uint32_t seen = rows_mask;
+      if (!whole) {
+        const int first_new = now.length - now.n;
+        const int from = max(0, min(j - first_new, now.n)) * a.G - now.unit.row0;
+        const bool bounded = a.window > 0 && j >= a.sinks;
+        const int end = (bounded ? int(max(int64_t(0), min(j + a.window - first_new, int64_t(now.n)))) : now.n) * a.G - now.unit.row0;
+        auto below = [](int r) { return r >= 32 ? 0xffffffffu : r <= 0 ? 0u : (1u << r) - 1; };
+        seen &= there >> lane & 1 ? below(end) & ~below(from) : 0u;
 #pragma unroll
-        for (int r = 0; r < HR; ++r) z[r] = mine >> r & 1 ? z[r] : -INFINITY;
-        if (there >> lane & 1)
-#pragma unroll 1
-          for (int row = 0; row < nrows; ++row) partly |= !sees(row);
+        for (int r = 0; r < HR; ++r) z[r] = seen >> (first_row + r) & 1 ? z[r] : -INFINITY;
       }
+      const bool partly = seen != rows_mask;
       // Weights beside the maximum as it was; a unit's first tile has none yet.
       float p[HR];
       auto weigh = [&]() {
@@ -545,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
           hi -= __uint_as_float(u & 0xffff0000u);
         }
       }
-      // A value that some rows do not see must not reach them, and 0 times an infinity or NaN would: such values are taken
+      // A value that some rows do not see (or none: the rest of a page) must not reach them, and 0 times an infinity or NaN would: such values are taken
       // out of the tile, and added to the sums of the rows that see them.
       if (__builtin_expect(__any_sync(0xffffffffu, partly), 0)) {
         const int seq = 2 * i + 1, slot = seq % kSlots;
@@ -553,9 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
         __syncwarp();
         if (partly && first_row == 0) {  // the other half of the rows leaves it to this thread
           bool odd = false;
-#pragma unroll 1
-          for (int k = 0; k < 16; ++k) {
-            const uint32_t v = smem_addr(ring) + slot * kHalf + (k / 8) * (kHalf / 2) + t * 128 + (k % 8) * 16;
+#pragma unroll 4
+          for (int k = 0; k < 16; ++k) {  // lanes begin at different banks
+            const uint32_t v = smem_addr(ring) + slot * kHalf + (k / 8) * (kHalf / 2) + t * 128 + ((k ^ t) % 8) * 16;
             uint32_t u[4];
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(v) : "memory");
             if (odd_value(u[0]) || odd_value(u[1]) || odd_value(u[2]) || odd_value(u[3])) {
@@ -568,12 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
               asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(v), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
             }
           }
-          if (odd) {
-            uint32_t seen = 0;
-#pragma unroll 1
-            for (int row = 0; row < nrows; ++row) seen |= unsigned(sees(row)) << row;
-            c.odd[buf][atomicAdd(&c.odd_count[buf], 1)] = Odd{t, seen};
-          }
+          if (odd && seen) c.odd[buf][atomicAdd(&c.odd_count[buf], 1)] = Odd{t, seen};
         }
       }
       if (__builtin_expect(now.ends || i + 1 == count, 0)) {
@@ -607,13 +598,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
 }
 
 template <int NR, bool F32>
-cudaError_t launch_as(const Args& a, int grid, cudaStream_t s) {
+cudaError_t launch_as(const Args& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int grid, cudaStream_t s) {
   constexpr int kBytes = 1024 + kSlots * kHalf + 3 * NR * 256 + (F32 ? 3 : 2) * NR * 256;
   int dev = 0;
   cudaGetDevice(&dev);
   const cudaError_t e = raise_smem_cap(attn_paged_tc_kernel<NR, F32>, dev, kBytes);
   if (e != cudaSuccess) return e;
-  return launch(attn_paged_tc_kernel<NR, F32>, dim3(grid), dim3(kThreads), kBytes, s, overlap_enabled(), a);
+  return launch(attn_paged_tc_kernel<NR, F32>, dim3(grid), dim3(kThreads), kBytes, s, overlap_enabled(), a, k_map, v_map);
 }
 
 }  // namespace
@@ -621,7 +612,13 @@ cudaError_t launch_as(const Args& a, int grid, cudaStream_t s) {
 namespace attn {
 
 cudaError_t launch_tc(const Args& a, int grid, bool f32, cudaStream_t s) {
-  return f32 ? launch_as<32, true>(a, grid, s) : launch_as<32, false>(a, grid, s);
+  const bool whole = a.page % 128 == 0 || (a.page < 128 && a.page >= 8 && 128 % a.page == 0);
+  CUtensorMap k_map, v_map;
+  const uint64_t blocks = uint64_t(a.pages) * a.Hk;
+  if (!whole || blocks >= 0x7fffffff || !encode_tmap_blocks_bf16(&k_map, a.k, a.D, a.page, blocks, 64, std::min(a.page, 128)) ||
+      !encode_tmap_blocks_bf16(&v_map, a.v, a.D, a.page, blocks, 64, std::min(a.page, 128)))
+    return cudaErrorNotSupported;
+  return f32 ? launch_as<32, true>(a, k_map, v_map, grid, s) : launch_as<32, false>(a, k_map, v_map, grid, s);
 }
 
 }  // namespace attn

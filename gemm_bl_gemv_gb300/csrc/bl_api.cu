@@ -55,12 +55,12 @@ cudaStream_t S(bl_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 bool overlap_enabled() { return g_overlap.load(std::memory_order_relaxed) != 0; }
 
-bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
-                       uint32_t box_inner, uint32_t box_outer, bool swizzle128) {
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static Encode encode = nullptr;
+namespace {
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static EncodeTiled encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
     void* fn = nullptr;
@@ -68,8 +68,15 @@ bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint6
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
             cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      encode = reinterpret_cast<Encode>(fn);
+      encode = reinterpret_cast<EncodeTiled>(fn);
   });
+  return encode;
+}
+}  // namespace
+
+bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                       uint32_t box_inner, uint32_t box_outer, bool swizzle128) {
+  const EncodeTiled encode = encode_tiled();
   if (!encode || box_inner % 16 || box_inner == 0 || box_inner > 256 || box_outer == 0 || box_outer > 256 ||
       row_bytes % 16 || inner == 0 || outer == 0 || inner >= (uint64_t(1) << 32) || outer >= (uint64_t(1) << 32))
     return false;
@@ -78,6 +85,19 @@ bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint6
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dim, stride, boxd, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tmap_blocks_bf16(CUtensorMap* map, const void* base, uint64_t width, uint64_t rows, uint64_t blocks,
+                             uint32_t box_width, uint32_t box_rows) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode || width % 8 || width == 0 || rows == 0 || blocks == 0 || blocks >= (uint64_t(1) << 31) ||
+      rows >= (uint64_t(1) << 31) || box_width % 8 || box_width > 64 || box_rows == 0 || box_rows > 256)
+    return false;
+  const cuuint64_t dim[3] = {width, rows, blocks}, stride[2] = {width * 2, rows * width * 2};
+  const cuuint32_t boxd[3] = {box_width, box_rows, 1}, estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, stride, boxd, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 unsigned int* dev_error_ptr() {

@@ -37,6 +37,11 @@ unsigned int* dev_error_ptr();
 bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                        uint32_t box_inner, uint32_t box_outer, bool swizzle128);
 
+// A 3-D tiled TMA descriptor over bf16 [blocks][rows][width] without gaps at `base` (16-byte aligned, width a multiple of
+// 8), loading boxes of box_rows x box_width of one block in the 128-byte swizzle; elements outside read as zero.
+bool encode_tmap_blocks_bf16(CUtensorMap* map, const void* base, uint64_t width, uint64_t rows, uint64_t blocks,
+                             uint32_t box_width, uint32_t box_rows);
+
 // Launch plans (geometry, grid, kernel attributes already set) remembered per
 // (device, N, K) so that repeated calls skip the occupancy queries.
 template <class P>
