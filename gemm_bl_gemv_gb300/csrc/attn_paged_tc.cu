@@ -29,7 +29,10 @@ struct TcShape {
 
 constexpr int kThreads = 16 * 32;
 constexpr int kSlots = 5, kHalf = 128 * 256;  // bytes of 128 rows of k or v
-constexpr int kBack = 4, kInfo = 8;           // tiles whose lists of odd values, whose descriptions are kept
+constexpr int kBack = 4;                      // tiles whose pages, lists of odd values and sums of weights are kept
+// Tiles whose descriptions are kept.  Warp 15 describes tile j when the copies of j - 4 are on their way; those waited for
+// the product with v of j - 7, and that for the sums of j - 9: the sums of j - 8 may still read their tile's.
+constexpr int kInfo = 16;
 constexpr int kWeigh = 256;                   // threads of the weights
 constexpr float kSlack = 8.f;                 // log2 of what a weight may be above 1
 

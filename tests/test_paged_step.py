@@ -384,8 +384,9 @@ def test_rope_append_infinities_stay_in_their_head(B):
 class Cache:
     """Requests of the given lengths on randomly placed pages; what no request owns, and the rest of their pages, is NaN."""
 
-    def __init__(self, lengths, Hk, D, page, seed, spare=3, extra_w=1, k_scale=1.0):
+    def __init__(self, lengths, Hk, D, page, seed, spare=3, wide=False, k_scale=1.0):
         g = rng(Hk, D, page, seed, len(lengths))
+        extra_w = -(-4096 // page) if wide else 1  # tables for 4096 tokens and more: tiles of 128 tokens where D is 104..128
         self.lengths, self.page, self.Hk, self.D = list(lengths), page, Hk, D
         need = [-(-n // page) for n in lengths]
         self.pages = sum(need) + spare
@@ -448,67 +449,83 @@ def check_attn(B, cache, counts, H, f32, window=0, sinks=0, scale=None, seed=0, 
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("lengths,H,Hk,D,page", [
     ([1], 1, 1, 8, 16), ([2, 15, 16, 17], 4, 4, 64, 16), ([33, 100, 1], 10, 2, 128, 16), ([700], 20, 5, 128, 16), ([31, 32, 33, 64], 3, 1, 40, 32),
     ([129, 5], 8, 1, 80, 7), ([90, 300], 6, 2, 256, 16), ([50, 1, 2], 2, 2, 136, 1), ([400, 3, 77], 40, 8, 128, 128), ([65], 17, 1, 96, 8),
     ([140, 20], 40, 1, 64, 16), ([1500, 40, 900], 8, 2, 64, 64)])
-def test_attn_one_token(B, lengths, H, Hk, D, page, f32):
-    check_attn(B, Cache(lengths, Hk, D, page, 1), [1] * len(lengths), H, f32)
+def test_attn_one_token(B, lengths, H, Hk, D, page, f32, wide):
+    check_attn(B, Cache(lengths, Hk, D, page, 1, wide=wide), [1] * len(lengths), H, f32)
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("lengths,counts,H,Hk,D,page", [
     ([40, 100, 17], [5, 2, 1], 10, 2, 128, 16), ([5, 9, 200], [5, 8, 3], 8, 8, 64, 16), ([70, 16, 30], [9, 16, 0], 6, 3, 128, 7), ([300], [33], 4, 1, 128, 16),
     ([130, 60], [4, 7], 16, 1, 256, 32), ([64, 40], [40, 40], 5, 1, 80, 16), ([20, 8, 100, 1], [0, 8, 0, 1], 4, 2, 64, 16),
     ([500, 3, 130, 128, 129], [5, 3, 8, 4, 1], 10, 2, 128, 16), ([1000, 127], [8, 7], 8, 1, 128, 64), ([260, 255, 40], [5, 6, 5], 8, 2, 72, 16), ([90, 4, 385], [17, 4, 9], 3, 1, 128, 1)])
-def test_attn_drafts(B, lengths, counts, H, Hk, D, page, f32):
+def test_attn_drafts(B, lengths, counts, H, Hk, D, page, f32, wide):
     """Several new tokens, each of which sees those before it; requests without any; rows behind the last request."""
-    check_attn(B, Cache(lengths, Hk, D, page, 2), counts, H, f32, padding=3)
+    check_attn(B, Cache(lengths, Hk, D, page, 2, wide=wide), counts, H, f32, padding=3)
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (16, 0), (16, 4), (100, 1), (5, 64), (33, 17), (1000, 4), (40, 1000), (1, 1)])
 @pytest.mark.parametrize("lengths,counts,H,Hk,D", [([300, 17, 64, 1], [1, 1, 1, 1], 10, 2, 128), ([260, 40, 90], [5, 3, 8], 4, 2, 64), ([150, 33], [4, 2], 6, 2, 256),
                                                    ([700, 140, 9], [5, 8, 9], 8, 1, 128), ([400, 130], [7, 6], 8, 2, 64)])
-def test_attn_window(B, lengths, counts, H, Hk, D, window, sinks):
-    check_attn(B, Cache(lengths, Hk, D, 16, 3), counts, H, True, window=window, sinks=sinks)
+def test_attn_window(B, lengths, counts, H, Hk, D, window, sinks, wide):
+    check_attn(B, Cache(lengths, Hk, D, 16, 3, wide=wide), counts, H, True, window=window, sinks=sinks)
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("f32", [False, True])
-def test_attn_many_requests_and_long_ones(B, f32):
+def test_attn_many_requests_and_long_ones(B, f32, wide):
     g = rng(11)
     lengths = [int(n) for n in g.integers(1, 60, 300)]
-    check_attn(B, Cache(lengths, 1, 64, 16, 4), [1] * 300, 2, f32)
-    check_attn(B, Cache([6000, 3, 2500], 1, 128, 16, 5), [1, 1, 2], 2, f32)
-    check_attn(B, Cache([6000, 5, 2500], 1, 128, 16, 5), [3, 5, 6], 5, f32)
-    check_attn(B, Cache([max(n, 4) for n in lengths], 1, 64, 16, 4), [4] * 300, 5, f32)
+    check_attn(B, Cache(lengths, 1, 64, 16, 4, wide=wide), [1] * 300, 2, f32)
+    check_attn(B, Cache([6000, 3, 2500], 1, 128, 16, 5, wide=wide), [1, 1, 2], 2, f32)
+    check_attn(B, Cache([6000, 5, 2500], 1, 128, 16, 5, wide=wide), [3, 5, 6], 5, f32)
+    check_attn(B, Cache([max(n, 4) for n in lengths], 1, 128, 16, 4, wide=wide), [4] * 300, 5, f32)
 
 
 @gpu
-def test_attn_rows_that_see_nothing(B):
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("page,window,sinks", [(32, 0, 0), (16, 1000, 4), (256, 0, 0), (8, 300, 200)])
+def test_attn_units_that_follow_each_other(B, page, window, sinks, wide):
+    """Many units of many rows and a few tiles each, one after the other in a CTA."""
+    lengths = [int(n) for n in rng(page).integers(200, 1500, 20)]
+    check_attn(B, Cache(lengths, 8, 128, page, 15, wide=wide), [1 + r % 5 for r in range(20)], 40, True, window=window, sinks=sinks)
+
+
+@gpu
+@pytest.mark.parametrize("wide", [False, True])
+def test_attn_rows_that_see_nothing(B, wide):
     """A length of zero, new tokens before the beginning, an empty table: 0."""
-    cache = Cache([0, 3, 40], 2, 64, 16, 6)
+    cache = Cache([0, 3, 40], 2, 128, 16, 6, wide=wide)
     check_attn(B, cache, [2, 5, 1], 4, True)
     k, v, table, length = cache.gpu()
-    q = torch.ones(3, 4, 64, dtype=BF, device="cuda")
+    q = torch.ones(3, 4, 128, dtype=BF, device="cuda")
     out = B.bl_attn_paged(q, k, v, table, ints([0, 0, 0]), ints([0, 1, 2, 3]), 1.0, out_dtype=F32)
     assert torch.equal(out, torch.zeros_like(out))
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
-def test_attn_scale_and_peaked_scores(B, scale):
-    check_attn(B, Cache([200, 31], 2, 64, 16, 7, k_scale=2.0), [1, 3], 4, True, scale=scale)
+def test_attn_scale_and_peaked_scores(B, scale, wide):
+    check_attn(B, Cache([200, 31, 700], 2, 112, 16, 7, k_scale=2.0, wide=wide), [1, 3, 9], 4, True, scale=scale)
 
 
 @gpu
-def test_attn_scores_of_minus_infinity(B):
+@pytest.mark.parametrize("wide", [False, True])
+def test_attn_scores_of_minus_infinity(B, wide):
     """Keys with an infinity against the query have no weight; a row with no other key gives 0."""
-    cache = Cache([40, 20], 1, 64, 16, 8)
-    q = np.abs(bf16_round(rng(1).standard_normal((2, 2, 64)).astype(np.float32))) + np.float32(0.125)
+    cache = Cache([40, 20], 1, 128, 16, 8, wide=wide)
+    q = np.abs(bf16_round(rng(1).standard_normal((2, 2, 128)).astype(np.float32))) + np.float32(0.125)
     q = bf16_round(q)
     for k, _ in cache.rows[1:]:
         k[:, :, 3] = -np.inf
@@ -523,17 +540,18 @@ def test_attn_scores_of_minus_infinity(B):
     keep = np.r_[0:5, 30:40]
     for h in range(2):
         ref, cond, size = R.attention_row(q[0, h], k0[keep, 0], cache.rows[0][1][keep, 0], np.ones(15, bool), 0.125)
-        assert np.all(np.abs(out[0, h] - ref) <= attn_bound(ref[None], cond[None], np.array([size]), 40, 64, True)[0])
+        assert np.all(np.abs(out[0, h] - ref) <= attn_bound(ref[None], cond[None], np.array([size]), 40, 128, True)[0])
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
 @pytest.mark.parametrize("D,H", [(64, 4), (128, 4), (256, 2), (128, 12)])
-def test_attn_infinities_stay_where_they_are_seen(B, what, D, H):
+def test_attn_infinities_stay_where_they_are_seen(B, what, D, H, wide):
     """A key or value that is not finite reaches the rows that see it and no others: later drafts, other windows, other
     requests, other heads."""
     lengths, counts = [70, 50], [6, 2]
-    cache = Cache(lengths, 2, D, 16, 9)
+    cache = Cache(lengths, 2, D, 16, 9, wide=wide)
     base = host(check_attn(B, cache, counts, H, True, window=20, sinks=3))
     G = H // 2
     for name, r, j, first, last in (("v", 0, 67, 3, 6), ("v", 0, 46, 0, 2), ("k", 0, 67, 3, 6), ("v", 1, 49, 7, 8), ("v", 0, 1, 0, 6), ("v", 0, 30, 0, 0)):
@@ -555,9 +573,10 @@ def test_attn_infinities_stay_where_they_are_seen(B, what, D, H):
 
 
 @gpu
-def test_attn_bad_pages_are_left_out(B):
-    cache = Cache([100, 40], 2, 64, 16, 10)
-    q = bf16_round(rng(3).standard_normal((2, 4, 64)).astype(np.float32))
+@pytest.mark.parametrize("wide", [False, True])
+def test_attn_bad_pages_are_left_out(B, wide):
+    cache = Cache([100, 40], 2, 128, 16, 10, wide=wide)
+    q = bf16_round(rng(3).standard_normal((2, 4, 128)).astype(np.float32))
     for entry in (cache.pages, 1 << 30, -1, -(1 << 31)):
         k, v, table, length = cache.gpu()
         table[0, 2] = entry
@@ -567,23 +586,24 @@ def test_attn_bad_pages_are_left_out(B):
         seen[32:48] = False
         for h in range(4):
             ref, cond, size = R.attention_row(q[0, h], cache.rows[0][0][:, h // 2], cache.rows[0][1][:, h // 2], seen, 0.125)
-            assert np.all(np.abs(host(out)[0, h] - ref) <= attn_bound(ref[None], cond[None], np.array([size]), 100, 64, True)[0])
+            assert np.all(np.abs(host(out)[0, h] - ref) <= attn_bound(ref[None], cond[None], np.array([size]), 100, 128, True)[0])
     k, v, table, length = cache.gpu()
     # lengths beyond the table, negative ones, starts outside the rows or falling
-    for length, start in (([16 * 8, 40], [0, 1, 2]), ([-3, 40], [0, 1, 2]), ([100, 40], [0, 1, 9]), ([100, 40], [-2, 1, 2]), ([100, 40], [0, 2, 1]),
+    for length, start in (([1 << 20, 40], [0, 1, 2]), ([-3, 40], [0, 1, 2]), ([100, 40], [0, 1, 9]), ([100, 40], [-2, 1, 2]), ([100, 40], [0, 2, 1]),
                           ([100, 40], [0, 1 << 31 - 1, 2])):
         out = B.bl_attn_paged(dev(q, BF), k, v, table, ints(length), ints(start), 0.125, out_dtype=F32)
         assert range_error(B), (length, start)
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("H,Hk,counts", [(10, 2, [1, 1, 1]), (16, 2, [3, 5, 1])])
-def test_attn_repeats_bit_for_bit_and_shares_a_workspace(B, H, Hk, counts):
-    cache = Cache([900, 17, 2000], Hk, 128, 16, 11)
+def test_attn_repeats_bit_for_bit_and_shares_a_workspace(B, H, Hk, counts, wide):
+    cache = Cache([900, 17, 2000], Hk, 128, 16, 11, wide=wide)
     ws = B.attn_paged_workspace(sum(counts), H, Hk, 128)
     ws.fill_(255)
     first = check_attn(B, cache, counts, H, False, workspace=ws)
-    other = Cache([30, 1200], Hk, 128, 16, 12)
+    other = Cache([30, 1200], Hk, 128, 16, 12, wide=wide)
     check_attn(B, other, [1, 1], H, True, workspace=ws)
     again = check_attn(B, cache, counts, H, False, workspace=ws)
     assert torch.equal(first, again)
