@@ -4,7 +4,8 @@
 // for coordinates i and i + rotary / 2, in fp32 and rounded to bf16 once; q goes to
 // q, k and v to row `slot` of the paged cache.
 //
-// Bound: HBM for prompts, launch and two dependent reads (position, angle) for few tokens.
+// Bound: HBM for prompts, launch and two dependent reads (position, angle) for few tokens: one token 2.2 us, 311 of 56
+// heads in fp32 3.6 us, 8192 of 30 heads in bf16 26.5 us (4.9 TB/s; a copy of the same bytes takes 21.5 us).
 #include "bl_device.cuh"
 #include "bl_internal.h"
 
@@ -61,7 +62,6 @@ __device__ __forceinline__ void store(uint16_t* y, int64_t i, const float (&v)[V
 // first loads of a row go out before its position and slot are there.
 template <bool XB, int VEC>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a) {
-  constexpr int kTurn = XB ? 4 : 2, kCopy = 2;  // loads in flight
   const int64_t m = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
   const int t = threadIdx.x, threads = blockDim.x;
   const int pairs = a.half / VEC, heads = a.H + 2 * a.Hk, turned = a.H + a.Hk;
@@ -74,32 +74,27 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a) {
   pdl_wait();
   if (m < a.M) {
     const int position = a.position[m], slot = a.slot[m];
-    Raw<XB, VEC> v[kTurn], w[kTurn], c[kCopy];
-    auto load_pairs = [&](int h0, int chunk) {
-#pragma unroll
-      for (int k = 0; k < kTurn; ++k)
-        if (h0 + k * groups < turned && group < groups) {
-          const int64_t i = from + int64_t(h0 + k * groups) * a.D + chunk * VEC;
-          v[k].load(a.x, i);
-          w[k].load(a.x, i + a.half);
-        }
+    Raw<XB, VEC> v, w, c;
+    auto load_pair = [&](int head, int chunk) {
+      if (head < turned && group < groups) {
+        const int64_t i = from + int64_t(head) * a.D + chunk * VEC;
+        v.load(a.x, i);
+        w.load(a.x, i + a.half);
+      }
     };
     auto item = [&](int at, int& head, int& i) {
       head = at < first ? at / rest : turned + (at - first) / all;
       i = at < first ? 2 * a.half + at % rest * VEC : (at - first) % all * VEC;
     };
-    auto load_items = [&](int at0) {
-#pragma unroll
-      for (int k = 0; k < kCopy; ++k)
-        if (at0 + k * threads < items) {
-          int head, i;
-          item(at0 + k * threads, head, i);
-          c[k].load(a.x, from + int64_t(head) * a.D + i);
-        }
+    auto load_item = [&](int at) {
+      if (at >= items) return;
+      int head, i;
+      item(at, head, i);
+      c.load(a.x, from + int64_t(head) * a.D + i);
     };
     const int chunk0 = t % min(pairs, threads);
-    load_pairs(group, chunk0);
-    load_items(t);
+    load_pair(group, chunk0);
+    load_item(t);
     const bool stored = slot >= 0 && slot < a.slots;
     bad = position >= a.positions || (position >= 0 && slot >= a.slots);
     if (position >= 0 && position < a.positions) {
@@ -115,39 +110,31 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a) {
         Raw<false, VEC> cs, sn;
         cs.load(a.cos, int64_t(position) * a.half + chunk * VEC);
         sn.load(a.sin, int64_t(position) * a.half + chunk * VEC);
-        for (int h0 = group; h0 < turned; h0 += kTurn * groups) {
-          if (h0 != group || chunk != chunk0) load_pairs(h0, chunk);
+        for (int head = group; head < turned; head += groups) {
+          if (head != group || chunk != chunk0) load_pair(head, chunk);
+          uint16_t* to = place(head);
+          if (!to) continue;
+          float x[VEC], y[VEC];
 #pragma unroll
-          for (int k = 0; k < kTurn; ++k) {
-            const int head = h0 + k * groups;
-            uint16_t* to = head < turned ? place(head) : nullptr;
-            if (!to) continue;
-            float x[VEC], y[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              const float p = v[k].get(j), q = w[k].get(j), co = cs.get(j), si = sn.get(j);
-              x[j] = __fmaf_rn(p, co, -__fmul_rn(q, si));
-              y[j] = __fmaf_rn(q, co, __fmul_rn(p, si));
-            }
-            store<VEC>(to, chunk * VEC, x);
-            store<VEC>(to, chunk * VEC + a.half, y);
+          for (int j = 0; j < VEC; ++j) {
+            const float p = v.get(j), q = w.get(j), co = cs.get(j), si = sn.get(j);
+            x[j] = __fmaf_rn(p, co, -__fmul_rn(q, si));
+            y[j] = __fmaf_rn(q, co, __fmul_rn(p, si));
           }
+          store<VEC>(to, chunk * VEC, x);
+          store<VEC>(to, chunk * VEC + a.half, y);
         }
       }
-      for (int at0 = t; at0 < items; at0 += kCopy * threads) {
-        if (at0 != t) load_items(at0);
+      for (int at = t; at < items; at += threads) {
+        if (at != t) load_item(at);
+        int head, i;
+        item(at, head, i);
+        uint16_t* to = place(head);
+        if (!to) continue;
+        float x[VEC];
 #pragma unroll
-        for (int k = 0; k < kCopy; ++k)
-          if (at0 + k * threads < items) {
-            int head, i;
-            item(at0 + k * threads, head, i);
-            uint16_t* to = place(head);
-            if (!to) continue;
-            float x[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) x[j] = c[k].get(j);
-            store<VEC>(to, i, x);
-          }
+        for (int j = 0; j < VEC; ++j) x[j] = c.get(j);
+        store<VEC>(to, i, x);
       }
     }
   }
@@ -157,8 +144,11 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Args a) {
 
 template <bool XB, int VEC>
 cudaError_t launch_as(const Args& a, cudaStream_t s) {
-  // few tokens: as many threads as a CTA has for each
-  const unsigned per = a.M > 4 * sm_count() ? 64 : kThreads, tokens = kThreads / per;
+  // Few tokens: as many threads as a CTA has for each, so that a thread makes one trip; many: 64, whose angles serve several
+  // heads, in small CTAs, whose last ones end together.  256 / 64 threads in us, 56 heads: bf16 400 tokens 3.4 / 4.8, 1200
+  // 8.7 / 8.7, 2000 14.4 / 12.4, 4000 25.8 / 22.2; fp32 1200 11.0 / 11.8, 2000 16.7 / 15.7, 4000 30.2 / 28.7.
+  const bool many = a.M > 8 * sm_count();
+  const unsigned per = many ? 64 : kThreads, tokens = many ? 2 : 1;
   return launch(rope_append_kernel<XB, VEC>, dim3(unsigned((a.M + tokens - 1) / tokens)), dim3(per, tokens), 0, s, overlap_enabled(), a);
 }
 
