@@ -2,7 +2,7 @@
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j - max),
 // j over the tokens of the request's pages that the new token sees.
 //
-// A unit is a request's key-value head with up to 16 MT rows, a row being one
+// A unit is a request's key-value head with up to 16 rows, a row being one
 // (new token, query head of the group).  A unit's visible cache is cut into tiles
 // of TT tokens, and all tiles of all units, one after the other, are dealt out in
 // equal contiguous stretches to the warps of the grid, whatever the lengths are:
@@ -17,7 +17,10 @@
 // The products run on mma.sync m16n8k16 (bf16, fp32 sums): up to 16 rows of queries
 // against the tile.  They are bound by the cache's bytes: at the measured copy rate an
 // SM receives 12 values of k and v per clock, 190 multiply-adds with 16 rows, of the
-// 1017 that mma.sync does (tcgen05's tiles of 64 to 128 rows would be 4/5 empty).
+// 1017 that mma.sync does.  What bounds the kernel is the issue of the copies (16 bytes
+// a lane, some 55 clocks for 32 lanes) and of the weights, and, in short calls, the 6 us
+// before the first tile arrives: 64 requests of up to 8192 tokens (40 heads of queries,
+// 8 of keys, D 128) 198 us, 5.5 TB/s; 256 of up to 600 77 us; one of 4096 15 us.
 // The tensor core cuts its sums off instead of rounding them, so a tile's weighted
 // sum starts from zero and is added to the running one in fp32.  The weights go in
 // as two bf16 terms (16 bits) for bf16 results, three (24 bits) for fp32 ones.
@@ -41,12 +44,12 @@ struct Part {
   const float* acc;    // [row][D] weighted sums
 };
 
-template <int DP_, int MT_>
+template <int DP_>
 struct Shape {
-  static constexpr int DP = DP_, MT = MT_;
-  static constexpr int ROWS = 16 * MT;
+  static constexpr int DP = DP_;
+  static constexpr int ROWS = 16;
   static constexpr int TT = DP == 64 ? 32 : 16;        // tokens of a tile
-  static constexpr int WARPS = DP == 256 ? 4 : MT == 1 ? 12 : 8;
+  static constexpr int WARPS = DP == 256 ? 4 : 12;
   static constexpr int STAGES = WARPS == 12 ? 2 : 3;
   static constexpr int CHUNKS = DP / 8;                // 16-byte chunks of a row
   static constexpr int TILE = TT * DP * 2;             // bytes of a tile of k
@@ -88,7 +91,7 @@ __device__ __forceinline__ void copies_wait() {
 
 template <class S, bool F32>
 __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args a) {
-  constexpr int TT = S::TT, NT = TT / 8, KS = S::DP / 16, MT = S::MT, TERMS = F32 ? 3 : 2;
+  constexpr int TT = S::TT, NT = TT / 8, KS = S::DP / 16, TERMS = F32 ? 3 : 2;
   constexpr int kThreads = S::WARPS * 32;
   constexpr uint32_t kAll = TT == 32 ? 0xffffffffu : (1u << TT) - 1;
   extern __shared__ __align__(128) uint8_t ring[];
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
   pdl_wait();
 
   // tiles before every share of the requests
-  const int64_t share = (a.R + kThreads - 1) / kThreads;
+  const int64_t share = quotient(a.R + kThreads - 1, kThreads);
   {
     int64_t mine = 0;
     for (int64_t r = tid * share; r < min(a.R, (tid + 1) * share); ++r) {
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
   }
   const int64_t all = before[kThreads];
   // equal stretches for the CTAs, and for the warps of a CTA
-  const int64_t quota = max(int64_t(1), (all + gridDim.x - 1) / gridDim.x);
+  const int64_t quota = max(int64_t(1), quotient(all + gridDim.x - 1, gridDim.x));
   const int64_t end = min(all, (blockIdx.x + 1) * quota);
   const int64_t each = (quota + S::WARPS - 1) / S::WARPS;
   const int64_t t0 = blockIdx.x * quota + warp * each;
@@ -212,9 +215,9 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
     for (int i = 0; i + 1 < S::STAGES; ++i) fetch_next();
 
     const int g = lane / 4, c2 = lane % 4 * 2;  // this lane's row (and row + 8) and columns of an accumulator
-    uint32_t qf[MT][KS][4];
-    float acc[MT][2 * KS][4], top[MT][2], sum[MT][2];
-    int mine_at[MT][2];  // a row's position
+    uint32_t qf[KS][4];
+    float acc[2 * KS][4], top[2], sum[2];
+    int mine_at[2];  // a row's position
     int head = 0, row0 = 0, nrows = 0;
     bool begun = false, fresh = true;
 
@@ -227,26 +230,23 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
         row0 = at.row0();
         nrows = min(S::ROWS, int(min(int64_t(at.q.n) * a.G - row0, int64_t(S::ROWS))));
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int s = 0; s < 2; ++s) {
+          const int row = g + s * 8;
+          const uint16_t* q = a.q + row_at(a, {at.q.first, head, row0, nrows}, row);
+          mine_at[s] = at.q.length - at.q.n + a.by_group.quotient(row0 + row);
+          top[s] = -INFINITY;
+          sum[s] = 0.f;
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const int row = mt * 16 + g + s * 8;
-            const uint16_t* q = a.q + row_at(a, {at.q.first, head, row0, nrows}, row);
-            mine_at[mt][s] = at.q.length - at.q.n + a.by_group.quotient(row0 + row);
-            top[mt][s] = -INFINITY;
-            sum[mt][s] = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              const int d = ks * 16 + c2;
-              qf[mt][ks][s] = row < nrows && d < a.D && !a.zero ? *reinterpret_cast<const uint32_t*>(q + d) ^ a.sign : 0;
-              qf[mt][ks][s + 2] = row < nrows && d + 8 < a.D && !a.zero ? *reinterpret_cast<const uint32_t*>(q + d + 8) ^ a.sign : 0;
-            }
+          for (int ks = 0; ks < KS; ++ks) {
+            const int d = ks * 16 + c2;
+            qf[ks][s] = row < nrows && d < a.D && !a.zero ? *reinterpret_cast<const uint32_t*>(q + d) ^ a.sign : 0;
+            qf[ks][s + 2] = row < nrows && d + 8 < a.D && !a.zero ? *reinterpret_cast<const uint32_t*>(q + d + 8) ^ a.sign : 0;
           }
-#pragma unroll
-          for (int nt = 0; nt < 2 * KS; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
         }
+#pragma unroll
+        for (int nt = 0; nt < 2 * KS; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
       }
       fetch_next();
       copies_wait<S::STAGES - 1>();
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
       const int j0 = at.token();
 
       // scores
-      float z[MT][NT][4];
+      float z[NT][4];
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -264,15 +264,12 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
           const int row = p * 16 + (lane / 16) * 8 + (lane & 7), chunk = ks * 2 + (lane / 8 & 1);
           uint32_t b[4];
           ldmatrix4(b, k + row * (S::DP * 2) + ((chunk ^ (row & 7)) * 16));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if (ks == 0) {
-              mma_first(z[mt][2 * p], qf[mt][ks], b[0], b[1]);
-              mma_first(z[mt][2 * p + 1], qf[mt][ks], b[2], b[3]);
-            } else {
-              mma(z[mt][2 * p], qf[mt][ks], b[0], b[1]);
-              mma(z[mt][2 * p + 1], qf[mt][ks], b[2], b[3]);
-            }
+          if (ks == 0) {
+            mma_first(z[2 * p], qf[ks], b[0], b[1]);
+            mma_first(z[2 * p + 1], qf[ks], b[2], b[3]);
+          } else {
+            mma(z[2 * p], qf[ks], b[0], b[1]);
+            mma(z[2 * p + 1], qf[ks], b[2], b[3]);
           }
         }
       // Every row sees the whole tile, unless it reaches past the first new token, lies at the window's edge or has
@@ -285,38 +282,34 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
       };
       if (!whole) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!sees(mine_at[mt][e / 2], j0 + nt * 8 + c2 + (e & 1))) z[mt][nt][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e)
+            if (!sees(mine_at[e / 2], j0 + nt * 8 + c2 + (e & 1))) z[nt][e] = -INFINITY;
       }
       // weights
-      float keep[MT][2];  // what the sums so far are multiplied by
+      float keep[2];  // what the sums so far are multiplied by
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int s = 0; s < 2; ++s) {
+        float m = top[s];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          float m = top[mt][s];
+        for (int nt = 0; nt < NT; ++nt) m = fmaxf(m, fmaxf(z[nt][2 * s], z[nt][2 * s + 1]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: all weights are 0
+        const float shift = base * a.scale;
+        keep[s] = exp2_fast((top[s] - base) * a.scale);
+        top[s] = m;
+        float add = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) m = fmaxf(m, fmaxf(z[mt][nt][2 * s], z[mt][nt][2 * s + 1]));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: all weights are 0
-          const float shift = base * a.scale;
-          keep[mt][s] = exp2_fast((top[mt][s] - base) * a.scale);
-          top[mt][s] = m;
-          float add = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 2 * s; e < 2 * s + 2; ++e) {
-              z[mt][nt][e] = exp2_fast(__fmaf_rn(z[mt][nt][e], a.scale, -shift));
-              add += z[mt][nt][e];
-            }
-          sum[mt][s] = __fmaf_rn(sum[mt][s], keep[mt][s], add);
-        }
+          for (int e = 2 * s; e < 2 * s + 2; ++e) {
+            z[nt][e] = exp2_fast(__fmaf_rn(z[nt][e], a.scale, -shift));
+            add += z[nt][e];
+          }
+        sum[s] = __fmaf_rn(sum[s], keep[s], add);
+      }
       // A value that some rows do not see must not reach them, and 0 times an infinity or NaN would: such tiles
       // are looked through, and added up value by value where there is one.
       bool apart = false;
@@ -333,22 +326,20 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
         apart = __any_sync(0xffffffffu, odd != 0);
       }
       if (!apart) {
-        uint32_t w[MT][TT / 16][TERMS][4];
+        uint32_t w[TT / 16][TERMS][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int p = 0; p < TT / 16; ++p)
 #pragma unroll
-          for (int p = 0; p < TT / 16; ++p)
+          for (int e = 0; e < 4; ++e) {
+            float lo = z[2 * p + e / 2][2 * (e & 1)], hi = z[2 * p + e / 2][2 * (e & 1) + 1];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float lo = z[mt][2 * p + e / 2][2 * (e & 1)], hi = z[mt][2 * p + e / 2][2 * (e & 1) + 1];
-#pragma unroll
-              for (int t = 0; t < TERMS; ++t) {
-                const uint32_t u = bf16x2_rn(lo, hi);
-                w[mt][p][t][e] = u;
-                lo -= __uint_as_float(u << 16);
-                hi -= __uint_as_float(u & 0xffff0000u);
-              }
+            for (int t = 0; t < TERMS; ++t) {
+              const uint32_t u = bf16x2_rn(lo, hi);
+              w[p][t][e] = u;
+              lo -= __uint_as_float(u << 16);
+              hi -= __uint_as_float(u & 0xffff0000u);
             }
+          }
 #pragma unroll
         for (int np = 0; np < KS; ++np) {
           uint32_t b[TT / 16][4];
@@ -357,64 +348,58 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
             const int row = p * 16 + (lane & 15), chunk = np * 2 + lane / 16;
             ldmatrix4_trans(b[p], v + row * (S::DP * 2) + ((chunk ^ (row & 7)) * 16));
           }
+          float o0[4], o1[4];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float o0[4], o1[4];
+          for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
-            for (int t = TERMS - 1; t >= 0; --t)
-#pragma unroll
-              for (int p = 0; p < TT / 16; ++p) {
-                if (t == TERMS - 1 && p == 0) {
-                  mma_first(o0, w[mt][p][t], b[p][0], b[p][1]);
-                  mma_first(o1, w[mt][p][t], b[p][2], b[p][3]);
-                } else {
-                  mma(o0, w[mt][p][t], b[p][0], b[p][1]);
-                  mma(o1, w[mt][p][t], b[p][2], b[p][3]);
-                }
+            for (int p = 0; p < TT / 16; ++p) {
+              if (t == TERMS - 1 && p == 0) {
+                mma_first(o0, w[p][t], b[p][0], b[p][1]);
+                mma_first(o1, w[p][t], b[p][2], b[p][3]);
+              } else {
+                mma(o0, w[p][t], b[p][0], b[p][1]);
+                mma(o1, w[p][t], b[p][2], b[p][3]);
               }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              acc[mt][2 * np][e] = __fmaf_rn(acc[mt][2 * np][e], keep[mt][e / 2], o0[e]);
-              acc[mt][2 * np + 1][e] = __fmaf_rn(acc[mt][2 * np + 1][e], keep[mt][e / 2], o1[e]);
             }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[2 * np][e] = __fmaf_rn(acc[2 * np][e], keep[e / 2], o0[e]);
+            acc[2 * np + 1][e] = __fmaf_rn(acc[2 * np + 1][e], keep[e / 2], o1[e]);
           }
         }
       } else {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int nt = 0; nt < 2 * KS; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < 2 * KS; ++nt)
+          for (int e = 0; e < 4; ++e) acc[nt][e] *= keep[e / 2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[mt][nt][e] *= keep[mt][e / 2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll 1
-            for (int jj = 0; jj < 8; ++jj) {
-              const int row = nt * 8 + jj, from = g * 4 + jj / 2;
-              float wr[2];
+          for (int jj = 0; jj < 8; ++jj) {
+            const int row = nt * 8 + jj, from = g * 4 + jj / 2;
+            float wr[2];
 #pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                const float even = __shfl_sync(0xffffffffu, z[mt][nt][2 * s], from);
-                const float uneven = __shfl_sync(0xffffffffu, z[mt][nt][2 * s + 1], from);
-                wr[s] = jj & 1 ? uneven : even;
+            for (int s = 0; s < 2; ++s) {
+              const float even = __shfl_sync(0xffffffffu, z[nt][2 * s], from);
+              const float uneven = __shfl_sync(0xffffffffu, z[nt][2 * s + 1], from);
+              wr[s] = jj & 1 ? uneven : even;
+            }
+            const bool see0 = sees(mine_at[0], j0 + row), see1 = sees(mine_at[1], j0 + row);
+#pragma unroll
+            for (int n = 0; n < 2 * KS; ++n) {
+              uint32_t u;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(v + row * (S::DP * 2) + ((n ^ (row & 7)) * 16) + c2 * 2) : "memory");
+              const float v0 = __uint_as_float(u << 16), v1 = __uint_as_float(u & 0xffff0000u);
+              if (see0) {
+                acc[n][0] = __fmaf_rn(wr[0], v0, acc[n][0]);
+                acc[n][1] = __fmaf_rn(wr[0], v1, acc[n][1]);
               }
-              const bool see0 = sees(mine_at[mt][0], j0 + row), see1 = sees(mine_at[mt][1], j0 + row);
-#pragma unroll
-              for (int n = 0; n < 2 * KS; ++n) {
-                uint32_t u;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(v + row * (S::DP * 2) + ((n ^ (row & 7)) * 16) + c2 * 2) : "memory");
-                const float v0 = __uint_as_float(u << 16), v1 = __uint_as_float(u & 0xffff0000u);
-                if (see0) {
-                  acc[mt][n][0] = __fmaf_rn(wr[0], v0, acc[mt][n][0]);
-                  acc[mt][n][1] = __fmaf_rn(wr[0], v1, acc[mt][n][1]);
-                }
-                if (see1) {
-                  acc[mt][n][2] = __fmaf_rn(wr[1], v0, acc[mt][n][2]);
-                  acc[mt][n][3] = __fmaf_rn(wr[1], v1, acc[mt][n][3]);
-                }
+              if (see1) {
+                acc[n][2] = __fmaf_rn(wr[1], v0, acc[n][2]);
+                acc[n][3] = __fmaf_rn(wr[1], v1, acc[n][3]);
               }
             }
-        }
+          }
       }
       __syncwarp();  // the stage has been read
 
@@ -431,35 +416,33 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
         float2* stat = final ? reinterpret_cast<float2*>(mine) : a.stat + slot * a.rows;
         float* sums = final ? reinterpret_cast<float*>(mine + S::ROWS * sizeof(float2)) : a.acc + slot * a.rows * a.D;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int s = 0; s < 2; ++s) {
+          float l = sum[s];
+          l += __shfl_xor_sync(0xffffffffu, l, 1);
+          l += __shfl_xor_sync(0xffffffffu, l, 2);
+          const int row = g + s * 8;
+          if (row >= nrows) continue;
+          if (out) {
+            const int64_t to = row_at(a, {at.q.first, head, row0, nrows}, row);
+            const float inv = top[s] == -INFINITY && l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            float l = sum[mt][s];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            const int row = mt * 16 + g + s * 8;
-            if (row >= nrows) continue;
-            if (out) {
-              const int64_t to = row_at(a, {at.q.first, head, row0, nrows}, row);
-              const float inv = top[mt][s] == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+            for (int n = 0; n < 2 * KS; ++n)
+              if (n * 8 < a.D) {
+                const float x = acc[n][2 * s] * inv, y = acc[n][2 * s + 1] * inv;
+                if (F32)
+                  *reinterpret_cast<float2*>(static_cast<float*>(a.out) + to + n * 8 + c2) = make_float2(x, y);
+                else
+                  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to + n * 8 + c2) = bf16x2_rn(x, y);
+              }
+          } else {
+            if (lane % 4 == 0) stat[row] = make_float2(top[s], l);
+            float* to = sums + row * a.D;
 #pragma unroll
-              for (int n = 0; n < 2 * KS; ++n)
-                if (n * 8 < a.D) {
-                  const float x = acc[mt][n][2 * s] * inv, y = acc[mt][n][2 * s + 1] * inv;
-                  if (F32)
-                    *reinterpret_cast<float2*>(static_cast<float*>(a.out) + to + n * 8 + c2) = make_float2(x, y);
-                  else
-                    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to + n * 8 + c2) = bf16x2_rn(x, y);
-                }
-            } else {
-              if (lane % 4 == 0) stat[row] = make_float2(top[mt][s], l);
-              float* to = sums + row * a.D;
-#pragma unroll
-              for (int n = 0; n < 2 * KS; ++n)
-                if (n * 8 < a.D)
-                  *reinterpret_cast<float2*>(to + n * 8 + c2) = make_float2(acc[mt][n][2 * s], acc[mt][n][2 * s + 1]);
-            }
+            for (int n = 0; n < 2 * KS; ++n)
+              if (n * 8 < a.D)
+                *reinterpret_cast<float2*>(to + n * 8 + c2) = make_float2(acc[n][2 * s], acc[n][2 * s + 1]);
           }
+        }
         if (!out && lane == 0)
           parts[warp][begun] = {true, ends, {at.q.first, head, row0, nrows}, t0 + i + (at.q.tiles - 1 - at.tile), stat, sums};
         fresh = true;
@@ -468,31 +451,35 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
     }
   }
   // The units that are cut: each begins with a part that goes on (or, the first, with what an earlier CTA began) and
-  // runs through the next warps' parts.  A warp joins every eighth row of all of them.
+  // runs through the next warps' parts.  A warp joins every WARPS-th row of all of them.
   const bool any_bad = __syncthreads_or(bad);
   if (any_bad && tid == 0) atomicOr(a.err, BL_DEVERR_RANGE);
+  const Part& of_lane = parts[min(lane, S::WARPS - 1)][0];
+  const bool mine = lane < S::WARPS;
+  const unsigned goes_on = __ballot_sync(0xffffffffu, mine && of_lane.present && !of_lane.ends);  // through the whole stretch
+  const unsigned ended = __ballot_sync(0xffffffffu, mine && of_lane.present && of_lane.ends);
+  const unsigned begins = __ballot_sync(0xffffffffu, mine && parts[min(lane, S::WARPS - 1)][1].present);
   if (tid == 0) {
     Header header = {};
-    for (int w = 0; w < S::WARPS; ++w)
-      if (parts[w][1].present && parts[w][1].last >= end) {
-        header.unit = parts[w][1].unit;
-        header.present = 1;
-        header.follow = int(parts[w][1].last / quota - blockIdx.x);
-      }
+    const Part& last = parts[31 - __clz(begins | 1)][1];  // the unit that goes on behind the CTA, if one does
+    if (begins && last.last >= end) {
+      header.unit = last.unit;
+      header.present = 1;
+      header.follow = int(quotient(last.last, quota) - blockIdx.x);
+    }
     a.header[blockIdx.x] = header;
   }
   int task = warp;
-  for (int w0 = -1; w0 < S::WARPS; ++w0) {
-    // w0 = -1: the unit that was begun before this CTA
+  // a bit per unit: 0 for one that was begun before this CTA, w + 1 for one that begins in warp w's stretch
+  for (unsigned todo = begins << 1 | ((goes_on | ended) & 1); todo; todo &= todo - 1) {
+    const int w0 = __ffs(todo) - 2, from = max(w0, 0);
     const Part& first = w0 < 0 ? parts[0][0] : parts[w0][1];
-    if (!first.present) continue;
     int n = 1;
-    if (!first.ends)
-      for (int w = max(w0, 0) + 1; w < S::WARPS && parts[w][0].present; ++w) {
-        ++n;
-        if (parts[w][0].ends) break;
-      }
-    const int from = max(w0, 0);
+    if (w0 >= 0 || !(ended & 1)) {  // the next warps' parts, up to one that ends
+      const unsigned rest = ~goes_on >> (from + 1);  // its lowest bit: the first that does not go on
+      const int through = __ffs(rest) - 1;
+      n += through + (ended >> (from + 1 + through) & 1);
+    }
     auto part = [&](int p) -> const Part& { return p == 0 ? first : parts[from + p][0]; };
     for (; task < first.unit.n; task += S::WARPS) {
       const int row = task;
@@ -554,17 +541,22 @@ cudaError_t launch_as(const Args& given, cudaStream_t s) {
 
 template <bool F32>
 cudaError_t launch_for(const Args& a, cudaStream_t s) {
-  // Two blocks of 16 rows share a tile where the requests have, on the average, more than 16 rows.
-  const bool two = (a.M + a.R - 1) / a.R * a.G > 16;
-  if (two && a.D <= 128) {
+  // Tiles of 128 tokens by TMA on tcgen05, or of 16 (32) by each warp on mma.sync.  The former need little per token and
+  // much per unit, and are half empty at D 64, so they take D 104 to 128 where the tables leave room for long requests (the
+  // lengths are known on the device only).  Measured, mma.sync / tcgen05, in us, D 128 unless stated (requests x tokens,
+  // query / key heads): 64 x up to 8192, 40/8: 198/181, pages of 64 199/175; 1 x 131072 119/113; 48 x 5 new tokens, window
+  // 4096, fp32: 230/178; 64 x 4000, 3 new: 89/83; 1 x 4096: 15.5/13.9; 4 x 30000, 8/8: 61.5/60.6; on the other side
+  // 256 x 600, 20/5: 76/96; 256 x 100: 29/43; 64 x 2000: 51/56; 16 x 1000: 17/20; 64 x 1000, 8 new: 107/110; D 64, 64 x 4000:
+  // 58/112; D 80, 4 x 30000: 87/93.  With a table of 4096 tokens and short requests in it the rule so loses a quarter.
+  if (a.D > 96 && a.D <= 128 && a.W * a.page >= 4096) {
     const int grid = std::min(sm_count(), kMostCtas);
     const cudaError_t e = launch_tc(a, grid, F32, s);
     if (e == cudaSuccess) return launch(attn_join_kernel<F32>, dim3(grid, 8), dim3(128), 0, s, true, a);
-    if (e != cudaErrorNotSupported) return e;
+    if (e != cudaErrorNotSupported) return e;  // else: pages that it has no boxes for
   }
-  if (a.D <= 64) return launch_as<Shape<64, 1>, F32>(a, s);
-  if (a.D <= 128) return launch_as<Shape<128, 1>, F32>(a, s);
-  return launch_as<Shape<256, 1>, F32>(a, s);
+  if (a.D <= 64) return launch_as<Shape<64>, F32>(a, s);
+  if (a.D <= 128) return launch_as<Shape<128>, F32>(a, s);
+  return launch_as<Shape<256>, F32>(a, s);
 }
 
 }  // namespace

@@ -23,6 +23,11 @@ struct Divisor {
   }
   __device__ __forceinline__ int quotient(int n) const { return int(__umulhi(2 * uint32_t(n), mul) >> shift); }
 };
+// a / b for a >= 0, b > 0: 64-bit divisions take some 400 clocks, and small numbers do not need them.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if ((a | b) >> 31 == 0) return uint32_t(a) / uint32_t(b);
+  return a / b;
+}
 // What a CTA leaves of the unit that goes on in the next CTA's stretch.
 struct __align__(16) Header {
   Unit unit;
@@ -181,8 +186,8 @@ struct Place {
       if (rest < all) break;
       rest -= all;
     }
-    unit = int(rest / q.tiles);
-    tile = int(rest % q.tiles);
+    unit = int(quotient(rest, q.tiles));
+    tile = int(rest - int64_t(unit) * q.tiles);
   }
   // To the next tile; there must be one.
   __device__ __forceinline__ void next(const Args& a) {

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
   pdl_wait();
 
   // tiles before every share of the requests
-  const int64_t share = (a.R + kThreads - 1) / kThreads;
+  const int64_t share = quotient(a.R + kThreads - 1, kThreads);
   {
     int64_t mine = 0;
     for (int64_t r = tid * share; r < min(a.R, (tid + 1) * share); ++r) {
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
   }
   const uint32_t tmem = c.tmem;
   const int64_t all = c.before[kThreads];
-  const int64_t quota = max(int64_t(1), (all + gridDim.x - 1) / gridDim.x);
+  const int64_t quota = max(int64_t(1), quotient(all + gridDim.x - 1, gridDim.x));
   const int64_t t0 = blockIdx.x * quota;
   const int count = int(max(int64_t(0), min(quota, all - t0)));
 
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
         }
         if (t == 0 && i + 1 == count) {
           Header header = {};
-          if (was.begun && !was.ends) header = Header{was.unit, 1, int((t0 + i + was.left) / quota - blockIdx.x), {0, 0}};
+          if (was.begun && !was.ends) header = Header{was.unit, 1, int(quotient(t0 + i + was.left, quota) - blockIdx.x), {0, 0}};
           a.header[blockIdx.x] = header;
         }
       }
