@@ -11,6 +11,7 @@ import os
 
 import torch
 
+_Tensor = torch.Tensor
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbl.so")
 
@@ -107,11 +108,11 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:  # the handle without a Stream object around it
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if dev is None else dev)
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -367,6 +368,8 @@ def bl_gemm_tq2_0_int8(q, s, packed, N, y=None, stream=None):
 
 def _like(t, name, dtype, shape, device):
     """A tensor given for an argument: exactly this dtype and shape, contiguous, on CUDA device `device`."""
+    if type(t) is _Tensor and t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype is not dtype:
@@ -458,8 +461,15 @@ def bl_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
 
 # ---- a decode step over a paged key-value cache --------------------------------
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _here(t, name, dims):
     """A contiguous CUDA tensor of so many dimensions on the current device; its device's number."""
+    if type(t) is _Tensor and t.is_cuda and t.is_contiguous() and t.dim() == dims:
+        dev = t.get_device()
+        if dev == _current_device():  # a CUDA tensor exists, so the runtime is up
+            return dev
     if _cuda(t, name).dim() != dims:
         raise ValueError("%s must have %d dimensions" % (name, dims))
     dev = t.get_device()
@@ -484,19 +494,23 @@ def bl_page_map(length, count, table, owned, free, free_count, page, tokens, sta
     R, W = table.shape
     i32 = torch.int32
     _like(table, "table", i32, (R, W), dev)
-    for t, n in ((length, "length"), (count, "count"), (owned, "owned")):
-        _like(t, n, i32, (R,), dev)
+    of_requests = (R,)
+    _like(length, "length", i32, of_requests, dev)
+    _like(count, "count", i32, of_requests, dev)
+    _like(owned, "owned", i32, of_requests, dev)
     _here(free, "free", 1)
     _like(free, "free", i32, free.shape, dev)
     _like(free_count, "free_count", i32, (1,), dev)
     M = int(tokens)
-    start, position, slot = (_out(t, n, i32, shape, dev) for t, n, shape in (
-        (start, "start", (R + 1,)), (position, "position", (M,)), (slot, "slot", (M,))))
-    length_out, owned_out, free_left = (_out(t, n, i32, shape, dev) for t, n, shape in (
-        (length_out, "length_out", (R,)), (owned_out, "owned_out", (R,)), (free_left, "free_left", (1,))))
-    _check(_lib.bl_page_map(_ptr(length), _ptr(count), _ptr(table), _ptr(owned), _ptr(free), _ptr(free_count), R, W,
-                            free.numel(), int(page), M, _ptr(start), _ptr(position), _ptr(slot), _ptr(length_out),
-                            _ptr(owned_out), _ptr(free_left), _stream(stream)))
+    start = _out(start, "start", i32, (R + 1,), dev)
+    position = _out(position, "position", i32, (M,), dev)
+    slot = _out(slot, "slot", i32, (M,), dev)
+    length_out = _out(length_out, "length_out", i32, of_requests, dev)
+    owned_out = _out(owned_out, "owned_out", i32, of_requests, dev)
+    free_left = _out(free_left, "free_left", i32, (1,), dev)
+    _check(_lib.bl_page_map(length.data_ptr(), count.data_ptr(), table.data_ptr(), owned.data_ptr(), free.data_ptr(), free_count.data_ptr(), R, W,
+                            free.numel(), int(page), M, start.data_ptr(), position.data_ptr(), slot.data_ptr(), length_out.data_ptr(),
+                            owned_out.data_ptr(), free_left.data_ptr(), _stream(stream, dev)))
     return start, position, slot, length_out, owned_out, free_left
 
 
@@ -524,8 +538,8 @@ def bl_rope_append(qkv, cos, sin, position, slot, k_cache, v_cache, heads, q=Non
     _like(position, "position", torch.int32, (M,), dev)
     _like(slot, "slot", torch.int32, (M,), dev)
     q = _out(q, "q", torch.bfloat16, (M, H, D), dev)
-    _check(_lib.bl_rope_append(_ptr(qkv), xt, _ptr(cos), _ptr(sin), _ptr(position), _ptr(slot), M, H, Hk, D, 2 * half,
-                               positions, _ptr(q), _ptr(k_cache), _ptr(v_cache), pages, page, _stream(stream)))
+    _check(_lib.bl_rope_append(qkv.data_ptr(), xt, cos.data_ptr(), sin.data_ptr(), position.data_ptr(), slot.data_ptr(), M, H, Hk, D, 2 * half,
+                               positions, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pages, page, _stream(stream, dev)))
     return q
 
 
@@ -556,9 +570,9 @@ def bl_attn_paged(q, k_cache, v_cache, table, length, start, scale, window=0, si
         workspace = attn_paged_workspace(M, H, Hk, D, q.device)
     else:
         _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    _check(_lib.bl_attn_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(length), _ptr(start), float(scale),
-                              int(window), int(sinks), M, R, H, Hk, D, pages, page, W, _ptr(out), ot, _ptr(workspace),
-                              workspace.numel(), _stream(stream)))
+    _check(_lib.bl_attn_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), length.data_ptr(), start.data_ptr(), float(scale),
+                              int(window), int(sinks), M, R, H, Hk, D, pages, page, W, out.data_ptr(), ot, workspace.data_ptr(),
+                              workspace.numel(), _stream(stream, dev)))
     return out
 
 
@@ -594,7 +608,7 @@ def bl_verify(logits, token, start, u, u_sample, draft_logits=None, temperature=
         workspace = verify_workspace(M, logits.device)
     else:
         _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    _check(_lib.bl_verify(_ptr(logits), _ptr(draft_logits), lt, _ptr(token), _ptr(start), _ptr(temperature), _ptr(u),
-                          _ptr(u_sample), M, R, V, _ptr(accepted), _ptr(next_token), _ptr(workspace), workspace.numel(),
-                          _stream(stream)))
+    _check(_lib.bl_verify(logits.data_ptr(), _ptr(draft_logits), lt, token.data_ptr(), start.data_ptr(), _ptr(temperature), u.data_ptr(),
+                          u_sample.data_ptr(), M, R, V, accepted.data_ptr(), next_token.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                          _stream(stream, dev)))
     return accepted, next_token
