@@ -24,9 +24,10 @@ struct Divisor {
   __device__ __forceinline__ int quotient(int n) const { return int(__umulhi(2 * uint32_t(n), mul) >> shift); }
 };
 // a / b for a >= 0, b > 0: 64-bit divisions take some 400 clocks, and small numbers do not need them.
+static __device__ __noinline__ int64_t long_quotient(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   if ((a | b) >> 31 == 0) return uint32_t(a) / uint32_t(b);
-  return a / b;
+  return long_quotient(a, b);
 }
 // What a CTA leaves of the unit that goes on in the next CTA's stretch.
 struct __align__(16) Header {
@@ -68,7 +69,7 @@ struct Request {
   bool bad;
 };
 template <class S>
-__device__ __forceinline__ Request request_of(const Args& a, int64_t r) {
+__device__ __noinline__ Request request_of(const Args& a, int64_t r) {
   Request q;
   const Rows rows = rows_of(a.start, r, a.M);
   q.first = rows.first;

@@ -68,6 +68,7 @@ struct __align__(16) Tables {
   uint64_t found[kBack], taken[kBack];  // the pages of a tile
   uint64_t q_full[3];
   uint32_t tmem;
+  unsigned dead;                 // a wait gave up
   Tile tile[kInfo];
   int block[kBack][16];          // the blocks of rows of a tile's pages in the caches
   int row[kBack];                // the first row in them
@@ -104,11 +105,11 @@ __device__ __forceinline__ float fold(float (&v)[16], int lane, Op op) {
 
 __device__ __forceinline__ bool odd_value(uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; }
 
-// The rest of a wait that did not end at once, out of line: the roles' loops have to share the instruction cache.
-// Returns whether this or an earlier wait gave up.
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, bool dead, unsigned int* err) {
-  if (!dead) dead = !mbar_wait_bounded(bar, parity, err);
-  return __any_sync(0xffffffffu, dead);
+// The rest of a wait that did not end at once, out of line: the roles' loops have to share the instruction cache.  One that
+// gave up is not repeated (`dead`): the rest of the work then goes on on whatever is there.
+__device__ __noinline__ void wait_on(uint64_t* bar, uint32_t parity, unsigned* dead) {
+  if (*static_cast<volatile unsigned*>(dead) == 0 && !mbar_wait_bounded(bar, parity, nullptr)) *static_cast<volatile unsigned*>(dead) = 1;
+  __syncwarp();
 }
 
 template <class S>
@@ -130,10 +131,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
   uint8_t* queries = ring + kSlots * kHalf;     // three units' q: [2][NR][64]
   uint8_t* weights = queries + 3 * kQBytes;     // [2][PN][64 tokens]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  bool bad = false, dead = false;
-  // A wait that gave up is not repeated: the rest of the work then goes on on whatever is there.
+  bool bad = false;
   auto wait = [&](uint64_t* bar, int parity) {
-    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, uint32_t(parity & 1)))) dead = wait_on(bar, parity & 1, dead, a.err);
+    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, uint32_t(parity & 1)))) wait_on(bar, parity & 1, &c.dead);
   };
 
   if (warp == 14) {
@@ -141,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
     tmem_relinquish();
   }
   if (tid == 0) {
+    c.dead = 0;
+#pragma unroll 1
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&c.full[i], 1);
       mbar_init(&c.empty[i], 1);
@@ -208,18 +210,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
     };
     const int box_log = 31 - __clz(min(a.page, 128));
     int entry[4], then_entry[4];
-#pragma unroll
-    for (int h = 0; h < 4; ++h) entry[h] = page_of(at, h * 32 + lane);
     Place<S> then = at;  // the tile after this one, whose pages are looked up meanwhile
     bool fresh = true, begun = false;
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      const int buf = i % kBack;
-      if (i + 1 < count) {
-        then.next(a);
+    for (int i = -1; i < count; ++i) {
+      if (i >= 0) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) then_entry[h] = page_of(then, h * 32 + lane);
+        for (int h = 0; h < 4; ++h) entry[h] = then_entry[h];
+        at = then;
+        if (i + 1 < count) then.next(a);
       }
+#pragma unroll
+      for (int h = 0; h < 4; ++h) then_entry[h] = page_of(then, h * 32 + lane);
+      if (i < 0) continue;
+      const int buf = i % kBack;
       if (i >= kBack) wait(&c.taken[buf], i / kBack - 1);
       const int head = at.head(), row0 = at.row0(), j0 = at.token();
       Tile& info = c.tile[i % kInfo];
@@ -255,9 +259,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.found[buf]);
       fresh = at.tile + 1 == at.q.tiles;
-      at = then;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) entry[h] = then_entry[h];
     }
   } else if (count > 0 && (warp == 12 || warp == 13)) {
     // ---- copies of k (and the queries) or v ----
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       if (lane == 0) mbar_arrive_expect_tx(&c.full[slot], kHalf);
       __syncwarp();
       // a lane per box of 64 columns of a page's rows
+#pragma unroll 1
       for (int x = lane; x < 2 * boxes; x += 32)
         tma_load_3d(smem_addr(ring) + slot * kHalf + (x & 1) * (kHalf / 2) + (x >> 1) * rows * 128, map, (x & 1) * 64, c.row[buf], c.block[buf][x >> 1],
                     &c.full[slot]);
@@ -392,33 +394,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
         if (!(fabsf(v) < INFINITY)) {
 #pragma unroll
           for (int r = 0; r < NR; ++r)
-            if (x.seen >> r & 1) acc[r] += v;  // times a weight above 0
+            acc[r] += x.seen >> r & 1 ? v : 0.f;  // times a weight above 0
         }
       }
       if (was.ends || i + 1 == count) {
-        // To the workspace: as a part, or for the rolled loop below, which reads this thread's own sums back.
+        // A lane has a row's sum of weights, and where the row goes: to the result, or to the workspace as a part.
+        static_assert(NR == 32, "a lane per row");
         const bool out = was.begun && was.ends;
-        const int64_t part = out ? 2 * int64_t(gridDim.x) + blockIdx.x : 2 * int64_t(blockIdx.x) + was.begun;
-        float* sums = a.acc + part * a.rows * a.D + t;
-        if (t < a.D) {
-#pragma unroll
-          for (int row = 0; row < NR; ++row)
-            if (row < was.unit.n) sums[row * a.D] = acc[row];
-        }
+        const int64_t part = 2 * int64_t(blockIdx.x) + was.begun;
+        const int n = was.unit.n;
+        const float l = (c.sum[buf][0][lane] + c.sum[buf][1][lane]) + (c.sum[buf][2][lane] + c.sum[buf][3][lane]);
+        const float top = c.final_top[buf][lane];
+        const float inv = !out ? 1.f : top == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+        const int64_t first = out ? row_at(a, was.unit, 0) : part * a.rows * a.D;
+        const int mine = !out ? lane * a.D : lane < n ? int(row_at(a, was.unit, lane) - first) : 0;
+        if (!out && warp == 8 && lane < n) a.stat[part * a.rows + lane] = make_float2(top, l);
+        const int end = t < a.D ? n : 0;
+        auto each_row = [&](auto store) {
 #pragma unroll 1
-        for (int row = 0; row < was.unit.n; ++row) {
-          const float l = (c.sum[buf][0][row] + c.sum[buf][1][row]) + (c.sum[buf][2][row] + c.sum[buf][3][row]);
-          const float top = c.final_top[buf][row];
-          if (!out) {
-            if (t == 0) a.stat[part * a.rows + row] = make_float2(top, l);
-          } else if (t < a.D) {
-            const float v = top == -INFINITY && l == 0.f ? 0.f : sums[row * a.D] * (1.f / l);
-            const int64_t to = row_at(a, was.unit, row) + t;
-            if (F32)
-              static_cast<float*>(a.out)[to] = v;
-            else
-              static_cast<uint16_t*>(a.out)[to] = f32_to_bf16_bits_rn(v);
+          for (int row = 0; row < NR; row += 8) {  // eight at a time, the next ones moved to their place: little code
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const int to = __shfl_sync(0xffffffffu, mine, row + r);
+              const float by = __shfl_sync(0xffffffffu, inv, row + r);
+              store(to, acc[r] * by, row + r < end);
+            }
+#pragma unroll
+            for (int r = 0; r + 8 < NR; ++r) acc[r] = acc[r + 8];
           }
+        };
+        if (F32 || !out) {
+          float* sums = (out ? static_cast<float*>(a.out) : a.acc) + first + t;
+          each_row([&](int to, float v, bool real) {
+            asm volatile("{.reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.f32 [%0], %1;}" ::"l"(sums + to), "f"(v), "r"(unsigned(real)) : "memory");
+          });
+        } else {
+          uint16_t* sums = static_cast<uint16_t*>(a.out) + first + t;
+          each_row([&](int to, float v, bool real) {
+            asm volatile("{.reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.u16 [%0], %1;}" ::"l"(sums + to), "h"(f32_to_bf16_bits_rn(v)), "r"(unsigned(real))
+                         : "memory");
+          });
         }
         if (t == 0 && i + 1 == count) {
           Header header = {};
@@ -552,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
         __syncwarp();
         if (partly && first_row == 0) {  // the other half of the rows leaves it to this thread
           bool odd = false;
-#pragma unroll 4
+#pragma unroll 1
           for (int k = 0; k < 16; ++k) {  // lanes begin at different banks
             const uint32_t v = smem_addr(ring) + slot * kHalf + (k / 8) * (kHalf / 2) + t * 128 + ((k ^ t) % 8) * 16;
             uint32_t u[4];
@@ -590,9 +605,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
   } else if (count == 0 && tid == 0) {
     a.header[blockIdx.x] = Header{};
   }
-  if (count > 0 && warp == 14) mbar_wait_bounded(&c.last, 0, a.err);  // no product is in flight
+  if (count > 0 && warp == 14) mbar_wait_bounded(&c.last, 0, nullptr);  // no product is in flight
   __syncwarp();
   if (__syncthreads_or(bad) && tid == 0) atomicOr(a.err, BL_DEVERR_RANGE);
+  if (c.dead) {  // copies may still be in flight: they have time to land
+    if (tid == 0) atomicOr(a.err, BL_DEVERR_WAIT_TIMEOUT);
+    const unsigned long long from = globaltimer_ns();
+    while (globaltimer_ns() - from < 1000000) __nanosleep(1000);
+    __syncthreads();
+  }
   if (warp == 14) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
@@ -618,7 +639,8 @@ cudaError_t launch_tc(const Args& a, int grid, bool f32, cudaStream_t s) {
   const bool whole = a.page % 128 == 0 || (a.page < 128 && a.page >= 8 && 128 % a.page == 0);
   CUtensorMap k_map, v_map;
   const uint64_t blocks = uint64_t(a.pages) * a.Hk;
-  if (!whole || blocks >= 0x7fffffff || !encode_tmap_blocks_bf16(&k_map, a.k, a.D, a.page, blocks, 64, std::min(a.page, 128)) ||
+  // (a unit's rows are found by 32-bit offsets)
+  if (!whole || blocks >= 0x7fffffff || int64_t(a.H) * a.D > 1 << 25 || !encode_tmap_blocks_bf16(&k_map, a.k, a.D, a.page, blocks, 64, std::min(a.page, 128)) ||
       !encode_tmap_blocks_bf16(&v_map, a.v, a.D, a.page, blocks, 64, std::min(a.page, 128)))
     return cudaErrorNotSupported;
   return f32 ? launch_as<32, true>(a, k_map, v_map, grid, s) : launch_as<32, false>(a, k_map, v_map, grid, s);
