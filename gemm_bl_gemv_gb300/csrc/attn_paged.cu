@@ -541,14 +541,17 @@ cudaError_t launch_as(const Args& given, cudaStream_t s) {
 
 template <bool F32>
 cudaError_t launch_for(const Args& a, cudaStream_t s) {
-  // Tiles of 128 tokens by TMA on tcgen05, or of 16 (32) by each warp on mma.sync.  The former need little per token and
-  // much per unit, and are half empty at D 64, so they take D 104 to 128 where the tables leave room for long requests (the
-  // lengths are known on the device only).  Measured, mma.sync / tcgen05, in us, D 128 unless stated (requests x tokens,
-  // query / key heads): 64 x up to 8192, 40/8: 198/181, pages of 64 199/175; 1 x 131072 119/113; 48 x 5 new tokens, window
-  // 4096, fp32: 230/178; 64 x 4000, 3 new: 89/83; 1 x 4096: 15.5/13.9; 4 x 30000, 8/8: 61.5/60.6; on the other side
-  // 256 x 600, 20/5: 76/96; 256 x 100: 29/43; 64 x 2000: 51/56; 16 x 1000: 17/20; 64 x 1000, 8 new: 107/110; D 64, 64 x 4000:
-  // 58/112; D 80, 4 x 30000: 87/93.  With a table of 4096 tokens and short requests in it the rule so loses a quarter.
-  if (a.D > 96 && a.D <= 128 && a.W * a.page >= 4096) {
+  // Units of 32 rows with tiles of 128 tokens by TMA on tcgen05, or of 16 rows with tiles of 16 (32) by each warp on mma.sync.
+  // The former takes 1.3 us a tile, however many rows there are, with 1 to 4 us for a unit; the latter less for a short unit,
+  // and twice as much for more than 16 rows.  So tcgen05 has requests with ten rows of a key-value head and more, and D 104 to
+  // 128 where the tables have room for long requests (the lengths are known on the device only).  Measured, mma.sync / tcgen05,
+  // us, requests x (evenly spread) lengths up to, query / key heads, D 128 unless stated, pages of 16:
+  //   rows: 256 x 600, 20/5: 2 new tokens (8 rows) 83/92, 3: 100/93, 5: 143/94; 64 x 300, 5 new 40/26; 64 x 1000, 32/8, 8 new
+  //     110/60; 48 x 20000, 40/8, 5 new, window 4096, fp32 232/138; D 80, 64 x 1000, 5 new 58/42; D 64 35/42.
+  //   one token: 64 x 8192, 40/8 198/176, pages of 64 197/172; 3 x 131072 116/111; 1 x 4096 14.5/14.3; 4 x 30000, 8/8 60/60;
+  //     and 64 x 2000 50/53; 16 x 1000 16/21; 256 x 600 75/92; 256 x 100 28/44; D 80, 8 x 30000 86/87; D 64, 64 x 4000 56/102.
+  const bool rows = a.M * a.G >= 10 * a.R, room = a.D > 96 && a.W * a.page >= 4096;
+  if (a.D > 64 && a.D <= 128 && (rows || room)) {
     const int grid = std::min(sm_count(), kMostCtas);
     const cudaError_t e = launch_tc(a, grid, F32, s);
     if (e == cudaSuccess) return launch(attn_join_kernel<F32>, dim3(grid, 8), dim3(128), 0, s, true, a);

@@ -587,9 +587,11 @@ bl_status bl_rope_append(const void* qkv, bl_dtype xt, const float* cos, const f
  *   calls.  Calls that share one must not overlap on the GPU.
  * Products are bf16 with fp32 sums; weights enter the second product in 16
  * bits for bf16 results and 24 for fp32 ones, and the running maximum, sum and
- * weighted sum are fp32.  Which warp takes which tokens depends on the lengths
- * and the device's number of SMs, so sums are the same from call to call but
- * not between batches.
+ * weighted sum are fp32.  Which warp takes which tokens, and by which kernel
+ * (one for requests with ten rows and more or wide tables, D 72 to 128 and
+ * pages of 8, 16, 32, 64 or multiples of 128; one for all others), depends on
+ * the arguments, the lengths and the device's number of SMs, so sums are the
+ * same from call to call but not between batches.
  * Requires M, R, pages, page, W >= 1, H % Hk == 0, M * H < 2^31, D % 8 == 0,
  * 8 <= D <= 256, window, sinks >= 0, pages * page < 2^31; q, caches and out
  * 16-byte aligned, the others 4-byte aligned.
@@ -621,9 +623,10 @@ bl_status bl_attn_paged(const uint16_t* q_bf16, const uint16_t* k_cache, const u
  * is -1, as is that of a request without rows (accepted 0).  A draft outside
  * [0, V) is refused and sets BL_DEVERR_RANGE, as does a start outside 0 .. M
  * or falling.
- * The test of acceptance is made in fp32 (2^-20 of p and q); the sums that the
- * token is found by are sums of integers, with weights within 2^-21 of their
- * value, those above 2^-8 of the largest within 2^-30.
+ * The test of acceptance is made in fp32 (2^-20 of p and q).  The sums that the
+ * token is found by are 64-bit integers: weights above 2^-8 of the largest are
+ * within 2^-30 of their value, lighter ones within 2^-20, either way alike, and
+ * a thread's (a few hundred) are summed in fp32 first.
  *   logits, draft_logits : [M, V] fp32 or bf16 (lt); draft_logits may be NULL
  *   (its last row of a request is not read).  token : int32 [M].  temperature :
  *   fp32 [R] or NULL (1).  u : fp32 [M].  u_sample : fp32 [R].
