@@ -546,7 +546,7 @@ def test_attn_scores_of_minus_infinity(B, wide):
 @gpu
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
-@pytest.mark.parametrize("D,H", [(64, 4), (128, 4), (256, 2), (128, 12)])
+@pytest.mark.parametrize("D,H", [(64, 4), (128, 4), (256, 2), (128, 12), (80, 12)])
 def test_attn_infinities_stay_where_they_are_seen(B, what, D, H, wide):
     """A key or value that is not finite reaches the rows that see it and no others: later drafts, other windows, other
     requests, other heads."""
@@ -621,9 +621,10 @@ def test_attn_offsets_beyond_32_bits(B):
         for i, p in enumerate(place):
             c[p] = dev(s[small.table[0, i]], BF)
     q = bf16_round(rng(4).standard_normal((1, 8, D)).astype(np.float32))
-    out = B.bl_attn_paged(dev(q, BF), k, v, ints([place]), ints([150]), ints([0, 1]), 0.1, out_dtype=F32)
     ref, cond, size = attn_ref(q, small, [1], 0.1, 0, 0)
-    assert np.all(np.abs(host(out) - ref) <= attn_bound(ref, cond, size, 150, D, True))
+    for table in (place, place + [-1] * 61):
+        out = B.bl_attn_paged(dev(q, BF), k, v, ints([table]), ints([150]), ints([0, 1]), 0.1, out_dtype=F32)
+        assert np.all(np.abs(host(out) - ref) <= attn_bound(ref, cond, size, 150, D, True))
     x = rng(5).standard_normal((1, (8 + 2 * Hk) * D)).astype(np.float32)
     one, none = np.ones((1, D // 2), np.float32), np.zeros((1, D // 2), np.float32)
     at = (pages - 1) * page + 5
@@ -808,10 +809,11 @@ def test_verify_distribution(B):
 # ---------------------------------------------------------------------------
 
 @gpu
-def test_calls_on_another_stream_and_captured(B):
+@pytest.mark.parametrize("D,wide", [(64, False), (128, False), (128, True)])
+def test_calls_on_another_stream_and_captured(B, D, wide):
     """The same results on a side stream, and from a graph that is replayed with other contents in its tensors."""
-    H, Hk, D, page = 8, 2, 64, 16
-    cache = Cache([100, 33, 260], Hk, D, page, 14)
+    H, Hk, page = 8, 2, 16
+    cache = Cache([100, 33, 260], Hk, D, page, 14, wide=wide)
     k, v, table, length = cache.gpu()
     q = torch.randn(5, H, D, device="cuda").to(BF)
     start = ints([0, 1, 3, 5])
@@ -909,3 +911,67 @@ def test_steps_of_a_paged_cache_together(B):
         for r in range(requests):
             for lst in rows[r]:
                 del lst[len(lst) - gone[r]:]
+
+
+@gpu
+def test_two_calls_at_once_and_a_cache_that_is_shared(B):
+    """Calls on two streams with a workspace each; requests whose tables hold the same pages (a common prefix)."""
+    H, Hk, D, page = 40, 8, 128, 16
+    cache = Cache([640, 1000, 333], Hk, D, page, 16, wide=True)
+    cache.table[1, :20] = cache.table[0, :20]  # 320 tokens
+    for i in range(2):
+        cache.rows[1][i][:320] = cache.rows[0][i][:320]
+    want = [check_attn(B, cache, counts, H, True) for counts in ([5, 4, 3], [1, 1, 1])]
+    k, v, table, length = cache.gpu()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    work = []
+    for counts, w in zip(([5, 4, 3], [1, 1, 1]), want):
+        q = dev(bf16_round(1.3 * rng(H, D, sum(counts), 0).standard_normal((sum(counts), H, D)).astype(np.float32)), BF)
+        work.append((q, ints(np.concatenate([[0], np.cumsum(counts)])), torch.empty(sum(counts), H, D, device="cuda"),
+                     B.attn_paged_workspace(sum(counts), H, Hk, D)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (q, start, out, ws) in zip(streams, work):
+            B.bl_attn_paged(q, k, v, table, length, start, D ** -0.5, out=out, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for w, (_, _, out, _) in zip(want, work):
+        assert torch.equal(out, w[:len(out)])
+
+
+@gpu
+@pytest.mark.parametrize("requests,drafts", [(1, 3), (5, 0), (7, 4)])
+def test_example_paged_step(B, requests, drafts):
+    """The example runs, eagerly and captured, with the same tokens; lengths and pages add up."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_step.py")
+    spec = importlib.util.spec_from_file_location("paged_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    model = example.Model(5001, heads=4, kv_heads=2, dim=128, positions=512)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    tokens = torch.randint(0, 5001, (requests, 20), generator=g, device="cuda", dtype=I32)
+    numbers = [(torch.rand(requests * (drafts + 1), generator=g, device="cuda"), torch.rand(requests, generator=g, device="cuda")) for _ in range(6)]
+    temperature = torch.full((requests,), 0.8, device="cuda")
+    u, us = (torch.empty_like(t) for t in numbers[0])
+    runs = []
+    for captured in (False, True):
+        req = example.Requests(model, requests, 100)
+        example.prompt(model, req, tokens)
+        u.copy_(numbers[0][0]), us.copy_(numbers[0][1])
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                example.step(model, req, drafts, u, us, temperature)
+        seen = []
+        for n in numbers:
+            u.copy_(n[0]), us.copy_(n[1])
+            graph.replay() if captured else example.step(model, req, drafts, u, us, temperature)
+            seen.append((req.accepted.clone(), req.next.clone()))
+        runs.append(seen)
+        accepted, nxt = (torch.stack(t) for t in zip(*seen))
+        assert bool(((accepted >= 0) & (accepted <= drafts) & (nxt >= 0) & (nxt < 5001)).all())
+        assert torch.equal(req.length, 19 + (accepted + 1).sum(0).to(I32))
+        assert int(req.free_count) + int(req.owned.sum()) == len(req.free)
+        assert bool((req.owned * req.page >= req.length).all())
+    assert all(torch.equal(x, y) for a, b in zip(*runs) for x, y in zip(a, b))
