@@ -15,7 +15,12 @@
 // others: their exponent is formed from an exact offset), in 10 instructions; the few
 // others from sample_weight.cuh (2^-30), in 40.
 //
-// Bound: HBM and exponentials in the first kernel, instruction issue in the second.
+// Bound, 64 requests of one to five rows, bf16 logits of target and draft model over 248320 tokens (157 MB): the first
+// kernel takes 31 us, 5.1 TB/s (HBM 57 % of its time's peak, issue 70 %); the second 42 us, of which two passes over a
+// target's and a draft's row (issue, 12 instructions a pair of logits) are 25, the third of a part and the exchanges the rest;
+// 128 of the 152 SMs have work.  One request with four drafts 15 us, 32 requests with fp32 logits over 100003 tokens 46 us.
+// Masses from the first kernel, which are within 2^-22, would save one pass, and move the borders between tokens by 2^-22
+// over what max(p - q, 0) leaves: more than an unlikely token is wide.
 #include <cfloat>
 
 #include "bl_device.cuh"
@@ -26,7 +31,7 @@
 namespace bl {
 namespace {
 
-constexpr int kMassThreads = 256;
+constexpr int kMassThreads = 128;  // 64 requests: 31 us; with 256 34, with 512 39
 constexpr int kMostStretches = 16;
 constexpr int kThreads = 1024, kWarps = kThreads / 32;  // a lane per warp in the sums over warps
 constexpr int kListed = 32;
@@ -95,6 +100,7 @@ struct Word {
     return __uint_as_float(!XB ? u[e % 4] : e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
   }
   __device__ __forceinline__ f2 pair(int k) const { return pack2(at(2 * k), at(2 * k + 1)); }
+  __device__ __forceinline__ void fill() { u[0] = u[1] = u[2] = u[3] = XB ? 0xff80ff80u : 0xff800000u; }  // -inf
   // e known at run time only
   __device__ __forceinline__ float pick(int e) const {
     float v = at(0);
@@ -103,19 +109,30 @@ struct Word {
     return v;
   }
   // The largest; NaN if there is one.
-  __device__ __forceinline__ float most() const {
-    float r;
+  __device__ __forceinline__ float most() const { return most_of<1>(this); }
+  template <int N>
+  static __device__ __forceinline__ float most_of(const Word* w) {
+    uint32_t m[2 * N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) m[2 * i] = larger(w[i].u[0], w[i].u[1]), m[2 * i + 1] = larger(w[i].u[2], w[i].u[3]);
+#pragma unroll
+    for (int o = N; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < o; ++i) m[i] = larger(m[i], m[i + o]);
+    float r = __uint_as_float(m[0]);
+    if (XB) asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(m[0] << 16)), "f"(__uint_as_float(m[0] & 0xffff0000u)));
+    return r;
+  }
+
+ private:
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t r;
     if (XB) {
-      uint32_t a, b, c;
-      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(u[0]), "r"(u[1]));
-      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(u[2]), "r"(u[3]));
-      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(c << 16)), "f"(__uint_as_float(c & 0xffff0000u)));
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     } else {
-      float a, b;
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(at(0)), "f"(at(1)));
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(at(2)), "f"(at(3)));
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+      float f;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+      r = __float_as_uint(f);
     }
     return r;
   }
@@ -123,8 +140,10 @@ struct Word {
 
 // The elements [from, to) of MATS rows at x[m] + base, shared by n threads (this is the t-th): words(w, i) gets 16 bytes
 // of each row, of its elements i, i + 1, ..., and one(i) the elements at the ends.  The rows' addresses are equal modulo 16
-// (`wide`), or every element comes by itself.  The next words are loaded before the present ones are worked on.
-template <bool XB, int MATS, int kAtOnce, class One, class Words>
+// (`wide`), or every element comes by itself.  Of one row the next words are loaded
+// before the present ones are worked on; of two there are no registers for that, and other warps to wait with.
+// kTogether: words(w, i) gets the thread's next kAtOnce words, n words apart, -inf behind the last.
+template <bool XB, int MATS, int kAtOnce, bool kTogether = false, class One, class Words>
 __device__ __forceinline__ void each(const void* x0, const void* x1, bool wide, int64_t base, int from, int to, int t, int n, One one, Words f) {
   constexpr int E = Word<XB>::E;
   const int off = int((reinterpret_cast<uintptr_t>(x0) / (XB ? 2 : 4) + uint64_t(base) + uint64_t(from)) % E);
@@ -138,19 +157,28 @@ __device__ __forceinline__ void each(const void* x0, const void* x1, bool wide, 
       if (w0 + j * n < words) {
         next[j][0].load(x0, base + body + int64_t(w0 + j * n) * E);
         if (MATS == 2) next[j][MATS - 1].load(x1, base + body + int64_t(w0 + j * n) * E);
+      } else if (kTogether) {
+        next[j][0].fill();
+        if (MATS == 2) next[j][MATS - 1].fill();
       }
   };
-  load(t);
+  constexpr bool kAhead = MATS == 1;
+  if (kAhead) load(t);
   for (int w0 = t; w0 < words; w0 += kAtOnce * n) {
+    if (!kAhead) load(w0);
     Word<XB> now[kAtOnce][MATS];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j)
 #pragma unroll
       for (int m = 0; m < MATS; ++m) now[j][m] = next[j][m];
-    load(w0 + kAtOnce * n);
+    if (kAhead) load(w0 + kAtOnce * n);
+    if constexpr (kTogether) {
+      f(now, body + w0 * E);
+    } else {
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j)
-      if (w0 + j * n < words) f(now[j], body + (w0 + j * n) * E);
+      for (int j = 0; j < kAtOnce; ++j)
+        if (w0 + j * n < words) f(now[j], body + (w0 + j * n) * E);
+    }
   }
 }
 
@@ -206,27 +234,42 @@ __global__ void __launch_bounds__(kMassThreads) verify_mass_kernel(const Args a)
       sum += E > -INFINITY ? exp2_fast(__fmaf_rn(l, rate, -E)) : float(l == top);
     };
     const f2 rate2 = pack2(rate, rate);
-    each<XB, 1, 4>(x, x, true, row * a.V, from, to, threadIdx.x, kMassThreads, [&](int i) { add(logit<XB>(x, row * a.V + i)); },
-                   [&](const Word<XB>(&w)[1], int) {
-                     const float most = w[0].most();
-                     if (most > top) raise(most);
-                     if (most == -INFINITY) return;
-                     if (most == most && !(E > -INFINITY)) {
+    // Four words at a time: their largest and what hangs on it cost more than a word's weights.
+    constexpr int N = 4, kPairs = Word<XB>::E / 2;
+    each<XB, 1, N, true>(x, x, true, row * a.V, from, to, threadIdx.x, kMassThreads, [&](int i) { add(logit<XB>(x, row * a.V + i)); },
+                         [&](const Word<XB>(&w)[N][1], int) {
+                           const float most = Word<XB>::template most_of<N>(&w[0][0]);
+                           if (most > top) raise(most);
+                           if (most == -INFINITY) return;
+                           if (most == most && E > -INFINITY && rate > 0.f) {
+                             const f2 e2 = pack2(-E, -E);
+                             f2 t[N];
 #pragma unroll
-                       for (int e = 0; e < Word<XB>::E; ++e) sum += float(w[0].at(e) == top);
-                     } else if (most == most && E > -INFINITY && rate > 0.f) {
-                       const f2 e2 = pack2(-E, -E);
-                       f2 t = exp2_of(fma2(w[0].pair(0), rate2, e2));
+                             for (int i = 0; i < N; ++i) t[i] = exp2_of(fma2(w[i][0].pair(0), rate2, e2));
 #pragma unroll
-                       for (int k = 1; k < Word<XB>::E / 2; ++k) t = add2(t, exp2_of(fma2(w[0].pair(k), rate2, e2)));
-                       float t0, t1;
-                       unpack2(t, t0, t1);
-                       sum += t0 + t1;
-                     } else {
+                             for (int k = 1; k < kPairs; ++k)
+#pragma unroll
+                               for (int i = 0; i < N; ++i) t[i] = add2(t[i], exp2_of(fma2(w[i][0].pair(k), rate2, e2)));
+                             float t0, t1;
+                             unpack2(add2(add2(t[0], t[1]), add2(t[2], t[3])), t0, t1);
+                             sum += t0 + t1;
+                           } else if (most == most && !(E > -INFINITY)) {
+#pragma unroll
+                             for (int i = 0; i < N; ++i)
+#pragma unroll
+                               for (int e = 0; e < Word<XB>::E; ++e) sum += float(w[i][0].at(e) == top);
+                           } else {
 #pragma unroll 1
-                       for (int e = 0; e < Word<XB>::E; ++e) add(w[0].pick(e));
-                     }
-                   });
+                             for (int i = 0; i < N; ++i)
+#pragma unroll 1
+                               for (int e = 0; e < Word<XB>::E; ++e) {
+                                 float l = w[0][0].pick(e);
+#pragma unroll
+                                 for (int k = 1; k < N; ++k) l = i == k ? w[k][0].pick(e) : l;
+                                 add(l);
+                               }
+                           }
+                         });
     // to the warp's and the CTA's largest: the sums are beside their maximum from here on, as elsewhere
     if (E > -INFINITY) sum *= exp2_fast(-__fmaf_rn(top, rate, -E));
     float most = warp_max(top);
