@@ -18,7 +18,7 @@
 // Bound, 64 requests of one to five rows, bf16 logits of target and draft model over 248320 tokens (157 MB): the first
 // kernel takes 31 us, 5.1 TB/s (HBM 57 % of its time's peak, issue 70 %); the second 42 us, of which two passes over a
 // target's and a draft's row (issue, 12 instructions a pair of logits) are 25, the third of a part and the exchanges the rest;
-// 128 of the 152 SMs have work.  One request with four drafts 15 us, 32 requests with fp32 logits over 100003 tokens 46 us.
+// 128 of the 152 SMs have work.  One request with four drafts 15 us, 32 requests with fp32 logits over 100003 tokens 44 us.
 // Masses from the first kernel, which are within 2^-22, would save one pass, and move the borders between tokens by 2^-22
 // over what max(p - q, 0) leaves: more than an unlikely token is wide.
 #include <cfloat>
@@ -689,8 +689,9 @@ cudaError_t launch_verify(const void* logits, const void* draft_logits, bl_dtype
   if (!err) return cudaErrorUnknown;
   Args a{logits, draft_logits, token, start, temperature, u, u_sample, M, R, V, accepted, next, static_cast<float2*>(ws), 1, 0, err};
   const int mats = draft_logits ? 2 : 1;
-  // Long stretches: a CTA's own 1.5 us are little then; short ones fill the GPU when there are few rows.
-  const int64_t wanted = std::max<int64_t>({V / 32768, 4 * sm_count() / (M * mats), 1});
+  // Long stretches: a CTA's own 1.5 us are little then; short ones fill the GPU when there are few rows.  Of 8192, 16384,
+  // 24576 and 32768 logits: 32 requests of 100003 fp32 logits 20.8, 19.6, 20.8, 22.0 us; 64 of 248320 in bf16 31, 31, 30, 31.
+  const int64_t wanted = std::max<int64_t>({V / 16384, 4 * sm_count() / (M * mats), 1});
   a.stretch = int((V + wanted - 1) / std::min<int64_t>(wanted, kMostStretches) + 4095) / 4096 * 4096;
   a.stretches = int((V + a.stretch - 1) / a.stretch);
   const bool pdl = overlap_enabled();
