@@ -580,7 +580,7 @@ cudaError_t launch_attn_paged(const uint16_t* q, const uint16_t* k_cache, const 
   if (!a.err) return cudaErrorUnknown;
   a.M = M, a.R = R, a.pages = pages, a.W = W;
   a.H = H, a.Hk = Hk, a.G = H / Hk, a.D = D, a.page = page, a.rows = part_rows(M, H, Hk, D);
-  a.window = window, a.sinks = sinks;
+  a.window = std::min(window, int64_t(1) << 31), a.sinks = std::min(sinks, int64_t(1) << 31);  // all tokens: sums of them stay in 64 bits
   // The kernel works with a positive factor, whose largest score is the largest sum: the sign goes to the queries, and
   // with a scale of 0 all of them (times any key) are 0.
   a.scale = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;

@@ -74,7 +74,7 @@ __device__ __noinline__ Request request_of(const Args& a, int64_t r) {
   const Rows rows = rows_of(a.start, r, a.M);
   q.first = rows.first;
   q.n = rows.n;
-  const int64_t most = min(a.W * a.page, int64_t(INT32_MAX));
+  const int64_t most = min(a.W * a.page, int64_t(INT32_MAX - 255));  // so that a tile's tokens have numbers
   const int given = a.length[r];
   q.length = int(max(int64_t(0), min(int64_t(given), most)));
   q.bad = rows.bad || q.length != given;

@@ -105,11 +105,12 @@ __device__ __forceinline__ float fold(float (&v)[16], int lane, Op op) {
 
 __device__ __forceinline__ bool odd_value(uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; }
 
-// The rest of a wait that did not end at once, out of line: the roles' loops have to share the instruction cache.  One that
-// gave up is not repeated (`dead`): the rest of the work then goes on on whatever is there.
-__device__ __noinline__ void wait_on(uint64_t* bar, uint32_t parity, unsigned* dead) {
-  if (*static_cast<volatile unsigned*>(dead) == 0 && !mbar_wait_bounded(bar, parity, nullptr)) *static_cast<volatile unsigned*>(dead) = 1;
-  __syncwarp();
+// The rest of a wait that did not end at once, out of line: the roles' loops have to share the instruction cache.  False: it
+// gave up, or, unless `all`, another one has (`dead`); the role then ends, and touches nothing that it has not waited for.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, unsigned* dead, bool all) {
+  const bool ok = (all || *static_cast<volatile unsigned*>(dead) == 0) && mbar_wait_bounded(bar, parity, nullptr);
+  if (!ok) *static_cast<volatile unsigned*>(dead) = 1;
+  return __all_sync(0xffffffffu, ok);
 }
 
 template <class S>
@@ -132,8 +133,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
   uint8_t* weights = queries + 3 * kQBytes;     // [2][PN][64 tokens]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
-  auto wait = [&](uint64_t* bar, int parity) {
-    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, uint32_t(parity & 1)))) wait_on(bar, parity & 1, &c.dead);
+  auto wait = [&](uint64_t* bar, int parity, bool all = false) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, uint32_t(parity & 1))) || wait_on(bar, parity & 1, &c.dead, all);
   };
 
   if (warp == 14) {
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       for (int h = 0; h < 4; ++h) then_entry[h] = page_of(then, h * 32 + lane);
       if (i < 0) continue;
       const int buf = i % kBack;
-      if (i >= kBack) wait(&c.taken[buf], i / kBack - 1);
+      if (i >= kBack && !wait(&c.taken[buf], i / kBack - 1)) break;
       const int head = at.head(), row0 = at.row0(), j0 = at.token();
       Tile& info = c.tile[i % kInfo];
 #pragma unroll
@@ -269,9 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
       const int buf = i % kBack, seq = 2 * i + half, slot = seq % kSlots;
-      wait(&c.found[buf], i / kBack);
+      if (!wait(&c.found[buf], i / kBack)) break;
       const Tile& now = c.tile[i % kInfo];
-      if (seq >= kSlots) wait(&c.empty[slot], seq / kSlots - 1);
+      if (seq >= kSlots && !wait(&c.empty[slot], seq / kSlots - 1)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(&c.full[slot], kHalf);
       __syncwarp();
@@ -305,12 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
     for (int i = 0; i <= count; ++i) {
       if (i < count) {  // S(i)
         const int slot = 2 * i % kSlots;
-        wait(&c.full[slot], 2 * i / kSlots);
-        if (i >= 2) wait(&c.s_empty[i & 1], i / 2 - 1);
+        if (!wait(&c.full[slot], 2 * i / kSlots)) break;
+        if (i >= 2 && !wait(&c.s_empty[i & 1], i / 2 - 1)) break;
         tc_fence_after();
         if (c.tile[i % kInfo].fresh) {
           ++units;
-          wait(&c.q_full[units % 3], units / 3);
+          if (!wait(&c.q_full[units % 3], units / 3)) break;
           fence_async_smem();  // the queries were copied by the generic proxy
           __syncwarp();
         }
@@ -326,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       }
       if (i > 0) {  // O(i - 1)
         const int j = i - 1, slot = (2 * j + 1) % kSlots;
-        wait(&c.full[slot], (2 * j + 1) / kSlots);
-        if (j >= 2) wait(&c.o_empty[j & 1], j / 2 - 1);
-        wait(&c.p_full, j);
+        if (!wait(&c.full[slot], (2 * j + 1) / kSlots)) break;
+        if (j >= 2 && !wait(&c.o_empty[j & 1], j / 2 - 1)) break;
+        if (!wait(&c.p_full, j)) break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t v = v_at + slot * (kHalf >> 4);
@@ -353,8 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
     for (int i = 0; i < count; ++i) {
       const int buf = i % kBack;
       const Tile& was = c.tile[i % kInfo];
-      wait(&c.info[buf], i / kBack);
-      wait(&c.o_full[i & 1], i / 2);
+      if (!wait(&c.info[buf], i / kBack)) break;
+      if (!wait(&c.o_full[i & 1], i / 2)) break;
       __syncwarp();
       tc_fence_after();
       if (was.fresh) {
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
       const int buf = i % kBack;
-      wait(&c.s_full[i & 1], i / 2);
+      if (!wait(&c.s_full[i & 1], i / 2)) break;
       __syncwarp();
       tc_fence_after();
       uint32_t zu[HR];
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       if (__any_sync(0xffffffffu, far) && lane == 0) c.vote[buf] = 1;
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.voted[i & 1]);
-      wait(&c.voted[i & 1], i / 2);
+      if (!wait(&c.voted[i & 1], i / 2, true)) break;  // all eight warps or none: barriers follow
       const bool rises = c.vote[buf] != 0;
       if (__builtin_expect(rises, 0)) {
         float v[HR];
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       }
       if (!rises && tid < NR) reinterpret_cast<float*>(c.keep[buf])[tid] = 1.f;
       if (tid == 0) c.vote[(i + 2) % kBack] = 0;
-      if (i > 0) wait(&c.p_empty, i - 1);
+      if (i > 0 && !wait(&c.p_empty, i - 1)) break;
       __syncwarp();
       if (tid == 0) c.odd_count[(i + 1) % kBack] = 0;
       // Two lanes exchange rows, so that each stores a pair of tokens; rows r and r + 4 lie in different banks.
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       // out of the tile, and added to the sums of the rows that see them.
       if (__builtin_expect(__any_sync(0xffffffffu, partly), 0)) {
         const int seq = 2 * i + 1, slot = seq % kSlots;
-        wait(&c.full[slot], seq / kSlots);
+        if (!wait(&c.full[slot], seq / kSlots)) break;
         __syncwarp();
         if (partly && first_row == 0) {  // the other half of the rows leaves it to this thread
           bool odd = false;

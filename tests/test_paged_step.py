@@ -482,6 +482,13 @@ def test_attn_window(B, lengths, counts, H, Hk, D, window, sinks, wide):
 
 @gpu
 @pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("window,sinks", [(1 << 31, 0), ((1 << 63) - 1, 0), ((1 << 63) - 1, (1 << 63) - 1), (50, (1 << 63) - 1), (0, (1 << 63) - 1)])
+def test_attn_windows_wider_than_any_request(B, window, sinks, wide):
+    check_attn(B, Cache([300, 17, 129], 2, 128, 16, 17, wide=wide), [5, 1, 3], 10, True, window=window, sinks=sinks)
+
+
+@gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("f32", [False, True])
 def test_attn_many_requests_and_long_ones(B, f32, wide):
     g = rng(11)
