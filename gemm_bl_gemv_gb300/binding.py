@@ -478,9 +478,19 @@ def _here(t, name, dims):
     return dev
 
 
-def _out(t, name, dtype, shape, dev):
+def _new(dtype, shape, dev, stream):
+    """A tensor whose memory is the call's stream's own: what the current stream has freed may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda:%d" % dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device="cuda:%d" % dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda:%d" % dev)
+
+
+def _out(t, name, dtype, shape, dev, stream):
     """The tensor given for an output, or a new one."""
-    return torch.empty(shape, dtype=dtype, device="cuda:%d" % dev) if t is None else _like(t, name, dtype, shape, dev)
+    return _new(dtype, shape, dev, stream) if t is None else _like(t, name, dtype, shape, dev)
 
 
 def bl_page_map(length, count, table, owned, free, free_count, page, tokens, start=None, position=None, slot=None,
@@ -502,12 +512,12 @@ def bl_page_map(length, count, table, owned, free, free_count, page, tokens, sta
     _like(free, "free", i32, free.shape, dev)
     _like(free_count, "free_count", i32, (1,), dev)
     M = int(tokens)
-    start = _out(start, "start", i32, (R + 1,), dev)
-    position = _out(position, "position", i32, (M,), dev)
-    slot = _out(slot, "slot", i32, (M,), dev)
-    length_out = _out(length_out, "length_out", i32, of_requests, dev)
-    owned_out = _out(owned_out, "owned_out", i32, of_requests, dev)
-    free_left = _out(free_left, "free_left", i32, (1,), dev)
+    start = _out(start, "start", i32, (R + 1,), dev, stream)
+    position = _out(position, "position", i32, (M,), dev, stream)
+    slot = _out(slot, "slot", i32, (M,), dev, stream)
+    length_out = _out(length_out, "length_out", i32, of_requests, dev, stream)
+    owned_out = _out(owned_out, "owned_out", i32, of_requests, dev, stream)
+    free_left = _out(free_left, "free_left", i32, (1,), dev, stream)
     _check(_lib.bl_page_map(length.data_ptr(), count.data_ptr(), table.data_ptr(), owned.data_ptr(), free.data_ptr(), free_count.data_ptr(), R, W,
                             free.numel(), int(page), M, start.data_ptr(), position.data_ptr(), slot.data_ptr(), length_out.data_ptr(),
                             owned_out.data_ptr(), free_left.data_ptr(), _stream(stream, dev)))
@@ -537,7 +547,7 @@ def bl_rope_append(qkv, cos, sin, position, slot, k_cache, v_cache, heads, q=Non
     _like(sin, "sin", torch.float32, (positions, half), dev)
     _like(position, "position", torch.int32, (M,), dev)
     _like(slot, "slot", torch.int32, (M,), dev)
-    q = _out(q, "q", torch.bfloat16, (M, H, D), dev)
+    q = _out(q, "q", torch.bfloat16, (M, H, D), dev, stream)
     _check(_lib.bl_rope_append(qkv.data_ptr(), xt, cos.data_ptr(), sin.data_ptr(), position.data_ptr(), slot.data_ptr(), M, H, Hk, D, 2 * half,
                                positions, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pages, page, _stream(stream, dev)))
     return q
@@ -564,10 +574,10 @@ def bl_attn_paged(q, k_cache, v_cache, table, length, start, scale, window=0, si
     _like(table, "table", torch.int32, (R, W), dev)
     _like(length, "length", torch.int32, (R,), dev)
     _like(start, "start", torch.int32, (R + 1,), dev)
-    out = _out(out, "out", out_dtype or (torch.bfloat16 if out is None else out.dtype), (M, H, D), dev)
+    out = _out(out, "out", out_dtype or (torch.bfloat16 if out is None else out.dtype), (M, H, D), dev, stream)
     ot = _dtype_code(out)
     if workspace is None:
-        workspace = attn_paged_workspace(M, H, Hk, D, q.device)
+        workspace = _new(torch.uint8, (int(_lib.bl_attn_paged_workspace(M, H, Hk, D)),), dev, stream)
     else:
         _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
     _check(_lib.bl_attn_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), length.data_ptr(), start.data_ptr(), float(scale),
@@ -602,10 +612,10 @@ def bl_verify(logits, token, start, u, u_sample, draft_logits=None, temperature=
         _like(draft_logits, "draft_logits", logits.dtype, (M, V), dev)
     if temperature is not None:
         _like(temperature, "temperature", torch.float32, (R,), dev)
-    accepted = _out(accepted, "accepted", torch.int32, (max(R, 0),), dev)
-    next_token = _out(next_token, "next_token", torch.int32, (max(R, 0),), dev)
+    accepted = _out(accepted, "accepted", torch.int32, (max(R, 0),), dev, stream)
+    next_token = _out(next_token, "next_token", torch.int32, (max(R, 0),), dev, stream)
     if workspace is None:
-        workspace = verify_workspace(M, logits.device)
+        workspace = _new(torch.uint8, (int(_lib.bl_verify_workspace(M)),), dev, stream)
     else:
         _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
     _check(_lib.bl_verify(logits.data_ptr(), _ptr(draft_logits), lt, token.data_ptr(), start.data_ptr(), _ptr(temperature), u.data_ptr(),

@@ -921,6 +921,30 @@ def test_steps_of_a_paged_cache_together(B):
 
 
 @gpu
+def test_memory_of_calls_on_another_stream(B):
+    """What a call allocates is not handed out again to the current stream while the call waits on its own."""
+    H, Hk, D = 40, 8, 128
+    cache = Cache([900, 1300], Hk, D, 16, 18, wide=True)
+    k, v, table, length = cache.gpu()
+    q, start = torch.randn(9, H, D, device="cuda").to(BF), ints([0, 5, 9])
+    vi = verify_inputs([5, 4], 40000, True, True, 10)
+    vt = [dev(vi[0], BF), ints(vi[2]), start, dev(vi[3]), dev(vi[4])]
+    dl, tt = dev(vi[1], BF), dev(vi[5])
+    side = torch.cuda.Stream()
+    want = (B.bl_attn_paged(q, k, v, table, length, start, D ** -0.5), *B.bl_verify(*vt, draft_logits=dl, temperature=tt))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # 10 ms
+        got = (B.bl_attn_paged(q, k, v, table, length, start, D ** -0.5, stream=side), *B.bl_verify(*vt, draft_logits=dl, temperature=tt, stream=side))
+        sizes = (B.attn_paged_workspace(9, H, Hk, D).numel(), B.verify_workspace(9).numel(), 2 * 9 * H * D, 8)
+        kept = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        assert all(bool((t == 0).all()) for t in kept)
+
+
+@gpu
 def test_two_calls_at_once_and_a_cache_that_is_shared(B):
     """Calls on two streams with a workspace each; requests whose tables hold the same pages (a common prefix)."""
     H, Hk, D, page = 40, 8, 128, 16
