@@ -326,6 +326,13 @@ def test_rope_append(B, M, H, Hk, D, rotary, page, xb):
 
 
 @gpu
+@pytest.mark.parametrize("xb", [True, False])
+@pytest.mark.parametrize("M,D,rotary", [(1301, 1024, 1024), (1217, 1024, 1022), (1250, 136, 136), (2001, 8, 2)])
+def test_rope_append_many_tokens_with_long_and_short_heads(B, M, D, rotary, xb):
+    check_rope(B, rope_inputs(M, 2, 1, D, rotary, 16, xb, 3), 2, 1, 16, xb)
+
+
+@gpu
 def test_rope_append_unaligned_tables(B):
     def off(t):
         buf = torch.empty(t.numel() + 1, device="cuda")
@@ -501,7 +508,7 @@ def test_attn_many_requests_and_long_ones(B, f32, wide):
 
 @gpu
 @pytest.mark.parametrize("wide", [False, True])
-@pytest.mark.parametrize("page,window,sinks", [(32, 0, 0), (16, 1000, 4), (256, 0, 0), (8, 300, 200)])
+@pytest.mark.parametrize("page,window,sinks", [(32, 0, 0), (16, 1000, 4), (256, 0, 0), (8, 300, 200), (64, 0, 0), (128, 100, 0), (384, 700, 1)])
 def test_attn_units_that_follow_each_other(B, page, window, sinks, wide):
     """Many units of many rows and a few tiles each, one after the other in a CTA."""
     lengths = [int(n) for n in rng(page).integers(200, 1500, 20)]
