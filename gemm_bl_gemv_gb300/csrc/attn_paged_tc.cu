@@ -15,6 +15,12 @@
 // Warps: 0-7 weights; 8-11 sums; 12 and 13 start the copies of k and v (TMA boxes of a page's rows, zeros for a page that
 // is not there); 14 products; 15 looks ahead: the pages of the next tiles' tokens.  k and v of a tile share a ring of
 // five half tiles.  A page is 128 tokens or more in steps of 128, or 8, 16, 32 or 64; the other kernel takes others.
+//
+// Bound: HBM where lengths are long (64 requests of up to 8192 tokens, 40 / 8 heads, one new token: 175 us, 6.2 TB/s; 3 of
+// up to 131072 110 us); a tile's weights, 1.3 us, and 1 to 2 us for a unit's begin and end and for each tile that rows see in part
+// (48 requests with 5 new tokens, window 4096, fp32 results: 137 us, 5.4 TB/s).  The roles run side by side, so the code of all
+// has to stay in the instruction cache: 94 KB took 178 us there, 85 KB 138.  Hence the rolled loops and the functions that
+// are not inlined.
 #include "attn_paged.cuh"
 
 namespace bl {
@@ -560,8 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
           hi -= __uint_as_float(u & 0xffff0000u);
         }
       }
-      // A value that some rows do not see (or none: the rest of a page) must not reach them, and 0 times an infinity or NaN would: such values are taken
-      // out of the tile, and added to the sums of the rows that see them.
+      // A value that some rows do not see (or none: the rest of a page) must not reach them, and 0 times an infinity or
+      // NaN would: such values are taken out of the tile, and added to the sums of the rows that see them.
       if (__builtin_expect(__any_sync(0xffffffffu, partly), 0)) {
         const int seq = 2 * i + 1, slot = seq % kSlots;
         if (!wait(&c.full[slot], seq / kSlots)) break;
@@ -641,7 +647,8 @@ cudaError_t launch_tc(const Args& a, int grid, bool f32, cudaStream_t s) {
   CUtensorMap k_map, v_map;
   const uint64_t blocks = uint64_t(a.pages) * a.Hk;
   // (a unit's rows are found by 32-bit offsets)
-  if (!whole || blocks >= 0x7fffffff || int64_t(a.H) * a.D > 1 << 25 || !encode_tmap_blocks_bf16(&k_map, a.k, a.D, a.page, blocks, 64, std::min(a.page, 128)) ||
+  if (!whole || blocks >= 0x7fffffff || int64_t(a.H) * a.D > 1 << 25 ||
+      !encode_tmap_blocks_bf16(&k_map, a.k, a.D, a.page, blocks, 64, std::min(a.page, 128)) ||
       !encode_tmap_blocks_bf16(&v_map, a.v, a.D, a.page, blocks, 64, std::min(a.page, 128)))
     return cudaErrorNotSupported;
   return f32 ? launch_as<32, true>(a, k_map, v_map, grid, s) : launch_as<32, false>(a, k_map, v_map, grid, s);

@@ -575,7 +575,8 @@ bl_status bl_rope_append(const void* qkv, bl_dtype xt, const float* cos, const f
  * the first 2^31 - 256 is left out and sets BL_DEVERR_RANGE (as do a negative
  * length and a start outside 0 .. M or falling).  A row that sees no token, or whose scores are all -inf,
  * gives 0.  Infinities and NaN in tokens that a row does not see, in the rest
- * of a page and in other rows do not reach it.
+ * of a page and in other rows do not reach it; one among the values that it
+ * sees makes its column an infinity or NaN.
  * Any number of new tokens is computed, but the kernel is made for few
  * (a decode step, drafts): every 16 or 32 rows (new tokens times H / Hk) read
  * the request's cache again.
