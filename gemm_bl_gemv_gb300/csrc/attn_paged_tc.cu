@@ -8,9 +8,10 @@
 //   O^T [D x TERMS NR]     = V^T [D x tokens] P^T,         a tile of v as it lies in the cache, M-major
 // A thread then has a token's scores of half of the rows, or a coordinate's sums of all: nothing is exchanged between
 // threads in a tile, unless a row's maximum rises by more than 2^8: weights are beside a maximum that may be that much
-// out of date.  The weights' bf16 terms (two, 16 bits, for bf16 results, three, 24 bits, for fp32 ones) are TERMS rows of
-// P each, so one pass over v does for all.  The tensor core cuts its sums off instead of rounding them; a tile's sums
-// start from zero and are added to the running ones in registers, in fp32.
+// out of date.  A row that has seen nothing yet has one below all scores, so that the first that it sees raises it.  The
+// weights' bf16 terms (two, 16 bits, for bf16 results, three, 24 bits, for fp32 ones) are TERMS rows of P each, so one
+// pass over v does for all.  The tensor core cuts its sums off instead of rounding them; a tile's sums start from zero and
+// are added to the running ones in registers, in fp32.
 //
 // Warps: 0-7 weights; 8-11 sums; 12 and 13 start the copies of k and v (TMA boxes of a page's rows, zeros for a page that
 // is not there); 14 products; 15 looks ahead: the pages of the next tiles' tokens.  k and v of a tile share a ring of
@@ -21,6 +22,8 @@
 // (48 requests with 5 new tokens, window 4096, fp32 results: 137 us, 5.4 TB/s).  The roles run side by side, so the code of all
 // has to stay in the instruction cache: 94 KB took 178 us there, 85 KB 138.  Hence the rolled loops and the functions that
 // are not inlined.
+#include <cfloat>
+
 #include "attn_paged.cuh"
 
 namespace bl {
@@ -531,10 +534,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
         if (tid < NR) {
           const float old = fresh ? -INFINITY : c.top[tid];
           const float top = fmaxf(fmaxf(fmaxf(c.part[0][tid], c.part[1][tid]), fmaxf(c.part[2][tid], c.part[3][tid])), old);
-          const float base = top == -INFINITY ? 0.f : top;  // nothing seen yet: all weights are 0
+          // A row that has seen nothing: what it does not see keeps a weight of 0, and the first score that it sees lies far
+          // above -FLT_MAX, whatever its size, and raises the maximum.  Rows behind the unit's last have none to raise.
+          const bool none = top == -INFINITY;
           c.top[tid] = top;
-          reinterpret_cast<float*>(c.shift)[tid] = base * a.scale;
-          reinterpret_cast<float*>(c.keep[buf])[tid] = exp2_fast((old - base) * a.scale);
+          reinterpret_cast<float*>(c.shift)[tid] = !none ? top * a.scale : tid < nrows ? -FLT_MAX : 0.f;
+          reinterpret_cast<float*>(c.keep[buf])[tid] = none ? 0.f : exp2_fast((old - top) * a.scale);
         }
         named_barrier_sync(2, kWeigh);
         weigh();

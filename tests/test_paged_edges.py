@@ -1,0 +1,100 @@
+"""Edges of the operators over a paged key-value cache: rows that see nothing of a tile, parts of a row without weight, values
+at the ends of their types, the precision of unlikely tokens.  Tolerances are derived beside each test."""
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as R
+from serving_ref import bf16_round
+from test_paged_step import (BF, F32, B, Cache, attn_bound, check_attn, dev, host, ints, no_device_error,  # noqa: F401
+                             range_error, rng)
+
+gpu = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# attention: rows that see no token in a unit's first tile, or in the first tile of a CTA's stretch.  The bound is that of
+# the other attention tests.
+# ---------------------------------------------------------------------------
+
+def spread_queries(M, H, D, deviation, shift, seed):
+    """Queries whose scores (times D ** -0.5, against keys of deviation 1 around a common part of 0.5) have about this
+    deviation; with `shift` the first coordinate is kept for it."""
+    q = deviation / 1.25 ** 0.5 * rng(M, H, D, seed).standard_normal((M, H, D)).astype(np.float32)
+    if shift:
+        q[..., 0] = 8
+    return bf16_round(q)
+
+
+def shift_scores(cache, by):
+    """All scores by about `by`, through the first coordinate (the queries have 8 there)."""
+    value = bf16_round(np.float32([by * cache.D ** 0.5 / 8]))[0]
+    for k, _ in cache.rows:
+        k[:, :, 0] = value
+    real = ~np.isnan(cache.k)
+    cache.k[..., 0] = np.where(real[..., 0], value, cache.k[..., 0])
+
+
+@gpu
+@pytest.mark.parametrize("window,new", [(300, 2), (512, 5), (1000, 8), (400, 5)])
+@pytest.mark.parametrize("deviation,shift", [(0.8, 0), (1.2, 0), (1.5, 0), (2.0, 0), (1.2, -100), (1.2, 100), (2.0, -300)])
+def test_attn_window_that_begins_in_a_tiles_last_tokens(B, window, new, deviation, shift):
+    lengths = [128 * (r % 4) + 120 + r % 8 + new - 1 + window for r in range(24)]
+    cache = Cache(lengths, 2, 128, 16, 31)
+    if shift:
+        shift_scores(cache, shift)
+    q = spread_queries(24 * new, 10, 128, deviation, shift, window)
+    check_attn(B, cache, [new] * 24, 10, True, window=window, q=q)
+
+
+@gpu
+@pytest.mark.parametrize("length,new,window", [(300, 300, 64), (700, 700, 512), (900, 300, 256), (640, 200, 100), (1500, 640, 128)])
+@pytest.mark.parametrize("D,page,f32", [(128, 16, True), (80, 64, False)])
+def test_attn_prompt_chunks_with_a_window(B, length, new, window, D, page, f32):
+    cache = Cache([length, 40], 1, D, page, 32)
+    q = spread_queries(new + 3, 4, D, 1.0, 0, length)
+    check_attn(B, cache, [new, 3], 4, f32, window=window, q=q)
+
+
+@gpu
+@pytest.mark.parametrize("sinks", [0, 4])
+@pytest.mark.parametrize("deviation,shift", [(0.5, 0), (1.5, 0), (1.0, -200)])
+def test_attn_windows_cut_between_ctas(B, deviation, shift, sinks):
+    """Units of 33 tiles, of which a CTA has some 14."""
+    new, window = 5, 4096
+    lengths = [128 * (1 + r) + 124 + r % 4 + new - 1 + window for r in range(8)]
+    cache = Cache(lengths, 8, 128, 64, 33)
+    if shift:
+        shift_scores(cache, shift)
+    q = spread_queries(8 * new, 16, 128, deviation, shift, sinks)
+    check_attn(B, cache, [new] * 8, 16, True, window=window, sinks=sinks, q=q)
+
+
+@gpu
+@pytest.mark.parametrize("new", [1, 6])
+@pytest.mark.parametrize("deviation,shift", [(0.5, 0), (1.5, 0), (1.0, -200)])
+def test_attn_first_tiles_on_bad_pages_or_without_weight(B, new, deviation, shift):
+    """A request's first tile has no pages, or keys whose scores are all -inf: its rows have seen nothing when the next comes."""
+    lengths, H, D, scale = [300, 1000, 2900, 260] * 3, 24, 128, 128 ** -0.5  # some 900 tiles: a CTA has several
+    cache = Cache(lengths, 8, D, 16, 34, wide=True)
+    if shift:
+        shift_scores(cache, shift)
+    q = spread_queries(12 * new, H, D, deviation, shift, 7)
+    q[..., 1] = 1
+    first = [128, 256, 1280, 128] * 3  # hidden tokens of each request
+    for how in ("pages", "scores"):
+        k, v, table, length = cache.gpu()
+        for r, n in enumerate(first):
+            if how == "pages":
+                table[r, :n // 16] = -1
+            else:
+                k[table[r, :n // 16].long(), :, :, 1] = -float("inf")
+        out = host(B.bl_attn_paged(dev(q, BF), k, v, table, length, ints(np.arange(13) * new), scale, out_dtype=F32))
+        assert range_error(B) == (how == "pages")
+        for r, n in enumerate(lengths):
+            for t in range(new):
+                seen = R.seen_by(n - new + t, n, 0, 0) & (np.arange(n) >= first[r])
+                for h in range(H):
+                    kr, vr = (c[:, h // 3] for c in cache.rows[r])
+                    ref, cond, size = R.attention_row(q[r * new + t, h], kr, vr, seen, scale)
+                    assert np.all(np.abs(out[r * new + t, h] - ref) <= attn_bound(ref[None], cond[None], np.array([size]), n, D, True)[0]), (how, r, t, h)
