@@ -620,13 +620,17 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
         while (true) {  // the warp's part that has it, cut again while it is long
           const u64 v = sh.warps[lane], through = warp_scan(v);
           const unsigned live = __ballot_sync(0xffffffffu, v != 0), past = __ballot_sync(0xffffffffu, through_parts + through > target);
-          const int in = past ? __ffs(past) - 1 : 31 - __clz(live);  // the last that has any, where the sums end early
-          through_parts += __shfl_sync(0xffffffffu, through - v, in);
-          const int nf = part(f, e, in), ne = part(f, e, in + 1);
-          f = nf;
-          e = ne;
+          // A lane rounds its sum once, so a part may have one where none of those that it is cut into does: then it is
+          // looked through as it is.
+          if (live) {
+            const int in = past ? __ffs(past) - 1 : 31 - __clz(live);  // the last that has any, where the sums end early
+            through_parts += __shfl_sync(0xffffffffu, through - v, in);
+            const int nf = part(f, e, in), ne = part(f, e, in + 1);
+            f = nf;
+            e = ne;
+          }
           __syncthreads();  // sh.warps has been read
-          if (e - f <= 2 * kThreads) break;
+          if (!live || e - f <= 2 * kThreads) break;
           const u64 t = sum_of(attempt, part(f, e, warp), part(f, e, warp + 1));
           if (lane == 0) sh.warps[warp] = t;
           __syncthreads();

@@ -98,3 +98,57 @@ def test_attn_first_tiles_on_bad_pages_or_without_weight(B, new, deviation, shif
                     kr, vr = (c[:, h // 3] for c in cache.rows[r])
                     ref, cond, size = R.attention_row(q[r * new + t, h], kr, vr, seen, scale)
                     assert np.all(np.abs(out[r * new + t, h] - ref) <= attn_bound(ref[None], cond[None], np.array([size]), n, D, True)[0]), (how, r, t, h)
+
+
+# ---------------------------------------------------------------------------
+# verification: what is drawn from lies in many tokens below the sums' units (2^-44 of a weight, 2^-60 of p - q).  The sums
+# are within 2^-20 of the mass.
+# ---------------------------------------------------------------------------
+
+NUMBERS = [0.0, float("nan"), -1.0, 1e-12, 1e-7, 0.3, 0.5, 0.99, 0.99999994, 2.0]
+
+
+def tail_rows(rows, V, tail, bf16):
+    """Logits of 0 at V - 5, nothing at V - 1, `tail` elsewhere."""
+    l = torch.full((rows, V), tail, dtype=BF if bf16 else F32, device="cuda")
+    l[:, V - 5] = 0
+    l[:, V - 1] = -float("inf")
+    return l
+
+
+@gpu
+@pytest.mark.parametrize("requests", [1, 64, 200])
+@pytest.mark.parametrize("tail", [-31.0, -34.0, -35.0, -38.0, -42.0, -45.0])
+def test_verify_tails_below_the_unit_of_the_sums(B, tail, requests):
+    V = 248320
+    us = np.resize(np.float32(NUMBERS), requests)
+    if requests == 1:
+        us = np.float32([0])
+    for bf16 in (True, False):
+        _, got = B.bl_verify(tail_rows(requests, V, tail, bf16), ints(np.zeros(requests)), ints(np.arange(requests + 1)), dev(us), dev(us))
+        got = got.cpu().numpy()
+        w = np.full(V, np.exp(tail))
+        w[V - 5], w[V - 1] = 1, 0
+        mass = np.cumsum(w) / w.sum()
+        u = np.clip(np.nan_to_num(us), 0, np.float32(0.99999994))
+        assert np.all((got >= 0) & (got < V - 1)), got
+        assert np.all((mass[got] - w[got] / w.sum() <= u + 2.0 ** -20) & (mass[got] >= u - 2.0 ** -20)), got
+
+
+@gpu
+@pytest.mark.parametrize("requests", [1, 64, 200])
+@pytest.mark.parametrize("tail", [-31.0, -38.0, -42.0, -43.0, -44.0, -45.0])
+def test_verify_tails_below_the_unit_of_what_is_left(B, tail, requests):
+    """A draft that both models mask is refused, and the draft's model has all but the tail: the tail is what is left."""
+    V = 248320
+    us = np.resize(np.float32(NUMBERS), requests)
+    if requests == 1:
+        us = np.float32([0])
+    u = np.full(2 * requests, 0.5, np.float32)
+    token = np.resize([0, V - 1], 2 * requests)
+    for bf16 in (True, False):
+        drafts = tail_rows(2 * requests, V, -float("inf"), bf16)
+        accepted, got = B.bl_verify(tail_rows(2 * requests, V, tail, bf16), ints(token), ints(2 * np.arange(requests + 1)), dev(u), dev(us), draft_logits=drafts)
+        got = got.cpu().numpy()
+        assert not accepted.any()
+        assert np.all((got >= 0) & (got < V - 1)), got
