@@ -71,11 +71,6 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ f2 add2(f2 a, f2 b) {
   f2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -358,7 +353,8 @@ struct __align__(16) Shared {
   Shown shown;
   Weights w[2];
   Reciprocal share[2];
-  float scale[2];  // light weights in units of 2^-40 of the mass
+  float ratio;     // p's mass over q's: q's light weights beside p's
+  float unit;      // from light weights of p, in units of 2^-40, to units of 2^-60 of the mass
   u64 warps[kWarps], masses[2][kWarps];
   int listed[kWarps];          // tokens of a warp's part whose weights are not light, and where they are
   int list[kWarps][kListed];
@@ -370,11 +366,15 @@ __device__ __noinline__ u64 weight_in(const Shared& sh, int m, float l) {
   const float y = sh.w[m].light(l);
   return y < 32.f ? __float2ull_rn(16.f * exp2_fast(y)) : sh.w[m].full(l, sh.exp2);
 }
+// What light weights leave of p - q, as a weight of p in units of 2^-40.  One rounding: where p equals q (a ratio of 1),
+// nothing is left.
+__device__ __forceinline__ float light_excess(const Shared& sh, float yp, float yq) {
+  return fmaxf(__fmaf_rn(exp2_fast(yq), -sh.ratio, exp2_fast(yp)), 0.f);
+}
 // What p has over q, in units of 2^-60 of their masses.
 __device__ __noinline__ u64 excess(const Shared& sh, float lp, float lq) {
   const float yp = sh.w[0].light(lp), yq = sh.w[1].light(lq);
-  if (yp < 32.f && yq < 32.f)
-    return __float2ull_rn(1048576.f * fmaxf(__fmaf_rn(exp2_fast(yp), sh.scale[0], -__fmul_rn(exp2_fast(yq), sh.scale[1])), 0.f));
+  if (yp < 32.f && yq < 32.f) return __float2ull_rn(sh.unit * light_excess(sh, yp, yq));
   const u64 p = sh.share[0].share(weight_in(sh, 0, lp)), q = sh.share[1].share(weight_in(sh, 1, lq));
   return p > q ? p - q : 0;
 }
@@ -522,11 +522,17 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
         if (lane == 0) sh.shown.mass[warp] = s;
       }
       sync_cluster<kC>();
-      if (tid < 2) {
+      if (warp == 0) {
         u64 s = 0;
-        for (int c = 0; c < kC; ++c) s += *of(&sh.shown.mass[tid], c);
-        sh.share[tid].set(s);
-        sh.scale[tid] = s ? float(1ull << kWeightBits) / float(s) : 0.f;
+        if (lane < 2) {
+          for (int c = 0; c < kC; ++c) s += *of(&sh.shown.mass[lane], c);
+          sh.share[lane].set(s);
+        }
+        const float scale = s ? float(1ull << kWeightBits) / float(s) : 0.f, of_q = __shfl_sync(0xffffffffu, scale, 1);
+        if (lane == 0) {
+          sh.ratio = scale > 0.f ? __fdiv_rn(of_q, scale) : 0.f;
+          sh.unit = 1048576.f * scale;
+        }
       }
       __syncthreads();
     }
@@ -559,14 +565,14 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
                          if (wp.light(v[0].most()) < 32.f && wq.light(v[1].most()) < 32.f) {
                            const f2 hp = pack2(wp.hi, wp.hi), lp = pack2(wp.lo, wp.lo), op = pack2(wp.offset, wp.offset);
                            const f2 hq = pack2(wq.hi, wq.hi), lq = pack2(wq.lo, wq.lo), oq = pack2(wq.offset, wq.offset);
-                           const f2 sp = pack2(sh.scale[0], sh.scale[0]), sq = pack2(-sh.scale[1], -sh.scale[1]);
+                           const f2 ratio = pack2(-sh.ratio, -sh.ratio);
                            f2 t = 0;
 #pragma unroll
                            for (int k = 0; k < N / 2; ++k) {
                              const f2 ep = exp2_of(fma2(v[0].pair(k), lp, fma2(v[0].pair(k), hp, op)));
                              const f2 eq = exp2_of(fma2(v[1].pair(k), lq, fma2(v[1].pair(k), hq, oq)));
                              float d0, d1;
-                             unpack2(fma2(ep, sp, mul2(eq, sq)), d0, d1);
+                             unpack2(fma2(eq, ratio, ep), d0, d1);  // light_excess
                              t = add2(t, pack2(fmaxf(d0, 0.f), fmaxf(d1, 0.f)));
                            }
                            float t0, t1;
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
                            for (int j = 0; j < N; ++j) {
                              const float l0 = v[0].at(j), yp = wp.light(l0), yq = wq.light(v[1].at(j));
                              if (yp < 32.f && yq < 32.f)
-                               sum += fmaxf(__fmaf_rn(exp2_fast(yp), sh.scale[0], -__fmul_rn(exp2_fast(yq), sh.scale[1])), 0.f);
+                               sum += light_excess(sh, yp, yq);
                              else
                                heavy |= unsigned(l0 > -INFINITY && !(wp.few && l0 < wp.top)) << j;  // p has none otherwise
                            }
@@ -591,7 +597,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
                        });
       }
       each_listed([&](int i, float lp, float lq) { more += rest_at(attempt, i, lp, lq); });
-      return warp_sum_u64(more + __float2ull_rn((p_only ? 16.f : 1048576.f) * sum));
+      return warp_sum_u64(more + __float2ull_rn((p_only ? 16.f : sh.unit) * sum));
     };
     for (int attempt = 0; attempt < 2; ++attempt) {
       const u64 s = sum_of(attempt, wfrom, wto);

@@ -152,3 +152,37 @@ def test_verify_tails_below_the_unit_of_what_is_left(B, tail, requests):
         got = got.cpu().numpy()
         assert not accepted.any()
         assert np.all((got >= 0) & (got < V - 1)), got
+
+
+def near(us, w, got, slack=2.0 ** -20):
+    """Whether `got` is a token whose stretch of the weights w holds the number, up to `slack` of the mass."""
+    mass = np.cumsum(w) / w.sum()
+    u = min(max(float(np.nan_to_num(us)), 0.0), float(np.float32(0.99999994)))
+    return w[got] > 0 and mass[got] - w[got] / w.sum() - slack <= u <= mass[got] + slack
+
+
+@gpu
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("requests,V", [(3, 20000), (40, 20001), (70, 100000)])
+def test_verify_equal_rows_leave_nothing_of_their_difference(B, requests, V, apart, bf16):
+    """p = q in every token, light and heavy ones: nothing is left, so p is taken.  `apart`: rows at other addresses modulo 16."""
+    g = rng(V, requests, 41)
+    l = (2.5 * g.standard_normal((2 * requests, V))).astype(np.float32)
+    l[np.arange(2 * requests)[:, None], g.integers(0, V, (2 * requests, 5))] += 6
+    l = bf16_round(l) if bf16 else l
+    x = g.integers(0, V, requests)
+    l[2 * np.arange(requests), x] = -np.inf
+    t, us = g.uniform(0.4, 1.6, requests).astype(np.float32), g.random(requests).astype(np.float32)
+    token = np.stack([x * 0, x], 1).reshape(-1)
+    lt = dev(l, BF if bf16 else F32)
+    drafts = lt.clone()
+    if apart:
+        buf = torch.empty(lt.numel() + 1, dtype=lt.dtype, device="cuda")
+        drafts = buf[1:].view(lt.shape)
+        drafts.copy_(lt)
+    accepted, got = B.bl_verify(lt, ints(token), ints(2 * np.arange(requests + 1)), dev(np.full(2 * requests, 0.3, np.float32)), dev(us),
+                                temperature=dev(t), draft_logits=drafts)
+    assert not accepted.any()
+    for r, n in enumerate(got.tolist()):
+        assert near(us[r], R.weights(l[2 * r], t[r]), n), r
