@@ -642,12 +642,18 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
           __syncthreads();
         }
         // The part's sum was formed in another order than the tokens' own shares are: where these end before the
-        // target, the last token that has one is taken, and the likeliest where the shares are below their unit.
-        u64 best = 0;  // (whether it has a share, how likely) over the token
+        // target, the last token that has one is taken, and where they are below their unit the token that has most.
+        auto light_share = [&](int i, float lp, float lq) {  // unrounded; of a weight that is not light the share is whole
+          const float yp = sh.w[0].light(lp), yq = sh.w[1].light(lq);
+          if (!(yp < 32.f)) return 0.f;
+          if (attempt == 0 && both) return yq < 32.f ? light_excess(sh, yp, yq) : 0.f;
+          return attempt == 0 && i == drafted ? 0.f : exp2_fast(yp);
+        };
+        u64 best = 0;  // (whether it has a share, its light one) over the token
         for (int i0 = f; i0 < e; i0 += kThreads) {
           const int i = i0 + tid;
-          const float l = i < e ? at(0, i) : -INFINITY;
-          const u64 v = i < e ? rest_at(attempt, i, l, at(1, i)) : 0ull;
+          const float l = i < e ? at(0, i) : -INFINITY, lq = i < e ? at(1, i) : -INFINITY;
+          const u64 v = i < e ? rest_at(attempt, i, l, lq) : 0ull;
           const u64 through = warp_scan(v);
           if (lane == 31) sh.warps[warp] = through;
           __syncthreads();
@@ -656,8 +662,8 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
           through_parts += __shfl_sync(0xffffffffu, through_w, 31);
           if (v > 0 && b <= target)
             best = max(best, 1ull << 63 | u64(i));
-          else if (l > -INFINITY)
-            best = max(best, u64(key_of_f32(l) >> 1) << 32 | u64(i));
+          else if (const float share = light_share(i, l, lq); share > 0.f)
+            best = max(best, u64(__float_as_uint(share)) << 32 | u64(i));
           __syncthreads();
         }
 #pragma unroll

@@ -186,3 +186,30 @@ def test_verify_equal_rows_leave_nothing_of_their_difference(B, requests, V, apa
     assert not accepted.any()
     for r, n in enumerate(got.tolist()):
         assert near(us[r], R.weights(l[2 * r], t[r]), n), r
+
+
+@gpu
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("model", [False, True])
+def test_verify_tokens_without_a_share_are_not_drawn(B, model, bf16):
+    """The tokens that hold the number have each less than a unit (2^-44 of the largest weight, 2^-60 of the mass of p - q); among
+    them lies the refused draft, which is far likelier and has no share."""
+    V, end = 30000, 29000
+    for x in (96, 100, 103, 110):
+        # the other tokens of the first part: a fifth of a unit each, four of them above half of one
+        tail = np.float32(np.log(0.2 * 1.66) - 60 * np.log(2) if model else np.log(0.2) - 44 * np.log(2))
+        l = np.full((2, V), -np.inf, np.float32)
+        l[:, :300], l[:, x], l[:, end] = tail, np.log(np.float32(0.66)), 0
+        q = np.full((2, V), -np.inf, np.float32)
+        q[:, x], q[:, end] = 0, np.log(np.float32(0.66))
+        if bf16:
+            l, q = bf16_round(l), bf16_round(q)
+        u = np.float32([0.9, 0])  # p(x) = 0.4, q(x) = 0.6 or 1
+        for us in (0.0, -1.0, 1e-30):
+            accepted, got = B.bl_verify(dev(l, BF if bf16 else F32), ints([0, x]), ints([0, 2]), dev(u), dev(np.float32([us])),
+                                        draft_logits=dev(q, BF if bf16 else F32) if model else None)
+            w = R.weights(l[0], 1.0)
+            w[x] = 0
+            if model:
+                w = np.maximum(R.weights(l[0], 1.0) / R.weights(l[0], 1.0).sum() - R.weights(q[0], 1.0) / R.weights(q[0], 1.0).sum(), 0)
+            assert accepted.item() == 0 and w[got.item()] > 0 and near(us, w, got.item()), (x, us, got.item())
