@@ -35,6 +35,10 @@ constexpr int kMassThreads = 128;  // 64 requests: 31 us; with 256 34, with 512 
 constexpr int kMostStretches = 16;
 constexpr int kThreads = 1024, kWarps = kThreads / 32;  // a lane per warp in the sums over warps
 constexpr int kListed = 32;
+// Exponents l log2(e) / T of this size and above differ by 64 and more between neighbouring numbers (2^-24 of it), and a
+// half of a step of theirs stays below the largest exponent of fp32.
+constexpr float kMostExponent = 1073741824.f;
+constexpr float kLeast = 1.40129846e-45f;  // the smallest number above 0
 
 struct Args {
   const void *logits, *drafts;
@@ -215,11 +219,11 @@ __global__ void __launch_bounds__(kMassThreads) verify_mass_kernel(const Args a)
     const void* x = mat ? a.drafts : a.logits;
     const int from = stretch * a.stretch, to = min(int(a.V), from + a.stretch);
     // The sum is in units of 2^E, E a whole number, so that l rate - E is rounded once; -inf: only the largest have
-    // weight (greedy, or exponents beyond fp32, where the next smaller number has none).
+    // weight (greedy, or exponents of kMostExponent and more, where the next smaller number has 2^-64).
     float top = -INFINITY, E = -INFINITY, sum = 0.f;
     auto raise = [&](float l) {  // to a larger maximum
       top = l;
-      const float next = few || !(fabsf(l * rate) <= FLT_MAX) ? -INFINITY : ceilf(l * rate);
+      const float next = few || !(fabsf(l * rate) < kMostExponent) ? -INFINITY : ceilf(l * rate);
       sum *= next > -INFINITY ? exp2_fast(E - next) : 0.f;
       E = next;
     };
@@ -312,32 +316,40 @@ struct Reciprocal {
 
 // Weights of a row's logits, 2^(l log2(e) / T - E) in units of 2^-44, where E is a whole number so near to the largest
 // logit's exponent that its weight is in (2^43, 2^44].  log2(e) / T = hi + lo with lo > 0 (-inf has weight 0 then).
+// `apart`: where the exponents are too large for that (their steps are no fractions any more), the weights are formed from
+// the difference to the largest logit, as in the sampling.
 struct Weights {
   float hi, lo, E;
   float top;
-  bool none, few;  // no logit above -inf; only the largest have weight: greedy, an infinity, or exponents beyond fp32
-  float offset;    // 40 - E
+  bool none, few, apart;  // no logit above -inf; only the largest have weight: greedy, an infinity, or too large exponents
+  float offset;           // 40 - E
+  Slope slope;
 
   __device__ __forceinline__ void set(float2 stat, float temperature) {
     top = stat.x;
     none = !(stat.y > 0.f);
     const float lh = 1.44269502162933349609375f, ll = 1.92596303313e-8f;  // log2(e) = lh + ll
-    hi = __fdiv_rd(lh, temperature);
-    lo = fmaxf(__fdiv_rn(__fadd_rn(__fmaf_rn(-hi, temperature, lh), ll), temperature), FLT_MIN);  // lh - hi T is exact
+    hi = fmaxf(__fdiv_rd(lh, temperature), kLeast);
+    lo = fmaxf(__fdiv_rn(__fadd_rn(__fmaf_rn(-hi, temperature, lh), ll), temperature), kLeast);  // lh - hi T is exact
     const float p = __fmul_rn(top, hi);
     E = ceilf(p);
-    few = !(temperature >= kGreedyBelow) || !(fabsf(p) <= FLT_MAX);
-    offset = !few && !none && fabsf(E) < 4194304.f ? 40.f - E : NAN;  // every weight by full()
+    few = !(temperature >= kGreedyBelow) || !(fabsf(p) < kMostExponent);
+    apart = !(fabsf(E) < 4194304.f);
+    offset = !few && !none && !apart ? 40.f - E : NAN;  // every weight by full()
+    slope = slope_of(temperature);
   }
   // log2 of the weight in units of 2^-40, where it is below 32 (NaN where only the largest have weight)
   __device__ __forceinline__ float light(float l) const { return __fmaf_rn(l, lo, __fmaf_rn(l, hi, offset)); }
   __device__ __forceinline__ u64 full(float l, const Exp2Table& t) const {
+    if (none) return 0;
+    if (few) return u64(l == top) << kWeightBits;
+    if (apart) return weight_of(l, top, slope, t);
     const float p = __fmul_rn(l, hi);
     const float e = __fsub_rn(p, E), z = __fsub_rn(e, p);
     const float el = __fadd_rn(__fsub_rn(p, __fsub_rn(e, z)), __fsub_rn(-E, z)) + __fmaf_rn(l, lo, __fmaf_rn(l, hi, -p));
     int shift;
-    const u64 w = exp2_mantissa(e, el, none || few, t, shift);
-    return few && !none ? u64(l == top) << kWeightBits : (w + ((1ull << shift) >> 1)) >> shift;
+    const u64 w = exp2_mantissa(e, el, false, t, shift);
+    return (w + ((1ull << shift) >> 1)) >> shift;
   }
 };
 

@@ -213,3 +213,64 @@ def test_verify_tokens_without_a_share_are_not_drawn(B, model, bf16):
             if model:
                 w = np.maximum(R.weights(l[0], 1.0) / R.weights(l[0], 1.0).sum() - R.weights(q[0], 1.0) / R.weights(q[0], 1.0).sum(), 0)
             assert accepted.item() == 0 and w[got.item()] > 0 and near(us, w, got.item()), (x, us, got.item())
+
+
+# ---------------------------------------------------------------------------
+# verification: logits and temperatures at the ends of their types
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("model", [False, True])
+@pytest.mark.parametrize("temperature", [0.0, 1e-4, 0.7, 1.4, 1.5, 1.7, 2.0, 3.0, 5.0, 100.0, 1e10, 1e17, 1e19, 1e30, 1e36, 1e37, 1e38, 3e38, np.inf])
+def test_verify_masks_of_the_lowest_value(B, temperature, model, bf16):
+    """Logits of the type's lowest value have the weight that the temperature leaves them, -inf none at any; whole words, threads
+    and stretches of them."""
+    low = np.float32(-3.3895313892515355e38) if bf16 else np.finfo(np.float32).min
+    for V, live in ((96, slice(0, 32)), (9000, slice(40, 90)), (9000, slice(8000, 9000, 7))):
+        n = 40
+        l = np.full((2 * n, V), low, np.float32)
+        l[:, live] = 0
+        l[:, V - V // 3:V - V // 4] = -np.inf
+        x = V - V // 3
+        us = ((np.arange(n) + 0.5) / n).astype(np.float32)
+        q = l.copy()
+        q[:, :60] = -np.inf
+        _, got = B.bl_verify(dev(l, BF if bf16 else F32), ints(np.resize([0, x], 2 * n)), ints(2 * np.arange(n + 1)), dev(np.resize(us, 2 * n)), dev(us),
+                             temperature=dev(np.full(n, temperature, np.float32)), draft_logits=dev(q, BF if bf16 else F32) if model else None)
+
+        def weights(row):
+            if temperature < 1e-5:
+                return (row == row.max()) * 1.0
+            z = (np.where(row > -np.inf, row, low).astype(np.float64) - row.max()) / np.float64(np.float32(temperature))
+            return np.where(row > -np.inf, np.exp(z), 0)
+        w, slack = weights(l[0]), 2.0 ** -20
+        if model:  # each share is rounded to a unit of 2^-60 of the mass; below that nothing is left, and p is taken
+            rest = np.maximum(w / w.sum() - weights(q[0]) / weights(q[0]).sum(), 0)
+            if rest.max() > 2.0 ** -60:
+                w, slack = rest, slack + (rest > 0).sum() * 2.0 ** -61 / rest.sum()
+        for r in range(n):
+            assert near(us[r], w, got[r].item(), slack), (V, r, got[r].item())
+
+
+@gpu
+@pytest.mark.parametrize("model", [False, True])
+@pytest.mark.parametrize("top,temperature", [(1000.0, 2e-5), (-1000.0, 2e-5), (60.0, 1e-5), (1e6, 0.03), (-1e6, 0.03), (3e7, 1.0), (-3e8, 20.0), (5e9, 300.0), (1e12, 0.5), (-1e20, 1e12)])
+def test_verify_large_exponents(B, top, temperature, model):
+    """Logits whose differences are steps of fp32 and whose exponents have no fraction any more: the weights are those of the
+    differences, in tests of acceptance too."""
+    V, n = 5000, 64
+    step = abs(np.spacing(np.float32(top)))
+    g = rng(71, int(abs(top)))
+    l = (np.float32(top) - step * g.integers(0, 6, (2 * n, V))).astype(np.float32)
+    l[:, 17] = top
+    q = (np.float32(top) - step * g.integers(0, 6, (2 * n, V))).astype(np.float32) if model else None
+    t = np.full(n, temperature, np.float32)
+    us, u = g.random(n).astype(np.float32), g.random(2 * n).astype(np.float32)
+    token = g.integers(0, V, 2 * n)
+    accepted, got = B.bl_verify(dev(l), ints(token), ints(2 * np.arange(n + 1)), dev(u), dev(us), temperature=dev(t), draft_logits=dev(q) if model else None)
+    for r in range(n):
+        a, x, margin, w = R.verify(l[2 * r:2 * r + 2], q[2 * r:2 * r + 2] if model else None, token[2 * r:2 * r + 2], u[2 * r:2 * r + 2], us[r], t[r])
+        if margin > 2.0 ** -15:
+            assert accepted[r].item() == a, (r, margin)
+            assert near(us[r], w, got[r].item()), (r, got[r].item())
