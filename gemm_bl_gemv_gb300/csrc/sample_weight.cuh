@@ -76,16 +76,24 @@ __device__ __forceinline__ unsigned long long exp2_mantissa(float e, float el, b
   return none ? 0ull : base.x + static_cast<unsigned long long>(more);
 }
 
-// The weight of logit l: -z = (l - max) log2(e) / T in pairs of floats.
-__device__ __forceinline__ unsigned long long weight_mantissa(float l, float top, Slope c, const Exp2Table& t,
-                                                              int& shift) {
+// (l - max) log2(e) / T as a pair of floats.
+struct Pair {
+  float e, el;
+};
+__device__ __forceinline__ Pair exponent_of(float l, float top, Slope c) {
   const float d = __fsub_rn(l, top);  // < 0; its rounding error is dl
   const float z = __fsub_rn(d, l);
   const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(d, z)), __fsub_rn(-top, z));
   const float e = __fmul_rn(d, c.hi);
-  const float el = __fmaf_rn(d, c.hi, -e) + __fmaf_rn(d, c.lo, __fmul_rn(dl, c.hi));
+  return {e, __fmaf_rn(d, c.hi, -e) + __fmaf_rn(d, c.lo, __fmul_rn(dl, c.hi))};
+}
+
+// The weight of logit l.
+__device__ __forceinline__ unsigned long long weight_mantissa(float l, float top, Slope c, const Exp2Table& t,
+                                                              int& shift) {
+  const Pair x = exponent_of(l, top, c);
   // no weight: too small, greedy, -inf, NaN, beside +inf
-  const unsigned long long w = exp2_mantissa(e, el, c.hi < 0.f, t, shift);
+  const unsigned long long w = exp2_mantissa(x.e, x.el, c.hi < 0.f, t, shift);
   shift = l == top ? 0 : shift;
   return l == top ? 1ull << kWeightBits : w;
 }

@@ -5,7 +5,8 @@
 //
 // The first kernel forms maximum and mass of all rows that have a draft, each row cut
 // into stretches so that few rows fill the GPU; for the tests of acceptance, which are
-// comparisons of two numbers, fp32 will do.  The second kernel takes a cluster per
+// comparisons of two numbers, fp32 will do (a draft's own weight is formed on its own, to
+// 2^-21 however unlikely it is).  The second kernel takes a cluster per
 // request: it joins the stretches, finds the row where the request stops, and draws
 // from that row.  There the sums' borders between neighbouring tokens count, so the
 // weights are integers in units of 2^-44 and their sums exact; for max(p - q, 0) both
@@ -192,12 +193,27 @@ __device__ __forceinline__ float weight(float l, float top, float rate) {
   return rate < 0.f ? float(l == top) : l == top ? 1.f : exp2_fast(fmaxf((l - top) * rate, -200.f));
 }
 
+// Weight of l beside a maximum (which has 1) as m 2^e, m returned: with the exponent's whole part kept apart, an unlikely
+// token's weight is as exact as a likely one's (2^-21).  0 below 2^-1000, as where only the largest have weight.
+__device__ __forceinline__ float weight_apart(float l, float top, Slope c, int& e) {
+  e = 0;
+  if (l == top) return 1.f;
+  const Pair x = exponent_of(l, top, c);
+  if (c.hi < 0.f || !(x.e > -1000.f)) return 0.f;
+  const float n = rintf(x.e);
+  e = int(n);
+  return exp2_fast(__fsub_rn(x.e, n) + x.el);
+}
+
 // Maximum and mass of the logits of two sets.
 __device__ __forceinline__ float2 join(float2 a, float2 b, float rate) {
   const float top = fmaxf(a.x, b.x);
   return make_float2(top, a.y * weight(a.x, top, rate) + b.y * weight(b.x, top, rate));
 }
 
+// A mass is within 2^-17 of its value, mostly within 2^-21: the slope's error, 2^-23.4, counts up to 19 times (a token of
+// 2^-z of the largest counts if there are 2^z of them, of 2^19): 2^-20; an exponent's rounding 2^-20.5; exp2 2^-22; 26
+// additions behind one another 2^-19.3; the joining of threads and stretches, two roundings of up to 19, 2^-19.3.
 template <bool XB>
 __global__ void __launch_bounds__(kMassThreads) verify_mass_kernel(const Args a) {
   __shared__ int64_t found;
@@ -420,21 +436,26 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
     return s;
   };
   // the first draft that is refused: a warp per draft
+  const Slope slope = slope_of(t);
   for (int j = warp; rank == 0 && j < drafts; j += kWarps) {
     const int64_t row = int64_t(rows.first) + j;
     const int x = a.token[row + 1];
     const float u = a.u[row];
     const bool mine = lane < kMostStretches || a.drafts;
-    const float2 s = mass_of(row, a.drafts != nullptr);
-    float share = lane < kMostStretches ? 0.f : 1.f;
+    float2 s = mass_of(row, a.drafts != nullptr);
+    float w = mine ? 0.f : 1.f;  // w 2^e / s.y: p in lane 0, q in lane 16
+    int e = 0;
     if (x < 0 || x >= a.V) {
       bad = true;
-    } else if (mine) {
-      const float l = logit<XB>(lane < kMostStretches ? a.logits : a.drafts, row * a.V + x);
-      share = s.y > 0.f ? __fdiv_rn(weight(l, s.x, rate), s.y) : 0.f;
+    } else if (mine && s.y > 0.f) {
+      w = weight_apart(logit<XB>(lane < kMostStretches ? a.logits : a.drafts, row * a.V + x), s.x, slope, e);
     }
-    const float qx = __shfl_sync(0xffffffffu, share, kMostStretches);
-    if (lane == 0 && !(__fmul_rn(u > 0.f ? fminf(u, 0.99999994f) : 0.f, qx) < share)) atomicMin(&sh.shown.stop, j);
+    if (!mine || !(s.y > 0.f)) s.y = 1.f;
+    const float wq = __shfl_sync(0xffffffffu, w, kMostStretches), mass_q = __shfl_sync(0xffffffffu, s.y, kMostStretches);
+    const int eq = __shfl_sync(0xffffffffu, e, kMostStretches);
+    // u q < p with both sides times both masses and 2^-e, which fp64 has the range for
+    const double u_q = double(u > 0.f ? fminf(u, 0.99999994f) : 0.f) * double(wq) * double(s.y) * __hiloint2double((1023 + eq - e) << 20, 0);
+    if (lane == 0 && !(u_q < double(w) * double(mass_q))) atomicMin(&sh.shown.stop, j);
   }
   __syncthreads();
   if (rank == 0 && warp == 0 && rows.n > 0) {

@@ -624,10 +624,15 @@ bl_status bl_attn_paged(const uint16_t* q_bf16, const uint16_t* k_cache, const u
  * is -1, as is that of a request without rows (accepted 0).  A draft outside
  * [0, V) is refused and sets BL_DEVERR_RANGE, as does a start outside 0 .. M
  * or falling.
- * The test of acceptance is made in fp32 (2^-20 of p and q).  The sums that the
- * token is found by are 64-bit integers: weights above 2^-8 of the largest are
- * within 2^-30 of their value, lighter ones within 2^-20, either way alike, and
- * a thread's (a few hundred) are summed in fp32 first.
+ * The test of acceptance takes p and q within 2^-17 of their value each (2^-16
+ * where logits / temperature lie beyond 2^22), however unlikely the draft is;
+ * weights below 2^-1000 of the largest are 0 in it.  The sums that the token is
+ * found by are 64-bit integers, of weights in units of 2^-44 of the largest, of
+ * p - q in units of 2^-60 (what is left of it below that counts as nothing):
+ * weights above 2^-8 of the largest are within 2^-30 of their value, lighter
+ * ones within 2^-19, either way alike, and a thread's light ones (a few hundred)
+ * are summed in fp32 first, within 2^-18 at worst.  Where the number lies that
+ * near to the border between two tokens, bl_sample may take the other one.
  *   logits, draft_logits : [M, V] fp32 or bf16 (lt); draft_logits may be NULL
  *   (its last row of a request is not read).  token : int32 [M].  temperature :
  *   fp32 [R] or NULL (1).  u : fp32 [M].  u_sample : fp32 [R].

@@ -274,3 +274,67 @@ def test_verify_large_exponents(B, top, temperature, model):
         if margin > 2.0 ** -15:
             assert accepted[r].item() == a, (r, margin)
             assert near(us[r], w, got[r].item()), (r, got[r].item())
+
+
+# ---------------------------------------------------------------------------
+# verification: unlikely drafts.  p and q are within 2^-17 of their value each (include/bl.h), so tests of acceptance that are
+# 2^-16 of p away from going the other way are sure.
+# ---------------------------------------------------------------------------
+
+def acceptance(l, q, x, t):
+    """p(x) / q(x) in 64 bits, of rows with an own temperature."""
+    def share(a):
+        z = (a.astype(np.float64) - a.max()) / np.float64(t)
+        return np.exp(z[x]) / np.exp(z).sum()
+    return share(l) / (share(q) if q is not None else 1.0)
+
+
+@gpu
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("z", [2, 20, 60, 100, 140, 400, 900])
+def test_verify_unlikely_drafts(B, z, bf16):
+    """Drafts whose weights under both models are about 2^-z of the largest, tested by numbers just beside p / q."""
+    V, requests = 700, 64
+    g = rng(61, z, bf16)
+    t = g.uniform(0.02, 0.2, requests).astype(np.float32)
+    l, q = ((0.2 * g.standard_normal((2 * requests, V))).astype(np.float32) for _ in range(2))
+    x = g.integers(0, V, requests)
+    for r in range(requests):
+        for a in (l, q):
+            a[2 * r, (x[r] + 5) % V] = 4 + g.random()
+            a[2 * r, x[r]] = a[2 * r].max() - t[r] * z * np.log(2) * g.uniform(0.99, 1)
+        q[2 * r, x[r]] += t[r] * g.uniform(1, 3) + (0.1 if bf16 else 0)
+    if bf16:
+        l, q = bf16_round(l), bf16_round(q)
+    u, want, sure = np.zeros(2 * requests, np.float32), np.zeros(requests, int), 0
+    for r in range(requests):
+        ratio = acceptance(l[2 * r], q[2 * r], x[r], t[r])
+        want[r] = r % 2
+        u[2 * r] = np.float32(ratio * (1 - 2.0 ** -15.9 if want[r] else 1 + 2.0 ** -15.9))  # (the number's own rounding: 2^-24)
+        if not 0 < u[2 * r] < 0.9999:  # q no likelier than p: accepted whatever the number
+            u[2 * r], want[r] = 0.5, ratio > 0.5
+            assert abs(ratio - 0.5) > 1e-3
+        else:
+            sure += 1
+    assert sure >= requests // 2
+    accepted, _ = B.bl_verify(dev(l, BF if bf16 else F32), ints(np.stack([0 * x, x], 1).reshape(-1)), ints(2 * np.arange(requests + 1)), dev(u),
+                              dev(u[:requests]), temperature=dev(t), draft_logits=dev(q, BF if bf16 else F32))
+    assert np.array_equal(accepted.cpu().numpy(), want), np.nonzero(accepted.cpu().numpy() != want)
+
+
+@gpu
+@pytest.mark.parametrize("temperature", [1.0, 0.05])
+def test_verify_a_number_of_zero_accepts_what_the_model_can_say(B, temperature):
+    """u = 0 accepts every draft with p(x) > 0, given ones and a model's, and none without."""
+    V = 5000
+    l = np.zeros((8, V), np.float32)
+    l[:, 30] = -20
+    l[:, 40] = -np.inf
+    l[:, 50] = -0.5 * 700 * temperature
+    token = np.array([0, 30, 0, 40, 0, 50, 0, 60])
+    q = np.zeros((8, V), np.float32)
+    q[:, 50] = 30
+    zero, t = np.zeros(8, np.float32), np.full(4, temperature, np.float32)
+    for drafts in (None, dev(q)):
+        accepted, _ = B.bl_verify(dev(l), ints(token), ints([0, 2, 4, 6, 8]), dev(zero), dev(zero[:4]), temperature=dev(t), draft_logits=drafts)
+        assert accepted.tolist() == [1, 0, 1, 1]
