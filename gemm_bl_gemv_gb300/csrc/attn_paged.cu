@@ -598,6 +598,7 @@ cudaError_t launch_attn_paged(const uint16_t* q, const uint16_t* k_cache, const 
   a.scale = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;
   a.sign = scale < 0.f ? 0x80008000u : 0u;
   a.zero = scale == 0.f;
+  a.wait_ns = wait_limit_ns();
   a.by_page.set(uint32_t(page));
   a.by_group.set(uint32_t(a.G));
   a.header = reinterpret_cast<Header*>(ws);

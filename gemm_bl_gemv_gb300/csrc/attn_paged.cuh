@@ -51,6 +51,7 @@ struct Args {
   bool zero;      // a scale of 0: so are the queries
   Divisor by_page, by_group;
   bool tiled;  // a tile lies within a page
+  unsigned long long wait_ns;  // a test limit of the roles' waits, or 0
   unsigned int* err;
 };
 

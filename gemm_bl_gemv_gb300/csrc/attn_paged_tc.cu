@@ -78,6 +78,7 @@ struct __align__(16) Tables {
   uint64_t q_full[3];
   uint32_t tmem;
   unsigned dead;                 // a wait gave up
+  int fills[kSlots];             // times that a slot's copies have been started
   Tile tile[kInfo];
   int block[kBack][16];          // the blocks of rows of a tile's pages in the caches
   int row[kBack];                // the first row in them
@@ -116,6 +117,8 @@ __device__ __forceinline__ bool odd_value(uint32_t u) { return (u & 0x7f80u) == 
 
 // The rest of a wait that did not end at once, out of line: the roles' loops have to share the instruction cache.  False: it
 // gave up, or, unless `all`, another one has (`dead`); the role then ends, and touches nothing that it has not waited for.
+// `all` is for the warps of the weights, which meet at barriers behind their vote: no look at `dead`, so that either all of
+// them pass or none does.
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, unsigned* dead, bool all) {
   const bool ok = (all || *static_cast<volatile unsigned*>(dead) == 0) && mbar_wait_bounded(bar, parity, nullptr);
   if (!ok) *static_cast<volatile unsigned*>(dead) = 1;
@@ -151,11 +154,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
     tmem_relinquish();
   }
   if (tid == 0) {
-    c.dead = 0;
+    c.dead = a.wait_ns != 0;  // a test limit: as if a wait had given up
 #pragma unroll 1
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&c.full[i], 1);
       mbar_init(&c.empty[i], 1);
+      c.fills[i] = 0;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.s_full[i], 1);
@@ -283,7 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
       const Tile& now = c.tile[i % kInfo];
       if (seq >= kSlots && !wait(&c.empty[slot], seq / kSlots - 1)) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&c.full[slot], kHalf);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&c.full[slot], kHalf);
+        c.fills[slot] = seq / kSlots + 1;
+      }
       __syncwarp();
       // a lane per box of 64 columns of a page's rows
 #pragma unroll 1
@@ -620,10 +627,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
   if (count > 0 && warp == 14) mbar_wait_bounded(&c.last, 0, nullptr);  // no product is in flight
   __syncwarp();
   if (__syncthreads_or(bad) && tid == 0) atomicOr(a.err, BL_DEVERR_RANGE);
-  if (c.dead) {  // copies may still be in flight: they have time to land
-    if (tid == 0) atomicOr(a.err, BL_DEVERR_WAIT_TIMEOUT);
-    const unsigned long long from = globaltimer_ns();
-    while (globaltimer_ns() - from < 1000000) __nanosleep(1000);
+  if (c.dead) {  // copies may still be in flight: they land before the CTA ends; no unit goes on from here
+    if (tid < kSlots && c.fills[tid] > 0) mbar_wait_bounded(&c.full[tid], (c.fills[tid] - 1) & 1, nullptr);
+    if (tid == 0) {
+      atomicOr(a.err, BL_DEVERR_WAIT_TIMEOUT);
+      a.header[blockIdx.x] = Header{};
+    }
     __syncthreads();
   }
   if (warp == 14) {

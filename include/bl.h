@@ -89,8 +89,11 @@ bl_status bl_device_error(uint32_t* flags, int clear);
  * flight runs the limit out.  A wait that gives up records
  * BL_DEVERR_WAIT_TIMEOUT, the kernel skips the rest of its work and its
  * outputs are unspecified; the waits that let a CTA's own copies land before
- * it exits keep the full second, so the kernel still returns cleanly.  Other
- * kernels keep the default limit.  Always returns BL_OK.
+ * it exits keep the full second, so the kernel still returns cleanly.  In
+ * bl_attn_paged's kernel for requests with many rows, whose warps wait on one
+ * another, any test limit makes every wait give up that does not end at its
+ * first try (but the one behind which warps meet at barriers, which keeps the
+ * second).  Other kernels keep the default limit.  Always returns BL_OK.
  */
 bl_status bl_set_wait_limit(uint64_t ns);
 

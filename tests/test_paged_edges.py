@@ -338,3 +338,41 @@ def test_verify_a_number_of_zero_accepts_what_the_model_can_say(B, temperature):
     for drafts in (None, dev(q)):
         accepted, _ = B.bl_verify(dev(l), ints(token), ints([0, 2, 4, 6, 8]), dev(zero), dev(zero[:4]), temperature=dev(t), draft_logits=drafts)
         assert accepted.tolist() == [1, 0, 1, 1]
+
+
+# ---------------------------------------------------------------------------
+# attention: waits that give up
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("f32", [True, False])
+def test_attn_waits_that_run_out(B, f32):
+    """With a test limit the roles give up: the call returns, says so, writes no row but its own (whatever an earlier
+    call has left in the workspace), and the next one is right."""
+    H, Hk, D = 40, 8, 128
+    t = F32 if f32 else BF
+    big, small = Cache([3000, 900, 2000, 1700, 2500, 1100], Hk, D, 16, 81), Cache([700, 1300], Hk, D, 16, 82)
+    ws = B.attn_paged_workspace(60, H, Hk, D)
+    buf = torch.empty(70, H, D, dtype=t, device="cuda")
+    out = buf[:10]
+
+    def call(cache, new, out):
+        k, v, table, length = cache.gpu()
+        n = len(cache.lengths)
+        q = dev(bf16_round(rng(n, 83).standard_normal((n * new, H, D)).astype(np.float32)), BF)
+        return B.bl_attn_paged(q, k, v, table, length, ints(np.arange(n + 1) * new), D ** -0.5, out=out, workspace=ws)
+    want = call(small, 5, torch.empty(10, H, D, dtype=t, device="cuda"))
+    for _ in range(2):
+        call(big, 10, torch.empty(60, H, D, dtype=t, device="cuda"))  # leaves units of 60 rows that go on in other CTAs
+        buf.fill_(5)
+        torch.cuda.synchronize()
+        B.set_wait_limit(1)
+        try:
+            call(small, 5, out)
+            torch.cuda.synchronize()
+        finally:
+            B.set_wait_limit(0)
+        assert B.device_error(clear=True) == B.BL_DEVERR_WAIT_TIMEOUT
+        assert bool((buf[10:] == 5).all())
+        assert torch.equal(call(small, 5, out), want)
+        assert bool((buf[10:] == 5).all())
