@@ -25,7 +25,9 @@
 // 100 tokens and 93 instead of 86 for D 80; with 6 and four 40 and 117.
 // The tensor core cuts its sums off instead of rounding them, so a tile's weighted
 // sum starts from zero and is added to the running one in fp32.  The weights go in
-// as two bf16 terms (16 bits) for bf16 results, three (24 bits) for fp32 ones.
+// as three bf16 terms, all their 24 bits, so a bf16 result is the fp32 one rounded
+// once; two terms (16 bits) move 2 of 1000 bf16 results by a step, and are 1 to 3 %
+// faster (D 80 and 256: a tenth).
 #include <cmath>
 
 #include "attn_paged.cuh"
@@ -93,7 +95,7 @@ __device__ __forceinline__ void copies_wait() {
 
 template <class S, bool F32>
 __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args a) {
-  constexpr int TT = S::TT, NT = TT / 8, KS = S::DP / 16, TERMS = F32 ? 3 : 2;
+  constexpr int TT = S::TT, NT = TT / 8, KS = S::DP / 16;
   constexpr int kThreads = S::WARPS * 32;
   constexpr uint32_t kAll = TT == 32 ? 0xffffffffu : (1u << TT) - 1;
   extern __shared__ __align__(128) uint8_t ring[];

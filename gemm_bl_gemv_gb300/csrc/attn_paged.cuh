@@ -7,6 +7,7 @@
 namespace bl {
 namespace attn {
 
+constexpr int TERMS = 3;        // of a weight: bf16 numbers that it enters the second product in, 24 bits
 constexpr int kMostCtas = 160;  // of the first kernel, for the size of the workspace
 
 // Rows of a unit: n from row0 on, of a request's new tokens from `token` on and a key-value head.

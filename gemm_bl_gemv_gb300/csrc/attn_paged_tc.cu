@@ -9,8 +9,7 @@
 // A thread then has a token's scores of half of the rows, or a coordinate's sums of all: nothing is exchanged between
 // threads in a tile, unless a row's maximum rises by more than 2^8: weights are beside a maximum that may be that much
 // out of date.  A row that has seen nothing yet has one below all scores, so that the first that it sees raises it.  The
-// weights' bf16 terms (two, 16 bits, for bf16 results, three, 24 bits, for fp32 ones) are TERMS rows of P each, so one
-// pass over v does for all.  The tensor core cuts its sums off instead of rounding them; a tile's sums start from zero and
+// weights' bf16 terms (three, all their 24 bits) are TERMS rows of P each, so one pass over v does for all.  The tensor core cuts its sums off instead of rounding them; a tile's sums start from zero and
 // are added to the running ones in registers, in fp32.
 //
 // Warps: 0-7 weights; 8-11 sums; 12 and 13 start the copies of k and v (TMA boxes of a page's rows, zeros for a page that
@@ -136,7 +135,7 @@ template <int NR, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a, const __grid_constant__ CUtensorMap k_map,
                                                                    const __grid_constant__ CUtensorMap v_map) {
   using S = TcShape<NR>;
-  constexpr int TERMS = F32 ? 3 : 2, PN = TERMS * NR;
+  constexpr int PN = TERMS * NR;
   constexpr int kQBytes = NR * 256, kCols = 2 * NR + 2 * PN <= 128 ? 128 : 256;
   extern __shared__ uint8_t raw[];
   __shared__ Tables<NR> c;
@@ -644,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_tc_kernel(const Args a
 
 template <int NR, bool F32>
 cudaError_t launch_as(const Args& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int grid, cudaStream_t s) {
-  constexpr int kBytes = 1024 + kSlots * kHalf + 3 * NR * 256 + (F32 ? 3 : 2) * NR * 256;
+  constexpr int kBytes = 1024 + kSlots * kHalf + 3 * NR * 256 + TERMS * NR * 256;
   int dev = 0;
   cudaGetDevice(&dev);
   const cudaError_t e = raise_smem_cap(attn_paged_tc_kernel<NR, F32>, dev, kBytes);

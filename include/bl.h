@@ -589,9 +589,9 @@ bl_status bl_rope_append(const void* qkv, bl_dtype xt, const float* cos, const f
  *   workspace : at least bl_attn_paged_workspace(M, H, Hk, D) bytes, 256-byte
  *   aligned; its contents do not matter and nothing is kept in it between
  *   calls.  Calls that share one must not overlap on the GPU.
- * Products are bf16 with fp32 sums; weights enter the second product in 16
- * bits for bf16 results and 24 for fp32 ones, and the running maximum, sum and
- * weighted sum are fp32.  Which warp takes which tokens, and by which kernel
+ * Products are bf16 with fp32 sums; weights enter the second product in 24
+ * bits, and the running maximum, sum and weighted sum are fp32; a bf16 result is
+ * the fp32 one rounded once.  Which warp takes which tokens, and by which kernel
  * (one for requests with ten rows and more or wide tables, D 72 to 128 and
  * pages of 8, 16, 32, 64 or multiples of 128; one for all others), depends on
  * the arguments, the lengths and the device's number of SMs, so sums are the

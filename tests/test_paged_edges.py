@@ -376,3 +376,18 @@ def test_attn_waits_that_run_out(B, f32):
         assert bool((buf[10:] == 5).all())
         assert torch.equal(call(small, 5, out), want)
         assert bool((buf[10:] == 5).all())
+
+
+# ---------------------------------------------------------------------------
+# attention: precision
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("H,Hk,D,new", [(10, 2, 128, 1), (10, 2, 128, 6), (8, 2, 64, 1), (40, 8, 80, 3), (16, 4, 256, 1)])
+def test_attn_bf16_results_are_the_fp32_ones_rounded_once(B, H, Hk, D, new, wide):
+    cache = Cache([900, 40, 2000, 333], Hk, D, 16, 91, wide=wide)
+    k, v, table, length = cache.gpu()
+    q = dev(bf16_round(1.3 * rng(H, D, new, 92).standard_normal((4 * new, H, D)).astype(np.float32)), BF)
+    full, short = (B.bl_attn_paged(q, k, v, table, length, ints(np.arange(5) * new), D ** -0.5, out_dtype=t) for t in (F32, BF))
+    assert torch.equal(full.to(BF), short)
