@@ -81,11 +81,14 @@ __device__ __forceinline__ Request request_of(const Args& a, int64_t r) {
   q.bad = length < 0 || q.owned != owned;
   q.total = q.ends ? 0 : int64_t(max(length, 0)) + q.count;
   int64_t need = (q.total + a.page - 1) / a.page;
-  if (need > a.W || q.total > INT32_MAX) q.bad = true;
+  if (need > a.W || q.total >= INT32_MAX) q.bad = true;
   need = min(need, a.W);
   q.ask = q.ends ? 0 : max(int64_t(0), need - q.owned);
   return q;
 }
+
+// A request's tokens before the step, from its new length; -1: its positions do not fit, so that its tokens have none.
+__device__ __forceinline__ int old_length(int length, int count) { return length == INT32_MAX ? -1 : length - max(count, 0); }
 
 // f(x, y, j) for j = 0..n-1 of every lane's (n, x, y), lane by lane, by the whole converged warp.
 template <class F>
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const Args a) {
         a.start[r] = int(min(mine.tokens, a.M));
         if (r < kCached) {
           starts[r] = int(min(mine.tokens, a.M));
-          old[r] = int(min(q.total, int64_t(INT32_MAX))) - q.count;
+          old[r] = old_length(int(min(q.total, int64_t(INT32_MAX))), q.count);
         }
         a.length_out[r] = int(min(q.total, int64_t(INT32_MAX)));
         if (!q.ends) a.owned_out[r] = q.owned + int(got);
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const Args a) {
   if (cached && rank != 0) {
     for (int r = tid; r <= a.R; r += kThreads) {
       starts[r] = a.start[r];
-      if (r < a.R) old[r] = a.length_out[r] - max(a.count[r], 0);
+      if (r < a.R) old[r] = old_length(a.length_out[r], a.count[r]);
     }
   }
   __syncthreads();
@@ -183,11 +186,14 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const Args a) {
     int position = -1, slot = -1;
     if (i < last) {
       const int64_t r = request_of_token(start, a.R, int(i));
-      position = (cached ? old[r] : a.length_out[r] - max(a.count[r], 0)) + int(i) - start[r];
-      const int entry = position / a.page;
-      const int page = entry < a.W ? a.table[r * a.W + entry] : -1;
-      if (page >= 0 && page < a.pages) slot = page * a.page + position % a.page;
-      bad |= page >= a.pages;
+      const int before = cached ? old[r] : old_length(a.length_out[r], a.count[r]);
+      if (before >= 0) {
+        position = before + int(i) - start[r];
+        const int entry = position / a.page;
+        const int page = entry < a.W ? a.table[r * a.W + entry] : -1;
+        if (page >= 0 && page < a.pages) slot = page * a.page + position % a.page;
+        bad |= page >= a.pages;
+      }
     }
     a.position[i] = position;
     a.slot[i] = slot;

@@ -526,7 +526,9 @@ bl_status bl_sample(const void* logits, bl_dtype lt, const float* temperature, c
  * BL_DEVERR_RANGE, and so do a negative length, an owned or free_count outside
  * [0, W] or [0, pages] (both are brought into the range), more than M new
  * tokens (those behind M are left out), pages returned beyond `pages` (left
- * out), and a table entry >= pages that a new token lies in.
+ * out), a table entry >= pages that a new token lies in, and a request that
+ * comes to 2^31 - 1 tokens or more (position and slot of its new tokens are -1,
+ * length_out 2^31 - 1).
  *   length, count, owned : int32 [R];  table : int32 [R, W], updated in place;
  *   free_pages : int32 [pages], updated in place where requests end;
  *   free_count : int32 [1];  start : int32 [R + 1];  position, slot : int32

@@ -6,7 +6,7 @@ import torch
 
 import paged_ref as R
 from serving_ref import bf16_round
-from test_paged_step import (BF, F32, B, Cache, attn_bound, check_attn, dev, host, ints, no_device_error,  # noqa: F401
+from test_paged_step import (BF, F32, I32, B, Cache, attn_bound, check_attn, dev, host, ints, no_device_error,  # noqa: F401
                              range_error, rng)
 
 gpu = pytest.mark.gpu
@@ -391,3 +391,27 @@ def test_attn_bf16_results_are_the_fp32_ones_rounded_once(B, H, Hk, D, new, wide
     q = dev(bf16_round(1.3 * rng(H, D, new, 92).standard_normal((4 * new, H, D)).astype(np.float32)), BF)
     full, short = (B.bl_attn_paged(q, k, v, table, length, ints(np.arange(5) * new), D ** -0.5, out_dtype=t) for t in (F32, BF))
     assert torch.equal(full.to(BF), short)
+
+
+# ---------------------------------------------------------------------------
+# page maps: requests whose positions do not fit
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("requests", [3, 2100])
+@pytest.mark.parametrize("tokens", [40, 5000])
+def test_page_map_lengths_next_to_the_largest(B, requests, tokens):
+    """New tokens of a request that comes to 2^31 - 1 tokens or more get no slot (they took those of earlier tokens)."""
+    page, pages, W, most = 1 << 20, 2047, 2049, (1 << 31) - 1
+    length, count, owned = np.zeros(requests, int), np.zeros(requests, int), np.zeros(requests, int)
+    length[:3], count[:3], owned[:3] = (most - 7, most - 3, 5), (6, 5, 2), (2048, 2048, 1)
+    table = torch.full((requests, W), -1, dtype=I32, device="cuda")
+    table[:2] = torch.arange(W, device="cuda", dtype=I32) % pages
+    table[2, 0] = 7
+    start, position, slot, length_out, owned_out, left = B.bl_page_map(ints(length), ints(count), table, ints(owned), ints(np.arange(pages)), ints([4]), page, tokens)
+    assert range_error(B)
+    assert position[:6].tolist() == list(range(most - 7, most - 1))
+    assert slot[:6].tolist() == [(p // page) % pages * page + p % page for p in range(most - 7, most - 1)]
+    assert position[6:11].tolist() == [-1] * 5 and slot[6:11].tolist() == [-1] * 5
+    assert position[11:13].tolist() == [5, 6] and slot[11:13].tolist() == [7 * page + 5, 7 * page + 6]
+    assert length_out[:3].tolist() == [most - 1, most, 7] and bool((position[13:] == -1).all()) and bool((slot[13:] == -1).all())
