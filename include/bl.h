@@ -575,7 +575,7 @@ bl_status bl_rope_append(const void* qkv, bl_dtype xt, const float* cos, const f
  * length[r] - n + t.  For each of its heads h, with key-value head h / (H / Hk):
  *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale q . k_j - max),
  * over the tokens j <= p that it sees: all of them if window = 0, otherwise
- * those with j > p - window or j < sinks.
+ * those with j > p - window or j < sinks.  Scores are to lie within +-2^30.
  * A token on a page outside [0, pages), behind the table's W pages or behind
  * the first 2^31 - 256 is left out and sets BL_DEVERR_RANGE (as do a negative
  * length and a start outside 0 .. M or falling).  A row that sees no token, or whose scores are all -inf,

@@ -415,3 +415,38 @@ def test_page_map_lengths_next_to_the_largest(B, requests, tokens):
     assert position[6:11].tolist() == [-1] * 5 and slot[6:11].tolist() == [-1] * 5
     assert position[11:13].tolist() == [5, 6] and slot[11:13].tolist() == [7 * page + 5, 7 * page + 6]
     assert length_out[:3].tolist() == [most - 1, most, 7] and bool((position[13:] == -1).all()) and bool((slot[13:] == -1).all())
+
+
+# ---------------------------------------------------------------------------
+# attention: scores that are large against the steps of fp32.  The keys' first coordinate alone makes them, in numbers that
+# bf16, the products and their sums hold exactly, so the weights are 1 at the largest and 0 elsewhere: the values at the
+# largest come out to 2^-21 (a weight's three terms and its sum, 2^-23 each, 1 / sum and the product, 2^-24 each; several
+# equal ones add up in fp32, 2^-22).
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 20, 2.0 ** 24, 2.0 ** 28, 2.0 ** 29])
+@pytest.mark.parametrize("H,Hk,D,new", [(10, 2, 128, 1), (10, 2, 128, 6), (8, 2, 64, 2), (4, 2, 256, 1)])
+def test_attn_large_scores(B, H, Hk, D, new, size, sign, wide):
+    g = rng(H, D, new, int(np.log2(size)))
+    lengths = [300, 40, 1000]
+    cache = Cache(lengths, Hk, D, 16, 95, wide=wide)
+    level = [g.integers(0, 100, (n, Hk)) for n in lengths]  # of 128: (1 + level / 128) times the size
+    for (k, _), l in zip(cache.rows, level):
+        k[:] = 0
+        k[:, :, 0] = sign * 64 * (1 + l / 128)
+    for r, n in enumerate(lengths):
+        for j in range(n):
+            cache.k[cache.table[r, j // 16], :, j % 16] = cache.rows[r][0][j]
+    k, v, table, length = cache.gpu()
+    q = np.zeros((3 * new, H, D), np.float32)
+    q[..., 0] = size / 64
+    out = host(B.bl_attn_paged(dev(q, BF), k, v, table, length, ints(np.arange(4) * new), 1.0, out_dtype=F32))
+    for r, n in enumerate(lengths):
+        for t in range(new):
+            for h in range(H):
+                l = level[r][:n - new + t + 1, h // (H // Hk)] * sign
+                best = cache.rows[r][1][:len(l), h // (H // Hk)][l == l.max()].astype(np.float64)
+                assert np.all(np.abs(out[r * new + t, h] - best.mean(0)) <= 2.0 ** -21 * np.abs(best).mean(0)), (r, t, h)
