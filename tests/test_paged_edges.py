@@ -6,8 +6,8 @@ import torch
 
 import paged_ref as R
 from serving_ref import bf16_round
-from test_paged_step import (BF, F32, I32, B, Cache, attn_bound, check_attn, dev, host, ints, no_device_error,  # noqa: F401
-                             range_error, rng)
+from test_paged_step import (BF, F32, I32, B, Cache, attn_bound, attn_ref, check_attn, dev, host, ints,  # noqa: F401
+                             no_device_error, range_error, rng)
 
 gpu = pytest.mark.gpu
 
@@ -450,3 +450,54 @@ def test_attn_large_scores(B, H, Hk, D, new, size, sign, wide):
                 l = level[r][:n - new + t + 1, h // (H // Hk)] * sign
                 best = cache.rows[r][1][:len(l), h // (H // Hk)][l == l.max()].astype(np.float64)
                 assert np.all(np.abs(out[r * new + t, h] - best.mean(0)) <= 2.0 ** -21 * np.abs(best).mean(0)), (r, t, h)
+
+
+# ---------------------------------------------------------------------------
+# more requests than a CTA has threads; rows before the first request's; flat rows of the largest vocabulary
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("H,Hk,D,wide,most_new", [(2, 1, 64, False, 1), (4, 1, 128, True, 1), (12, 1, 128, False, 2), (2, 1, 256, False, 1)])
+def test_attn_more_requests_than_threads(B, H, Hk, D, wide, most_new):
+    g = rng(H, D, 101)
+    lengths = [int(n) for n in g.integers(0, 40, 1700)]
+    counts = [int(min(n, c)) for n, c in zip(lengths, g.integers(0, most_new + 1, 1700))]
+    check_attn(B, Cache(lengths, Hk, D, 8, 102, wide=wide), counts, H, True, padding=2)
+
+
+@gpu
+@pytest.mark.parametrize("H,wide", [(4, False), (12, False), (2, True)])
+def test_rows_before_the_first_request_are_left_alone(B, H, wide):
+    D, before, counts = 128, 3, [2, 1, 4]
+    cache = Cache([50, 300, 140], 1, D, 16, 103, wide=wide)
+    k, v, table, length = cache.gpu()
+    q = bf16_round(rng(H, 104).standard_normal((before + 7, H, D)).astype(np.float32))
+    start = before + np.concatenate([[0], np.cumsum(counts)])
+    out = torch.full((before + 7, H, D), 5.0, device="cuda")
+    B.bl_attn_paged(dev(q, BF), k, v, table, length, ints(start), D ** -0.5, out=out)
+    ref, cond, size = attn_ref(q[before:], cache, counts, D ** -0.5, 0, 0)
+    assert bool((out[:before] == 5).all()) and np.all(np.abs(host(out)[before:] - ref) <= attn_bound(ref, cond, size, 300, D, True))
+    l = (3 * rng(105).standard_normal((before + 7, 2000))).astype(np.float32)
+    l[:before] = np.nan
+    token, u, us = rng(106).integers(0, 2000, before + 7), np.full(before + 7, 1e-3, np.float32), np.float32([0.2, 0.5, 0.9])
+    a = B.bl_verify(dev(l), ints(token), ints(start), dev(u), dev(us), draft_logits=dev(l[::-1]))
+    b = B.bl_verify(dev(l[before:]), ints(token[before:]), ints(start - before), dev(u[before:]), dev(us), draft_logits=dev(l[::-1][before:]))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@gpu
+@pytest.mark.parametrize("requests", [1, 9, 80])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_verify_flat_rows_of_the_largest_vocabulary(B, requests, bf16):
+    """The sums reach 2^63: token u V, from p alone and where nothing is left of p - q."""
+    V = 524288
+    l = torch.full((2 * requests, V), 1.5, dtype=BF if bf16 else F32, device="cuda")
+    us = ((np.arange(requests) + 0.5) / requests).astype(np.float32)
+    us[-1] = 0.99999994
+    u, token = np.zeros(2 * requests, np.float32), np.resize([0, V], 2 * requests)  # out of range: refused
+    for drafts in (None, l.clone()):
+        accepted, got = B.bl_verify(l, ints(token), ints(2 * np.arange(requests + 1)), dev(u), dev(us), draft_logits=drafts)
+        assert range_error(B)
+        assert not accepted.any() and got.tolist() == [int(np.float64(x) * V) for x in us]
+    _, got = B.bl_verify(l[:requests].contiguous(), ints(token[:requests] * 0), ints(np.arange(requests + 1)), dev(u[:requests]), dev(us))
+    assert got.tolist() == [int(np.float64(x) * V) for x in us]
