@@ -20,9 +20,10 @@
 // 1017 that mma.sync does.  What bounds the kernel is the issue of the copies (16 bytes
 // a lane, some 55 clocks for 32 lanes) and of the weights, and, in short calls, the 6 us
 // before the first tile arrives: 64 requests of up to 8192 tokens (40 heads of queries,
-// 8 of keys, D 128) 198 us, 5.5 TB/s; 256 of up to 600 73 us; one of 4096 14.5 us.  12 warps
+// 8 of keys, D 128) 194 us, 5.6 TB/s; 256 of up to 600 73 us; one of 4096 15 us.  12 warps
 // with two stages each: with 8 and three, 31.5 us instead of 28.3 for 256 requests of up to
-// 100 tokens and 93 instead of 86 for D 80; with 6 and four 40 and 117.
+// 100 tokens and 93 instead of 86 for D 80; with 6 and four 40 and 117 (all with weights of
+// 16 bits).
 // The tensor core cuts its sums off instead of rounding them, so a tile's weighted
 // sum starts from zero and is added to the running one in fp32.  The weights go in
 // as three bf16 terms, all their 24 bits, so a bf16 result is the fp32 one rounded
@@ -201,8 +202,8 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) attn_paged_kernel(const Args
       }
     };
 
-    // The queries of a unit that begins with the tile to come are asked into L2, a lane per 128 bytes (64 requests of up to
-    // 2000 tokens 49.6 -> 47.2 us).
+    // The queries of a unit that begins with the tile to come are asked into L2, a lane per 128 bytes (2.4 us of
+    // 64 requests of up to 2000 tokens).
     auto ask_queries = [&](const Place<S>& p) {
       const int row0 = p.row0(), n = min(S::ROWS, int(min(int64_t(p.q.n) * a.G - row0, int64_t(S::ROWS))));
       const int lines = (a.D * 2 + 127) / 128;
@@ -559,11 +560,12 @@ cudaError_t launch_for(const Args& a, cudaStream_t s) {
   // The former takes 1.3 us a tile, however many rows there are, with 1 to 4 us for a unit; the latter less for a short unit,
   // and twice as much for more than 16 rows.  So tcgen05 has requests with ten rows of a key-value head and more, and D 104 to
   // 128 where the tables have room for long requests (the lengths are known on the device only).  Measured, mma.sync / tcgen05,
-  // us, requests x (evenly spread) lengths up to, query / key heads, D 128 unless stated, pages of 16:
-  //   rows: 256 x 600, 20/5: 2 new tokens (8 rows) 83/92, 3: 100/93, 5: 143/94; 64 x 300, 5 new 40/26; 64 x 1000, 32/8, 8 new
-  //     110/60; 48 x 20000, 40/8, 5 new, window 4096, fp32 232/138; D 80, 64 x 1000, 5 new 58/42; D 64 35/42.
-  //   one token: 64 x 8192, 40/8 198/176, pages of 64 197/172; 3 x 131072 116/111; 1 x 4096 14.5/14.3; 4 x 30000, 8/8 60/60;
-  //     and 64 x 2000 50/53; 16 x 1000 16/21; 256 x 600 73/92; 256 x 100 28/44; D 80, 8 x 30000 86/87; D 64, 64 x 4000 56/102.
+  // us, requests x (evenly spread) lengths up to, 20/5 query / key heads, D 128 and pages of 16 unless stated:
+  //   rows: 256 x 600: 2 new tokens (8 rows) 83/96, 3: 97/97, 5: 143/97; 64 x 300, 5 new 41/26; 64 x 1000, 32/8, 8 new
+  //     108/61; 48 x 20000, 40/8, 5 new, window 4096, fp32 234/139; D 80, 64 x 1000, 5 new 61/42; D 64 37/42.
+  //   one token: 64 x 8192, 40/8 194/180, pages of 64 194/173; 3 x 131072 116/112; 1 x 4096 15.2/14.8; 4 x 30000, 8/8 62/61;
+  //     and 64 x 2000 49/56; 16 x 1000 17/21; 256 x 600 73/96; 256 x 100 29/44; D 80, 8 x 30000, 40/8 97/93; D 64, 64 x 4000,
+  //     16/8 57/111.
   const bool rows = a.M * a.G >= 10 * a.R, room = a.D > 96 && a.W * a.page >= 4096;
   if (a.D > 64 && a.D <= 128 && (rows || room)) {
     const int grid = std::min(sm_count(), kMostCtas);

@@ -16,9 +16,9 @@
 // is not there); 14 products; 15 looks ahead: the pages of the next tiles' tokens.  k and v of a tile share a ring of
 // five half tiles.  A page is 128 tokens or more in steps of 128, or 8, 16, 32 or 64; the other kernel takes others.
 //
-// Bound: HBM where lengths are long (64 requests of up to 8192 tokens, 40 / 8 heads, one new token: 175 us, 6.2 TB/s; 3 of
-// up to 131072 110 us); a tile's weights, 1.3 us, and 1 to 2 us for a unit's begin and end and for each tile that rows see in part
-// (48 requests with 5 new tokens, window 4096, fp32 results: 137 us, 5.4 TB/s).  The roles run side by side, so the code of all
+// Bound: HBM where lengths are long (64 requests of up to 8192 tokens, 40 / 8 heads, one new token: 180 us, 6.1 TB/s; 3 of
+// up to 131072 112 us); a tile's weights, 1.3 us, and 1 to 2 us for a unit's begin and end and for each tile that rows see in part
+// (48 requests with 5 new tokens, window 4096, fp32 results: 139 us, 5.3 TB/s).  The roles run side by side, so the code of all
 // has to stay in the instruction cache: 94 KB took 178 us there, 85 KB 138.  Hence the rolled loops and the functions that
 // are not inlined.
 #include <cfloat>

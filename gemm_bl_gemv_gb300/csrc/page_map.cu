@@ -11,7 +11,7 @@
 // its cluster share the slots.  Pages are pushed only after all have been popped.
 //
 // Bound: latency (a few dependent reads of some KB, the barriers of the scan, a binary search per token in shared
-// memory): 64 requests with a token each 4.3 us; 256 requests, 12 of them prompts, 8200 tokens 7.5 us.  Scans of a
+// memory): 64 requests with a token each 4.4 us; 256 requests, 12 of them prompts, 8200 tokens 7.8 us.  Scans of a
 // warp's sums by one thread and searches in global memory took 5.7 and 9.7 us.
 #include "bl_device.cuh"
 #include "bl_internal.h"

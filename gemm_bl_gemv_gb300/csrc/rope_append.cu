@@ -5,7 +5,8 @@
 // q, k and v to row `slot` of the paged cache.
 //
 // Bound: HBM for prompts, launch and two dependent reads (position, angle) for few tokens: one token 2.2 us, 311 of 56
-// heads in fp32 3.6 us, 8192 of 30 heads in bf16 26.5 us (4.9 TB/s; a copy of the same bytes takes 21.5 us).
+// heads in fp32 3.6 us, 8192 of 30 heads in bf16 27 us (4.8 TB/s; a copy of the same bytes takes 21.5 us).  Where the rotary
+// part or the tables allow no vector loads, one value at a time: 8.7, 16 and 149 us.
 #include "bl_device.cuh"
 #include "bl_internal.h"
 
@@ -146,7 +147,7 @@ template <bool XB, int VEC>
 cudaError_t launch_as(const Args& a, cudaStream_t s) {
   // Few tokens: as many threads as a CTA has for each, so that a thread makes one trip; many: 64, whose angles serve several
   // heads, in small CTAs, whose last ones end together.  256 / 64 threads in us, 56 heads: bf16 400 tokens 3.4 / 4.8, 1200
-  // 8.7 / 8.7, 2000 14.4 / 12.4, 4000 25.8 / 22.2; fp32 1200 11.0 / 11.8, 2000 16.7 / 15.7, 4000 30.2 / 28.7.
+  // 8.7 / 8.7, 2000 14.4 / 12.8, 4000 25.8 / 22.5; fp32 1200 11.0 / 11.8, 2000 16.7 / 16.1, 4000 30.2 / 29.1.
   const bool many = a.M > 8 * sm_count();
   const unsigned per = many ? 64 : kThreads, tokens = many ? 2 : 1;
   return launch(rope_append_kernel<XB, VEC>, dim3(unsigned((a.M + tokens - 1) / tokens)), dim3(per, tokens), 0, s, overlap_enabled(), a);

@@ -17,9 +17,9 @@
 // others from sample_weight.cuh (2^-30), in 40.
 //
 // Bound, 64 requests of one to five rows, bf16 logits of target and draft model over 248320 tokens (157 MB): the first
-// kernel takes 31 us, 5.1 TB/s (HBM 57 % of its time's peak, issue 70 %); the second 42 us, of which two passes over a
-// target's and a draft's row (issue, 12 instructions a pair of logits) are 25, the third of a part and the exchanges the rest;
-// 128 of the 152 SMs have work.  One request with four drafts 15 us, 32 requests with fp32 logits over 100003 tokens 44 us.
+// kernel takes 30 us, 5.2 TB/s (HBM 57 % of its time's peak, issue 70 %); the second 41 us, of which two passes over a
+// target's and a draft's row (issue, 12 and 11 instructions a pair of logits) are 25, the third of a part and the exchanges the
+// rest; 128 of the 152 SMs have work.  One request with four drafts 16 us, 32 requests with fp32 logits over 100003 tokens 44 us.
 // Masses from the first kernel, which are within 2^-22, would save one pass, and move the borders between tokens by 2^-22
 // over what max(p - q, 0) leaves: more than an unlikely token is wide.
 #include <cfloat>
