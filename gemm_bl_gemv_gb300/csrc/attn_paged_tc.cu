@@ -9,8 +9,9 @@
 // A thread then has a token's scores of half of the rows, or a coordinate's sums of all: nothing is exchanged between
 // threads in a tile, unless a row's maximum rises by more than 2^8: weights are beside a maximum that may be that much
 // out of date.  A row that has seen nothing yet has one below all scores, so that the first that it sees raises it.  The
-// weights' bf16 terms (three, all their 24 bits) are TERMS rows of P each, so one pass over v does for all.  The tensor core cuts its sums off instead of rounding them; a tile's sums start from zero and
-// are added to the running ones in registers, in fp32.
+// weights' bf16 terms (three, all their 24 bits) are TERMS rows of P each, so one pass over v does for all.  The tensor
+// core cuts its sums off instead of rounding them; a tile's sums start from zero and are added to the running ones in
+// registers, in fp32.
 //
 // Warps: 0-7 weights; 8-11 sums; 12 and 13 start the copies of k and v (TMA boxes of a page's rows, zeros for a page that
 // is not there); 14 products; 15 looks ahead: the pages of the next tiles' tokens.  k and v of a tile share a ring of

@@ -332,13 +332,14 @@ struct Reciprocal {
 
 // Weights of a row's logits, 2^(l log2(e) / T - E) in units of 2^-44, where E is a whole number so near to the largest
 // logit's exponent that its weight is in (2^43, 2^44].  log2(e) / T = hi + lo with lo > 0 (-inf has weight 0 then).
-// `apart`: where the exponents are too large for that (their steps are no fractions any more), the weights are formed from
-// the difference to the largest logit, as in the sampling.
+// `apart`: from exponents of 2^15 on, whose products are rounded by 2^-10 and more (the polynomial takes 2^-6), the weights
+// are formed from the difference to the largest logit, as in the sampling.
 struct Weights {
   float hi, lo, E;
   float top;
   bool none, few, apart;  // no logit above -inf; only the largest have weight: greedy, an infinity, or too large exponents
   float offset;           // 40 - E
+  float least;            // logits below this one have no weight (where offset is NaN: they need not be looked at)
   Slope slope;
 
   __device__ __forceinline__ void set(float2 stat, float temperature) {
@@ -350,9 +351,10 @@ struct Weights {
     const float p = __fmul_rn(top, hi);
     E = ceilf(p);
     few = !(temperature >= kGreedyBelow) || !(fabsf(p) < kMostExponent);
-    apart = !(fabsf(E) < 4194304.f);
+    apart = !(fabsf(E) < 32768.f);
     offset = !few && !none && !apart ? 40.f - E : NAN;  // every weight by full()
     slope = slope_of(temperature);
+    least = few ? top : apart ? __fsub_rd(top, __fdiv_ru(64.f, hi)) : -INFINITY;
   }
   // log2 of the weight in units of 2^-40, where it is below 32 (NaN where only the largest have weight)
   __device__ __forceinline__ float light(float l) const { return __fmaf_rn(l, lo, __fmaf_rn(l, hi, offset)); }
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
         float t0, t1;
         unpack2(t, t0, t1);
         sum += t0 + t1;
-      } else if (!w.none && !(w.few && l.most() < w.top)) {
+      } else if (!w.none && !(l.most() < w.least)) {
         unsigned heavy = 0;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
@@ -517,7 +519,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
           if (y < 32.f)
             sum += exp2_fast(y);
           else
-            heavy |= unsigned(l.at(e) > -INFINITY && !(w.few && l.at(e) < w.top)) << e;  // -inf and NaN have no weight
+            heavy |= unsigned(l.at(e) > -INFINITY && !(l.at(e) < w.least)) << e;  // -inf and NaN have no weight
         }
         for (; heavy; heavy &= heavy - 1) {
           const int e = __ffs(heavy) - 1;
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
                            float t0, t1;
                            unpack2(t, t0, t1);
                            sum += t0 + t1;
-                         } else if (!wp.none && !(wp.few && v[0].most() < wp.top)) {
+                         } else if (!wp.none && !(v[0].most() < wp.least)) {
                            unsigned heavy = 0;
 #pragma unroll
                            for (int j = 0; j < N; ++j) {
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
                              if (yp < 32.f && yq < 32.f)
                                sum += light_excess(sh, yp, yq);
                              else
-                               heavy |= unsigned(l0 > -INFINITY && !(wp.few && l0 < wp.top)) << j;  // p has none otherwise
+                               heavy |= unsigned(l0 > -INFINITY && !(l0 < wp.least)) << j;  // p has none otherwise
                            }
                            for (; heavy; heavy &= heavy - 1) {
                              const int j = __ffs(heavy) - 1;

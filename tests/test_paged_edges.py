@@ -501,3 +501,22 @@ def test_verify_flat_rows_of_the_largest_vocabulary(B, requests, bf16):
         assert not accepted.any() and got.tolist() == [int(np.float64(x) * V) for x in us]
     _, got = B.bl_verify(l[:requests].contiguous(), ints(token[:requests] * 0), ints(np.arange(requests + 1)), dev(u[:requests]), dev(us))
     assert got.tolist() == [int(np.float64(x) * V) for x in us]
+
+
+@gpu
+@pytest.mark.parametrize("model", [False, True])
+@pytest.mark.parametrize("top,temperature", [(20.0, 0.01), (20.0, 1e-3), (-20.0, 1e-3), (20.0, 1e-4), (-300.0, 1e-3), (5.0, 2e-5), (100.0, 3e-4), (1000.0, 0.01), (1e5, 1.0), (-4e5, 0.3)])
+def test_verify_low_temperatures_beside_large_logits(B, top, temperature, model):
+    """Exponents of 2^11 to 2^21, whose fractions are steps of fp32 still: the likely tokens lie within a few temperatures."""
+    V, n = 5000, 64
+    g = rng(72, int(abs(top)), int(1 / temperature))
+    l, q = ((top - temperature * g.uniform(0, 9, (2 * n, V))).astype(np.float32) for _ in range(2))
+    t = np.full(n, temperature, np.float32)
+    us, u = g.random(n).astype(np.float32), g.random(2 * n).astype(np.float32)
+    token = g.integers(0, V, 2 * n)
+    accepted, got = B.bl_verify(dev(l), ints(token), ints(2 * np.arange(n + 1)), dev(u), dev(us), temperature=dev(t), draft_logits=dev(q) if model else None)
+    for r in range(n):
+        a, x, margin, w = R.verify(l[2 * r:2 * r + 2], q[2 * r:2 * r + 2] if model else None, token[2 * r:2 * r + 2], u[2 * r:2 * r + 2], us[r], t[r])
+        if margin > 2.0 ** -15:
+            assert accepted[r].item() == a, (r, margin)
+            assert near(us[r], w, got[r].item()), (r, got[r].item())
