@@ -18,7 +18,7 @@
 //
 // Bound, 64 requests of one to five rows, bf16 logits of target and draft model over 248320 tokens (157 MB): the first
 // kernel takes 30 us, 5.2 TB/s (HBM 57 % of its time's peak, issue 70 %); the second 41 us, of which two passes over a
-// target's and a draft's row (issue, 12 and 11 instructions a pair of logits) are 25, the third of a part and the exchanges the
+// target's and a draft's row (issue, 12 instructions a pair of logits) are 25, the third of a part and the exchanges the
 // rest; 128 of the 152 SMs have work.  One request with four drafts 16 us, 32 requests with fp32 logits over 100003 tokens 44 us.
 // Masses from the first kernel, which are within 2^-22, would save one pass, and move the borders between tokens by 2^-22
 // over what max(p - q, 0) leaves: more than an unlikely token is wide.
@@ -39,6 +39,9 @@ constexpr int kListed = 32;
 // Exponents l log2(e) / T of this size and above differ by 64 and more between neighbouring numbers (2^-24 of it), and a
 // half of a step of theirs stays below the largest exponent of fp32.
 constexpr float kMostExponent = 1073741824.f;
+// Light weights, below 2^-8 of the largest, are floats in units of 2^-16 of it: their logarithm is below kLight; in units
+// of 2^-44 and 2^-60.
+constexpr float kLight = 8.f, kLightUnits = 268435456.f, kFineUnits = 17592186044416.f;
 constexpr float kLeast = 1.40129846e-45f;  // the smallest number above 0
 
 struct Args {
@@ -328,6 +331,8 @@ struct Reciprocal {
     }
   }
   __device__ __forceinline__ u64 share(u64 w) const { return __umul64hi(w << 19, r) >> shift; }
+  // The same of a sum of light weights (2^61 at most) in units of 2^-60.
+  __device__ __forceinline__ u64 fine(u64 w) const { return __umul64hi(w << 2, r) >> (shift - 1); }
 };
 
 // Weights of a row's logits, 2^(l log2(e) / T - E) in units of 2^-44, where E is a whole number so near to the largest
@@ -338,7 +343,7 @@ struct Weights {
   float hi, lo, E;
   float top;
   bool none, few, apart;  // no logit above -inf; only the largest have weight: greedy, an infinity, or too large exponents
-  float offset;           // 40 - E
+  float offset;           // 16 - E
   float least;            // logits below this one have no weight (where offset is NaN: they need not be looked at)
   Slope slope;
 
@@ -352,11 +357,12 @@ struct Weights {
     E = ceilf(p);
     few = !(temperature >= kGreedyBelow) || !(fabsf(p) < kMostExponent);
     apart = !(fabsf(E) < 32768.f);
-    offset = !few && !none && !apart ? 40.f - E : NAN;  // every weight by full()
+    offset = !few && !none && !apart ? 16.f - E : NAN;  // every weight by full()
     slope = slope_of(temperature);
     least = few ? top : apart ? __fsub_rd(top, __fdiv_ru(64.f, hi)) : -INFINITY;
   }
-  // log2 of the weight in units of 2^-40, where it is below 32 (NaN where only the largest have weight)
+  // log2 of the weight in units of 2^-16, where it is below 8 (NaN where all are formed by full()): in this unit the
+  // exponents of the light weights that count, 2^-8 to 2^-24, lie within +-8, where a rounding is 2^-22.
   __device__ __forceinline__ float light(float l) const { return __fmaf_rn(l, lo, __fmaf_rn(l, hi, offset)); }
   __device__ __forceinline__ u64 full(float l, const Exp2Table& t) const {
     if (none) return 0;
@@ -383,8 +389,7 @@ struct __align__(16) Shared {
   Shown shown;
   Weights w[2];
   Reciprocal share[2];
-  float ratio;     // p's mass over q's: q's light weights beside p's
-  float unit;      // from light weights of p, in units of 2^-40, to units of 2^-60 of the mass
+  float ratio[2];  // p's mass over q's, which q's light weights are multiplied by, in two terms
   u64 warps[kWarps], masses[2][kWarps];
   int listed[kWarps];          // tokens of a warp's part whose weights are not light, and where they are
   int list[kWarps][kListed];
@@ -394,17 +399,18 @@ struct __align__(16) Shared {
 // The weight of a logit of the target's row (m = 0) or the draft's.
 __device__ __noinline__ u64 weight_in(const Shared& sh, int m, float l) {
   const float y = sh.w[m].light(l);
-  return y < 32.f ? __float2ull_rn(16.f * exp2_fast(y)) : sh.w[m].full(l, sh.exp2);
+  return y < kLight ? __float2ull_rn(kLightUnits * exp2_fast(y)) : sh.w[m].full(l, sh.exp2);
 }
-// What light weights leave of p - q, as a weight of p in units of 2^-40.  One rounding: where p equals q (a ratio of 1),
-// nothing is left.
+// What light weights leave of p - q, as a weight of p in units of 2^-16.  Where p equals q (a ratio of 1), nothing is left:
+// each fma rounds once.
 __device__ __forceinline__ float light_excess(const Shared& sh, float yp, float yq) {
-  return fmaxf(__fmaf_rn(exp2_fast(yq), -sh.ratio, exp2_fast(yp)), 0.f);
+  const float q = exp2_fast(yq);
+  return fmaxf(__fmaf_rn(q, -sh.ratio[1], __fmaf_rn(q, -sh.ratio[0], exp2_fast(yp))), 0.f);
 }
 // What p has over q, in units of 2^-60 of their masses.
 __device__ __noinline__ u64 excess(const Shared& sh, float lp, float lq) {
   const float yp = sh.w[0].light(lp), yq = sh.w[1].light(lq);
-  if (yp < 32.f && yq < 32.f) return __float2ull_rn(sh.unit * light_excess(sh, yp, yq));
+  if (yp < kLight && yq < kLight) return sh.share[0].fine(__float2ull_rn(kFineUnits * light_excess(sh, yp, yq)));
   const u64 p = sh.share[0].share(weight_in(sh, 0, lp)), q = sh.share[1].share(weight_in(sh, 1, lq));
   return p > q ? p - q : 0;
 }
@@ -497,13 +503,13 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
       __syncwarp();
     };
     auto at = [&](int m, int i) { return logit<XB>(x[m], base + i); };
-    // The weights of logits from i on: light ones to `sum` (fp32: a lane has few of them), in units of 2^-40, others to
+    // The weights of logits from i on: light ones to `sum` (fp32: a lane has few of them), in units of 2^-16, others to
     // the list or `more`.
     auto weigh_one = [&](int m, int i, u64& more) { more += weight_in(sh, m, at(m, i)); };
     auto weigh = [&](int m, const Word<XB>& l, int i, float& sum, u64& more) {
       constexpr int N = Word<XB>::E;
       const Weights& w = sh.w[m];
-      if (w.light(l.most()) < 32.f) {
+      if (w.light(l.most()) < kLight) {
         const f2 hi = pack2(w.hi, w.hi), lo = pack2(w.lo, w.lo), offset = pack2(w.offset, w.offset);
         f2 t = 0;
 #pragma unroll
@@ -516,7 +522,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const float y = w.light(l.at(e));
-          if (y < 32.f)
+          if (y < kLight)
             sum += exp2_fast(y);
           else
             heavy |= unsigned(l.at(e) > -INFINITY && !(l.at(e) < w.least)) << e;  // -inf and NaN have no weight
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
         mass[1] += i < 0 ? w : 0;
       });
       for (int m = 0; m < 2; ++m) {
-        mass[m] = warp_sum_u64(mass[m] + __float2ull_rn(16.f * sum[m]));
+        mass[m] = warp_sum_u64(mass[m] + __float2ull_rn(kLightUnits * sum[m]));
         if (lane == 0) sh.masses[m][warp] = mass[m];
       }
       __syncthreads();
@@ -563,10 +569,11 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
           for (int c = 0; c < kC; ++c) s += *of(&sh.shown.mass[lane], c);
           sh.share[lane].set(s);
         }
-        const float scale = s ? float(1ull << kWeightBits) / float(s) : 0.f, of_q = __shfl_sync(0xffffffffu, scale, 1);
+        const u64 of_q = __shfl_sync(0xffffffffu, s, 1);
         if (lane == 0) {
-          sh.ratio = scale > 0.f ? __fdiv_rn(of_q, scale) : 0.f;
-          sh.unit = 1048576.f * scale;
+          const double ratio = of_q ? double(s) / double(of_q) : 0.0;
+          sh.ratio[0] = float(ratio);
+          sh.ratio[1] = float(ratio - double(sh.ratio[0]));
         }
       }
       __syncthreads();
@@ -597,17 +604,17 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
         each<XB, 2, 1>(x[0], x[1], wide, base, f, e, lane, 32, [&](int i) { more += excess(sh, at(0, i), at(1, i)); },
                        [&](const Word<XB>(&v)[2], int i) {
                          constexpr int N = Word<XB>::E;
-                         if (wp.light(v[0].most()) < 32.f && wq.light(v[1].most()) < 32.f) {
+                         if (wp.light(v[0].most()) < kLight && wq.light(v[1].most()) < kLight) {
                            const f2 hp = pack2(wp.hi, wp.hi), lp = pack2(wp.lo, wp.lo), op = pack2(wp.offset, wp.offset);
                            const f2 hq = pack2(wq.hi, wq.hi), lq = pack2(wq.lo, wq.lo), oq = pack2(wq.offset, wq.offset);
-                           const f2 ratio = pack2(-sh.ratio, -sh.ratio);
+                           const f2 r0 = pack2(-sh.ratio[0], -sh.ratio[0]), r1 = pack2(-sh.ratio[1], -sh.ratio[1]);
                            f2 t = 0;
 #pragma unroll
                            for (int k = 0; k < N / 2; ++k) {
                              const f2 ep = exp2_of(fma2(v[0].pair(k), lp, fma2(v[0].pair(k), hp, op)));
                              const f2 eq = exp2_of(fma2(v[1].pair(k), lq, fma2(v[1].pair(k), hq, oq)));
                              float d0, d1;
-                             unpack2(fma2(eq, ratio, ep), d0, d1);  // light_excess
+                             unpack2(fma2(eq, r1, fma2(eq, r0, ep)), d0, d1);  // light_excess
                              t = add2(t, pack2(fmaxf(d0, 0.f), fmaxf(d1, 0.f)));
                            }
                            float t0, t1;
@@ -618,7 +625,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
 #pragma unroll
                            for (int j = 0; j < N; ++j) {
                              const float l0 = v[0].at(j), yp = wp.light(l0), yq = wq.light(v[1].at(j));
-                             if (yp < 32.f && yq < 32.f)
+                             if (yp < kLight && yq < kLight)
                                sum += light_excess(sh, yp, yq);
                              else
                                heavy |= unsigned(l0 > -INFINITY && !(l0 < wp.least)) << j;  // p has none otherwise
@@ -632,7 +639,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
                        });
       }
       each_listed([&](int i, float lp, float lq) { more += rest_at(attempt, i, lp, lq); });
-      return warp_sum_u64(more + __float2ull_rn((p_only ? 16.f : sh.unit) * sum));
+      return warp_sum_u64(more + (p_only ? __float2ull_rn(kLightUnits * sum) : sh.share[0].fine(__float2ull_rn(kFineUnits * sum))));
     };
     for (int attempt = 0; attempt < 2; ++attempt) {
       const u64 s = sum_of(attempt, wfrom, wto);
@@ -680,8 +687,8 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const Args a) {
         // target, the last token that has one is taken, and where they are below their unit the token that has most.
         auto light_share = [&](int i, float lp, float lq) {  // unrounded; of a weight that is not light the share is whole
           const float yp = sh.w[0].light(lp), yq = sh.w[1].light(lq);
-          if (!(yp < 32.f)) return 0.f;
-          if (attempt == 0 && both) return yq < 32.f ? light_excess(sh, yp, yq) : 0.f;
+          if (!(yp < kLight)) return 0.f;
+          if (attempt == 0 && both) return yq < kLight ? light_excess(sh, yp, yq) : 0.f;
           return attempt == 0 && i == drafted ? 0.f : exp2_fast(yp);
         };
         u64 best = 0;  // (whether it has a share, its light one) over the token

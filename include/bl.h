@@ -635,9 +635,10 @@ bl_status bl_attn_paged(const uint16_t* q_bf16, const uint16_t* k_cache, const u
  * found by are 64-bit integers, of weights in units of 2^-44 of the largest, of
  * p - q in units of 2^-60 (what is left of it below that counts as nothing):
  * weights above 2^-8 of the largest are within 2^-30 of their value, lighter
- * ones within 2^-19, either way alike, and a thread's light ones (a few hundred)
- * are summed in fp32 first, within 2^-18 at worst.  Where the number lies that
- * near to the border between two tokens, bl_sample may take the other one.
+ * ones within 2^-20 (2^-19 below 2^-24), either way alike, and a thread's light
+ * ones (a few hundred) are summed in fp32 first, within 2^-18 at worst.  These
+ * errors even out: of 10000 numbers against 248320 logits one lies so near to a
+ * border that the exact sums give the token beside it.
  *   logits, draft_logits : [M, V] fp32 or bf16 (lt); draft_logits may be NULL
  *   (its last row of a request is not read).  token : int32 [M].  temperature :
  *   fp32 [R] or NULL (1).  u : fp32 [M].  u_sample : fp32 [R].

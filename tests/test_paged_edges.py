@@ -520,3 +520,32 @@ def test_verify_low_temperatures_beside_large_logits(B, top, temperature, model)
         if margin > 2.0 ** -15:
             assert accepted[r].item() == a, (r, margin)
             assert near(us[r], w, got[r].item()), (r, got[r].item())
+
+
+# ---------------------------------------------------------------------------
+# verification: the precision of light weights.  A row of one likely token and many with one light logit: all of these have
+# the same error, so the border behind the first token shows it, times its distances to both ends.  Between 2^-8 and 2^-16 of the
+# largest it is two roundings of an exponent, up to 2^-22 each, times ln 2; exp2's 2^-22; and six additions of fp32, 2^-24 each:
+# 2^-20 in all, and, the roundings spread evenly, 2^-20 sqrt(0.14^2 + 0.25^2 + 0.09^2) = 0.30 2^-20 in the mean of the squares.
+# The numbers' own steps are a tenth of 2^-20 there.
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("bf16", [True, False])
+def test_verify_light_weights_move_no_border(B, bf16):
+    n, V = 64, 20000
+    tail = -rng(111).uniform(5.6, 9.6, n).astype(np.float32)
+    tail = bf16_round(tail) if bf16 else tail
+    l = dev(np.zeros((n, V), np.float32) + tail[:, None], BF if bf16 else F32)
+    l[:, 0] = 0
+    border = 1 / (1 + (V - 1) * np.exp(tail.astype(np.float64)))
+    low = border.astype(np.float32).view(np.int32) - 200  # numbers as their bits: token 0 below, others above
+    high = low + 400
+    zero = dev(np.zeros(n, np.float32))
+    while np.any(high - low > 1):
+        mid = (low + high) // 2
+        _, got = B.bl_verify(l, ints(np.zeros(n)), ints(np.arange(n + 1)), zero, dev(mid.view(np.float32)))
+        first = got.cpu().numpy() == 0
+        low, high = np.where(first, mid, low), np.where(first, high, mid)
+    off = ((low.view(np.float32).astype(np.float64) + high.view(np.float32)) / 2 - border) / (border * (1 - border)) * 2.0 ** 20
+    assert np.all(np.abs(off) <= 1.1) and np.sqrt(np.mean(off ** 2)) <= 0.33, (np.abs(off).max(), np.sqrt(np.mean(off ** 2)))
