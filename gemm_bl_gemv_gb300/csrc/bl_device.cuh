@@ -89,13 +89,14 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // A pipeline wait with a launch-given limit: limit_ns = 0 is mbar_wait_bounded;
 // otherwise (a test limit, see bl_set_wait_limit) the barrier is polled
 // without try_wait's hardware suspension, so that a phase still in progress
-// runs the limit out.
+// runs the limit out; by the SM's clock (two clocks taken for a nanosecond),
+// because %globaltimer may stand still for longer than a copy takes.
 __device__ __forceinline__ bool mbar_wait_limited(uint64_t* bar, uint32_t parity, unsigned int* err,
                                                   unsigned long long limit_ns) {
   if (limit_ns == 0) return mbar_wait_bounded(bar, parity, err);
-  const unsigned long long t0 = globaltimer_ns();
+  const long long t0 = clock64();
   while (!mbar_test_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > limit_ns) {
+    if (static_cast<unsigned long long>(clock64() - t0) / 2 > limit_ns) {
       if (err) atomicOr(err, BL_DEVERR_WAIT_TIMEOUT);
       return false;
     }

@@ -257,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     bulk_g2s(smem + size_t(t) * g.RS, pk(m) + int64_t(r0 + i) * row_bytes + 32 * gx0, uint32_t(g.RS), &wbar,
              policy_evict_first());
   }
+  // a test limit is tried at once: the rows may be there by the time the records are built
+  if (g.wait_ns != 0 && tid == 0 && !mbar_wait_limited(&wbar, 0, g.err, g.wait_ns)) abort_flag = 1;
   // the next kernel's CTAs may become resident now: they fetch their own
   // weights, then wait for this grid to complete before reading its output
   pdl_launch_dependents();

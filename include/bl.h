@@ -82,8 +82,8 @@ bl_status bl_device_error(uint32_t* flags, int clear);
  * Test aid for the failure path (no counterpart on the pages): the weight
  * waits of the i2_s GEMV kernels (bl_gemv_i2s, bl_gemv_i2s_residual,
  * bl_gemv_i2s_rmsnorm and bl_gemv_i2s_gate_up, in their one-CTA-per-SM
- * resident plan) launched afterwards give up after `ns` nanoseconds of
- * %globaltimer instead of the default second (ns = 0 restores the default;
+ * resident plan) launched afterwards give up after `ns` nanoseconds (two of
+ * the SM's clocks each) instead of the default second (ns = 0 restores it;
  * the setting is process-wide and read at each launch).  With a test limit
  * the wait polls without the hardware's suspension, so a copy still in
  * flight runs the limit out.  A wait that gives up records
